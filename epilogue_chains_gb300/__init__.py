@@ -14,12 +14,13 @@ import ctypes
 import threading
 
 FUSE_OK, FUSE_EINVAL, FUSE_EALIGN, FUSE_EUNSUPPORTED = 0, -1, -2, -3
-FUSE_ECUDA, FUSE_ETIMEOUT, FUSE_EWORKSPACE = -4, -5, -6
+FUSE_ECUDA, FUSE_ETIMEOUT, FUSE_EWORKSPACE, FUSE_EINDEX = -4, -5, -6, -7
 FUSE_F32, FUSE_F16, FUSE_BF16 = 0, 1, 2
 FUSE_FUSED, FUSE_UNFUSED, FUSE_FAT = 0, 1, 2
 FUSE_OP_AFFINE, FUSE_OP_AFFINE_RELU = 0, 1
 FUSE_MAX_STAGES = 32
 FUSE_FAT_TEMPS = 48
+FUSE_ROPE_INTERLEAVED = 1
 
 
 class FuseError(RuntimeError):
@@ -101,6 +102,16 @@ SIGNATURES = {
     "fuse_chain_bytes": ([_I32, _I64, _I32, _I32], _I64),
     "fuse_rmsnorm_bytes": ([_I64, _I64, _I32], _I64),
     "fuse_causal_softmax_bytes": ([_I64, _I64, _I32, _I32, _I32], _I64),
+    "fuse_rope_append": ([_P, _I64, _P, _I64, _I64, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64, _I32,
+                          _U32, _P], _I32),
+    "fuse_rope_append_bytes": ([_I64, _I64, _I64, _I64, _I64, _I64], _I64),
+    "fuse_paged_attention": ([_P, _P, _P, _P, _I64, _P, _P, _I64, _P, _I64, _I64, _I64, _I64, _I64, _I64, _F32,
+                              _I32, _P, _SZ, _P], _I32),
+    "fuse_paged_attention_workspace_bytes": ([_I64, _I64, _I64, _I64, _I64], _SZ),
+    "fuse_paged_attention_bytes": ([_I64, _I64, _I64, _I64, _I64, _I64], _I64),
+    "fuse_paged_attention_flops": ([_I64, _I64, _I64, _I64, _I64], _I64),
+    "fuse_w4_gemv": ([_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I32, _I32, _P], _I32),
+    "fuse_w4_gemv_bytes": ([_I64, _I64, _I64, _I64, _I32, _I32, _I32], _I64),
     "fuse_kernel_count": ([], _I32),
     "fuse_kernel_report": ([_I32, ctypes.POINTER(fuse_kernel_record)], _I32),
     "fuse_ptxas_count": ([], _I32),
@@ -369,6 +380,141 @@ def fuse_attention_schedule(bh: int, S: int, clusters: int):
 
 def fuse_gemm_bytes(M: int, N: int, K: int, cut_mask: int) -> int:
     return _load().fuse_gemm_bytes(M, N, K, cut_mask)
+
+
+# ------------------------------------------------------------------------------- single-token decode
+def _decode_operands(dtypes, *ts):
+    """The device index of the tensors, which have to be contiguous, of their dtype and all on torch's
+    current device (the library launches there)."""
+    import torch
+    dev = ts[0].get_device()
+    for t, want in zip(ts, dtypes):
+        if t is not None and (t.get_device() != dev or t.dtype is not want or not t.is_contiguous()):
+            raise ValueError(f"expected contiguous CUDA tensors of one device; {tuple(t.shape)} {t.dtype} on "
+                             f"{t.device}, {want} wanted")
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError("the tensors must be on the current CUDA device")
+    return dev
+
+
+def fuse_rope_append(qkv, cos_sin, positions, slots, q_out, k_cache, v_cache, interleaved: bool = False,
+                     stream=None) -> None:
+    """Rotate the queries and keys of qkv [tokens, (q_heads + 2 kv_heads) D] (rows may be strided) by
+    their positions, write the queries to q_out [tokens, q_heads, D] and append keys and values to
+    k_cache, v_cache [num_pages, kv_heads, page_size, D] at slots (int32; negative: append nothing).
+    cos_sin: fp32 [max_pos, rot], the cosines then the sines of a position's rot / 2 pairs."""
+    import torch
+    dt, i32 = qkv.dtype, torch.int32
+    _decode_operands((dt, dt, dt, i32, i32, torch.float32), q_out, k_cache, v_cache, positions, slots, cos_sin)
+    if dt is not torch.bfloat16 and dt is not torch.float16:
+        raise ValueError("fp16 or bf16 tensors expected")
+    tokens, q_heads, D = q_out.shape
+    pages, kv_heads, page_size, D2 = k_cache.shape
+    if qkv.get_device() != q_out.get_device() or qkv.dim() != 2 or qkv.stride(1) != 1:
+        raise ValueError("qkv must be a 2-D tensor with unit column stride on the device of the others")
+    if (D2 != D or v_cache.shape != k_cache.shape or qkv.shape != (tokens, (q_heads + 2 * kv_heads) * D)
+            or positions.shape != (tokens,) or slots.shape != (tokens,) or cos_sin.dim() != 2):
+        raise ValueError("shape mismatch")
+    ld = qkv.stride(0) if tokens > 1 else qkv.shape[1]
+    _check(_load().fuse_rope_append(qkv.data_ptr(), ld, cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1],
+                                    positions.data_ptr(), slots.data_ptr(), q_out.data_ptr(), k_cache.data_ptr(),
+                                    v_cache.data_ptr(), tokens, q_heads, kv_heads, D, pages, page_size,
+                                    FUSE_F16 if dt is torch.float16 else FUSE_BF16,
+                                    FUSE_ROPE_INTERLEAVED if interleaved else 0, _stream(stream)),
+           "fuse_rope_append")
+
+
+# workspaces of fuse_paged_attention(workspace=None): one zero-filled buffer per (device, stream), grown
+# as needed; every completed call leaves its counters zero
+_PAGED_WS = {}
+
+
+def _paged_workspace(need: int, dev: int, stream_handle):
+    import torch
+    current = torch.cuda.current_stream(dev)
+    if stream_handle != current.cuda_stream or torch.cuda.is_current_stream_capturing():
+        raise ValueError("pass a zero-filled workspace of fuse_paged_attention_workspace_bytes() bytes: this module's "
+                         "own ones serve calls on torch's current stream outside a graph capture only (a captured "
+                         "graph may be replayed next to other calls)")
+    ws = _PAGED_WS.get((dev, stream_handle))
+    if ws is None or ws.numel() < need:
+        ws = torch.zeros(need, dtype=torch.uint8, device=torch.device("cuda", dev))   # on the current stream
+        _PAGED_WS[dev, stream_handle] = ws
+    return ws
+
+
+def fuse_paged_attention(q, k_cache, v_cache, block_table, seq_lens, o, scale: float, prefix_table=None,
+                         prefix_len: int = 0, workspace=None, stream=None) -> None:
+    """o = softmax(scale q k^T) v for one query per sequence (q, o [batch, q_heads, D]) over the first
+    prefix_len keys of prefix_table's pages, which all sequences share, and the first seq_lens[b] keys of
+    block_table[b]'s; k_cache, v_cache [num_pages, kv_heads, page_size, D].  workspace: a zero-filled
+    device tensor (see fuse_paged_attention in the header); None: a buffer kept by this module for the
+    current stream."""
+    import torch
+    dt, i32 = q.dtype, torch.int32
+    dev = _decode_operands((dt, dt, dt, dt, i32, i32, i32), q, k_cache, v_cache, o, block_table, seq_lens, prefix_table)
+    if dt is not torch.bfloat16 and dt is not torch.float16:
+        raise ValueError("fp16 or bf16 tensors expected")
+    batch, q_heads, D = q.shape
+    pages, kv_heads, page_size, D2 = k_cache.shape
+    if (D2 != D or o.shape != q.shape or v_cache.shape != k_cache.shape or block_table.dim() != 2
+            or block_table.shape[0] != batch or seq_lens.shape != (batch,)):
+        raise ValueError("shape mismatch")
+    if prefix_len and (prefix_table is None or prefix_table.numel() * page_size < prefix_len):
+        raise ValueError("prefix_table does not hold prefix_len keys")
+    lib, sh = _load(), _stream(stream)
+    if workspace is None:
+        workspace = _paged_workspace(lib.fuse_paged_attention_workspace_bytes(batch, q_heads, kv_heads, D, prefix_len),
+                                     dev, sh)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("the workspace must be a contiguous tensor on the device of the others")
+    _check(lib.fuse_paged_attention(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                                    block_table.shape[1], seq_lens.data_ptr(), _ptr(prefix_table), prefix_len,
+                                    o.data_ptr(), batch, q_heads, kv_heads, D, pages, page_size, scale,
+                                    FUSE_F16 if dt is torch.float16 else FUSE_BF16, workspace.data_ptr(),
+                                    workspace.numel() * workspace.element_size(), sh), "fuse_paged_attention")
+
+
+def fuse_paged_attention_workspace_bytes(batch: int, q_heads: int, kv_heads: int, D: int, prefix_len: int = 0) -> int:
+    return _load().fuse_paged_attention_workspace_bytes(batch, q_heads, kv_heads, D, prefix_len)
+
+
+def fuse_w4_gemv(x, wq, scales, y, zeros=None, bias=None, residual=None, gelu: bool = False, stream=None) -> None:
+    """y = GELU(x W^T + bias) + residual for x [M, K], M <= 64, and W [N, K] in 4 bits: wq uint8 [N, K / 2]
+    (input 2j in a byte's low half), scales [N, K / group] and zeros uint8 [N, K / group] (None: 8),
+    W = (q - zero) scale.  bias [N], residual [M, N] and the GELU are optional."""
+    import torch
+    dt, u8 = x.dtype, torch.uint8
+    _decode_operands((dt, u8, dt, dt, u8, dt, dt), x, wq, scales, y, zeros, bias, residual)
+    if dt is not torch.bfloat16 and dt is not torch.float16:
+        raise ValueError("fp16 or bf16 tensors expected")
+    M, K = x.shape
+    N, half = wq.shape
+    groups = scales.shape[1] if scales.dim() == 2 else 0
+    if (2 * half != K or groups < 1 or K % groups or scales.shape[0] != N or y.shape != (M, N)
+            or (zeros is not None and zeros.shape != scales.shape) or (bias is not None and bias.shape != (N,))
+            or (residual is not None and residual.shape != y.shape)):
+        raise ValueError("shape mismatch")
+    _check(_load().fuse_w4_gemv(x.data_ptr(), wq.data_ptr(), scales.data_ptr(), _ptr(zeros), _ptr(bias), _ptr(residual),
+                                y.data_ptr(), M, N, K, K // groups, 1 if gelu else 0,
+                                FUSE_F16 if dt is torch.float16 else FUSE_BF16, _stream(stream)), "fuse_w4_gemv")
+
+
+def fuse_rope_append_bytes(tokens: int, appended: int, q_heads: int, kv_heads: int, D: int, rot: int) -> int:
+    return _load().fuse_rope_append_bytes(tokens, appended, q_heads, kv_heads, D, rot)
+
+
+def fuse_paged_attention_bytes(batch: int, q_heads: int, kv_heads: int, D: int, prefix_len: int, keys: int) -> int:
+    return _load().fuse_paged_attention_bytes(batch, q_heads, kv_heads, D, prefix_len, keys)
+
+
+def fuse_paged_attention_flops(batch: int, q_heads: int, D: int, prefix_len: int, keys: int) -> int:
+    return _load().fuse_paged_attention_flops(batch, q_heads, D, prefix_len, keys)
+
+
+def fuse_w4_gemv_bytes(M: int, N: int, K: int, group: int, zeros: bool = False, bias: bool = False,
+                       residual: bool = False) -> int:
+    return _load().fuse_w4_gemv_bytes(M, N, K, group, int(zeros), int(bias), int(residual))
 
 
 # ------------------------------------------------------------------------------- ledgers

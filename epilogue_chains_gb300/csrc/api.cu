@@ -23,7 +23,15 @@ int silu_report_count();
 int silu_report(int i, fuse_kernel_record* out);
 int attn_report_count();
 int attn_report(int i, fuse_kernel_record* out);
-int watchdog_take();  // 1 if a bounded device wait expired since the last call (and clears it)
+int rope_report_count();
+int rope_report(int i, fuse_kernel_record* out);
+int paged_report_count();
+int paged_report(int i, fuse_kernel_record* out);
+int w4_report_count();
+int w4_report(int i, fuse_kernel_record* out);
+// FUSE_ETIMEOUT if a bounded device wait expired, FUSE_EINDEX if a kernel met an index out of range,
+// since the last call (and clears both), else FUSE_OK
+int status_take();
 
 namespace {
 thread_local char t_last_error[256] = "";
@@ -182,6 +190,24 @@ bool make_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols, int
     return r == CUDA_SUCCESS;
 }
 
+bool make_map_3d(CUtensorMap* map, const void* ptr, MapType type, const int64_t (&dims)[3],
+                 const int64_t (&strides)[2], const int (&box)[3], bool swizzle128) {
+    auto enc = encode_fn();
+    if (!enc) return false;
+    cuuint64_t d[3], st[2];
+    cuuint32_t bx[3], estr[3] = {1, 1, 1};
+    for (int i = 0; i < 3; ++i) {
+        d[i] = static_cast<cuuint64_t>(dims[i]);
+        bx[i] = static_cast<cuuint32_t>(box[i]);
+    }
+    for (int i = 0; i < 2; ++i) st[i] = static_cast<cuuint64_t>(strides[i]);
+    CUresult r = enc(map, type == kMapU8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3,
+                     const_cast<void*>(ptr), d, st, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 }  // namespace fc
 
 namespace {
@@ -196,6 +222,9 @@ const ReportTable kTables[] = {
     {fc::gemm_report_count, fc::gemm_report},
     {fc::silu_report_count, fc::silu_report},
     {fc::attn_report_count, fc::attn_report},
+    {fc::rope_report_count, fc::rope_report},
+    {fc::paged_report_count, fc::paged_report},
+    {fc::w4_report_count, fc::w4_report},
 };
 }  // namespace
 
@@ -231,6 +260,7 @@ extern "C" const char* fuse_strerror(int status) {
         case FUSE_EUNSUPPORTED: return "unsupported size or combination";
         case FUSE_ECUDA: return "CUDA launch or runtime error";
         case FUSE_ETIMEOUT: return "bounded device wait expired (watchdog)";
+        case FUSE_EINDEX: return "page, slot, position or length out of range in device memory";
         case FUSE_EWORKSPACE: return "workspace missing or too small";
         default: return "unknown status";
     }
@@ -241,8 +271,7 @@ extern "C" const char* fuse_last_cuda_error(void) { return fc::t_last_error; }
 extern "C" int fuse_check(fuse_stream_t stream) {
     cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fc::record_cuda_error(e);
-    if (fc::watchdog_take()) return FUSE_ETIMEOUT;
-    return FUSE_OK;
+    return fc::status_take();
 }
 
 extern "C" int fuse_version(void) { return (1 << 16) | 0; }

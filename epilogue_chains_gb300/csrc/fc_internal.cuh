@@ -85,6 +85,9 @@ int opt_in_smem(const void* kernel, int bytes, bool max_shared_carveout = false)
 // Device address of the watchdog word on the current device (nullptr on failure).  Kernels with
 // bounded waits take it as a parameter and set it when a wait runs out.
 int* watchdog_flag();
+// Device address of the index word: kernels that read page, slot or position indexes from device
+// memory set it when one is out of range (fuse_check() then returns FUSE_EINDEX).
+int* index_flag();
 
 // Occupancy-derived blocks per SM for a kernel at a block size (cached by caller as needed).
 template <typename K>
@@ -103,6 +106,12 @@ int describe_kernel(const void* kernel, const char* name, int block, int dyn_sme
                     fuse_kernel_record* out, int tmem_cols = 0);
 
 inline bool is_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// True if [a, a + a_bytes) and [b, b + b_bytes) share a byte.
+inline bool ranges_overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + static_cast<uintptr_t>(b_bytes) && y < x + static_cast<uintptr_t>(a_bytes);
+}
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 

@@ -14,6 +14,11 @@ namespace fc {
 // missing or the encoder rejects the arguments (base alignment, strides, box size).
 bool make_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols, int box_cols,
               int box_rows, bool bf16 = false);
+// Host: a TMA descriptor of a 3-D tensor of bytes or of 16-bit elements: extents dims[0..2] (innermost
+// first), byte strides of dims[1] and dims[2], box extents, with or without the 128-byte swizzle.
+enum MapType { kMapU8, kMap16 };
+bool make_map_3d(CUtensorMap* map, const void* ptr, MapType type, const int64_t (&dims)[3],
+                 const int64_t (&strides)[2], const int (&box)[3], bool swizzle128);
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y,
                                             uint32_t bar) {
@@ -21,6 +26,14 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, uint32_t src) {

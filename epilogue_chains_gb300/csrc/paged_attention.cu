@@ -1,0 +1,984 @@
+// paged_attention.cu -- attention of one new token per sequence over a paged key/value cache, with a
+// prefix that the whole batch shares.
+//
+//     o_bh = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m),   s_j = scale q_bh . k_j
+// over the prefix's keys and the sequence's own.  A part of the keys gives (m, l, O) = (reference, sum of
+// 2^(s - m), sum of 2^(s - m) v), s in base-2 units; parts join as m = max m_i, l = sum 2^(m_i - m) l_i
+// and O likewise, so any split of the key axis gives the same result up to fp32 rounding.  Two kernels:
+//
+//  * paged_own_kernel: the sequences' own keys.  Every key and value is used by one group of query heads
+//    only (q_heads / kv_heads rows), so reading them bounds the time.  The work is cut into units of 64
+//    keys of one (sequence, key/value head), numbered in one line, and the CTAs take equal runs of it,
+//    whatever the lengths are: a long sequence is shared by many CTAs, a CTA covers many short ones.
+//    Each warp streams its own 16 keys of every unit through a private TMA ring (no CTA barrier in the
+//    loop) and multiplies them with the query rows by mma.sync (16 rows, mostly one group); the warps'
+//    parts meet in shared memory when a sequence ends.  Parts of a sequence that several CTAs share go
+//    through the workspace: the CTA that arrives last joins them, in the order of the keys.
+//  * paged_prefix_kernel: the shared prefix.  Here all batch * group query rows of a key/value head meet
+//    the same keys: tcgen05 tiles of 128 rows by 128 keys, scores and output in TMEM, the key axis split
+//    over the SMs the same way.  Its parts are joined by paged_own_kernel.
+//
+// The lengths are in device memory, so one launch configuration (and a captured graph) serves every
+// length.  All waits are bounded (watchdog).
+#include <cudaTypedefs.h>
+#include <math.h>
+
+#include <type_traits>
+
+#include "fc_internal.cuh"
+#include "fc_mma.cuh"
+#include "fc_ptx.cuh"
+#include "fc_tc.cuh"
+
+namespace fc {
+namespace {
+
+constexpr int kOwnWarps = 4;
+constexpr int kOwnThreads = 32 * kOwnWarps;
+constexpr int kChunk = 16;                        // keys of a warp per unit
+constexpr int kUnit = kChunk * kOwnWarps;         // keys of a unit
+constexpr int kOwnGrid = 320;                     // most CTAs of paged_own_kernel (workspace bound)
+constexpr int kCounterBytes = 2048;
+static_assert(kOwnGrid * 4 <= kCounterBytes, "one counter per CTA");
+constexpr int kPrefixGrid = 160;                  // most CTAs of paged_prefix_kernel (workspace bound)
+constexpr int kMaxBatch = 4096;
+constexpr int kOwnSmem = 226 * 1024;              // dynamic shared memory at most, next to a few static words
+// A running reference is replaced when a row's maximum exceeds it by more than 2^8, so weights stay
+// within [0, 2^8]; for fp16 weights it is also set 2^7 below the maximum, which uses fp16's range
+// upwards (2^15 at most) and keeps weights down to 2^-21 of the maximum at full precision.
+constexpr float kLag = 8.0f;
+template <typename T> struct Shift { static constexpr float V = 0.0f; };
+template <> struct Shift<__half> { static constexpr float V = 7.0f; };
+
+__device__ __forceinline__ float ex2f(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float max3f(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+struct PagedArgs {
+    const void* q;
+    void* o;
+    const int32_t *table, *lens, *ptable;
+    int64_t table_ld;
+    int batch, hq, hk, group, rt;      // rt = ceil(group / 16) row tiles of a key/value head
+    int rows;                          // query rows of a tile, at most 16
+    int page_shift, num_pages;
+    int cache_rows;                    // num_pages hk page_size: a row past the cache reads zeros
+    float c;                           // scale * log2(e)
+    int stages;
+    uint32_t off_om, off_ml, off_bar, off_pre;
+    // workspace
+    // A CTA's run has at most one item that began in an earlier CTA (its part has slot 2 c) and one
+    // that goes on in a later one (slot 2 c + 1 if it begins here; an item begins in one CTA, which
+    // names its counter).
+    int* count;                        // [kOwnGrid] parts that have arrived, by the item's first CTA
+    float *oml, *oo;                   // [2 kOwnGrid][rows] (m, l) and [..][rows][D]
+    float *pml, *po;                   // [kPrefixGrid + pitems][128] (m, l, l', -) and [..][128][D]
+    // prefix
+    int plen, ptiles, prt, pgrid;      // keys, 128-key tiles, 128-row tiles of a head, CTAs
+    int *flag, *bad;
+};
+
+// The CTA of `grid` that a unit belongs to when CTA c takes units [c U / grid, (c + 1) U / grid).
+__device__ __forceinline__ int cta_of(int64_t u, int64_t U, int64_t grid) {
+    return static_cast<int>(((u + 1) * grid - 1) / U);
+}
+
+// Join (m, l, acc) with another part; a part without keys has m = -inf, l = 0.
+__device__ __forceinline__ void join(float& m, float& l, float4& acc, float m2, float l2, const float4& o2) {
+    if (m2 == -INFINITY) return;
+    const float nm = fmaxf(m, m2);
+    const float a = m == -INFINITY ? 0.0f : ex2f(m - nm), b = ex2f(m2 - nm);
+    l = l * a + l2 * b;
+    acc.x = acc.x * a + o2.x * b;
+    acc.y = acc.y * a + o2.y * b;
+    acc.z = acc.z * a + o2.z * b;
+    acc.w = acc.w * a + o2.w * b;
+    m = nm;
+}
+
+// ================================================================== the sequences' own keys
+template <int D>
+struct OwnLayout {
+    static constexpr uint32_t ATOM = kChunk * 128;               // 16 keys x 64 components
+    static constexpr uint32_t KV = ATOM * (D / 64);              // K or V of a chunk
+    static constexpr uint32_t STAGE = 2 * KV;
+    static constexpr int CTAS = D == 256 ? 1 : 2;                // per SM
+    static constexpr uint32_t BUDGET = (D == 256 ? 224u : 111u) * 1024u;
+};
+
+// Where a CTA or a warp's loads are in the line of units.
+struct Cursor {
+    int left;        // units left of the CTA's run, this one included
+    int b, hr;       // sequence; key/value head * rt + row tile
+    int j, n, len;   // unit of the sequence, their number, its keys
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kOwnThreads, OwnLayout<D>::CTAS) paged_own_kernel(
+    const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
+    const __grid_constant__ PagedArgs a) {
+    using L = OwnLayout<D>;
+    pdl_trigger();
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    uint8_t* gbase = smem_raw + (base - smem_addr(smem_raw));
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int g = lane / 4, t = lane % 4;
+    float* om = reinterpret_cast<float*>(gbase + a.off_om);      // [warp][rows][D]
+    float* ml = reinterpret_cast<float*>(gbase + a.off_ml);      // [warp][rows][2]
+    int* pre = reinterpret_cast<int*>(gbase + a.off_pre);        // [batch + 1] units before a sequence
+    int* slen = pre + a.batch + 1;                               // [batch]
+    __shared__ int wsum[kOwnWarps];
+    __shared__ int is_last;
+    auto bar = [&](int s) { return base + a.off_bar + 8u * (warp * a.stages + s); };
+    if (lane == 0) {
+        for (int s = 0; s < a.stages; ++s) mbar_init(bar(s), 1);
+        fence_mbar_init();
+        if (warp == 0) {
+            prefetch_map(&mK);
+            prefetch_map(&mV);
+        }
+    }
+    pdl_wait();  // the preceding kernel (the prefix kernel, if there is one) has completed
+
+    // ------------------------------------------------------------ units of every sequence
+    const int page_size = 1 << a.page_shift;
+    {
+        const int64_t most = a.table_ld << a.page_shift;
+        const int per = (a.batch + kOwnThreads - 1) / kOwnThreads, b0 = tid * per;
+        int sum = 0;
+        for (int b = b0; b < b0 + per && b < a.batch; ++b) {
+            int n = a.lens[b];
+            if (n < 0 || n > most) {
+                if (blockIdx.x == 0) atomicExch(a.bad, 1);
+                n = n < 0 ? 0 : static_cast<int>(most);
+            }
+            slen[b] = n;
+            sum += n > kUnit ? (n - 1) / kUnit + 1 : 1;
+        }
+        int scan = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, scan, o);
+            if (lane >= o) scan += v;
+        }
+        if (lane == 31) wsum[warp] = scan;
+        __syncthreads();
+        int at = scan - sum;
+        for (int w = 0; w < warp; ++w) at += wsum[w];
+        for (int b = b0; b < b0 + per && b < a.batch; ++b) {
+            pre[b] = at;
+            at += slen[b] > kUnit ? (slen[b] - 1) / kUnit + 1 : 1;
+            if (b == a.batch - 1) pre[a.batch] = at;
+        }
+        __syncthreads();
+    }
+    const int HR = a.hk * a.rt;
+    const int64_t U = static_cast<int64_t>(pre[a.batch]) * HR;
+    const int G = static_cast<int>(min(static_cast<int64_t>(gridDim.x), U));   // CTAs with work: one unit at least
+    if (static_cast<int>(blockIdx.x) >= G) return;
+    const int64_t u0 = blockIdx.x * U / G, u1 = (blockIdx.x + 1) * U / G;
+
+    auto enter = [&](Cursor& k) {   // sequence k.b
+        k.n = pre[k.b + 1] - pre[k.b];
+        k.len = slen[k.b];
+    };
+    auto next = [&](Cursor& k) {
+        --k.left;
+        if (++k.j < k.n) return;
+        k.j = 0;
+        if (++k.hr < HR) return;
+        k.hr = 0;
+        if (++k.b < a.batch) enter(k);
+    };
+    Cursor cur;
+    {
+        int lo = 0, hi = a.batch - 1;   // the last sequence that starts at or before u0
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (static_cast<int64_t>(pre[mid]) * HR <= u0) lo = mid; else hi = mid - 1;
+        }
+        cur.left = static_cast<int>(u1 - u0);
+        cur.b = lo;
+        enter(cur);
+        const int64_t in = u0 - static_cast<int64_t>(pre[lo]) * HR;
+        cur.hr = static_cast<int>(in / cur.n);
+        cur.j = static_cast<int>(in % cur.n);
+    }
+    auto key0 = [&](const Cursor& k) { return k.j * kUnit + warp * kChunk; };   // first key of this warp
+    // -------------------------------------------------------------------- loads
+    const uint32_t ring = base + static_cast<uint32_t>(warp * a.stages) * L::STAGE;
+    Cursor ahead = cur;
+    int fs = 0, pending = 0;     // stage loaded next; chunks loaded and not used yet
+    auto skip_empty = [&] {
+        while (ahead.left > 0 && key0(ahead) >= ahead.len) next(ahead);
+    };
+    int page = -1;
+    auto look = [&] {   // the page of the chunk that is loaded next
+        skip_empty();
+        if (ahead.left > 0) page = a.table[ahead.b * a.table_ld + (key0(ahead) >> a.page_shift)];
+    };
+    auto fetch = [&] {
+        if (ahead.left <= 0) return;
+        if (lane == 0) {
+            int row = a.cache_rows;     // past the cache: zeros
+            if (page >= 0 && page < a.num_pages)
+                row = ((page * a.hk + ahead.hr / a.rt) << a.page_shift) + (key0(ahead) & (page_size - 1));
+            else
+                atomicExch(a.bad, 1);
+            const uint32_t dst = ring + static_cast<uint32_t>(fs) * L::STAGE;
+            mbar_arrive_expect_tx(bar(fs), L::STAGE);
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) tma_load_2d(dst + i * L::ATOM, &mK, 64 * i, row, bar(fs));
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) tma_load_2d(dst + L::KV + i * L::ATOM, &mV, 64 * i, row, bar(fs));
+        }
+        if (++fs == a.stages) fs = 0;
+        ++pending;
+        next(ahead);
+        look();
+    };
+    look();
+    for (int s = 0; s < a.stages; ++s) fetch();
+
+    // -------------------------------------------------------------------- units
+    int cs = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    // ldmatrix addresses: key and 16-byte column of this lane's matrix row, K and V (transposed)
+    const int kkey = ((lane >> 4) << 3) | (lane & 7), kcol = (lane >> 3) & 1;
+    const int vkey = (((lane >> 3) & 1) << 3) | (lane & 7), vcol = lane >> 4;
+    while (cur.left > 0) {
+        // ---- a run of units of one sequence and head: this CTA's part of it
+        const int b = cur.b, hr = cur.hr, j0 = cur.j, n = cur.n;
+        const int head = hr / a.rt, row0 = (hr % a.rt) * 16;
+        const int rows = min(a.rows, a.group - row0);
+        const int j1 = min(n - j0, cur.left) + j0;
+        uint32_t qf[D / 16][4];
+        {
+            const T* q = static_cast<const T*>(a.q) + (static_cast<int64_t>(b) * a.hq + head * a.group + row0) * D;
+            const uint32_t* q0 = reinterpret_cast<const uint32_t*>(q + static_cast<int64_t>(g) * D + 2 * t);
+            const uint32_t* q1 = reinterpret_cast<const uint32_t*>(q + static_cast<int64_t>(g + 8) * D + 2 * t);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                qf[k][0] = g < rows ? q0[8 * k] : 0u;
+                qf[k][1] = g + 8 < rows ? q1[8 * k] : 0u;
+                qf[k][2] = g < rows ? q0[8 * k + 4] : 0u;
+                qf[k][3] = g + 8 < rows ? q1[8 * k + 4] : 0u;
+            }
+        }
+        float o[D / 8][4] = {};
+        float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;   // rows g and g + 8
+        for (int j = j0; j < j1; ++j, next(cur)) {
+            const int nv = cur.len - key0(cur);      // keys of the chunk in use
+            if (nv <= 0 || !ok) continue;
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar(cs), phase, a.flag))) {
+                ok = false;
+                continue;
+            }
+            const uint32_t kb = ring + static_cast<uint32_t>(cs) * L::STAGE, vb = kb + L::KV;
+            float s[2][4] = {};
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                uint32_t f[4];
+                ldsm4(f, kb + (k / 4) * L::ATOM + kkey * 128 + ((((2 * k + kcol) & 7) ^ (kkey & 7)) << 4));
+                mma16816<T>(s[0], qf[k], f[0], f[1]);
+                mma16816<T>(s[1], qf[k], f[2], f[3]);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    s[i][e] *= a.c;
+                    if (8 * i + 2 * t + (e & 1) >= nv) s[i][e] = -INFINITY;
+                }
+            float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
+            float x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+            x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
+            x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
+            x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
+            x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
+            constexpr float SH = Shift<T>::V;
+            const bool up0 = x0 > m0 + (SH + kLag), up1 = x1 > m1 + (SH + kLag);
+            if (__any_sync(0xffffffffu, up0 || up1)) {
+                const float n0 = up0 ? x0 - SH : m0, n1 = up1 ? x1 - SH : m1;
+                const float a0 = up0 ? ex2f(m0 - n0) : 1.0f, a1 = up1 ? ex2f(m1 - n1) : 1.0f;
+                m0 = n0;
+                m1 = n1;
+                l0 *= a0;
+                l1 *= a1;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    o[i][0] *= a0;
+                    o[i][1] *= a0;
+                    o[i][2] *= a1;
+                    o[i][3] *= a1;
+                }
+            }
+            const float r0 = m0 == -INFINITY ? 0.0f : m0, r1 = m1 == -INFINITY ? 0.0f : m1;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                s[i][0] = ex2f(s[i][0] - r0);
+                s[i][1] = ex2f(s[i][1] - r0);
+                s[i][2] = ex2f(s[i][2] - r1);
+                s[i][3] = ex2f(s[i][3] - r1);
+            }
+            l0 += (s[0][0] + s[0][1]) + (s[1][0] + s[1][1]);
+            l1 += (s[0][2] + s[0][3]) + (s[1][2] + s[1][3]);
+            // the weights rounded to T for the product with V; the sums above are of the unrounded ones
+            const uint32_t p[4] = {pack2<T>(s[0][0], s[0][1]), pack2<T>(s[0][2], s[0][3]),
+                                   pack2<T>(s[1][0], s[1][1]), pack2<T>(s[1][2], s[1][3])};
+            auto pv = [&](auto tail) {
+                // keys past the sequence's end: 0 x whatever lies in the page must be 0
+                const uint32_t k0 = tail ? (2 * t < nv ? 0xFFFFu : 0u) | (2 * t + 1 < nv ? 0xFFFF0000u : 0u) : 0u;
+                const uint32_t k1 = tail ? (2 * t + 8 < nv ? 0xFFFFu : 0u) | (2 * t + 9 < nv ? 0xFFFF0000u : 0u) : 0u;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    uint32_t f[4];
+                    ldsm4_t(f, vb + (k / 4) * L::ATOM + vkey * 128 + ((((2 * k + vcol) & 7) ^ (vkey & 7)) << 4));
+                    if (tail) {
+                        f[0] &= k0;
+                        f[1] &= k1;
+                        f[2] &= k0;
+                        f[3] &= k1;
+                    }
+                    mma16816<T>(o[2 * k], p, f[0], f[1]);
+                    mma16816<T>(o[2 * k + 1], p, f[2], f[3]);
+                }
+            };
+            if (nv >= kChunk) pv(std::false_type{});
+            else pv(std::true_type{});
+            __syncwarp();       // every lane has read the stage
+            --pending;
+            if (++cs == a.stages) {
+                cs = 0;
+                phase ^= 1u;
+            }
+            fetch();
+        }
+        // ---- the warps' parts
+        l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+        l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+            if (g < rows) *reinterpret_cast<float2*>(om + (warp * a.rows + g) * D + 8 * i + 2 * t) = make_float2(o[i][0], o[i][1]);
+            if (g + 8 < rows) *reinterpret_cast<float2*>(om + (warp * a.rows + g + 8) * D + 8 * i + 2 * t) = make_float2(o[i][2], o[i][3]);
+        }
+        if (t == 0) {
+            if (g < rows) {
+                ml[(warp * a.rows + g) * 2] = m0;
+                ml[(warp * a.rows + g) * 2 + 1] = l0;
+            }
+            if (g + 8 < rows) {
+                ml[(warp * a.rows + g + 8) * 2] = m1;
+                ml[(warp * a.rows + g + 8) * 2 + 1] = l1;
+            }
+        }
+        __syncthreads();
+        const bool whole = j0 == 0 && j1 == n;
+        const int64_t first = static_cast<int64_t>(pre[b]) * HR + static_cast<int64_t>(hr) * n;   // the item's first unit
+        // the parts of the shared prefix, then the division
+        auto finish = [&](int r, int col, float m, float l, float4 acc) {
+            if (a.plen > 0) {
+                const int prow = b * a.group + row0 + r;
+                const int pit = head * a.prt + prow / 128, lr = prow % 128;
+                const int64_t PU = static_cast<int64_t>(a.hk) * a.prt * a.ptiles, p0 = static_cast<int64_t>(pit) * a.ptiles;
+                const int c1 = cta_of(p0 + a.ptiles - 1, PU, a.pgrid);
+                for (int c = cta_of(p0, PU, a.pgrid); c <= c1; ++c) {
+                    const int64_t at = static_cast<int64_t>(c + pit) * 128 + lr;
+                    const float4 pm = *reinterpret_cast<const float4*>(a.pml + at * 4);
+                    join(m, l, acc, pm.x, pm.y + pm.z, *reinterpret_cast<const float4*>(a.po + at * D + 4 * col));
+                }
+            }
+            // l == 0: no key (or none with a score above -inf): zeros
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            uint2 w;
+            w.x = l == 0.0f ? 0u : pack2<T>(acc.x * inv, acc.y * inv);
+            w.y = l == 0.0f ? 0u : pack2<T>(acc.z * inv, acc.w * inv);
+            T* dst = static_cast<T*>(a.o) + (static_cast<int64_t>(b) * a.hq + head * a.group + row0 + r) * D + 4 * col;
+            *reinterpret_cast<uint2*>(dst) = w;
+        };
+        for (int i = tid; i < rows * (D / 4); i += kOwnThreads) {
+            const int r = i / (D / 4), col = i % (D / 4);
+            float m = -INFINITY, l = 0.0f;
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int w = 0; w < kOwnWarps; ++w) {
+                const int at = w * a.rows + r;
+                join(m, l, acc, ml[2 * at], ml[2 * at + 1], *reinterpret_cast<const float4*>(om + at * D + 4 * col));
+            }
+            if (whole) {
+                finish(r, col, m, l, acc);
+            } else {
+                const int64_t at = static_cast<int64_t>(2 * blockIdx.x + (j0 == 0 ? 1 : 0)) * a.rows + r;
+                if (col == 0) *reinterpret_cast<float2*>(a.oml + 2 * at) = make_float2(m, l);
+                *reinterpret_cast<float4*>(a.oo + at * D + 4 * col) = acc;
+            }
+        }
+        if (!whole) {
+            const int c0 = cta_of(first, U, G), c1 = cta_of(first + n - 1, U, G);
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) is_last = atomicAdd(a.count + c0, 1) == c1 - c0;
+            __syncthreads();
+            if (is_last) {
+                __threadfence();
+                for (int i = tid; i < rows * (D / 4); i += kOwnThreads) {
+                    const int r = i / (D / 4), col = i % (D / 4);
+                    float m = -INFINITY, l = 0.0f;
+                    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+                    for (int c = c0; c <= c1; ++c) {
+                        const int64_t at = static_cast<int64_t>(2 * c + (c == c0 ? 1 : 0)) * a.rows + r;
+                        const float2 q = __ldcg(reinterpret_cast<const float2*>(a.oml + 2 * at));
+                        join(m, l, acc, q.x, q.y, __ldcg(reinterpret_cast<const float4*>(a.oo + at * D + 4 * col)));
+                    }
+                    finish(r, col, m, l, acc);
+                }
+                if (tid == 0) a.count[c0] = 0;
+            }
+        }
+        __syncthreads();        // om, ml and is_last are free for the next part
+    }
+    // after a wait that ran out: the copies in flight land before the shared memory goes away
+    for (; pending > 0; --pending) {
+        (void)mbar_wait_drain(bar(cs), phase);
+        if (++cs == a.stages) {
+            cs = 0;
+            phase ^= 1u;
+        }
+    }
+}
+
+// ================================================================== the shared prefix
+constexpr int kPreSoftmaxWarps = 8;                       // two per TMEM lane quadrant
+constexpr int kPreThreads = 32 * (3 + kPreSoftmaxWarps);  // warp 0: K, 1: MMA issue, 2: V, 3-10: softmax
+
+template <int D>
+struct PrefixLayout {
+    static constexpr int ATOMS = D / 64;
+    static constexpr int KV = D == 64 ? 4 : D == 128 ? 2 : 1;  // K and V stages
+    static constexpr uint32_t REGION = 128 * 128;              // one 64-column atom of 128 rows
+    static constexpr uint32_t TILE = REGION * ATOMS;           // Q, K or V: 128 rows x D
+    static constexpr uint32_t P_BYTES = 128 * 128 * 2;
+    static constexpr uint32_t OFF_Q = 0;
+    static constexpr uint32_t OFF_K = TILE;
+    static constexpr uint32_t OFF_V = OFF_K + KV * TILE;
+    static constexpr uint32_t OFF_P = OFF_V + KV * TILE;
+    static constexpr uint32_t OFF_BAR = OFF_P + P_BYTES;
+    static constexpr int N_BARS = 2 + 4 * KV + 2 + 4;
+    static constexpr uint32_t OFF_HOLD = OFF_BAR + N_BARS * 8;
+    static constexpr uint32_t SMEM = OFF_HOLD + 16 + 1024;
+    static constexpr uint32_t TMEM_COLS = 512, O_COL = 256;    // two 128-column score buffers, then O
+    static_assert(SMEM <= 232448, "shared-memory budget");
+};
+
+// One CTA per SM walks an equal run of (128-row tile of a key/value head, 128-key tile) pairs.  Per row
+// tile it loads Q (rows b * group + i of the head), then S_j = Q K_j^T into one of two TMEM buffers while
+// the softmax warps work on the other, P_j = 2^(S_j c - m) into shared memory, O += P_j V_j in TMEM, and
+// at the end of the run it writes (m, l, O) as the run's part.
+template <typename T, int D>
+__global__ void __launch_bounds__(kPreThreads, 1) paged_prefix_kernel(const __grid_constant__ CUtensorMap mK,
+                                                                      const __grid_constant__ CUtensorMap mV,
+                                                                      const __grid_constant__ PagedArgs a) {
+    using L = PrefixLayout<D>;
+    constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
+    pdl_trigger();
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    uint8_t* gbase = smem_raw + (base - smem_addr(smem_raw));
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    constexpr int KV = L::KV;
+    const uint32_t bar0 = base + L::OFF_BAR;
+    // A ring of n buffers used by tiles i = 0, 1, ... of this CTA: buffer i % n, parity (i / n) & 1.
+    const uint32_t q_full = bar0, drain = bar0 + 8;
+    auto k_full = [&](int i) { return bar0 + 8u * (2 + i); };
+    auto k_empty = [&](int i) { return bar0 + 8u * (2 + KV + i); };
+    auto v_full = [&](int i) { return bar0 + 8u * (2 + 2 * KV + i); };
+    auto v_empty = [&](int i) { return bar0 + 8u * (2 + 3 * KV + i); };
+    const uint32_t p_full = bar0 + 8u * (2 + 4 * KV), o_done = p_full + 8;
+    auto s_full = [&](int i) { return bar0 + 8u * (4 + 4 * KV + i); };
+    auto s_free = [&](int i) { return bar0 + 8u * (6 + 4 * KV + i); };
+    int* flag = a.flag;
+    if (threadIdx.x == 0) {
+        mbar_init(q_full, kPreSoftmaxWarps);
+        mbar_init(drain, 1);
+        for (int i = 0; i < KV; ++i) {
+            mbar_init(k_full(i), 1);
+            mbar_init(k_empty(i), 1);
+            mbar_init(v_full(i), 1);
+            mbar_init(v_empty(i), 1);
+        }
+        mbar_init(p_full, kPreSoftmaxWarps);
+        mbar_init(o_done, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(s_full(i), 1);
+            mbar_init(s_free(i), kPreSoftmaxWarps);
+        }
+        fence_mbar_init();
+    }
+    if (warp == 1) tmem_alloc(base + L::OFF_HOLD, L::TMEM_COLS);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + L::OFF_HOLD);
+    pdl_wait();
+
+    const int64_t U = static_cast<int64_t>(a.hk) * a.prt * a.ptiles;
+    const int64_t u0 = blockIdx.x * U / gridDim.x, u1 = (blockIdx.x + 1) * U / gridDim.x;
+    auto keys_of = [&](int tile) { return min(128, a.plen - tile * 128); };
+
+    if (warp == 0 || warp == 2) {
+        // ---------------------------------------------------------------- K and V loads
+        // a tile is 128 / box boxes of one page each, loaded by one lane each
+        const bool is_k = warp == 0;
+        const CUtensorMap* map = is_k ? &mK : &mV;
+        const int box_shift = min(a.page_shift, 7);
+        if (lane == 0) prefetch_map(map);
+        int i = 0;
+        const int total = static_cast<int>(u1 - u0);
+        for (; i < total; ++i) {
+            const int64_t u = u0 + i;
+            const int tile = static_cast<int>(u % a.ptiles), head = static_cast<int>(u / a.ptiles) / a.prt;
+            const int st = i % KV;
+            const uint32_t full = is_k ? k_full(st) : v_full(st), empty = is_k ? k_empty(st) : v_empty(st);
+            const int nbox = (keys_of(tile) + (1 << box_shift) - 1) >> box_shift;
+            int row = a.cache_rows;
+            if (lane < nbox) {
+                const int key = tile * 128 + (lane << box_shift);
+                const int page = a.ptable[key >> a.page_shift];
+                if (page >= 0 && page < a.num_pages)
+                    row = ((page * a.hk + head) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+                else
+                    atomicExch(a.bad, 1);
+            }
+            if (i >= KV && !__all_sync(0xffffffffu, mbar_wait_bounded(empty, ((i - KV) / KV) & 1, flag))) break;
+            if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(nbox << box_shift) * (D * 2));
+            __syncwarp();
+            if (lane < nbox) {
+                const uint32_t dst = base + (is_k ? L::OFF_K : L::OFF_V) + st * L::TILE + (static_cast<uint32_t>(lane) << box_shift) * 128;
+                for (int c = 0; c < L::ATOMS; ++c) tma_load_2d(dst + c * L::REGION, map, 64 * c, row, full);
+            }
+        }
+        if (i < total)   // copies in flight land before the shared memory goes away
+            for (int j = i - KV < 0 ? 0 : i - KV; j < i; ++j)
+                (void)mbar_wait_drain(is_k ? k_full(j % KV) : v_full(j % KV), (j / KV) & 1);
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- MMA issue
+        if (lane == 0) {
+            constexpr uint32_t idS = idesc_f16(128, 128, false, false, BF);
+            constexpr uint32_t idO = idesc_f16(128, D, false, true, BF);
+            bool issued = false, ok = true;
+            auto issue_s = [&](int i) -> bool {
+                const int st = i % KV, sb = i & 1;
+                if (!mbar_wait_bounded(k_full(st), (i / KV) & 1, flag)) return false;
+                if (i >= 2 && !mbar_wait_bounded(s_free(sb), ((i - 2) / 2) & 1, flag)) return false;
+                tc_fence_after();
+                const uint32_t kb = base + L::OFF_K + st * L::TILE;
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s)
+                    tc_mma(tmem + sb * 128, smem_desc_sw128(base + L::OFF_Q + (s / 4) * L::REGION + (s % 4) * 32, 16, 1024),
+                           smem_desc_sw128(kb + (s / 4) * L::REGION + (s % 4) * 32, 16, 1024), idS, s > 0 ? 1u : 0u);
+                tc_commit(s_full(sb));
+                tc_commit(k_empty(st));
+                issued = true;
+                return true;
+            };
+            auto issue_pv = [&](int i, bool first) -> bool {
+                const int st = i % KV;
+                if (!mbar_wait_bounded(p_full, i & 1, flag)) return false;
+                if (!mbar_wait_bounded(v_full(st), (i / KV) & 1, flag)) return false;
+                tc_fence_after();
+                const uint32_t vb = base + L::OFF_V + st * L::TILE;
+#pragma unroll
+                for (int s = 0; s < 8; ++s)   // 16 keys each: P atom s / 4; V rows 16 s ..
+                    tc_mma(tmem + L::O_COL, smem_desc_sw128(base + L::OFF_P + (s / 4) * L::REGION + (s % 4) * 32, 16, 1024),
+                           smem_desc_sw128(vb + s * 2048, L::REGION, 1024), idO, !first || s > 0 ? 1u : 0u);
+                tc_commit(o_done);
+                tc_commit(v_empty(st));
+                issued = true;
+                return true;
+            };
+            int i = 0, seg = 0;
+            for (int64_t u = u0; ok && u < u1; ++seg) {
+                const int n = static_cast<int>(min(static_cast<int64_t>(a.ptiles) - u % a.ptiles, u1 - u));
+                ok = mbar_wait_bounded(q_full, seg & 1, flag);
+                if (ok) ok = issue_s(i);
+                for (int j = 0; ok && j < n; ++j) {
+                    if (j + 1 < n) ok = issue_s(i + j + 1);
+                    if (ok) ok = issue_pv(i + j, j == 0);
+                }
+                i += n;
+                u += n;
+            }
+            if (!ok && issued) {   // MMAs in flight finish before TMEM is freed
+                tc_commit(drain);
+                (void)mbar_wait_drain(drain, 0);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------------------- softmax
+        // Warp w serves TMEM lane quadrant w % 4 (query rows 32 (w % 4) + lane) and half hh of each tile's
+        // keys and of O's columns; both warps of a quadrant read the whole score row for its maximum.
+        const int qd = warp % 4, hh = (warp - 3) / 4, r = 32 * qd + lane;
+        const uint32_t lanes = static_cast<uint32_t>(32 * qd) << 16;
+        const int sid = (warp - 3) * 32 + lane;     // 0..255
+        const int total_rows = a.batch * a.group;
+        constexpr float SH = Shift<T>::V;
+        constexpr int HK = 64;
+        bool ok = true;
+        int i = 0;
+        for (int64_t u = u0; ok && u < u1;) {
+            const int item = static_cast<int>(u / a.ptiles), t0 = static_cast<int>(u % a.ptiles);
+            const int n = static_cast<int>(min(static_cast<int64_t>(a.ptiles) - t0, u1 - u));
+            const int head = item / a.prt, qrow0 = (item % a.prt) * 128;
+            // Q: row qrow0 + k of the head is query head `head * group + (..) % group` of sequence (..) / group.
+            // The MMAs that read the previous tile's Q have completed (its last O was waited for).
+            for (int v = sid; v < 128 * (D / 8); v += 32 * kPreSoftmaxWarps) {
+                const int k = v / (D / 8), ch = v % (D / 8), row = qrow0 + k;
+                uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                if (row < total_rows)
+                    x = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (static_cast<int64_t>(row / a.group) * a.hq + head * a.group + row % a.group) * D + 8 * ch);
+                *reinterpret_cast<uint4*>(gbase + L::OFF_Q + (ch / 8) * L::REGION + k * 128 + (((ch % 8) ^ (k & 7)) << 4)) = x;
+            }
+            fence_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
+            float m = -INFINITY, l = 0.0f;
+            for (int j = 0; j < n; ++j, ++i) {
+                const int sb = i & 1, nk = keys_of(t0 + j);
+                if (!__all_sync(0xffffffffu, mbar_wait_bounded(s_full(sb), (i / 2) & 1, flag))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                float s[HK], so[HK];
+                const uint32_t sbase = tmem + lanes + sb * 128;
+#pragma unroll
+                for (int k = 0; k < HK / 32; ++k) {
+                    tmem_ld32(sbase + HK * hh + 32 * k, s + 32 * k);
+                    tmem_ld32(sbase + HK * (1 - hh) + 32 * k, so + 32 * k);
+                }
+                tmem_ld_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s_free(sb));
+                if (nk < 128) {   // keys past the prefix's end
+                    const int ts = nk - HK * hh, to = nk - HK * (1 - hh);
+#pragma unroll
+                    for (int k = 0; k < HK; ++k) {
+                        s[k] = k >= ts ? -INFINITY : s[k];
+                        so[k] = k >= to ? -INFINITY : so[k];
+                    }
+                }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int k = 0; k < HK; ++k) mx[k & 3] = max3f(mx[k & 3], s[k], so[k]);
+                const float x = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.c;
+                float alpha = 1.0f;
+                bool rescale = false;
+                if (x > m + (SH + kLag)) {
+                    if (j > 0) {
+                        alpha = ex2f(m - (x - SH));
+                        rescale = true;
+                    }
+                    m = x - SH;
+                }
+                const float ref = m == -INFINITY ? 0.0f : m;
+                uint32_t pk[HK / 2];
+                const float2 c2 = make_float2(a.c, a.c), nm2 = make_float2(-ref, -ref);
+                float2 sum2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+                for (int k = 0; k < HK; k += 2) {
+                    const float2 e = __ffma2_rn(make_float2(s[k], s[k + 1]), c2, nm2);
+                    const float2 p = make_float2(ex2f(e.x), ex2f(e.y));
+                    sum2 = __fadd2_rn(sum2, p);
+                    pk[k / 2] = pack2<T>(p.x, p.y);
+                }
+                l = l * alpha + (sum2.x + sum2.y);
+                // P and O are free once the previous tile's PV has completed
+                if (i > 0 && !__all_sync(0xffffffffu, mbar_wait_bounded(o_done, (i - 1) & 1, flag))) {
+                    ok = false;
+                    break;
+                }
+                if (__any_sync(0xffffffffu, rescale)) {
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int k = 0; k < D / 64; ++k) {
+                        const uint32_t col = L::O_COL + (D / 2) * hh + 32 * k;
+                        float o[32];
+                        tmem_ld32(tmem + lanes + col, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] *= alpha;
+                        tmem_st32(tmem + lanes + col, o);
+                    }
+                    tmem_st_wait();
+                }
+                uint8_t* prow = gbase + L::OFF_P + r * 128;
+#pragma unroll
+                for (int q = 0; q < HK / 8; ++q) {
+                    const int ch = (HK / 8) * hh + q;
+                    *reinterpret_cast<uint4*>(prow + (ch / 8) * L::REGION + (((ch % 8) ^ (r & 7)) << 4)) =
+                        make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
+                }
+                if (nk < 128) {   // V rows past the end: 0 x whatever lies there must be 0
+                    const int st = i % KV;
+                    if (!__all_sync(0xffffffffu, mbar_wait_bounded(v_full(st), (i / KV) & 1, flag))) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* vb = gbase + L::OFF_V + st * L::TILE;
+                    for (int v = sid; v < (128 - nk) * L::ATOMS * 8; v += 32 * kPreSoftmaxWarps) {
+                        const int row = nk + v / (L::ATOMS * 8), c = v % (L::ATOMS * 8);
+                        *reinterpret_cast<uint4*>(vb + (c / 8) * L::REGION + row * 128 + (c % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+                fence_async_smem();   // the generic-proxy writes become visible to the tensor core
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full);
+            }
+            if (ok && !__all_sync(0xffffffffu, mbar_wait_bounded(o_done, (i - 1) & 1, flag))) ok = false;
+            if (ok) {
+                tc_fence_after();
+                const int64_t at = (static_cast<int64_t>(blockIdx.x) + item) * 128 + r;
+                const bool in = qrow0 + r < total_rows;
+                if (in) {
+                    if (hh == 0) *reinterpret_cast<float2*>(a.pml + at * 4) = make_float2(m, l);
+                    else a.pml[at * 4 + 2] = l;
+                }
+                float* dst = a.po + at * D + (D / 2) * hh;
+#pragma unroll 1
+                for (int k = 0; k < D / 64; ++k) {
+                    float o[32];
+                    tmem_ld32(tmem + lanes + L::O_COL + (D / 2) * hh + 32 * k, o);
+                    tmem_ld_wait();
+                    if (in)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            *reinterpret_cast<float4*>(dst + 32 * k + 4 * e) = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                }
+            }
+            u += n;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, L::TMEM_COLS);
+    }
+}
+
+// ================================================================== host side
+struct Sizes {
+    int64_t rows, pitems;            // rows per part of own keys; prefix row tiles
+    size_t count, oml, oo, pml, po;  // byte offsets of the workspace's parts
+    size_t bytes;
+};
+Sizes sizes(int64_t batch, int64_t hq, int64_t hk, int64_t D, int64_t plen) {
+    Sizes s{};
+    const int64_t group = hq / hk;
+    s.rows = group < 16 ? group : 16;
+    s.pitems = plen > 0 ? hk * ceil_div(batch * group, 128) : 0;
+    size_t at = 0;
+    auto part = [&](int64_t n) {
+        const size_t was = at;
+        at += (static_cast<size_t>(n) + 255) / 256 * 256;
+        return was;
+    };
+    s.count = part(kCounterBytes);   // at the same place whatever the sizes
+    s.oml = part(2 * kOwnGrid * s.rows * 8);
+    s.oo = part(2 * kOwnGrid * s.rows * D * 4);
+    if (plen > 0) {
+        s.pml = part((kPrefixGrid + s.pitems) * 128 * 16);
+        s.po = part((kPrefixGrid + s.pitems) * 128 * D * 4);
+    }
+    s.bytes = at;
+    return s;
+}
+
+template <typename T, int D>
+int own_smem(PagedArgs* a, uint32_t* bytes) {
+    using L = OwnLayout<D>;
+    const uint32_t om = static_cast<uint32_t>(kOwnWarps * a->rows * D * 4), ml = kOwnWarps * 16 * 8, bars = 8u * kOwnWarps * 8;
+    const uint32_t pre = static_cast<uint32_t>(2 * a->batch + 1) * 4;
+    const uint32_t fixed = om + ml + bars + pre + 1024;
+    int st = 8;
+    while (st > 1 && st * kOwnWarps * L::STAGE + fixed > L::BUDGET) --st;
+    a->stages = st;
+    a->off_om = st * kOwnWarps * L::STAGE;
+    a->off_ml = a->off_om + om;
+    a->off_bar = a->off_ml + ml;
+    a->off_pre = a->off_bar + bars;
+    *bytes = a->off_pre + pre + 1024;
+    return *bytes <= kOwnSmem ? FUSE_OK : FUSE_EUNSUPPORTED;
+}
+
+template <typename T, int D>
+int run_paged(PagedArgs a, const void* k, const void* v, cudaStream_t st) {
+    const bool bf = std::is_same<T, __nv_bfloat16>::value;
+    CUtensorMap mK, mV;
+    if (a.plen > 0) {
+        const int box = 1 << (a.page_shift < 7 ? a.page_shift : 7);
+        if (!make_map(&mK, k, a.cache_rows, D, 64, box, bf) || !make_map(&mV, v, a.cache_rows, D, 64, box, bf)) return FUSE_ECUDA;
+        constexpr int smem = PrefixLayout<D>::SMEM > 120u * 1024u ? PrefixLayout<D>::SMEM : 120u * 1024u;
+        int rc = opt_in_smem((const void*)paged_prefix_kernel<T, D>, smem);
+        if (rc != FUSE_OK) return rc;
+        rc = launch_pdl(paged_prefix_kernel<T, D>, dim3(static_cast<unsigned>(a.pgrid)), dim3(kPreThreads), smem, st, 1, mK, mV, a);
+        if (rc != FUSE_OK) return rc;
+    }
+    if (!make_map(&mK, k, a.cache_rows, D, 64, kChunk, bf) || !make_map(&mV, v, a.cache_rows, D, 64, kChunk, bf)) return FUSE_ECUDA;
+    uint32_t smem = 0;
+    int rc = own_smem<T, D>(&a, &smem);
+    if (rc != FUSE_OK) return rc;
+    rc = opt_in_smem((const void*)paged_own_kernel<T, D>, kOwnSmem, true);
+    if (rc != FUSE_OK) return rc;
+    // every CTA is resident at once; more than there can be units would have nothing to do
+    int64_t grid = static_cast<int64_t>(sm_count()) * OwnLayout<D>::CTAS;
+    const int64_t units = static_cast<int64_t>(a.batch) * a.hk * a.rt * (ceil_div(a.table_ld << a.page_shift, kUnit) + 1);
+    if (grid > units) grid = units;
+    if (grid > kOwnGrid) grid = kOwnGrid;
+    if (units / grid >= 0x7fffffffLL) return FUSE_EUNSUPPORTED;
+    return launch_pdl(paged_own_kernel<T, D>, dim3(static_cast<unsigned>(grid)), dim3(kOwnThreads), smem, st, 1, mK, mV, a);
+}
+
+}  // namespace
+
+int paged_report_count() { return 12; }
+int paged_report(int i, fuse_kernel_record* out) {
+    const int smem_own = 111 * 1024;
+    switch (i) {
+#define FC_OWN(N, T, TN, D) case N: return describe_kernel((const void*)paged_own_kernel<T, D>, "paged_own_kernel<" TN ", D=" #D "> (own keys)", kOwnThreads, D == 256 ? 224 * 1024 : smem_own, out)
+#define FC_PRE(N, T, TN, D) case N: return describe_kernel((const void*)paged_prefix_kernel<T, D>, "paged_prefix_kernel<" TN ", D=" #D "> (shared prefix, tcgen05)", kPreThreads, PrefixLayout<D>::SMEM, out, PrefixLayout<D>::TMEM_COLS)
+        FC_OWN(0, __nv_bfloat16, "bf16", 64);
+        FC_OWN(1, __nv_bfloat16, "bf16", 128);
+        FC_OWN(2, __nv_bfloat16, "bf16", 256);
+        FC_OWN(3, __half, "f16", 64);
+        FC_OWN(4, __half, "f16", 128);
+        FC_OWN(5, __half, "f16", 256);
+        FC_PRE(6, __nv_bfloat16, "bf16", 64);
+        FC_PRE(7, __nv_bfloat16, "bf16", 128);
+        FC_PRE(8, __nv_bfloat16, "bf16", 256);
+        FC_PRE(9, __half, "f16", 64);
+        FC_PRE(10, __half, "f16", 128);
+        FC_PRE(11, __half, "f16", 256);
+#undef FC_OWN
+#undef FC_PRE
+        default: return FUSE_EINVAL;
+    }
+}
+
+}  // namespace fc
+
+extern "C" size_t fuse_paged_attention_workspace_bytes(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t D,
+                                                       int64_t prefix_len) {
+    if (batch < 1 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || D < 1 || prefix_len < 0) return 0;
+    return fc::sizes(batch, q_heads, kv_heads, D, prefix_len).bytes;
+}
+
+extern "C" int fuse_paged_attention(const void* q, const void* k_cache, const void* v_cache,
+                                    const int32_t* block_table, int64_t table_ld, const int32_t* seq_lens,
+                                    const int32_t* prefix_table, int64_t prefix_len, void* o, int64_t batch,
+                                    int64_t q_heads, int64_t kv_heads, int64_t D, int64_t num_pages,
+                                    int64_t page_size, float scale, int dtype, void* workspace, size_t ws_bytes,
+                                    fuse_stream_t stream) {
+    using namespace fc;
+    if (batch < 0 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || D < 1 || num_pages < 1 ||
+        page_size < 1 || table_ld < 0 || prefix_len < 0 || !(scale > 0.0f) || !isfinite(scale))
+        return FUSE_EINVAL;
+    if (dtype != FUSE_F16 && dtype != FUSE_BF16) return FUSE_EINVAL;
+    if (D != 64 && D != 128 && D != 256) return FUSE_EUNSUPPORTED;
+    if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1)) != 0) return FUSE_EUNSUPPORTED;
+    const int64_t top = int64_t(1) << 31;
+    if (batch > kMaxBatch || q_heads > 65536 || batch * q_heads >= top || num_pages >= top / (kv_heads * page_size) ||
+        table_ld >= (top - 256) / page_size || prefix_len >= top - 128)
+        return FUSE_EUNSUPPORTED;
+    // units of the whole batch, and tiles of the prefix, stay below 2^31
+    if ((table_ld * page_size / kUnit + 1) * batch >= top) return FUSE_EUNSUPPORTED;
+    const int64_t group = q_heads / kv_heads;
+    if (prefix_len > 0 && ceil_div(prefix_len, 128) * kv_heads * ceil_div(batch * group, 128) >= top) return FUSE_EUNSUPPORTED;
+    if (batch == 0) return FUSE_OK;
+    if (!q || !k_cache || !v_cache || !o || !seq_lens || (table_ld > 0 && !block_table) || (prefix_len > 0 && !prefix_table))
+        return FUSE_EINVAL;
+    if (!is_aligned(q, 16) || !is_aligned(k_cache, 16) || !is_aligned(v_cache, 16) || !is_aligned(o, 16) ||
+        !is_aligned(block_table, 4) || !is_aligned(seq_lens, 4) || !is_aligned(prefix_table, 4))
+        return FUSE_EALIGN;
+    const Sizes s = sizes(batch, q_heads, kv_heads, D, prefix_len);
+    if (!workspace || ws_bytes < s.bytes) return FUSE_EWORKSPACE;
+    if (!is_aligned(workspace, 256)) return FUSE_EALIGN;
+    const int64_t qb = batch * q_heads * D * 2, cb = num_pages * kv_heads * page_size * D * 2;
+    struct { const void* p; int64_t n; } in[6] = {{q, qb}, {k_cache, cb}, {v_cache, cb}, {table_ld > 0 ? block_table : nullptr, batch * table_ld * 4},
+                                                 {seq_lens, batch * 4}, {prefix_len > 0 ? prefix_table : nullptr, ceil_div(prefix_len, page_size) * 4}};
+    for (const auto& x : in)
+        if (x.p && (ranges_overlap(o, qb, x.p, x.n) || ranges_overlap(workspace, static_cast<int64_t>(s.bytes), x.p, x.n))) return FUSE_EINVAL;
+    if (ranges_overlap(workspace, static_cast<int64_t>(s.bytes), o, qb)) return FUSE_EINVAL;
+    PagedArgs a{};
+    a.q = q;
+    a.o = o;
+    a.table = block_table;
+    a.lens = seq_lens;
+    a.ptable = prefix_table;
+    a.table_ld = table_ld;
+    a.batch = static_cast<int>(batch);
+    a.hq = static_cast<int>(q_heads);
+    a.hk = static_cast<int>(kv_heads);
+    a.group = static_cast<int>(group);
+    a.rt = static_cast<int>(ceil_div(group, 16));
+    a.rows = static_cast<int>(s.rows);
+    while ((1 << a.page_shift) < page_size) ++a.page_shift;
+    a.num_pages = static_cast<int>(num_pages);
+    a.cache_rows = static_cast<int>(num_pages * kv_heads * page_size);
+    a.c = scale * 1.4426950408889634f;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    a.count = reinterpret_cast<int*>(ws + s.count);
+    a.oml = reinterpret_cast<float*>(ws + s.oml);
+    a.oo = reinterpret_cast<float*>(ws + s.oo);
+    a.pml = reinterpret_cast<float*>(ws + s.pml);
+    a.po = reinterpret_cast<float*>(ws + s.po);
+    a.plen = static_cast<int>(prefix_len);
+    if (prefix_len > 0) {
+        a.ptiles = static_cast<int>(ceil_div(prefix_len, 128));
+        a.prt = static_cast<int>(ceil_div(batch * group, 128));
+        const int64_t units = static_cast<int64_t>(a.hk) * a.prt * a.ptiles;
+        int64_t grid = sm_count() < kPrefixGrid ? sm_count() : kPrefixGrid;
+        a.pgrid = static_cast<int>(grid < units ? grid : units);
+    }
+    a.flag = watchdog_flag();
+    a.bad = index_flag();
+    if (!a.flag || !a.bad) return FUSE_ECUDA;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (dtype == FUSE_F16) {
+        if (D == 64) return run_paged<__half, 64>(a, k_cache, v_cache, st);
+        if (D == 128) return run_paged<__half, 128>(a, k_cache, v_cache, st);
+        return run_paged<__half, 256>(a, k_cache, v_cache, st);
+    }
+    if (D == 64) return run_paged<__nv_bfloat16, 64>(a, k_cache, v_cache, st);
+    if (D == 128) return run_paged<__nv_bfloat16, 128>(a, k_cache, v_cache, st);
+    return run_paged<__nv_bfloat16, 256>(a, k_cache, v_cache, st);
+}
+
+extern "C" int64_t fuse_paged_attention_bytes(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t D,
+                                              int64_t prefix_len, int64_t keys) {
+    if (batch < 0 || q_heads < 1 || kv_heads < 1 || D < 1 || prefix_len < 0 || keys < 0) return FUSE_EINVAL;
+    return 4 * D * (kv_heads * (prefix_len + keys) + batch * q_heads);   // K and V once; q and o
+}
+
+extern "C" int64_t fuse_paged_attention_flops(int64_t batch, int64_t q_heads, int64_t D, int64_t prefix_len,
+                                              int64_t keys) {
+    if (batch < 0 || q_heads < 1 || D < 1 || prefix_len < 0 || keys < 0) return FUSE_EINVAL;
+    return 4 * D * q_heads * (batch * prefix_len + keys);
+}

@@ -8,7 +8,10 @@
 #include "fc_internal.cuh"
 #include "fc_ptx.cuh"
 
-__device__ int g_fc_watchdog;
+// [0] the watchdog word, [1] the index word: set by a kernel that met a page, slot or position index
+// (or a length) outside its range in device memory, where the host cannot check it.  The kernel leaves
+// out what the index named and goes on; fuse_check() reports FUSE_EINDEX.
+__device__ int g_fc_status[2];
 
 namespace fc {
 
@@ -24,7 +27,7 @@ int* watchdog_flag() {
     std::lock_guard<std::mutex> lock(mu);
     if (!cached[dev]) {
         void* p = nullptr;
-        if (cudaGetSymbolAddress(&p, g_fc_watchdog) != cudaSuccess) {
+        if (cudaGetSymbolAddress(&p, g_fc_status) != cudaSuccess) {
             (void)cudaGetLastError();
             return nullptr;
         }
@@ -33,17 +36,22 @@ int* watchdog_flag() {
     return cached[dev];
 }
 
-int watchdog_take() {
-    int v = 0;
-    if (cudaMemcpyFromSymbol(&v, g_fc_watchdog, sizeof(int)) != cudaSuccess) {
+int* index_flag() {
+    int* p = watchdog_flag();
+    return p ? p + 1 : nullptr;
+}
+
+int status_take() {
+    int v[2] = {0, 0};
+    if (cudaMemcpyFromSymbol(v, g_fc_status, sizeof(v)) != cudaSuccess) {
         (void)cudaGetLastError();
-        return 0;
+        return FUSE_OK;
     }
-    if (v) {
-        const int zero = 0;
-        (void)cudaMemcpyToSymbol(g_fc_watchdog, &zero, sizeof(int));
+    if (v[0] || v[1]) {
+        const int zero[2] = {0, 0};
+        (void)cudaMemcpyToSymbol(g_fc_status, zero, sizeof(zero));
     }
-    return v != 0;
+    return v[0] ? FUSE_ETIMEOUT : v[1] ? FUSE_EINDEX : FUSE_OK;
 }
 
 namespace {

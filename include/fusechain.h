@@ -46,7 +46,9 @@ typedef enum {
     FUSE_EUNSUPPORTED = -3,   /* a size or combination this build does not implement          */
     FUSE_ECUDA = -4,          /* a CUDA launch or runtime call failed                         */
     FUSE_ETIMEOUT = -5,       /* a bounded device-side wait ran out (watchdog)                */
-    FUSE_EWORKSPACE = -6      /* workspace pointer missing or smaller than required           */
+    FUSE_EWORKSPACE = -6,     /* workspace pointer missing or smaller than required           */
+    FUSE_EINDEX = -7          /* fuse_check(): an index or length read from device memory was out
+                                 of range; what it named was left out                          */
 } fuse_status;
 
 typedef enum { FUSE_F32 = 0, FUSE_F16 = 1, FUSE_BF16 = 2 } fuse_dtype;
@@ -327,6 +329,101 @@ int64_t fuse_attention_flops(int64_t bh, int64_t S, int64_t D);
  * Returns the number of items, or a negative FUSE_E* code. */
 int64_t fuse_attention_schedule(int64_t bh, int64_t S, int clusters, int32_t* first, int32_t* items);
 
+/* ===================================================================== rotate and append to a paged cache
+ * What follows the query/key/value projection of a decoder layer ("AIGC fundamentals | operator
+ * fusion and CUDA Graph", appendix launch_model [F3]: "RoPE fused"): the queries and keys are
+ * rotated by their positions and keys and values go to their places in a paged cache, in one pass.
+ * Per token t with position n, for each query and key head and each pair (a, b) of its first
+ * `rot` components, with cos and sin row n of the table,
+ *     a' = a cos_i - b sin_i,   b' = b cos_i + a sin_i        (i = 0 .. rot/2 - 1)
+ * in fp32, rounded once to `dtype`.  Pair i is components (i, i + rot/2), or (2i, 2i + 1) with
+ * FUSE_ROPE_INTERLEAVED.  Components from `rot` on, and values, are copied.
+ *
+ *   qkv      device [tokens, ld] of `dtype`, ld >= (q_heads + 2 kv_heads) D: per row the query heads,
+ *            then the key heads, then the value heads (a merged projection's output)
+ *   cos_sin  device fp32 [max_pos, rot]: the rot/2 cosines of a position, then its rot/2 sines (may be
+ *            NULL when rot == 0)
+ *   positions, slots  device int32 [tokens].  slots[t] = page * page_size + offset is where token t's
+ *            key and value go; a negative slot appends nothing (a padded row; its query is written).
+ *            Two tokens with the same slot leave one of their values in each 16 bytes of it.
+ *   q_out    device [tokens, q_heads, D] of `dtype`
+ *   k_cache, v_cache  device [num_pages, kv_heads, page_size, D] of `dtype` (the layout
+ *            fuse_paged_attention() reads); slots not named are left as they are
+ *   Rules: dtype FUSE_F16 or FUSE_BF16; D a multiple of 16, at most 512; 0 <= rot <= D, rot a multiple
+ *          of 16; page_size a power of two, 16..256; num_pages kv_heads page_size < 2^31 (else
+ *          FUSE_EUNSUPPORTED); pointers 16-byte aligned (positions and slots 4-byte) and ld a
+ *          multiple of 8 (else FUSE_EALIGN); outputs overlap neither each other nor an input.
+ *   Out of range in device memory (nothing is read or written there; fuse_check() then returns
+ *   FUSE_EINDEX): a slot >= num_pages page_size appends nothing; a token whose position is not in
+ *   [0, max_pos) appends nothing and gets a zero query row (not reported if its slot is negative).
+ *   Without rotation (rot == 0) positions are not read and may be NULL.
+ */
+#define FUSE_ROPE_INTERLEAVED 1u
+int fuse_rope_append(const void* qkv, int64_t ld, const float* cos_sin, int64_t max_pos, int64_t rot,
+                     const int32_t* positions, const int32_t* slots, void* q_out, void* k_cache,
+                     void* v_cache, int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t D,
+                     int64_t num_pages, int64_t page_size, int dtype, uint32_t flags,
+                     fuse_stream_t stream);
+
+/* ===================================================================== attention over a paged cache
+ * The single-token form of fuse_attention(): one query per sequence, attending to the keys of a
+ * prefix that all sequences share (prefix_len may be 0) and then to the sequence's own keys:
+ *     o_bh = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m),   s_j = scale q_bh . k_j,   m = max_j s_j,
+ * with query head h reading key/value head h / (q_heads / kv_heads).  The prefix is read once for the
+ * whole batch, not once per sequence.  A sequence without any key (prefix_len == 0 and length 0)
+ * gets zeros.
+ *
+ *   q, o     device [batch, q_heads, D] of `dtype`; o must not overlap an input
+ *   k_cache, v_cache  device [num_pages, kv_heads, page_size, D] of `dtype`; what lies in a page past
+ *            the keys in use is not used, whatever its bits
+ *   block_table  device int32 [batch, table_ld]: entry i is the page of own keys i page_size .. ; only
+ *            the entries that seq_lens covers are read.  May be NULL when table_ld == 0.
+ *   seq_lens device int32 [batch]: the number of own keys of each sequence, 0 .. table_ld page_size
+ *   prefix_table  device int32 [ceil(prefix_len / page_size)]: the pages of the shared prefix
+ *   Rules: dtype FUSE_F16 or FUSE_BF16; D in {64, 128, 256}; q_heads a multiple of kv_heads; page_size
+ *          a power of two, 16..256; batch <= 4096; num_pages kv_heads page_size, table_ld page_size
+ *          and prefix_len below 2^31 - 256, batch table_ld page_size / 64 below 2^31 (else FUSE_EUNSUPPORTED); scale > 0; tensors
+ *          16-byte aligned, tables and lengths 4-byte.
+ *   Out of range in device memory (fuse_check() then returns FUSE_EINDEX): a page index outside
+ *   [0, num_pages) counts as a page of zeros; a length is taken into 0 .. table_ld page_size.
+ *   workspace  device memory of at least fuse_paged_attention_workspace_bytes() bytes, 256-byte
+ *          aligned, its first 2048 bytes zero before its first use (every completed call leaves them
+ *          so; calls of any sizes may follow one another in it), not shared with a call that may run
+ *          at the same time, in a replayed graph or otherwise; it must overlap no operand.  After a
+ *          FUSE_ETIMEOUT, zero those bytes again.
+ * Scores, maxima, sums and the accumulated output are fp32; the weights e^(s - m) are rounded to
+ * `dtype` for the product with V and the output once at the end.  The keys are split over the SMs and
+ * the parts joined in a fixed order: equal calls give equal bits.
+ */
+int fuse_paged_attention(const void* q, const void* k_cache, const void* v_cache,
+                         const int32_t* block_table, int64_t table_ld, const int32_t* seq_lens,
+                         const int32_t* prefix_table, int64_t prefix_len, void* o, int64_t batch,
+                         int64_t q_heads, int64_t kv_heads, int64_t D, int64_t num_pages,
+                         int64_t page_size, float scale, int dtype, void* workspace, size_t ws_bytes,
+                         fuse_stream_t stream);
+size_t fuse_paged_attention_workspace_bytes(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t D,
+                                            int64_t prefix_len);
+
+/* ===================================================================== 4-bit weights, few tokens
+ * The decode form of a projection whose weight is held in 4 bits with one scale per group of
+ * `group` consecutive inputs, with the epilogue of fuse_gemm_epilogue() (each stage optional):
+ *     w_nk = (q_nk - z_{n, k / group}) s_{n, k / group},   Y = GELU(X W^T + bias) + R.
+ *   x       device [M, K] of `dtype`, 1 <= M <= 64 (M == 0 enqueues nothing; more: FUSE_EUNSUPPORTED)
+ *   wq      device uint8 [N, K / 2]: byte j of a row holds input 2j in its low and 2j + 1 in its high
+ *           four bits
+ *   scales  device [N, K / group] of `dtype`;  zeros  device uint8 [N, K / group], each 0..15 (higher
+ *           bits are ignored), or NULL for z = 8
+ *   bias [N], R [M, N] of `dtype`, or NULL;  gelu 0 or 1;  y device [M, N] of `dtype`
+ *   Rules: dtype FUSE_F16 or FUSE_BF16; group in {32, 64, 128}; K a multiple of group; N, K < 2^31 (else
+ *          FUSE_EUNSUPPORTED); x and wq 16-byte aligned, the others to their element (else
+ *          FUSE_EALIGN); y overlaps no input.
+ * (q - z) is exact in `dtype`, its products with x are summed in fp32 over each group, the scale
+ * multiplies that sum in fp32, and Y is rounded once.  The order of the sums is fixed.
+ */
+int fuse_w4_gemv(const void* x, const void* wq, const void* scales, const void* zeros, const void* bias,
+                 const void* R, void* y, int64_t M, int64_t N, int64_t K, int64_t group, int gelu,
+                 int dtype, fuse_stream_t stream);
+
 /* ===================================================================== ledgers
  * [K4] §① traffic(): a cut plan splits the K stages into consecutive kernels (cut_mask bit i =
  * a kernel boundary after stage i).  Each kernel reads the previous kernel's output (the
@@ -379,6 +476,16 @@ int64_t fuse_causal_softmax_bytes(int64_t batch_heads, int64_t S, int skip_tile,
                                   int mode);
 int64_t fuse_add_rmsnorm_bytes(int64_t rows, int64_t hidden, int mode);
 int64_t fuse_silu_mul_bytes(int64_t rows, int64_t cols, int dtype, int mode);
+/* `appended` of the `tokens` rows have a slot; the table's rows are counted once per token. */
+int64_t fuse_rope_append_bytes(int64_t tokens, int64_t appended, int64_t q_heads, int64_t kv_heads,
+                               int64_t D, int64_t rot);
+/* keys = the sum of seq_lens; tables and lengths are not counted.  flops: 4 D per query head and key. */
+int64_t fuse_paged_attention_bytes(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t D,
+                                   int64_t prefix_len, int64_t keys);
+int64_t fuse_paged_attention_flops(int64_t batch, int64_t q_heads, int64_t D, int64_t prefix_len,
+                                   int64_t keys);
+int64_t fuse_w4_gemv_bytes(int64_t M, int64_t N, int64_t K, int64_t group, int zeros, int bias,
+                           int residual);
 
 /* ===================================================================== reports and status
  * [K4] §③ and [C05] §6.2: registers per thread, spills and blocks per SM decide when fusion
@@ -462,7 +569,8 @@ const char* fuse_strerror(int status);
 /* Message of the last CUDA error seen by this library on this thread ("" if none). */
 const char* fuse_last_cuda_error(void);
 /* Synchronize `stream`, then return FUSE_ETIMEOUT if a device watchdog fired since the last
- * check (and clear it), FUSE_ECUDA if the stream reported an error, else FUSE_OK. */
+ * check, FUSE_EINDEX if a kernel met a page, slot, position or length outside its range in device
+ * memory since then (both are cleared), FUSE_ECUDA if the stream reported an error, else FUSE_OK. */
 int fuse_check(fuse_stream_t stream);
 /* Test hook of the watchdog: one thread waits on an mbarrier that nothing arrives on, for
  * budget_cycles SM clock cycles (0 <= budget_cycles < 2^31), then records the timeout and
