@@ -169,10 +169,31 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+_torch = None         # the torch module, and its calls for the current device's index and stream handle
+_current_device = None
+_current_handle = None
+
+
+def _bind_torch():
+    """torch, imported at the first call that needs it (an import statement or a Stream object at every
+    call costs the host more than the launch of a small kernel)."""
+    global _torch, _current_device, _current_handle
+    import torch
+    if not torch.cuda.is_available():
+        raise ValueError("no CUDA device")
+    torch.cuda.current_stream()        # initialises CUDA
+    _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    _current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    _torch = torch
+    return torch
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _torch is None:
+            _bind_torch()
+        return _current_handle(_current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -383,17 +404,21 @@ def fuse_gemm_bytes(M: int, N: int, K: int, cut_mask: int) -> int:
 
 
 # ------------------------------------------------------------------------------- single-token decode
-def _decode_operands(dtypes, *ts):
-    """The device index of the tensors, which have to be contiguous, of their dtype and all on torch's
-    current device (the library launches there)."""
-    import torch
+def _decode_operands(dt, ts, others) -> int:
+    """The device index of the tensors: contiguous, of dtype dt (fp16 or bf16; `others`: pairs of a tensor
+    or None and its dtype), all on torch's current device (the library launches there)."""
+    torch = _torch
+    if dt is not torch.bfloat16 and dt is not torch.float16:
+        raise ValueError(f"fp16 or bf16 tensors expected, not {dt}")
     dev = ts[0].get_device()
-    for t, want in zip(ts, dtypes):
-        if t is not None and (t.get_device() != dev or t.dtype is not want or not t.is_contiguous()):
-            raise ValueError(f"expected contiguous CUDA tensors of one device; {tuple(t.shape)} {t.dtype} on "
-                             f"{t.device}, {want} wanted")
-    if dev < 0 or dev != torch.cuda.current_device():
+    if dev != _current_device():
         raise ValueError("the tensors must be on the current CUDA device")
+    for t in ts:
+        if t is not None and (t.dtype is not dt or t.get_device() != dev or not t.is_contiguous()):
+            raise ValueError(f"{tuple(t.shape)} {t.dtype} on {t.device}: contiguous {dt} on one device expected")
+    for t, want in others:
+        if t is not None and (t.dtype is not want or t.get_device() != dev or not t.is_contiguous()):
+            raise ValueError(f"{tuple(t.shape)} {t.dtype} on {t.device}: contiguous {want} on one device expected")
     return dev
 
 
@@ -403,14 +428,13 @@ def fuse_rope_append(qkv, cos_sin, positions, slots, q_out, k_cache, v_cache, in
     their positions, write the queries to q_out [tokens, q_heads, D] and append keys and values to
     k_cache, v_cache [num_pages, kv_heads, page_size, D] at slots (int32; negative: append nothing).
     cos_sin: fp32 [max_pos, rot], the cosines then the sines of a position's rot / 2 pairs."""
-    import torch
-    dt, i32 = qkv.dtype, torch.int32
-    _decode_operands((dt, dt, dt, i32, i32, torch.float32), q_out, k_cache, v_cache, positions, slots, cos_sin)
-    if dt is not torch.bfloat16 and dt is not torch.float16:
-        raise ValueError("fp16 or bf16 tensors expected")
+    torch = _torch or _bind_torch()
+    dt = qkv.dtype
+    dev = _decode_operands(dt, (q_out, k_cache, v_cache), ((positions, torch.int32), (slots, torch.int32),
+                                                           (cos_sin, torch.float32)))
     tokens, q_heads, D = q_out.shape
     pages, kv_heads, page_size, D2 = k_cache.shape
-    if qkv.get_device() != q_out.get_device() or qkv.dim() != 2 or qkv.stride(1) != 1:
+    if qkv.get_device() != dev or qkv.dim() != 2 or qkv.stride(1) != 1:
         raise ValueError("qkv must be a 2-D tensor with unit column stride on the device of the others")
     if (D2 != D or v_cache.shape != k_cache.shape or qkv.shape != (tokens, (q_heads + 2 * kv_heads) * D)
             or positions.shape != (tokens,) or slots.shape != (tokens,) or cos_sin.dim() != 2):
@@ -430,9 +454,8 @@ _PAGED_WS = {}
 
 
 def _paged_workspace(need: int, dev: int, stream_handle):
-    import torch
-    current = torch.cuda.current_stream(dev)
-    if stream_handle != current.cuda_stream or torch.cuda.is_current_stream_capturing():
+    torch = _torch
+    if stream_handle != _current_handle(dev) or torch.cuda.is_current_stream_capturing():
         raise ValueError("pass a zero-filled workspace of fuse_paged_attention_workspace_bytes() bytes: this module's "
                          "own ones serve calls on torch's current stream outside a graph capture only (a captured "
                          "graph may be replayed next to other calls)")
@@ -450,11 +473,9 @@ def fuse_paged_attention(q, k_cache, v_cache, block_table, seq_lens, o, scale: f
     block_table[b]'s; k_cache, v_cache [num_pages, kv_heads, page_size, D].  workspace: a zero-filled
     device tensor (see fuse_paged_attention in the header); None: a buffer kept by this module for the
     current stream."""
-    import torch
+    torch = _torch or _bind_torch()
     dt, i32 = q.dtype, torch.int32
-    dev = _decode_operands((dt, dt, dt, dt, i32, i32, i32), q, k_cache, v_cache, o, block_table, seq_lens, prefix_table)
-    if dt is not torch.bfloat16 and dt is not torch.float16:
-        raise ValueError("fp16 or bf16 tensors expected")
+    dev = _decode_operands(dt, (q, k_cache, v_cache, o), ((block_table, i32), (seq_lens, i32), (prefix_table, i32)))
     batch, q_heads, D = q.shape
     pages, kv_heads, page_size, D2 = k_cache.shape
     if (D2 != D or o.shape != q.shape or v_cache.shape != k_cache.shape or block_table.dim() != 2
@@ -483,11 +504,9 @@ def fuse_w4_gemv(x, wq, scales, y, zeros=None, bias=None, residual=None, gelu: b
     """y = GELU(x W^T + bias) + residual for x [M, K], M <= 64, and W [N, K] in 4 bits: wq uint8 [N, K / 2]
     (input 2j in a byte's low half), scales [N, K / group] and zeros uint8 [N, K / group] (None: 8),
     W = (q - zero) scale.  bias [N], residual [M, N] and the GELU are optional."""
-    import torch
-    dt, u8 = x.dtype, torch.uint8
-    _decode_operands((dt, u8, dt, dt, u8, dt, dt), x, wq, scales, y, zeros, bias, residual)
-    if dt is not torch.bfloat16 and dt is not torch.float16:
-        raise ValueError("fp16 or bf16 tensors expected")
+    torch = _torch or _bind_torch()
+    dt = x.dtype
+    _decode_operands(dt, (x, scales, y, bias, residual), ((wq, torch.uint8), (zeros, torch.uint8)))
     M, K = x.shape
     N, half = wq.shape
     groups = scales.shape[1] if scales.dim() == 2 else 0

@@ -32,6 +32,7 @@ namespace {
 constexpr int kW4Warps = 8;
 constexpr int kW4Threads = 32 * (kW4Warps + 1);   // warp 8 produces
 constexpr int kW4MaxStages = 8;
+constexpr int kAhead = 4;                         // stages that scales are loaded ahead
 
 struct W4Args {
     int M, N, K;
@@ -50,7 +51,6 @@ struct W4Args {
 template <typename T> struct Nib;   // 2^e + q pairs and their exact difference with 2^e + z
 template <> struct Nib<__half> {
     static constexpr uint32_t MAGIC = 0x64006400u;   // 1024
-    __device__ __forceinline__ static uint32_t base(uint32_t z) { return MAGIC | z | (z << 16); }
     __device__ __forceinline__ static uint32_t sub(uint32_t v, uint32_t b) {
         __half2 r = __hsub2(*reinterpret_cast<__half2*>(&v), *reinterpret_cast<__half2*>(&b));
         return *reinterpret_cast<uint32_t*>(&r);
@@ -58,7 +58,6 @@ template <> struct Nib<__half> {
 };
 template <> struct Nib<__nv_bfloat16> {
     static constexpr uint32_t MAGIC = 0x43004300u;   // 128
-    __device__ __forceinline__ static uint32_t base(uint32_t z) { return MAGIC | z | (z << 16); }
     __device__ __forceinline__ static uint32_t sub(uint32_t v, uint32_t b) {
         __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&v), *reinterpret_cast<__nv_bfloat162*>(&b));
         return *reinterpret_cast<uint32_t*>(&r);
@@ -75,8 +74,6 @@ __device__ __forceinline__ void unpack_word(uint32_t w, uint32_t zb, uint32_t (&
         p[i] = Nib<T>::sub(v, zb);
     }
 }
-
-template <typename T> __device__ __forceinline__ float ld_elem(const T* p) { return to_f32(*p); }
 
 template <typename T, int G, int NT>
 __global__ void __launch_bounds__(kW4Threads) w4_gemv_kernel(const __grid_constant__ CUtensorMap mW,
@@ -139,25 +136,28 @@ __global__ void __launch_bounds__(kW4Threads) w4_gemv_kernel(const __grid_consta
         const int g = lane / 4, t = lane % 4;
         const int KG = a.K / G;
         const int nlo = n0 + 16 * wr + g, nhi = nlo + 8;
-        const T* sc = static_cast<const T*>(a.s);
-        const uint8_t* zp = static_cast<const uint8_t*>(a.z);
-        // lane t of a row loads group t % NG of the chunk, the four lanes share by shuffles
-        float s_lo = 0.0f, s_hi = 0.0f;
-        uint32_t z_lo = 8, z_hi = 8;
-        auto load_scales = [&](int chunk) {
+        // lane t of a row loads group t % NG of a chunk, the four lanes share by shuffles; kAhead stages
+        // ahead of their use, each as one word of two scales and one of two zero points (rows g, g + 8)
+        uint32_t sc_ring[kAhead], zp_ring[kAhead];
+        const uint16_t* sc_lo = static_cast<const uint16_t*>(a.s) + static_cast<int64_t>(nlo < a.N ? nlo : 0) * KG;
+        const uint16_t* sc_hi = static_cast<const uint16_t*>(a.s) + static_cast<int64_t>(nhi < a.N ? nhi : 0) * KG;
+        const uint8_t* zp_lo = static_cast<const uint8_t*>(a.z) + static_cast<int64_t>(nlo < a.N ? nlo : 0) * KG;
+        const uint8_t* zp_hi = static_cast<const uint8_t*>(a.z) + static_cast<int64_t>(nhi < a.N ? nhi : 0) * KG;
+        auto load_scales = [&](int chunk, uint32_t& sc, uint32_t& zp) {
             const int gi = chunk * NG + t % NG;
-            const bool in = gi < KG;
-            s_lo = in && nlo < a.N ? to_f32(sc[static_cast<int64_t>(nlo) * KG + gi]) : 0.0f;
-            s_hi = in && nhi < a.N ? to_f32(sc[static_cast<int64_t>(nhi) * KG + gi]) : 0.0f;
-            if (zp) {
-                z_lo = in && nlo < a.N ? zp[static_cast<int64_t>(nlo) * KG + gi] & 15u : 0u;
-                z_hi = in && nhi < a.N ? zp[static_cast<int64_t>(nhi) * KG + gi] & 15u : 0u;
+            sc = 0u;
+            zp = 0x00080008u;
+            if (gi < KG) {   // past the last chunk: scale zero
+                sc = __ldg(sc_lo + gi) | static_cast<uint32_t>(__ldg(sc_hi + gi)) << 16;
+                if (a.z) zp = (__ldg(zp_lo + gi) & 15u) | (__ldg(zp_hi + gi) & 15u) << 16;
             }
         };
         // one group: WPG words of each row against the matching X pieces
-        auto group = [&](int gi, const uint32_t* wl, const uint32_t* wh, auto&& xpiece, float sl, float sh, uint32_t zl, uint32_t zh) {
+        auto group = [&](int gi, const uint32_t* wl, const uint32_t* wh, auto&& xpiece, uint32_t sc, uint32_t zp) {
             float part[NT][4] = {};
-            const uint32_t bl = Nib<T>::base(zl), bh = Nib<T>::base(zh);
+            const uint32_t bl = Nib<T>::MAGIC | __byte_perm(zp, 0u, 0x1010), bh = Nib<T>::MAGIC | __byte_perm(zp, 0u, 0x3232);
+            const float2 s2 = unpack2<T>(sc);
+            const float sl = s2.x, sh = s2.y;
 #pragma unroll
             for (int w = 0; w < WPG; ++w) {
                 uint32_t pl[4], ph[4];
@@ -182,13 +182,17 @@ __global__ void __launch_bounds__(kW4Threads) w4_gemv_kernel(const __grid_consta
         // k of word w of group gi within the chunk
         auto kof = [&](int gi, int w) { return gi * G + t * (G / 4) + 8 * w; };
         bool ok = true;
-        if (iters > 0) load_scales(rank * WK + wk);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) load_scales((i * a.split + rank) * WK + wk, sc_ring[i], zp_ring[i]);
         int s = 0;
         uint32_t phase = 0;
-        for (int it = 0; it < iters; ++it) {
-            const float csl = s_lo, csh = s_hi;
-            const uint32_t czl = z_lo, czh = z_hi;
-            if (it + 1 < iters) load_scales(((it + 1) * a.split + rank) * WK + wk);
+        for (int it0 = 0; ok && it0 < iters; it0 += kAhead)
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) {
+            const int it = it0 + i;
+            if (it >= iters || !ok) break;
+            const uint32_t sc = sc_ring[i], zp = zp_ring[i];
+            load_scales(((it + kAhead) * a.split + rank) * WK + wk, sc_ring[i], zp_ring[i]);
             if (!__all_sync(0xffffffffu, mbar_wait_bounded(full(s), phase, a.flag))) {
                 ok = false;
                 break;
@@ -218,8 +222,7 @@ __global__ void __launch_bounds__(kW4Threads) w4_gemv_kernel(const __grid_consta
                     wh[0] = lds32(at + 512u);
                 }
                 const int src = (lane & 28) | gi;
-                group(gi, wl, wh, xpiece, __shfl_sync(0xffffffffu, csl, src), __shfl_sync(0xffffffffu, csh, src),
-                      __shfl_sync(0xffffffffu, czl, src), __shfl_sync(0xffffffffu, czh, src));
+                group(gi, wl, wh, xpiece, __shfl_sync(0xffffffffu, sc, src), __shfl_sync(0xffffffffu, zp, src));
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(empty(s));
@@ -231,7 +234,8 @@ __global__ void __launch_bounds__(kW4Threads) w4_gemv_kernel(const __grid_consta
         // the last K % 128 inputs (groups of 32 and 64), from global memory by the first K warps
         if (G < 128 && ok && rank == 0 && wk == 0 && a.nchunk * 128 < a.K) {
             const int k0 = a.nchunk * 128;
-            load_scales(a.nchunk);
+            uint32_t sc, zp;
+            load_scales(a.nchunk, sc, zp);
             const T* x = static_cast<const T*>(a.x);
             const uint8_t* wq = static_cast<const uint8_t*>(a.wq);
             const int ng = (a.K - k0) / G;
@@ -248,8 +252,7 @@ __global__ void __launch_bounds__(kW4Threads) w4_gemv_kernel(const __grid_consta
                     return *reinterpret_cast<const uint4*>(x + static_cast<int64_t>(m) * a.K + k0 + kof(gj, w));
                 };
                 const int src = (lane & 28) | gi;
-                group(gi, wl, wh, xpiece, __shfl_sync(0xffffffffu, s_lo, src), __shfl_sync(0xffffffffu, s_hi, src),
-                      __shfl_sync(0xffffffffu, z_lo, src), __shfl_sync(0xffffffffu, z_hi, src));
+                group(gi, wl, wh, xpiece, __shfl_sync(0xffffffffu, sc, src), __shfl_sync(0xffffffffu, zp, src));
             }
         }
     }
