@@ -34,9 +34,11 @@ namespace fc {
 namespace {
 
 constexpr int kOwnWarps = 4;
-constexpr int kOwnThreads = 32 * kOwnWarps;
+constexpr int kOwnThreads = 32 * (kOwnWarps + 1); // the last warp loads
 constexpr int kChunk = 16;                        // keys of a warp per unit
 constexpr int kUnit = kChunk * kOwnWarps;         // keys of a unit
+constexpr int kOwnSlots = 8;                       // most ring slots
+constexpr int kOwnQ = 2;                          // buffers of query rows
 constexpr int kOwnGrid = 320;                     // most CTAs of paged_own_kernel (workspace bound)
 constexpr int kCounterBytes = 2048;
 static_assert(kOwnGrid * 4 <= kCounterBytes, "one counter per CTA");
@@ -71,14 +73,15 @@ struct PagedArgs {
     int page_shift, num_pages;
     int cache_rows;                    // num_pages hk page_size: a row past the cache reads zeros
     float c;                           // scale * log2(e)
-    int stages;
-    uint32_t off_om, off_ml, off_bar, off_pre;
+    int slots, nbuf;                   // ring slots; buffers of the warps' parts
+    uint32_t off_q, off_om, off_ml, off_bar, off_pre;
     // workspace
     // A CTA's run has at most one item that began in an earlier CTA (its part has slot 2 c) and one
     // that goes on in a later one (slot 2 c + 1 if it begins here; an item begins in one CTA, which
     // names its counter).
     int* count;                        // [kOwnGrid] parts that have arrived, by the item's first CTA
     float *oml, *oo;                   // [2 kOwnGrid][rows] (m, l) and [..][rows][D]
+    float *rml, *ro;                   // with a prefix: own part of every row, [batch hq] (m, l) and [..][D]
     float *pml, *po;                   // [kPrefixGrid + pitems][128] (m, l, l', -) and [..][128][D]
     // prefix
     int plen, ptiles, prt, pgrid;      // keys, 128-key tiles, 128-row tiles of a head, CTAs
@@ -86,15 +89,17 @@ struct PagedArgs {
 };
 
 // The CTA of `grid` that a unit belongs to when CTA c takes units [c U / grid, (c + 1) U / grid).
-__device__ __forceinline__ int cta_of(int64_t u, int64_t U, int64_t grid) {
-    return static_cast<int>(((u + 1) * grid - 1) / U);
+__device__ __forceinline__ int cta_of(int64_t u, int64_t U, int grid) {
+    const uint64_t n = static_cast<uint64_t>(u + 1) * static_cast<uint32_t>(grid) - 1;
+    if (((n | static_cast<uint64_t>(U)) >> 32) == 0)   // a 64-bit division takes several times as long
+        return static_cast<int>(static_cast<uint32_t>(n) / static_cast<uint32_t>(U));
+    return static_cast<int>(n / static_cast<uint64_t>(U));
 }
 
 // Join (m, l, acc) with another part; a part without keys has m = -inf, l = 0.
 __device__ __forceinline__ void join(float& m, float& l, float4& acc, float m2, float l2, const float4& o2) {
-    if (m2 == -INFINITY) return;
     const float nm = fmaxf(m, m2);
-    const float a = m == -INFINITY ? 0.0f : ex2f(m - nm), b = ex2f(m2 - nm);
+    const float a = m == -INFINITY ? 0.0f : ex2f(m - nm), b = m2 == -INFINITY ? 0.0f : ex2f(m2 - nm);
     l = l * a + l2 * b;
     acc.x = acc.x * a + o2.x * b;
     acc.y = acc.y * a + o2.y * b;
@@ -103,53 +108,92 @@ __device__ __forceinline__ void join(float& m, float& l, float4& acc, float m2, 
     m = nm;
 }
 
+// Join the parts c0 .. c1 that lie in memory, in order, for N pieces of four output columns; part(c, k, &m,
+// &l) gives the address of piece k of part c.  Two parts of all pieces are loaded at a time, so that their
+// memory latencies overlap.
+template <int N, typename F>
+__device__ __forceinline__ void join_parts(int c0, int c1, float (&m)[N], float (&l)[N], float4 (&acc)[N], F&& part) {
+    for (int c = c0; c <= c1; c += 2) {
+        float pm[2][N], pl[2][N];
+        float4 po[2][N];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int k = 0; k < N; ++k) po[i][k] = __ldcg(part(min(c + i, c1), k, pm[i][k], pl[i][k]));
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int k = 0; k < N; ++k) join(m[k], l[k], acc[k], c + i <= c1 ? pm[i][k] : -INFINITY, pl[i][k], po[i][k]);
+    }
+}
+
 // ================================================================== the sequences' own keys
 template <int D>
 struct OwnLayout {
-    static constexpr uint32_t ATOM = kChunk * 128;               // 16 keys x 64 components
-    static constexpr uint32_t KV = ATOM * (D / 64);              // K or V of a chunk
-    static constexpr uint32_t STAGE = 2 * KV;
-    static constexpr int CTAS = D == 256 ? 1 : 2;                // per SM
-    static constexpr uint32_t BUDGET = (D == 256 ? 224u : 111u) * 1024u;
+    static constexpr int ATOMS = D / 64;
+    static constexpr uint32_t ATOM = kUnit * 128;                // 64 keys x 64 components
+    static constexpr uint32_t SLOT = ATOM * ATOMS;               // K or V of a unit
+    static constexpr uint32_t QATOM = 16 * 128;                  // 16 query rows x 64 components
+    static constexpr uint32_t QSLOT = QATOM * ATOMS;
+    // D = 256 leaves no registers to hold the query rows next to the output; they are read again from
+    // shared memory for every unit
+    static constexpr bool Q_REGS = D <= 128;
 };
 
-// Where a CTA or a warp's loads are in the line of units.
+// A unit of a CTA's run.
 struct Cursor {
-    int left;        // units left of the CTA's run, this one included
+    int left;        // units left of the run, this one included
     int b, hr;       // sequence; key/value head * rt + row tile
     int j, n, len;   // unit of the sequence, their number, its keys
 };
 
+// Four computing warps and one that loads.  The loading warp places 32 units at a time, one per lane (which
+// sequence and head, which pages), a batch ahead of the loads, so that no table entry is waited for between
+// two loads; it loads the query rows of a run, then K and V of every unit, each into the next slot of a ring.
+// Under load a dependent read of global memory takes several microseconds (the ring keeps the memory queues
+// full), which is why nothing else reads global memory inside the loop.
 template <typename T, int D>
-__global__ void __launch_bounds__(kOwnThreads, OwnLayout<D>::CTAS) paged_own_kernel(
-    const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
-    const __grid_constant__ PagedArgs a) {
+__global__ void __launch_bounds__(kOwnThreads, 2) paged_own_kernel(
+    const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
+    const __grid_constant__ CUtensorMap mV, const __grid_constant__ PagedArgs a) {
     using L = OwnLayout<D>;
     pdl_trigger();
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
     uint8_t* gbase = smem_raw + (base - smem_addr(smem_raw));
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const int g = lane / 4, t = lane % 4;
-    float* om = reinterpret_cast<float*>(gbase + a.off_om);      // [warp][rows][D]
-    float* ml = reinterpret_cast<float*>(gbase + a.off_ml);      // [warp][rows][2]
     int* pre = reinterpret_cast<int*>(gbase + a.off_pre);        // [batch + 1] units before a sequence
     int* slen = pre + a.batch + 1;                               // [batch]
-    __shared__ int wsum[kOwnWarps];
-    __shared__ int is_last;
-    auto bar = [&](int s) { return base + a.off_bar + 8u * (warp * a.stages + s); };
-    if (lane == 0) {
-        for (int s = 0; s < a.stages; ++s) mbar_init(bar(s), 1);
-        fence_mbar_init();
-        if (warp == 0) {
-            prefetch_map(&mK);
-            prefetch_map(&mV);
+    __shared__ int wsum[kOwnWarps + 1];
+    const uint32_t bars = base + a.off_bar;
+    auto full = [&](int i) { return bars + 8u * i; };
+    auto empty = [&](int i) { return bars + 8u * (kOwnSlots + i); };
+    auto q_full = [&](int i) { return bars + 8u * (2 * kOwnSlots + i); };
+    auto q_empty = [&](int i) { return bars + 8u * (2 * kOwnSlots + kOwnQ + i); };
+    // parts of run r in buffer r % nbuf: filled by every computing warp, joined by one of them
+    auto parts_full = [&](int i) { return bars + 8u * (2 * kOwnSlots + 2 * kOwnQ + i); };
+    auto parts_free = [&](int i) { return bars + 8u * (2 * kOwnSlots + 2 * kOwnQ + 2 + i); };
+    if (tid == 0) {
+        for (int i = 0; i < a.slots; ++i) {
+            mbar_init(full(i), 1);
+            mbar_init(empty(i), kOwnWarps);
         }
+        for (int i = 0; i < kOwnQ; ++i) {
+            mbar_init(q_full(i), 1);
+            mbar_init(q_empty(i), kOwnWarps);
+        }
+        for (int i = 0; i < a.nbuf; ++i) {
+            mbar_init(parts_full(i), kOwnWarps);
+            mbar_init(parts_free(i), 1);
+        }
+        fence_mbar_init();
+        prefetch_map(&mQ);
+        prefetch_map(&mK);
+        prefetch_map(&mV);
     }
-    pdl_wait();  // the preceding kernel (the prefix kernel, if there is one) has completed
+    pdl_wait();
 
     // ------------------------------------------------------------ units of every sequence
-    const int page_size = 1 << a.page_shift;
     {
         const int64_t most = a.table_ld << a.page_shift;
         const int per = (a.batch + kOwnThreads - 1) / kOwnThreads, b0 = tid * per;
@@ -184,279 +228,479 @@ __global__ void __launch_bounds__(kOwnThreads, OwnLayout<D>::CTAS) paged_own_ker
     const int64_t U = static_cast<int64_t>(pre[a.batch]) * HR;
     const int G = static_cast<int>(min(static_cast<int64_t>(gridDim.x), U));   // CTAs with work: one unit at least
     if (static_cast<int>(blockIdx.x) >= G) return;
-    const int64_t u0 = blockIdx.x * U / G, u1 = (blockIdx.x + 1) * U / G;
+    const int64_t u0 = blockIdx.x * U / G;
+    const int total = static_cast<int>((blockIdx.x + 1) * U / G - u0);
 
-    auto enter = [&](Cursor& k) {   // sequence k.b
-        k.n = pre[k.b + 1] - pre[k.b];
-        k.len = slen[k.b];
+    auto locate = [&](int64_t u, Cursor& k) {
+        int lo = 0, hi = a.batch - 1;   // the last sequence that starts at or before u
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (static_cast<int64_t>(pre[mid]) * HR <= u) lo = mid; else hi = mid - 1;
+        }
+        k.b = lo;
+        k.n = pre[lo + 1] - pre[lo];
+        k.len = slen[lo];
+        const int64_t in = u - static_cast<int64_t>(pre[lo]) * HR;
+        if ((in >> 32) == 0) {
+            k.hr = static_cast<int>(static_cast<uint32_t>(in) / static_cast<uint32_t>(k.n));
+            k.j = static_cast<int>(static_cast<uint32_t>(in) % static_cast<uint32_t>(k.n));
+        } else {
+            k.hr = static_cast<int>(in / k.n);
+            k.j = static_cast<int>(in % k.n);
+        }
     };
+
+    if (warp == kOwnWarps) {
+        // ---------------------------------------------------------------- loads
+        const int box_shift = min(a.page_shift, 6);              // keys of one TMA box
+        struct Place {
+            int row[4];      // cache rows of the unit's boxes
+            int boxes;       // boxes with keys; 0 where the sequence has none
+            int qrow;        // first query row if a run begins here, else -1
+        };
+        auto place = [&](int i, Place& p) {   // unit u0 + i
+            p.boxes = 0;
+            p.qrow = -1;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) p.row[x] = a.cache_rows;
+            if (i >= total) return;
+            Cursor k;
+            locate(u0 + i, k);
+            const int head = k.hr / a.rt, nk = min(kUnit, k.len - k.j * kUnit);
+            p.boxes = nk > 0 ? (nk + (1 << box_shift) - 1) >> box_shift : 0;
+            if ((i == 0 || k.j == 0) && nk > 0) p.qrow = k.b * a.hq + head * a.group + (k.hr % a.rt) * 16;
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                if (x < p.boxes) {
+                    const int key = k.j * kUnit + (x << box_shift);
+                    const int page = a.table[k.b * a.table_ld + (key >> a.page_shift)];
+                    if (page >= 0 && page < a.num_pages)
+                        p.row[x] = ((page * a.hk + head) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+                    else
+                        atomicExch(a.bad, 1);   // its rows stay past the cache: zeros
+                }
+        };
+        int slot = 0, loads = 0, qs = 0, qloads = 0;
+        uint32_t phase = 0, qphase = 0;          // completions of the current slot's barriers so far, mod 2
+        bool ok = true;
+        Place cur, ahead;
+        place(lane, cur);
+        for (int i0 = 0; ok && i0 < total; i0 += 32) {
+            place(i0 + 32 + lane, ahead);
+            for (int x = 0; ok && x < 32 && i0 + x < total; ++x) {
+                const int boxes = __shfl_sync(0xffffffffu, cur.boxes, x);
+                if (boxes == 0) continue;
+                const int qrow = __shfl_sync(0xffffffffu, cur.qrow, x);
+                if (qrow >= 0) {
+                    if (qloads >= kOwnQ && !__all_sync(0xffffffffu, mbar_wait_bounded(q_empty(qs), qphase ^ 1u, a.flag))) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) mbar_arrive_expect_tx(q_full(qs), static_cast<uint32_t>(a.rows) * (D * 2));
+                    __syncwarp();
+                    if (lane < L::ATOMS) tma_load_2d(base + a.off_q + qs * L::QSLOT + lane * L::QATOM, &mQ, 64 * lane, qrow, q_full(qs));
+                    ++qloads;
+                    if (++qs == kOwnQ) {
+                        qs = 0;
+                        qphase ^= 1u;
+                    }
+                }
+                // lane l < boxes * ATOMS loads component atom l % ATOMS of box l / ATOMS
+                int row = 0;
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const int r = __shfl_sync(0xffffffffu, cur.row[y], x);
+                    if (lane / L::ATOMS == y) row = r;
+                }
+                const int atom = lane % L::ATOMS, box = lane / L::ATOMS;
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    if (loads >= a.slots && !__all_sync(0xffffffffu, mbar_wait_bounded(empty(slot), phase ^ 1u, a.flag))) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) mbar_arrive_expect_tx(full(slot), static_cast<uint32_t>(boxes << box_shift) * (D * 2));
+                    __syncwarp();
+                    if (box < boxes)
+                        tma_load_2d(base + slot * L::SLOT + atom * L::ATOM + ((static_cast<uint32_t>(box) << box_shift) * 128), kv ? &mV : &mK, 64 * atom, row, full(slot));
+                    ++loads;
+                    if (++slot == a.slots) {
+                        slot = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            cur = ahead;
+        }
+        if (!ok) {   // after a wait that ran out: copies in flight land before the shared memory goes away
+            for (int j = max(0, loads - a.slots); j < loads; ++j) (void)mbar_wait_drain(full(j % a.slots), (j / a.slots) & 1);
+            for (int j = max(0, qloads - kOwnQ); j < qloads; ++j) (void)mbar_wait_drain(q_full(j % kOwnQ), (j / kOwnQ) & 1);
+        }
+        return;
+    }
+
+    // -------------------------------------------------------------------- joining a run's parts
+    const int g = lane / 4, t = lane % 4;
+    float* om = reinterpret_cast<float*>(gbase + a.off_om);      // [nbuf][warp][rows][D]
+    float* ml = reinterpret_cast<float*>(gbase + a.off_ml);      // [nbuf][warp][16][2]
+    // By one warp: kAt x 32 pieces of four output columns at a time.
+    auto join_run = [&](int b, int hr, int j0, int j1, int n, const float* omb, const float* mlb) {
+        constexpr int kAt = 2;
+        const int head = hr / a.rt, row0 = (hr % a.rt) * 16, rows = min(a.rows, a.group - row0);
+        int c0 = 0, c1 = 0;
+        bool last = j0 == 0 && j1 == n;
+        if (!last) {
+            const int64_t first = static_cast<int64_t>(pre[b]) * HR + static_cast<int64_t>(hr) * n;
+            c0 = cta_of(first, U, G);
+            c1 = cta_of(first + n - 1, U, G);
+        }
+        const int64_t orow = static_cast<int64_t>(b) * a.hq + head * a.group + row0;
+        for (int pass = 0; pass < 2; ++pass) {
+            // pass 0: the warps' parts, to the output if this is all of the item, else to the workspace;
+            // pass 1 (the CTA that arrives last): the CTAs' parts, to the output
+            for (int i0 = 0; i0 < rows * (D / 4); i0 += 32 * kAt) {
+                float m[kAt], l[kAt];
+                float4 acc[kAt];
+                int r[kAt], col[kAt];
+#pragma unroll
+                for (int k = 0; k < kAt; ++k) {
+                    const int i = min(i0 + 32 * k + lane, rows * (D / 4) - 1);   // past the end: the last piece again
+                    r[k] = i / (D / 4);
+                    col[k] = i % (D / 4);
+                    m[k] = -INFINITY;
+                    l[k] = 0.0f;
+                    acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                }
+                if (pass == 0) {
+#pragma unroll
+                    for (int w = 0; w < kOwnWarps; ++w)
+#pragma unroll
+                        for (int k = 0; k < kAt; ++k) {
+                            const float2 x = *reinterpret_cast<const float2*>(mlb + (w * 16 + r[k]) * 2);
+                            join(m[k], l[k], acc[k], x.x, x.y, *reinterpret_cast<const float4*>(omb + (w * a.rows + r[k]) * D + 4 * col[k]));
+                        }
+                } else {
+                    join_parts<kAt>(c0, c1, m, l, acc, [&](int c, int k, float& pm, float& pl) {
+                        const int64_t at = static_cast<int64_t>(2 * c + (c == c0 ? 1 : 0)) * a.rows + r[k];
+                        const float2 x = __ldcg(reinterpret_cast<const float2*>(a.oml + 2 * at));
+                        pm = x.x;
+                        pl = x.y;
+                        return reinterpret_cast<const float4*>(a.oo + at * D + 4 * col[k]);
+                    });
+                }
+#pragma unroll
+                for (int k = 0; k < kAt; ++k) {
+                    if (last && a.plen == 0) {
+                        // l == 0: no key (or none with a score above -inf): zeros
+                        const float inv = l[k] == 0.0f ? 0.0f : 1.0f / l[k];
+                        uint2 w;
+                        w.x = l[k] == 0.0f ? 0u : pack2<T>(acc[k].x * inv, acc[k].y * inv);
+                        w.y = l[k] == 0.0f ? 0u : pack2<T>(acc[k].z * inv, acc[k].w * inv);
+                        *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + (orow + r[k]) * D + 4 * col[k]) = w;
+                    } else {   // a part for the item's last CTA, or the row's own part for paged_join_kernel
+                        const int64_t at = last ? orow + r[k] : static_cast<int64_t>(2 * blockIdx.x + (j0 == 0 ? 1 : 0)) * a.rows + r[k];
+                        if (col[k] == 0) *reinterpret_cast<float2*>((last ? a.rml : a.oml) + 2 * at) = make_float2(m[k], l[k]);
+                        *reinterpret_cast<float4*>((last ? a.ro : a.oo) + at * D + 4 * col[k]) = acc[k];
+                    }
+                }
+            }
+            if (last) return;
+            __threadfence();
+            __syncwarp();
+            int arrived = 0;
+            if (lane == 0) arrived = atomicAdd(a.count + c0, 1);
+            last = __shfl_sync(0xffffffffu, arrived, 0) == c1 - c0;
+            if (!last) return;
+            __threadfence();
+            if (lane == 0) a.count[c0] = 0;
+        }
+    };
+
+    // -------------------------------------------------------------------- units
+    Cursor cur;
+    locate(u0, cur);
+    cur.left = total;
     auto next = [&](Cursor& k) {
         --k.left;
         if (++k.j < k.n) return;
         k.j = 0;
         if (++k.hr < HR) return;
         k.hr = 0;
-        if (++k.b < a.batch) enter(k);
-    };
-    Cursor cur;
-    {
-        int lo = 0, hi = a.batch - 1;   // the last sequence that starts at or before u0
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) / 2;
-            if (static_cast<int64_t>(pre[mid]) * HR <= u0) lo = mid; else hi = mid - 1;
+        if (++k.b < a.batch) {
+            k.n = pre[k.b + 1] - pre[k.b];
+            k.len = slen[k.b];
         }
-        cur.left = static_cast<int>(u1 - u0);
-        cur.b = lo;
-        enter(cur);
-        const int64_t in = u0 - static_cast<int64_t>(pre[lo]) * HR;
-        cur.hr = static_cast<int>(in / cur.n);
-        cur.j = static_cast<int>(in % cur.n);
-    }
-    auto key0 = [&](const Cursor& k) { return k.j * kUnit + warp * kChunk; };   // first key of this warp
-    // -------------------------------------------------------------------- loads
-    const uint32_t ring = base + static_cast<uint32_t>(warp * a.stages) * L::STAGE;
-    Cursor ahead = cur;
-    int fs = 0, pending = 0;     // stage loaded next; chunks loaded and not used yet
-    auto skip_empty = [&] {
-        while (ahead.left > 0 && key0(ahead) >= ahead.len) next(ahead);
     };
-    int page = -1;
-    auto look = [&] {   // the page of the chunk that is loaded next
-        skip_empty();
-        if (ahead.left > 0) page = a.table[ahead.b * a.table_ld + (key0(ahead) >> a.page_shift)];
+    int slot = 0, qs = 0, buf = 0, turn = 0;   // turn: the warp that joins this run's parts
+    uint32_t phase = 0, qphase = 0, buf_phase = 0;
+    bool ok = true, reuse = false;             // reuse: the buffers of parts have been used
+    // Wait for a slot; done() gives it back.
+    auto wait_full = [&](uint32_t bar, uint32_t ph) {
+        ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar, ph, a.flag));
+        return ok;
     };
-    auto fetch = [&] {
-        if (ahead.left <= 0) return;
-        if (lane == 0) {
-            int row = a.cache_rows;     // past the cache: zeros
-            if (page >= 0 && page < a.num_pages)
-                row = ((page * a.hk + ahead.hr / a.rt) << a.page_shift) + (key0(ahead) & (page_size - 1));
-            else
-                atomicExch(a.bad, 1);
-            const uint32_t dst = ring + static_cast<uint32_t>(fs) * L::STAGE;
-            mbar_arrive_expect_tx(bar(fs), L::STAGE);
-#pragma unroll
-            for (int i = 0; i < D / 64; ++i) tma_load_2d(dst + i * L::ATOM, &mK, 64 * i, row, bar(fs));
-#pragma unroll
-            for (int i = 0; i < D / 64; ++i) tma_load_2d(dst + L::KV + i * L::ATOM, &mV, 64 * i, row, bar(fs));
+    auto done = [&] {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty(slot));
+        if (++slot == a.slots) {
+            slot = 0;
+            phase ^= 1u;
         }
-        if (++fs == a.stages) fs = 0;
-        ++pending;
-        next(ahead);
-        look();
     };
-    look();
-    for (int s = 0; s < a.stages; ++s) fetch();
-
-    // -------------------------------------------------------------------- units
-    int cs = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    // ldmatrix addresses: key and 16-byte column of this lane's matrix row, K and V (transposed)
-    const int kkey = ((lane >> 4) << 3) | (lane & 7), kcol = (lane >> 3) & 1;
-    const int vkey = (((lane >> 3) & 1) << 3) | (lane & 7), vcol = lane >> 4;
+    // ldmatrix addresses: row and 16-byte column of this lane's matrix row, for Q, K and V (transposed)
+    const int qrow = lane & 15, qcol = lane >> 4;
+    const int kkey = warp * kChunk + (((lane >> 4) << 3) | (lane & 7)), kcol = (lane >> 3) & 1;
+    const int vkey = warp * kChunk + ((((lane >> 3) & 1) << 3) | (lane & 7)), vcol = lane >> 4;
+    auto swz = [](int row, int col) { return static_cast<uint32_t>(row * 128 + (((col & 7) ^ (row & 7)) << 4)); };
     while (cur.left > 0) {
         // ---- a run of units of one sequence and head: this CTA's part of it
         const int b = cur.b, hr = cur.hr, j0 = cur.j, n = cur.n;
-        const int head = hr / a.rt, row0 = (hr % a.rt) * 16;
-        const int rows = min(a.rows, a.group - row0);
         const int j1 = min(n - j0, cur.left) + j0;
-        uint32_t qf[D / 16][4];
-        {
-            const T* q = static_cast<const T*>(a.q) + (static_cast<int64_t>(b) * a.hq + head * a.group + row0) * D;
-            const uint32_t* q0 = reinterpret_cast<const uint32_t*>(q + static_cast<int64_t>(g) * D + 2 * t);
-            const uint32_t* q1 = reinterpret_cast<const uint32_t*>(q + static_cast<int64_t>(g + 8) * D + 2 * t);
+        const int rows = min(a.rows, a.group - (hr % a.rt) * 16);
+        const bool any = cur.len > 0;
+        const uint32_t qb = base + a.off_q + qs * L::QSLOT;
+        auto load_q = [&](uint32_t (&f)[4], int k) { ldsm4(f, qb + (k / 4) * L::QATOM + swz(qrow, 2 * k + qcol)); };
+        auto free_q = [&] {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_empty(qs));
+            if (++qs == kOwnQ) {
+                qs = 0;
+                qphase ^= 1u;
+            }
+        };
+        uint32_t qf[L::Q_REGS ? D / 16 : 1][4];
+        if (any && wait_full(q_full(qs), qphase)) {
+            if constexpr (L::Q_REGS) {
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                qf[k][0] = g < rows ? q0[8 * k] : 0u;
-                qf[k][1] = g + 8 < rows ? q1[8 * k] : 0u;
-                qf[k][2] = g < rows ? q0[8 * k + 4] : 0u;
-                qf[k][3] = g + 8 < rows ? q1[8 * k + 4] : 0u;
+                for (int k = 0; k < D / 16; ++k) load_q(qf[k], k);
+                free_q();
             }
         }
         float o[D / 8][4] = {};
         float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;   // rows g and g + 8
         for (int j = j0; j < j1; ++j, next(cur)) {
-            const int nv = cur.len - key0(cur);      // keys of the chunk in use
-            if (nv <= 0 || !ok) continue;
-            if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar(cs), phase, a.flag))) {
-                ok = false;
-                continue;
-            }
-            const uint32_t kb = ring + static_cast<uint32_t>(cs) * L::STAGE, vb = kb + L::KV;
-            float s[2][4] = {};
+            if (!any) continue;
+            const int nv = cur.len - j * kUnit - warp * kChunk;       // keys of this warp in use
+            if (!wait_full(full(slot), phase)) continue;
+            uint32_t p[4];
+            if (nv > 0) {
+                const uint32_t kb = base + slot * L::SLOT;
+                float s[2][4] = {};
+                {
+                    // fragments are loaded kDeep steps ahead; even and odd steps add up apart
+                    constexpr int kDeep = L::Q_REGS ? 4 : 2;
+                    float s2[2][4] = {};
+                    uint32_t f[kDeep][4], fq[kDeep][4];
+                    auto load = [&](int k) {
+                        ldsm4(f[k % kDeep], kb + (k / 4) * L::ATOM + swz(kkey, 2 * k + kcol));
+                        if constexpr (!L::Q_REGS) load_q(fq[k % kDeep], k);
+                    };
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                uint32_t f[4];
-                ldsm4(f, kb + (k / 4) * L::ATOM + kkey * 128 + ((((2 * k + kcol) & 7) ^ (kkey & 7)) << 4));
-                mma16816<T>(s[0], qf[k], f[0], f[1]);
-                mma16816<T>(s[1], qf[k], f[2], f[3]);
-            }
+                    for (int k = 0; k < kDeep; ++k) load(k);
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    s[i][e] *= a.c;
-                    if (8 * i + 2 * t + (e & 1) >= nv) s[i][e] = -INFINITY;
-                }
-            float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-            float x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
-            x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
-            x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
-            x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
-            x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
-            constexpr float SH = Shift<T>::V;
-            const bool up0 = x0 > m0 + (SH + kLag), up1 = x1 > m1 + (SH + kLag);
-            if (__any_sync(0xffffffffu, up0 || up1)) {
-                const float n0 = up0 ? x0 - SH : m0, n1 = up1 ? x1 - SH : m1;
-                const float a0 = up0 ? ex2f(m0 - n0) : 1.0f, a1 = up1 ? ex2f(m1 - n1) : 1.0f;
-                m0 = n0;
-                m1 = n1;
-                l0 *= a0;
-                l1 *= a1;
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    o[i][0] *= a0;
-                    o[i][1] *= a0;
-                    o[i][2] *= a1;
-                    o[i][3] *= a1;
-                }
-            }
-            const float r0 = m0 == -INFINITY ? 0.0f : m0, r1 = m1 == -INFINITY ? 0.0f : m1;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                s[i][0] = ex2f(s[i][0] - r0);
-                s[i][1] = ex2f(s[i][1] - r0);
-                s[i][2] = ex2f(s[i][2] - r1);
-                s[i][3] = ex2f(s[i][3] - r1);
-            }
-            l0 += (s[0][0] + s[0][1]) + (s[1][0] + s[1][1]);
-            l1 += (s[0][2] + s[0][3]) + (s[1][2] + s[1][3]);
-            // the weights rounded to T for the product with V; the sums above are of the unrounded ones
-            const uint32_t p[4] = {pack2<T>(s[0][0], s[0][1]), pack2<T>(s[0][2], s[0][3]),
-                                   pack2<T>(s[1][0], s[1][1]), pack2<T>(s[1][2], s[1][3])};
-            auto pv = [&](auto tail) {
-                // keys past the sequence's end: 0 x whatever lies in the page must be 0
-                const uint32_t k0 = tail ? (2 * t < nv ? 0xFFFFu : 0u) | (2 * t + 1 < nv ? 0xFFFF0000u : 0u) : 0u;
-                const uint32_t k1 = tail ? (2 * t + 8 < nv ? 0xFFFFu : 0u) | (2 * t + 9 < nv ? 0xFFFF0000u : 0u) : 0u;
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    uint32_t f[4];
-                    ldsm4_t(f, vb + (k / 4) * L::ATOM + vkey * 128 + ((((2 * k + vcol) & 7) ^ (vkey & 7)) << 4));
-                    if (tail) {
-                        f[0] &= k0;
-                        f[1] &= k1;
-                        f[2] &= k0;
-                        f[3] &= k1;
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t (&q)[4] = L::Q_REGS ? qf[L::Q_REGS ? k : 0] : fq[k % kDeep];
+                        mma16816<T>(k & 1 ? s2[0] : s[0], q, f[k % kDeep][0], f[k % kDeep][1]);
+                        mma16816<T>(k & 1 ? s2[1] : s[1], q, f[k % kDeep][2], f[k % kDeep][3]);
+                        if (k + kDeep < D / 16) load(k + kDeep);
                     }
-                    mma16816<T>(o[2 * k], p, f[0], f[1]);
-                    mma16816<T>(o[2 * k + 1], p, f[2], f[3]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        s[0][e] += s2[0][e];
+                        s[1][e] += s2[1][e];
+                    }
                 }
-            };
-            if (nv >= kChunk) pv(std::false_type{});
-            else pv(std::true_type{});
-            __syncwarp();       // every lane has read the stage
-            --pending;
-            if (++cs == a.stages) {
-                cs = 0;
-                phase ^= 1u;
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        s[i][e] *= a.c;
+                        if (8 * i + 2 * t + (e & 1) >= nv) s[i][e] = -INFINITY;
+                    }
+                float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
+                float x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+                x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
+                x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
+                x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
+                x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
+                constexpr float SH = Shift<T>::V;
+                const bool up0 = x0 > m0 + (SH + kLag), up1 = x1 > m1 + (SH + kLag);
+                if (__any_sync(0xffffffffu, up0 || up1)) {
+                    const float n0 = up0 ? x0 - SH : m0, n1 = up1 ? x1 - SH : m1;
+                    const float a0 = up0 ? ex2f(m0 - n0) : 1.0f, a1 = up1 ? ex2f(m1 - n1) : 1.0f;
+                    m0 = n0;
+                    m1 = n1;
+                    l0 *= a0;
+                    l1 *= a1;
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i) {
+                        o[i][0] *= a0;
+                        o[i][1] *= a0;
+                        o[i][2] *= a1;
+                        o[i][3] *= a1;
+                    }
+                }
+                const float r0 = m0 == -INFINITY ? 0.0f : m0, r1 = m1 == -INFINITY ? 0.0f : m1;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    s[i][0] = ex2f(s[i][0] - r0);
+                    s[i][1] = ex2f(s[i][1] - r0);
+                    s[i][2] = ex2f(s[i][2] - r1);
+                    s[i][3] = ex2f(s[i][3] - r1);
+                }
+                l0 += (s[0][0] + s[0][1]) + (s[1][0] + s[1][1]);
+                l1 += (s[0][2] + s[0][3]) + (s[1][2] + s[1][3]);
+                // the weights rounded to T for the product with V; the sums above are of the unrounded ones
+                p[0] = pack2<T>(s[0][0], s[0][1]);
+                p[1] = pack2<T>(s[0][2], s[0][3]);
+                p[2] = pack2<T>(s[1][0], s[1][1]);
+                p[3] = pack2<T>(s[1][2], s[1][3]);
             }
-            fetch();
+            done();
+            if (!wait_full(full(slot), phase)) continue;
+            if (nv > 0) {
+                const uint32_t vb = base + slot * L::SLOT;
+                auto pv = [&](auto tail) {
+                    // keys past the sequence's end: 0 x whatever lies in the page must be 0
+                    const uint32_t k0 = tail ? (2 * t < nv ? 0xFFFFu : 0u) | (2 * t + 1 < nv ? 0xFFFF0000u : 0u) : 0u;
+                    const uint32_t k1 = tail ? (2 * t + 8 < nv ? 0xFFFFu : 0u) | (2 * t + 9 < nv ? 0xFFFF0000u : 0u) : 0u;
+                    constexpr int kDeep = L::Q_REGS ? 3 : 2;
+                    uint32_t f[kDeep][4];
+                    auto load = [&](int k) { ldsm4_t(f[k % kDeep], vb + (k / 4) * L::ATOM + swz(vkey, 2 * k + vcol)); };
+#pragma unroll
+                    for (int k = 0; k < kDeep; ++k) load(k);
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        uint32_t (&r)[4] = f[k % kDeep];
+                        if (tail) {
+                            r[0] &= k0;
+                            r[1] &= k1;
+                            r[2] &= k0;
+                            r[3] &= k1;
+                        }
+                        mma16816<T>(o[2 * k], p, r[0], r[1]);
+                        mma16816<T>(o[2 * k + 1], p, r[2], r[3]);
+                        if (k + kDeep < D / 16) load(k + kDeep);
+                    }
+                };
+                if (nv >= kChunk) pv(std::false_type{});
+                else pv(std::true_type{});
+            }
+            done();
         }
+        if (!L::Q_REGS && any) free_q();
         // ---- the warps' parts
         l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
         l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
         l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
         l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+        if (reuse) wait_full(parts_free(buf), buf_phase ^ 1u);
+        float* omb = om + buf * (kOwnWarps * a.rows * D);
+        float* mlb = ml + buf * (kOwnWarps * 32);
+        if (ok) {
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-            if (g < rows) *reinterpret_cast<float2*>(om + (warp * a.rows + g) * D + 8 * i + 2 * t) = make_float2(o[i][0], o[i][1]);
-            if (g + 8 < rows) *reinterpret_cast<float2*>(om + (warp * a.rows + g + 8) * D + 8 * i + 2 * t) = make_float2(o[i][2], o[i][3]);
-        }
-        if (t == 0) {
-            if (g < rows) {
-                ml[(warp * a.rows + g) * 2] = m0;
-                ml[(warp * a.rows + g) * 2 + 1] = l0;
+            for (int i = 0; i < D / 8; ++i) {
+                if (g < rows) *reinterpret_cast<float2*>(omb + (warp * a.rows + g) * D + 8 * i + 2 * t) = make_float2(o[i][0], o[i][1]);
+                if (g + 8 < rows) *reinterpret_cast<float2*>(omb + (warp * a.rows + g + 8) * D + 8 * i + 2 * t) = make_float2(o[i][2], o[i][3]);
             }
-            if (g + 8 < rows) {
-                ml[(warp * a.rows + g + 8) * 2] = m1;
-                ml[(warp * a.rows + g + 8) * 2 + 1] = l1;
+            if (t == 0) {
+                if (g < rows) *reinterpret_cast<float2*>(mlb + (warp * 16 + g) * 2) = make_float2(m0, l0);
+                if (g + 8 < rows) *reinterpret_cast<float2*>(mlb + (warp * 16 + g + 8) * 2) = make_float2(m1, l1);
             }
         }
-        __syncthreads();
-        const bool whole = j0 == 0 && j1 == n;
-        const int64_t first = static_cast<int64_t>(pre[b]) * HR + static_cast<int64_t>(hr) * n;   // the item's first unit
-        // the parts of the shared prefix, then the division
-        auto finish = [&](int r, int col, float m, float l, float4 acc) {
-            if (a.plen > 0) {
-                const int prow = b * a.group + row0 + r;
-                const int pit = head * a.prt + prow / 128, lr = prow % 128;
-                const int64_t PU = static_cast<int64_t>(a.hk) * a.prt * a.ptiles, p0 = static_cast<int64_t>(pit) * a.ptiles;
-                const int c1 = cta_of(p0 + a.ptiles - 1, PU, a.pgrid);
-                for (int c = cta_of(p0, PU, a.pgrid); c <= c1; ++c) {
-                    const int64_t at = static_cast<int64_t>(c + pit) * 128 + lr;
-                    const float4 pm = *reinterpret_cast<const float4*>(a.pml + at * 4);
-                    join(m, l, acc, pm.x, pm.y + pm.z, *reinterpret_cast<const float4*>(a.po + at * D + 4 * col));
-                }
-            }
-            // l == 0: no key (or none with a score above -inf): zeros
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            uint2 w;
-            w.x = l == 0.0f ? 0u : pack2<T>(acc.x * inv, acc.y * inv);
-            w.y = l == 0.0f ? 0u : pack2<T>(acc.z * inv, acc.w * inv);
-            T* dst = static_cast<T*>(a.o) + (static_cast<int64_t>(b) * a.hq + head * a.group + row0 + r) * D + 4 * col;
-            *reinterpret_cast<uint2*>(dst) = w;
-        };
-        for (int i = tid; i < rows * (D / 4); i += kOwnThreads) {
-            const int r = i / (D / 4), col = i % (D / 4);
-            float m = -INFINITY, l = 0.0f;
-            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-            for (int w = 0; w < kOwnWarps; ++w) {
-                const int at = w * a.rows + r;
-                join(m, l, acc, ml[2 * at], ml[2 * at + 1], *reinterpret_cast<const float4*>(om + at * D + 4 * col));
-            }
-            if (whole) {
-                finish(r, col, m, l, acc);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(parts_full(buf));
+        // the warps take turns in joining a run's parts; the others go on with the next run meanwhile
+        if (turn == warp) {
+            if (wait_full(parts_full(buf), buf_phase)) join_run(b, hr, j0, j1, n, omb, mlb);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(parts_free(buf));
+        }
+        if (++turn == kOwnWarps) turn = 0;
+        if (++buf == a.nbuf) {
+            buf = 0;
+            buf_phase ^= 1u;
+            reuse = true;
+        }
+    }
+}
+
+// With a shared prefix, the last step: a row's own part and the prefix's parts.  One warp per query row, lane c
+// taking D / 32 columns.
+constexpr int kJoinThreads = 128;
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedArgs a) {
+    constexpr int W = D / 32;
+    pdl_begin();
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kJoinThreads / 32) + threadIdx.x / 32;
+    const int lane = threadIdx.x % 32;
+    if (row >= static_cast<int64_t>(a.batch) * a.hq) return;
+    const int b = static_cast<int>(row / a.hq), h = static_cast<int>(row % a.hq);
+    const int head = h / a.group, prow = b * a.group + h % a.group;
+    const int pit = head * a.prt + prow / 128;
+    const int64_t PU = static_cast<int64_t>(a.hk) * a.prt * a.ptiles, u = static_cast<int64_t>(pit) * a.ptiles;
+    const int c0 = cta_of(u, PU, a.pgrid), np = cta_of(u + a.ptiles - 1, PU, a.pgrid) - c0 + 1;
+    // lane 0 has the row's own part, lanes 1 .. the prefix's; 31 of those at a time
+    float m = -INFINITY, l = 0.0f, acc[W] = {};
+    for (int p0 = 0; p0 < np; p0 += 31) {
+        const int n = min(31, np - p0);
+        const int64_t first = (static_cast<int64_t>(c0 + p0) + pit) * 128 + prow % 128;   // parts are 128 rows apart
+        float pm = -INFINITY, pl = 0.0f;
+        if (lane == 0) {
+            if (p0 == 0) {
+                const float2 x = *reinterpret_cast<const float2*>(a.rml + 2 * row);
+                pm = x.x;
+                pl = x.y;
             } else {
-                const int64_t at = static_cast<int64_t>(2 * blockIdx.x + (j0 == 0 ? 1 : 0)) * a.rows + r;
-                if (col == 0) *reinterpret_cast<float2*>(a.oml + 2 * at) = make_float2(m, l);
-                *reinterpret_cast<float4*>(a.oo + at * D + 4 * col) = acc;
+                pm = m;      // what has been joined so far
+                pl = l;
             }
+        } else if (lane <= n) {
+            const float4 x = *reinterpret_cast<const float4*>(a.pml + (first + 128 * (lane - 1)) * 4);
+            pm = x.x;
+            pl = x.y + x.z;
         }
-        if (!whole) {
-            const int c0 = cta_of(first, U, G), c1 = cta_of(first + n - 1, U, G);
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) is_last = atomicAdd(a.count + c0, 1) == c1 - c0;
-            __syncthreads();
-            if (is_last) {
-                __threadfence();
-                for (int i = tid; i < rows * (D / 4); i += kOwnThreads) {
-                    const int r = i / (D / 4), col = i % (D / 4);
-                    float m = -INFINITY, l = 0.0f;
-                    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float top = pm;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float w = pm == -INFINITY ? 0.0f : ex2f(pm - top);
+        float sum = pl * w;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float w0 = __shfl_sync(0xffffffffu, w, 0);
+        const float* own = a.ro + row * D + W * lane;
+#pragma unroll
+        for (int e = 0; e < W; ++e) acc[e] = (p0 == 0 ? own[e] : acc[e]) * w0;
 #pragma unroll 4
-                    for (int c = c0; c <= c1; ++c) {
-                        const int64_t at = static_cast<int64_t>(2 * c + (c == c0 ? 1 : 0)) * a.rows + r;
-                        const float2 q = __ldcg(reinterpret_cast<const float2*>(a.oml + 2 * at));
-                        join(m, l, acc, q.x, q.y, __ldcg(reinterpret_cast<const float4*>(a.oo + at * D + 4 * col)));
-                    }
-                    finish(r, col, m, l, acc);
+        for (int c = 0; c < n; ++c) {
+            const float* src = a.po + (first + 128 * c) * D + W * lane;
+            const float wc = __shfl_sync(0xffffffffu, w, c + 1);
+            float v[W];
+            if constexpr (W == 2) {
+                const float2 x = *reinterpret_cast<const float2*>(src);
+                v[0] = x.x;
+                v[1] = x.y;
+            } else {
+#pragma unroll
+                for (int e = 0; e < W; e += 4) {
+                    const float4 x = *reinterpret_cast<const float4*>(src + e);
+                    v[e] = x.x;
+                    v[e + 1] = x.y;
+                    v[e + 2] = x.z;
+                    v[e + 3] = x.w;
                 }
-                if (tid == 0) a.count[c0] = 0;
             }
+#pragma unroll
+            for (int e = 0; e < W; ++e) acc[e] += wc * v[e];
         }
-        __syncthreads();        // om, ml and is_last are free for the next part
+        m = top;
+        l = sum;
     }
-    // after a wait that ran out: the copies in flight land before the shared memory goes away
-    for (; pending > 0; --pending) {
-        (void)mbar_wait_drain(bar(cs), phase);
-        if (++cs == a.stages) {
-            cs = 0;
-            phase ^= 1u;
-        }
-    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    T* dst = static_cast<T*>(a.o) + row * D + W * lane;
+#pragma unroll
+    for (int e = 0; e < W; e += 2)
+        *reinterpret_cast<uint32_t*>(dst + e) = l == 0.0f ? 0u : pack2<T>(acc[e] * inv, acc[e + 1] * inv);
 }
 
 // ================================================================== the shared prefix
@@ -786,7 +1030,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix_kernel(const __gr
 // ================================================================== host side
 struct Sizes {
     int64_t rows, pitems;            // rows per part of own keys; prefix row tiles
-    size_t count, oml, oo, pml, po;  // byte offsets of the workspace's parts
+    size_t count, oml, oo, rml, ro, pml, po;  // byte offsets of the workspace's parts
     size_t bytes;
 };
 Sizes sizes(int64_t batch, int64_t hq, int64_t hk, int64_t D, int64_t plen) {
@@ -804,6 +1048,8 @@ Sizes sizes(int64_t batch, int64_t hq, int64_t hk, int64_t D, int64_t plen) {
     s.oml = part(2 * kOwnGrid * s.rows * 8);
     s.oo = part(2 * kOwnGrid * s.rows * D * 4);
     if (plen > 0) {
+        s.rml = part(batch * hq * 8);
+        s.ro = part(batch * hq * D * 4);
         s.pml = part((kPrefixGrid + s.pitems) * 128 * 16);
         s.po = part((kPrefixGrid + s.pitems) * 128 * D * 4);
     }
@@ -811,27 +1057,40 @@ Sizes sizes(int64_t batch, int64_t hq, int64_t hk, int64_t D, int64_t plen) {
     return s;
 }
 
-template <typename T, int D>
-int own_smem(PagedArgs* a, uint32_t* bytes) {
+// Ring slots, shared memory and CTAs per SM of paged_own_kernel: two CTAs with 64 KB of loads in flight each
+// where that fits, else one with as many as fit.
+template <int D>
+int own_smem(PagedArgs* a, uint32_t* bytes, int* ctas) {
     using L = OwnLayout<D>;
-    const uint32_t om = static_cast<uint32_t>(kOwnWarps * a->rows * D * 4), ml = kOwnWarps * 16 * 8, bars = 8u * kOwnWarps * 8;
-    const uint32_t pre = static_cast<uint32_t>(2 * a->batch + 1) * 4;
-    const uint32_t fixed = om + ml + bars + pre + 1024;
-    int st = 8;
-    while (st > 1 && st * kOwnWarps * L::STAGE + fixed > L::BUDGET) --st;
-    a->stages = st;
-    a->off_om = st * kOwnWarps * L::STAGE;
+    const uint32_t part = static_cast<uint32_t>(kOwnWarps * a->rows * D * 4), bars = 8u * (2 * kOwnSlots + 2 * kOwnQ + 4);
+    const uint32_t pre = static_cast<uint32_t>(2 * a->batch + 1) * 4, q = kOwnQ * L::QSLOT;
+    uint32_t om = 0, ml = 0;
+    int n = 0;
+    for (int choice = 0; choice < 3; ++choice) {   // CTAs and buffers of parts: 2, 2; 2, 1; 1, 1
+        *ctas = choice < 2 ? 2 : 1;
+        a->nbuf = choice == 0 ? 2 : 1;
+        om = a->nbuf * part;
+        ml = a->nbuf * kOwnWarps * 16 * 8;
+        const uint32_t fixed = q + om + ml + bars + pre + 1024;
+        const uint32_t budget = *ctas == 2 ? 112u * 1024u : static_cast<uint32_t>(kOwnSmem);
+        n = fixed < budget ? static_cast<int>((budget - fixed) / L::SLOT) : 0;
+        if (n * L::SLOT >= 64u * 1024u) break;
+    }
+    if (n < 1) return FUSE_EUNSUPPORTED;
+    a->slots = n < kOwnSlots ? n : kOwnSlots;
+    a->off_q = a->slots * L::SLOT;
+    a->off_om = a->off_q + q;
     a->off_ml = a->off_om + om;
     a->off_bar = a->off_ml + ml;
     a->off_pre = a->off_bar + bars;
     *bytes = a->off_pre + pre + 1024;
-    return *bytes <= kOwnSmem ? FUSE_OK : FUSE_EUNSUPPORTED;
+    return FUSE_OK;
 }
 
 template <typename T, int D>
 int run_paged(PagedArgs a, const void* k, const void* v, cudaStream_t st) {
     const bool bf = std::is_same<T, __nv_bfloat16>::value;
-    CUtensorMap mK, mV;
+    CUtensorMap mQ, mK, mV;
     if (a.plen > 0) {
         const int box = 1 << (a.page_shift < 7 ? a.page_shift : 7);
         if (!make_map(&mK, k, a.cache_rows, D, 64, box, bf) || !make_map(&mV, v, a.cache_rows, D, 64, box, bf)) return FUSE_ECUDA;
@@ -841,28 +1100,35 @@ int run_paged(PagedArgs a, const void* k, const void* v, cudaStream_t st) {
         rc = launch_pdl(paged_prefix_kernel<T, D>, dim3(static_cast<unsigned>(a.pgrid)), dim3(kPreThreads), smem, st, 1, mK, mV, a);
         if (rc != FUSE_OK) return rc;
     }
-    if (!make_map(&mK, k, a.cache_rows, D, 64, kChunk, bf) || !make_map(&mV, v, a.cache_rows, D, 64, kChunk, bf)) return FUSE_ECUDA;
+    const int box = 1 << (a.page_shift < 6 ? a.page_shift : 6);
+    if (!make_map(&mQ, a.q, static_cast<int64_t>(a.batch) * a.hq, D, 64, a.rows, bf) || !make_map(&mK, k, a.cache_rows, D, 64, box, bf) ||
+        !make_map(&mV, v, a.cache_rows, D, 64, box, bf))
+        return FUSE_ECUDA;
     uint32_t smem = 0;
-    int rc = own_smem<T, D>(&a, &smem);
+    int ctas = 0;
+    int rc = own_smem<D>(&a, &smem, &ctas);
     if (rc != FUSE_OK) return rc;
     rc = opt_in_smem((const void*)paged_own_kernel<T, D>, kOwnSmem, true);
     if (rc != FUSE_OK) return rc;
     // every CTA is resident at once; more than there can be units would have nothing to do
-    int64_t grid = static_cast<int64_t>(sm_count()) * OwnLayout<D>::CTAS;
+    int64_t grid = static_cast<int64_t>(sm_count()) * ctas;
     const int64_t units = static_cast<int64_t>(a.batch) * a.hk * a.rt * (ceil_div(a.table_ld << a.page_shift, kUnit) + 1);
     if (grid > units) grid = units;
     if (grid > kOwnGrid) grid = kOwnGrid;
     if (units / grid >= 0x7fffffffLL) return FUSE_EUNSUPPORTED;
-    return launch_pdl(paged_own_kernel<T, D>, dim3(static_cast<unsigned>(grid)), dim3(kOwnThreads), smem, st, 1, mK, mV, a);
+    rc = launch_pdl(paged_own_kernel<T, D>, dim3(static_cast<unsigned>(grid)), dim3(kOwnThreads), smem, st, 1, mQ, mK, mV, a);
+    if (rc != FUSE_OK || a.plen == 0) return rc;
+    const int64_t warps = static_cast<int64_t>(a.batch) * a.hq;
+    return launch_pdl(paged_join_kernel<T, D>, dim3(static_cast<unsigned>(ceil_div(warps, kJoinThreads / 32))), dim3(kJoinThreads), 0, st, 1, a);
 }
 
 }  // namespace
 
-int paged_report_count() { return 12; }
+int paged_report_count() { return 18; }
 int paged_report(int i, fuse_kernel_record* out) {
     const int smem_own = 111 * 1024;
     switch (i) {
-#define FC_OWN(N, T, TN, D) case N: return describe_kernel((const void*)paged_own_kernel<T, D>, "paged_own_kernel<" TN ", D=" #D "> (own keys)", kOwnThreads, D == 256 ? 224 * 1024 : smem_own, out)
+#define FC_OWN(N, T, TN, D) case N: return describe_kernel((const void*)paged_own_kernel<T, D>, "paged_own_kernel<" TN ", D=" #D "> (own keys)", kOwnThreads, smem_own, out)
 #define FC_PRE(N, T, TN, D) case N: return describe_kernel((const void*)paged_prefix_kernel<T, D>, "paged_prefix_kernel<" TN ", D=" #D "> (shared prefix, tcgen05)", kPreThreads, PrefixLayout<D>::SMEM, out, PrefixLayout<D>::TMEM_COLS)
         FC_OWN(0, __nv_bfloat16, "bf16", 64);
         FC_OWN(1, __nv_bfloat16, "bf16", 128);
@@ -876,6 +1142,14 @@ int paged_report(int i, fuse_kernel_record* out) {
         FC_PRE(9, __half, "f16", 64);
         FC_PRE(10, __half, "f16", 128);
         FC_PRE(11, __half, "f16", 256);
+#define FC_JOIN(N, T, TN, D) case N: return describe_kernel((const void*)paged_join_kernel<T, D>, "paged_join_kernel<" TN ", D=" #D "> (own part and prefix)", kJoinThreads, 0, out)
+        FC_JOIN(12, __nv_bfloat16, "bf16", 64);
+        FC_JOIN(13, __nv_bfloat16, "bf16", 128);
+        FC_JOIN(14, __nv_bfloat16, "bf16", 256);
+        FC_JOIN(15, __half, "f16", 64);
+        FC_JOIN(16, __half, "f16", 128);
+        FC_JOIN(17, __half, "f16", 256);
+#undef FC_JOIN
 #undef FC_OWN
 #undef FC_PRE
         default: return FUSE_EINVAL;
@@ -905,7 +1179,7 @@ extern "C" int fuse_paged_attention(const void* q, const void* k_cache, const vo
     if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1)) != 0) return FUSE_EUNSUPPORTED;
     const int64_t top = int64_t(1) << 31;
     if (batch > kMaxBatch || q_heads > 65536 || batch * q_heads >= top || num_pages >= top / (kv_heads * page_size) ||
-        table_ld >= (top - 256) / page_size || prefix_len >= top - 128)
+        table_ld >= (top - 4096) / page_size || prefix_len >= top - 4096)
         return FUSE_EUNSUPPORTED;
     // units of the whole batch, and tiles of the prefix, stay below 2^31
     if ((table_ld * page_size / kUnit + 1) * batch >= top) return FUSE_EUNSUPPORTED;
@@ -947,6 +1221,8 @@ extern "C" int fuse_paged_attention(const void* q, const void* k_cache, const vo
     a.count = reinterpret_cast<int*>(ws + s.count);
     a.oml = reinterpret_cast<float*>(ws + s.oml);
     a.oo = reinterpret_cast<float*>(ws + s.oo);
+    a.rml = reinterpret_cast<float*>(ws + s.rml);
+    a.ro = reinterpret_cast<float*>(ws + s.ro);
     a.pml = reinterpret_cast<float*>(ws + s.pml);
     a.po = reinterpret_cast<float*>(ws + s.po);
     a.plen = static_cast<int>(prefix_len);
