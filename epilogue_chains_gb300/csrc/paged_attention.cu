@@ -38,10 +38,10 @@ constexpr int kOwnThreads = 32 * (kOwnWarps + 1); // the last warp loads
 constexpr int kChunk = 16;                        // keys of a warp per unit
 constexpr int kUnit = kChunk * kOwnWarps;         // keys of a unit
 constexpr int kOwnSlots = 8;                       // most ring slots
-constexpr int kOwnQ = 2;                          // buffers of query rows
+constexpr int kOwnQ = 4;                          // buffers of query rows
 constexpr int kOwnGrid = 320;                     // most CTAs of paged_own_kernel (workspace bound)
-constexpr int kCounterBytes = 2048;
-static_assert(kOwnGrid * 4 <= kCounterBytes, "one counter per CTA");
+constexpr int kCounterBytes = 8192;
+static_assert(kOwnGrid * kOwnWarps * 4 <= kCounterBytes, "one counter per CTA and warp");
 constexpr int kPrefixGrid = 160;                  // most CTAs of paged_prefix_kernel (workspace bound)
 constexpr int kMaxBatch = 4096;
 constexpr int kOwnSmem = 226 * 1024;              // dynamic shared memory at most, next to a few static words
@@ -73,13 +73,13 @@ struct PagedArgs {
     int page_shift, num_pages;
     int cache_rows;                    // num_pages hk page_size: a row past the cache reads zeros
     float c;                           // scale * log2(e)
-    int slots, nbuf;                   // ring slots; buffers of the warps' parts
+    int slots;                         // of the ring
     uint32_t off_q, off_om, off_ml, off_bar, off_pre;
     // workspace
-    // A CTA's run has at most one item that began in an earlier CTA (its part has slot 2 c) and one
+    // A CTA's units have at most one item that began in an earlier CTA (its part has slot 2 c) and one
     // that goes on in a later one (slot 2 c + 1 if it begins here; an item begins in one CTA, which
     // names its counter).
-    int* count;                        // [kOwnGrid] parts that have arrived, by the item's first CTA
+    int* count;                        // [kOwnGrid][kOwnWarps] parts that have arrived, by the item's first CTA
     float *oml, *oo;                   // [2 kOwnGrid][rows] (m, l) and [..][rows][D]
     float *rml, *ro;                   // with a prefix: own part of every row, [batch hq] (m, l) and [..][D]
     float *pml, *po;                   // [kPrefixGrid + pitems][128] (m, l, l', -) and [..][128][D]
@@ -108,22 +108,17 @@ __device__ __forceinline__ void join(float& m, float& l, float4& acc, float m2, 
     m = nm;
 }
 
-// Join the parts c0 .. c1 that lie in memory, in order, for N pieces of four output columns; part(c, k, &m,
-// &l) gives the address of piece k of part c.  Two parts of all pieces are loaded at a time, so that their
-// memory latencies overlap.
-template <int N, typename F>
-__device__ __forceinline__ void join_parts(int c0, int c1, float (&m)[N], float (&l)[N], float4 (&acc)[N], F&& part) {
-    for (int c = c0; c <= c1; c += 2) {
-        float pm[2][N], pl[2][N];
-        float4 po[2][N];
+// Join the parts c0 .. c1 of four output columns that lie in memory, in order; part(c, &m, &l) gives the
+// address of part c's columns.  Eight parts are loaded at a time, so that their memory latencies overlap.
+template <typename F>
+__device__ __forceinline__ void join_parts(int c0, int c1, float& m, float& l, float4& acc, F&& part) {
+    for (int c = c0; c <= c1; c += 8) {
+        float pm[8], pl[8];
+        float4 po[8];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 8; ++i) po[i] = __ldcg(part(min(c + i, c1), pm[i], pl[i]));
 #pragma unroll
-            for (int k = 0; k < N; ++k) po[i][k] = __ldcg(part(min(c + i, c1), k, pm[i][k], pl[i][k]));
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int k = 0; k < N; ++k) join(m[k], l[k], acc[k], c + i <= c1 ? pm[i][k] : -INFINITY, pl[i][k], po[i][k]);
+        for (int i = 0; i < 8; ++i) join(m, l, acc, c + i <= c1 ? pm[i] : -INFINITY, pl[i], po[i]);
     }
 }
 
@@ -170,7 +165,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2) paged_own_kernel(
     auto empty = [&](int i) { return bars + 8u * (kOwnSlots + i); };
     auto q_full = [&](int i) { return bars + 8u * (2 * kOwnSlots + i); };
     auto q_empty = [&](int i) { return bars + 8u * (2 * kOwnSlots + kOwnQ + i); };
-    // parts of run r in buffer r % nbuf: filled by every computing warp, joined by one of them
+    // parts of run r in buffer r % 2, filled and joined by all computing warps
     auto parts_full = [&](int i) { return bars + 8u * (2 * kOwnSlots + 2 * kOwnQ + i); };
     auto parts_free = [&](int i) { return bars + 8u * (2 * kOwnSlots + 2 * kOwnQ + 2 + i); };
     if (tid == 0) {
@@ -182,9 +177,9 @@ __global__ void __launch_bounds__(kOwnThreads, 2) paged_own_kernel(
             mbar_init(q_full(i), 1);
             mbar_init(q_empty(i), kOwnWarps);
         }
-        for (int i = 0; i < a.nbuf; ++i) {
+        for (int i = 0; i < 2; ++i) {
             mbar_init(parts_full(i), kOwnWarps);
-            mbar_init(parts_free(i), 1);
+            mbar_init(parts_free(i), kOwnWarps);
         }
         fence_mbar_init();
         prefetch_map(&mQ);
@@ -341,78 +336,72 @@ __global__ void __launch_bounds__(kOwnThreads, 2) paged_own_kernel(
 
     // -------------------------------------------------------------------- joining a run's parts
     const int g = lane / 4, t = lane % 4;
-    float* om = reinterpret_cast<float*>(gbase + a.off_om);      // [nbuf][warp][rows][D]
-    float* ml = reinterpret_cast<float*>(gbase + a.off_ml);      // [nbuf][warp][16][2]
-    // By one warp: kAt x 32 pieces of four output columns at a time.
-    auto join_run = [&](int b, int hr, int j0, int j1, int n, const float* omb, const float* mlb) {
-        constexpr int kAt = 2;
-        const int head = hr / a.rt, row0 = (hr % a.rt) * 16, rows = min(a.rows, a.group - row0);
+    float* om = reinterpret_cast<float*>(gbase + a.off_om);      // [2][warp][rows][D]
+    float* ml = reinterpret_cast<float*>(gbase + a.off_ml);      // [2][warp][16][2]
+    // Every warp joins its share of the run's pieces of four output columns (and counts arrivals of its share).
+    struct Run {
+        int b, hr, j0, j1, n, buf;
+    };
+    auto join_run = [&](const Run& k) {
+        const int head = k.hr / a.rt, row0 = (k.hr % a.rt) * 16, rows = min(a.rows, a.group - row0);
+        if (warp * 32 >= rows * (D / 4)) return;
+        const float* omb = om + k.buf * (kOwnWarps * a.rows * D);
+        const float* mlb = ml + k.buf * (kOwnWarps * 32);
         int c0 = 0, c1 = 0;
-        bool last = j0 == 0 && j1 == n;
+        bool last = k.j0 == 0 && k.j1 == k.n;
         if (!last) {
-            const int64_t first = static_cast<int64_t>(pre[b]) * HR + static_cast<int64_t>(hr) * n;
+            const int64_t first = static_cast<int64_t>(pre[k.b]) * HR + static_cast<int64_t>(k.hr) * k.n;
             c0 = cta_of(first, U, G);
-            c1 = cta_of(first + n - 1, U, G);
+            c1 = cta_of(first + k.n - 1, U, G);
         }
-        const int64_t orow = static_cast<int64_t>(b) * a.hq + head * a.group + row0;
+        const int64_t orow = static_cast<int64_t>(k.b) * a.hq + head * a.group + row0;
         for (int pass = 0; pass < 2; ++pass) {
             // pass 0: the warps' parts, to the output if this is all of the item, else to the workspace;
-            // pass 1 (the CTA that arrives last): the CTAs' parts, to the output
-            for (int i0 = 0; i0 < rows * (D / 4); i0 += 32 * kAt) {
-                float m[kAt], l[kAt];
-                float4 acc[kAt];
-                int r[kAt], col[kAt];
-#pragma unroll
-                for (int k = 0; k < kAt; ++k) {
-                    const int i = min(i0 + 32 * k + lane, rows * (D / 4) - 1);   // past the end: the last piece again
-                    r[k] = i / (D / 4);
-                    col[k] = i % (D / 4);
-                    m[k] = -INFINITY;
-                    l[k] = 0.0f;
-                    acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                }
+            // pass 1 (where the CTA's warp arrives last): the CTAs' parts, to the output
+            for (int i = warp * 32 + lane; i < rows * (D / 4); i += 32 * kOwnWarps) {
+                const int r = i / (D / 4), col = i % (D / 4);
+                float m = -INFINITY, l = 0.0f;
+                float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 if (pass == 0) {
 #pragma unroll
-                    for (int w = 0; w < kOwnWarps; ++w)
-#pragma unroll
-                        for (int k = 0; k < kAt; ++k) {
-                            const float2 x = *reinterpret_cast<const float2*>(mlb + (w * 16 + r[k]) * 2);
-                            join(m[k], l[k], acc[k], x.x, x.y, *reinterpret_cast<const float4*>(omb + (w * a.rows + r[k]) * D + 4 * col[k]));
-                        }
+                    for (int w = 0; w < kOwnWarps; ++w) {
+                        const float2 x = *reinterpret_cast<const float2*>(mlb + (w * 16 + r) * 2);
+                        join(m, l, acc, x.x, x.y, *reinterpret_cast<const float4*>(omb + (w * a.rows + r) * D + 4 * col));
+                    }
                 } else {
-                    join_parts<kAt>(c0, c1, m, l, acc, [&](int c, int k, float& pm, float& pl) {
-                        const int64_t at = static_cast<int64_t>(2 * c + (c == c0 ? 1 : 0)) * a.rows + r[k];
+                    join_parts(c0, c1, m, l, acc, [&](int c, float& pm, float& pl) {
+                        const int64_t at = static_cast<int64_t>(2 * c + (c == c0 ? 1 : 0)) * a.rows + r;
                         const float2 x = __ldcg(reinterpret_cast<const float2*>(a.oml + 2 * at));
                         pm = x.x;
                         pl = x.y;
-                        return reinterpret_cast<const float4*>(a.oo + at * D + 4 * col[k]);
+                        return reinterpret_cast<const float4*>(a.oo + at * D + 4 * col);
                     });
                 }
-#pragma unroll
-                for (int k = 0; k < kAt; ++k) {
-                    if (last && a.plen == 0) {
-                        // l == 0: no key (or none with a score above -inf): zeros
-                        const float inv = l[k] == 0.0f ? 0.0f : 1.0f / l[k];
-                        uint2 w;
-                        w.x = l[k] == 0.0f ? 0u : pack2<T>(acc[k].x * inv, acc[k].y * inv);
-                        w.y = l[k] == 0.0f ? 0u : pack2<T>(acc[k].z * inv, acc[k].w * inv);
-                        *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + (orow + r[k]) * D + 4 * col[k]) = w;
-                    } else {   // a part for the item's last CTA, or the row's own part for paged_join_kernel
-                        const int64_t at = last ? orow + r[k] : static_cast<int64_t>(2 * blockIdx.x + (j0 == 0 ? 1 : 0)) * a.rows + r[k];
-                        if (col[k] == 0) *reinterpret_cast<float2*>((last ? a.rml : a.oml) + 2 * at) = make_float2(m[k], l[k]);
-                        *reinterpret_cast<float4*>((last ? a.ro : a.oo) + at * D + 4 * col[k]) = acc[k];
-                    }
+                if (last && a.plen == 0) {
+                    // l == 0: no key (or none with a score above -inf): zeros
+                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                    uint2 w;
+                    w.x = l == 0.0f ? 0u : pack2<T>(acc.x * inv, acc.y * inv);
+                    w.y = l == 0.0f ? 0u : pack2<T>(acc.z * inv, acc.w * inv);
+                    *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + (orow + r) * D + 4 * col) = w;
+                } else {   // a part for the item's last CTA, or the row's own part for paged_join_kernel
+                    const int64_t at = last ? orow + r : static_cast<int64_t>(2 * blockIdx.x + (k.j0 == 0 ? 1 : 0)) * a.rows + r;
+                    // (m, l) of a row goes with the first of its columns that this warp holds: every warp's
+                    // share is read back by the same warp of another CTA
+                    if (col == 0 || lane == 0) *reinterpret_cast<float2*>((last ? a.rml : a.oml) + 2 * at) = make_float2(m, l);
+                    *reinterpret_cast<float4*>((last ? a.ro : a.oo) + at * D + 4 * col) = acc;
                 }
             }
             if (last) return;
             __threadfence();
             __syncwarp();
+            int* count = a.count + c0 * kOwnWarps + warp;
             int arrived = 0;
-            if (lane == 0) arrived = atomicAdd(a.count + c0, 1);
+            if (lane == 0) arrived = atomicAdd(count, 1);
             last = __shfl_sync(0xffffffffu, arrived, 0) == c1 - c0;
             if (!last) return;
             __threadfence();
-            if (lane == 0) a.count[c0] = 0;
+            if (lane == 0) *count = 0;
         }
     };
 
@@ -431,10 +420,10 @@ __global__ void __launch_bounds__(kOwnThreads, 2) paged_own_kernel(
             k.len = slen[k.b];
         }
     };
-    int slot = 0, qs = 0, buf = 0, turn = 0;   // turn: the warp that joins this run's parts
-    uint32_t phase = 0, qphase = 0, buf_phase = 0;
-    bool ok = true, reuse = false;             // reuse: the buffers of parts have been used
-    // Wait for a slot; done() gives it back.
+    int slot = 0, qs = 0, runs = 0;
+    uint32_t phase = 0, qphase = 0;
+    bool ok = true;
+    // Wait for a barrier; done() gives a slot back.
     auto wait_full = [&](uint32_t bar, uint32_t ph) {
         ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar, ph, a.flag));
         return ok;
@@ -446,6 +435,14 @@ __global__ void __launch_bounds__(kOwnThreads, 2) paged_own_kernel(
             slot = 0;
             phase ^= 1u;
         }
+    };
+    // The parts of run r are joined once those of run r + 1 have been written (or at the end): by then all
+    // warps have written them, and nothing is waited for.
+    Run before{};
+    auto join_before = [&] {
+        if (wait_full(parts_full(before.buf), ((runs - 1) >> 1) & 1)) join_run(before);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(parts_free(before.buf));
     };
     // ldmatrix addresses: row and 16-byte column of this lane's matrix row, for Q, K and V (transposed)
     const int qrow = lane & 15, qcol = lane >> 4;
@@ -594,7 +591,8 @@ __global__ void __launch_bounds__(kOwnThreads, 2) paged_own_kernel(
         l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
         l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
         l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-        if (reuse) wait_full(parts_free(buf), buf_phase ^ 1u);
+        const int buf = runs & 1;
+        if (runs >= 2) wait_full(parts_free(buf), ((runs >> 1) - 1) & 1);
         float* omb = om + buf * (kOwnWarps * a.rows * D);
         float* mlb = ml + buf * (kOwnWarps * 32);
         if (ok) {
@@ -610,19 +608,11 @@ __global__ void __launch_bounds__(kOwnThreads, 2) paged_own_kernel(
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(parts_full(buf));
-        // the warps take turns in joining a run's parts; the others go on with the next run meanwhile
-        if (turn == warp) {
-            if (wait_full(parts_full(buf), buf_phase)) join_run(b, hr, j0, j1, n, omb, mlb);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(parts_free(buf));
-        }
-        if (++turn == kOwnWarps) turn = 0;
-        if (++buf == a.nbuf) {
-            buf = 0;
-            buf_phase ^= 1u;
-            reuse = true;
-        }
+        if (runs > 0) join_before();
+        before = Run{b, hr, j0, j1, n, buf};
+        ++runs;
     }
+    join_before();
 }
 
 // With a shared prefix, the last step: a row's own part and the prefix's parts.  One warp per query row, lane c
@@ -1062,19 +1052,15 @@ Sizes sizes(int64_t batch, int64_t hq, int64_t hk, int64_t D, int64_t plen) {
 template <int D>
 int own_smem(PagedArgs* a, uint32_t* bytes, int* ctas) {
     using L = OwnLayout<D>;
-    const uint32_t part = static_cast<uint32_t>(kOwnWarps * a->rows * D * 4), bars = 8u * (2 * kOwnSlots + 2 * kOwnQ + 4);
+    const uint32_t om = static_cast<uint32_t>(2 * kOwnWarps * a->rows * D * 4), ml = 2 * kOwnWarps * 16 * 8;
+    const uint32_t bars = 8u * (2 * kOwnSlots + 2 * kOwnQ + 4);
     const uint32_t pre = static_cast<uint32_t>(2 * a->batch + 1) * 4, q = kOwnQ * L::QSLOT;
-    uint32_t om = 0, ml = 0;
+    const uint32_t fixed = q + om + ml + bars + pre + 1024;
     int n = 0;
-    for (int choice = 0; choice < 3; ++choice) {   // CTAs and buffers of parts: 2, 2; 2, 1; 1, 1
-        *ctas = choice < 2 ? 2 : 1;
-        a->nbuf = choice == 0 ? 2 : 1;
-        om = a->nbuf * part;
-        ml = a->nbuf * kOwnWarps * 16 * 8;
-        const uint32_t fixed = q + om + ml + bars + pre + 1024;
+    for (*ctas = 2;; --*ctas) {
         const uint32_t budget = *ctas == 2 ? 112u * 1024u : static_cast<uint32_t>(kOwnSmem);
         n = fixed < budget ? static_cast<int>((budget - fixed) / L::SLOT) : 0;
-        if (n * L::SLOT >= 64u * 1024u) break;
+        if (n * L::SLOT >= 64u * 1024u || *ctas == 1) break;
     }
     if (n < 1) return FUSE_EUNSUPPORTED;
     a->slots = n < kOwnSlots ? n : kOwnSlots;

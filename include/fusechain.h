@@ -387,7 +387,7 @@ int fuse_rope_append(const void* qkv, int64_t ld, const float* cos_sin, int64_t 
  *   Out of range in device memory (fuse_check() then returns FUSE_EINDEX): a page index outside
  *   [0, num_pages) counts as a page of zeros; a length is taken into 0 .. table_ld page_size.
  *   workspace  device memory of at least fuse_paged_attention_workspace_bytes() bytes, 256-byte
- *          aligned, its first 2048 bytes zero before its first use (every completed call leaves them
+ *          aligned, its first 8192 bytes zero before its first use (every completed call leaves them
  *          so; calls of any sizes may follow one another in it), not shared with a call that may run
  *          at the same time, in a replayed graph or otherwise; it must overlap no operand.  After a
  *          FUSE_ETIMEOUT, zero those bytes again.

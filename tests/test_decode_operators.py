@@ -88,7 +88,7 @@ def test_rope_append_refusals(kw, want):
     (dict(q=A + 8), fc.FUSE_EALIGN),
     (dict(lens=D_ + 2), fc.FUSE_EALIGN),
     (dict(ws=None), fc.FUSE_EWORKSPACE),
-    (dict(ws_bytes=4096), fc.FUSE_EWORKSPACE),
+    (dict(ws_bytes=16384), fc.FUSE_EWORKSPACE),
     (dict(ws=F + 128), fc.FUSE_EALIGN),
     (dict(o=A), fc.FUSE_EINVAL),                 # o overlaps q
     (dict(o=C + 256), fc.FUSE_EINVAL),           # o overlaps the value cache
@@ -141,7 +141,7 @@ def test_ledgers():
 def test_paged_workspace_is_host_arithmetic():
     ws = fc.fuse_paged_attention_workspace_bytes
     # counters, then (m, l) and fp32 output rows of two parts for each of at most 320 CTAs
-    assert ws(1, 32, 8, 128) == 2048 + 640 * 4 * 8 + 640 * 4 * 128 * 4
+    assert ws(1, 32, 8, 128) == 8192 + 640 * 4 * 8 + 640 * 4 * 128 * 4
     assert ws(512, 32, 8, 128) == ws(1, 32, 8, 128)          # independent of the batch
     # with a prefix: every row's own part, and 128-row parts of at most 160 CTAs and one more per row tile
     assert ws(64, 32, 8, 128, 100) == ws(1, 32, 8, 128) + 64 * 32 * (8 + 512) + (160 + 16) * 128 * (16 + 512)

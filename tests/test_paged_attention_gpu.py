@@ -191,12 +191,12 @@ def test_equal_calls_give_equal_bits_in_a_used_workspace(cuda_device):
     small = make([3000], 8, 8, 128, 32, "bf16", seed=12)
     need = max(fc.fuse_paged_attention_workspace_bytes(5, 16, 4, 64, 300), fc.fuse_paged_attention_workspace_bytes(1, 8, 8, 128))
     ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
-    ws[:2048] = 0                                                            # all that has to be zero
+    ws[:8192] = 0                                                            # all that has to be zero
     first, other = run(p, workspace=ws).clone(), run(small, workspace=ws).clone()
     for _ in range(3):
         assert torch.equal(run(p, workspace=ws), first)
         assert torch.equal(run(small, workspace=ws), other)
-        assert not ws[:2048].any()
+        assert not ws[:8192].any()
 
 
 def test_lengths_change_between_replays(cuda_device):
