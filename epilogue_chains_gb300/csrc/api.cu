@@ -191,7 +191,7 @@ bool make_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols, int
 }
 
 bool make_map_3d(CUtensorMap* map, const void* ptr, MapType type, const int64_t (&dims)[3],
-                 const int64_t (&strides)[2], const int (&box)[3], bool swizzle128) {
+                 const int64_t (&strides)[2], const int (&box)[3], int swizzle) {
     auto enc = encode_fn();
     if (!enc) return false;
     cuuint64_t d[3], st[2];
@@ -203,7 +203,7 @@ bool make_map_3d(CUtensorMap* map, const void* ptr, MapType type, const int64_t 
     for (int i = 0; i < 2; ++i) st[i] = static_cast<cuuint64_t>(strides[i]);
     CUresult r = enc(map, type == kMapU8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3,
                      const_cast<void*>(ptr), d, st, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                     swizzle == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : swizzle == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }

@@ -20,6 +20,8 @@
 // distributed shared memory in rank order.
 #include <cudaTypedefs.h>
 
+#include <type_traits>
+
 #include "fc_internal.cuh"
 #include "fc_mma.cuh"
 #include "fc_ptx.cuh"
@@ -320,7 +322,7 @@ int launch_w4(W4Args a, cudaStream_t st) {
         const int wb[3] = {64, ROWS, WK};
         const int64_t xd[3] = {64, a.M, 2 * static_cast<int64_t>(a.nchunk)}, xs[2] = {static_cast<int64_t>(a.K) * 2, 128};
         const int xb[3] = {64, a.M, 2 * WK};
-        if (!make_map_3d(&mW, a.wq, kMapU8, wd, ws, wb, false) || !make_map_3d(&mX, a.x, kMap16, xd, xs, xb, true)) return FUSE_ECUDA;
+        if (!make_map_3d(&mW, a.wq, kMapU8, wd, ws, wb, 0) || !make_map_3d(&mX, a.x, kMap16, xd, xs, xb, 128)) return FUSE_ECUDA;
     }
     a.x_off = WK * ROWS * 64;
     a.stage_bytes = static_cast<uint32_t>((a.x_off + 2 * WK * a.M * 128 + 1023) / 1024 * 1024);
@@ -340,8 +342,375 @@ int launch_w4(W4Args a, cudaStream_t st) {
     return launch_pdl(w4_gemv_kernel<T, G, NT>, dim3(static_cast<unsigned>(row_tiles * a.split)), dim3(kW4Threads), smem, st, a.split, mW, mX, a);
 }
 
+
+// ================================================================== tcgen05 tiles
+// More than a few tokens make the matrix instructions count.  The integers q - z go from registers into
+// tensor memory as the A operand of tcgen05.mma (128 weight rows x 128 k per unit, two 16-bit integers per
+// TMEM column), X is the B operand from shared memory, and every group of k has its own fp32 accumulator
+// in TMEM, which is read out, multiplied by the group's scale and added up in registers.
+//
+// 320 threads: warps 0-7 work (TMEM lane quadrant warp % 4, i.e. 32 weight rows, one per lane; half
+// warp / 4 of a unit's k when unpacking and of the tokens when reading out), warp 8 issues the MMAs, warp 9
+// loads by TMA: weights (64-byte swizzle: the 16-byte reads of 8 consecutive rows are free of bank
+// conflicts), X (128-byte swizzle), and scales and zero points for 16 groups at a time.  A worker unpacks
+// unit u + 1 before it reads out unit u, so the MMAs of a unit run while the next one is unpacked.  Two
+// CTAs share an SM (256 TMEM columns each): A 2 x 64, accumulators 128.  A cluster splits K; its sums meet
+// in distributed shared memory in rank order.
+constexpr int kTileWorkers = 8;
+constexpr int kTileThreads = 32 * (kTileWorkers + 2);
+constexpr int kTileStages = 4;
+constexpr uint32_t kTileCols = 256, kTileD = 128;   // TMEM columns; first accumulator column
+
+template <int NM>
+struct TileLayout {
+    static constexpr uint32_t W = 128 * 64;                          // weights of a stage
+    static constexpr uint32_t X = NM * 128;                          // one 64-k atom of X
+    static constexpr uint32_t STAGE = W + 2 * X;
+    static constexpr uint32_t S = 2 * 128 * 16, Z = 128 * 16;        // scales and zeros of 16 groups
+    static constexpr uint32_t OFF_S = kTileStages * STAGE;
+    static constexpr uint32_t OFF_Z = OFF_S + 2 * S;
+    static constexpr uint32_t OFF_BAR = OFF_Z + 2 * Z;
+    static constexpr int ND = 128 / NM < 4 ? 128 / NM : 4;           // accumulators
+    static constexpr int N_BARS = 2 * kTileStages + 4 + 4 + 2 * ND + 1;
+    static constexpr uint32_t OFF_HOLD = OFF_BAR + N_BARS * 8;
+    static constexpr uint32_t SMEM = OFF_HOLD + 16 + 1024;
+    static_assert(SMEM <= 113 * 1024, "two CTAs per SM");
+    static_assert(NM * 128 * 4 <= kTileStages * STAGE, "the sums of a split fit in the ring");
+};
+
+struct TileArgs {
+    int M, N, KG;
+    int nchunk;        // 128-k chunks, the last one possibly partial
+    int per;           // chunks of a CTA (a multiple of those that 16 groups fill, when split)
+    int split, gelu, zeros;
+    const void *bias, *R;
+    void* y;
+    int* flag;
+};
+
+template <typename T, int G, int NM>
+__global__ void __launch_bounds__(kTileThreads, 2) w4_tile_kernel(
+    const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX,
+    const __grid_constant__ CUtensorMap mS, const __grid_constant__ CUtensorMap mZ,
+    const __grid_constant__ TileArgs a) {
+    using L = TileLayout<NM>;
+    constexpr int NG = 128 / G;          // groups of a unit
+    constexpr int UPB = 16 / NG;         // units of a block of scales
+    constexpr int HT = NM / 2;           // tokens of a worker
+    constexpr int ND = L::ND;
+    pdl_trigger();
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    uint8_t* gbase = smem_raw + (base - smem_addr(smem_raw));
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int rank = a.split > 1 ? static_cast<int>(cluster_rank()) : 0;
+    const int n0 = static_cast<int>(blockIdx.x) / a.split * 128;
+    const int c0 = rank * a.per;
+    const int units = max(0, min(a.per, a.nchunk - c0));
+    const uint32_t bar0 = base + L::OFF_BAR;
+    // A ring of n buffers used for the 0th, 1st, ... time: parity of use i of a buffer is i & 1.
+    auto full = [&](int i) { return bar0 + 8u * i; };
+    auto empty = [&](int i) { return bar0 + 8u * (kTileStages + i); };
+    auto s_full = [&](int i) { return bar0 + 8u * (2 * kTileStages + i); };
+    auto s_empty = [&](int i) { return bar0 + 8u * (2 * kTileStages + 2 + i); };
+    auto a_full = [&](int i) { return bar0 + 8u * (2 * kTileStages + 4 + i); };
+    auto a_empty = [&](int i) { return bar0 + 8u * (2 * kTileStages + 6 + i); };
+    auto d_full = [&](int i) { return bar0 + 8u * (2 * kTileStages + 8 + i); };
+    auto d_empty = [&](int i) { return bar0 + 8u * (2 * kTileStages + 8 + ND + i); };
+    const uint32_t drain = bar0 + 8u * (2 * kTileStages + 8 + 2 * ND);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kTileStages; ++i) {
+            mbar_init(full(i), 1);
+            mbar_init(empty(i), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(s_full(i), 1);
+            mbar_init(s_empty(i), kTileWorkers);
+            mbar_init(a_full(i), kTileWorkers);
+            mbar_init(a_empty(i), 1);
+        }
+        for (int i = 0; i < ND; ++i) {
+            mbar_init(d_full(i), 1);
+            mbar_init(d_empty(i), kTileWorkers);
+        }
+        mbar_init(drain, 1);
+        fence_mbar_init();
+    }
+    if (warp == kTileWorkers) tmem_alloc(base + L::OFF_HOLD, kTileCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + L::OFF_HOLD);
+    pdl_wait();
+
+    float acc[HT];
+#pragma unroll
+    for (int i = 0; i < HT; ++i) acc[i] = 0.0f;
+    if (warp == kTileWorkers + 1) {
+        // ---------------------------------------------------------------- loads
+        if (lane == 0 && units > 0) {
+            prefetch_map(&mW);
+            prefetch_map(&mX);
+            prefetch_map(&mS);
+            if (a.zeros) prefetch_map(&mZ);
+            const uint32_t bytes = L::W + 2u * a.M * 128u;
+            int u = 0, blocks = 0;
+            bool ok = true;
+            for (; u < units; ++u) {
+                const int st = u % kTileStages;
+                if (u % UPB == 0) {
+                    const int sb = blocks & 1;
+                    if (blocks >= 2 && !mbar_wait_bounded(s_empty(sb), ((blocks >> 1) - 1) & 1, a.flag)) {
+                        ok = false;
+                        break;
+                    }
+                    const int g0 = (c0 + u) * NG;
+                    mbar_arrive_expect_tx(s_full(sb), L::S + (a.zeros ? L::Z : 0u));
+                    tma_load_3d(base + L::OFF_S + sb * L::S, &mS, g0, n0, 0, s_full(sb));
+                    tma_load_3d(base + L::OFF_S + sb * L::S + L::S / 2, &mS, g0 + 8, n0, 0, s_full(sb));
+                    if (a.zeros) tma_load_3d(base + L::OFF_Z + sb * L::Z, &mZ, g0, n0, 0, s_full(sb));
+                    ++blocks;
+                }
+                if (u >= kTileStages && !mbar_wait_bounded(empty(st), (u / kTileStages - 1) & 1, a.flag)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t at = base + st * L::STAGE;
+                mbar_arrive_expect_tx(full(st), bytes);
+                tma_load_3d(at, &mW, (c0 + u) * 64, n0, 0, full(st));
+                tma_load_2d(at + L::W, &mX, (c0 + u) * 128, 0, full(st));
+                tma_load_2d(at + L::W + L::X, &mX, (c0 + u) * 128 + 64, 0, full(st));
+            }
+            if (!ok) {   // copies in flight land before the shared memory goes away
+                for (int j = max(0, u - kTileStages); j < u; ++j) (void)mbar_wait_drain(full(j % kTileStages), (j / kTileStages) & 1);
+                for (int j = max(0, blocks - 2); j < blocks; ++j) (void)mbar_wait_drain(s_full(j & 1), (j >> 1) & 1);
+            }
+        }
+        __syncwarp();
+    } else if (warp == kTileWorkers) {
+        // ---------------------------------------------------------------- MMA issue
+        if (lane == 0) {
+            constexpr uint32_t idesc = idesc_f16(128, NM, false, false, std::is_same<T, __nv_bfloat16>::value);
+            bool ok = true, issued = false;
+            int d = 0, dn = 0;     // accumulator, and how often the ring has gone round
+            for (int u = 0; ok && u < units; ++u) {
+                const int st = u % kTileStages, ab = u & 1;
+                ok = mbar_wait_bounded(full(st), (u / kTileStages) & 1, a.flag) && mbar_wait_bounded(a_full(ab), (u >> 1) & 1, a.flag);
+                const uint32_t xb = base + st * L::STAGE + L::W;
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    if (ok && dn > 0) ok = mbar_wait_bounded(d_empty(d), (dn - 1) & 1, a.flag);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < G / 16; ++k) {
+                        const int s = g * (G / 16) + k;
+                        tc_mma_ts(tmem + kTileD + d * NM, tmem + ab * 64 + s * 8,
+                                  smem_desc_sw128(xb + (s / 4) * L::X + (s % 4) * 32, 16, 1024), idesc, k > 0 ? 1u : 0u);
+                    }
+                    tc_commit(d_full(d));
+                    issued = true;
+                    if (++d == ND) {
+                        d = 0;
+                        ++dn;
+                    }
+                }
+                if (ok) {
+                    tc_commit(a_empty(ab));
+                    tc_commit(empty(st));
+                }
+            }
+            if (!ok && issued) {   // MMAs in flight finish before TMEM is freed
+                tc_commit(drain);
+                (void)mbar_wait_drain(drain, 0);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------------------- unpack and read out
+        const int qd = warp % 4, hh = warp / 4, r = 32 * qd + lane;
+        const uint32_t lanes = static_cast<uint32_t>(32 * qd) << 16;
+        bool ok = true;
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity & 1u, a.flag));
+            return ok;
+        };
+        auto arrive = [&](uint32_t bar) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
+        int d = 0, dn = 0;
+        for (int u = 0; u <= units && ok; ++u) {
+            if (u < units) {
+                const int st = u % kTileStages, ab = u & 1, blk = u / UPB, sb = blk & 1;
+                if (u % UPB == 0 && !wait(s_full(sb), blk >> 1)) break;
+                if (!wait(full(st), u / kTileStages)) break;
+                if (u >= 2 && !wait(a_empty(ab), (u >> 1) - 1)) break;
+                tc_fence_after();
+                // this thread's row: 64 k from 64 hh on, two 16-byte pieces of the row's four
+                const uint32_t row = base + st * L::STAGE + r * 64;
+                const uint32_t sw = static_cast<uint32_t>((r >> 1) & 3);
+                const uint4 w0 = lds128(row + (((2u * hh) ^ sw) << 4)), w1 = lds128(row + (((2u * hh + 1u) ^ sw) << 4));
+                const uint32_t words[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+                uint32_t zb[2] = {Nib<T>::MAGIC | 0x00080008u, Nib<T>::MAGIC | 0x00080008u};   // first and second 32 k
+                if (a.zeros) {
+                    const uint8_t* zp = gbase + L::OFF_Z + sb * L::Z + r * 16 + (u % UPB) * NG;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) zb[i] = Nib<T>::MAGIC | (zp[(64 * hh + 32 * i) / G] & 15u) * 0x00010001u;
+                }
+                float p[32];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    uint32_t q[4];
+                    unpack_word<T>(words[i], zb[i / 4], q);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) p[4 * i + e] = __uint_as_float(q[e]);
+                }
+                tmem_st32(tmem + lanes + ab * 64 + 32 * hh, p);
+                tmem_st_wait();
+                tc_fence_before();
+                arrive(a_full(ab));
+            }
+            if (u > 0) {
+                const int v = u - 1, blk = v / UPB, sb = blk & 1;
+                const uint8_t* sp = gbase + L::OFF_S + sb * L::S + r * 16;
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    if (!wait(d_full(d), dn)) break;
+                    tc_fence_after();
+                    float x[HT];
+                    const uint32_t at = tmem + lanes + kTileD + d * NM + HT * hh;
+                    if constexpr (HT == 32) tmem_ld32(at, x);
+                    else if constexpr (HT == 16) tmem_ld16(at, x);
+                    else tmem_ld8(at, x);
+                    const int gb = (v % UPB) * NG + g;      // group of the block
+                    const float s = to_f32(*reinterpret_cast<const T*>(sp + (gb / 8) * (L::S / 2) + (gb % 8) * 2));
+                    tmem_ld_wait();
+                    tc_fence_before();
+                    arrive(d_empty(d));
+#pragma unroll
+                    for (int i = 0; i < HT; i += 2) {
+                        const float2 t = __ffma2_rn(make_float2(s, s), make_float2(x[i], x[i + 1]), make_float2(acc[i], acc[i + 1]));
+                        acc[i] = t.x;
+                        acc[i + 1] = t.y;
+                    }
+                    if (++d == ND) {
+                        d = 0;
+                        ++dn;
+                    }
+                }
+                if (ok && (v % UPB == UPB - 1 || v == units - 1)) arrive(s_empty(sb));
+            }
+        }
+    }
+
+    // epilogue: thread (row r, tokens HT hh ..) of the workers; a split's sums in rank order
+    const T* bias = static_cast<const T*>(a.bias);
+    const T* R = static_cast<const T*>(a.R);
+    T* y = static_cast<T*>(a.y);
+    auto finish = [&](float v, float b, int m, int n) {
+        v += b;
+        if (a.gelu) v = gelu_erf(v);
+        const int64_t at = static_cast<int64_t>(m) * a.N + n;
+        if (R) v += to_f32(R[at]);
+        y[at] = from_f32<T>(v);
+    };
+    tc_fence_before();
+    __syncthreads();      // every load has landed and every MMA is done: TMEM and the ring are free
+    if (warp == kTileWorkers) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTileCols);
+    }
+    const int r = 32 * (warp % 4) + lane, t0 = HT * (warp / 4);
+    if (a.split == 1) {
+        const int n = n0 + r;
+        if (warp < kTileWorkers && n < a.N) {
+            const float b = bias ? to_f32(bias[n]) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < HT; ++i)
+                if (t0 + i < a.M) finish(acc[i], b, t0 + i, n);
+        }
+        return;
+    }
+    float* red = reinterpret_cast<float*>(gbase);   // [token][128]
+    if (warp < kTileWorkers) {
+#pragma unroll
+        for (int i = 0; i < HT; ++i) red[(t0 + i) * 128 + r] = acc[i];
+    }
+    __syncwarp();
+    cluster_sync();
+    for (int i = rank * kTileThreads + threadIdx.x; i < a.M * 128; i += a.split * kTileThreads) {
+        const int n = n0 + i % 128;
+        if (n >= a.N) continue;
+        const uint32_t at = smem_addr(red + i);
+        float v = 0.0f;
+        for (int c = 0; c < a.split; ++c) {
+            float p;
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(p) : "r"(mapa_shared(at, c)) : "memory");
+            v += p;
+        }
+        finish(v, bias ? to_f32(bias[n]) : 0.0f, i / 128, n);
+    }
+    __syncwarp();
+    cluster_sync();   // the sums stay in place until every CTA has read them
+}
+
+// Whether the tile kernel can load the scales (and zero points): whole 16-byte pieces of a row.
+bool tile_fits(const W4Args& a, int group) {
+    const int kg = a.K / group;
+    return kg % 8 == 0 && is_aligned(a.s, 16) && (!a.z || (kg % 16 == 0 && is_aligned(a.z, 16)));
+}
+
+template <typename T, int G, int NM>
+int launch_tile(const W4Args& w, cudaStream_t st) {
+    using L = TileLayout<NM>;
+    constexpr int UPB = 16 * G / 128;
+    TileArgs a{};
+    a.M = w.M;
+    a.N = w.N;
+    a.KG = w.K / G;
+    a.nchunk = static_cast<int>(ceil_div(w.K, 128));
+    a.gelu = w.gelu;
+    a.zeros = w.z ? 1 : 0;
+    a.bias = w.bias;
+    a.R = w.R;
+    a.y = w.y;
+    a.flag = w.flag;
+    const int tiles = static_cast<int>(ceil_div(w.N, 128)), sms = sm_count();
+    // A CTA's chunks, times how often the SMs go round: the least, and of equal splits the smallest
+    int64_t best = INT64_MAX;
+    for (int s = 1; s <= 8; s *= 2) {
+        int64_t per = ceil_div(a.nchunk, s);
+        if (s > 1) per = ceil_div(per, UPB) * UPB;      // blocks of scales start with a CTA
+        const int64_t cost = ceil_div(static_cast<int64_t>(tiles) * s, sms) * (per + 2);
+        if (cost < best) {
+            best = cost;
+            a.split = s;
+            a.per = static_cast<int>(per);
+        }
+    }
+    CUtensorMap mW{}, mX{}, mS{}, mZ{};
+    const int64_t wd[3] = {w.K / 2, w.N, 1}, ws[2] = {w.K / 2, static_cast<int64_t>(w.K / 2) * w.N};
+    const int wb[3] = {64, 128, 1};
+    const int64_t sd[3] = {a.KG, w.N, 1}, ss[2] = {static_cast<int64_t>(a.KG) * 2, static_cast<int64_t>(a.KG) * 2 * w.N};
+    const int sbx[3] = {8, 128, 1};
+    const int64_t zd[3] = {a.KG, w.N, 1}, zs[2] = {a.KG, static_cast<int64_t>(a.KG) * w.N};
+    const int zbx[3] = {16, 128, 1};
+    if (!make_map_3d(&mW, w.wq, kMapU8, wd, ws, wb, 64) || !make_map(&mX, w.x, w.M, w.K, 64, w.M, std::is_same<T, __nv_bfloat16>::value) ||
+        !make_map_3d(&mS, w.s, kMap16, sd, ss, sbx, 0) || (w.z && !make_map_3d(&mZ, w.z, kMapU8, zd, zs, zbx, 0)))
+        return FUSE_ECUDA;
+    const int rc = opt_in_smem((const void*)w4_tile_kernel<T, G, NM>, L::SMEM, true);
+    if (rc != FUSE_OK) return rc;
+    return launch_pdl(w4_tile_kernel<T, G, NM>, dim3(static_cast<unsigned>(tiles * a.split)), dim3(kTileThreads), L::SMEM, st, a.split, mW, mX, mS, mZ, a);
+}
+
 template <typename T, int G>
 int run_w4_g(const W4Args& a, cudaStream_t st) {
+    if (a.M > 8 && tile_fits(a, G)) {
+        if (a.M <= 16) return launch_tile<T, G, 16>(a, st);
+        if (a.M <= 32) return launch_tile<T, G, 32>(a, st);
+        return launch_tile<T, G, 64>(a, st);
+    }
     if (a.M <= 8) return launch_w4<T, G, 1>(a, st);
     if (a.M <= 16) return launch_w4<T, G, 2>(a, st);
     if (a.M <= 32) return launch_w4<T, G, 4>(a, st);
