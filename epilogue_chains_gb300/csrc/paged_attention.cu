@@ -730,7 +730,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix_kernel(const __gr
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
     uint8_t* gbase = smem_raw + (base - smem_addr(smem_raw));
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     constexpr int KV = L::KV;
     const uint32_t bar0 = base + L::OFF_BAR;
     // A ring of n buffers used by tiles i = 0, 1, ... of this CTA: buffer i % n, parity (i / n) & 1.
@@ -764,7 +764,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix_kernel(const __gr
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + L::OFF_HOLD);
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(gbase + L::OFF_HOLD), 0);
     pdl_wait();
 
     const int64_t U = static_cast<int64_t>(a.hk) * a.prt * a.ptiles;
@@ -809,56 +809,58 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix_kernel(const __gr
         __syncwarp();
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issue
-        if (lane == 0) {
-            constexpr uint32_t idS = idesc_f16(128, 128, false, false, BF);
-            constexpr uint32_t idO = idesc_f16(128, D, false, true, BF);
-            bool issued = false, ok = true;
-            auto issue_s = [&](int i) -> bool {
-                const int st = i % KV, sb = i & 1;
-                if (!mbar_wait_bounded(k_full(st), (i / KV) & 1, flag)) return false;
-                if (i >= 2 && !mbar_wait_bounded(s_free(sb), ((i - 2) / 2) & 1, flag)) return false;
-                tc_fence_after();
-                const uint32_t kb = base + L::OFF_K + st * L::TILE;
+        constexpr uint32_t idS = idesc_f16(128, 128, false, false, BF);
+        constexpr uint32_t idO = idesc_f16(128, D, false, true, BF);
+        const uint32_t one = elect_one();
+        const uint64_t dq = smem_desc_sw128(base + L::OFF_Q, 16, 1024), dk = smem_desc_sw128(base + L::OFF_K, 16, 1024);
+        const uint64_t dp = smem_desc_sw128(base + L::OFF_P, 16, 1024), dv = smem_desc_sw128(base + L::OFF_V, L::REGION, 1024);
+        bool issued = false, ok = true;
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity & 1u, flag));
+            return ok;
+        };
+        auto issue_s = [&](int i) {
+            const int st = i % KV, sb = i & 1;
+            if (!wait(k_full(st), i / KV)) return;
+            if (i >= 2 && !wait(s_free(sb), (i >> 1) - 1)) return;
+            tc_fence_after();
+            const uint64_t kd = dk + static_cast<uint64_t>(st * (L::TILE >> 4));
 #pragma unroll
-                for (int s = 0; s < D / 16; ++s)
-                    tc_mma(tmem + sb * 128, smem_desc_sw128(base + L::OFF_Q + (s / 4) * L::REGION + (s % 4) * 32, 16, 1024),
-                           smem_desc_sw128(kb + (s / 4) * L::REGION + (s % 4) * 32, 16, 1024), idS, s > 0 ? 1u : 0u);
-                tc_commit(s_full(sb));
-                tc_commit(k_empty(st));
-                issued = true;
-                return true;
-            };
-            auto issue_pv = [&](int i, bool first) -> bool {
-                const int st = i % KV;
-                if (!mbar_wait_bounded(p_full, i & 1, flag)) return false;
-                if (!mbar_wait_bounded(v_full(st), (i / KV) & 1, flag)) return false;
-                tc_fence_after();
-                const uint32_t vb = base + L::OFF_V + st * L::TILE;
+            for (int s = 0; s < D / 16; ++s)
+                tc_mma_if(one, tmem + sb * 128, dq + ((s / 4) * (L::REGION >> 4) + (s % 4) * 2), kd + ((s / 4) * (L::REGION >> 4) + (s % 4) * 2),
+                          idS, s > 0 ? 1u : 0u);
+            tc_commit_if(one, s_full(sb));
+            tc_commit_if(one, k_empty(st));
+            issued = true;
+        };
+        auto issue_pv = [&](int i, bool first) {
+            const int st = i % KV;
+            if (!wait(p_full, i) || !wait(v_full(st), i / KV)) return;
+            tc_fence_after();
+            const uint64_t vd = dv + static_cast<uint64_t>(st * (L::TILE >> 4));
 #pragma unroll
-                for (int s = 0; s < 8; ++s)   // 16 keys each: P atom s / 4; V rows 16 s ..
-                    tc_mma(tmem + L::O_COL, smem_desc_sw128(base + L::OFF_P + (s / 4) * L::REGION + (s % 4) * 32, 16, 1024),
-                           smem_desc_sw128(vb + s * 2048, L::REGION, 1024), idO, !first || s > 0 ? 1u : 0u);
-                tc_commit(o_done);
-                tc_commit(v_empty(st));
-                issued = true;
-                return true;
-            };
-            int i = 0, seg = 0;
-            for (int64_t u = u0; ok && u < u1; ++seg) {
-                const int n = static_cast<int>(min(static_cast<int64_t>(a.ptiles) - u % a.ptiles, u1 - u));
-                ok = mbar_wait_bounded(q_full, seg & 1, flag);
-                if (ok) ok = issue_s(i);
-                for (int j = 0; ok && j < n; ++j) {
-                    if (j + 1 < n) ok = issue_s(i + j + 1);
-                    if (ok) ok = issue_pv(i + j, j == 0);
-                }
-                i += n;
-                u += n;
+            for (int s = 0; s < 8; ++s)   // 16 keys each: P atom s / 4; V rows 16 s ..
+                tc_mma_if(one, tmem + L::O_COL, dp + ((s / 4) * (L::REGION >> 4) + (s % 4) * 2), vd + s * (2048 >> 4), idO,
+                          !first || s > 0 ? 1u : 0u);
+            tc_commit_if(one, o_done);
+            tc_commit_if(one, v_empty(st));
+            issued = true;
+        };
+        int i = 0, seg = 0;
+        for (int64_t u = u0; ok && u < u1; ++seg) {
+            const int n = static_cast<int>(min(static_cast<int64_t>(a.ptiles) - u % a.ptiles, u1 - u));
+            if (!wait(q_full, seg)) break;
+            issue_s(i);
+            for (int j = 0; ok && j < n; ++j) {
+                if (j + 1 < n) issue_s(i + j + 1);
+                if (ok) issue_pv(i + j, j == 0);
             }
-            if (!ok && issued) {   // MMAs in flight finish before TMEM is freed
-                tc_commit(drain);
-                (void)mbar_wait_drain(drain, 0);
-            }
+            i += n;
+            u += n;
+        }
+        if (!ok && issued) {   // MMAs in flight finish before TMEM is freed
+            tc_commit_if(one, drain);
+            (void)mbar_wait_drain(drain, 0);
         }
         __syncwarp();
     } else {

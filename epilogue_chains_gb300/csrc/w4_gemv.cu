@@ -370,8 +370,7 @@ struct TileLayout {
     static constexpr uint32_t OFF_S = kTileStages * STAGE;
     static constexpr uint32_t OFF_Z = OFF_S + 2 * S;
     static constexpr uint32_t OFF_BAR = OFF_Z + 2 * Z;
-    static constexpr int ND = 128 / NM < 4 ? 128 / NM : 4;           // accumulators
-    static constexpr int N_BARS = 2 * kTileStages + 4 + 4 + 2 * ND + 1;
+    static constexpr int N_BARS = 2 * kTileStages + 4 + 2 + 4 + 1;
     static constexpr uint32_t OFF_HOLD = OFF_BAR + N_BARS * 8;
     static constexpr uint32_t SMEM = OFF_HOLD + 16 + 1024;
     static_assert(SMEM <= 113 * 1024, "two CTAs per SM");
@@ -383,6 +382,7 @@ struct TileArgs {
     int nchunk;        // 128-k chunks, the last one possibly partial
     int per;           // chunks of a CTA (a multiple of those that 16 groups fill, when split)
     int split, gelu, zeros;
+    int y_vec;         // y is 8-byte aligned
     const void *bias, *R;
     void* y;
     int* flag;
@@ -397,12 +397,16 @@ __global__ void __launch_bounds__(kTileThreads, 2) w4_tile_kernel(
     constexpr int NG = 128 / G;          // groups of a unit
     constexpr int UPB = 16 / NG;         // units of a block of scales
     constexpr int HT = NM / 2;           // tokens of a worker
-    constexpr int ND = L::ND;
+    // The accumulators of a unit's groups form one set (two, one after the other, where a unit has more
+    // groups than there are columns for); as many sets as fit, at most two.
+    constexpr int SG = NG * NM <= 128 ? NG : 128 / NM;   // groups of a set
+    constexpr int SETS = NG / SG;                        // sets of a unit
+    constexpr int ND = 2 * SG * NM <= 128 ? 2 : 1;       // set buffers
     pdl_trigger();
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
     uint8_t* gbase = smem_raw + (base - smem_addr(smem_raw));
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const int rank = a.split > 1 ? static_cast<int>(cluster_rank()) : 0;
     const int n0 = static_cast<int>(blockIdx.x) / a.split * 128;
     const int c0 = rank * a.per;
@@ -414,10 +418,9 @@ __global__ void __launch_bounds__(kTileThreads, 2) w4_tile_kernel(
     auto s_full = [&](int i) { return bar0 + 8u * (2 * kTileStages + i); };
     auto s_empty = [&](int i) { return bar0 + 8u * (2 * kTileStages + 2 + i); };
     auto a_full = [&](int i) { return bar0 + 8u * (2 * kTileStages + 4 + i); };
-    auto a_empty = [&](int i) { return bar0 + 8u * (2 * kTileStages + 6 + i); };
-    auto d_full = [&](int i) { return bar0 + 8u * (2 * kTileStages + 8 + i); };
-    auto d_empty = [&](int i) { return bar0 + 8u * (2 * kTileStages + 8 + ND + i); };
-    const uint32_t drain = bar0 + 8u * (2 * kTileStages + 8 + 2 * ND);
+    auto d_full = [&](int i) { return bar0 + 8u * (2 * kTileStages + 6 + i); };
+    auto d_empty = [&](int i) { return bar0 + 8u * (2 * kTileStages + 8 + i); };
+    const uint32_t drain = bar0 + 8u * (2 * kTileStages + 10);
     if (threadIdx.x == 0) {
         for (int i = 0; i < kTileStages; ++i) {
             mbar_init(full(i), 1);
@@ -427,9 +430,6 @@ __global__ void __launch_bounds__(kTileThreads, 2) w4_tile_kernel(
             mbar_init(s_full(i), 1);
             mbar_init(s_empty(i), kTileWorkers);
             mbar_init(a_full(i), kTileWorkers);
-            mbar_init(a_empty(i), 1);
-        }
-        for (int i = 0; i < ND; ++i) {
             mbar_init(d_full(i), 1);
             mbar_init(d_empty(i), kTileWorkers);
         }
@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) w4_tile_kernel(
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + L::OFF_HOLD);
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(gbase + L::OFF_HOLD), 0);
     pdl_wait();
 
     float acc[HT];
@@ -489,41 +489,52 @@ __global__ void __launch_bounds__(kTileThreads, 2) w4_tile_kernel(
         __syncwarp();
     } else if (warp == kTileWorkers) {
         // ---------------------------------------------------------------- MMA issue
-        if (lane == 0) {
-            constexpr uint32_t idesc = idesc_f16(128, NM, false, false, std::is_same<T, __nv_bfloat16>::value);
-            bool ok = true, issued = false;
-            int d = 0, dn = 0;     // accumulator, and how often the ring has gone round
-            for (int u = 0; ok && u < units; ++u) {
-                const int st = u % kTileStages, ab = u & 1;
-                ok = mbar_wait_bounded(full(st), (u / kTileStages) & 1, a.flag) && mbar_wait_bounded(a_full(ab), (u >> 1) & 1, a.flag);
-                const uint32_t xb = base + st * L::STAGE + L::W;
+        constexpr uint32_t idesc = idesc_f16(128, NM, false, false, std::is_same<T, __nv_bfloat16>::value);
+        const uint32_t one = elect_one();
+        const uint64_t desc0 = smem_desc_sw128(base + L::W, 16, 1024);
+        bool ok = true, issued = false;
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, a.flag));
+            return ok;
+        };
+        int st = 0, d = 0;
+        uint32_t st_par = 0, a_par = 0, d_par = 1;   // parities of the next waits; d_empty needs none at first
+        bool d_again = false;
+        for (int u = 0; ok && u < units; ++u) {
+            const int ab = u & 1;
+            if (!wait(a_full(ab), a_par) || !wait(full(st), st_par)) break;
+            const uint64_t xd = desc0 + static_cast<uint64_t>(st * (L::STAGE >> 4));
+            const uint32_t at = tmem + ab * 64;
 #pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    if (ok && dn > 0) ok = mbar_wait_bounded(d_empty(d), (dn - 1) & 1, a.flag);
-                    if (!ok) break;
-                    tc_fence_after();
+            for (int h = 0; h < SETS; ++h) {
+                if (d_again && !wait(d_empty(d), d_par)) break;
+                tc_fence_after();
+                const uint32_t dt = tmem + kTileD + d * (SG * NM);
+#pragma unroll
+                for (int g = 0; g < SG; ++g)
 #pragma unroll
                     for (int k = 0; k < G / 16; ++k) {
-                        const int s = g * (G / 16) + k;
-                        tc_mma_ts(tmem + kTileD + d * NM, tmem + ab * 64 + s * 8,
-                                  smem_desc_sw128(xb + (s / 4) * L::X + (s % 4) * 32, 16, 1024), idesc, k > 0 ? 1u : 0u);
+                        const int s = (h * SG + g) * (G / 16) + k;
+                        tc_mma_ts_if(one, dt + g * NM, at + s * 8, xd + ((s / 4) * (L::X >> 4) + (s % 4) * 2), idesc, k > 0 ? 1u : 0u);
                     }
-                    tc_commit(d_full(d));
-                    issued = true;
-                    if (++d == ND) {
-                        d = 0;
-                        ++dn;
-                    }
-                }
-                if (ok) {
-                    tc_commit(a_empty(ab));
-                    tc_commit(empty(st));
+                tc_commit_if(one, d_full(d));
+                issued = true;
+                if (++d == ND) {
+                    d = 0;
+                    d_par ^= 1u;
+                    d_again = true;
                 }
             }
-            if (!ok && issued) {   // MMAs in flight finish before TMEM is freed
-                tc_commit(drain);
-                (void)mbar_wait_drain(drain, 0);
+            if (ok) tc_commit_if(one, empty(st));
+            a_par ^= static_cast<uint32_t>(ab);
+            if (++st == kTileStages) {
+                st = 0;
+                st_par ^= 1u;
             }
+        }
+        if (!ok && issued) {   // MMAs in flight finish before TMEM is freed
+            tc_commit_if(one, drain);
+            (void)mbar_wait_drain(drain, 0);
         }
         __syncwarp();
     } else {
@@ -539,14 +550,14 @@ __global__ void __launch_bounds__(kTileThreads, 2) w4_tile_kernel(
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
-        int d = 0, dn = 0;
+        int d = 0, st = 0;
+        uint32_t d_par = 0, st_par = 0;
         for (int u = 0; u <= units && ok; ++u) {
             if (u < units) {
-                const int st = u % kTileStages, ab = u & 1, blk = u / UPB, sb = blk & 1;
+                const int ab = u & 1, blk = u / UPB, sb = blk & 1;
                 if (u % UPB == 0 && !wait(s_full(sb), blk >> 1)) break;
-                if (!wait(full(st), u / kTileStages)) break;
-                if (u >= 2 && !wait(a_empty(ab), (u >> 1) - 1)) break;
-                tc_fence_after();
+                if (!wait(full(st), st_par)) break;
+                // A buffer ab is free: the accumulators of unit u - 2 have been waited for
                 // this thread's row: 64 k from 64 hh on, two 16-byte pieces of the row's four
                 const uint32_t row = base + st * L::STAGE + r * 64;
                 const uint32_t sw = static_cast<uint32_t>((r >> 1) & 3);
@@ -570,33 +581,40 @@ __global__ void __launch_bounds__(kTileThreads, 2) w4_tile_kernel(
                 tmem_st_wait();
                 tc_fence_before();
                 arrive(a_full(ab));
+                if (++st == kTileStages) {
+                    st = 0;
+                    st_par ^= 1u;
+                }
             }
             if (u > 0) {
                 const int v = u - 1, blk = v / UPB, sb = blk & 1;
                 const uint8_t* sp = gbase + L::OFF_S + sb * L::S + r * 16;
 #pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    if (!wait(d_full(d), dn)) break;
+                for (int h = 0; h < SETS; ++h) {
+                    if (!wait(d_full(d), d_par)) break;
                     tc_fence_after();
-                    float x[HT];
-                    const uint32_t at = tmem + lanes + kTileD + d * NM + HT * hh;
-                    if constexpr (HT == 32) tmem_ld32(at, x);
-                    else if constexpr (HT == 16) tmem_ld16(at, x);
-                    else tmem_ld8(at, x);
-                    const int gb = (v % UPB) * NG + g;      // group of the block
-                    const float s = to_f32(*reinterpret_cast<const T*>(sp + (gb / 8) * (L::S / 2) + (gb % 8) * 2));
-                    tmem_ld_wait();
+#pragma unroll
+                    for (int g = 0; g < SG; ++g) {
+                        float x[HT];
+                        const uint32_t at = tmem + lanes + kTileD + (d * SG + g) * NM + HT * hh;
+                        if constexpr (HT == 32) tmem_ld32(at, x);
+                        else if constexpr (HT == 16) tmem_ld16(at, x);
+                        else tmem_ld8(at, x);
+                        const int gb = (v % UPB) * NG + h * SG + g;      // group of the block
+                        const float s = to_f32(*reinterpret_cast<const T*>(sp + (gb / 8) * (L::S / 2) + (gb % 8) * 2));
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < HT; i += 2) {
+                            const float2 t = __ffma2_rn(make_float2(s, s), make_float2(x[i], x[i + 1]), make_float2(acc[i], acc[i + 1]));
+                            acc[i] = t.x;
+                            acc[i + 1] = t.y;
+                        }
+                    }
                     tc_fence_before();
                     arrive(d_empty(d));
-#pragma unroll
-                    for (int i = 0; i < HT; i += 2) {
-                        const float2 t = __ffma2_rn(make_float2(s, s), make_float2(x[i], x[i + 1]), make_float2(acc[i], acc[i + 1]));
-                        acc[i] = t.x;
-                        acc[i + 1] = t.y;
-                    }
                     if (++d == ND) {
                         d = 0;
-                        ++dn;
+                        d_par ^= 1u;
                     }
                 }
                 if (ok && (v % UPB == UPB - 1 || v == units - 1)) arrive(s_empty(sb));
@@ -608,13 +626,6 @@ __global__ void __launch_bounds__(kTileThreads, 2) w4_tile_kernel(
     const T* bias = static_cast<const T*>(a.bias);
     const T* R = static_cast<const T*>(a.R);
     T* y = static_cast<T*>(a.y);
-    auto finish = [&](float v, float b, int m, int n) {
-        v += b;
-        if (a.gelu) v = gelu_erf(v);
-        const int64_t at = static_cast<int64_t>(m) * a.N + n;
-        if (R) v += to_f32(R[at]);
-        y[at] = from_f32<T>(v);
-    };
     tc_fence_before();
     __syncthreads();      // every load has landed and every MMA is done: TMEM and the ring are free
     if (warp == kTileWorkers) {
@@ -626,9 +637,17 @@ __global__ void __launch_bounds__(kTileThreads, 2) w4_tile_kernel(
         const int n = n0 + r;
         if (warp < kTileWorkers && n < a.N) {
             const float b = bias ? to_f32(bias[n]) : 0.0f;
+            float res[HT];        // all of them on their way before the first store
 #pragma unroll
             for (int i = 0; i < HT; ++i)
-                if (t0 + i < a.M) finish(acc[i], b, t0 + i, n);
+                res[i] = R && t0 + i < a.M ? to_f32(R[static_cast<int64_t>(t0 + i) * a.N + n]) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < HT; i += 2) {
+                float2 v = make_float2(acc[i] + b, acc[i + 1] + b);
+                if (a.gelu) v = gelu_erf2(v);
+                if (t0 + i < a.M) y[static_cast<int64_t>(t0 + i) * a.N + n] = from_f32<T>(v.x + res[i]);
+                if (t0 + i + 1 < a.M) y[static_cast<int64_t>(t0 + i + 1) * a.N + n] = from_f32<T>(v.y + res[i + 1]);
+            }
         }
         return;
     }
@@ -639,17 +658,61 @@ __global__ void __launch_bounds__(kTileThreads, 2) w4_tile_kernel(
     }
     __syncwarp();
     cluster_sync();
-    for (int i = rank * kTileThreads + threadIdx.x; i < a.M * 128; i += a.split * kTileThreads) {
-        const int n = n0 + i % 128;
-        if (n >= a.N) continue;
-        const uint32_t at = smem_addr(red + i);
-        float v = 0.0f;
-        for (int c = 0; c < a.split; ++c) {
-            float p;
-            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(p) : "r"(mapa_shared(at, c)) : "memory");
-            v += p;
+    // four rows of one token at a time, two such pieces per thread with their loads together
+    const int pieces = a.M * 32;
+    for (int i0 = rank * kTileThreads + threadIdx.x; i0 < pieces; i0 += 2 * a.split * kTileThreads) {
+        float v[2][4], b[2][4], res[2][4];
+        int m[2], n[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int i = min(i0 + j * a.split * kTileThreads, pieces - 1);   // past the end: not stored
+            m[j] = i / 32;
+            n[j] = n0 + i % 32 * 4;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[j][e] = 0.0f;
+                b[j][e] = bias && n[j] + e < a.N ? to_f32(bias[n[j] + e]) : 0.0f;
+                res[j][e] = R && n[j] + e < a.N ? to_f32(R[static_cast<int64_t>(m[j]) * a.N + n[j] + e]) : 0.0f;
+            }
         }
-        finish(v, bias ? to_f32(bias[n]) : 0.0f, i / 128, n);
+        for (int c = 0; c < a.split; c += 2) {      // split is 2, 4 or 8
+            float p[2][2][4];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const uint32_t at = mapa_shared(smem_addr(red + m[j] * 128 + (n[j] - n0)), c + k);
+                    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                                 : "=f"(p[k][j][0]), "=f"(p[k][j][1]), "=f"(p[k][j][2]), "=f"(p[k][j][3]) : "r"(at) : "memory");
+                }
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[j][e] += p[k][j][e];
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (i0 + j * a.split * kTileThreads >= pieces) break;
+            float o[4];
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+                float2 x = make_float2(v[j][e] + b[j][e], v[j][e + 1] + b[j][e + 1]);
+                if (a.gelu) x = gelu_erf2(x);
+                o[e] = x.x + res[j][e];
+                o[e + 1] = x.y + res[j][e + 1];
+            }
+            T* dst = y + static_cast<int64_t>(m[j]) * a.N + n[j];
+            if (n[j] >= a.N) continue;
+            if (a.N % 4 == 0 && a.y_vec) {
+                *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<T>(o[0], o[1]), pack2<T>(o[2], o[3]));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (n[j] + e < a.N) dst[e] = from_f32<T>(o[e]);
+            }
+        }
     }
     __syncwarp();
     cluster_sync();   // the sums stay in place until every CTA has read them
@@ -672,6 +735,7 @@ int launch_tile(const W4Args& w, cudaStream_t st) {
     a.nchunk = static_cast<int>(ceil_div(w.K, 128));
     a.gelu = w.gelu;
     a.zeros = w.z ? 1 : 0;
+    a.y_vec = is_aligned(w.y, 8) ? 1 : 0;
     a.bias = w.bias;
     a.R = w.R;
     a.y = w.y;
