@@ -10,16 +10,20 @@
 // Layout: no repacking.  The order of k within a matrix instruction is free as long as both operands
 // agree, so lane 4 g + t takes consecutive k of its rows: one 128-k chunk gives it four 32-bit words of
 // row g and of row g + 8 (eight k each), from one 16-byte, two 8-byte or four 4-byte pieces for groups
-// of 128, 64 and 32, such that the four lanes of a row always work on the same group.
+// of 128, 64 and 32, such that the four lanes of a row always work on the same group.  A warp takes two such
+// chunks at a time: a row's 128 bytes, one request of the copy engine, and half as much of the loop's own
+// work per weight.
 //
-// A CTA of eight computing warps covers 16 WR rows and 128 WK inputs per stage (WR WK = 8): few tokens
+// A CTA of eight computing warps covers 16 WR rows and 256 WK inputs per stage (WR WK = 8): few tokens
 // put the warps along K, which keeps the row tiles small and the grid large; many put them along N,
 // which keeps the number of times that X is read from L2 down.  One producing thread fills a ring of
-// stages by TMA (weights [WK][16 WR][64 B] and X [2 WK][M][64 elements, 128-byte swizzle], two copies
-// per stage).  Where the row tiles alone leave SMs idle, a cluster splits K and sums through
-// distributed shared memory in rank order.
+// stages by TMA (weights [WK][16 WR][128 B] and X [4 WK][M][64 elements], 128-byte swizzle, two copies
+// per stage); a CTA stays for several row tiles, so that the ring runs on while a tile is finished.
+// Where the row tiles alone leave SMs idle, a cluster splits K and sums through distributed shared
+// memory in rank order.
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "fc_internal.cuh"
@@ -34,14 +38,16 @@ namespace {
 constexpr int kW4Warps = 8;
 constexpr int kW4Threads = 32 * (kW4Warps + 1);   // warp 8 produces
 constexpr int kW4MaxStages = 8;
-constexpr int kAhead = 4;                         // stages that scales are loaded ahead
+constexpr int kW4Smem = 200 * 1024;               // most dynamic shared memory of a CTA
 
 struct W4Args {
     int M, N, K;
-    int nchunk;        // whole 128-k chunks
+    int nchunk;        // whole 256-k chunks
     int split;         // CTAs of a cluster along K
+    int tiles;         // row tiles
     int stages;
-    uint32_t x_off;    // offset of X within a stage
+    int x_resident;    // X is loaded once per CTA, not with every stage
+    uint32_t x_off;    // offset of X within a stage, or of the resident X
     uint32_t stage_bytes;
     uint32_t off_bar, off_red;
     int gelu;
@@ -72,40 +78,47 @@ __device__ __forceinline__ void unpack_word(uint32_t w, uint32_t zb, uint32_t (&
     const uint32_t h = w >> 4;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t v = (__byte_perm(w, h, (i << 0) | (i << 4) | ((4 + i) << 8) | ((4 + i) << 12)) & 0x000F000Fu) | Nib<T>::MAGIC;
+        uint32_t v = __byte_perm(w, h, (i << 0) | (i << 4) | ((4 + i) << 8) | ((4 + i) << 12));
+        asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(v), "r"(0x000F000Fu), "r"(Nib<T>::MAGIC));   // (v & mask) | magic
         p[i] = Nib<T>::sub(v, zb);
     }
 }
 
+// Synchronize the computing warps (the loading warp goes on).
+__device__ __forceinline__ void sync_compute() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kW4Warps) : "memory"); }
+
 template <typename T, int G, int NT>
-__global__ void __launch_bounds__(kW4Threads) w4_gemv_kernel(const __grid_constant__ CUtensorMap mW,
-                                                             const __grid_constant__ CUtensorMap mX,
-                                                             const __grid_constant__ W4Args a) {
+__global__ void __launch_bounds__(kW4Threads, NT <= 2 ? 3 : 1) w4_gemv_kernel(const __grid_constant__ CUtensorMap mW,
+                                                                                           const __grid_constant__ CUtensorMap mX,
+                                                                                           const __grid_constant__ W4Args a) {
     constexpr int WR = NT, WK = kW4Warps / NT;
-    constexpr int ROWS = 16 * WR, COLS = 8 * NT;
+    constexpr int ROWS = 16 * WR, COLS = 8 * NT, PITCH = ROWS + 4;
     constexpr int WPG = G / 32;         // words of a lane per group
-    constexpr int NG = 4 / WPG;         // groups per 128-k chunk
+    constexpr int NG = 8 / WPG;         // groups per 256-k chunk
+    constexpr int RED = WK * COLS * PITCH;      // floats of one buffer of partial sums
     pdl_trigger();
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
     uint8_t* gbase = smem_raw + (base - smem_addr(smem_raw));
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int rank = a.split > 1 ? static_cast<int>(cluster_rank()) : 0;
-    const int n0 = static_cast<int>(blockIdx.x) / a.split * ROWS;
     const int nblk = (a.nchunk + WK - 1) / WK;                       // stages' worth of K
     const int iters = rank < nblk ? (nblk - rank + a.split - 1) / a.split : 0;
+    // row tiles of this CTA: a split has one, else every gridDim.x-th
+    const int tile0 = static_cast<int>(blockIdx.x) / a.split, tile_step = a.split > 1 ? a.tiles : static_cast<int>(gridDim.x);
     auto full = [&](int s) { return base + a.off_bar + 8u * s; };
     auto empty = [&](int s) { return base + a.off_bar + 8u * (kW4MaxStages + s); };
+    const uint32_t x_full = base + a.off_bar + 8u * (2 * kW4MaxStages);
     if (threadIdx.x == 0) {
         for (int s = 0; s < a.stages; ++s) {
             mbar_init(full(s), 1);
             mbar_init(empty(s), kW4Warps);
         }
+        mbar_init(x_full, 1);
         fence_mbar_init();
     }
     __syncthreads();
 
-    float acc[NT][4] = {};
     if (warp == kW4Warps) {
         if (lane == 0) {
             if (iters > 0) {
@@ -113,46 +126,90 @@ __global__ void __launch_bounds__(kW4Threads) w4_gemv_kernel(const __grid_consta
                 prefetch_map(&mX);
             }
             pdl_wait();
-            const uint32_t bytes = WK * ROWS * 64u + 2u * WK * a.M * 128u;
-            int it = 0, s = 0;
+            const uint32_t x_bytes = 4u * WK * a.M * 128u;
+            const uint32_t bytes = WK * ROWS * 128u + (a.x_resident ? 0u : x_bytes);
+            int s = 0, loads = 0;
             uint32_t phase = 0;      // completions of the current stage's barriers so far, mod 2
-            for (; it < iters; ++it) {
-                if (it >= a.stages && !mbar_wait_bounded(empty(s), phase ^ 1u, a.flag)) break;
-                const int kb = (it * a.split + rank) * WK;           // first chunk of the stage
-                mbar_arrive_expect_tx(full(s), bytes);
-                tma_load_3d(base + s * a.stage_bytes, &mW, 0, n0, kb, full(s));
-                tma_load_3d(base + s * a.stage_bytes + a.x_off, &mX, 0, 0, 2 * kb, full(s));
-                if (++s == a.stages) {
-                    s = 0;
-                    phase ^= 1u;
+            bool ok = true;
+            const bool x_once = a.x_resident && iters > 0;
+            if (x_once) {
+                mbar_arrive_expect_tx(x_full, x_bytes * iters);
+                for (int it = 0; it < iters; ++it)
+                    tma_load_3d(base + a.x_off + it * x_bytes, &mX, 0, 0, 4 * (it * a.split + rank) * WK, x_full);
+            }
+            for (int tile = tile0; ok && tile < a.tiles; tile += tile_step) {
+                for (int it = 0; it < iters; ++it) {
+                    if (loads >= a.stages && !mbar_wait_bounded(empty(s), phase ^ 1u, a.flag)) {
+                        ok = false;
+                        break;
+                    }
+                    const int kb = (it * a.split + rank) * WK;           // first chunk of the stage
+                    mbar_arrive_expect_tx(full(s), bytes);
+                    tma_load_3d(base + s * a.stage_bytes, &mW, 0, tile * ROWS, kb, full(s));
+                    if (!a.x_resident) tma_load_3d(base + s * a.stage_bytes + a.x_off, &mX, 0, 0, 4 * kb, full(s));
+                    ++loads;
+                    if (++s == a.stages) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
                 }
             }
-            if (it < iters)   // copies in flight land before the shared memory goes away
-                for (int j = it - a.stages < 0 ? 0 : it - a.stages; j < it; ++j)
-                    (void)mbar_wait_drain(full(j % a.stages), (j / a.stages) & 1);
+            if (!ok) {   // copies in flight land before the shared memory goes away
+                for (int j = max(0, loads - a.stages); j < loads; ++j) (void)mbar_wait_drain(full(j % a.stages), (j / a.stages) & 1);
+                if (x_once) (void)mbar_wait_drain(x_full, 0);
+            }
         }
         __syncwarp();
-    } else {
+        if (a.split == 1) return;
+    }
+
+    float acc[NT][4];
+    const int wr = warp % WR, wk = warp / WR;
+    const int g = lane / 4, t = lane % 4;
+    const T* bias = static_cast<const T*>(a.bias);
+    const T* R = static_cast<const T*>(a.R);
+    float* red = reinterpret_cast<float*>(gbase + a.off_red);   // [2][WK][COLS][PITCH]
+    auto write_red = [&](float* buf) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                buf[(wk * COLS + 8 * nt + 2 * t + (e & 1)) * PITCH + 16 * wr + g + 8 * (e >> 1)] = acc[nt][e];
+    };
+    auto finish = [&](float v, int m, int n) {
+        if (bias) v += to_f32(bias[n]);
+        if (a.gelu) v = gelu_erf(v);
+        const int64_t at = static_cast<int64_t>(m) * a.N + n;
+        if (R) v += to_f32(R[at]);
+        static_cast<T*>(a.y)[at] = from_f32<T>(v);
+    };
+    if (warp < kW4Warps) {
         pdl_wait();
-        const int wr = warp % WR, wk = warp / WR;
-        const int g = lane / 4, t = lane % 4;
         const int KG = a.K / G;
-        const int nlo = n0 + 16 * wr + g, nhi = nlo + 8;
-        // lane t of a row loads group t % NG of a chunk, the four lanes share by shuffles; kAhead stages
-        // ahead of their use, each as one word of two scales and one of two zero points (rows g, g + 8)
-        uint32_t sc_ring[kAhead], zp_ring[kAhead];
-        const uint16_t* sc_lo = static_cast<const uint16_t*>(a.s) + static_cast<int64_t>(nlo < a.N ? nlo : 0) * KG;
-        const uint16_t* sc_hi = static_cast<const uint16_t*>(a.s) + static_cast<int64_t>(nhi < a.N ? nhi : 0) * KG;
-        const uint8_t* zp_lo = static_cast<const uint8_t*>(a.z) + static_cast<int64_t>(nlo < a.N ? nlo : 0) * KG;
-        const uint8_t* zp_hi = static_cast<const uint8_t*>(a.z) + static_cast<int64_t>(nhi < a.N ? nhi : 0) * KG;
-        auto load_scales = [&](int chunk, uint32_t& sc, uint32_t& zp) {
-            const int gi = chunk * NG + t % NG;
+        // Scales and zero points: the four lanes of a row load one group each (two for groups of 32) and share by
+        // shuffles; one word of two scales and one of two zero points (rows g, g + 8) per lane and group, a block
+        // of stages ahead of its use (across row tiles).
+        constexpr int SB = NG < 4 ? 4 / NG : 1;    // stages of a block
+        constexpr int SW = NG < 4 ? 1 : NG / 4;    // words of a lane per block
+        const int gstep = a.split * WK * NG;       // groups from a stage to the next
+        const int gfirst = (rank * WK + wk) * NG + (NG < 4 ? t / NG * gstep + t % NG : t);
+        auto load_scale = [&](int tile, int gi, uint32_t& sc, uint32_t& zp) {
             sc = 0u;
             zp = 0x00080008u;
-            if (gi < KG) {   // past the last chunk: scale zero
-                sc = __ldg(sc_lo + gi) | static_cast<uint32_t>(__ldg(sc_hi + gi)) << 16;
-                if (a.z) zp = (__ldg(zp_lo + gi) & 15u) | (__ldg(zp_hi + gi) & 15u) << 16;
+            const int nlo = tile * ROWS + 16 * wr + g, nhi = nlo + 8;
+            if (gi < KG && nlo < a.N) {   // past the last chunk or row: scale zero
+                const int64_t lo = static_cast<int64_t>(nlo) * KG + gi, hi = nhi < a.N ? lo + 8 * static_cast<int64_t>(KG) : lo;
+                const uint16_t* sp = static_cast<const uint16_t*>(a.s);
+                sc = __ldg(sp + lo) | static_cast<uint32_t>(__ldg(sp + hi)) << 16;
+                if (a.z) {
+                    const uint8_t* zq = static_cast<const uint8_t*>(a.z);
+                    zp = (__ldg(zq + lo) & 15u) | (__ldg(zq + hi) & 15u) << 16;
+                }
             }
+        };
+        auto load_scales = [&](int tile, int gi, uint32_t (&sc)[SW], uint32_t (&zp)[SW]) {
+#pragma unroll
+            for (int i = 0; i < SW; ++i) load_scale(tile, gi + 4 * i, sc[i], zp[i]);
         };
         // one group: WPG words of each row against the matching X pieces
         auto group = [&](int gi, const uint32_t* wl, const uint32_t* wh, auto&& xpiece, uint32_t sc, uint32_t zp) {
@@ -184,164 +241,209 @@ __global__ void __launch_bounds__(kW4Threads) w4_gemv_kernel(const __grid_consta
         // k of word w of group gi within the chunk
         auto kof = [&](int gi, int w) { return gi * G + t * (G / 4) + 8 * w; };
         bool ok = true;
+        // Where this lane's X pieces lie within a stage, of the chunk's eight words in the order of the groups:
+        // columns 8 nt + g are rows apart by 1024 bytes, which leaves the swizzle alone.  Rows past M are
+        // other rows or unused space: those columns are never stored.
+        uint32_t xoff[8];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) load_scales((i * a.split + rank) * WK + wk, sc_ring[i], zp_ring[i]);
-        int s = 0;
+        for (int i = 0; i < 8; ++i) {
+            const int k8 = kof(i / WPG, i % WPG) / 8;                 // 16-byte piece of the chunk, 0..31
+            const uint32_t row = static_cast<uint32_t>((4 * wk + k8 / 8) * a.M + g);
+            xoff[i] = a.x_off + row * 128u + ((static_cast<uint32_t>(k8 & 7) ^ (row & 7u)) << 4);
+        }
+        // the weights of group gi: byte gi G / 2 + t G / 8 of the row's 128, swizzled by the row
+        const uint32_t woff = static_cast<uint32_t>((wk * ROWS + 16 * wr + g) * 128), wsw = static_cast<uint32_t>(g & 7) << 4;
+        const uint32_t x_step = a.x_resident ? 4u * WK * a.M * 128u : 0u;
+        uint32_t sc_next[SW], zp_next[SW], sc[SW] = {}, zp[SW] = {};
+        load_scales(tile0, gfirst, sc_next, zp_next);
+        int s = 0, turn = 0;
         uint32_t phase = 0;
-        for (int it0 = 0; ok && it0 < iters; it0 += kAhead)
+        if (a.x_resident && iters > 0) ok = __all_sync(0xffffffffu, mbar_wait_bounded(x_full, 0, a.flag));
+        for (int tile = tile0; tile < a.tiles; tile += tile_step) {
 #pragma unroll
-          for (int i = 0; i < kAhead; ++i) {
-            const int it = it0 + i;
-            if (it >= iters || !ok) break;
-            const uint32_t sc = sc_ring[i], zp = zp_ring[i];
-            load_scales(((it + kAhead) * a.split + rank) * WK + wk, sc_ring[i], zp_ring[i]);
-            if (!__all_sync(0xffffffffu, mbar_wait_bounded(full(s), phase, a.flag))) {
-                ok = false;
-                break;
-            }
-            const uint32_t wbase = base + s * a.stage_bytes + static_cast<uint32_t>((wk * ROWS + 16 * wr + g) * 64);
-            const uint32_t xbase = base + s * a.stage_bytes + a.x_off;
-            auto xpiece = [&](int nt, int gi, int w) {
-                const int k8 = kof(gi, w) / 8;                         // 16-byte piece of the chunk, 0..15
-                const int m = min(8 * nt + g, a.M - 1);                // columns past M are never stored
-                const uint32_t row = static_cast<uint32_t>((2 * wk + k8 / 8) * a.M + m);
-                return lds128(xbase + row * 128u + ((static_cast<uint32_t>(k8 & 7) ^ (row & 7u)) << 4));
-            };
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int gi = 0; gi < NG; ++gi) {
-                uint32_t wl[WPG], wh[WPG];
-                const uint32_t at = wbase + static_cast<uint32_t>(kof(gi, 0) / 2);
-                if constexpr (WPG == 4) {
-                    const uint4 l = lds128(at), h = lds128(at + 512u);
-                    wl[0] = l.x; wl[1] = l.y; wl[2] = l.z; wl[3] = l.w;
-                    wh[0] = h.x; wh[1] = h.y; wh[2] = h.z; wh[3] = h.w;
-                } else if constexpr (WPG == 2) {
-                    const uint2 l = lds64(at), h = lds64(at + 512u);
-                    wl[0] = l.x; wl[1] = l.y;
-                    wh[0] = h.x; wh[1] = h.y;
-                } else {
-                    wl[0] = lds32(at);
-                    wh[0] = lds32(at + 512u);
+                for (int e = 0; e < 4; ++e) acc[nt][e] = 0.0f;
+            uint32_t xres = 0;
+            for (int it0 = 0; ok && it0 < iters; it0 += SB)
+#pragma unroll
+              for (int i = 0; i < SB; ++i) {
+                if (it0 + i >= iters || !ok) break;
+                if (i == 0) {
+#pragma unroll
+                    for (int j = 0; j < SW; ++j) {
+                        sc[j] = sc_next[j];
+                        zp[j] = zp_next[j];
+                    }
+                    if (it0 + SB < iters) load_scales(tile, gfirst + (it0 + SB) * gstep, sc_next, zp_next);
+                    else load_scales(tile + tile_step, gfirst, sc_next, zp_next);
                 }
-                const int src = (lane & 28) | gi;
-                group(gi, wl, wh, xpiece, __shfl_sync(0xffffffffu, sc, src), __shfl_sync(0xffffffffu, zp, src));
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(empty(s));
-            if (++s == a.stages) {
-                s = 0;
-                phase ^= 1u;
-            }
-        }
-        // the last K % 128 inputs (groups of 32 and 64), from global memory by the first K warps
-        if (G < 128 && ok && rank == 0 && wk == 0 && a.nchunk * 128 < a.K) {
-            const int k0 = a.nchunk * 128;
-            uint32_t sc, zp;
-            load_scales(a.nchunk, sc, zp);
-            const T* x = static_cast<const T*>(a.x);
-            const uint8_t* wq = static_cast<const uint8_t*>(a.wq);
-            const int ng = (a.K - k0) / G;
-            for (int gi = 0; gi < ng; ++gi) {
-                uint32_t wl[WPG], wh[WPG];
-#pragma unroll
-                for (int w = 0; w < WPG; ++w) {
-                    const int64_t at = (k0 + kof(gi, w)) / 2;
-                    wl[w] = nlo < a.N ? *reinterpret_cast<const uint32_t*>(wq + static_cast<int64_t>(nlo) * (a.K / 2) + at) : 0u;
-                    wh[w] = nhi < a.N ? *reinterpret_cast<const uint32_t*>(wq + static_cast<int64_t>(nhi) * (a.K / 2) + at) : 0u;
+                if (!__all_sync(0xffffffffu, mbar_wait_bounded(full(s), phase, a.flag))) {
+                    ok = false;
+                    break;
                 }
-                auto xpiece = [&](int nt, int gj, int w) {
-                    const int m = min(8 * nt + g, a.M - 1);
-                    return *reinterpret_cast<const uint4*>(x + static_cast<int64_t>(m) * a.K + k0 + kof(gj, w));
+                // plain loads: the compiler keeps them behind the wait, and free to move among the rest
+                const uint32_t stage = s * a.stage_bytes;
+                const uint8_t* xs = gbase + (a.x_resident ? xres : stage);
+                xres += x_step;
+                const uint8_t* wbase = gbase + stage + woff;
+                auto xpiece = [&](int nt, int gi, int w) {
+                    return *reinterpret_cast<const uint4*>(xs + xoff[gi * WPG + w] + nt * 1024);
                 };
-                const int src = (lane & 28) | gi;
-                group(gi, wl, wh, xpiece, __shfl_sync(0xffffffffu, sc, src), __shfl_sync(0xffffffffu, zp, src));
+#pragma unroll
+                for (int gi = 0; gi < NG; ++gi) {
+                    uint32_t wl[WPG], wh[WPG];
+                    const uint8_t* at = wbase + (static_cast<uint32_t>(gi * (G / 2) + t * (G / 8)) ^ wsw);
+                    if constexpr (WPG == 4) {
+                        const uint4 l = *reinterpret_cast<const uint4*>(at), h = *reinterpret_cast<const uint4*>(at + 1024);
+                        wl[0] = l.x; wl[1] = l.y; wl[2] = l.z; wl[3] = l.w;
+                        wh[0] = h.x; wh[1] = h.y; wh[2] = h.z; wh[3] = h.w;
+                    } else if constexpr (WPG == 2) {
+                        const uint2 l = *reinterpret_cast<const uint2*>(at), h = *reinterpret_cast<const uint2*>(at + 1024);
+                        wl[0] = l.x; wl[1] = l.y;
+                        wh[0] = h.x; wh[1] = h.y;
+                    } else {
+                        wl[0] = *reinterpret_cast<const uint32_t*>(at);
+                        wh[0] = *reinterpret_cast<const uint32_t*>(at + 1024);
+                    }
+                    const int src = (lane & 28) | (NG < 4 ? i * NG + gi : gi % 4);
+                    group(gi, wl, wh, xpiece, __shfl_sync(0xffffffffu, sc[NG < 4 ? 0 : gi / 4], src),
+                          a.z ? __shfl_sync(0xffffffffu, zp[NG < 4 ? 0 : gi / 4], src) : 0x00080008u);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty(s));
+                if (++s == a.stages) {
+                    s = 0;
+                    phase ^= 1u;
+                }
+            }
+            // the last K % 256 inputs, from global memory by the first K warps
+            if (ok && rank == 0 && wk == 0 && a.nchunk * 256 < a.K) {
+                const int k0 = a.nchunk * 256, nlo = tile * ROWS + 16 * wr + g, nhi = nlo + 8;
+                const T* x = static_cast<const T*>(a.x);
+                const uint8_t* wq = static_cast<const uint8_t*>(a.wq);
+                const int ng = (a.K - k0) / G;
+                for (int gi = 0; gi < ng; ++gi) {
+                    uint32_t wl[WPG], wh[WPG], tsc, tzp;
+                    load_scale(tile, a.nchunk * NG + gi, tsc, tzp);
+#pragma unroll
+                    for (int w = 0; w < WPG; ++w) {
+                        const int64_t at = (k0 + kof(gi, w)) / 2;
+                        wl[w] = nlo < a.N ? *reinterpret_cast<const uint32_t*>(wq + static_cast<int64_t>(nlo) * (a.K / 2) + at) : 0u;
+                        wh[w] = nhi < a.N ? *reinterpret_cast<const uint32_t*>(wq + static_cast<int64_t>(nhi) * (a.K / 2) + at) : 0u;
+                    }
+                    auto xpiece = [&](int nt, int gj, int w) {
+                        const int m = min(8 * nt + g, a.M - 1);
+                        return *reinterpret_cast<const uint4*>(x + static_cast<int64_t>(m) * a.K + k0 + kof(gj, w));
+                    };
+                    group(gi, wl, wh, xpiece, tsc, tzp);
+                }
+            }
+            if (a.split > 1) break;
+            // Sum over the K warps in fixed order, then the epilogue.  Two buffers: a warp writes one again only
+            // after all have passed the next tile's barrier, having read it.
+            float* buf = red + (turn & 1) * RED;
+            ++turn;
+            write_red(buf);
+            sync_compute();
+            for (int i = threadIdx.x; i < ROWS * a.M; i += 32 * kW4Warps) {
+                const int m = i / ROWS, r = i % ROWS, n = tile * ROWS + r;
+                if (n >= a.N) continue;
+                float v = 0.0f;
+#pragma unroll
+                for (int k = 0; k < WK; ++k) v += buf[(k * COLS + m) * PITCH + r];
+                finish(v, m, n);
             }
         }
     }
+    if (a.split == 1) return;
 
-    // sum over the K warps, then over the cluster, in fixed order; then the epilogue
-    float* red = reinterpret_cast<float*>(gbase + a.off_red);   // [WK][COLS][ROWS + 4]
-    constexpr int PITCH = ROWS + 4;
+    // a split: sums over the K warps, then over the cluster in rank order
     __syncthreads();
-    if (warp < kW4Warps) {
-        const int wr = warp % WR, wk = warp / WR, g = lane / 4, t = lane % 4;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                red[(wk * COLS + 8 * nt + 2 * t + (e & 1)) * PITCH + 16 * wr + g + 8 * (e >> 1)] = acc[nt][e];
-    }
+    if (warp < kW4Warps) write_red(red);
     __syncthreads();
     const int per = ROWS * a.M;
-    if (a.split > 1) {
-        for (int i = threadIdx.x; i < per; i += kW4Threads) {
-            const int m = i / ROWS, r = i % ROWS;
-            float v = red[m * PITCH + r];
+    for (int i = threadIdx.x; i < per; i += kW4Threads) {
+        const int m = i / ROWS, r = i % ROWS;
+        float v = red[m * PITCH + r];
 #pragma unroll
-            for (int k = 1; k < WK; ++k) v += red[(k * COLS + m) * PITCH + r];
-            red[m * PITCH + r] = v;
-        }
-        __syncwarp();
-        cluster_sync();
-    }
-    const T* bias = static_cast<const T*>(a.bias);
-    const T* R = static_cast<const T*>(a.R);
-    for (int i = rank * kW4Threads + threadIdx.x; i < per; i += a.split * kW4Threads) {
-        const int m = i / ROWS, r = i % ROWS, n = n0 + r;
-        if (n >= a.N) continue;
-        float v = 0.0f;
-        if (a.split > 1) {
-            const uint32_t at = smem_addr(red + m * PITCH + r);
-            for (int c = 0; c < a.split; ++c) {
-                float p;
-                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(p) : "r"(mapa_shared(at, c)) : "memory");
-                v += p;
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < WK; ++k) v += red[(k * COLS + m) * PITCH + r];
-        }
-        if (bias) v += to_f32(bias[n]);
-        if (a.gelu) v = gelu_erf(v);
-        const int64_t at = static_cast<int64_t>(m) * a.N + n;
-        if (R) v += to_f32(R[at]);
-        static_cast<T*>(a.y)[at] = from_f32<T>(v);
+        for (int k = 1; k < WK; ++k) v += red[(k * COLS + m) * PITCH + r];
+        red[m * PITCH + r] = v;
     }
     __syncwarp();
-    if (a.split > 1) cluster_sync();   // the sums stay in place until every CTA has read them
+    cluster_sync();
+    for (int i = rank * kW4Threads + threadIdx.x; i < per; i += a.split * kW4Threads) {
+        const int m = i / ROWS, r = i % ROWS, n = tile0 * ROWS + r;
+        if (n >= a.N) continue;
+        const uint32_t at = smem_addr(red + m * PITCH + r);
+        float v = 0.0f;
+        for (int c = 0; c < a.split; c += 2) {      // split is 2, 4 or 8
+            float p0, p1;
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(p0) : "r"(mapa_shared(at, c)) : "memory");
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(p1) : "r"(mapa_shared(at, c + 1)) : "memory");
+            v = (v + p0) + p1;
+        }
+        finish(v, m, n);
+    }
+    __syncwarp();
+    cluster_sync();   // the sums stay in place until every CTA has read them
 }
 
 template <typename T, int G, int NT>
 int launch_w4(W4Args a, cudaStream_t st) {
     constexpr int WR = NT, WK = kW4Warps / NT, ROWS = 16 * WR;
     CUtensorMap mW{}, mX{};
-    a.nchunk = a.K / 128;
-    // a map needs a chunk to describe; without one (K < 128) no stage is loaded
+    a.nchunk = a.K / 256;
+    // a map needs a chunk to describe; without one (K < 256) no stage is loaded
     if (a.nchunk > 0) {
-        const int64_t wd[3] = {64, a.N, a.nchunk}, ws[2] = {a.K / 2, 64};
-        const int wb[3] = {64, ROWS, WK};
-        const int64_t xd[3] = {64, a.M, 2 * static_cast<int64_t>(a.nchunk)}, xs[2] = {static_cast<int64_t>(a.K) * 2, 128};
-        const int xb[3] = {64, a.M, 2 * WK};
-        if (!make_map_3d(&mW, a.wq, kMapU8, wd, ws, wb, 0) || !make_map_3d(&mX, a.x, kMap16, xd, xs, xb, 128)) return FUSE_ECUDA;
+        const int64_t wd[3] = {128, a.N, a.nchunk}, ws[2] = {a.K / 2, 128};
+        const int wb[3] = {128, ROWS, WK};
+        const int64_t xd[3] = {64, a.M, 4 * static_cast<int64_t>(a.nchunk)}, xs[2] = {static_cast<int64_t>(a.K) * 2, 128};
+        const int xb[3] = {64, a.M, 4 * WK};
+        if (!make_map_3d(&mW, a.wq, kMapU8, wd, ws, wb, 128) || !make_map_3d(&mX, a.x, kMap16, xd, xs, xb, 128)) return FUSE_ECUDA;
     }
-    a.x_off = WK * ROWS * 64;
-    a.stage_bytes = static_cast<uint32_t>((a.x_off + 2 * WK * a.M * 128 + 1023) / 1024 * 1024);
-    const uint32_t red = static_cast<uint32_t>(WK * 8 * NT * (ROWS + 4) * 4);
-    const int row_tiles = static_cast<int>(ceil_div(a.N, ROWS));
+    a.tiles = static_cast<int>(ceil_div(a.N, ROWS));
     const int nblk = static_cast<int>(ceil_div(a.nchunk, WK));
     a.split = 1;
-    while (a.split < 8 && row_tiles * a.split * 2 <= 2 * sm_count() && nblk >= 4 * a.split) a.split *= 2;
+    while (a.split < 8 && a.tiles * a.split * 2 <= 2 * sm_count() && nblk >= 2 * a.split) a.split *= 2;
     const int iters = static_cast<int>(ceil_div(nblk > 0 ? nblk : 1, a.split));
-    a.stages = iters < kW4MaxStages ? iters : kW4MaxStages;
-    while (a.stages > 1 && a.stages * a.stage_bytes + red > 110 * 1024) --a.stages;
-    a.off_red = a.stages * a.stage_bytes;
+    // X stays in shared memory for all of a CTA's tiles where it is small (whole stages of it keep the
+    // swizzle's phase: 4 WK M rows are a multiple of 8), else it comes with every stage
+    const int x_stage = 4 * WK * a.M * 128;
+    a.x_resident = NT <= 2 && a.split == 1 && a.tiles > sm_count() && iters * x_stage <= 32 * 1024 ? 1 : 0;
+    const uint32_t w_stage = WK * ROWS * 128;
+    a.stage_bytes = static_cast<uint32_t>((w_stage + (a.x_resident ? 0 : x_stage) + 1023) / 1024 * 1024);
+    const uint32_t x_all = a.x_resident ? iters * x_stage : 0;
+    const uint32_t pad = 8 * NT * 128;      // columns past M are read from behind the last rows of X
+    const bool several = NT <= 2 && a.split == 1;     // row tiles per CTA, with two buffers of partial sums
+    const uint32_t red = static_cast<uint32_t>((several ? 2 : 1) * WK * 8 * NT * (ROWS + 4) * 4);
+    const uint32_t bars = 8 * (2 * kW4MaxStages + 1);
+    const int per_sm = static_cast<int>(ceil_div(static_cast<int64_t>(a.tiles) * a.split, sm_count()));
+    const uint32_t budget = NT > 2 ? kW4Smem : per_sm > 2 ? 73 * 1024 : 112 * 1024;   // 1, 3 or 2 CTAs per SM
+    const int want = a.split > 1 ? iters : kW4MaxStages;
+    a.stages = want < kW4MaxStages ? want : kW4MaxStages;
+    while (a.stages > 2 && a.stages * a.stage_bytes + x_all + red + pad + bars + 1024 > budget) --a.stages;
+    a.x_off = a.x_resident ? a.stages * a.stage_bytes : w_stage;
+    a.off_red = (a.stages * a.stage_bytes + x_all + pad + 15) / 16 * 16;
     a.off_bar = a.off_red + (red + 15) / 16 * 16;
-    const uint32_t smem = a.off_bar + 16 * kW4MaxStages + 1024;
-    const int rc = opt_in_smem((const void*)w4_gemv_kernel<T, G, NT>, 116 * 1024, true);
+    const uint32_t smem = a.off_bar + bars + 1024;
+    if (smem > kW4Smem) return FUSE_EUNSUPPORTED;
+    const int rc = opt_in_smem((const void*)w4_gemv_kernel<T, G, NT>, kW4Smem, true);
     if (rc != FUSE_OK) return rc;
-    return launch_pdl(w4_gemv_kernel<T, G, NT>, dim3(static_cast<unsigned>(row_tiles * a.split)), dim3(kW4Threads), smem, st, a.split, mW, mX, a);
+    int64_t grid = static_cast<int64_t>(a.tiles) * a.split;
+    if (several) {   // as many CTAs as are resident; each takes every grid-th row tile
+        static std::atomic<uint32_t> known{0};    // shared memory (KB) and CTAs per SM of the last launch
+        const uint32_t kb = (smem + 1023) / 1024;
+        uint32_t k = known.load(std::memory_order_relaxed);
+        if ((k >> 8) != kb) {
+            k = (kb << 8) | static_cast<uint32_t>(blocks_per_sm(w4_gemv_kernel<T, G, NT>, kW4Threads, kb * 1024));
+            known.store(k, std::memory_order_relaxed);
+        }
+        const int64_t resident = static_cast<int64_t>(sm_count()) * (k & 255u);
+        if (grid > resident) grid = resident;
+    }
+    return launch_pdl(w4_gemv_kernel<T, G, NT>, dim3(static_cast<unsigned>(grid)), dim3(kW4Threads), smem, st, a.split, mW, mX, a);
 }
-
 
 // ================================================================== tcgen05 tiles
 // More than a few tokens make the matrix instructions count.  The integers q - z go from registers into
@@ -559,9 +661,9 @@ __global__ void __launch_bounds__(kTileThreads, 2) w4_tile_kernel(
                 if (!wait(full(st), st_par)) break;
                 // A buffer ab is free: the accumulators of unit u - 2 have been waited for
                 // this thread's row: 64 k from 64 hh on, two 16-byte pieces of the row's four
-                const uint32_t row = base + st * L::STAGE + r * 64;
+                const uint8_t* row = gbase + st * L::STAGE + r * 64;
                 const uint32_t sw = static_cast<uint32_t>((r >> 1) & 3);
-                const uint4 w0 = lds128(row + (((2u * hh) ^ sw) << 4)), w1 = lds128(row + (((2u * hh + 1u) ^ sw) << 4));
+                const uint4 w0 = *reinterpret_cast<const uint4*>(row + (((2u * hh) ^ sw) << 4)), w1 = *reinterpret_cast<const uint4*>(row + (((2u * hh + 1u) ^ sw) << 4));
                 const uint32_t words[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
                 uint32_t zb[2] = {Nib<T>::MAGIC | 0x00080008u, Nib<T>::MAGIC | 0x00080008u};   // first and second 32 k
                 if (a.zeros) {
