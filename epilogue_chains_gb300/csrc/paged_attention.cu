@@ -150,7 +150,8 @@ struct Cursor {
 template <typename T, int D>
 __global__ void __launch_bounds__(kOwnThreads, 2) paged_own_kernel(
     const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
-    const __grid_constant__ CUtensorMap mV, const __grid_constant__ PagedArgs a) {
+    const __grid_constant__ CUtensorMap mV, const __grid_constant__ CUtensorMap mK16,
+    const __grid_constant__ CUtensorMap mV16, const __grid_constant__ PagedArgs a) {
     using L = OwnLayout<D>;
     pdl_trigger();
     extern __shared__ uint8_t smem_raw[];
@@ -247,83 +248,105 @@ __global__ void __launch_bounds__(kOwnThreads, 2) paged_own_kernel(
 
     if (warp == kOwnWarps) {
         // ---------------------------------------------------------------- loads
-        const int box_shift = min(a.page_shift, 6);              // keys of one TMA box
+        // Whole units come in boxes of a page (64 keys at most), the last one of a sequence in boxes of 16, so
+        // that hardly more is read than there is.
+        const int big_shift = min(a.page_shift, 6);
         struct Place {
-            int row[4];      // cache rows of the unit's boxes
+            int page[4];     // of the unit's boxes, as the table has them
+            int in[4];       // row of a box within its page, all heads counted
             int boxes;       // boxes with keys; 0 where the sequence has none
-            int qrow;        // first query row if a run begins here, else -1
+            int shift;       // keys of a box
+            int qrow;        // first query row if a part begins here, else -1
         };
+        // The table is read for 32 units, one per lane, and the entries are used only when the 32 before them
+        // have been loaded.
         auto place = [&](int i, Place& p) {   // unit u0 + i
             p.boxes = 0;
+            p.shift = 4;
             p.qrow = -1;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) p.row[x] = a.cache_rows;
             if (i >= total) return;
             Cursor k;
             locate(u0 + i, k);
             const int head = k.hr / a.rt, nk = min(kUnit, k.len - k.j * kUnit);
-            p.boxes = nk > 0 ? (nk + (1 << box_shift) - 1) >> box_shift : 0;
-            if ((i == 0 || k.j == 0) && nk > 0) p.qrow = k.b * a.hq + head * a.group + (k.hr % a.rt) * 16;
+            if (nk <= 0) return;
+            p.shift = nk == kUnit ? big_shift : 4;
+            p.boxes = (nk + (1 << p.shift) - 1) >> p.shift;
+            if (i == 0 || k.j == 0) p.qrow = k.b * a.hq + head * a.group + (k.hr % a.rt) * 16;
 #pragma unroll
             for (int x = 0; x < 4; ++x)
                 if (x < p.boxes) {
-                    const int key = k.j * kUnit + (x << box_shift);
-                    const int page = a.table[k.b * a.table_ld + (key >> a.page_shift)];
-                    if (page >= 0 && page < a.num_pages)
-                        p.row[x] = ((page * a.hk + head) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
-                    else
-                        atomicExch(a.bad, 1);   // its rows stay past the cache: zeros
+                    const int key = k.j * kUnit + (x << p.shift);
+                    p.page[x] = a.table[k.b * a.table_ld + (key >> a.page_shift)];
+                    p.in[x] = (head << a.page_shift) + (key & ((1 << a.page_shift) - 1));
                 }
         };
+        const int page_rows = a.hk << a.page_shift;
+        auto row_of = [&](const Place& p, int x) {
+            if (x >= p.boxes) return 0;
+            if (p.page[x] >= 0 && p.page[x] < a.num_pages) return p.page[x] * page_rows + p.in[x];
+            atomicExch(a.bad, 1);
+            return a.cache_rows;         // past the cache: zeros
+        };
+        const uint32_t one = elect_one();
         int slot = 0, loads = 0, qs = 0, qloads = 0;
         uint32_t phase = 0, qphase = 0;          // completions of the current slot's barriers so far, mod 2
         bool ok = true;
-        Place cur, ahead;
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, a.flag));
+            return ok;
+        };
+        Place cur{}, ahead{};
         place(lane, cur);
         for (int i0 = 0; ok && i0 < total; i0 += 32) {
-            place(i0 + 32 + lane, ahead);
-            for (int x = 0; ok && x < 32 && i0 + x < total; ++x) {
+            int row[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) row[x] = row_of(cur, x);
+            const int n = min(32, total - i0);
+            for (int x = 0; ok && x < n; ++x) {
                 const int boxes = __shfl_sync(0xffffffffu, cur.boxes, x);
-                if (boxes == 0) continue;
-                const int qrow = __shfl_sync(0xffffffffu, cur.qrow, x);
-                if (qrow >= 0) {
-                    if (qloads >= kOwnQ && !__all_sync(0xffffffffu, mbar_wait_bounded(q_empty(qs), qphase ^ 1u, a.flag))) {
-                        ok = false;
-                        break;
-                    }
-                    if (lane == 0) mbar_arrive_expect_tx(q_full(qs), static_cast<uint32_t>(a.rows) * (D * 2));
-                    __syncwarp();
-                    if (lane < L::ATOMS) tma_load_2d(base + a.off_q + qs * L::QSLOT + lane * L::QATOM, &mQ, 64 * lane, qrow, q_full(qs));
-                    ++qloads;
-                    if (++qs == kOwnQ) {
-                        qs = 0;
-                        qphase ^= 1u;
-                    }
-                }
-                // lane l < boxes * ATOMS loads component atom l % ATOMS of box l / ATOMS
-                int row = 0;
+                if (boxes > 0) {
+                    const int qrow = __shfl_sync(0xffffffffu, cur.qrow, x), shift = __shfl_sync(0xffffffffu, cur.shift, x);
+                    if (qrow >= 0) {
+                        if (qloads >= kOwnQ && !wait(q_empty(qs), qphase ^ 1u)) break;
+                        if (lane == 0) mbar_arrive_expect_tx(q_full(qs), static_cast<uint32_t>(a.rows) * (D * 2));
+                        __syncwarp();
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const int r = __shfl_sync(0xffffffffu, cur.row[y], x);
-                    if (lane / L::ATOMS == y) row = r;
-                }
-                const int atom = lane % L::ATOMS, box = lane / L::ATOMS;
+                        for (int i = 0; i < L::ATOMS; ++i) tma_load_2d_if(one, base + a.off_q + qs * L::QSLOT + i * L::QATOM, &mQ, 64 * i, qrow, q_full(qs));
+                        ++qloads;
+                        if (++qs == kOwnQ) {
+                            qs = 0;
+                            qphase ^= 1u;
+                        }
+                    }
+                    int r[4];
 #pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    if (loads >= a.slots && !__all_sync(0xffffffffu, mbar_wait_bounded(empty(slot), phase ^ 1u, a.flag))) {
-                        ok = false;
-                        break;
-                    }
-                    if (lane == 0) mbar_arrive_expect_tx(full(slot), static_cast<uint32_t>(boxes << box_shift) * (D * 2));
-                    __syncwarp();
-                    if (box < boxes)
-                        tma_load_2d(base + slot * L::SLOT + atom * L::ATOM + ((static_cast<uint32_t>(box) << box_shift) * 128), kv ? &mV : &mK, 64 * atom, row, full(slot));
-                    ++loads;
-                    if (++slot == a.slots) {
-                        slot = 0;
-                        phase ^= 1u;
+                    for (int y = 0; y < 4; ++y) r[y] = __shfl_sync(0xffffffffu, row[y], x);
+                    auto load = [&](const CUtensorMap* map) {
+                        if (loads >= a.slots && !wait(empty(slot), phase ^ 1u)) return;
+                        if (lane == 0) mbar_arrive_expect_tx(full(slot), static_cast<uint32_t>(boxes << shift) * (D * 2));
+                        __syncwarp();
+                        const uint32_t dst = base + slot * L::SLOT;
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            if (y < boxes)
+#pragma unroll
+                                for (int i = 0; i < L::ATOMS; ++i)
+                                    tma_load_2d_if(one, dst + i * L::ATOM + ((static_cast<uint32_t>(y) << shift) * 128), map, 64 * i, r[y], full(slot));
+                        ++loads;
+                        if (++slot == a.slots) {
+                            slot = 0;
+                            phase ^= 1u;
+                        }
+                    };
+                    if (shift == big_shift) {
+                        load(&mK);
+                        if (ok) load(&mV);
+                    } else {
+                        load(&mK16);
+                        if (ok) load(&mV16);
                     }
                 }
+                if (x == min(3, n - 1)) place(i0 + 32 + lane, ahead);   // once the ring has something to load
             }
             cur = ahead;
         }
@@ -777,6 +800,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix_kernel(const __gr
         const bool is_k = warp == 0;
         const CUtensorMap* map = is_k ? &mK : &mV;
         const int box_shift = min(a.page_shift, 7);
+        const uint32_t one = elect_one();
         if (lane == 0) prefetch_map(map);
         int i = 0;
         const int total = static_cast<int>(u1 - u0);
@@ -798,9 +822,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix_kernel(const __gr
             if (i >= KV && !__all_sync(0xffffffffu, mbar_wait_bounded(empty, ((i - KV) / KV) & 1, flag))) break;
             if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(nbox << box_shift) * (D * 2));
             __syncwarp();
-            if (lane < nbox) {
-                const uint32_t dst = base + (is_k ? L::OFF_K : L::OFF_V) + st * L::TILE + (static_cast<uint32_t>(lane) << box_shift) * 128;
-                for (int c = 0; c < L::ATOMS; ++c) tma_load_2d(dst + c * L::REGION, map, 64 * c, row, full);
+            const uint32_t dst = base + (is_k ? L::OFF_K : L::OFF_V) + st * L::TILE;
+            for (int y = 0; y < nbox; ++y) {
+                const int r = __shfl_sync(0xffffffffu, row, y);
+#pragma unroll
+                for (int c = 0; c < L::ATOMS; ++c)
+                    tma_load_2d_if(one, dst + c * L::REGION + ((static_cast<uint32_t>(y) << box_shift) * 128), map, 64 * c, r, full);
             }
         }
         if (i < total)   // copies in flight land before the shared memory goes away
@@ -1078,7 +1105,7 @@ int own_smem(PagedArgs* a, uint32_t* bytes, int* ctas) {
 template <typename T, int D>
 int run_paged(PagedArgs a, const void* k, const void* v, cudaStream_t st) {
     const bool bf = std::is_same<T, __nv_bfloat16>::value;
-    CUtensorMap mQ, mK, mV;
+    CUtensorMap mQ, mK, mV, mK16, mV16;
     if (a.plen > 0) {
         const int box = 1 << (a.page_shift < 7 ? a.page_shift : 7);
         if (!make_map(&mK, k, a.cache_rows, D, 64, box, bf) || !make_map(&mV, v, a.cache_rows, D, 64, box, bf)) return FUSE_ECUDA;
@@ -1090,7 +1117,8 @@ int run_paged(PagedArgs a, const void* k, const void* v, cudaStream_t st) {
     }
     const int box = 1 << (a.page_shift < 6 ? a.page_shift : 6);
     if (!make_map(&mQ, a.q, static_cast<int64_t>(a.batch) * a.hq, D, 64, a.rows, bf) || !make_map(&mK, k, a.cache_rows, D, 64, box, bf) ||
-        !make_map(&mV, v, a.cache_rows, D, 64, box, bf))
+        !make_map(&mV, v, a.cache_rows, D, 64, box, bf) || !make_map(&mK16, k, a.cache_rows, D, 64, 16, bf) ||
+        !make_map(&mV16, v, a.cache_rows, D, 64, 16, bf))
         return FUSE_ECUDA;
     uint32_t smem = 0;
     int ctas = 0;
@@ -1104,7 +1132,7 @@ int run_paged(PagedArgs a, const void* k, const void* v, cudaStream_t st) {
     if (grid > units) grid = units;
     if (grid > kOwnGrid) grid = kOwnGrid;
     if (units / grid >= 0x7fffffffLL) return FUSE_EUNSUPPORTED;
-    rc = launch_pdl(paged_own_kernel<T, D>, dim3(static_cast<unsigned>(grid)), dim3(kOwnThreads), smem, st, 1, mQ, mK, mV, a);
+    rc = launch_pdl(paged_own_kernel<T, D>, dim3(static_cast<unsigned>(grid)), dim3(kOwnThreads), smem, st, 1, mQ, mK, mV, mK16, mV16, a);
     if (rc != FUSE_OK || a.plen == 0) return rc;
     const int64_t warps = static_cast<int64_t>(a.batch) * a.hq;
     return launch_pdl(paged_join_kernel<T, D>, dim3(static_cast<unsigned>(ceil_div(warps, kJoinThreads / 32))), dim3(kJoinThreads), 0, st, 1, a);
