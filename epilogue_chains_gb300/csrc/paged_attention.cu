@@ -88,7 +88,7 @@ struct PagedArgs {
     int *flag, *bad;
 };
 
-// The CTA of `grid` that a unit belongs to when CTA c takes units [c U / grid, (c + 1) U / grid).
+// The CTA of `grid` that place u belongs to when CTA c takes places [c U / grid, (c + 1) U / grid).
 __device__ __forceinline__ int cta_of(int64_t u, int64_t U, int grid) {
     const uint64_t n = static_cast<uint64_t>(u + 1) * static_cast<uint32_t>(grid) - 1;
     if (((n | static_cast<uint64_t>(U)) >> 32) == 0)   // a 64-bit division takes several times as long
@@ -135,12 +135,16 @@ struct OwnLayout {
     static constexpr bool Q_REGS = D <= 128;
 };
 
-// A unit of a CTA's run.
+// What is dealt out to the CTAs are places in one line: per item, that is sequence and row tile of a key/value
+// head, an entry and then its units.  The entry stands for what an item costs apart from its units (loading
+// the query rows, joining the parts: about a unit's time).  Without it, CTAs that got sequences of one unit took
+// up to 40 us where the median took 27 (256 sequences of 1 to 256 keys).
 struct Cursor {
-    int left;        // units left of the run, this one included
+    int left;        // places left of the CTA's, this one included
     int b, hr;       // sequence; key/value head * rt + row tile
-    int j, n, len;   // unit of the sequence, their number, its keys
+    int j, n, len;   // unit of the sequence (-1: the entry), their number, its keys
 };
+__device__ __forceinline__ int places_of(int len) { return 1 + (len > kUnit ? (len - 1) / kUnit + 1 : 1); }
 
 // Four computing warps and one that loads.  The loading warp places 32 units at a time, one per lane (which
 // sequence and head, which pages), a batch ahead of the loads, so that no table entry is waited for between
@@ -158,7 +162,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2) paged_own_kernel(
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
     uint8_t* gbase = smem_raw + (base - smem_addr(smem_raw));
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    int* pre = reinterpret_cast<int*>(gbase + a.off_pre);        // [batch + 1] units before a sequence
+    int* pre = reinterpret_cast<int*>(gbase + a.off_pre);        // [batch + 1] places of a head before a sequence
     int* slen = pre + a.batch + 1;                               // [batch]
     __shared__ int wsum[kOwnWarps + 1];
     const uint32_t bars = base + a.off_bar;
@@ -189,7 +193,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2) paged_own_kernel(
     }
     pdl_wait();
 
-    // ------------------------------------------------------------ units of every sequence
+    // ------------------------------------------------------------ places of every sequence
     {
         const int64_t most = a.table_ld << a.page_shift;
         const int per = (a.batch + kOwnThreads - 1) / kOwnThreads, b0 = tid * per;
@@ -201,7 +205,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2) paged_own_kernel(
                 n = n < 0 ? 0 : static_cast<int>(most);
             }
             slen[b] = n;
-            sum += n > kUnit ? (n - 1) / kUnit + 1 : 1;
+            sum += places_of(n);
         }
         int scan = sum;
 #pragma unroll
@@ -215,14 +219,14 @@ __global__ void __launch_bounds__(kOwnThreads, 2) paged_own_kernel(
         for (int w = 0; w < warp; ++w) at += wsum[w];
         for (int b = b0; b < b0 + per && b < a.batch; ++b) {
             pre[b] = at;
-            at += slen[b] > kUnit ? (slen[b] - 1) / kUnit + 1 : 1;
+            at += places_of(slen[b]);
             if (b == a.batch - 1) pre[a.batch] = at;
         }
         __syncthreads();
     }
     const int HR = a.hk * a.rt;
     const int64_t U = static_cast<int64_t>(pre[a.batch]) * HR;
-    const int G = static_cast<int>(min(static_cast<int64_t>(gridDim.x), U));   // CTAs with work: one unit at least
+    const int G = static_cast<int>(min(static_cast<int64_t>(gridDim.x), U));   // CTAs with work: one place at least
     if (static_cast<int>(blockIdx.x) >= G) return;
     const int64_t u0 = blockIdx.x * U / G;
     const int total = static_cast<int>((blockIdx.x + 1) * U / G - u0);
@@ -234,15 +238,16 @@ __global__ void __launch_bounds__(kOwnThreads, 2) paged_own_kernel(
             if (static_cast<int64_t>(pre[mid]) * HR <= u) lo = mid; else hi = mid - 1;
         }
         k.b = lo;
-        k.n = pre[lo + 1] - pre[lo];
+        const int places = pre[lo + 1] - pre[lo];
+        k.n = places - 1;
         k.len = slen[lo];
         const int64_t in = u - static_cast<int64_t>(pre[lo]) * HR;
         if ((in >> 32) == 0) {
-            k.hr = static_cast<int>(static_cast<uint32_t>(in) / static_cast<uint32_t>(k.n));
-            k.j = static_cast<int>(static_cast<uint32_t>(in) % static_cast<uint32_t>(k.n));
+            k.hr = static_cast<int>(static_cast<uint32_t>(in) / static_cast<uint32_t>(places));
+            k.j = static_cast<int>(static_cast<uint32_t>(in) % static_cast<uint32_t>(places)) - 1;
         } else {
-            k.hr = static_cast<int>(in / k.n);
-            k.j = static_cast<int>(in % k.n);
+            k.hr = static_cast<int>(in / places);
+            k.j = static_cast<int>(in % places) - 1;
         }
     };
 
@@ -260,7 +265,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2) paged_own_kernel(
         };
         // The table is read for 32 units, one per lane, and the entries are used only when the 32 before them
         // have been loaded.
-        auto place = [&](int i, Place& p) {   // unit u0 + i
+        auto place = [&](int i, Place& p) {   // place u0 + i
             p.boxes = 0;
             p.shift = 4;
             p.qrow = -1;
@@ -268,7 +273,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2) paged_own_kernel(
             Cursor k;
             locate(u0 + i, k);
             const int head = k.hr / a.rt, nk = min(kUnit, k.len - k.j * kUnit);
-            if (nk <= 0) return;
+            if (k.j < 0 || nk <= 0) return;
             p.shift = nk == kUnit ? big_shift : 4;
             p.boxes = (nk + (1 << p.shift) - 1) >> p.shift;
             if (i == 0 || k.j == 0) p.qrow = k.b * a.hq + head * a.group + (k.hr % a.rt) * 16;
@@ -373,7 +378,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2) paged_own_kernel(
         int c0 = 0, c1 = 0;
         bool last = k.j0 == 0 && k.j1 == k.n;
         if (!last) {
-            const int64_t first = static_cast<int64_t>(pre[k.b]) * HR + static_cast<int64_t>(k.hr) * k.n;
+            const int64_t first = static_cast<int64_t>(pre[k.b]) * HR + static_cast<int64_t>(k.hr) * (k.n + 1) + 1;
             c0 = cta_of(first, U, G);
             c1 = cta_of(first + k.n - 1, U, G);
         }
@@ -435,11 +440,11 @@ __global__ void __launch_bounds__(kOwnThreads, 2) paged_own_kernel(
     auto next = [&](Cursor& k) {
         --k.left;
         if (++k.j < k.n) return;
-        k.j = 0;
+        k.j = -1;
         if (++k.hr < HR) return;
         k.hr = 0;
         if (++k.b < a.batch) {
-            k.n = pre[k.b + 1] - pre[k.b];
+            k.n = pre[k.b + 1] - pre[k.b] - 1;
             k.len = slen[k.b];
         }
     };
@@ -473,6 +478,10 @@ __global__ void __launch_bounds__(kOwnThreads, 2) paged_own_kernel(
     const int vkey = warp * kChunk + ((((lane >> 3) & 1) << 3) | (lane & 7)), vcol = lane >> 4;
     auto swz = [](int row, int col) { return static_cast<uint32_t>(row * 128 + (((col & 7) ^ (row & 7)) << 4)); };
     while (cur.left > 0) {
+        if (cur.j < 0) {
+            next(cur);
+            continue;
+        }
         // ---- a run of units of one sequence and head: this CTA's part of it
         const int b = cur.b, hr = cur.hr, j0 = cur.j, n = cur.n;
         const int j1 = min(n - j0, cur.left) + j0;
@@ -635,7 +644,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2) paged_own_kernel(
         before = Run{b, hr, j0, j1, n, buf};
         ++runs;
     }
-    join_before();
+    if (runs > 0) join_before();
 }
 
 // With a shared prefix, the last step: a row's own part and the prefix's parts.  One warp per query row, lane c
@@ -1128,7 +1137,7 @@ int run_paged(PagedArgs a, const void* k, const void* v, cudaStream_t st) {
     if (rc != FUSE_OK) return rc;
     // every CTA is resident at once; more than there can be units would have nothing to do
     int64_t grid = static_cast<int64_t>(sm_count()) * ctas;
-    const int64_t units = static_cast<int64_t>(a.batch) * a.hk * a.rt * (ceil_div(a.table_ld << a.page_shift, kUnit) + 1);
+    const int64_t units = static_cast<int64_t>(a.batch) * a.hk * a.rt * (ceil_div(a.table_ld << a.page_shift, kUnit) + 2);
     if (grid > units) grid = units;
     if (grid > kOwnGrid) grid = kOwnGrid;
     if (units / grid >= 0x7fffffffLL) return FUSE_EUNSUPPORTED;
@@ -1197,8 +1206,8 @@ extern "C" int fuse_paged_attention(const void* q, const void* k_cache, const vo
     if (batch > kMaxBatch || q_heads > 65536 || batch * q_heads >= top || num_pages >= top / (kv_heads * page_size) ||
         table_ld >= (top - 4096) / page_size || prefix_len >= top - 4096)
         return FUSE_EUNSUPPORTED;
-    // units of the whole batch, and tiles of the prefix, stay below 2^31
-    if ((table_ld * page_size / kUnit + 1) * batch >= top) return FUSE_EUNSUPPORTED;
+    // places of the whole batch, and tiles of the prefix, stay below 2^31
+    if ((table_ld * page_size / kUnit + 2) * batch >= top) return FUSE_EUNSUPPORTED;
     const int64_t group = q_heads / kv_heads;
     if (prefix_len > 0 && ceil_div(prefix_len, 128) * kv_heads * ceil_div(batch * group, 128) >= top) return FUSE_EUNSUPPORTED;
     if (batch == 0) return FUSE_OK;
