@@ -82,9 +82,9 @@ struct PagedArgs {
     int* count;                        // [kOwnGrid][kOwnWarps] parts that have arrived, by the item's first CTA
     float *oml, *oo;                   // [2 kOwnGrid][rows] (m, l) and [..][rows][D]
     float *rml, *ro;                   // with a prefix: own part of every row, [batch hq] (m, l) and [..][D]
-    float *pml, *po;                   // [kPrefixGrid + pitems][128] (m, l, l', -) and [..][128][D]
+    float *pml, *po;                   // [kPrefixGrid + pitems][prow] (m, l, l', -) and [..][prow][D]
     // prefix
-    int plen, ptiles, prt, pgrid;      // keys, 128-key tiles, 128-row tiles of a head, CTAs
+    int plen, ptiles, prow, prt, pgrid; // keys, 128-key tiles, rows of an item (128 or 256), a head's items, CTAs
     int *flag, *bad;
 };
 
@@ -659,14 +659,15 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     if (row >= static_cast<int64_t>(a.batch) * a.hq) return;
     const int b = static_cast<int>(row / a.hq), h = static_cast<int>(row % a.hq);
     const int head = h / a.group, prow = b * a.group + h % a.group;
-    const int pit = head * a.prt + prow / 128;
+    const int rpi = a.prow;
+    const int pit = head * a.prt + prow / rpi;
     const int64_t PU = static_cast<int64_t>(a.hk) * a.prt * a.ptiles, u = static_cast<int64_t>(pit) * a.ptiles;
     const int c0 = cta_of(u, PU, a.pgrid), np = cta_of(u + a.ptiles - 1, PU, a.pgrid) - c0 + 1;
     // lane 0 has the row's own part, lanes 1 .. the prefix's; 31 of those at a time
     float m = -INFINITY, l = 0.0f, acc[W] = {};
     for (int p0 = 0; p0 < np; p0 += 31) {
         const int n = min(31, np - p0);
-        const int64_t first = (static_cast<int64_t>(c0 + p0) + pit) * 128 + prow % 128;   // parts are 128 rows apart
+        const int64_t first = (static_cast<int64_t>(c0 + p0) + pit) * rpi + prow % rpi;   // parts are rpi rows apart
         float pm = -INFINITY, pl = 0.0f;
         if (lane == 0) {
             if (p0 == 0) {
@@ -678,7 +679,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
                 pl = l;
             }
         } else if (lane <= n) {
-            const float4 x = *reinterpret_cast<const float4*>(a.pml + (first + 128 * (lane - 1)) * 4);
+            const float4 x = *reinterpret_cast<const float4*>(a.pml + (first + rpi * (lane - 1)) * 4);
             pm = x.x;
             pl = x.y + x.z;
         }
@@ -695,7 +696,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
         for (int e = 0; e < W; ++e) acc[e] = (p0 == 0 ? own[e] : acc[e]) * w0;
 #pragma unroll 4
         for (int c = 0; c < n; ++c) {
-            const float* src = a.po + (first + 128 * c) * D + W * lane;
+            const float* src = a.po + (first + rpi * c) * D + W * lane;
             const float wc = __shfl_sync(0xffffffffu, w, c + 1);
             float v[W];
             if constexpr (W == 2) {
@@ -746,6 +747,78 @@ struct PrefixLayout {
     static constexpr uint32_t SMEM = OFF_HOLD + 16 + 1024;
     static constexpr uint32_t TMEM_COLS = 512, O_COL = 256;    // two 128-column score buffers, then O
     static_assert(SMEM <= 232448, "shared-memory budget");
+};
+
+// A whole 32-byte sector per thread.
+__device__ __forceinline__ void st_v8(float* p, const float* v) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])),
+                 "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
+                 "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
+                 : "memory");
+}
+
+// Query rows qrow0 .. qrow0 + 127 of a key/value head into a swizzled tile, by THREADS threads (tid their number).
+// Row x of a head is query head `head * group + x % group` of sequence x / group; rows past the batch are zeros.
+// All of a thread's loads are under way before the first is stored: one at a time, they took 10 us of a call.
+template <typename T, int D, int THREADS>
+__device__ __forceinline__ void load_q_tile(uint8_t* tile, int head, int qrow0, int tid, const PagedArgs& a) {
+    constexpr int PER = 128 * (D / 8) / THREADS, STEP = THREADS / (D / 8);   // vectors of a thread, rows apart
+    uint4 x[PER];
+    int row = qrow0 + tid / (D / 8), b = row / a.group, g = row - b * a.group;
+    const int step_b = STEP / a.group, step_g = STEP - step_b * a.group;      // no division per vector
+    const T* q = static_cast<const T*>(a.q) + head * a.group * D + 8 * (tid % (D / 8));
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        x[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (row < a.batch * a.group) x[i] = __ldg(reinterpret_cast<const uint4*>(q + (static_cast<int64_t>(b) * a.hq + g) * D));
+        row += STEP;
+        b += step_b;
+        g += step_g;
+        if (g >= a.group) {
+            g -= a.group;
+            ++b;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int v = tid + i * THREADS, k = v / (D / 8), ch = v % (D / 8);
+        *reinterpret_cast<uint4*>(tile + (ch / 8) * (128 * 128) + k * 128 + (((ch % 8) ^ (k & 7)) << 4)) = x[i];
+    }
+}
+
+// Loads 128-key K or V tiles, by one warp.  A tile is 128 / box boxes of one page each.
+template <int D>
+struct PrefixLoader {
+    const PagedArgs& a;
+    const int lane, box_shift;
+    const uint32_t one;
+    int head = 0, page = 0;
+    __device__ __forceinline__ PrefixLoader(const PagedArgs& args, int l)
+        : a(args), lane(l), box_shift(min(args.page_shift, 7)), one(elect_one()) {}
+    // Read this lane's page of a tile from the table; load() uses it.
+    __device__ __forceinline__ void look(int tile) {
+        const int key = tile * 128 + (lane << box_shift);
+        if (lane << box_shift < 128 && key < a.plen) page = a.ptable[key >> a.page_shift];
+    }
+    __device__ __forceinline__ void load(const CUtensorMap* map, uint32_t dst, uint32_t full, int tile) {
+        const int nk = min(128, a.plen - tile * 128), nbox = (nk + (1 << box_shift) - 1) >> box_shift;
+        int row = a.cache_rows;         // past the cache: zeros
+        if (lane < nbox) {
+            const int key = tile * 128 + (lane << box_shift);
+            if (page >= 0 && page < a.num_pages)
+                row = ((page * a.hk + head) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+            else
+                atomicExch(a.bad, 1);
+        }
+        if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(nbox << box_shift) * (D * 2));
+        __syncwarp();
+        for (int y = 0; y < nbox; ++y) {
+            const int r = __shfl_sync(0xffffffffu, row, y);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+                tma_load_2d_if(one, dst + c * (128 * 128) + ((static_cast<uint32_t>(y) << box_shift) * 128), map, 64 * c, r, full);
+        }
+    }
 };
 
 // One CTA per SM walks an equal run of (128-row tile of a key/value head, 128-key tile) pairs.  Per row
@@ -799,49 +872,27 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix_kernel(const __gr
     const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(gbase + L::OFF_HOLD), 0);
     pdl_wait();
 
-    const int64_t U = static_cast<int64_t>(a.hk) * a.prt * a.ptiles;
-    const int64_t u0 = blockIdx.x * U / gridDim.x, u1 = (blockIdx.x + 1) * U / gridDim.x;
+    const int64_t U = static_cast<int64_t>(a.hk) * a.prt * a.ptiles;     // below 2^31
+    const int u0 = static_cast<int>(blockIdx.x * U / gridDim.x), u1 = static_cast<int>((blockIdx.x + 1) * U / gridDim.x);
     auto keys_of = [&](int tile) { return min(128, a.plen - tile * 128); };
 
     if (warp == 0 || warp == 2) {
-        // ---------------------------------------------------------------- K and V loads
-        // a tile is 128 / box boxes of one page each, loaded by one lane each
+        // ---------------------------------------------------------------- K loads; V loads
         const bool is_k = warp == 0;
         const CUtensorMap* map = is_k ? &mK : &mV;
-        const int box_shift = min(a.page_shift, 7);
-        const uint32_t one = elect_one();
         if (lane == 0) prefetch_map(map);
+        PrefixLoader<D> ld(a, lane);
         int i = 0;
-        const int total = static_cast<int>(u1 - u0);
+        const int total = u1 - u0;
         for (; i < total; ++i) {
-            const int64_t u = u0 + i;
-            const int tile = static_cast<int>(u % a.ptiles), head = static_cast<int>(u / a.ptiles) / a.prt;
-            const int st = i % KV;
-            const uint32_t full = is_k ? k_full(st) : v_full(st), empty = is_k ? k_empty(st) : v_empty(st);
-            const int nbox = (keys_of(tile) + (1 << box_shift) - 1) >> box_shift;
-            int row = a.cache_rows;
-            if (lane < nbox) {
-                const int key = tile * 128 + (lane << box_shift);
-                const int page = a.ptable[key >> a.page_shift];
-                if (page >= 0 && page < a.num_pages)
-                    row = ((page * a.hk + head) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
-                else
-                    atomicExch(a.bad, 1);
-            }
-            if (i >= KV && !__all_sync(0xffffffffu, mbar_wait_bounded(empty, ((i - KV) / KV) & 1, flag))) break;
-            if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(nbox << box_shift) * (D * 2));
-            __syncwarp();
-            const uint32_t dst = base + (is_k ? L::OFF_K : L::OFF_V) + st * L::TILE;
-            for (int y = 0; y < nbox; ++y) {
-                const int r = __shfl_sync(0xffffffffu, row, y);
-#pragma unroll
-                for (int c = 0; c < L::ATOMS; ++c)
-                    tma_load_2d_if(one, dst + c * L::REGION + ((static_cast<uint32_t>(y) << box_shift) * 128), map, 64 * c, r, full);
-            }
+            const int tile = (u0 + i) % a.ptiles, st = i % KV;
+            ld.head = (u0 + i) / a.ptiles / a.prt;
+            ld.look(tile);
+            if (i >= KV && !__all_sync(0xffffffffu, mbar_wait_bounded(is_k ? k_empty(st) : v_empty(st), ((i - KV) / KV) & 1, flag))) break;
+            ld.load(map, base + (is_k ? L::OFF_K : L::OFF_V) + st * L::TILE, is_k ? k_full(st) : v_full(st), tile);
         }
         if (i < total)   // copies in flight land before the shared memory goes away
-            for (int j = i - KV < 0 ? 0 : i - KV; j < i; ++j)
-                (void)mbar_wait_drain(is_k ? k_full(j % KV) : v_full(j % KV), (j / KV) & 1);
+            for (int j = max(0, i - KV); j < i; ++j) (void)mbar_wait_drain(is_k ? k_full(j % KV) : v_full(j % KV), (j / KV) & 1);
         __syncwarp();
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issue
@@ -883,8 +934,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix_kernel(const __gr
             issued = true;
         };
         int i = 0, seg = 0;
-        for (int64_t u = u0; ok && u < u1; ++seg) {
-            const int n = static_cast<int>(min(static_cast<int64_t>(a.ptiles) - u % a.ptiles, u1 - u));
+        for (int u = u0; ok && u < u1; ++seg) {
+            const int n = min(a.ptiles - u % a.ptiles, u1 - u);
             if (!wait(q_full, seg)) break;
             issue_s(i);
             for (int j = 0; ok && j < n; ++j) {
@@ -911,19 +962,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix_kernel(const __gr
         constexpr int HK = 64;
         bool ok = true;
         int i = 0;
-        for (int64_t u = u0; ok && u < u1;) {
-            const int item = static_cast<int>(u / a.ptiles), t0 = static_cast<int>(u % a.ptiles);
-            const int n = static_cast<int>(min(static_cast<int64_t>(a.ptiles) - t0, u1 - u));
+        for (int u = u0; ok && u < u1;) {
+            const int item = u / a.ptiles, t0 = u - item * a.ptiles;
+            const int n = min(a.ptiles - t0, u1 - u);
             const int head = item / a.prt, qrow0 = (item % a.prt) * 128;
-            // Q: row qrow0 + k of the head is query head `head * group + (..) % group` of sequence (..) / group.
             // The MMAs that read the previous tile's Q have completed (its last O was waited for).
-            for (int v = sid; v < 128 * (D / 8); v += 32 * kPreSoftmaxWarps) {
-                const int k = v / (D / 8), ch = v % (D / 8), row = qrow0 + k;
-                uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                if (row < total_rows)
-                    x = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (static_cast<int64_t>(row / a.group) * a.hq + head * a.group + row % a.group) * D + 8 * ch);
-                *reinterpret_cast<uint4*>(gbase + L::OFF_Q + (ch / 8) * L::REGION + k * 128 + (((ch % 8) ^ (k & 7)) << 4)) = x;
-            }
+            load_q_tile<T, D, 32 * kPreSoftmaxWarps>(gbase + L::OFF_Q, head, qrow0, sid, a);
             fence_async_smem();
             tc_fence_before();
             __syncwarp();
@@ -1040,8 +1084,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix_kernel(const __gr
                     tmem_ld_wait();
                     if (in)
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            *reinterpret_cast<float4*>(dst + 32 * k + 4 * e) = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        for (int e = 0; e < 4; ++e) st_v8(dst + 32 * k + 8 * e, o + 8 * e);
                 }
             }
             u += n;
@@ -1055,9 +1098,311 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix_kernel(const __gr
     }
 }
 
+// ------------------------------------------------------------------ two row tiles at a time
+// For more than 128 rows per key/value head and D <= 128: the CTA holds two row tiles (256 rows) against the
+// same K and V tiles, so every K and V byte serves twice as many rows, and while the softmax warps of one row
+// tile wait for the tensor core, those of the other work.  One softmax thread per row takes its 128 scores into
+// registers and gives the score buffer back at once, so S_t(j + 1) is computed while the thread works on
+// S_t(j).  P goes through shared memory.  K and V tiles share one ring of three tiles in the order of their use,
+// K(0) K(1) V(0) K(2) V(1) ...; the MMA warp issues S_0(j + 1), PV_1(j - 1), S_1(j + 1), PV_0(j), with row tile
+// 1 half a step behind row tile 0.
+// (P in TMEM over the scores it was made from, which leaves room for two stages of K and of V: S_t(j + 1) then
+// waits for PV_t(j), and a step of 256 x 128 took 3000 cycles.)
+template <int D>
+struct Prefix2Layout {
+    static constexpr int ATOMS = D / 64;
+    static constexpr int RING = D == 64 ? 6 : 3;               // K and V tiles
+    static constexpr uint32_t REGION = 128 * 128;
+    static constexpr uint32_t TILE = REGION * ATOMS;
+    static constexpr uint32_t P_BYTES = 128 * 128 * 2;
+    static constexpr uint32_t OFF_Q = 0;                       // two tiles
+    static constexpr uint32_t OFF_KV = 2 * TILE;
+    static constexpr uint32_t OFF_P = OFF_KV + RING * TILE;    // two tiles
+    static constexpr uint32_t OFF_BAR = OFF_P + 2 * P_BYTES;
+    static constexpr int N_BARS = 2 + 2 * RING + 8;
+    static constexpr uint32_t OFF_HOLD = OFF_BAR + N_BARS * 8;
+    static constexpr uint32_t SMEM = OFF_HOLD + 16 + 1024;
+    static constexpr uint32_t TMEM_COLS = 512, O_COL = 256;    // scores of tile t at 128 t, output at 256 + D t
+    static_assert(SMEM <= 232448, "shared-memory budget");
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kPreThreads, 1) paged_prefix2_kernel(const __grid_constant__ CUtensorMap mK,
+                                                                       const __grid_constant__ CUtensorMap mV,
+                                                                       const __grid_constant__ PagedArgs a) {
+    using L = Prefix2Layout<D>;
+    constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
+    constexpr int RING = L::RING;
+    pdl_trigger();
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    uint8_t* gbase = smem_raw + (base - smem_addr(smem_raw));
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
+    const uint32_t bar0 = base + L::OFF_BAR;
+    const uint32_t q_full = bar0, drain = bar0 + 8;
+    auto full = [&](int i) { return bar0 + 8u * (2 + i); };
+    auto empty = [&](int i) { return bar0 + 8u * (2 + RING + i); };
+    auto s_full = [&](int t) { return bar0 + 8u * (2 + 2 * RING + t); };
+    auto s_free = [&](int t) { return bar0 + 8u * (4 + 2 * RING + t); };
+    auto p_full = [&](int t) { return bar0 + 8u * (6 + 2 * RING + t); };
+    auto o_done = [&](int t) { return bar0 + 8u * (8 + 2 * RING + t); };
+    int* flag = a.flag;
+    if (threadIdx.x == 0) {
+        mbar_init(q_full, kPreSoftmaxWarps);
+        mbar_init(drain, 1);
+        for (int i = 0; i < RING; ++i) {
+            mbar_init(full(i), 1);
+            mbar_init(empty(i), 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(s_full(t), 1);
+            mbar_init(s_free(t), kPreSoftmaxWarps / 2);
+            mbar_init(p_full(t), kPreSoftmaxWarps / 2);
+            mbar_init(o_done(t), 1);
+        }
+        fence_mbar_init();
+    }
+    if (warp == 1) tmem_alloc(base + L::OFF_HOLD, L::TMEM_COLS);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(gbase + L::OFF_HOLD), 0);
+    pdl_wait();
+
+    const int64_t U = static_cast<int64_t>(a.hk) * a.prt * a.ptiles;     // below 2^31
+    const int u0 = static_cast<int>(blockIdx.x * U / gridDim.x), u1 = static_cast<int>((blockIdx.x + 1) * U / gridDim.x);
+    // Place of K tile j and V tile j of a segment of n in the segment's loads: K(0), then K(j + 1) before V(j).
+    auto k_at = [](int j) { return j == 0 ? 0 : 2 * j - 1; };
+    auto v_at = [](int j, int n) { return j + 1 < n ? 2 * j + 2 : 2 * j + 1; };
+
+    if (warp == 0) {
+        // ---------------------------------------------------------------- K and V loads
+        if (lane == 0) {
+            prefetch_map(&mK);
+            prefetch_map(&mV);
+        }
+        PrefixLoader<D> ld(a, lane);
+        int c = 0, slot = 0;             // loads so far, and the next one's slot
+        uint32_t phase = 1;              // of the wait for it to be empty
+        bool ok = true;
+        for (int u = u0; ok && u < u1;) {
+            const int item = u / a.ptiles, t0 = u - item * a.ptiles;
+            const int n = min(a.ptiles - t0, u1 - u);
+            ld.head = item / a.prt;
+            for (int x = 0; x < 2 * n; ++x, ++c) {
+                // x-th load of the segment: K for 0 and odd x below 2 n - 1, V for the others
+                const bool is_k = x == 0 || (x % 2 == 1 && x < 2 * n - 1);
+                const int j = is_k ? (x + 1) / 2 : (x == 2 * n - 1 ? n - 1 : x / 2 - 1);
+                ld.look(t0 + j);
+                if (c >= RING) {
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty(slot), phase, flag));
+                    if (!ok) break;
+                }
+                ld.load(is_k ? &mK : &mV, base + L::OFF_KV + slot * L::TILE, full(slot), t0 + j);
+                if (++slot == RING) {
+                    slot = 0;
+                    phase ^= 1u;
+                }
+            }
+            u += n;
+        }
+        if (!ok)   // copies in flight land before the shared memory goes away
+            for (int j = max(0, c - RING); j < c; ++j) (void)mbar_wait_drain(full(j % RING), (j / RING) & 1);
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- MMA issue
+        constexpr uint32_t idS = idesc_f16(128, 128, false, false, BF);
+        constexpr uint32_t idO = idesc_f16(128, D, false, true, BF);
+        const uint32_t one = elect_one();
+        const uint64_t dq = smem_desc_sw128(base + L::OFF_Q, 16, 1024), dk = smem_desc_sw128(base + L::OFF_KV, 16, 1024);
+        const uint64_t dp = smem_desc_sw128(base + L::OFF_P, 16, 1024), dv = smem_desc_sw128(base + L::OFF_KV, L::REGION, 1024);
+        bool issued = false, ok = true;
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity & 1u, flag));
+            return ok;
+        };
+        // i: steps before this one (parities of the tile's barriers); c: the K or V tile's number among all loads
+        auto issue_s = [&](int t, int i, int c) {
+            if (i > 0 && !wait(s_free(t), i - 1)) return;
+            if (t == 0 && !wait(full(c % RING), c / RING)) return;     // row tile 1 comes second
+            tc_fence_after();
+            const uint64_t kd = dk + static_cast<uint64_t>((c % RING) * (L::TILE >> 4)), qd = dq + static_cast<uint64_t>(t * (L::TILE >> 4));
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s)
+                tc_mma_if(one, tmem + t * 128, qd + ((s / 4) * (L::REGION >> 4) + (s % 4) * 2), kd + ((s / 4) * (L::REGION >> 4) + (s % 4) * 2),
+                          idS, s > 0 ? 1u : 0u);
+            tc_commit_if(one, s_full(t));
+            if (t == 1) tc_commit_if(one, empty(c % RING));
+            issued = true;
+        };
+        auto issue_pv = [&](int t, int i, int c, bool first) {
+            if (!wait(p_full(t), i)) return;
+            if (t == 0 && !wait(full(c % RING), c / RING)) return;
+            tc_fence_after();
+            const uint64_t vd = dv + static_cast<uint64_t>((c % RING) * (L::TILE >> 4)), pd = dp + static_cast<uint64_t>(t * (L::P_BYTES >> 4));
+#pragma unroll
+            for (int s = 0; s < 8; ++s)   // 16 keys each
+                tc_mma_if(one, tmem + L::O_COL + t * D, pd + ((s / 4) * (L::REGION >> 4) + (s % 4) * 2), vd + s * (2048 >> 4), idO,
+                          !first || s > 0 ? 1u : 0u);
+            tc_commit_if(one, o_done(t));
+            if (t == 1) tc_commit_if(one, empty(c % RING));
+            issued = true;
+        };
+        int i = 0, c = 0, seg = 0;
+        for (int u = u0; ok && u < u1; ++seg) {
+            const int n = min(a.ptiles - u % a.ptiles, u1 - u);
+            if (!wait(q_full, seg)) break;
+            issue_s(0, i, c);
+            if (ok) issue_s(1, i, c);
+            for (int j = 0; ok && j < n; ++j) {
+                if (j + 1 < n) issue_s(0, i + j + 1, c + k_at(j + 1));
+                if (ok && j > 0) issue_pv(1, i + j - 1, c + v_at(j - 1, n), j == 1);
+                if (ok && j + 1 < n) issue_s(1, i + j + 1, c + k_at(j + 1));
+                if (ok) issue_pv(0, i + j, c + v_at(j, n), j == 0);
+            }
+            if (ok) issue_pv(1, i + n - 1, c + v_at(n - 1, n), n == 1);
+            i += n;
+            c += 2 * n;
+            u += n;
+        }
+        if (!ok && issued) {   // MMAs in flight finish before TMEM is freed
+            tc_commit_if(one, drain);
+            (void)mbar_wait_drain(drain, 0);
+        }
+        __syncwarp();
+    } else if (warp >= 3) {
+        // ---------------------------------------------------------------- softmax: thread r of tile t, one row
+        const int t = (warp - 3) / 4, r = 32 * (warp % 4) + lane;
+        const uint32_t lanes = static_cast<uint32_t>(32 * (warp % 4)) << 16;
+        const uint32_t st = tmem + lanes + t * 128, ot = tmem + lanes + L::O_COL + t * D;
+        const int total_rows = a.batch * a.group;
+        constexpr float SH = Shift<T>::V;
+        bool ok = true;
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity & 1u, flag));
+            return ok;
+        };
+        int i = 0, c = 0;
+        for (int u = u0; ok && u < u1;) {
+            const int item = u / a.ptiles, t0 = u - item * a.ptiles;
+            const int n = min(a.ptiles - t0, u1 - u);
+            const int head = item / a.prt, qrow0 = (item % a.prt) * 256 + t * 128;
+            // this tile's Q, by its own warps: the MMAs that read the last one have completed
+            load_q_tile<T, D, 32 * kPreSoftmaxWarps / 2>(gbase + L::OFF_Q + t * L::TILE, head, qrow0, r, a);
+            fence_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
+            float m = -INFINITY, l = 0.0f;
+            for (int j = 0; j < n; ++j, ++i) {
+                const int nk = min(128, a.plen - (t0 + j) * 128);
+                if (!wait(s_full(t), i)) break;
+                tc_fence_after();
+                float x[128];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) tmem_ld32(st + 32 * k, x + 32 * k);
+                tmem_ld_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s_free(t));
+                if (nk < 128) {          // keys past the prefix's end
+#pragma unroll
+                    for (int k = 0; k < 128; ++k) x[k] = k >= nk ? -INFINITY : x[k];
+                }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int k = 0; k < 128; k += 2) mx[(k >> 1) & 3] = max3f(mx[(k >> 1) & 3], x[k], x[k + 1]);
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.c;
+                float alpha = 1.0f;
+                bool rescale = false;
+                if (top > m + (SH + kLag)) {
+                    if (j > 0) {
+                        alpha = ex2f(m - (top - SH));
+                        rescale = true;
+                    }
+                    m = top - SH;
+                }
+                // P and O are free once the previous PV has completed
+                if (i > 0 && !wait(o_done(t), i - 1)) break;
+                const float ref = m == -INFINITY ? 0.0f : m;
+                const float2 c2 = make_float2(a.c, a.c), nm2 = make_float2(-ref, -ref);
+                float2 sum2 = make_float2(0.0f, 0.0f);
+                uint8_t* prow = gbase + L::OFF_P + t * L::P_BYTES + r * 128;
+#pragma unroll
+                for (int q = 0; q < 16; ++q) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 e = __ffma2_rn(make_float2(x[8 * q + 2 * k], x[8 * q + 2 * k + 1]), c2, nm2);
+                        const float2 p = make_float2(ex2f(e.x), ex2f(e.y));
+                        sum2 = __fadd2_rn(sum2, p);
+                        w[k] = pack2<T>(p.x, p.y);
+                    }
+                    *reinterpret_cast<uint4*>(prow + (q / 8) * L::REGION + (((q % 8) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                l = l * alpha + (sum2.x + sum2.y);
+                if (__any_sync(0xffffffffu, rescale)) {
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int k = 0; k < D / 32; ++k) {
+                        float o[32];
+                        tmem_ld32(ot + 32 * k, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] *= alpha;
+                        tmem_st32(ot + 32 * k, o);
+                    }
+                    tmem_st_wait();
+                }
+                if (nk < 128 && t == 0) {   // V rows past the end: 0 x whatever lies there must be 0
+                    const int cv = c + v_at(j, n);      // (row tile 1's PV is issued after row tile 0's)
+                    if (!wait(full(cv % RING), cv / RING)) break;
+                    uint8_t* vb = gbase + L::OFF_KV + (cv % RING) * L::TILE;
+                    for (int v = r; v < (128 - nk) * L::ATOMS * 8; v += 128) {
+                        const int row = nk + v / (L::ATOMS * 8), ch = v % (L::ATOMS * 8);
+                        *reinterpret_cast<uint4*>(vb + (ch / 8) * L::REGION + row * 128 + (ch % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+                fence_async_smem();      // the generic-proxy writes become visible to the tensor core
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full(t));
+            }
+            if (ok && wait(o_done(t), i - 1)) {
+                tc_fence_after();
+                const int64_t at = (static_cast<int64_t>(blockIdx.x) + item) * 256 + t * 128 + r;
+                const bool in = qrow0 + r < total_rows;
+                if (in) *reinterpret_cast<float4*>(a.pml + at * 4) = make_float4(m, l, 0.0f, 0.0f);
+                float* dst = a.po + at * D;
+#pragma unroll 1
+                for (int k = 0; k < D / 32; ++k) {
+                    float o[32];
+                    tmem_ld32(ot + 32 * k, o);
+                    tmem_ld_wait();
+                    if (in)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) st_v8(dst + 32 * k + 8 * e, o + 8 * e);
+                }
+            }
+            u += n;
+            c += 2 * n;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, L::TMEM_COLS);
+    }
+}
+
 // ================================================================== host side
+// Rows of the prefix kernel's items: two tiles where there are more rows than one tile's and TMEM holds two outputs
+// next to two tiles of scores.
+int64_t prefix_rows(int64_t rows, int64_t D) { return rows > 128 && D <= 128 ? 256 : 128; }
+
 struct Sizes {
-    int64_t rows, pitems;            // rows per part of own keys; prefix row tiles
+    int64_t rows, prow, pitems;      // rows per part of own keys; of the prefix, and its items
     size_t count, oml, oo, rml, ro, pml, po;  // byte offsets of the workspace's parts
     size_t bytes;
 };
@@ -1065,7 +1410,8 @@ Sizes sizes(int64_t batch, int64_t hq, int64_t hk, int64_t D, int64_t plen) {
     Sizes s{};
     const int64_t group = hq / hk;
     s.rows = group < 16 ? group : 16;
-    s.pitems = plen > 0 ? hk * ceil_div(batch * group, 128) : 0;
+    s.prow = prefix_rows(batch * group, D);
+    s.pitems = plen > 0 ? hk * ceil_div(batch * group, s.prow) : 0;
     size_t at = 0;
     auto part = [&](int64_t n) {
         const size_t was = at;
@@ -1078,8 +1424,8 @@ Sizes sizes(int64_t batch, int64_t hq, int64_t hk, int64_t D, int64_t plen) {
     if (plen > 0) {
         s.rml = part(batch * hq * 8);
         s.ro = part(batch * hq * D * 4);
-        s.pml = part((kPrefixGrid + s.pitems) * 128 * 16);
-        s.po = part((kPrefixGrid + s.pitems) * 128 * D * 4);
+        s.pml = part((kPrefixGrid + s.pitems) * s.prow * 16);
+        s.po = part((kPrefixGrid + s.pitems) * s.prow * D * 4);
     }
     s.bytes = at;
     return s;
@@ -1112,17 +1458,30 @@ int own_smem(PagedArgs* a, uint32_t* bytes, int* ctas) {
 }
 
 template <typename T, int D>
+int launch_prefix(const CUtensorMap& mK, const CUtensorMap& mV, const PagedArgs& a, cudaStream_t st) {
+    // at least 120 KB, so that one CTA runs per SM (each takes all of TMEM)
+    if constexpr (D <= 128) {
+        if (a.prow == 256) {
+            constexpr int smem = Prefix2Layout<D>::SMEM > 120u * 1024u ? Prefix2Layout<D>::SMEM : 120u * 1024u;
+            const int rc = opt_in_smem((const void*)paged_prefix2_kernel<T, D>, smem);
+            if (rc != FUSE_OK) return rc;
+            return launch_pdl(paged_prefix2_kernel<T, D>, dim3(static_cast<unsigned>(a.pgrid)), dim3(kPreThreads), smem, st, 1, mK, mV, a);
+        }
+    }
+    constexpr int smem = PrefixLayout<D>::SMEM > 120u * 1024u ? PrefixLayout<D>::SMEM : 120u * 1024u;
+    const int rc = opt_in_smem((const void*)paged_prefix_kernel<T, D>, smem);
+    if (rc != FUSE_OK) return rc;
+    return launch_pdl(paged_prefix_kernel<T, D>, dim3(static_cast<unsigned>(a.pgrid)), dim3(kPreThreads), smem, st, 1, mK, mV, a);
+}
+
+template <typename T, int D>
 int run_paged(PagedArgs a, const void* k, const void* v, cudaStream_t st) {
     const bool bf = std::is_same<T, __nv_bfloat16>::value;
     CUtensorMap mQ, mK, mV, mK16, mV16;
     if (a.plen > 0) {
         const int box = 1 << (a.page_shift < 7 ? a.page_shift : 7);
         if (!make_map(&mK, k, a.cache_rows, D, 64, box, bf) || !make_map(&mV, v, a.cache_rows, D, 64, box, bf)) return FUSE_ECUDA;
-        constexpr int smem = PrefixLayout<D>::SMEM > 120u * 1024u ? PrefixLayout<D>::SMEM : 120u * 1024u;
-        int rc = opt_in_smem((const void*)paged_prefix_kernel<T, D>, smem);
-        if (rc != FUSE_OK) return rc;
-        rc = launch_pdl(paged_prefix_kernel<T, D>, dim3(static_cast<unsigned>(a.pgrid)), dim3(kPreThreads), smem, st, 1, mK, mV, a);
-        if (rc != FUSE_OK) return rc;
+        if (const int rc = launch_prefix<T, D>(mK, mV, a, st); rc != FUSE_OK) return rc;
     }
     const int box = 1 << (a.page_shift < 6 ? a.page_shift : 6);
     if (!make_map(&mQ, a.q, static_cast<int64_t>(a.batch) * a.hq, D, 64, a.rows, bf) || !make_map(&mK, k, a.cache_rows, D, 64, box, bf) ||
@@ -1149,7 +1508,7 @@ int run_paged(PagedArgs a, const void* k, const void* v, cudaStream_t st) {
 
 }  // namespace
 
-int paged_report_count() { return 18; }
+int paged_report_count() { return 22; }
 int paged_report(int i, fuse_kernel_record* out) {
     const int smem_own = 111 * 1024;
     switch (i) {
@@ -1175,6 +1534,12 @@ int paged_report(int i, fuse_kernel_record* out) {
         FC_JOIN(16, __half, "f16", 128);
         FC_JOIN(17, __half, "f16", 256);
 #undef FC_JOIN
+#define FC_PRE2(N, T, TN, D) case N: return describe_kernel((const void*)paged_prefix2_kernel<T, D>, "paged_prefix2_kernel<" TN ", D=" #D "> (shared prefix, 256 rows)", kPreThreads, Prefix2Layout<D>::SMEM, out, Prefix2Layout<D>::TMEM_COLS)
+        FC_PRE2(18, __nv_bfloat16, "bf16", 64);
+        FC_PRE2(19, __nv_bfloat16, "bf16", 128);
+        FC_PRE2(20, __half, "f16", 64);
+        FC_PRE2(21, __half, "f16", 128);
+#undef FC_PRE2
 #undef FC_OWN
 #undef FC_PRE
         default: return FUSE_EINVAL;
@@ -1253,7 +1618,8 @@ extern "C" int fuse_paged_attention(const void* q, const void* k_cache, const vo
     a.plen = static_cast<int>(prefix_len);
     if (prefix_len > 0) {
         a.ptiles = static_cast<int>(ceil_div(prefix_len, 128));
-        a.prt = static_cast<int>(ceil_div(batch * group, 128));
+        a.prow = static_cast<int>(s.prow);
+        a.prt = static_cast<int>(ceil_div(batch * group, s.prow));
         const int64_t units = static_cast<int64_t>(a.hk) * a.prt * a.ptiles;
         int64_t grid = sm_count() < kPrefixGrid ? sm_count() : kPrefixGrid;
         a.pgrid = static_cast<int>(grid < units ? grid : units);
