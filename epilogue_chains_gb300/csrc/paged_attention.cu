@@ -38,7 +38,6 @@ constexpr int kOwnThreads = 32 * (kOwnWarps + 1); // the last warp loads
 constexpr int kChunk = 16;                        // keys of a warp per unit
 constexpr int kUnit = kChunk * kOwnWarps;         // keys of a unit
 constexpr int kOwnSlots = 8;                       // most ring slots
-constexpr int kOwnQ = 4;                          // buffers of query rows
 constexpr int kOwnGrid = 320;                     // most CTAs of paged_own_kernel (workspace bound)
 constexpr int kCounterBytes = 8192;
 static_assert(kOwnGrid * kOwnWarps * 4 <= kCounterBytes, "one counter per CTA and warp");
@@ -132,7 +131,9 @@ struct OwnLayout {
     static constexpr uint32_t QSLOT = QATOM * ATOMS;
     // D = 256 leaves no registers to hold the query rows next to the output; they are read again from
     // shared memory for every unit
-    static constexpr bool Q_REGS = D <= 128;
+    static constexpr bool Q_REGS = true || D <= 128;
+    static constexpr int CTAS = D <= 128 ? 2 : 1;                // CTAs per SM
+    static constexpr int NQ = D <= 128 ? 4 : 2;                  // buffers of query rows
 };
 
 // What is dealt out to the CTAs are places in one line: per item, that is sequence and row tile of a key/value
@@ -152,7 +153,7 @@ __device__ __forceinline__ int places_of(int len) { return 1 + (len > kUnit ? (l
 // Under load a dependent read of global memory takes several microseconds (the ring keeps the memory queues
 // full), which is why nothing else reads global memory inside the loop.
 template <typename T, int D>
-__global__ void __launch_bounds__(kOwnThreads, 2) paged_own_kernel(
+__global__ void __launch_bounds__(kOwnThreads, OwnLayout<D>::CTAS) paged_own_kernel(
     const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
     const __grid_constant__ CUtensorMap mV, const __grid_constant__ CUtensorMap mK16,
     const __grid_constant__ CUtensorMap mV16, const __grid_constant__ PagedArgs a) {
@@ -169,16 +170,16 @@ __global__ void __launch_bounds__(kOwnThreads, 2) paged_own_kernel(
     auto full = [&](int i) { return bars + 8u * i; };
     auto empty = [&](int i) { return bars + 8u * (kOwnSlots + i); };
     auto q_full = [&](int i) { return bars + 8u * (2 * kOwnSlots + i); };
-    auto q_empty = [&](int i) { return bars + 8u * (2 * kOwnSlots + kOwnQ + i); };
+    auto q_empty = [&](int i) { return bars + 8u * (2 * kOwnSlots + L::NQ + i); };
     // parts of run r in buffer r % 2, filled and joined by all computing warps
-    auto parts_full = [&](int i) { return bars + 8u * (2 * kOwnSlots + 2 * kOwnQ + i); };
-    auto parts_free = [&](int i) { return bars + 8u * (2 * kOwnSlots + 2 * kOwnQ + 2 + i); };
+    auto parts_full = [&](int i) { return bars + 8u * (2 * kOwnSlots + 2 * L::NQ + i); };
+    auto parts_free = [&](int i) { return bars + 8u * (2 * kOwnSlots + 2 * L::NQ + 2 + i); };
     if (tid == 0) {
         for (int i = 0; i < a.slots; ++i) {
             mbar_init(full(i), 1);
             mbar_init(empty(i), kOwnWarps);
         }
-        for (int i = 0; i < kOwnQ; ++i) {
+        for (int i = 0; i < L::NQ; ++i) {
             mbar_init(q_full(i), 1);
             mbar_init(q_empty(i), kOwnWarps);
         }
@@ -191,7 +192,11 @@ __global__ void __launch_bounds__(kOwnThreads, 2) paged_own_kernel(
         prefetch_map(&mK);
         prefetch_map(&mV);
     }
-    pdl_wait();
+    // With a prefix, the kernel before this one is the prefix's, of which nothing is read here.  It lets this one
+    // start once it has itself waited for what came before, so CTAs of this kernel take over the SMs as the
+    // prefix's CTAs leave them; the wait is made up for at the end, for paged_join_kernel's sake.  (What is read
+    // by plain loads comes from L2, past anything an SM may still hold of earlier contents.)
+    if (a.plen == 0) pdl_wait();
 
     // ------------------------------------------------------------ places of every sequence
     {
@@ -199,7 +204,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2) paged_own_kernel(
         const int per = (a.batch + kOwnThreads - 1) / kOwnThreads, b0 = tid * per;
         int sum = 0;
         for (int b = b0; b < b0 + per && b < a.batch; ++b) {
-            int n = a.lens[b];
+            int n = __ldcg(a.lens + b);
             if (n < 0 || n > most) {
                 if (blockIdx.x == 0) atomicExch(a.bad, 1);
                 n = n < 0 ? 0 : static_cast<int>(most);
@@ -281,7 +286,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2) paged_own_kernel(
             for (int x = 0; x < 4; ++x)
                 if (x < p.boxes) {
                     const int key = k.j * kUnit + (x << p.shift);
-                    p.page[x] = a.table[k.b * a.table_ld + (key >> a.page_shift)];
+                    p.page[x] = __ldcg(a.table + k.b * a.table_ld + (key >> a.page_shift));
                     p.in[x] = (head << a.page_shift) + (key & ((1 << a.page_shift) - 1));
                 }
         };
@@ -312,13 +317,13 @@ __global__ void __launch_bounds__(kOwnThreads, 2) paged_own_kernel(
                 if (boxes > 0) {
                     const int qrow = __shfl_sync(0xffffffffu, cur.qrow, x), shift = __shfl_sync(0xffffffffu, cur.shift, x);
                     if (qrow >= 0) {
-                        if (qloads >= kOwnQ && !wait(q_empty(qs), qphase ^ 1u)) break;
+                        if (qloads >= L::NQ && !wait(q_empty(qs), qphase ^ 1u)) break;
                         if (lane == 0) mbar_arrive_expect_tx(q_full(qs), static_cast<uint32_t>(a.rows) * (D * 2));
                         __syncwarp();
 #pragma unroll
                         for (int i = 0; i < L::ATOMS; ++i) tma_load_2d_if(one, base + a.off_q + qs * L::QSLOT + i * L::QATOM, &mQ, 64 * i, qrow, q_full(qs));
                         ++qloads;
-                        if (++qs == kOwnQ) {
+                        if (++qs == L::NQ) {
                             qs = 0;
                             qphase ^= 1u;
                         }
@@ -357,8 +362,9 @@ __global__ void __launch_bounds__(kOwnThreads, 2) paged_own_kernel(
         }
         if (!ok) {   // after a wait that ran out: copies in flight land before the shared memory goes away
             for (int j = max(0, loads - a.slots); j < loads; ++j) (void)mbar_wait_drain(full(j % a.slots), (j / a.slots) & 1);
-            for (int j = max(0, qloads - kOwnQ); j < qloads; ++j) (void)mbar_wait_drain(q_full(j % kOwnQ), (j / kOwnQ) & 1);
+            for (int j = max(0, qloads - L::NQ); j < qloads; ++j) (void)mbar_wait_drain(q_full(j % L::NQ), (j / L::NQ) & 1);
         }
+        if (a.plen > 0) pdl_wait();      // this kernel is not over before the prefix's is
         return;
     }
 
@@ -492,7 +498,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2) paged_own_kernel(
         auto free_q = [&] {
             __syncwarp();
             if (lane == 0) mbar_arrive(q_empty(qs));
-            if (++qs == kOwnQ) {
+            if (++qs == L::NQ) {
                 qs = 0;
                 qphase ^= 1u;
             }
@@ -653,7 +659,7 @@ constexpr int kJoinThreads = 128;
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedArgs a) {
     constexpr int W = D / 32;
-    pdl_begin();
+    pdl_trigger();
     const int64_t row = static_cast<int64_t>(blockIdx.x) * (kJoinThreads / 32) + threadIdx.x / 32;
     const int lane = threadIdx.x % 32;
     if (row >= static_cast<int64_t>(a.batch) * a.hq) return;
@@ -663,23 +669,42 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     const int pit = head * a.prt + prow / rpi;
     const int64_t PU = static_cast<int64_t>(a.hk) * a.prt * a.ptiles, u = static_cast<int64_t>(pit) * a.ptiles;
     const int c0 = cta_of(u, PU, a.pgrid), np = cta_of(u + a.ptiles - 1, PU, a.pgrid) - c0 + 1;
-    // lane 0 has the row's own part, lanes 1 .. the prefix's; 31 of those at a time
-    float m = -INFINITY, l = 0.0f, acc[W] = {};
-    for (int p0 = 0; p0 < np; p0 += 31) {
-        const int n = min(31, np - p0);
-        const int64_t first = (static_cast<int64_t>(c0 + p0) + pit) * rpi + prow % rpi;   // parts are rpi rows apart
-        float pm = -INFINITY, pl = 0.0f;
-        if (lane == 0) {
-            if (p0 == 0) {
-                const float2 x = *reinterpret_cast<const float2*>(a.rml + 2 * row);
-                pm = x.x;
-                pl = x.y;
-            } else {
-                pm = m;      // what has been joined so far
-                pl = l;
+    pdl_wait();
+    // lane 0 has the row's own part (after that: what has been joined), lanes 1 .. kParts the prefix's.  The
+    // columns of a batch are loaded next to its maxima and sums, so one memory latency is waited for, not three.
+    constexpr int kParts = 7;
+    auto load = [&](float (&v)[W], const float* src) {
+        if constexpr (W == 2) {
+            const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+            v[0] = x.x;
+            v[1] = x.y;
+        } else {
+#pragma unroll
+            for (int e = 0; e < W; e += 4) {
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(src + e));
+                v[e] = x.x;
+                v[e + 1] = x.y;
+                v[e + 2] = x.z;
+                v[e + 3] = x.w;
             }
-        } else if (lane <= n) {
-            const float4 x = *reinterpret_cast<const float4*>(a.pml + (first + rpi * (lane - 1)) * 4);
+        }
+    };
+    float m = -INFINITY, l = 0.0f, acc[W];
+    load(acc, a.ro + row * D + W * lane);
+    if (lane == 0) {
+        const float2 x = __ldcg(reinterpret_cast<const float2*>(a.rml + 2 * row));
+        m = x.x;
+        l = x.y;
+    }
+    for (int p0 = 0; p0 < np; p0 += kParts) {
+        const int n = min(kParts, np - p0);
+        const int64_t first = (static_cast<int64_t>(c0 + p0) + pit) * rpi + prow % rpi;   // parts are rpi rows apart
+        float v[kParts][W];
+#pragma unroll
+        for (int c = 0; c < kParts; ++c) load(v[c], a.po + (first + rpi * min(c, n - 1)) * D + W * lane);
+        float pm = lane == 0 ? m : -INFINITY, pl = lane == 0 ? l : 0.0f;
+        if (lane >= 1 && lane <= n) {
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(a.pml + (first + rpi * (lane - 1)) * 4));
             pm = x.x;
             pl = x.y + x.z;
         }
@@ -691,30 +716,14 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         const float w0 = __shfl_sync(0xffffffffu, w, 0);
-        const float* own = a.ro + row * D + W * lane;
 #pragma unroll
-        for (int e = 0; e < W; ++e) acc[e] = (p0 == 0 ? own[e] : acc[e]) * w0;
-#pragma unroll 4
-        for (int c = 0; c < n; ++c) {
-            const float* src = a.po + (first + rpi * c) * D + W * lane;
+        for (int e = 0; e < W; ++e) acc[e] *= w0;
+#pragma unroll
+        for (int c = 0; c < kParts; ++c) {
             const float wc = __shfl_sync(0xffffffffu, w, c + 1);
-            float v[W];
-            if constexpr (W == 2) {
-                const float2 x = *reinterpret_cast<const float2*>(src);
-                v[0] = x.x;
-                v[1] = x.y;
-            } else {
+            if (c < n)
 #pragma unroll
-                for (int e = 0; e < W; e += 4) {
-                    const float4 x = *reinterpret_cast<const float4*>(src + e);
-                    v[e] = x.x;
-                    v[e + 1] = x.y;
-                    v[e + 2] = x.z;
-                    v[e + 3] = x.w;
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < W; ++e) acc[e] += wc * v[e];
+                for (int e = 0; e < W; ++e) acc[e] += wc * v[c][e];
         }
         m = top;
         l = sum;
@@ -831,7 +840,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix_kernel(const __gr
                                                                       const __grid_constant__ PagedArgs a) {
     using L = PrefixLayout<D>;
     constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
-    pdl_trigger();
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
     uint8_t* gbase = smem_raw + (base - smem_addr(smem_raw));
@@ -871,6 +879,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix_kernel(const __gr
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(gbase + L::OFF_HOLD), 0);
     pdl_wait();
+    pdl_trigger();   // only now: paged_own_kernel relies on it
 
     const int64_t U = static_cast<int64_t>(a.hk) * a.prt * a.ptiles;     // below 2^31
     const int u0 = static_cast<int>(blockIdx.x * U / gridDim.x), u1 = static_cast<int>((blockIdx.x + 1) * U / gridDim.x);
@@ -1133,7 +1142,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix2_kernel(const __g
     using L = Prefix2Layout<D>;
     constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
     constexpr int RING = L::RING;
-    pdl_trigger();
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
     uint8_t* gbase = smem_raw + (base - smem_addr(smem_raw));
@@ -1168,6 +1176,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix2_kernel(const __g
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(gbase + L::OFF_HOLD), 0);
     pdl_wait();
+    pdl_trigger();   // only now: paged_own_kernel relies on it
 
     const int64_t U = static_cast<int64_t>(a.hk) * a.prt * a.ptiles;     // below 2^31
     const int u0 = static_cast<int>(blockIdx.x * U / gridDim.x), u1 = static_cast<int>((blockIdx.x + 1) * U / gridDim.x);
@@ -1437,11 +1446,11 @@ template <int D>
 int own_smem(PagedArgs* a, uint32_t* bytes, int* ctas) {
     using L = OwnLayout<D>;
     const uint32_t om = static_cast<uint32_t>(2 * kOwnWarps * a->rows * D * 4), ml = 2 * kOwnWarps * 16 * 8;
-    const uint32_t bars = 8u * (2 * kOwnSlots + 2 * kOwnQ + 4);
-    const uint32_t pre = static_cast<uint32_t>(2 * a->batch + 1) * 4, q = kOwnQ * L::QSLOT;
+    const uint32_t bars = 8u * (2 * kOwnSlots + 2 * L::NQ + 4);
+    const uint32_t pre = static_cast<uint32_t>(2 * a->batch + 1) * 4, q = L::NQ * L::QSLOT;
     const uint32_t fixed = q + om + ml + bars + pre + 1024;
     int n = 0;
-    for (*ctas = 2;; --*ctas) {
+    for (*ctas = L::CTAS;; --*ctas) {
         const uint32_t budget = *ctas == 2 ? 112u * 1024u : static_cast<uint32_t>(kOwnSmem);
         n = fixed < budget ? static_cast<int>((budget - fixed) / L::SLOT) : 0;
         if (n * L::SLOT >= 64u * 1024u || *ctas == 1) break;
