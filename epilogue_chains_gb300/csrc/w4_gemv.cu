@@ -48,6 +48,7 @@ struct W4Args {
     int stages;
     int x_resident;    // X is loaded once per CTA, not with every stage
     uint32_t x_off;    // offset of X within a stage, or of the resident X
+    uint32_t s_off;    // of the scales within a stage
     uint32_t stage_bytes;
     uint32_t off_bar, off_red;
     int gelu;
@@ -87,15 +88,16 @@ __device__ __forceinline__ void unpack_word(uint32_t w, uint32_t zb, uint32_t (&
 // Synchronize the computing warps (the loading warp goes on).
 __device__ __forceinline__ void sync_compute() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kW4Warps) : "memory"); }
 
-template <typename T, int G, int NT>
-__global__ void __launch_bounds__(kW4Threads, NT <= 2 ? 3 : 1) w4_gemv_kernel(const __grid_constant__ CUtensorMap mW,
-                                                                                           const __grid_constant__ CUtensorMap mX,
-                                                                                           const __grid_constant__ W4Args a) {
+template <typename T, int G, int NT, bool TS>
+__global__ void __launch_bounds__(kW4Threads, NT <= 2 ? 3 : 1) w4_gemv_kernel(
+    const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX, const __grid_constant__ CUtensorMap mS,
+    const __grid_constant__ CUtensorMap mZ, const __grid_constant__ W4Args a) {
     constexpr int WR = NT, WK = kW4Warps / NT;
     constexpr int ROWS = 16 * WR, COLS = 8 * NT, PITCH = ROWS + 4;
     constexpr int WPG = G / 32;         // words of a lane per group
     constexpr int NG = 8 / WPG;         // groups per 256-k chunk
     constexpr int RED = WK * COLS * PITCH;      // floats of one buffer of partial sums
+    constexpr uint32_t SROW = WK * NG * 2;      // bytes of a row's scales in a stage; half as many of zero points
     pdl_trigger();
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
@@ -124,10 +126,12 @@ __global__ void __launch_bounds__(kW4Threads, NT <= 2 ? 3 : 1) w4_gemv_kernel(co
             if (iters > 0) {
                 prefetch_map(&mW);
                 prefetch_map(&mX);
+                if (TS) prefetch_map(&mS);
+                if (TS && a.z) prefetch_map(&mZ);
             }
             pdl_wait();
             const uint32_t x_bytes = 4u * WK * a.M * 128u;
-            const uint32_t bytes = WK * ROWS * 128u + (a.x_resident ? 0u : x_bytes);
+            const uint32_t bytes = WK * ROWS * 128u + (a.x_resident ? 0u : x_bytes) + (TS ? ROWS * SROW : 0u) + (TS && a.z ? ROWS * SROW / 2 : 0u);
             int s = 0, loads = 0;
             uint32_t phase = 0;      // completions of the current stage's barriers so far, mod 2
             bool ok = true;
@@ -147,6 +151,8 @@ __global__ void __launch_bounds__(kW4Threads, NT <= 2 ? 3 : 1) w4_gemv_kernel(co
                     mbar_arrive_expect_tx(full(s), bytes);
                     tma_load_3d(base + s * a.stage_bytes, &mW, 0, tile * ROWS, kb, full(s));
                     if (!a.x_resident) tma_load_3d(base + s * a.stage_bytes + a.x_off, &mX, 0, 0, 4 * kb, full(s));
+                    if (TS) tma_load_3d(base + s * a.stage_bytes + a.s_off, &mS, kb * NG, tile * ROWS, 0, full(s));
+                    if (TS && a.z) tma_load_3d(base + s * a.stage_bytes + a.s_off + ROWS * SROW, &mZ, kb * NG, tile * ROWS, 0, full(s));
                     ++loads;
                     if (++s == a.stages) {
                         s = 0;
@@ -189,7 +195,7 @@ __global__ void __launch_bounds__(kW4Threads, NT <= 2 ? 3 : 1) w4_gemv_kernel(co
         // Scales and zero points: the four lanes of a row load one group each (two for groups of 32) and share by
         // shuffles; one word of two scales and one of two zero points (rows g, g + 8) per lane and group, a block
         // of stages ahead of its use (across row tiles).
-        constexpr int SB = NG < 4 ? 4 / NG : 1;    // stages of a block
+        constexpr int SB = TS ? 1 : NG < 4 ? 4 / NG : 1;    // stages of a block
         constexpr int SW = NG < 4 ? 1 : NG / 4;    // words of a lane per block
         const int gstep = a.split * WK * NG;       // groups from a stage to the next
         const int gfirst = (rank * WK + wk) * NG + (NG < 4 ? t / NG * gstep + t % NG : t);
@@ -212,10 +218,9 @@ __global__ void __launch_bounds__(kW4Threads, NT <= 2 ? 3 : 1) w4_gemv_kernel(co
             for (int i = 0; i < SW; ++i) load_scale(tile, gi + 4 * i, sc[i], zp[i]);
         };
         // one group: WPG words of each row against the matching X pieces
-        auto group = [&](int gi, const uint32_t* wl, const uint32_t* wh, auto&& xpiece, uint32_t sc, uint32_t zp) {
+        auto group = [&](int gi, const uint32_t* wl, const uint32_t* wh, auto&& xpiece, float2 s2, uint32_t zl, uint32_t zh) {
             float part[NT][4] = {};
-            const uint32_t bl = Nib<T>::MAGIC | __byte_perm(zp, 0u, 0x1010), bh = Nib<T>::MAGIC | __byte_perm(zp, 0u, 0x3232);
-            const float2 s2 = unpack2<T>(sc);
+            const uint32_t bl = Nib<T>::MAGIC | zl, bh = Nib<T>::MAGIC | zh;      // a row's zero point, twice
             const float sl = s2.x, sh = s2.y;
 #pragma unroll
             for (int w = 0; w < WPG; ++w) {
@@ -255,7 +260,11 @@ __global__ void __launch_bounds__(kW4Threads, NT <= 2 ? 3 : 1) w4_gemv_kernel(co
         const uint32_t woff = static_cast<uint32_t>((wk * ROWS + 16 * wr + g) * 128), wsw = static_cast<uint32_t>(g & 7) << 4;
         const uint32_t x_step = a.x_resident ? 4u * WK * a.M * 128u : 0u;
         uint32_t sc_next[SW], zp_next[SW], sc[SW] = {}, zp[SW] = {};
-        load_scales(tile0, gfirst, sc_next, zp_next);
+        if (!TS) load_scales(tile0, gfirst, sc_next, zp_next);
+        // this lane's scales within a stage: row g (rows of 128 and 64 bytes swizzled), the warp's first group
+        const uint32_t srow = static_cast<uint32_t>(16 * wr + g) * SROW + wk * (NG * 2);
+        const uint32_t soff = srow ^ (G == 32 ? (srow >> 3) & 0x70u : G == 64 ? (srow >> 3) & 0x30u : 0u);
+        const uint32_t zoff = ROWS * SROW + static_cast<uint32_t>(16 * wr + g) * (SROW / 2) + wk * NG;
         int s = 0, turn = 0;
         uint32_t phase = 0;
         if (a.x_resident && iters > 0) ok = __all_sync(0xffffffffu, mbar_wait_bounded(x_full, 0, a.flag));
@@ -269,7 +278,7 @@ __global__ void __launch_bounds__(kW4Threads, NT <= 2 ? 3 : 1) w4_gemv_kernel(co
 #pragma unroll
               for (int i = 0; i < SB; ++i) {
                 if (it0 + i >= iters || !ok) break;
-                if (i == 0) {
+                if (!TS && i == 0) {
 #pragma unroll
                     for (int j = 0; j < SW; ++j) {
                         sc[j] = sc_next[j];
@@ -290,9 +299,36 @@ __global__ void __launch_bounds__(kW4Threads, NT <= 2 ? 3 : 1) w4_gemv_kernel(co
                 auto xpiece = [&](int nt, int gi, int w) {
                     return *reinterpret_cast<const uint4*>(xs + xoff[gi * WPG + w] + nt * 1024);
                 };
+                // (TS) scales and zero points of up to four groups, rows g and g + 8
+                constexpr int NS = NG < 4 ? NG : 4;
+                uint32_t sl[2], sh[2], zl = 0x08080808u, zh = 0x08080808u;
 #pragma unroll
                 for (int gi = 0; gi < NG; ++gi) {
                     uint32_t wl[WPG], wh[WPG];
+                    if (TS && gi % NS == 0) {
+                        const uint8_t* sp = gbase + stage + a.s_off + soff + 2 * gi;
+                        const uint8_t* zq = gbase + stage + a.s_off + zoff + gi;
+                        if constexpr (NG < 4) {
+                            sl[0] = *reinterpret_cast<const uint32_t*>(sp);
+                            sh[0] = *reinterpret_cast<const uint32_t*>(sp + 8 * SROW);
+                            if (a.z) {
+                                zl = *reinterpret_cast<const uint16_t*>(zq);
+                                zh = *reinterpret_cast<const uint16_t*>(zq + 4 * SROW);
+                            }
+                        } else {
+                            const uint2 l = *reinterpret_cast<const uint2*>(sp), h = *reinterpret_cast<const uint2*>(sp + 8 * SROW);
+                            sl[0] = l.x; sl[1] = l.y;
+                            sh[0] = h.x; sh[1] = h.y;
+                            if (a.z) {
+                                zl = *reinterpret_cast<const uint32_t*>(zq) & 0x0F0F0F0Fu;
+                                zh = *reinterpret_cast<const uint32_t*>(zq + 4 * SROW) & 0x0F0F0F0Fu;
+                            }
+                        }
+                        if (NG < 4 && a.z) {
+                            zl &= 0x0F0Fu;
+                            zh &= 0x0F0Fu;
+                        }
+                    }
                     const uint8_t* at = wbase + (static_cast<uint32_t>(gi * (G / 2) + t * (G / 8)) ^ wsw);
                     if constexpr (WPG == 4) {
                         const uint4 l = *reinterpret_cast<const uint4*>(at), h = *reinterpret_cast<const uint4*>(at + 1024);
@@ -306,9 +342,16 @@ __global__ void __launch_bounds__(kW4Threads, NT <= 2 ? 3 : 1) w4_gemv_kernel(co
                         wl[0] = *reinterpret_cast<const uint32_t*>(at);
                         wh[0] = *reinterpret_cast<const uint32_t*>(at + 1024);
                     }
-                    const int src = (lane & 28) | (NG < 4 ? i * NG + gi : gi % 4);
-                    group(gi, wl, wh, xpiece, __shfl_sync(0xffffffffu, sc[NG < 4 ? 0 : gi / 4], src),
-                          a.z ? __shfl_sync(0xffffffffu, zp[NG < 4 ? 0 : gi / 4], src) : 0x00080008u);
+                    if constexpr (TS) {
+                        const int w = gi % NS;
+                        const uint32_t pair = __byte_perm(sl[w / 2], sh[w / 2], w & 1 ? 0x7632 : 0x5410);
+                        group(gi, wl, wh, xpiece, unpack2<T>(pair), __byte_perm(zl, 0u, 0x4040 | w * 0x101), __byte_perm(zh, 0u, 0x4040 | w * 0x101));
+                    } else {
+                        const int src = (lane & 28) | (NG < 4 ? i * NG + gi : gi % 4);
+                        const uint32_t z2 = a.z ? __shfl_sync(0xffffffffu, zp[NG < 4 ? 0 : gi / 4], src) : 0x00080008u;
+                        group(gi, wl, wh, xpiece, unpack2<T>(__shfl_sync(0xffffffffu, sc[NG < 4 ? 0 : gi / 4], src)), __byte_perm(z2, 0u, 0x1010),
+                              __byte_perm(z2, 0u, 0x3232));
+                    }
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty(s));
@@ -336,7 +379,7 @@ __global__ void __launch_bounds__(kW4Threads, NT <= 2 ? 3 : 1) w4_gemv_kernel(co
                         const int m = min(8 * nt + g, a.M - 1);
                         return *reinterpret_cast<const uint4*>(x + static_cast<int64_t>(m) * a.K + k0 + kof(gj, w));
                     };
-                    group(gi, wl, wh, xpiece, tsc, tzp);
+                    group(gi, wl, wh, xpiece, unpack2<T>(tsc), __byte_perm(tzp, 0u, 0x1010), __byte_perm(tzp, 0u, 0x3232));
                 }
             }
             if (a.split > 1) break;
@@ -389,10 +432,11 @@ __global__ void __launch_bounds__(kW4Threads, NT <= 2 ? 3 : 1) w4_gemv_kernel(co
     cluster_sync();   // the sums stay in place until every CTA has read them
 }
 
-template <typename T, int G, int NT>
+template <typename T, int G, int NT, bool TS>
 int launch_w4(W4Args a, cudaStream_t st) {
     constexpr int WR = NT, WK = kW4Warps / NT, ROWS = 16 * WR;
-    CUtensorMap mW{}, mX{};
+    constexpr uint32_t SROW = WK * (256 / G) * 2;
+    CUtensorMap mW{}, mX{}, mS{}, mZ{};
     a.nchunk = a.K / 256;
     // a map needs a chunk to describe; without one (K < 256) no stage is loaded
     if (a.nchunk > 0) {
@@ -401,6 +445,12 @@ int launch_w4(W4Args a, cudaStream_t st) {
         const int64_t xd[3] = {64, a.M, 4 * static_cast<int64_t>(a.nchunk)}, xs[2] = {static_cast<int64_t>(a.K) * 2, 128};
         const int xb[3] = {64, a.M, 4 * WK};
         if (!make_map_3d(&mW, a.wq, kMapU8, wd, ws, wb, 128) || !make_map_3d(&mX, a.x, kMap16, xd, xs, xb, 128)) return FUSE_ECUDA;
+        if (TS) {
+            const int64_t kg = a.K / G, sd[3] = {kg, a.N, 1}, ss[2] = {kg * 2, kg * 2 * a.N}, zs[2] = {kg, kg * a.N};
+            const int sb[3] = {SROW / 2, ROWS, 1};
+            if (!make_map_3d(&mS, a.s, kMap16, sd, ss, sb, G == 32 ? 128 : G == 64 ? 64 : 0)) return FUSE_ECUDA;
+            if (a.z && !make_map_3d(&mZ, a.z, kMapU8, sd, zs, sb, 0)) return FUSE_ECUDA;
+        }
     }
     a.tiles = static_cast<int>(ceil_div(a.N, ROWS));
     const int nblk = static_cast<int>(ceil_div(a.nchunk, WK));
@@ -412,7 +462,8 @@ int launch_w4(W4Args a, cudaStream_t st) {
     const int x_stage = 4 * WK * a.M * 128;
     a.x_resident = NT <= 2 && a.split == 1 && a.tiles > sm_count() && iters * x_stage <= 32 * 1024 ? 1 : 0;
     const uint32_t w_stage = WK * ROWS * 128;
-    a.stage_bytes = static_cast<uint32_t>((w_stage + (a.x_resident ? 0 : x_stage) + 1023) / 1024 * 1024);
+    a.s_off = w_stage + (a.x_resident ? 0 : x_stage);
+    a.stage_bytes = (a.s_off + (TS ? ROWS * SROW + (a.z ? ROWS * SROW / 2 : 0) : 0) + 1023) / 1024 * 1024;
     const uint32_t x_all = a.x_resident ? iters * x_stage : 0;
     const uint32_t pad = 8 * NT * 128;      // columns past M are read from behind the last rows of X
     const bool several = NT <= 2 && a.split == 1;     // row tiles per CTA, with two buffers of partial sums
@@ -428,7 +479,7 @@ int launch_w4(W4Args a, cudaStream_t st) {
     a.off_bar = a.off_red + (red + 15) / 16 * 16;
     const uint32_t smem = a.off_bar + bars + 1024;
     if (smem > kW4Smem) return FUSE_EUNSUPPORTED;
-    const int rc = opt_in_smem((const void*)w4_gemv_kernel<T, G, NT>, kW4Smem, true);
+    const int rc = opt_in_smem((const void*)w4_gemv_kernel<T, G, NT, TS>, kW4Smem, true);
     if (rc != FUSE_OK) return rc;
     int64_t grid = static_cast<int64_t>(a.tiles) * a.split;
     if (several) {   // as many CTAs as are resident; each takes every grid-th row tile
@@ -436,13 +487,13 @@ int launch_w4(W4Args a, cudaStream_t st) {
         const uint32_t kb = (smem + 1023) / 1024;
         uint32_t k = known.load(std::memory_order_relaxed);
         if ((k >> 8) != kb) {
-            k = (kb << 8) | static_cast<uint32_t>(blocks_per_sm(w4_gemv_kernel<T, G, NT>, kW4Threads, kb * 1024));
+            k = (kb << 8) | static_cast<uint32_t>(blocks_per_sm(w4_gemv_kernel<T, G, NT, TS>, kW4Threads, kb * 1024));
             known.store(k, std::memory_order_relaxed);
         }
         const int64_t resident = static_cast<int64_t>(sm_count()) * (k & 255u);
         if (grid > resident) grid = resident;
     }
-    return launch_pdl(w4_gemv_kernel<T, G, NT>, dim3(static_cast<unsigned>(grid)), dim3(kW4Threads), smem, st, a.split, mW, mX, a);
+    return launch_pdl(w4_gemv_kernel<T, G, NT, TS>, dim3(static_cast<unsigned>(grid)), dim3(kW4Threads), smem, st, a.split, mW, mX, mS, mZ, a);
 }
 
 // ================================================================== tcgen05 tiles
@@ -820,8 +871,8 @@ __global__ void __launch_bounds__(kTileThreads, 2) w4_tile_kernel(
     cluster_sync();   // the sums stay in place until every CTA has read them
 }
 
-// Whether the tile kernel can load the scales (and zero points): whole 16-byte pieces of a row.
-bool tile_fits(const W4Args& a, int group) {
+// Whether the copy engine can load the scales (and zero points): whole 16-byte pieces of a row.
+bool scales_fit(const W4Args& a, int group) {
     const int kg = a.K / group;
     return kg % 8 == 0 && is_aligned(a.s, 16) && (!a.z || (kg % 16 == 0 && is_aligned(a.z, 16)));
 }
@@ -872,15 +923,16 @@ int launch_tile(const W4Args& w, cudaStream_t st) {
 
 template <typename T, int G>
 int run_w4_g(const W4Args& a, cudaStream_t st) {
-    if (a.M > 8 && tile_fits(a, G)) {
+    const bool fits = scales_fit(a, G);
+    if (a.M > 8 && fits) {
         if (a.M <= 16) return launch_tile<T, G, 16>(a, st);
         if (a.M <= 32) return launch_tile<T, G, 32>(a, st);
         return launch_tile<T, G, 64>(a, st);
     }
-    if (a.M <= 8) return launch_w4<T, G, 1>(a, st);
-    if (a.M <= 16) return launch_w4<T, G, 2>(a, st);
-    if (a.M <= 32) return launch_w4<T, G, 4>(a, st);
-    return launch_w4<T, G, 8>(a, st);
+    if (a.M <= 8) return fits ? launch_w4<T, G, 1, true>(a, st) : launch_w4<T, G, 1, false>(a, st);
+    if (a.M <= 16) return launch_w4<T, G, 2, false>(a, st);
+    if (a.M <= 32) return launch_w4<T, G, 4, false>(a, st);
+    return launch_w4<T, G, 8, false>(a, st);
 }
 template <typename T>
 int run_w4(const W4Args& a, int group, cudaStream_t st) {
@@ -889,38 +941,42 @@ int run_w4(const W4Args& a, int group, cudaStream_t st) {
     return run_w4_g<T, 128>(a, st);
 }
 
-struct W4Entry {
-    const void* kernel;
-    const char* name;
-};
 template <typename T, int G>
-void w4_entries(W4Entry* e, const char* const* names) {
-    e[0] = {(const void*)w4_gemv_kernel<T, G, 1>, names[0]};
-    e[1] = {(const void*)w4_gemv_kernel<T, G, 2>, names[1]};
-    e[2] = {(const void*)w4_gemv_kernel<T, G, 4>, names[2]};
-    e[3] = {(const void*)w4_gemv_kernel<T, G, 8>, names[3]};
+int w4_entry(int i, const char* const* names, fuse_kernel_record* out) {
+    switch (i) {
+        case 0: return describe_kernel((const void*)w4_gemv_kernel<T, G, 1, true>, names[0], kW4Threads, 110 * 1024, out);
+        case 1: return describe_kernel((const void*)w4_gemv_kernel<T, G, 1, false>, names[1], kW4Threads, 110 * 1024, out);
+        case 2: return describe_kernel((const void*)w4_gemv_kernel<T, G, 2, false>, names[2], kW4Threads, 110 * 1024, out);
+        case 3: return describe_kernel((const void*)w4_gemv_kernel<T, G, 4, false>, names[3], kW4Threads, 110 * 1024, out);
+        case 4: return describe_kernel((const void*)w4_gemv_kernel<T, G, 8, false>, names[4], kW4Threads, 110 * 1024, out);
+        case 5: return describe_kernel((const void*)w4_tile_kernel<T, G, 16>, names[5], kTileThreads, TileLayout<16>::SMEM, out, kTileCols);
+        case 6: return describe_kernel((const void*)w4_tile_kernel<T, G, 32>, names[6], kTileThreads, TileLayout<32>::SMEM, out, kTileCols);
+        default: return describe_kernel((const void*)w4_tile_kernel<T, G, 64>, names[7], kTileThreads, TileLayout<64>::SMEM, out, kTileCols);
+    }
 }
 
 }  // namespace
 
-int w4_report_count() { return 24; }
+int w4_report_count() { return 48; }
 int w4_report(int i, fuse_kernel_record* out) {
-    if (i < 0 || i >= 24) return FUSE_EINVAL;
-    static const char* const names[24] = {
-        "w4_gemv_kernel<bf16, group 32, M <= 8>", "w4_gemv_kernel<bf16, group 32, M <= 16>", "w4_gemv_kernel<bf16, group 32, M <= 32>", "w4_gemv_kernel<bf16, group 32, M <= 64>",
-        "w4_gemv_kernel<bf16, group 64, M <= 8>", "w4_gemv_kernel<bf16, group 64, M <= 16>", "w4_gemv_kernel<bf16, group 64, M <= 32>", "w4_gemv_kernel<bf16, group 64, M <= 64>",
-        "w4_gemv_kernel<bf16, group 128, M <= 8>", "w4_gemv_kernel<bf16, group 128, M <= 16>", "w4_gemv_kernel<bf16, group 128, M <= 32>", "w4_gemv_kernel<bf16, group 128, M <= 64>",
-        "w4_gemv_kernel<f16, group 32, M <= 8>", "w4_gemv_kernel<f16, group 32, M <= 16>", "w4_gemv_kernel<f16, group 32, M <= 32>", "w4_gemv_kernel<f16, group 32, M <= 64>",
-        "w4_gemv_kernel<f16, group 64, M <= 8>", "w4_gemv_kernel<f16, group 64, M <= 16>", "w4_gemv_kernel<f16, group 64, M <= 32>", "w4_gemv_kernel<f16, group 64, M <= 64>",
-        "w4_gemv_kernel<f16, group 128, M <= 8>", "w4_gemv_kernel<f16, group 128, M <= 16>", "w4_gemv_kernel<f16, group 128, M <= 32>", "w4_gemv_kernel<f16, group 128, M <= 64>"};
-    W4Entry e[24];
-    w4_entries<__nv_bfloat16, 32>(e, names);
-    w4_entries<__nv_bfloat16, 64>(e + 4, names + 4);
-    w4_entries<__nv_bfloat16, 128>(e + 8, names + 8);
-    w4_entries<__half, 32>(e + 12, names + 12);
-    w4_entries<__half, 64>(e + 16, names + 16);
-    w4_entries<__half, 128>(e + 20, names + 20);
-    return describe_kernel(e[i].kernel, e[i].name, kW4Threads, 110 * 1024, out);
+    if (i < 0 || i >= 48) return FUSE_EINVAL;
+#define FC_W4(T, G)                                                                                                       \
+    {"w4_gemv_kernel<" T ", group " G ", M <= 8>", "w4_gemv_kernel<" T ", group " G ", M <= 8, any alignment>",           \
+     "w4_gemv_kernel<" T ", group " G ", M <= 16, any alignment>", "w4_gemv_kernel<" T ", group " G ", M <= 32, any alignment>", \
+     "w4_gemv_kernel<" T ", group " G ", M <= 64, any alignment>", "w4_tile_kernel<" T ", group " G ", M <= 16> (tcgen05)", \
+     "w4_tile_kernel<" T ", group " G ", M <= 32> (tcgen05)", "w4_tile_kernel<" T ", group " G ", M <= 64> (tcgen05)"}
+    static const char* const names[6][8] = {FC_W4("bf16", "32"), FC_W4("bf16", "64"), FC_W4("bf16", "128"),
+                                            FC_W4("f16", "32"), FC_W4("f16", "64"), FC_W4("f16", "128")};
+#undef FC_W4
+    const int k = i / 8, v = i % 8;
+    switch (k) {
+        case 0: return w4_entry<__nv_bfloat16, 32>(v, names[k], out);
+        case 1: return w4_entry<__nv_bfloat16, 64>(v, names[k], out);
+        case 2: return w4_entry<__nv_bfloat16, 128>(v, names[k], out);
+        case 3: return w4_entry<__half, 32>(v, names[k], out);
+        case 4: return w4_entry<__half, 64>(v, names[k], out);
+        default: return w4_entry<__half, 128>(v, names[k], out);
+    }
 }
 
 }  // namespace fc
