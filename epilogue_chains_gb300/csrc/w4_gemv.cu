@@ -533,7 +533,7 @@ struct TileLayout {
 struct TileArgs {
     int M, N, KG;
     int nchunk;        // 128-k chunks, the last one possibly partial
-    int per;           // chunks of a CTA (a multiple of those that 16 groups fill, when split)
+    int per;           // chunks of a CTA
     int split, gelu, zeros;
     int y_vec;         // y is 8-byte aligned
     const void *bias, *R;
@@ -611,13 +611,13 @@ __global__ void __launch_bounds__(kTileThreads, 2) w4_tile_kernel(
             bool ok = true;
             for (; u < units; ++u) {
                 const int st = u % kTileStages;
-                if (u % UPB == 0) {
+                if (u == 0 || (c0 + u) % UPB == 0) {
                     const int sb = blocks & 1;
                     if (blocks >= 2 && !mbar_wait_bounded(s_empty(sb), ((blocks >> 1) - 1) & 1, a.flag)) {
                         ok = false;
                         break;
                     }
-                    const int g0 = (c0 + u) * NG;
+                    const int g0 = (c0 + u) / UPB * 16;     // whole blocks, whatever chunk the CTA starts at
                     mbar_arrive_expect_tx(s_full(sb), L::S + (a.zeros ? L::Z : 0u));
                     tma_load_3d(base + L::OFF_S + sb * L::S, &mS, g0, n0, 0, s_full(sb));
                     tma_load_3d(base + L::OFF_S + sb * L::S + L::S / 2, &mS, g0 + 8, n0, 0, s_full(sb));
@@ -703,12 +703,14 @@ __global__ void __launch_bounds__(kTileThreads, 2) w4_tile_kernel(
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
+        const uint32_t b0 = static_cast<uint32_t>(c0) / UPB;      // the CTA's first block of scales
         int d = 0, st = 0;
         uint32_t d_par = 0, st_par = 0;
         for (int u = 0; u <= units && ok; ++u) {
             if (u < units) {
-                const int ab = u & 1, blk = u / UPB, sb = blk & 1;
-                if (u % UPB == 0 && !wait(s_full(sb), blk >> 1)) break;
+                const uint32_t c = c0 + u, blk = c / UPB - b0, sb = blk & 1;
+                const int ab = u & 1;
+                if ((u == 0 || c % UPB == 0) && !wait(s_full(sb), blk >> 1)) break;
                 if (!wait(full(st), st_par)) break;
                 // A buffer ab is free: the accumulators of unit u - 2 have been waited for
                 // this thread's row: 64 k from 64 hh on, two 16-byte pieces of the row's four
@@ -718,7 +720,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) w4_tile_kernel(
                 const uint32_t words[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
                 uint32_t zb[2] = {Nib<T>::MAGIC | 0x00080008u, Nib<T>::MAGIC | 0x00080008u};   // first and second 32 k
                 if (a.zeros) {
-                    const uint8_t* zp = gbase + L::OFF_Z + sb * L::Z + r * 16 + (u % UPB) * NG;
+                    const uint8_t* zp = gbase + L::OFF_Z + sb * L::Z + r * 16 + c % UPB * NG;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) zb[i] = Nib<T>::MAGIC | (zp[(64 * hh + 32 * i) / G] & 15u) * 0x00010001u;
                 }
@@ -740,7 +742,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) w4_tile_kernel(
                 }
             }
             if (u > 0) {
-                const int v = u - 1, blk = v / UPB, sb = blk & 1;
+                const uint32_t v = c0 + u - 1, sb = (v / UPB - b0) & 1;      // chunk
                 const uint8_t* sp = gbase + L::OFF_S + sb * L::S + r * 16;
 #pragma unroll
                 for (int h = 0; h < SETS; ++h) {
@@ -753,7 +755,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) w4_tile_kernel(
                         if constexpr (HT == 32) tmem_ld32(at, x);
                         else if constexpr (HT == 16) tmem_ld16(at, x);
                         else tmem_ld8(at, x);
-                        const int gb = (v % UPB) * NG + h * SG + g;      // group of the block
+                        const uint32_t gb = v % UPB * NG + h * SG + g;      // group of the block
                         const float s = to_f32(*reinterpret_cast<const T*>(sp + (gb / 8) * (L::S / 2) + (gb % 8) * 2));
                         tmem_ld_wait();
 #pragma unroll
@@ -770,7 +772,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) w4_tile_kernel(
                         d_par ^= 1u;
                     }
                 }
-                if (ok && (v % UPB == UPB - 1 || v == units - 1)) arrive(s_empty(sb));
+                if (ok && v % UPB == UPB - 1) arrive(s_empty(sb));
             }
         }
     }
@@ -880,7 +882,6 @@ bool scales_fit(const W4Args& a, int group) {
 template <typename T, int G, int NM>
 int launch_tile(const W4Args& w, cudaStream_t st) {
     using L = TileLayout<NM>;
-    constexpr int UPB = 16 * G / 128;
     TileArgs a{};
     a.M = w.M;
     a.N = w.N;
@@ -897,8 +898,7 @@ int launch_tile(const W4Args& w, cudaStream_t st) {
     // A CTA's chunks, times how often the SMs go round: the least, and of equal splits the smallest
     int64_t best = INT64_MAX;
     for (int s = 1; s <= 8; s *= 2) {
-        int64_t per = ceil_div(a.nchunk, s);
-        if (s > 1) per = ceil_div(per, UPB) * UPB;      // blocks of scales start with a CTA
+        const int64_t per = ceil_div(a.nchunk, s);
         const int64_t cost = ceil_div(static_cast<int64_t>(tiles) * s, sms) * (per + 2);
         if (cost < best) {
             best = cost;
@@ -924,7 +924,9 @@ int launch_tile(const W4Args& w, cudaStream_t st) {
 template <typename T, int G>
 int run_w4_g(const W4Args& a, cudaStream_t st) {
     const bool fits = scales_fit(a, G);
-    if (a.M > 8 && fits) {
+    // Up to 16 tokens w4_gemv_kernel is quicker until there is a tile of 128 rows per SM: at 16 x 4096 x 4096 it takes
+    // 7.8 us (tiles 10.3), at 8192 x 8192 23.4 (27.5), at 14336 x 4096 20.7 (21.7), at 28672 x 4096 39 (28).
+    if (fits && (a.M > 16 || (a.M > 8 && ceil_div(a.N, 128) > sm_count()))) {
         if (a.M <= 16) return launch_tile<T, G, 16>(a, st);
         if (a.M <= 32) return launch_tile<T, G, 32>(a, st);
         return launch_tile<T, G, 64>(a, st);

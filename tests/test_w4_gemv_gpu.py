@@ -81,6 +81,20 @@ def test_odd_sizes(cuda_device, dtype, N, K, G, M):
     check(*make(M, N, K, G, dtype, zeros=N % 2 == 1, residual=True, seed=N + K))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("G", [32, 64, 128])
+def test_few_tokens_many_rows(cuda_device, dtype, G):
+    """9 to 16 tokens and more row tiles than SMs, the last one ragged."""
+    for M in (9, 16):
+        check(*make(M, 24604, 2048, G, dtype, zeros=M == 9, residual=True, seed=G + M))
+
+
+@pytest.mark.parametrize("M,N,K,G,zeros", [(40, 130, 11264, 128, False), (17, 130, 12288, 128, True),
+                                           (64, 300, 5120, 64, True), (33, 129, 5376, 32, False)])
+def test_splits_inside_a_block_of_scales(cuda_device, M, N, K, G, zeros):
+    check(*make(M, N, K, G, "bf16", zeros=zeros, bias=True, seed=K), gelu=True)
+
+
 @pytest.mark.parametrize("M,N,K,G,dtype", [(1, 4096, 4096, 128, "bf16"), (5, 4096, 14336, 32, "f16"),
                                            (64, 28672, 4096, 64, "bf16"), (16, 4096, 4096, 128, "f16")])
 def test_full_sizes(cuda_device, M, N, K, G, dtype):
