@@ -84,6 +84,7 @@ struct PagedArgs {
     float *pml, *po;                   // [kPrefixGrid + pitems][prow] (m, l, l', -) and [..][prow][D]
     // prefix
     int plen, ptiles, prow, prt, pgrid; // keys, 128-key tiles, rows of an item (128 or 256), a head's items, CTAs
+    int pent;                          // places that an item's entry counts for (see PrefixSeg)
     int *flag, *bad;
 };
 
@@ -653,6 +654,29 @@ __global__ void __launch_bounds__(kOwnThreads, OwnLayout<D>::CTAS) paged_own_ker
     if (runs > 0) join_before();
 }
 
+// The prefix's items (row tiles of a key/value head) lie in one line and are cut into equal ranges, one per CTA:
+// pent places that stand for what an item costs a CTA apart from its tiles (loading the query rows, filling and
+// emptying the pipeline, writing its part), then a place per 128-key tile.  Measured with 0, 2, 4 and 6 of them:
+// 256 sequences over 16384 shared keys (D = 128) 103.9, 101.7, 101.0 and 101.3 us, 8 over 2048 (D = 256) 54.4, 53.2,
+// 52.6 and 49.2.  With at most a tile per CTA there is nothing to even out (pent = 0).
+constexpr int kEntry = 6;
+struct PrefixSeg {
+    int item, t0, n;     // tiles t0 .. t0 + n - 1 of the item
+};
+// The next segment of places u .. u1 - 1, from which it is taken; false: none left.
+__device__ __forceinline__ bool next_seg(const PagedArgs& a, int& u, int u1, PrefixSeg& s) {
+    const int per = a.ptiles + a.pent;
+    while (u < u1) {
+        s.item = u / per;
+        const int in = u - s.item * per, end = min(per, in + (u1 - u));
+        u += end - in;
+        s.t0 = max(in - a.pent, 0);
+        s.n = end - a.pent - s.t0;
+        if (s.n > 0) return true;
+    }
+    return false;
+}
+
 // With a shared prefix, the last step: a row's own part and the prefix's parts.  One warp per query row, lane c
 // taking D / 32 columns.
 constexpr int kJoinThreads = 128;
@@ -667,7 +691,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     const int head = h / a.group, prow = b * a.group + h % a.group;
     const int rpi = a.prow;
     const int pit = head * a.prt + prow / rpi;
-    const int64_t PU = static_cast<int64_t>(a.hk) * a.prt * a.ptiles, u = static_cast<int64_t>(pit) * a.ptiles;
+    const int64_t per = a.ptiles + a.pent, PU = a.hk * a.prt * per, u = pit * per + a.pent;
     const int c0 = cta_of(u, PU, a.pgrid), np = cta_of(u + a.ptiles - 1, PU, a.pgrid) - c0 + 1;
     pdl_wait();
     // lane 0 has the row's own part (after that: what has been joined), lanes 1 .. kParts the prefix's.  The
@@ -881,7 +905,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix_kernel(const __gr
     pdl_wait();
     pdl_trigger();   // only now: paged_own_kernel relies on it
 
-    const int64_t U = static_cast<int64_t>(a.hk) * a.prt * a.ptiles;     // below 2^31
+    const int64_t U = static_cast<int64_t>(a.hk) * a.prt * (a.ptiles + a.pent);     // below 2^31
     const int u0 = static_cast<int>(blockIdx.x * U / gridDim.x), u1 = static_cast<int>((blockIdx.x + 1) * U / gridDim.x);
     auto keys_of = [&](int tile) { return min(128, a.plen - tile * 128); };
 
@@ -892,15 +916,19 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix_kernel(const __gr
         if (lane == 0) prefetch_map(map);
         PrefixLoader<D> ld(a, lane);
         int i = 0;
-        const int total = u1 - u0;
-        for (; i < total; ++i) {
-            const int tile = (u0 + i) % a.ptiles, st = i % KV;
-            ld.head = (u0 + i) / a.ptiles / a.prt;
-            ld.look(tile);
-            if (i >= KV && !__all_sync(0xffffffffu, mbar_wait_bounded(is_k ? k_empty(st) : v_empty(st), ((i - KV) / KV) & 1, flag))) break;
-            ld.load(map, base + (is_k ? L::OFF_K : L::OFF_V) + st * L::TILE, is_k ? k_full(st) : v_full(st), tile);
+        bool ok = true;
+        PrefixSeg seg;
+        for (int u = u0; ok && next_seg(a, u, u1, seg);) {
+            ld.head = seg.item / a.prt;
+            for (int j = 0; j < seg.n; ++j, ++i) {
+                const int tile = seg.t0 + j, st = i % KV;
+                ld.look(tile);
+                ok = i < KV || __all_sync(0xffffffffu, mbar_wait_bounded(is_k ? k_empty(st) : v_empty(st), ((i - KV) / KV) & 1, flag));
+                if (!ok) break;
+                ld.load(map, base + (is_k ? L::OFF_K : L::OFF_V) + st * L::TILE, is_k ? k_full(st) : v_full(st), tile);
+            }
         }
-        if (i < total)   // copies in flight land before the shared memory goes away
+        if (!ok)   // copies in flight land before the shared memory goes away
             for (int j = max(0, i - KV); j < i; ++j) (void)mbar_wait_drain(is_k ? k_full(j % KV) : v_full(j % KV), (j / KV) & 1);
         __syncwarp();
     } else if (warp == 1) {
@@ -942,17 +970,17 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix_kernel(const __gr
             tc_commit_if(one, v_empty(st));
             issued = true;
         };
-        int i = 0, seg = 0;
-        for (int u = u0; ok && u < u1; ++seg) {
-            const int n = min(a.ptiles - u % a.ptiles, u1 - u);
-            if (!wait(q_full, seg)) break;
+        int i = 0, segs = 0;
+        PrefixSeg seg;
+        for (int u = u0; ok && next_seg(a, u, u1, seg); ++segs) {
+            const int n = seg.n;
+            if (!wait(q_full, segs)) break;
             issue_s(i);
             for (int j = 0; ok && j < n; ++j) {
                 if (j + 1 < n) issue_s(i + j + 1);
                 if (ok) issue_pv(i + j, j == 0);
             }
             i += n;
-            u += n;
         }
         if (!ok && issued) {   // MMAs in flight finish before TMEM is freed
             tc_commit_if(one, drain);
@@ -971,9 +999,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix_kernel(const __gr
         constexpr int HK = 64;
         bool ok = true;
         int i = 0;
-        for (int u = u0; ok && u < u1;) {
-            const int item = u / a.ptiles, t0 = u - item * a.ptiles;
-            const int n = min(a.ptiles - t0, u1 - u);
+        PrefixSeg seg;
+        for (int u = u0; ok && next_seg(a, u, u1, seg);) {
+            const int item = seg.item, t0 = seg.t0, n = seg.n;
             const int head = item / a.prt, qrow0 = (item % a.prt) * 128;
             // The MMAs that read the previous tile's Q have completed (its last O was waited for).
             load_q_tile<T, D, 32 * kPreSoftmaxWarps>(gbase + L::OFF_Q, head, qrow0, sid, a);
@@ -1096,7 +1124,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix_kernel(const __gr
                         for (int e = 0; e < 4; ++e) st_v8(dst + 32 * k + 8 * e, o + 8 * e);
                 }
             }
-            u += n;
         }
     }
     tc_fence_before();
@@ -1178,7 +1205,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix2_kernel(const __g
     pdl_wait();
     pdl_trigger();   // only now: paged_own_kernel relies on it
 
-    const int64_t U = static_cast<int64_t>(a.hk) * a.prt * a.ptiles;     // below 2^31
+    const int64_t U = static_cast<int64_t>(a.hk) * a.prt * (a.ptiles + a.pent);     // below 2^31
     const int u0 = static_cast<int>(blockIdx.x * U / gridDim.x), u1 = static_cast<int>((blockIdx.x + 1) * U / gridDim.x);
     // Place of K tile j and V tile j of a segment of n in the segment's loads: K(0), then K(j + 1) before V(j).
     auto k_at = [](int j) { return j == 0 ? 0 : 2 * j - 1; };
@@ -1194,10 +1221,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix2_kernel(const __g
         int c = 0, slot = 0;             // loads so far, and the next one's slot
         uint32_t phase = 1;              // of the wait for it to be empty
         bool ok = true;
-        for (int u = u0; ok && u < u1;) {
-            const int item = u / a.ptiles, t0 = u - item * a.ptiles;
-            const int n = min(a.ptiles - t0, u1 - u);
-            ld.head = item / a.prt;
+        PrefixSeg seg;
+        for (int u = u0; ok && next_seg(a, u, u1, seg);) {
+            const int t0 = seg.t0, n = seg.n;
+            ld.head = seg.item / a.prt;
             for (int x = 0; x < 2 * n; ++x, ++c) {
                 // x-th load of the segment: K for 0 and odd x below 2 n - 1, V for the others
                 const bool is_k = x == 0 || (x % 2 == 1 && x < 2 * n - 1);
@@ -1213,7 +1240,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix2_kernel(const __g
                     phase ^= 1u;
                 }
             }
-            u += n;
         }
         if (!ok)   // copies in flight land before the shared memory goes away
             for (int j = max(0, c - RING); j < c; ++j) (void)mbar_wait_drain(full(j % RING), (j / RING) & 1);
@@ -1257,10 +1283,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix2_kernel(const __g
             if (t == 1) tc_commit_if(one, empty(c % RING));
             issued = true;
         };
-        int i = 0, c = 0, seg = 0;
-        for (int u = u0; ok && u < u1; ++seg) {
-            const int n = min(a.ptiles - u % a.ptiles, u1 - u);
-            if (!wait(q_full, seg)) break;
+        int i = 0, c = 0, segs = 0;
+        PrefixSeg seg;
+        for (int u = u0; ok && next_seg(a, u, u1, seg); ++segs) {
+            const int n = seg.n;
+            if (!wait(q_full, segs)) break;
             issue_s(0, i, c);
             if (ok) issue_s(1, i, c);
             for (int j = 0; ok && j < n; ++j) {
@@ -1272,7 +1299,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix2_kernel(const __g
             if (ok) issue_pv(1, i + n - 1, c + v_at(n - 1, n), n == 1);
             i += n;
             c += 2 * n;
-            u += n;
         }
         if (!ok && issued) {   // MMAs in flight finish before TMEM is freed
             tc_commit_if(one, drain);
@@ -1292,9 +1318,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix2_kernel(const __g
             return ok;
         };
         int i = 0, c = 0;
-        for (int u = u0; ok && u < u1;) {
-            const int item = u / a.ptiles, t0 = u - item * a.ptiles;
-            const int n = min(a.ptiles - t0, u1 - u);
+        PrefixSeg seg;
+        for (int u = u0; ok && next_seg(a, u, u1, seg);) {
+            const int item = seg.item, t0 = seg.t0, n = seg.n;
             const int head = item / a.prt, qrow0 = (item % a.prt) * 256 + t * 128;
             // this tile's Q, by its own warps: the MMAs that read the last one have completed
             load_q_tile<T, D, 32 * kPreSoftmaxWarps / 2>(gbase + L::OFF_Q + t * L::TILE, head, qrow0, r, a);
@@ -1393,7 +1419,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix2_kernel(const __g
                         for (int e = 0; e < 4; ++e) st_v8(dst + 32 * k + 8 * e, o + 8 * e);
                 }
             }
-            u += n;
             c += 2 * n;
         }
     }
@@ -1583,7 +1608,7 @@ extern "C" int fuse_paged_attention(const void* q, const void* k_cache, const vo
     // places of the whole batch, and tiles of the prefix, stay below 2^31
     if ((table_ld * page_size / kUnit + 2) * batch >= top) return FUSE_EUNSUPPORTED;
     const int64_t group = q_heads / kv_heads;
-    if (prefix_len > 0 && ceil_div(prefix_len, 128) * kv_heads * ceil_div(batch * group, 128) >= top) return FUSE_EUNSUPPORTED;
+    if (prefix_len > 0 && (ceil_div(prefix_len, 128) + kEntry) * kv_heads * ceil_div(batch * group, 128) >= top) return FUSE_EUNSUPPORTED;
     if (batch == 0) return FUSE_OK;
     if (!q || !k_cache || !v_cache || !o || !seq_lens || (table_ld > 0 && !block_table) || (prefix_len > 0 && !prefix_table))
         return FUSE_EINVAL;
@@ -1632,6 +1657,7 @@ extern "C" int fuse_paged_attention(const void* q, const void* k_cache, const vo
         const int64_t units = static_cast<int64_t>(a.hk) * a.prt * a.ptiles;
         int64_t grid = sm_count() < kPrefixGrid ? sm_count() : kPrefixGrid;
         a.pgrid = static_cast<int>(grid < units ? grid : units);
+        a.pent = units > grid ? kEntry : 0;
     }
     a.flag = watchdog_flag();
     a.bad = index_flag();
