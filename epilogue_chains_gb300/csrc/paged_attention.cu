@@ -4,19 +4,22 @@
 //     o_bh = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m),   s_j = scale q_bh . k_j
 // over the prefix's keys and the sequence's own.  A part of the keys gives (m, l, O) = (reference, sum of
 // 2^(s - m), sum of 2^(s - m) v), s in base-2 units; parts join as m = max m_i, l = sum 2^(m_i - m) l_i
-// and O likewise, so any split of the key axis gives the same result up to fp32 rounding.  Two kernels:
+// and O likewise, so any split of the key axis gives the same result up to fp32 rounding.
 //
 //  * paged_own_kernel: the sequences' own keys.  Every key and value is used by one group of query heads
 //    only (q_heads / kv_heads rows), so reading them bounds the time.  The work is cut into units of 64
 //    keys of one (sequence, key/value head), numbered in one line, and the CTAs take equal runs of it,
-//    whatever the lengths are: a long sequence is shared by many CTAs, a CTA covers many short ones.
-//    Each warp streams its own 16 keys of every unit through a private TMA ring (no CTA barrier in the
-//    loop) and multiplies them with the query rows by mma.sync (16 rows, mostly one group); the warps'
-//    parts meet in shared memory when a sequence ends.  Parts of a sequence that several CTAs share go
-//    through the workspace: the CTA that arrives last joins them, in the order of the keys.
-//  * paged_prefix_kernel: the shared prefix.  Here all batch * group query rows of a key/value head meet
-//    the same keys: tcgen05 tiles of 128 rows by 128 keys, scores and output in TMEM, the key axis split
-//    over the SMs the same way.  Its parts are joined by paged_own_kernel.
+//    whatever the lengths are: a long sequence is shared by many CTAs, a CTA covers many short ones.  One
+//    warp loads units by TMA into a ring, four compute: each multiplies its 16 keys of a unit with the
+//    query rows by mma.sync (16 rows, mostly one group), and the warps' parts meet in shared memory when
+//    a run ends.  Parts of a sequence that several CTAs share go through the workspace: the CTA that
+//    arrives last joins them, in the order of the keys.  3 x 65536 keys (D = 128) take 110 us, 0.96 of
+//    the copy rate; 32 sequences of up to 4096 keys 51.6 us, 0.80.
+//  * paged_prefix_kernel, paged_prefix2_kernel: the shared prefix.  Here all batch * group query rows of a
+//    key/value head meet the same keys: tcgen05 tiles of 128 or 256 rows by 128 keys, scores and output
+//    in TMEM, the key axis split over the SMs.  1024 rows per head over 16384 keys (8 heads, D = 128) take
+//    57 us of the call's 101, 1.2 PFLOP/s.
+//  * paged_join_kernel, with a prefix: a row's own part and the prefix's parts.
 //
 // The lengths are in device memory, so one launch configuration (and a captured graph) serves every
 // length.  All waits are bounded (watchdog).
@@ -130,10 +133,9 @@ struct OwnLayout {
     static constexpr uint32_t SLOT = ATOM * ATOMS;               // K or V of a unit
     static constexpr uint32_t QATOM = 16 * 128;                  // 16 query rows x 64 components
     static constexpr uint32_t QSLOT = QATOM * ATOMS;
-    // D = 256 leaves no registers to hold the query rows next to the output; they are read again from
-    // shared memory for every unit
-    static constexpr bool Q_REGS = true || D <= 128;
-    static constexpr int CTAS = D <= 128 ? 2 : 1;                // CTAs per SM
+    // CTAs per SM.  D = 256: one, whose 255 registers hold the query rows next to the output, and whose ring is
+    // twice as long (two, with the rows read again from shared memory for every unit: 69 us where one takes 59)
+    static constexpr int CTAS = D <= 128 ? 2 : 1;
     static constexpr int NQ = D <= 128 ? 4 : 2;                  // buffers of query rows
 };
 
@@ -495,7 +497,6 @@ __global__ void __launch_bounds__(kOwnThreads, OwnLayout<D>::CTAS) paged_own_ker
         const int rows = min(a.rows, a.group - (hr % a.rt) * 16);
         const bool any = cur.len > 0;
         const uint32_t qb = base + a.off_q + qs * L::QSLOT;
-        auto load_q = [&](uint32_t (&f)[4], int k) { ldsm4(f, qb + (k / 4) * L::QATOM + swz(qrow, 2 * k + qcol)); };
         auto free_q = [&] {
             __syncwarp();
             if (lane == 0) mbar_arrive(q_empty(qs));
@@ -504,13 +505,11 @@ __global__ void __launch_bounds__(kOwnThreads, OwnLayout<D>::CTAS) paged_own_ker
                 qphase ^= 1u;
             }
         };
-        uint32_t qf[L::Q_REGS ? D / 16 : 1][4];
+        uint32_t qf[D / 16][4];
         if (any && wait_full(q_full(qs), qphase)) {
-            if constexpr (L::Q_REGS) {
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) load_q(qf[k], k);
-                free_q();
-            }
+            for (int k = 0; k < D / 16; ++k) ldsm4(qf[k], qb + (k / 4) * L::QATOM + swz(qrow, 2 * k + qcol));
+            free_q();
         }
         float o[D / 8][4] = {};
         float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;   // rows g and g + 8
@@ -524,20 +523,16 @@ __global__ void __launch_bounds__(kOwnThreads, OwnLayout<D>::CTAS) paged_own_ker
                 float s[2][4] = {};
                 {
                     // fragments are loaded kDeep steps ahead; even and odd steps add up apart
-                    constexpr int kDeep = L::Q_REGS ? 4 : 2;
+                    constexpr int kDeep = D <= 128 ? 4 : 2;
                     float s2[2][4] = {};
-                    uint32_t f[kDeep][4], fq[kDeep][4];
-                    auto load = [&](int k) {
-                        ldsm4(f[k % kDeep], kb + (k / 4) * L::ATOM + swz(kkey, 2 * k + kcol));
-                        if constexpr (!L::Q_REGS) load_q(fq[k % kDeep], k);
-                    };
+                    uint32_t f[kDeep][4];
+                    auto load = [&](int k) { ldsm4(f[k % kDeep], kb + (k / 4) * L::ATOM + swz(kkey, 2 * k + kcol)); };
 #pragma unroll
                     for (int k = 0; k < kDeep; ++k) load(k);
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t (&q)[4] = L::Q_REGS ? qf[L::Q_REGS ? k : 0] : fq[k % kDeep];
-                        mma16816<T>(k & 1 ? s2[0] : s[0], q, f[k % kDeep][0], f[k % kDeep][1]);
-                        mma16816<T>(k & 1 ? s2[1] : s[1], q, f[k % kDeep][2], f[k % kDeep][3]);
+                        mma16816<T>(k & 1 ? s2[0] : s[0], qf[k], f[k % kDeep][0], f[k % kDeep][1]);
+                        mma16816<T>(k & 1 ? s2[1] : s[1], qf[k], f[k % kDeep][2], f[k % kDeep][3]);
                         if (k + kDeep < D / 16) load(k + kDeep);
                     }
 #pragma unroll
@@ -600,7 +595,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnLayout<D>::CTAS) paged_own_ker
                     // keys past the sequence's end: 0 x whatever lies in the page must be 0
                     const uint32_t k0 = tail ? (2 * t < nv ? 0xFFFFu : 0u) | (2 * t + 1 < nv ? 0xFFFF0000u : 0u) : 0u;
                     const uint32_t k1 = tail ? (2 * t + 8 < nv ? 0xFFFFu : 0u) | (2 * t + 9 < nv ? 0xFFFF0000u : 0u) : 0u;
-                    constexpr int kDeep = L::Q_REGS ? 3 : 2;
+                    constexpr int kDeep = D <= 128 ? 3 : 2;
                     uint32_t f[kDeep][4];
                     auto load = [&](int k) { ldsm4_t(f[k % kDeep], vb + (k / 4) * L::ATOM + swz(vkey, 2 * k + vcol)); };
 #pragma unroll
@@ -624,7 +619,6 @@ __global__ void __launch_bounds__(kOwnThreads, OwnLayout<D>::CTAS) paged_own_ker
             }
             done();
         }
-        if (!L::Q_REGS && any) free_q();
         // ---- the warps' parts
         l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
         l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
@@ -797,19 +791,24 @@ template <typename T, int D, int THREADS>
 __device__ __forceinline__ void load_q_tile(uint8_t* tile, int head, int qrow0, int tid, const PagedArgs& a) {
     constexpr int PER = 128 * (D / 8) / THREADS, STEP = THREADS / (D / 8);   // vectors of a thread, rows apart
     uint4 x[PER];
-    int row = qrow0 + tid / (D / 8), b = row / a.group, g = row - b * a.group;
-    const int step_b = STEP / a.group, step_g = STEP - step_b * a.group;      // no division per vector
-    const T* q = static_cast<const T*>(a.q) + head * a.group * D + 8 * (tid % (D / 8));
+    // Opaque copies: what depends on them is computed here, not kept in registers between the tiles (which spills)
+    int group = a.group;
+    asm volatile("" : "+r"(tid), "+r"(group));
+    int row = qrow0 + tid / (D / 8);
+    const int b = row / group, step_b = STEP / group, step_g = STEP - step_b * group;      // no division per vector
+    int g = row - b * group;
+    const uint4* at = static_cast<const uint4*>(a.q) + ((static_cast<int64_t>(b) * a.hq + head * group + g) * (D / 8) + tid % (D / 8));
+    const int64_t step = (static_cast<int64_t>(step_b) * a.hq + step_g) * (D / 8), wrap = static_cast<int64_t>(a.hq - group) * (D / 8);
+    const int rows = a.batch * group;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        x[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (row < a.batch * a.group) x[i] = __ldg(reinterpret_cast<const uint4*>(q + (static_cast<int64_t>(b) * a.hq + g) * D));
+        x[i] = row < rows ? __ldg(at) : make_uint4(0u, 0u, 0u, 0u);
         row += STEP;
-        b += step_b;
+        at += step;
         g += step_g;
-        if (g >= a.group) {
-            g -= a.group;
-            ++b;
+        if (g >= group) {
+            g -= group;
+            at += wrap;
         }
     }
 #pragma unroll
@@ -1310,27 +1309,25 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix2_kernel(const __g
         const int t = (warp - 3) / 4, r = 32 * (warp % 4) + lane;
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp % 4)) << 16;
         const uint32_t st = tmem + lanes + t * 128, ot = tmem + lanes + L::O_COL + t * D;
-        const int total_rows = a.batch * a.group;
         constexpr float SH = Shift<T>::V;
         bool ok = true;
         auto wait = [&](uint32_t bar, uint32_t parity) {
             ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity & 1u, flag));
             return ok;
         };
-        int i = 0, c = 0;
+        int i = 0;
         PrefixSeg seg;
         for (int u = u0; ok && next_seg(a, u, u1, seg);) {
-            const int item = seg.item, t0 = seg.t0, n = seg.n;
-            const int head = item / a.prt, qrow0 = (item % a.prt) * 256 + t * 128;
+            const int item = seg.item, n = seg.n;
+            int left = a.plen - seg.t0 * 128;        // keys from the tile on
             // this tile's Q, by its own warps: the MMAs that read the last one have completed
-            load_q_tile<T, D, 32 * kPreSoftmaxWarps / 2>(gbase + L::OFF_Q + t * L::TILE, head, qrow0, r, a);
+            load_q_tile<T, D, 32 * kPreSoftmaxWarps / 2>(gbase + L::OFF_Q + t * L::TILE, item / a.prt, item % a.prt * 256 + t * 128, r, a);
             fence_async_smem();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full);
             float m = -INFINITY, l = 0.0f;
-            for (int j = 0; j < n; ++j, ++i) {
-                const int nk = min(128, a.plen - (t0 + j) * 128);
+            for (int j = 0; j < n; ++j, ++i, left -= 128) {
                 if (!wait(s_full(t), i)) break;
                 tc_fence_after();
                 float x[128];
@@ -1340,9 +1337,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix2_kernel(const __g
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(s_free(t));
-                if (nk < 128) {          // keys past the prefix's end
+                if (left < 128) {        // keys past the prefix's end
 #pragma unroll
-                    for (int k = 0; k < 128; ++k) x[k] = k >= nk ? -INFINITY : x[k];
+                    for (int k = 0; k < 128; ++k) x[k] = k >= left ? -INFINITY : x[k];
                 }
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -1389,12 +1386,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix2_kernel(const __g
                     }
                     tmem_st_wait();
                 }
-                if (nk < 128 && t == 0) {   // V rows past the end: 0 x whatever lies there must be 0
-                    const int cv = c + v_at(j, n);      // (row tile 1's PV is issued after row tile 0's)
+                if (left < 128 && t == 0) {   // V rows past the end: 0 x whatever lies there must be 0
+                    const int cv = 2 * (i - j) + v_at(j, n);      // (row tile 1's PV is issued after row tile 0's)
                     if (!wait(full(cv % RING), cv / RING)) break;
                     uint8_t* vb = gbase + L::OFF_KV + (cv % RING) * L::TILE;
-                    for (int v = r; v < (128 - nk) * L::ATOMS * 8; v += 128) {
-                        const int row = nk + v / (L::ATOMS * 8), ch = v % (L::ATOMS * 8);
+                    for (int v = r; v < (128 - left) * L::ATOMS * 8; v += 128) {
+                        const int row = left + v / (L::ATOMS * 8), ch = v % (L::ATOMS * 8);
                         *reinterpret_cast<uint4*>(vb + (ch / 8) * L::REGION + row * 128 + (ch % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
                     }
                 }
@@ -1406,7 +1403,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix2_kernel(const __g
             if (ok && wait(o_done(t), i - 1)) {
                 tc_fence_after();
                 const int64_t at = (static_cast<int64_t>(blockIdx.x) + item) * 256 + t * 128 + r;
-                const bool in = qrow0 + r < total_rows;
+                const bool in = item % a.prt * 256 + t * 128 + r < a.batch * a.group;
                 if (in) *reinterpret_cast<float4*>(a.pml + at * 4) = make_float4(m, l, 0.0f, 0.0f);
                 float* dst = a.po + at * D;
 #pragma unroll 1
@@ -1419,7 +1416,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix2_kernel(const __g
                         for (int e = 0; e < 4; ++e) st_v8(dst + 32 * k + 8 * e, o + 8 * e);
                 }
             }
-            c += 2 * n;
         }
     }
     tc_fence_before();

@@ -2,25 +2,31 @@
 // per group of inputs (the decode form of a projection).
 //
 // w_nk = (q_nk - z) s with one z and s per `group` consecutive k.  Reading the weight bounds the time
-// while the tokens are few: N K / 2 bytes and 2 N K / group of scales.  Each warp multiplies 16 weight
-// rows (the 16-row operand of mma.sync m16n8k16) with 8 NT tokens.  q - z is an integer in -15..15 and
-// exact in fp16 and bf16, so the tensor cores' products are exact; the sums of one group are
-// multiplied by the scale in fp32 when the group ends.  Nothing but Y is rounded.
+// while the tokens are few: N K / 2 bytes and 2 N K / group of scales.  q - z is an integer in -15..15 and
+// exact in fp16 and bf16, so the tensor cores' products are exact; the sums of one group are multiplied
+// by the scale in fp32 when the group ends.  Nothing but Y is rounded.  The weights are used as they are
+// stored, without repacking.  Two kernels:
 //
-// Layout: no repacking.  The order of k within a matrix instruction is free as long as both operands
-// agree, so lane 4 g + t takes consecutive k of its rows: one 128-k chunk gives it four 32-bit words of
-// row g and of row g + 8 (eight k each), from one 16-byte, two 8-byte or four 4-byte pieces for groups
-// of 128, 64 and 32, such that the four lanes of a row always work on the same group.  A warp takes two such
-// chunks at a time: a row's 128 bytes, one request of the copy engine, and half as much of the loop's own
-// work per weight.
+// w4_gemv_kernel, for few tokens.  Each warp multiplies 16 weight rows (the 16-row operand of mma.sync
+// m16n8k16) with 8 tokens; blocks of 8 tokens are the grid's second axis (the second block finds the
+// weights in L2).  The order of k within a matrix instruction is free as long as both operands agree, so
+// lane 4 g + t takes consecutive k of its rows: one 128-k chunk gives it four 32-bit words of row g and of
+// row g + 8 (eight k each), from one 16-byte, two 8-byte or four 4-byte pieces for groups of 128, 64 and
+// 32, such that the four lanes of a row always work on the same group.  A warp takes two such chunks at a
+// time: a row's 128 bytes, one request of the copy engine.
+// A CTA of eight computing warps covers 16 rows and 2048 inputs per stage.  One producing thread fills a
+// ring of stages by TMA (weights [8][16][128 B] and X [32][tokens][64 elements], 128-byte swizzle, scales
+// and zero points); a CTA stays for several row tiles, so that the ring runs on while a tile is finished.
+// Where the row tiles alone leave SMs idle, a cluster splits K and sums through distributed shared memory
+// in rank order.  Scales that the copy engine cannot fetch (a row's are not whole 16-byte pieces) are
+// loaded a block of stages ahead by the lanes instead: under load such a read takes microseconds, so the
+// ring is used wherever it can be (5 x 4096 x 14336, groups of 32 with zero points: 18.9 -> 15.0 us).
+// Two CTAs per SM with a ring of 112 KB each: three with 73 KB took 14.0 us where two take 12.9 (5 x 4096 x
+// 14336) and 19.8 where two take 18.4 (1 x 28672 x 4096, 3.3 TB/s).  What bounds the large sizes is the
+// work per weight between the ring and the tensor core (about 13 instructions per 8 weights to unpack);
+// the same copies without any arithmetic take 12.4 us for 1 x 28672 x 4096.
 //
-// A CTA of eight computing warps covers 16 WR rows and 256 WK inputs per stage (WR WK = 8): few tokens
-// put the warps along K, which keeps the row tiles small and the grid large; many put them along N,
-// which keeps the number of times that X is read from L2 down.  One producing thread fills a ring of
-// stages by TMA (weights [WK][16 WR][128 B] and X [4 WK][M][64 elements], 128-byte swizzle, two copies
-// per stage); a CTA stays for several row tiles, so that the ring runs on while a tile is finished.
-// Where the row tiles alone leave SMs idle, a cluster splits K and sums through distributed shared
-// memory in rank order.
+// w4_tile_kernel, for more tokens: see below.
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -37,11 +43,13 @@ namespace {
 
 constexpr int kW4Warps = 8;
 constexpr int kW4Threads = 32 * (kW4Warps + 1);   // warp 8 produces
+constexpr int kW4Rows = 16, kW4Cols = 8;          // weight rows and tokens of a tile: one matrix instruction's
 constexpr int kW4MaxStages = 8;
 constexpr int kW4Smem = 200 * 1024;               // most dynamic shared memory of a CTA
 
 struct W4Args {
     int M, N, K;
+    int mbox;          // tokens of a tile in shared memory
     int nchunk;        // whole 256-k chunks
     int split;         // CTAs of a cluster along K
     int tiles;         // row tiles
@@ -88,12 +96,11 @@ __device__ __forceinline__ void unpack_word(uint32_t w, uint32_t zb, uint32_t (&
 // Synchronize the computing warps (the loading warp goes on).
 __device__ __forceinline__ void sync_compute() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kW4Warps) : "memory"); }
 
-template <typename T, int G, int NT, bool TS>
-__global__ void __launch_bounds__(kW4Threads, NT <= 2 ? 3 : 1) w4_gemv_kernel(
+template <typename T, int G, bool TS>
+__global__ void __launch_bounds__(kW4Threads, 2) w4_gemv_kernel(
     const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX, const __grid_constant__ CUtensorMap mS,
     const __grid_constant__ CUtensorMap mZ, const __grid_constant__ W4Args a) {
-    constexpr int WR = NT, WK = kW4Warps / NT;
-    constexpr int ROWS = 16 * WR, COLS = 8 * NT, PITCH = ROWS + 4;
+    constexpr int WK = kW4Warps, ROWS = kW4Rows, COLS = kW4Cols, PITCH = ROWS + 4;
     constexpr int WPG = G / 32;         // words of a lane per group
     constexpr int NG = 8 / WPG;         // groups per 256-k chunk
     constexpr int RED = WK * COLS * PITCH;      // floats of one buffer of partial sums
@@ -106,6 +113,7 @@ __global__ void __launch_bounds__(kW4Threads, NT <= 2 ? 3 : 1) w4_gemv_kernel(
     const int rank = a.split > 1 ? static_cast<int>(cluster_rank()) : 0;
     const int nblk = (a.nchunk + WK - 1) / WK;                       // stages' worth of K
     const int iters = rank < nblk ? (nblk - rank + a.split - 1) / a.split : 0;
+    const int m0 = COLS * static_cast<int>(blockIdx.y), mrows = min(COLS, a.M - m0);      // this CTA's tokens
     // row tiles of this CTA: a split has one, else every gridDim.x-th
     const int tile0 = static_cast<int>(blockIdx.x) / a.split, tile_step = a.split > 1 ? a.tiles : static_cast<int>(gridDim.x);
     auto full = [&](int s) { return base + a.off_bar + 8u * s; };
@@ -130,7 +138,7 @@ __global__ void __launch_bounds__(kW4Threads, NT <= 2 ? 3 : 1) w4_gemv_kernel(
                 if (TS && a.z) prefetch_map(&mZ);
             }
             pdl_wait();
-            const uint32_t x_bytes = 4u * WK * a.M * 128u;
+            const uint32_t x_bytes = 4u * WK * a.mbox * 128u;
             const uint32_t bytes = WK * ROWS * 128u + (a.x_resident ? 0u : x_bytes) + (TS ? ROWS * SROW : 0u) + (TS && a.z ? ROWS * SROW / 2 : 0u);
             int s = 0, loads = 0;
             uint32_t phase = 0;      // completions of the current stage's barriers so far, mod 2
@@ -139,7 +147,7 @@ __global__ void __launch_bounds__(kW4Threads, NT <= 2 ? 3 : 1) w4_gemv_kernel(
             if (x_once) {
                 mbar_arrive_expect_tx(x_full, x_bytes * iters);
                 for (int it = 0; it < iters; ++it)
-                    tma_load_3d(base + a.x_off + it * x_bytes, &mX, 0, 0, 4 * (it * a.split + rank) * WK, x_full);
+                    tma_load_3d(base + a.x_off + it * x_bytes, &mX, 0, m0, 4 * (it * a.split + rank) * WK, x_full);
             }
             for (int tile = tile0; ok && tile < a.tiles; tile += tile_step) {
                 for (int it = 0; it < iters; ++it) {
@@ -150,7 +158,7 @@ __global__ void __launch_bounds__(kW4Threads, NT <= 2 ? 3 : 1) w4_gemv_kernel(
                     const int kb = (it * a.split + rank) * WK;           // first chunk of the stage
                     mbar_arrive_expect_tx(full(s), bytes);
                     tma_load_3d(base + s * a.stage_bytes, &mW, 0, tile * ROWS, kb, full(s));
-                    if (!a.x_resident) tma_load_3d(base + s * a.stage_bytes + a.x_off, &mX, 0, 0, 4 * kb, full(s));
+                    if (!a.x_resident) tma_load_3d(base + s * a.stage_bytes + a.x_off, &mX, 0, m0, 4 * kb, full(s));
                     if (TS) tma_load_3d(base + s * a.stage_bytes + a.s_off, &mS, kb * NG, tile * ROWS, 0, full(s));
                     if (TS && a.z) tma_load_3d(base + s * a.stage_bytes + a.s_off + ROWS * SROW, &mZ, kb * NG, tile * ROWS, 0, full(s));
                     ++loads;
@@ -169,23 +177,20 @@ __global__ void __launch_bounds__(kW4Threads, NT <= 2 ? 3 : 1) w4_gemv_kernel(
         if (a.split == 1) return;
     }
 
-    float acc[NT][4];
-    const int wr = warp % WR, wk = warp / WR;
+    float acc[4];
+    const int wk = warp;
     const int g = lane / 4, t = lane % 4;
     const T* bias = static_cast<const T*>(a.bias);
     const T* R = static_cast<const T*>(a.R);
     float* red = reinterpret_cast<float*>(gbase + a.off_red);   // [2][WK][COLS][PITCH]
     auto write_red = [&](float* buf) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                buf[(wk * COLS + 8 * nt + 2 * t + (e & 1)) * PITCH + 16 * wr + g + 8 * (e >> 1)] = acc[nt][e];
+        for (int e = 0; e < 4; ++e) buf[(wk * COLS + 2 * t + (e & 1)) * PITCH + g + 8 * (e >> 1)] = acc[e];
     };
     auto finish = [&](float v, int m, int n) {
         if (bias) v += to_f32(bias[n]);
         if (a.gelu) v = gelu_erf(v);
-        const int64_t at = static_cast<int64_t>(m) * a.N + n;
+        const int64_t at = static_cast<int64_t>(m0 + m) * a.N + n;
         if (R) v += to_f32(R[at]);
         static_cast<T*>(a.y)[at] = from_f32<T>(v);
     };
@@ -202,7 +207,7 @@ __global__ void __launch_bounds__(kW4Threads, NT <= 2 ? 3 : 1) w4_gemv_kernel(
         auto load_scale = [&](int tile, int gi, uint32_t& sc, uint32_t& zp) {
             sc = 0u;
             zp = 0x00080008u;
-            const int nlo = tile * ROWS + 16 * wr + g, nhi = nlo + 8;
+            const int nlo = tile * ROWS + g, nhi = nlo + 8;
             if (gi < KG && nlo < a.N) {   // past the last chunk or row: scale zero
                 const int64_t lo = static_cast<int64_t>(nlo) * KG + gi, hi = nhi < a.N ? lo + 8 * static_cast<int64_t>(KG) : lo;
                 const uint16_t* sp = static_cast<const uint16_t*>(a.s);
@@ -219,7 +224,7 @@ __global__ void __launch_bounds__(kW4Threads, NT <= 2 ? 3 : 1) w4_gemv_kernel(
         };
         // one group: WPG words of each row against the matching X pieces
         auto group = [&](int gi, const uint32_t* wl, const uint32_t* wh, auto&& xpiece, float2 s2, uint32_t zl, uint32_t zh) {
-            float part[NT][4] = {};
+            float part[4] = {};
             const uint32_t bl = Nib<T>::MAGIC | zl, bh = Nib<T>::MAGIC | zh;      // a row's zero point, twice
             const float sl = s2.x, sh = s2.y;
 #pragma unroll
@@ -228,51 +233,43 @@ __global__ void __launch_bounds__(kW4Threads, NT <= 2 ? 3 : 1) w4_gemv_kernel(
                 unpack_word<T>(wl[w], bl, pl);
                 unpack_word<T>(wh[w], bh, ph);
                 const uint32_t a0[4] = {pl[0], ph[0], pl[1], ph[1]}, a1[4] = {pl[2], ph[2], pl[3], ph[3]};
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const uint4 xv = xpiece(nt, gi, w);
-                    mma16816<T>(part[nt], a0, xv.x, xv.y);
-                    mma16816<T>(part[nt], a1, xv.z, xv.w);
-                }
+                const uint4 xv = xpiece(gi, w);
+                mma16816<T>(part, a0, xv.x, xv.y);
+                mma16816<T>(part, a1, xv.z, xv.w);
             }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                acc[nt][0] += sl * part[nt][0];
-                acc[nt][1] += sl * part[nt][1];
-                acc[nt][2] += sh * part[nt][2];
-                acc[nt][3] += sh * part[nt][3];
-            }
+            acc[0] += sl * part[0];
+            acc[1] += sl * part[1];
+            acc[2] += sh * part[2];
+            acc[3] += sh * part[3];
         };
         // k of word w of group gi within the chunk
         auto kof = [&](int gi, int w) { return gi * G + t * (G / 4) + 8 * w; };
         bool ok = true;
         // Where this lane's X pieces lie within a stage, of the chunk's eight words in the order of the groups:
-        // columns 8 nt + g are rows apart by 1024 bytes, which leaves the swizzle alone.  Rows past M are
-        // other rows or unused space: those columns are never stored.
-        uint32_t xoff[8];
+        // row g is column g of the product.  Rows past M are other rows or unused space: those columns are never stored.
+        // Words next to each other (or, in groups of 32, groups) share a row and differ in one or two bits of
+        // the piece: XP of them come from one offset by exclusive or.
+        constexpr int XP = G == 128 ? 4 : 2, XBIT = G == 32 ? 6 : 4;
+        uint32_t xoff[8 / XP];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int k8 = kof(i / WPG, i % WPG) / 8;                 // 16-byte piece of the chunk, 0..31
-            const uint32_t row = static_cast<uint32_t>((4 * wk + k8 / 8) * a.M + g);
+        for (int i = 0; i < 8 / XP; ++i) {
+            const int k8 = kof(i * XP / WPG, i * XP % WPG) / 8;       // 16-byte piece of the chunk, 0..31
+            const uint32_t row = static_cast<uint32_t>((4 * wk + k8 / 8) * a.mbox + g);
             xoff[i] = a.x_off + row * 128u + ((static_cast<uint32_t>(k8 & 7) ^ (row & 7u)) << 4);
         }
-        // the weights of group gi: byte gi G / 2 + t G / 8 of the row's 128, swizzled by the row
-        const uint32_t woff = static_cast<uint32_t>((wk * ROWS + 16 * wr + g) * 128), wsw = static_cast<uint32_t>(g & 7) << 4;
-        const uint32_t x_step = a.x_resident ? 4u * WK * a.M * 128u : 0u;
+        // the weights of group gi: byte gi G / 2 + t G / 8 of the row's 128, swizzled by the row (gi by exclusive or)
+        const uint32_t woff = static_cast<uint32_t>((wk * ROWS + g) * 128) + (static_cast<uint32_t>(t * (G / 8)) ^ (static_cast<uint32_t>(g & 7) << 4));
+        const uint32_t x_step = a.x_resident ? 4u * WK * a.mbox * 128u : 0u;
         uint32_t sc_next[SW], zp_next[SW], sc[SW] = {}, zp[SW] = {};
         if (!TS) load_scales(tile0, gfirst, sc_next, zp_next);
         // this lane's scales within a stage: row g (rows of 128 and 64 bytes swizzled), the warp's first group
-        const uint32_t srow = static_cast<uint32_t>(16 * wr + g) * SROW + wk * (NG * 2);
-        const uint32_t soff = srow ^ (G == 32 ? (srow >> 3) & 0x70u : G == 64 ? (srow >> 3) & 0x30u : 0u);
-        const uint32_t zoff = ROWS * SROW + static_cast<uint32_t>(16 * wr + g) * (SROW / 2) + wk * NG;
+        const uint32_t srow = static_cast<uint32_t>(g) * SROW + wk * (NG * 2);
         int s = 0, turn = 0;
         uint32_t phase = 0;
         if (a.x_resident && iters > 0) ok = __all_sync(0xffffffffu, mbar_wait_bounded(x_full, 0, a.flag));
         for (int tile = tile0; tile < a.tiles; tile += tile_step) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[nt][e] = 0.0f;
+            for (int e = 0; e < 4; ++e) acc[e] = 0.0f;
             uint32_t xres = 0;
             for (int it0 = 0; ok && it0 < iters; it0 += SB)
 #pragma unroll
@@ -293,11 +290,11 @@ __global__ void __launch_bounds__(kW4Threads, NT <= 2 ? 3 : 1) w4_gemv_kernel(
                 }
                 // plain loads: the compiler keeps them behind the wait, and free to move among the rest
                 const uint32_t stage = s * a.stage_bytes;
-                const uint8_t* xs = gbase + (a.x_resident ? xres : stage);
+                const uint32_t xs = a.x_resident ? xres : stage;
                 xres += x_step;
-                const uint8_t* wbase = gbase + stage + woff;
-                auto xpiece = [&](int nt, int gi, int w) {
-                    return *reinterpret_cast<const uint4*>(xs + xoff[gi * WPG + w] + nt * 1024);
+                auto xpiece = [&](int gi, int w) {
+                    const int i = gi * WPG + w;
+                    return *reinterpret_cast<const uint4*>(gbase + ((xs + xoff[i / XP]) ^ (i % XP << XBIT)));
                 };
                 // (TS) scales and zero points of up to four groups, rows g and g + 8
                 constexpr int NS = NG < 4 ? NG : 4;
@@ -306,8 +303,9 @@ __global__ void __launch_bounds__(kW4Threads, NT <= 2 ? 3 : 1) w4_gemv_kernel(
                 for (int gi = 0; gi < NG; ++gi) {
                     uint32_t wl[WPG], wh[WPG];
                     if (TS && gi % NS == 0) {
+                        const uint32_t soff = srow ^ (G == 32 ? (srow >> 3) & 0x70u : G == 64 ? (srow >> 3) & 0x30u : 0u);
                         const uint8_t* sp = gbase + stage + a.s_off + soff + 2 * gi;
-                        const uint8_t* zq = gbase + stage + a.s_off + zoff + gi;
+                        const uint8_t* zq = gbase + stage + a.s_off + ROWS * SROW + srow / 2 + gi;
                         if constexpr (NG < 4) {
                             sl[0] = *reinterpret_cast<const uint32_t*>(sp);
                             sh[0] = *reinterpret_cast<const uint32_t*>(sp + 8 * SROW);
@@ -329,7 +327,7 @@ __global__ void __launch_bounds__(kW4Threads, NT <= 2 ? 3 : 1) w4_gemv_kernel(
                             zh &= 0x0F0Fu;
                         }
                     }
-                    const uint8_t* at = wbase + (static_cast<uint32_t>(gi * (G / 2) + t * (G / 8)) ^ wsw);
+                    const uint8_t* at = gbase + ((stage + woff) ^ (gi * (G / 2)));
                     if constexpr (WPG == 4) {
                         const uint4 l = *reinterpret_cast<const uint4*>(at), h = *reinterpret_cast<const uint4*>(at + 1024);
                         wl[0] = l.x; wl[1] = l.y; wl[2] = l.z; wl[3] = l.w;
@@ -362,7 +360,7 @@ __global__ void __launch_bounds__(kW4Threads, NT <= 2 ? 3 : 1) w4_gemv_kernel(
             }
             // the last K % 256 inputs, from global memory by the first K warps
             if (ok && rank == 0 && wk == 0 && a.nchunk * 256 < a.K) {
-                const int k0 = a.nchunk * 256, nlo = tile * ROWS + 16 * wr + g, nhi = nlo + 8;
+                const int k0 = a.nchunk * 256, nlo = tile * ROWS + g, nhi = nlo + 8;
                 const T* x = static_cast<const T*>(a.x);
                 const uint8_t* wq = static_cast<const uint8_t*>(a.wq);
                 const int ng = (a.K - k0) / G;
@@ -375,9 +373,8 @@ __global__ void __launch_bounds__(kW4Threads, NT <= 2 ? 3 : 1) w4_gemv_kernel(
                         wl[w] = nlo < a.N ? *reinterpret_cast<const uint32_t*>(wq + static_cast<int64_t>(nlo) * (a.K / 2) + at) : 0u;
                         wh[w] = nhi < a.N ? *reinterpret_cast<const uint32_t*>(wq + static_cast<int64_t>(nhi) * (a.K / 2) + at) : 0u;
                     }
-                    auto xpiece = [&](int nt, int gj, int w) {
-                        const int m = min(8 * nt + g, a.M - 1);
-                        return *reinterpret_cast<const uint4*>(x + static_cast<int64_t>(m) * a.K + k0 + kof(gj, w));
+                    auto xpiece = [&](int gj, int w) {
+                        return *reinterpret_cast<const uint4*>(x + static_cast<int64_t>(m0 + min(g, mrows - 1)) * a.K + k0 + kof(gj, w));
                     };
                     group(gi, wl, wh, xpiece, unpack2<T>(tsc), __byte_perm(tzp, 0u, 0x1010), __byte_perm(tzp, 0u, 0x3232));
                 }
@@ -389,7 +386,7 @@ __global__ void __launch_bounds__(kW4Threads, NT <= 2 ? 3 : 1) w4_gemv_kernel(
             ++turn;
             write_red(buf);
             sync_compute();
-            for (int i = threadIdx.x; i < ROWS * a.M; i += 32 * kW4Warps) {
+            for (int i = threadIdx.x; i < ROWS * mrows; i += 32 * kW4Warps) {
                 const int m = i / ROWS, r = i % ROWS, n = tile * ROWS + r;
                 if (n >= a.N) continue;
                 float v = 0.0f;
@@ -405,7 +402,7 @@ __global__ void __launch_bounds__(kW4Threads, NT <= 2 ? 3 : 1) w4_gemv_kernel(
     __syncthreads();
     if (warp < kW4Warps) write_red(red);
     __syncthreads();
-    const int per = ROWS * a.M;
+    const int per = ROWS * mrows;
     for (int i = threadIdx.x; i < per; i += kW4Threads) {
         const int m = i / ROWS, r = i % ROWS;
         float v = red[m * PITCH + r];
@@ -432,18 +429,20 @@ __global__ void __launch_bounds__(kW4Threads, NT <= 2 ? 3 : 1) w4_gemv_kernel(
     cluster_sync();   // the sums stay in place until every CTA has read them
 }
 
-template <typename T, int G, int NT, bool TS>
+template <typename T, int G, bool TS>
 int launch_w4(W4Args a, cudaStream_t st) {
-    constexpr int WR = NT, WK = kW4Warps / NT, ROWS = 16 * WR;
+    constexpr int WK = kW4Warps, ROWS = kW4Rows;
     constexpr uint32_t SROW = WK * (256 / G) * 2;
     CUtensorMap mW{}, mX{}, mS{}, mZ{};
+    a.mbox = a.M < kW4Cols ? a.M : kW4Cols;
+    const int blocks = static_cast<int>(ceil_div(a.M, kW4Cols));
     a.nchunk = a.K / 256;
     // a map needs a chunk to describe; without one (K < 256) no stage is loaded
     if (a.nchunk > 0) {
         const int64_t wd[3] = {128, a.N, a.nchunk}, ws[2] = {a.K / 2, 128};
         const int wb[3] = {128, ROWS, WK};
         const int64_t xd[3] = {64, a.M, 4 * static_cast<int64_t>(a.nchunk)}, xs[2] = {static_cast<int64_t>(a.K) * 2, 128};
-        const int xb[3] = {64, a.M, 4 * WK};
+        const int xb[3] = {64, a.mbox, 4 * WK};
         if (!make_map_3d(&mW, a.wq, kMapU8, wd, ws, wb, 128) || !make_map_3d(&mX, a.x, kMap16, xd, xs, xb, 128)) return FUSE_ECUDA;
         if (TS) {
             const int64_t kg = a.K / G, sd[3] = {kg, a.N, 1}, ss[2] = {kg * 2, kg * 2 * a.N}, zs[2] = {kg, kg * a.N};
@@ -455,22 +454,21 @@ int launch_w4(W4Args a, cudaStream_t st) {
     a.tiles = static_cast<int>(ceil_div(a.N, ROWS));
     const int nblk = static_cast<int>(ceil_div(a.nchunk, WK));
     a.split = 1;
-    while (a.split < 8 && a.tiles * a.split * 2 <= 2 * sm_count() && nblk >= 2 * a.split) a.split *= 2;
+    while (a.split < 8 && a.tiles * blocks * a.split * 2 <= 2 * sm_count() && nblk >= 2 * a.split) a.split *= 2;
     const int iters = static_cast<int>(ceil_div(nblk > 0 ? nblk : 1, a.split));
     // X stays in shared memory for all of a CTA's tiles where it is small (whole stages of it keep the
-    // swizzle's phase: 4 WK M rows are a multiple of 8), else it comes with every stage
-    const int x_stage = 4 * WK * a.M * 128;
-    a.x_resident = NT <= 2 && a.split == 1 && a.tiles > sm_count() && iters * x_stage <= 32 * 1024 ? 1 : 0;
+    // swizzle's phase: 4 WK mbox rows are a multiple of 8), else it comes with every stage
+    const int x_stage = 4 * WK * a.mbox * 128;
+    a.x_resident = a.split == 1 && a.tiles > sm_count() && iters * x_stage <= 32 * 1024 ? 1 : 0;
     const uint32_t w_stage = WK * ROWS * 128;
     a.s_off = w_stage + (a.x_resident ? 0 : x_stage);
     a.stage_bytes = (a.s_off + (TS ? ROWS * SROW + (a.z ? ROWS * SROW / 2 : 0) : 0) + 1023) / 1024 * 1024;
     const uint32_t x_all = a.x_resident ? iters * x_stage : 0;
-    const uint32_t pad = 8 * NT * 128;      // columns past M are read from behind the last rows of X
-    const bool several = NT <= 2 && a.split == 1;     // row tiles per CTA, with two buffers of partial sums
-    const uint32_t red = static_cast<uint32_t>((several ? 2 : 1) * WK * 8 * NT * (ROWS + 4) * 4);
+    const uint32_t pad = kW4Cols * 128;     // columns past M are read from behind the last rows of X
+    const bool several = a.split == 1;     // row tiles per CTA, with two buffers of partial sums
+    const uint32_t red = static_cast<uint32_t>((several ? 2 : 1) * WK * kW4Cols * (ROWS + 4) * 4);
     const uint32_t bars = 8 * (2 * kW4MaxStages + 1);
-    const int per_sm = static_cast<int>(ceil_div(static_cast<int64_t>(a.tiles) * a.split, sm_count()));
-    const uint32_t budget = NT > 2 ? kW4Smem : per_sm > 2 ? 73 * 1024 : 112 * 1024;   // 1, 3 or 2 CTAs per SM
+    constexpr uint32_t budget = 112 * 1024;     // two CTAs per SM
     const int want = a.split > 1 ? iters : kW4MaxStages;
     a.stages = want < kW4MaxStages ? want : kW4MaxStages;
     while (a.stages > 2 && a.stages * a.stage_bytes + x_all + red + pad + bars + 1024 > budget) --a.stages;
@@ -479,7 +477,7 @@ int launch_w4(W4Args a, cudaStream_t st) {
     a.off_bar = a.off_red + (red + 15) / 16 * 16;
     const uint32_t smem = a.off_bar + bars + 1024;
     if (smem > kW4Smem) return FUSE_EUNSUPPORTED;
-    const int rc = opt_in_smem((const void*)w4_gemv_kernel<T, G, NT, TS>, kW4Smem, true);
+    const int rc = opt_in_smem((const void*)w4_gemv_kernel<T, G, TS>, kW4Smem, true);
     if (rc != FUSE_OK) return rc;
     int64_t grid = static_cast<int64_t>(a.tiles) * a.split;
     if (several) {   // as many CTAs as are resident; each takes every grid-th row tile
@@ -487,13 +485,13 @@ int launch_w4(W4Args a, cudaStream_t st) {
         const uint32_t kb = (smem + 1023) / 1024;
         uint32_t k = known.load(std::memory_order_relaxed);
         if ((k >> 8) != kb) {
-            k = (kb << 8) | static_cast<uint32_t>(blocks_per_sm(w4_gemv_kernel<T, G, NT, TS>, kW4Threads, kb * 1024));
+            k = (kb << 8) | static_cast<uint32_t>(blocks_per_sm(w4_gemv_kernel<T, G, TS>, kW4Threads, kb * 1024));
             known.store(k, std::memory_order_relaxed);
         }
-        const int64_t resident = static_cast<int64_t>(sm_count()) * (k & 255u);
+        const int64_t resident = static_cast<int64_t>(sm_count()) * (k & 255u) / blocks > 0 ? static_cast<int64_t>(sm_count()) * (k & 255u) / blocks : 1;
         if (grid > resident) grid = resident;
     }
-    return launch_pdl(w4_gemv_kernel<T, G, NT, TS>, dim3(static_cast<unsigned>(grid)), dim3(kW4Threads), smem, st, a.split, mW, mX, mS, mZ, a);
+    return launch_pdl(w4_gemv_kernel<T, G, TS>, dim3(static_cast<unsigned>(grid), static_cast<unsigned>(blocks)), dim3(kW4Threads), smem, st, a.split, mW, mX, mS, mZ, a);
 }
 
 // ================================================================== tcgen05 tiles
@@ -501,6 +499,10 @@ int launch_w4(W4Args a, cudaStream_t st) {
 // tensor memory as the A operand of tcgen05.mma (128 weight rows x 128 k per unit, two 16-bit integers per
 // TMEM column), X is the B operand from shared memory, and every group of k has its own fp32 accumulator
 // in TMEM, which is read out, multiplied by the group's scale and added up in registers.
+//
+// Measured: 64 x 28672 x 4096 in groups of 64 35.5 us, 64 x 4096 x 4096 in groups of 128 12.6 us.  Not the loads but
+// the chain of a unit (unpack, MMAs, read-out) and its instructions bound it: the SMs issue half of the time, and
+// separate warps for unpacking and reading out were no faster (38.5 us).
 //
 // 320 threads: warps 0-7 work (TMEM lane quadrant warp % 4, i.e. 32 weight rows, one per lane; half
 // warp / 4 of a unit's k when unpacking and of the tokens when reading out), warp 8 issues the MMAs, warp 9
@@ -924,17 +926,14 @@ int launch_tile(const W4Args& w, cudaStream_t st) {
 template <typename T, int G>
 int run_w4_g(const W4Args& a, cudaStream_t st) {
     const bool fits = scales_fit(a, G);
-    // Up to 16 tokens w4_gemv_kernel is quicker until there is a tile of 128 rows per SM: at 16 x 4096 x 4096 it takes
-    // 7.8 us (tiles 10.3), at 8192 x 8192 23.4 (27.5), at 14336 x 4096 20.7 (21.7), at 28672 x 4096 39 (28).
+    // Up to 16 tokens w4_gemv_kernel (two blocks of 8) is quicker until there is a tile of 128 rows per SM: at 16 x 4096 x
+    // 4096 it takes 7.6 us (tiles 10.4), at 8192 x 8192 21.5 (27.5), at 14336 x 4096 18.1 (21.6), at 28672 x 4096 33 (28).
     if (fits && (a.M > 16 || (a.M > 8 && ceil_div(a.N, 128) > sm_count()))) {
         if (a.M <= 16) return launch_tile<T, G, 16>(a, st);
         if (a.M <= 32) return launch_tile<T, G, 32>(a, st);
         return launch_tile<T, G, 64>(a, st);
     }
-    if (a.M <= 8) return fits ? launch_w4<T, G, 1, true>(a, st) : launch_w4<T, G, 1, false>(a, st);
-    if (a.M <= 16) return launch_w4<T, G, 2, false>(a, st);
-    if (a.M <= 32) return launch_w4<T, G, 4, false>(a, st);
-    return launch_w4<T, G, 8, false>(a, st);
+    return fits ? launch_w4<T, G, true>(a, st) : launch_w4<T, G, false>(a, st);
 }
 template <typename T>
 int run_w4(const W4Args& a, int group, cudaStream_t st) {
@@ -946,31 +945,27 @@ int run_w4(const W4Args& a, int group, cudaStream_t st) {
 template <typename T, int G>
 int w4_entry(int i, const char* const* names, fuse_kernel_record* out) {
     switch (i) {
-        case 0: return describe_kernel((const void*)w4_gemv_kernel<T, G, 1, true>, names[0], kW4Threads, 110 * 1024, out);
-        case 1: return describe_kernel((const void*)w4_gemv_kernel<T, G, 1, false>, names[1], kW4Threads, 110 * 1024, out);
-        case 2: return describe_kernel((const void*)w4_gemv_kernel<T, G, 2, false>, names[2], kW4Threads, 110 * 1024, out);
-        case 3: return describe_kernel((const void*)w4_gemv_kernel<T, G, 4, false>, names[3], kW4Threads, 110 * 1024, out);
-        case 4: return describe_kernel((const void*)w4_gemv_kernel<T, G, 8, false>, names[4], kW4Threads, 110 * 1024, out);
-        case 5: return describe_kernel((const void*)w4_tile_kernel<T, G, 16>, names[5], kTileThreads, TileLayout<16>::SMEM, out, kTileCols);
-        case 6: return describe_kernel((const void*)w4_tile_kernel<T, G, 32>, names[6], kTileThreads, TileLayout<32>::SMEM, out, kTileCols);
-        default: return describe_kernel((const void*)w4_tile_kernel<T, G, 64>, names[7], kTileThreads, TileLayout<64>::SMEM, out, kTileCols);
+        case 0: return describe_kernel((const void*)w4_gemv_kernel<T, G, true>, names[0], kW4Threads, 110 * 1024, out);
+        case 1: return describe_kernel((const void*)w4_gemv_kernel<T, G, false>, names[1], kW4Threads, 110 * 1024, out);
+        case 2: return describe_kernel((const void*)w4_tile_kernel<T, G, 16>, names[2], kTileThreads, TileLayout<16>::SMEM, out, kTileCols);
+        case 3: return describe_kernel((const void*)w4_tile_kernel<T, G, 32>, names[3], kTileThreads, TileLayout<32>::SMEM, out, kTileCols);
+        default: return describe_kernel((const void*)w4_tile_kernel<T, G, 64>, names[4], kTileThreads, TileLayout<64>::SMEM, out, kTileCols);
     }
 }
 
 }  // namespace
 
-int w4_report_count() { return 48; }
+int w4_report_count() { return 30; }
 int w4_report(int i, fuse_kernel_record* out) {
-    if (i < 0 || i >= 48) return FUSE_EINVAL;
-#define FC_W4(T, G)                                                                                                       \
-    {"w4_gemv_kernel<" T ", group " G ", M <= 8>", "w4_gemv_kernel<" T ", group " G ", M <= 8, any alignment>",           \
-     "w4_gemv_kernel<" T ", group " G ", M <= 16, any alignment>", "w4_gemv_kernel<" T ", group " G ", M <= 32, any alignment>", \
-     "w4_gemv_kernel<" T ", group " G ", M <= 64, any alignment>", "w4_tile_kernel<" T ", group " G ", M <= 16> (tcgen05)", \
-     "w4_tile_kernel<" T ", group " G ", M <= 32> (tcgen05)", "w4_tile_kernel<" T ", group " G ", M <= 64> (tcgen05)"}
-    static const char* const names[6][8] = {FC_W4("bf16", "32"), FC_W4("bf16", "64"), FC_W4("bf16", "128"),
+    if (i < 0 || i >= 30) return FUSE_EINVAL;
+#define FC_W4(T, G)                                                                                             \
+    {"w4_gemv_kernel<" T ", group " G ">", "w4_gemv_kernel<" T ", group " G ", scales of any alignment>",       \
+     "w4_tile_kernel<" T ", group " G ", M <= 16> (tcgen05)", "w4_tile_kernel<" T ", group " G ", M <= 32> (tcgen05)", \
+     "w4_tile_kernel<" T ", group " G ", M <= 64> (tcgen05)"}
+    static const char* const names[6][5] = {FC_W4("bf16", "32"), FC_W4("bf16", "64"), FC_W4("bf16", "128"),
                                             FC_W4("f16", "32"), FC_W4("f16", "64"), FC_W4("f16", "128")};
 #undef FC_W4
-    const int k = i / 8, v = i % 8;
+    const int k = i / 5, v = i % 5;
     switch (k) {
         case 0: return w4_entry<__nv_bfloat16, 32>(v, names[k], out);
         case 1: return w4_entry<__nv_bfloat16, 64>(v, names[k], out);
