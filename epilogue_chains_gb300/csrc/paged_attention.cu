@@ -13,13 +13,13 @@
 //    warp loads units by TMA into a ring, four compute: each multiplies its 16 keys of a unit with the
 //    query rows by mma.sync (16 rows, mostly one group), and the warps' parts meet in shared memory when
 //    a run ends.  Parts of a sequence that several CTAs share go through the workspace: the CTA that
-//    arrives last joins them, in the order of the keys.  3 x 65536 keys (D = 128) take 110 us, 0.96 of
+//    arrives last joins them, in the order of the keys (with a prefix, paged_join_kernel does).  3 x 65536 keys (D = 128) take 110 us, 0.96 of
 //    the copy rate; 32 sequences of up to 4096 keys 51.6 us, 0.80.
 //  * paged_prefix_kernel, paged_prefix2_kernel: the shared prefix.  Here all batch * group query rows of a
 //    key/value head meet the same keys: tcgen05 tiles of 128 or 256 rows by 128 keys, scores and output
 //    in TMEM, the key axis split over the SMs.  1024 rows per head over 16384 keys (8 heads, D = 128) take
-//    57 us of the call's 101, 1.2 PFLOP/s.
-//  * paged_join_kernel, with a prefix: a row's own part and the prefix's parts.
+//    59 us of the call's 101, 1.2 PFLOP/s.
+//  * paged_join_kernel, with a prefix: a row's own parts and the prefix's.
 //
 // The lengths are in device memory, so one launch configuration (and a captured graph) serves every
 // length.  All waits are bounded (watchdog).
@@ -83,7 +83,10 @@ struct PagedArgs {
     // names its counter).
     int* count;                        // [kOwnGrid][kOwnWarps] parts that have arrived, by the item's first CTA
     float *oml, *oo;                   // [2 kOwnGrid][rows] (m, l) and [..][rows][D]
-    float *rml, *ro;                   // with a prefix: own part of every row, [batch hq] (m, l) and [..][D]
+    // with a prefix: where the own parts of an item (sequence, row tile of a key/value head) are, -1: in rml and ro
+    // (it has one), else the CTAs that have them, first | last << 16; [batch hk rt]
+    int* where;
+    float *rml, *ro;                   // [batch hq] (m, l) and [..][D]
     float *pml, *po;                   // [kPrefixGrid + pitems][prow] (m, l, l', -) and [..][prow][D]
     // prefix
     int plen, ptiles, prow, prt, pgrid; // keys, 128-key tiles, rows of an item (128 or 256), a head's items, CTAs
@@ -280,6 +283,10 @@ __global__ void __launch_bounds__(kOwnThreads, OwnLayout<D>::CTAS) paged_own_ker
             if (i >= total) return;
             Cursor k;
             locate(u0 + i, k);
+            if (a.plen > 0 && k.j == 0) {
+                const int c0 = static_cast<int>(blockIdx.x), c1 = cta_of(u0 + i + k.n - 1, U, G);
+                a.where[k.b * HR + k.hr] = c1 == c0 ? -1 : c0 | c1 << 16;
+            }
             const int head = k.hr / a.rt, nk = min(kUnit, k.len - k.j * kUnit);
             if (k.j < 0 || nk <= 0) return;
             p.shift = nk == kUnit ? big_shift : 4;
@@ -367,7 +374,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnLayout<D>::CTAS) paged_own_ker
             for (int j = max(0, loads - a.slots); j < loads; ++j) (void)mbar_wait_drain(full(j % a.slots), (j / a.slots) & 1);
             for (int j = max(0, qloads - L::NQ); j < qloads; ++j) (void)mbar_wait_drain(q_full(j % L::NQ), (j / L::NQ) & 1);
         }
-        if (a.plen > 0) pdl_wait();      // this kernel is not over before the prefix's is
+        if (a.plen > 0 && blockIdx.x == 0) pdl_wait();      // this kernel is not over before the prefix's is
         return;
     }
 
@@ -421,7 +428,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnLayout<D>::CTAS) paged_own_ker
                     w.x = l == 0.0f ? 0u : pack2<T>(acc.x * inv, acc.y * inv);
                     w.y = l == 0.0f ? 0u : pack2<T>(acc.z * inv, acc.w * inv);
                     *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + (orow + r) * D + 4 * col) = w;
-                } else {   // a part for the item's last CTA, or the row's own part for paged_join_kernel
+                } else {   // a part for the item's last CTA, or for paged_join_kernel
                     const int64_t at = last ? orow + r : static_cast<int64_t>(2 * blockIdx.x + (k.j0 == 0 ? 1 : 0)) * a.rows + r;
                     // (m, l) of a row goes with the first of its columns that this warp holds: every warp's
                     // share is read back by the same warp of another CTA
@@ -429,7 +436,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnLayout<D>::CTAS) paged_own_ker
                     *reinterpret_cast<float4*>((last ? a.ro : a.oo) + at * D + 4 * col) = acc;
                 }
             }
-            if (last) return;
+            if (last || a.plen > 0) return;
             __threadfence();
             __syncwarp();
             int* count = a.count + c0 * kOwnWarps + warp;
@@ -671,7 +678,8 @@ __device__ __forceinline__ bool next_seg(const PagedArgs& a, int& u, int u1, Pre
     return false;
 }
 
-// With a shared prefix, the last step: a row's own part and the prefix's parts.  One warp per query row, lane c
+// With a shared prefix, the last step: the prefix's parts of a row and its own.  It is bound by latency: 48 rows per
+// head and 8 heads take 6 us, 1024 rows per head 8.  One warp per query row, lane c
 // taking D / 32 columns.
 constexpr int kJoinThreads = 128;
 template <typename T, int D>
@@ -688,9 +696,12 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     const int64_t per = a.ptiles + a.pent, PU = a.hk * a.prt * per, u = pit * per + a.pent;
     const int c0 = cta_of(u, PU, a.pgrid), np = cta_of(u + a.ptiles - 1, PU, a.pgrid) - c0 + 1;
     pdl_wait();
-    // lane 0 has the row's own part (after that: what has been joined), lanes 1 .. kParts the prefix's.  The
-    // columns of a batch are loaded next to its maxima and sums, so one memory latency is waited for, not three.
+    // Lane 0 has what has been joined, lanes 1 .. kParts a part each: the prefix's, then the row's own.  The columns
+    // of a batch are loaded next to its maxima and sums, so one memory latency is waited for, not three (two, where
+    // the own parts have to be looked up; the prefix's are on their way by then).
     constexpr int kParts = 7;
+    const int tile = h % a.group / 16, w = __ldcg(a.where + (b * a.hk + head) * a.rt + tile);
+    const int o0 = w < 0 ? 0 : w & 0xffff, own = w < 0 ? 1 : (w >> 16) - o0 + 1, all = own + np;
     auto load = [&](float (&v)[W], const float* src) {
         if constexpr (W == 2) {
             const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
@@ -707,41 +718,43 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
             }
         }
     };
-    float m = -INFINITY, l = 0.0f, acc[W];
-    load(acc, a.ro + row * D + W * lane);
-    if (lane == 0) {
-        const float2 x = __ldcg(reinterpret_cast<const float2*>(a.rml + 2 * row));
-        m = x.x;
-        l = x.y;
-    }
-    for (int p0 = 0; p0 < np; p0 += kParts) {
-        const int n = min(kParts, np - p0);
-        const int64_t first = (static_cast<int64_t>(c0 + p0) + pit) * rpi + prow % rpi;   // parts are rpi rows apart
+    float m = -INFINITY, l = 0.0f, acc[W] = {};
+    const int64_t pre0 = static_cast<int64_t>(c0 + pit) * rpi + prow % rpi;          // the prefix's parts are rpi rows apart
+    auto own_at = [&](int p) { return static_cast<int64_t>(2 * (o0 + p) + (p == 0 ? 1 : 0)) * a.rows + h % a.group % 16; };
+    for (int p0 = 0; p0 < all; p0 += kParts) {
         float v[kParts][W];
 #pragma unroll
-        for (int c = 0; c < kParts; ++c) load(v[c], a.po + (first + rpi * min(c, n - 1)) * D + W * lane);
+        for (int c = 0; c < kParts; ++c) {
+            if (p0 + c < np) load(v[c], a.po + (pre0 + static_cast<int64_t>(rpi) * (p0 + c)) * D + W * lane);
+            else load(v[c], (w < 0 ? a.ro + row * D : a.oo + own_at(min(p0 + c, all - 1) - np) * D) + W * lane);
+        }
         float pm = lane == 0 ? m : -INFINITY, pl = lane == 0 ? l : 0.0f;
-        if (lane >= 1 && lane <= n) {
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(a.pml + (first + rpi * (lane - 1)) * 4));
+        const int p = p0 + lane - 1;
+        if (lane >= 1 && lane <= kParts && p < np) {
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(a.pml + (pre0 + static_cast<int64_t>(rpi) * p) * 4));
             pm = x.x;
             pl = x.y + x.z;
+        } else if (lane >= 1 && lane <= kParts && p < all) {
+            const float2 x = __ldcg(reinterpret_cast<const float2*>(w < 0 ? a.rml + row * 2 : a.oml + own_at(p - np) * 2));
+            pm = x.x;
+            pl = x.y;
         }
         float top = pm;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float w = pm == -INFINITY ? 0.0f : ex2f(pm - top);
-        float sum = pl * w;
+        const float e = pm == -INFINITY ? 0.0f : ex2f(pm - top);
+        float sum = pl * e;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const float w0 = __shfl_sync(0xffffffffu, w, 0);
+        const float e0 = __shfl_sync(0xffffffffu, e, 0);
 #pragma unroll
-        for (int e = 0; e < W; ++e) acc[e] *= w0;
+        for (int i = 0; i < W; ++i) acc[i] *= e0;
 #pragma unroll
         for (int c = 0; c < kParts; ++c) {
-            const float wc = __shfl_sync(0xffffffffu, w, c + 1);
-            if (c < n)
+            const float ec = __shfl_sync(0xffffffffu, e, c + 1);
+            if (p0 + c < all)
 #pragma unroll
-                for (int e = 0; e < W; ++e) acc[e] += wc * v[c][e];
+                for (int i = 0; i < W; ++i) acc[i] += ec * v[c][i];
         }
         m = top;
         l = sum;
@@ -1433,7 +1446,7 @@ int64_t prefix_rows(int64_t rows, int64_t D) { return rows > 128 && D <= 128 ? 2
 
 struct Sizes {
     int64_t rows, prow, pitems;      // rows per part of own keys; of the prefix, and its items
-    size_t count, oml, oo, rml, ro, pml, po;  // byte offsets of the workspace's parts
+    size_t count, oml, oo, where, rml, ro, pml, po;  // byte offsets of the workspace's parts
     size_t bytes;
 };
 Sizes sizes(int64_t batch, int64_t hq, int64_t hk, int64_t D, int64_t plen) {
@@ -1452,6 +1465,7 @@ Sizes sizes(int64_t batch, int64_t hq, int64_t hk, int64_t D, int64_t plen) {
     s.oml = part(2 * kOwnGrid * s.rows * 8);
     s.oo = part(2 * kOwnGrid * s.rows * D * 4);
     if (plen > 0) {
+        s.where = part(batch * hk * ceil_div(group, 16) * 4);
         s.rml = part(batch * hq * 8);
         s.ro = part(batch * hq * D * 4);
         s.pml = part((kPrefixGrid + s.pitems) * s.prow * 16);
@@ -1641,6 +1655,7 @@ extern "C" int fuse_paged_attention(const void* q, const void* k_cache, const vo
     a.count = reinterpret_cast<int*>(ws + s.count);
     a.oml = reinterpret_cast<float*>(ws + s.oml);
     a.oo = reinterpret_cast<float*>(ws + s.oo);
+    a.where = reinterpret_cast<int*>(ws + s.where);
     a.rml = reinterpret_cast<float*>(ws + s.rml);
     a.ro = reinterpret_cast<float*>(ws + s.ro);
     a.pml = reinterpret_cast<float*>(ws + s.pml);

@@ -143,9 +143,9 @@ def test_paged_workspace_is_host_arithmetic():
     # counters, then (m, l) and fp32 output rows of two parts for each of at most 320 CTAs
     assert ws(1, 32, 8, 128) == 8192 + 640 * 4 * 8 + 640 * 4 * 128 * 4
     assert ws(512, 32, 8, 128) == ws(1, 32, 8, 128)          # independent of the batch
-    # with a prefix: every row's own part, and 256-row parts (128 rows up to 128 rows or D = 256) of
+    # with a prefix: where an item's own parts are, every row's own part, and 256-row parts (128 rows up to 128 rows or D = 256) of
     # at most 160 CTAs and one more per item
-    assert ws(64, 32, 8, 128, 100) == ws(1, 32, 8, 128) + 64 * 32 * (8 + 512) + (160 + 8) * 256 * (16 + 512)
+    assert ws(64, 32, 8, 128, 100) == ws(1, 32, 8, 128) + 64 * 8 * 4 + 64 * 32 * (8 + 512) + (160 + 8) * 256 * (16 + 512)
     assert ws(1, 30, 8, 128) == 0 and ws(0, 32, 8, 128) == 0
 
 
