@@ -815,7 +815,7 @@ __device__ __forceinline__ void load_q_tile(uint8_t* tile, int head, int qrow0, 
     const int rows = a.batch * group;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        x[i] = row < rows ? __ldg(at) : make_uint4(0u, 0u, 0u, 0u);
+        x[i] = row < rows ? __ldcg(at) : make_uint4(0u, 0u, 0u, 0u);
         row += STEP;
         at += step;
         g += step_g;

@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kRopeBlock) rope_append_kernel(const __grid_co
     if (turn && pos_ok && h0 < p.hq + p.hk) {
         const float4* row = reinterpret_cast<const float4*>(p.cs + pos * p.rot) + 2 * pair;
         const float4* rs = row + p.rot / 8;
-        const float4 c0 = __ldg(row), c1 = __ldg(row + 1), s0 = __ldg(rs), s1 = __ldg(rs + 1);
+        const float4 c0 = row[0], c1 = row[1], s0 = rs[0], s1 = rs[1];
         c[0] = c0.x; c[1] = c0.y; c[2] = c0.z; c[3] = c0.w;
         c[4] = c1.x; c[5] = c1.y; c[6] = c1.z; c[7] = c1.w;
         s[0] = s0.x; s[1] = s0.y; s[2] = s0.z; s[3] = s0.w;

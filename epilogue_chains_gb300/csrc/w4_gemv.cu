@@ -211,16 +211,16 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_gemv_kernel(
             if (gi < KG && nlo < a.N) {   // past the last chunk or row: scale zero
                 const int64_t lo = static_cast<int64_t>(nlo) * KG + gi, hi = nhi < a.N ? lo + 8 * static_cast<int64_t>(KG) : lo;
                 const uint16_t* sp = static_cast<const uint16_t*>(a.s);
-                sc = __ldg(sp + lo) | static_cast<uint32_t>(__ldg(sp + hi)) << 16;
+                sc = sp[lo] | static_cast<uint32_t>(sp[hi]) << 16;
                 if (a.z) {
                     const uint8_t* zq = static_cast<const uint8_t*>(a.z);
-                    zp = (__ldg(zq + lo) & 15u) | (__ldg(zq + hi) & 15u) << 16;
+                    zp = (zq[lo] & 15u) | (zq[hi] & 15u) << 16;
                 }
             }
         };
         auto load_scales = [&](int tile, int gi, uint32_t (&sc)[SW], uint32_t (&zp)[SW]) {
 #pragma unroll
-            for (int i = 0; i < SW; ++i) load_scale(tile, gi + 4 * i, sc[i], zp[i]);
+            for (int i = 0; i < SW; ++i) load_scale(tile, gi + 4 * i < a.nchunk * NG ? gi + 4 * i : KG, sc[i], zp[i]);
         };
         // one group: WPG words of each row against the matching X pieces
         auto group = [&](int gi, const uint32_t* wl, const uint32_t* wh, auto&& xpiece, float2 s2, uint32_t zl, uint32_t zh) {
@@ -358,8 +358,8 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_gemv_kernel(
                     phase ^= 1u;
                 }
             }
-            // the last K % 256 inputs, from global memory by the first K warps
-            if (ok && rank == 0 && wk == 0 && a.nchunk * 256 < a.K) {
+            // the last K % 256 inputs, from global memory by the first warp (scales that come through the ring have none)
+            if (!TS && ok && rank == 0 && wk == 0 && a.nchunk * 256 < a.K) {
                 const int k0 = a.nchunk * 256, nlo = tile * ROWS + g, nhi = nlo + 8;
                 const T* x = static_cast<const T*>(a.x);
                 const uint8_t* wq = static_cast<const uint8_t*>(a.wq);
@@ -454,7 +454,7 @@ int launch_w4(W4Args a, cudaStream_t st) {
     a.tiles = static_cast<int>(ceil_div(a.N, ROWS));
     const int nblk = static_cast<int>(ceil_div(a.nchunk, WK));
     a.split = 1;
-    while (a.split < 8 && a.tiles * blocks * a.split * 2 <= 2 * sm_count() && nblk >= 2 * a.split) a.split *= 2;
+    while (a.split < 8 && static_cast<int64_t>(a.tiles) * blocks * a.split <= sm_count() && nblk >= 2 * a.split) a.split *= 2;
     const int iters = static_cast<int>(ceil_div(nblk > 0 ? nblk : 1, a.split));
     // X stays in shared memory for all of a CTA's tiles where it is small (whole stages of it keep the
     // swizzle's phase: 4 WK mbox rows are a multiple of 8), else it comes with every stage

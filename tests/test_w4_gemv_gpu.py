@@ -101,6 +101,23 @@ def test_full_sizes(cuda_device, M, N, K, G, dtype):
     check(*make(M, N, K, G, dtype, zeros=dtype == "f16", bias=True, residual=True), gelu=True)
 
 
+@pytest.mark.parametrize("K,G", [(320, 64), (288, 32), (2432, 128)])
+def test_infinite_scale_in_the_last_groups(cuda_device, K, G):
+    """A scale is multiplied with its own group's sum only: an infinite one in the inputs past the last whole
+    chunk makes its row infinite, not NaN, and no other row."""
+    import torch
+    x, wq, s, _, _, _ = make(3, 40, K, G, "bf16", seed=K)
+    x = x.abs() + 0.5
+    wq |= 0x88                                    # q - 8 in 0 .. 7
+    wq[5] = 0xFF
+    s[5, -1] = float("inf")
+    out = torch.empty(3, 40, dtype=x.dtype, device="cuda")
+    fc.fuse_w4_gemv(x, wq, s, out)
+    assert bool((out[:, 5] == float("inf")).all())
+    keep = [n for n in range(40) if n != 5]
+    assert bool(torch.isfinite(out[:, keep]).all())
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_integer_inputs_are_exact(cuda_device, dtype):
     """Integers and scales that are powers of two leave nothing to round: every bit of Y is fixed, so a
