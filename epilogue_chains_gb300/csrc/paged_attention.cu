@@ -18,7 +18,7 @@
 //  * paged_prefix_kernel, paged_prefix2_kernel: the shared prefix.  Here all batch * group query rows of a
 //    key/value head meet the same keys: tcgen05 tiles of 128 or 256 rows by 128 keys, scores and output
 //    in TMEM, the key axis split over the SMs.  1024 rows per head over 16384 keys (8 heads, D = 128) take
-//    59 us of the call's 101, 1.2 PFLOP/s.
+//    49 us of the call's 92, 1.4 PFLOP/s.
 //  * paged_join_kernel, with a prefix: a row's own parts and the prefix's.
 //
 // The lengths are in device memory, so one launch configuration (and a captured graph) serves every
@@ -1152,8 +1152,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix_kernel(const __gr
 // tile wait for the tensor core, those of the other work.  One softmax thread per row takes its 128 scores into
 // registers and gives the score buffer back at once, so S_t(j + 1) is computed while the thread works on
 // S_t(j).  P goes through shared memory.  K and V tiles share one ring of three tiles in the order of their use,
-// K(0) K(1) V(0) K(2) V(1) ...; the MMA warp issues S_0(j + 1), PV_1(j - 1), S_1(j + 1), PV_0(j), with row tile
-// 1 half a step behind row tile 0.
+// K(0) K(1) V(0) K(2) V(1) ...; one warp issues S_0(j), S_1(j), the next step's and so on, another the PVs, and the
+// row tiles fall half a step apart by themselves.
 // (P in TMEM over the scores it was made from, which leaves room for two stages of K and of V: S_t(j + 1) then
 // waits for PV_t(j), and a step of 256 x 128 took 3000 cycles.)
 template <int D>
@@ -1167,7 +1167,7 @@ struct Prefix2Layout {
     static constexpr uint32_t OFF_KV = 2 * TILE;
     static constexpr uint32_t OFF_P = OFF_KV + RING * TILE;    // two tiles
     static constexpr uint32_t OFF_BAR = OFF_P + 2 * P_BYTES;
-    static constexpr int N_BARS = 2 + 2 * RING + 8;
+    static constexpr int N_BARS = 2 + 2 * RING + 10;
     static constexpr uint32_t OFF_HOLD = OFF_BAR + N_BARS * 8;
     static constexpr uint32_t SMEM = OFF_HOLD + 16 + 1024;
     static constexpr uint32_t TMEM_COLS = 512, O_COL = 256;    // scores of tile t at 128 t, output at 256 + D t
@@ -1186,9 +1186,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix2_kernel(const __g
     uint8_t* gbase = smem_raw + (base - smem_addr(smem_raw));
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const uint32_t bar0 = base + L::OFF_BAR;
-    const uint32_t q_full = bar0, drain = bar0 + 8;
-    auto full = [&](int i) { return bar0 + 8u * (2 + i); };
-    auto empty = [&](int i) { return bar0 + 8u * (2 + RING + i); };
+    const uint32_t q_full = bar0;
+    auto drain = [&](int w) { return bar0 + 8u * (10 + 2 * RING + w); };     // of warps 1 and 2
+    auto full = [&](int i) { return bar0 + 8u * (1 + i); };
+    auto empty = [&](int i) { return bar0 + 8u * (1 + RING + i); };
     auto s_full = [&](int t) { return bar0 + 8u * (2 + 2 * RING + t); };
     auto s_free = [&](int t) { return bar0 + 8u * (4 + 2 * RING + t); };
     auto p_full = [&](int t) { return bar0 + 8u * (6 + 2 * RING + t); };
@@ -1196,7 +1197,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix2_kernel(const __g
     int* flag = a.flag;
     if (threadIdx.x == 0) {
         mbar_init(q_full, kPreSoftmaxWarps);
-        mbar_init(drain, 1);
+        mbar_init(drain(0), 1);
+        mbar_init(drain(1), 1);
         for (int i = 0; i < RING; ++i) {
             mbar_init(full(i), 1);
             mbar_init(empty(i), 1);
@@ -1256,68 +1258,73 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix2_kernel(const __g
         if (!ok)   // copies in flight land before the shared memory goes away
             for (int j = max(0, c - RING); j < c; ++j) (void)mbar_wait_drain(full(j % RING), (j / RING) & 1);
         __syncwarp();
-    } else if (warp == 1) {
-        // ---------------------------------------------------------------- MMA issue
-        constexpr uint32_t idS = idesc_f16(128, 128, false, false, BF);
-        constexpr uint32_t idO = idesc_f16(128, D, false, true, BF);
+    } else if (warp < 3) {
+        // ---------------------------------------------------------------- MMA issue: S by warp 1, PV by warp 2
+        // One warp for both took 3150 cycles for a step whose MMAs take 2270: each of its waits, even for what had long
+        // happened, left the tensor core idle for 150 to 200 cycles (16384 keys, 1024 rows of 8 heads: 59 us, with
+        // two warps 49, 1.4 PFLOP/s).
         const uint32_t one = elect_one();
-        const uint64_t dq = smem_desc_sw128(base + L::OFF_Q, 16, 1024), dk = smem_desc_sw128(base + L::OFF_KV, 16, 1024);
-        const uint64_t dp = smem_desc_sw128(base + L::OFF_P, 16, 1024), dv = smem_desc_sw128(base + L::OFF_KV, L::REGION, 1024);
         bool issued = false, ok = true;
         auto wait = [&](uint32_t bar, uint32_t parity) {
             ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity & 1u, flag));
             return ok;
         };
-        // i: steps before this one (parities of the tile's barriers); c: the K or V tile's number among all loads
-        auto issue_s = [&](int t, int i, int c) {
-            if (i > 0 && !wait(s_free(t), i - 1)) return;
-            if (t == 0 && !wait(full(c % RING), c / RING)) return;     // row tile 1 comes second
-            tc_fence_after();
-            const uint64_t kd = dk + static_cast<uint64_t>((c % RING) * (L::TILE >> 4)), qd = dq + static_cast<uint64_t>(t * (L::TILE >> 4));
-#pragma unroll
-            for (int s = 0; s < D / 16; ++s)
-                tc_mma_if(one, tmem + t * 128, qd + ((s / 4) * (L::REGION >> 4) + (s % 4) * 2), kd + ((s / 4) * (L::REGION >> 4) + (s % 4) * 2),
-                          idS, s > 0 ? 1u : 0u);
-            tc_commit_if(one, s_full(t));
-            if (t == 1) tc_commit_if(one, empty(c % RING));
-            issued = true;
-        };
-        auto issue_pv = [&](int t, int i, int c, bool first) {
-            if (!wait(p_full(t), i)) return;
-            if (t == 0 && !wait(full(c % RING), c / RING)) return;
-            tc_fence_after();
-            const uint64_t vd = dv + static_cast<uint64_t>((c % RING) * (L::TILE >> 4)), pd = dp + static_cast<uint64_t>(t * (L::P_BYTES >> 4));
-#pragma unroll
-            for (int s = 0; s < 8; ++s)   // 16 keys each
-                tc_mma_if(one, tmem + L::O_COL + t * D, pd + ((s / 4) * (L::REGION >> 4) + (s % 4) * 2), vd + s * (2048 >> 4), idO,
-                          !first || s > 0 ? 1u : 0u);
-            tc_commit_if(one, o_done(t));
-            if (t == 1) tc_commit_if(one, empty(c % RING));
-            issued = true;
-        };
-        int i = 0, c = 0, segs = 0;
+        int i = 0, c = 0, segs = 0;      // steps and loads of the segments before this one, their number
         PrefixSeg seg;
-        for (int u = u0; ok && next_seg(a, u, u1, seg); ++segs) {
-            const int n = seg.n;
-            if (!wait(q_full, segs)) break;
-            issue_s(0, i, c);
-            if (ok) issue_s(1, i, c);
-            for (int j = 0; ok && j < n; ++j) {
-                if (j + 1 < n) issue_s(0, i + j + 1, c + k_at(j + 1));
-                if (ok && j > 0) issue_pv(1, i + j - 1, c + v_at(j - 1, n), j == 1);
-                if (ok && j + 1 < n) issue_s(1, i + j + 1, c + k_at(j + 1));
-                if (ok) issue_pv(0, i + j, c + v_at(j, n), j == 0);
+        if (warp == 1) {
+            constexpr uint32_t idS = idesc_f16(128, 128, false, false, BF);
+            const uint64_t dq = smem_desc_sw128(base + L::OFF_Q, 16, 1024), dk = smem_desc_sw128(base + L::OFF_KV, 16, 1024);
+            for (int u = u0; ok && next_seg(a, u, u1, seg); ++segs, i += seg.n, c += 2 * seg.n) {
+                if (!wait(q_full, segs)) break;
+                for (int j = 0; ok && j < seg.n; ++j) {
+                    const int ck = c + k_at(j), slot = ck % RING;
+                    if (!wait(full(slot), ck / RING)) break;
+                    const uint64_t kd = dk + static_cast<uint64_t>(slot * (L::TILE >> 4));
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (i + j > 0 && !wait(s_free(t), i + j - 1)) break;
+                        tc_fence_after();
+                        const uint64_t qd = dq + static_cast<uint64_t>(t * (L::TILE >> 4));
+#pragma unroll
+                        for (int s = 0; s < D / 16; ++s)
+                            tc_mma_if(one, tmem + t * 128, qd + ((s / 4) * (L::REGION >> 4) + (s % 4) * 2),
+                                      kd + ((s / 4) * (L::REGION >> 4) + (s % 4) * 2), idS, s > 0 ? 1u : 0u);
+                        tc_commit_if(one, s_full(t));
+                        issued = true;
+                    }
+                    if (ok) tc_commit_if(one, empty(slot));
+                }
             }
-            if (ok) issue_pv(1, i + n - 1, c + v_at(n - 1, n), n == 1);
-            i += n;
-            c += 2 * n;
+        } else {
+            constexpr uint32_t idO = idesc_f16(128, D, false, true, BF);
+            const uint64_t dp = smem_desc_sw128(base + L::OFF_P, 16, 1024), dv = smem_desc_sw128(base + L::OFF_KV, L::REGION, 1024);
+            for (int u = u0; ok && next_seg(a, u, u1, seg); i += seg.n, c += 2 * seg.n) {
+                for (int j = 0; ok && j < seg.n; ++j) {
+                    const int cv = c + v_at(j, seg.n), slot = cv % RING;
+                    if (!wait(full(slot), cv / RING)) break;
+                    const uint64_t vd = dv + static_cast<uint64_t>(slot * (L::TILE >> 4));
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (!wait(p_full(t), i + j)) break;
+                        tc_fence_after();
+                        const uint64_t pd = dp + static_cast<uint64_t>(t * (L::P_BYTES >> 4));
+#pragma unroll
+                        for (int s = 0; s < 8; ++s)   // 16 keys each
+                            tc_mma_if(one, tmem + L::O_COL + t * D, pd + ((s / 4) * (L::REGION >> 4) + (s % 4) * 2), vd + s * (2048 >> 4), idO,
+                                      j > 0 || s > 0 ? 1u : 0u);
+                        tc_commit_if(one, o_done(t));
+                        issued = true;
+                    }
+                    if (ok) tc_commit_if(one, empty(slot));
+                }
+            }
         }
         if (!ok && issued) {   // MMAs in flight finish before TMEM is freed
-            tc_commit_if(one, drain);
-            (void)mbar_wait_drain(drain, 0);
+            tc_commit_if(one, drain(warp - 1));
+            (void)mbar_wait_drain(drain(warp - 1), 0);
         }
         __syncwarp();
-    } else if (warp >= 3) {
+    } else {
         // ---------------------------------------------------------------- softmax: thread r of tile t, one row
         const int t = (warp - 3) / 4, r = 32 * (warp % 4) + lane;
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp % 4)) << 16;
