@@ -1263,6 +1263,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix2_kernel(const __g
         // One warp for both took 3150 cycles for a step whose MMAs take 2270: each of its waits, even for what had long
         // happened, left the tensor core idle for 150 to 200 cycles (16384 keys, 1024 rows of 8 heads: 59 us, with
         // two warps 49, 1.4 PFLOP/s).
+        // The order of the waits matters: K and V tiles take turns in a ring slot, and a wait for a slot's use u tells
+        // it from use u - 2 by parity alone, so use u - 1, which may be the other warp's, must be known to have
+        // landed.  S(j) knows by s_free(j - 1): the thread that took S(j - 1) has stored P(j - 2) before, for which
+        // it waited for PV(j - 3), so V(j - 3) has landed (and q_full says so of the segments before).  PV(j) knows
+        // by p_full(j): S(j) is done, so K(j) and the tiles before it have landed.
         const uint32_t one = elect_one();
         bool issued = false, ok = true;
         auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -1278,11 +1283,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix2_kernel(const __g
                 if (!wait(q_full, segs)) break;
                 for (int j = 0; ok && j < seg.n; ++j) {
                     const int ck = c + k_at(j), slot = ck % RING;
-                    if (!wait(full(slot), ck / RING)) break;
                     const uint64_t kd = dk + static_cast<uint64_t>(slot * (L::TILE >> 4));
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         if (i + j > 0 && !wait(s_free(t), i + j - 1)) break;
+                        if (t == 0 && !wait(full(slot), ck / RING)) break;
                         tc_fence_after();
                         const uint64_t qd = dq + static_cast<uint64_t>(t * (L::TILE >> 4));
 #pragma unroll
@@ -1301,11 +1306,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix2_kernel(const __g
             for (int u = u0; ok && next_seg(a, u, u1, seg); i += seg.n, c += 2 * seg.n) {
                 for (int j = 0; ok && j < seg.n; ++j) {
                     const int cv = c + v_at(j, seg.n), slot = cv % RING;
-                    if (!wait(full(slot), cv / RING)) break;
                     const uint64_t vd = dv + static_cast<uint64_t>(slot * (L::TILE >> 4));
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         if (!wait(p_full(t), i + j)) break;
+                        if (t == 0 && !wait(full(slot), cv / RING)) break;
                         tc_fence_after();
                         const uint64_t pd = dp + static_cast<uint64_t>(t * (L::P_BYTES >> 4));
 #pragma unroll
