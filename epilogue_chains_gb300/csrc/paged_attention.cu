@@ -308,6 +308,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnLayout<D>::CTAS) paged_own_ker
             return a.cache_rows;         // past the cache: zeros
         };
         const uint32_t one = elect_one();
+        const uint64_t once = policy_evict_first();
         int slot = 0, loads = 0, qs = 0, qloads = 0;
         uint32_t phase = 0, qphase = 0;          // completions of the current slot's barriers so far, mod 2
         bool ok = true;
@@ -351,7 +352,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnLayout<D>::CTAS) paged_own_ker
                             if (y < boxes)
 #pragma unroll
                                 for (int i = 0; i < L::ATOMS; ++i)
-                                    tma_load_2d_if(one, dst + i * L::ATOM + ((static_cast<uint32_t>(y) << shift) * 128), map, 64 * i, r[y], full(slot));
+                                    tma_load_2d_once_if(one, dst + i * L::ATOM + ((static_cast<uint32_t>(y) << shift) * 128), map, 64 * i, r[y], full(slot), once);
                         ++loads;
                         if (++slot == a.slots) {
                             slot = 0;
