@@ -8,12 +8,13 @@
 // stored, without repacking.  Two kernels:
 //
 // w4_gemv_kernel, for few tokens.  Each warp multiplies 16 weight rows (the 16-row operand of mma.sync
-// m16n8k16) with 8 tokens; blocks of 8 tokens are the grid's second axis (the second block finds the
-// weights in L2).  The order of k within a matrix instruction is free as long as both operands agree, so
-// lane 4 g + t takes consecutive k of its rows: one 128-k chunk gives it four 32-bit words of row g and of
-// row g + 8 (eight k each), from one 16-byte, two 8-byte or four 4-byte pieces for groups of 128, 64 and
-// 32, such that the four lanes of a row always work on the same group.  A warp takes two such chunks at a
-// time: a row's 128 bytes, one request of the copy engine.
+// m16n8k16) with 8 tokens; more (where w4_tile_kernel cannot take them) are blocks of 8, the grid's
+// second axis, and later blocks find the weights in L2.  The order of k within a matrix instruction is
+// free as long as both operands agree, so lane 4 g + t takes consecutive k of its rows: one 128-k chunk
+// gives it four 32-bit words of row g and of row g + 8 (eight k each), from one 16-byte, two 8-byte or
+// four 4-byte pieces for groups of 128, 64 and 32, such that the four lanes of a row always work on the
+// same group.  A warp takes two such chunks at a time: a row's 128 bytes, one request of the copy
+// engine.
 // A CTA of eight computing warps covers 16 rows and 2048 inputs per stage.  One producing thread fills a
 // ring of stages by TMA (weights [8][16][128 B] and X [32][tokens][64 elements], 128-byte swizzle, scales
 // and zero points); a CTA stays for several row tiles, so that the ring runs on while a tile is finished.
@@ -500,7 +501,7 @@ int launch_w4(W4Args a, cudaStream_t st) {
 // TMEM column), X is the B operand from shared memory, and every group of k has its own fp32 accumulator
 // in TMEM, which is read out, multiplied by the group's scale and added up in registers.
 //
-// Measured: 64 x 28672 x 4096 in groups of 64 35.5 us, 64 x 4096 x 4096 in groups of 128 12.6 us.  Not the loads but
+// Measured: 64 x 28672 x 4096 in groups of 64 35.5 us, 64 x 4096 x 4096 in groups of 128 11.5 us, 32 x 8192 x 8192 18.1 us.  Not the loads but
 // the chain of a unit (unpack, MMAs, read-out) and its instructions bound it: the SMs issue half of the time, and
 // separate warps for unpacking and reading out were no faster (38.5 us).
 //
@@ -897,15 +898,25 @@ int launch_tile(const W4Args& w, cudaStream_t st) {
     a.y = w.y;
     a.flag = w.flag;
     const int tiles = static_cast<int>(ceil_div(w.N, 128)), sms = sm_count();
-    // A CTA's chunks, times how often the SMs go round: the least, and of equal splits the smallest
-    int64_t best = INT64_MAX;
+    // The split with the least of (chunks of a CTA + 5 for its start and end) x waves.  A wave is two CTAs per SM in whole
+    // clusters (a GPC, an eighth of the SMs, takes floor(38 / split) of them); a last wave that is not full counts half
+    // and half its share, as its CTAs get an SM to themselves, and so does three quarters of a wave that all fits one CTA
+    // per SM.  Measured for splits 1, 2, 4 and 8 (tiles of 128 rows x chunks of 128 inputs, us; best chosen but for 1 of
+    // 29 sizes, by 6 %): 16 x 32 24.8, 14.3, 12.1, 10.6; 40 x 32 32, 18.6, 12.8, 16.9; 76 x 64 42, 23, 30, 32;
+    // 32 x 112 78, 54, 31, 21; 140 x 32 40, 21, 26, 42; 224 x 32 42, 36, 45, 64; 300 x 32 41, 41, 55, 82.
+    double best = 0.0;
+    a.split = 0;
     for (int s = 1; s <= 8; s *= 2) {
-        const int64_t per = ceil_div(a.nchunk, s);
-        const int64_t cost = ceil_div(static_cast<int64_t>(tiles) * s, sms) * (per + 2);
-        if (cost < best) {
+        const int per = static_cast<int>(ceil_div(a.nchunk, s)), wave = sms / 4 / s * 8;
+        if (wave < 1) break;
+        const int full = tiles / wave, rest = tiles % wave;
+        double waves = full + (rest > 0 ? full > 0 ? 0.5 + 0.5 * rest / wave : 1.0 : 0.0);
+        if (static_cast<int64_t>(tiles) * s <= sms) waves = 0.75;
+        const double cost = (per + 5) * waves;
+        if (a.split == 0 || cost < best) {
             best = cost;
             a.split = s;
-            a.per = static_cast<int>(per);
+            a.per = per;
         }
     }
     CUtensorMap mW{}, mX{}, mS{}, mZ{};
@@ -926,9 +937,9 @@ int launch_tile(const W4Args& w, cudaStream_t st) {
 template <typename T, int G>
 int run_w4_g(const W4Args& a, cudaStream_t st) {
     const bool fits = scales_fit(a, G);
-    // Up to 16 tokens w4_gemv_kernel (two blocks of 8) is quicker until there is a tile of 128 rows per SM: at 16 x 4096 x
-    // 4096 it takes 7.6 us (tiles 10.4), at 8192 x 8192 21.5 (27.5), at 14336 x 4096 18.1 (21.6), at 28672 x 4096 33 (28).
-    if (fits && (a.M > 16 || (a.M > 8 && ceil_div(a.N, 128) > sm_count()))) {
+    // More than 8 tokens take another pass of w4_gemv_kernel over the weights.  At 9 tokens it takes 8.5 us for 4096 x
+    // 4096 (tiles 8.2), 22.2 for 8192 x 8192 (17.2), 41 for 28672 x 4096 (29); at 8 7.8, 13.4 and 19.8.
+    if (fits && a.M > 8) {
         if (a.M <= 16) return launch_tile<T, G, 16>(a, st);
         if (a.M <= 32) return launch_tile<T, G, 32>(a, st);
         return launch_tile<T, G, 64>(a, st);
