@@ -13,12 +13,12 @@
 //    warp loads units by TMA into a ring, four compute: each multiplies its 16 keys of a unit with the
 //    query rows by mma.sync (16 rows, mostly one group), and the warps' parts meet in shared memory when
 //    a run ends.  Parts of a sequence that several CTAs share go through the workspace: the CTA that
-//    arrives last joins them, in the order of the keys (with a prefix, paged_join_kernel does).  3 x 65536 keys (D = 128) take 110 us, 0.96 of
-//    the copy rate; 32 sequences of up to 4096 keys 51.6 us, 0.80.
+//    arrives last joins them, in the order of the keys (with a prefix, paged_join_kernel does).  3 x 65536 keys (D = 128) take 108 us, 0.97 of
+//    the copy rate; 32 sequences of up to 4096 keys 49.4 us, 0.84.
 //  * paged_prefix_kernel, paged_prefix2_kernel: the shared prefix.  Here all batch * group query rows of a
 //    key/value head meet the same keys: tcgen05 tiles of 128 or 256 rows by 128 keys, scores and output
 //    in TMEM, the key axis split over the SMs.  1024 rows per head over 16384 keys (8 heads, D = 128) take
-//    49 us of the call's 92, 1.4 PFLOP/s.
+//    49 us of the call's 90, 1.4 PFLOP/s.
 //  * paged_join_kernel, with a prefix: a row's own parts and the prefix's.
 //
 // The lengths are in device memory, so one launch configuration (and a captured graph) serves every
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnLayout<D>::CTAS) paged_own_ker
             return a.cache_rows;         // past the cache: zeros
         };
         const uint32_t one = elect_one();
-        const uint64_t once = policy_evict_first();
+        const uint64_t once = policy_evict_first();      // ragged batch 51.8 -> 49.4 us: what else lies in L2 stays there
         int slot = 0, loads = 0, qs = 0, qloads = 0;
         uint32_t phase = 0, qphase = 0;          // completions of the current slot's barriers so far, mod 2
         bool ok = true;

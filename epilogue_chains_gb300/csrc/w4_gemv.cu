@@ -455,7 +455,8 @@ int launch_w4(W4Args a, cudaStream_t st) {
     a.tiles = static_cast<int>(ceil_div(a.N, ROWS));
     const int nblk = static_cast<int>(ceil_div(a.nchunk, WK));
     a.split = 1;
-    while (a.split < 8 && static_cast<int64_t>(a.tiles) * blocks * a.split <= sm_count() && nblk >= 2 * a.split) a.split *= 2;
+    // as long as all clusters run at once (two CTAs per SM; a GPC, an eighth of the SMs, takes whole clusters)
+    while (a.split < 8 && static_cast<int64_t>(a.tiles) * blocks <= sm_count() / 8 / a.split * 8 && nblk >= 2 * a.split) a.split *= 2;
     const int iters = static_cast<int>(ceil_div(nblk > 0 ? nblk : 1, a.split));
     // X stays in shared memory for all of a CTA's tiles where it is small (whole stages of it keep the
     // swizzle's phase: 4 WK mbox rows are a multiple of 8), else it comes with every stage
@@ -558,7 +559,6 @@ __global__ void __launch_bounds__(kTileThreads, 2) w4_tile_kernel(
     constexpr int SG = NG * NM <= 128 ? NG : 128 / NM;   // groups of a set
     constexpr int SETS = NG / SG;                        // sets of a unit
     constexpr int ND = 2 * SG * NM <= 128 ? 2 : 1;       // set buffers
-    pdl_trigger();
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
     uint8_t* gbase = smem_raw + (base - smem_addr(smem_raw));
@@ -597,6 +597,9 @@ __global__ void __launch_bounds__(kTileThreads, 2) w4_tile_kernel(
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(gbase + L::OFF_HOLD), 0);
+    // Only with its tensor memory in hand: a kernel that starts early and takes all of an SM's would wait for this one,
+    // which would wait for the memory.
+    pdl_trigger();
     pdl_wait();
 
     float acc[HT];
