@@ -1534,17 +1534,21 @@ int launch_prefix(const CUtensorMap& mK, const CUtensorMap& mV, const PagedArgs&
 template <typename T, int D>
 int run_paged(PagedArgs a, const void* k, const void* v, cudaStream_t st) {
     const bool bf = std::is_same<T, __nv_bfloat16>::value;
+    // A map costs the host about as much as everything else of a call but the launches, so equal ones are made once.
     CUtensorMap mQ, mK, mV, mK16, mV16;
+    auto maps = [&](int box, CUtensorMap* k_map, CUtensorMap* v_map) {
+        return make_map(k_map, k, a.cache_rows, D, 64, box, bf) && make_map(v_map, v, a.cache_rows, D, 64, box, bf);
+    };
+    const int page = 1 << a.page_shift, box = page < 64 ? page : 64;
+    if (!maps(box, &mK, &mV)) return FUSE_ECUDA;
     if (a.plen > 0) {
-        const int box = 1 << (a.page_shift < 7 ? a.page_shift : 7);
-        if (!make_map(&mK, k, a.cache_rows, D, 64, box, bf) || !make_map(&mV, v, a.cache_rows, D, 64, box, bf)) return FUSE_ECUDA;
-        if (const int rc = launch_prefix<T, D>(mK, mV, a, st); rc != FUSE_OK) return rc;
+        CUtensorMap pK = mK, pV = mV;
+        if (page > 64 && !maps(128, &pK, &pV)) return FUSE_ECUDA;
+        if (const int rc = launch_prefix<T, D>(pK, pV, a, st); rc != FUSE_OK) return rc;
     }
-    const int box = 1 << (a.page_shift < 6 ? a.page_shift : 6);
-    if (!make_map(&mQ, a.q, static_cast<int64_t>(a.batch) * a.hq, D, 64, a.rows, bf) || !make_map(&mK, k, a.cache_rows, D, 64, box, bf) ||
-        !make_map(&mV, v, a.cache_rows, D, 64, box, bf) || !make_map(&mK16, k, a.cache_rows, D, 64, 16, bf) ||
-        !make_map(&mV16, v, a.cache_rows, D, 64, 16, bf))
-        return FUSE_ECUDA;
+    mK16 = mK;
+    mV16 = mV;
+    if ((box != 16 && !maps(16, &mK16, &mV16)) || !make_map(&mQ, a.q, static_cast<int64_t>(a.batch) * a.hq, D, 64, a.rows, bf)) return FUSE_ECUDA;
     uint32_t smem = 0;
     int ctas = 0;
     int rc = own_smem<D>(&a, &smem, &ctas);

@@ -175,3 +175,34 @@ def test_two_layers_share_a_workspace(cuda_device):
             fc.fuse_graph_destroy(g)
         want = want or got
         assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_two_streams_at_once(cuda_device):
+    """Steps of two layers on two streams, each with a workspace of its own, give the bits of the same steps one after
+    the other."""
+    import torch
+
+    def make():
+        return [Layer(40, 0, 1024, 16, 4, 128, 32, 128, "bf16", False, [b * 11 for b in range(40)], 700, 1, 5),
+                Layer(12, 1, 1024, 8, 8, 64, 16, 32, "bf16", True, [b * 50 for b in range(12)], 0, 1, 6)]
+
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    ms = make()
+    for m in ms:
+        m.advance(gen)
+    want = []
+    for m in ms:
+        m.step(False)
+        torch.cuda.synchronize()
+        want.append((m.o.clone(), m.y.clone()))
+    streams = [torch.cuda.Stream() for _ in ms]
+    torch.cuda.synchronize()
+    for _ in range(25):
+        for m, st in zip(ms, streams):
+            with torch.cuda.stream(st):
+                m.o.zero_()
+                m.step(False, st)
+        torch.cuda.synchronize()
+        assert fc.fuse_check() == fc.FUSE_OK
+        for m, (o, y) in zip(ms, want):
+            assert torch.equal(m.o, o) and torch.equal(m.y, y)
