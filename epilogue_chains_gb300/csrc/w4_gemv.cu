@@ -601,6 +601,12 @@ __global__ void __launch_bounds__(kTileThreads, 2) w4_tile_kernel(
     // which would wait for the memory.
     pdl_trigger();
     pdl_wait();
+    // the residual's lines of this tile, for the epilogue: 64 rows of a token each
+    if (a.R && rank == 0)
+        for (int l = threadIdx.x; l < 2 * a.M; l += kTileThreads) {
+            const int n = n0 + 64 * (l & 1);
+            if (n < a.N) asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const T*>(a.R) + static_cast<int64_t>(l >> 1) * a.N + n));
+        }
 
     float acc[HT];
 #pragma unroll
