@@ -702,7 +702,8 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     // the own parts have to be looked up; the prefix's are on their way by then).
     constexpr int kParts = 7;
     const int tile = h % a.group / 16, w = __ldcg(a.where + (b * a.hk + head) * a.rt + tile);
-    const int o0 = w < 0 ? 0 : w & 0xffff, own = w < 0 ? 1 : (w >> 16) - o0 + 1, all = own + np;
+    // (after a wait that ran out `where` may hold anything: within the workspace all the same)
+    const int o0 = w < 0 ? 0 : min(w & 0xffff, kOwnGrid - 1), own = w < 0 ? 1 : max(min(w >> 16, kOwnGrid - 1) - o0 + 1, 1), all = own + np;
     auto load = [&](float (&v)[W], const float* src) {
         if constexpr (W == 2) {
             const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
