@@ -11,6 +11,7 @@ PyTorch is used for device memory and streams only.
 from __future__ import annotations
 
 import ctypes
+import functools
 import threading
 
 FUSE_OK, FUSE_EINVAL, FUSE_EALIGN, FUSE_EUNSUPPORTED = 0, -1, -2, -3
@@ -485,17 +486,17 @@ def fuse_paged_attention(q, k_cache, v_cache, block_table, seq_lens, o, scale: f
         raise ValueError("prefix_table does not hold prefix_len keys")
     lib, sh = _load(), _stream(stream)
     if workspace is None:
-        workspace = _paged_workspace(lib.fuse_paged_attention_workspace_bytes(batch, q_heads, kv_heads, D, prefix_len),
-                                     dev, sh)
+        workspace = _paged_workspace(fuse_paged_attention_workspace_bytes(batch, q_heads, kv_heads, D, prefix_len), dev, sh)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("the workspace must be a contiguous tensor on the device of the others")
     _check(lib.fuse_paged_attention(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
                                     block_table.shape[1], seq_lens.data_ptr(), _ptr(prefix_table), prefix_len,
                                     o.data_ptr(), batch, q_heads, kv_heads, D, pages, page_size, scale,
                                     FUSE_F16 if dt is torch.float16 else FUSE_BF16, workspace.data_ptr(),
-                                    workspace.numel() * workspace.element_size(), sh), "fuse_paged_attention")
+                                    workspace.nbytes, sh), "fuse_paged_attention")
 
 
+@functools.lru_cache(maxsize=256)
 def fuse_paged_attention_workspace_bytes(batch: int, q_heads: int, kv_heads: int, D: int, prefix_len: int = 0) -> int:
     return _load().fuse_paged_attention_workspace_bytes(batch, q_heads, kv_heads, D, prefix_len)
 
