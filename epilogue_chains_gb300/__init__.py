@@ -452,6 +452,7 @@ def fuse_rope_append(qkv, cos_sin, positions, slots, q_out, k_cache, v_cache, in
 # workspaces of fuse_paged_attention(workspace=None): one zero-filled buffer per (device, stream), grown
 # as needed; every completed call leaves its counters zero
 _PAGED_WS = {}
+_PAGED_LOCK = threading.Lock()
 
 
 def _paged_workspace(need: int, dev: int, stream_handle):
@@ -485,15 +486,23 @@ def fuse_paged_attention(q, k_cache, v_cache, block_table, seq_lens, o, scale: f
     if prefix_len and (prefix_table is None or prefix_table.numel() * page_size < prefix_len):
         raise ValueError("prefix_table does not hold prefix_len keys")
     lib, sh = _load(), _stream(stream)
-    if workspace is None:
-        workspace = _paged_workspace(fuse_paged_attention_workspace_bytes(batch, q_heads, kv_heads, D, prefix_len), dev, sh)
-    elif workspace.get_device() != dev or not workspace.is_contiguous():
+    own = workspace is None
+    if not own and (workspace.get_device() != dev or not workspace.is_contiguous()):
         raise ValueError("the workspace must be a contiguous tensor on the device of the others")
-    _check(lib.fuse_paged_attention(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-                                    block_table.shape[1], seq_lens.data_ptr(), _ptr(prefix_table), prefix_len,
-                                    o.data_ptr(), batch, q_heads, kv_heads, D, pages, page_size, scale,
-                                    FUSE_F16 if dt is torch.float16 else FUSE_BF16, workspace.data_ptr(),
-                                    workspace.nbytes, sh), "fuse_paged_attention")
+    if own:      # a call is several launches: those of two threads on one stream must not mix over one workspace
+        _PAGED_LOCK.acquire()
+    try:
+        if own:
+            workspace = _paged_workspace(fuse_paged_attention_workspace_bytes(batch, q_heads, kv_heads, D, prefix_len), dev, sh)
+        status = lib.fuse_paged_attention(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                                          block_table.shape[1], seq_lens.data_ptr(), _ptr(prefix_table), prefix_len,
+                                          o.data_ptr(), batch, q_heads, kv_heads, D, pages, page_size, scale,
+                                          FUSE_F16 if dt is torch.float16 else FUSE_BF16, workspace.data_ptr(),
+                                          workspace.nbytes, sh)
+    finally:
+        if own:
+            _PAGED_LOCK.release()
+    _check(status, "fuse_paged_attention")
 
 
 @functools.lru_cache(maxsize=256)

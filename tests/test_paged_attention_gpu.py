@@ -286,3 +286,32 @@ def test_wrapper_refusals(cuda_device):
     with pytest.raises(fc.FuseError):
         fc.fuse_paged_attention(p["q"], p["k"], p["v"], p["table"], p["lens"], o, 0.1,
                                 workspace=torch.zeros(4096, dtype=torch.uint8, device="cuda"))
+
+
+def test_two_threads_on_one_stream(cuda_device):
+    """Calls of two threads on the same stream, with the module's own workspace, do not mix."""
+    import threading
+    import torch
+    ps = [make([70 + 13 * b for b in range(24)], 16, 2, 128, 32, "bf16", prefix=900, seed=1),
+          make([5 * b for b in range(40)], 8, 8, 64, 16, "bf16", prefix=140, seed=2)]
+    want = [run(p) for p in ps]
+    outs = [[torch.empty_like(p["q"]) for _ in range(100)] for p in ps]
+    errors = []
+
+    def work(p, os):
+        try:
+            for o in os:
+                fc.fuse_paged_attention(p["q"], p["k"], p["v"], p["table"], p["lens"], o, p["scale"], prefix_table=p["ptable"],
+                                        prefix_len=p["prefix"])
+        except Exception as e:      # shown by the main thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(ps, outs)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors and fc.fuse_check() == fc.FUSE_OK
+    for w, os in zip(want, outs):
+        assert all(torch.equal(o, w) for o in os)
