@@ -265,7 +265,6 @@ template <int D>
 __global__ void __launch_bounds__(kAttnThreads, 1) attn_fwd_kernel(
     const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
     const __grid_constant__ CUtensorMap mV, const __grid_constant__ AttnArgs a) {
-    pdl_trigger();  // the set-up below touches no global memory; pdl_wait() follows it
     using L = AttnLayout<D>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
@@ -321,6 +320,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_fwd_kernel(
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + L::OFF_HOLD);
+    pdl_trigger();  // only with the tensor memory in hand (see pdl_trigger())
     pdl_wait();  // the preceding kernel has completed: global memory may be touched
 
     if (warp == 0 || warp == 2) {
@@ -628,7 +628,6 @@ __global__ void __launch_bounds__(kPersistThreads, 1) attn_persist_kernel(
     const __grid_constant__ CUtensorMap mV,
     const __grid_constant__ CUtensorMap mO, const __grid_constant__ AttnArgs a,
     const __grid_constant__ AttnSched sch) {
-    pdl_trigger();  // the set-up below touches no global memory; pdl_wait() follows it
     using L = PairLayout<D>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
@@ -695,6 +694,7 @@ __global__ void __launch_bounds__(kPersistThreads, 1) attn_persist_kernel(
     cluster_sync();   // both CTAs' barriers exist before either signals the other
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + L::OFF_HOLD);
+    pdl_trigger();  // only with the tensor memory in hand (see pdl_trigger())
     // The cluster's first item's Q rows and first key and value blocks on their way into L2 while
     // the preceding kernel may still run (an L2 fill changes no data, whoever writes these lines
     // before the grid-dependency wait returns).

@@ -41,8 +41,10 @@ __device__ __forceinline__ void prefetch_l2_bulk(const void* ptr, uint32_t bytes
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(ptr), "r"(bytes) : "memory");
 }
 // Kernels with a set-up phase that touches no global memory (mbarrier init, TMEM allocation,
-// tensor-map prefetch) call pdl_trigger() at entry and pdl_wait() after the set-up, so the set-up
-// overlaps the end of the preceding kernel.
+// tensor-map prefetch) call pdl_wait() after the set-up, so the set-up overlaps the end of the
+// preceding kernel.  A kernel that allocates tensor memory calls pdl_trigger() only with it in hand:
+// the next kernel's CTAs, started on the same SM, could otherwise take the columns first and wait for
+// this kernel to complete, which would wait, without a bound, for the columns.
 
 // Launch `kernel` on `grid` x `block` threads with `smem` bytes of dynamic shared memory on `st`,
 // programmatic serialization allowed, as clusters of `cluster_x` CTAs when cluster_x > 1.

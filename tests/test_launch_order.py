@@ -1,0 +1,73 @@
+"""The order of programmatic launch against tensor memory and earlier writes, read from the kernels' sources.
+
+A kernel lets the next one start with pdl_trigger().  CTAs of the next kernel may then share an SM with its
+own, so a kernel that allocates tensor memory has to hold it by then: allocation waits without a bound, and
+the next kernel gives columns back only after this one has completed."""
+import os
+import re
+
+import pytest
+
+import epilogue_chains_gb300 as fc
+
+CSRC = os.path.join(os.path.dirname(os.path.abspath(fc.__file__)), "csrc")
+
+
+def kernels():
+    """{name: source from its name to the end of its body} of every kernel definition, comments left out."""
+    found = {}
+    for name in sorted(os.listdir(CSRC)):
+        if not name.endswith(".cu"):
+            continue
+        with open(os.path.join(CSRC, name), encoding="utf-8") as f:
+            text = re.sub(r"//[^\n]*", "", f.read())
+        for m in re.finditer(r"__global__[^;{]*?\b(\w+)\(\s*(?:const|float|__half|__nv_bfloat16|int|T\b)", text):
+            end = re.compile(r"^}", re.M).search(text, m.end())
+            found[m.group(1)] = text[m.start(1):end.end()]
+    return found
+
+
+def test_dependents_start_with_the_tensor_memory_in_hand():
+    seen = set()
+    for name, body in kernels().items():
+        alloc = re.search(r"\btmem_alloc(?:_pair)?\(", body)
+        if not alloc:
+            continue
+        seen.add(name)
+        trigger = re.search(r"\bpdl_(?:trigger|begin)\(\)", body)
+        assert trigger and trigger.start() > alloc.start(), name
+        # one warp allocates; the others know once they have passed a barrier
+        assert re.search(r"__syncthreads\(\)|cluster_sync\(\)", body[alloc.end():trigger.start()]), name
+    assert seen == {"attn_fwd_kernel", "attn_persist_kernel", "gemm_decode_kernel", "gemm_tc_kernel", "paged_prefix_kernel",
+                    "paged_prefix2_kernel", "w4_tile_kernel"}
+
+
+@pytest.mark.gpu
+def test_small_tensor_memory_kernels_in_a_row(cuda_device):
+    """Decode GEMM, dense attention and 4-bit tiles, whose CTAs fit on one SM together, back to back on one
+    stream: each reads what the one before it wrote, and every round gives the same bits."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(5)
+    H, S = 4096, 128
+    x = torch.randn(16, H, generator=g, device="cuda").half()
+    w = (torch.randn(H, H, generator=g, device="cuda") / 64).half()
+    bias, R = torch.zeros(H, device="cuda").half(), torch.zeros(16, H, device="cuda").half()
+    wq = torch.randint(0, 256, (H, H // 2), generator=g, device="cuda", dtype=torch.uint8)
+    s = ((0.5 + torch.rand(H, H // 128, generator=g, device="cuda")) * 0.2 / 64).half()
+    q, k, v = (torch.randn(2, S, 64, generator=g, device="cuda").bfloat16() for _ in range(3))
+    y, z, o = torch.empty_like(x), torch.empty_like(x), torch.empty_like(q)
+
+    def step():
+        fc.fuse_gemm_epilogue(x, w, bias, R, y)
+        fc.fuse_w4_gemv(y, wq, s, z)
+        fc.fuse_attention(q, k, v, o, 0.125)
+        fc.fuse_w4_gemv(z, wq, s, y)
+
+    step()
+    torch.cuda.synchronize()
+    first = [t.clone() for t in (y, z, o)]
+    for _ in range(200):
+        step()
+    assert fc.fuse_check() == fc.FUSE_OK
+    assert all(torch.equal(a, b) for a, b in zip((y, z, o), first))
+    assert all(bool(t.isfinite().all()) for t in first)
