@@ -43,7 +43,7 @@ constexpr int kUnit = kChunk * kOwnWarps;         // keys of a unit
 constexpr int kOwnSlots = 8;                       // most ring slots
 constexpr int kOwnGrid = 320;                     // most CTAs of paged_own_kernel (workspace bound)
 constexpr int kCounterBytes = 8192;
-static_assert(kOwnGrid * kOwnWarps * 4 <= kCounterBytes, "one counter per CTA and warp");
+static_assert(kOwnGrid * kOwnWarps * 4 + 4 <= kCounterBytes, "one counter per CTA and warp, and `ready`");
 constexpr int kPrefixGrid = 160;                  // most CTAs of paged_prefix_kernel (workspace bound)
 constexpr int kMaxBatch = 4096;
 constexpr int kOwnSmem = 226 * 1024;              // dynamic shared memory at most, next to a few static words
@@ -82,6 +82,7 @@ struct PagedArgs {
     // that goes on in a later one (slot 2 c + 1 if it begins here; an item begins in one CTA, which
     // names its counter).
     int* count;                        // [kOwnGrid][kOwnWarps] parts that have arrived, by the item's first CTA
+    int* ready;                        // with a prefix: 1 from the prefix kernel's grid-dependency wait to the join
     float *oml, *oo;                   // [2 kOwnGrid][rows] (m, l) and [..][rows][D]
     // with a prefix: where the own parts of an item (sequence, row tile of a key/value head) are, -1: in rml and ro
     // (it has one), else the CTAs that have them, first | last << 16; [batch hk rt]
@@ -200,9 +201,16 @@ __global__ void __launch_bounds__(kOwnThreads, OwnLayout<D>::CTAS) paged_own_ker
     }
     // With a prefix, the kernel before this one is the prefix's, of which nothing is read here.  It lets this one
     // start once it has itself waited for what came before, so CTAs of this kernel take over the SMs as the
-    // prefix's CTAs leave them; the wait is made up for at the end, for paged_join_kernel's sake.  (What is read
-    // by plain loads comes from L2, past anything an SM may still hold of earlier contents.)
-    if (a.plen == 0) pdl_wait();
+    // prefix's CTAs leave them; the wait is made up for at the end, for paged_join_kernel's sake.  Starting early
+    // does not make the writes of the kernels before the prefix's visible here: the prefix kernel's release of
+    // `ready`, after its wait, and the acquire here do (it is there by then: nothing is waited for).
+    if (a.plen == 0) {
+        pdl_wait();
+    } else {
+        if (tid == 32) (void)flag_wait_bounded(a.ready, 1, a.flag);
+        __syncthreads();
+        fence_async_global();          // for the copy engine's reads as well
+    }
 
     // ------------------------------------------------------------ places of every sequence
     {
@@ -699,6 +707,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     const int64_t per = a.ptiles + a.pent, PU = a.hk * a.prt * per, u = pit * per + a.pent;
     const int c0 = cta_of(u, PU, a.pgrid), np = cta_of(u + a.ptiles - 1, PU, a.pgrid) - c0 + 1;
     pdl_wait();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.ready = 0;
     // Lane 0 has what has been joined, lanes 1 .. kParts a part each: the prefix's, then the row's own.  The columns
     // of a batch are loaded next to its maxima and sums, so one memory latency is waited for, not three (two, where
     // the own parts have to be looked up; the prefix's are on their way by then).
@@ -919,6 +928,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix_kernel(const __gr
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(gbase + L::OFF_HOLD), 0);
     pdl_wait();
+    if (blockIdx.x == 0 && threadIdx.x == 0) st_release_gpu(a.ready, 1);
     pdl_trigger();   // only now: paged_own_kernel relies on it
 
     const int64_t U = static_cast<int64_t>(a.hk) * a.prt * (a.ptiles + a.pent);     // below 2^31
@@ -1221,6 +1231,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix2_kernel(const __g
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(gbase + L::OFF_HOLD), 0);
     pdl_wait();
+    if (blockIdx.x == 0 && threadIdx.x == 0) st_release_gpu(a.ready, 1);
     pdl_trigger();   // only now: paged_own_kernel relies on it
 
     const int64_t U = static_cast<int64_t>(a.hk) * a.prt * (a.ptiles + a.pent);     // below 2^31
@@ -1673,6 +1684,7 @@ extern "C" int fuse_paged_attention(const void* q, const void* k_cache, const vo
     a.c = scale * 1.4426950408889634f;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     a.count = reinterpret_cast<int*>(ws + s.count);
+    a.ready = a.count + kOwnGrid * kOwnWarps;
     a.oml = reinterpret_cast<float*>(ws + s.oml);
     a.oo = reinterpret_cast<float*>(ws + s.oo);
     a.where = reinterpret_cast<int*>(ws + s.where);

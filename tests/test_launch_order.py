@@ -42,6 +42,26 @@ def test_dependents_start_with_the_tensor_memory_in_hand():
                     "paged_prefix2_kernel", "w4_tile_kernel"}
 
 
+def test_own_keys_are_read_behind_what_was_written_before():
+    """With a shared prefix the own-key kernel starts while the prefix kernel still runs, without a wait for it.
+    That it may start does not order its reads behind the writes of earlier kernels: the prefix kernel has to
+    release a word after its own wait, the own-key kernel to acquire it before its first read, for its copies
+    (another proxy) too, and the join, which comes after both, to take the word back."""
+    k = kernels()
+    for name in ("paged_prefix_kernel", "paged_prefix2_kernel"):
+        at = [k[name].index(x) for x in ("pdl_wait();", "st_release_gpu(a.ready, 1);", "pdl_trigger();")]
+        assert at == sorted(at), name
+    own = k["paged_own_kernel"]
+    acquire = re.search(r"if \(a\.plen == 0\) \{\s*pdl_wait\(\);\s*\} else \{\s*if \(tid == 32\) \(void\)flag_wait_bounded\(a\.ready, 1, a\.flag\);"
+                        r"\s*__syncthreads\(\);\s*fence_async_global\(\);\s*\}", own)
+    assert acquire
+    read = re.search(r"a\.lens|a\.table \+|__ldcg\(|tma_load", own)
+    assert read and acquire.end() < read.start()
+    join = k["paged_join_kernel"]
+    back = join.index("*a.ready = 0;")
+    assert join.index("pdl_wait();") < back < join.index("__ldcg(")
+
+
 @pytest.mark.gpu
 def test_small_tensor_memory_kernels_in_a_row(cuda_device):
     """Decode GEMM, dense attention and 4-bit tiles, whose CTAs fit on one SM together, back to back on one
