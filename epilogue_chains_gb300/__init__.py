@@ -450,7 +450,8 @@ def fuse_rope_append(qkv, cos_sin, positions, slots, q_out, k_cache, v_cache, in
 
 
 # workspaces of fuse_paged_attention(workspace=None): one zero-filled buffer per (device, stream), grown
-# as needed; every completed call leaves its counters zero
+# as needed; every completed call leaves its counters zero, and fuse_check() drops them after a timeout
+# (their memory is the stream's they were allocated and used on, so work still queued there keeps it)
 _PAGED_WS = {}
 _PAGED_LOCK = threading.Lock()
 
@@ -648,7 +649,14 @@ def fuse_ptxas_table() -> list[dict]:
 
 
 def fuse_check(stream=None) -> int:
-    return _load().fuse_check(_stream(stream))
+    """Synchronize `stream`; FUSE_ETIMEOUT, FUSE_EINDEX or FUSE_ECUDA if a call since the last check met one,
+    else FUSE_OK.  After a timeout the workspaces that this module keeps for fuse_paged_attention() are dropped
+    (a call that was given up leaves arrival counts in them); one that the caller passed is the caller's to zero."""
+    status = _load().fuse_check(_stream(stream))
+    if status == FUSE_ETIMEOUT:
+        with _PAGED_LOCK:
+            _PAGED_WS.clear()
+    return status
 
 
 def fuse_debug_expire_wait(budget_cycles: int, stream=None) -> None:

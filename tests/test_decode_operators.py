@@ -165,3 +165,21 @@ def test_wrapper_refuses_host_tensors():
 
 def test_index_status_has_a_message():
     assert "out of range" in fc.fuse_strerror(fc.FUSE_EINDEX)
+
+
+class _Status:
+    """A library whose fuse_check() returns the given statuses in turn."""
+
+    def __init__(self, *statuses):
+        self.statuses = list(statuses)
+
+    def fuse_check(self, stream):
+        return self.statuses.pop(0)
+
+
+def test_a_timeout_drops_the_modules_workspaces(monkeypatch):
+    """A call that ran into a timeout leaves arrival counts behind; nobody else can zero the module's buffers."""
+    monkeypatch.setattr(fc, "_load", lambda lib=_Status(fc.FUSE_OK, fc.FUSE_EINDEX, fc.FUSE_ECUDA, fc.FUSE_ETIMEOUT): lib)
+    monkeypatch.setattr(fc, "_PAGED_WS", {(0, 0): object(), (0, 7): object()})
+    for want, kept in ((fc.FUSE_OK, 2), (fc.FUSE_EINDEX, 2), (fc.FUSE_ECUDA, 2), (fc.FUSE_ETIMEOUT, 0)):
+        assert fc.fuse_check(7) == want and len(fc._PAGED_WS) == kept

@@ -315,3 +315,17 @@ def test_two_threads_on_one_stream(cuda_device):
     assert not errors and fc.fuse_check() == fc.FUSE_OK
     for w, os in zip(want, outs):
         assert all(torch.equal(o, w) for o in os)
+
+
+def test_a_timeout_leaves_nothing_in_the_modules_workspace(cuda_device):
+    """Counts that a given-up call left in the module's own buffer do not reach the calls after fuse_check()."""
+    import torch
+    p = make([20000, 300], 8, 1, 128, 64, "bf16", seed=21)
+    want = run(p).clone()
+    torch.cuda.synchronize()
+    for ws in fc._PAGED_WS.values():
+        ws[:8192].view(torch.int32)[:1280] = 1                               # one arrival of every item
+    fc.fuse_debug_expire_wait(1000)
+    assert fc.fuse_check() == fc.FUSE_ETIMEOUT
+    for _ in range(3):
+        assert torch.equal(run(p), want)
