@@ -30,8 +30,8 @@ int paged_report(int i, fuse_kernel_record* out);
 int w4_report_count();
 int w4_report(int i, fuse_kernel_record* out);
 // FUSE_ETIMEOUT if a bounded device wait expired, FUSE_EINDEX if a kernel met an index out of range,
-// since the last call (and clears both), else FUSE_OK
-int status_take();
+// since the last call, else FUSE_OK; clears what it has read.  `stream` has been synchronized.
+int status_take(cudaStream_t stream);
 
 namespace {
 thread_local char t_last_error[256] = "";
@@ -271,7 +271,7 @@ extern "C" const char* fuse_last_cuda_error(void) { return fc::t_last_error; }
 extern "C" int fuse_check(fuse_stream_t stream) {
     cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fc::record_cuda_error(e);
-    return fc::status_take();
+    return fc::status_take(reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" int fuse_version(void) { return (1 << 16) | 0; }

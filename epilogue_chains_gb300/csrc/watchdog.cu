@@ -41,16 +41,28 @@ int* index_flag() {
     return p ? p + 1 : nullptr;
 }
 
-int status_take() {
+namespace {
+__device__ int g_fc_taken[2];
+// Read and clear both words, each in one step: what another stream's kernel sets in between stays for the next check.
+__global__ void status_take_kernel() {
+    for (int i = 0; i < 2; ++i) g_fc_taken[i] = atomicExch(&g_fc_status[i], 0);
+}
+}  // namespace
+
+int status_take(cudaStream_t stream) {
     int v[2] = {0, 0};
     if (cudaMemcpyFromSymbol(v, g_fc_status, sizeof(v)) != cudaSuccess) {
         (void)cudaGetLastError();
         return FUSE_OK;
     }
-    if (v[0] || v[1]) {
-        const int zero[2] = {0, 0};
-        (void)cudaMemcpyToSymbol(g_fc_status, zero, sizeof(zero));
-    }
+    if (!v[0] && !v[1]) return FUSE_OK;
+    static std::mutex mu;      // one check at a time over g_fc_taken
+    std::lock_guard<std::mutex> lock(mu);
+    status_take_kernel<<<1, 1, 0, stream>>>();
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) e = cudaMemcpyFromSymbolAsync(v, g_fc_taken, sizeof(v), 0, cudaMemcpyDeviceToHost, stream);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+    if (e != cudaSuccess) return record_cuda_error(e);
     return v[0] ? FUSE_ETIMEOUT : v[1] ? FUSE_EINDEX : FUSE_OK;
 }
 

@@ -78,3 +78,29 @@ def test_kernel_report_needs_no_prior_launch():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_a_check_takes_only_what_it_has_seen(cuda_device):
+    """A wait on another stream that runs out while fuse_check() reads and clears an index error is still
+    reported, by this check or the next.  The check comes after every delay around the wait's end."""
+    import time
+    import torch
+    qkv = torch.zeros(1, 48, dtype=torch.float16, device="cuda")
+    q = torch.zeros(1, 1, 16, dtype=torch.float16, device="cuda")
+    k, v = (torch.zeros(1, 1, 16, 16, dtype=torch.float16, device="cuda") for _ in range(2))
+    cs, zero = torch.zeros(1, 16, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    outside = torch.full((1,), 16, dtype=torch.int32, device="cuda")
+    here, there = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    assert fc.fuse_check() == fc.FUSE_OK
+    for us in range(0, 400):
+        fc.fuse_rope_append(qkv, cs, zero, outside, q, k, v, stream=here)
+        here.synchronize()
+        fc.fuse_debug_expire_wait(1000, stream=there)
+        until = time.perf_counter() + us * 1e-6
+        while time.perf_counter() < until:
+            pass
+        first = fc.fuse_check(stream=here)
+        then = fc.fuse_check(stream=there)
+        assert fc.FUSE_ETIMEOUT in (first, then), (us, first, then)
+        assert first != fc.FUSE_OK and fc.fuse_check() == fc.FUSE_OK
