@@ -1528,53 +1528,61 @@ int own_smem(PagedArgs* a, uint32_t* bytes, int* ctas) {
     return FUSE_OK;
 }
 
+// at least 120 KB, so that one CTA runs per SM (each takes all of TMEM)
+template <int D> constexpr int prefix_smem() { return PrefixLayout<D>::SMEM > 120u * 1024u ? PrefixLayout<D>::SMEM : 120u * 1024u; }
+template <int D> constexpr int prefix2_smem() { return Prefix2Layout<D>::SMEM > 120u * 1024u ? Prefix2Layout<D>::SMEM : 120u * 1024u; }
+
 template <typename T, int D>
-int launch_prefix(const CUtensorMap& mK, const CUtensorMap& mV, const PagedArgs& a, cudaStream_t st) {
-    // at least 120 KB, so that one CTA runs per SM (each takes all of TMEM)
-    if constexpr (D <= 128) {
-        if (a.prow == 256) {
-            constexpr int smem = Prefix2Layout<D>::SMEM > 120u * 1024u ? Prefix2Layout<D>::SMEM : 120u * 1024u;
-            const int rc = opt_in_smem((const void*)paged_prefix2_kernel<T, D>, smem);
-            if (rc != FUSE_OK) return rc;
-            return launch_pdl(paged_prefix2_kernel<T, D>, dim3(static_cast<unsigned>(a.pgrid)), dim3(kPreThreads), smem, st, 1, mK, mV, a);
-        }
-    }
-    constexpr int smem = PrefixLayout<D>::SMEM > 120u * 1024u ? PrefixLayout<D>::SMEM : 120u * 1024u;
-    const int rc = opt_in_smem((const void*)paged_prefix_kernel<T, D>, smem);
-    if (rc != FUSE_OK) return rc;
-    return launch_pdl(paged_prefix_kernel<T, D>, dim3(static_cast<unsigned>(a.pgrid)), dim3(kPreThreads), smem, st, 1, mK, mV, a);
+int prefix_opt_in(const PagedArgs& a) {
+    if constexpr (D <= 128)
+        if (a.prow == 256) return opt_in_smem((const void*)paged_prefix2_kernel<T, D>, prefix2_smem<D>());
+    return opt_in_smem((const void*)paged_prefix_kernel<T, D>, prefix_smem<D>());
 }
 
+template <typename T, int D>
+int launch_prefix(const CUtensorMap& mK, const CUtensorMap& mV, const PagedArgs& a, cudaStream_t st) {
+    const dim3 grid(static_cast<unsigned>(a.pgrid));
+    if constexpr (D <= 128)
+        if (a.prow == 256) return launch_pdl(paged_prefix2_kernel<T, D>, grid, dim3(kPreThreads), prefix2_smem<D>(), st, 1, mK, mV, a);
+    return launch_pdl(paged_prefix_kernel<T, D>, grid, dim3(kPreThreads), prefix_smem<D>(), st, 1, mK, mV, a);
+}
+
+// Everything that can refuse a call comes before the first launch.
 template <typename T, int D>
 int run_paged(PagedArgs a, const void* k, const void* v, cudaStream_t st) {
     const bool bf = std::is_same<T, __nv_bfloat16>::value;
     // A map costs the host about as much as everything else of a call but the launches, so equal ones are made once.
-    CUtensorMap mQ, mK, mV, mK16, mV16;
+    CUtensorMap mQ, mK, mV, mK16, mV16, pK, pV;
     auto maps = [&](int box, CUtensorMap* k_map, CUtensorMap* v_map) {
         return make_map(k_map, k, a.cache_rows, D, 64, box, bf) && make_map(v_map, v, a.cache_rows, D, 64, box, bf);
     };
     const int page = 1 << a.page_shift, box = page < 64 ? page : 64;
-    if (!maps(box, &mK, &mV)) return FUSE_ECUDA;
-    if (a.plen > 0) {
-        CUtensorMap pK = mK, pV = mV;
-        if (page > 64 && !maps(128, &pK, &pV)) return FUSE_ECUDA;
-        if (const int rc = launch_prefix<T, D>(pK, pV, a, st); rc != FUSE_OK) return rc;
-    }
-    mK16 = mK;
-    mV16 = mV;
-    if ((box != 16 && !maps(16, &mK16, &mV16)) || !make_map(&mQ, a.q, static_cast<int64_t>(a.batch) * a.hq, D, 64, a.rows, bf)) return FUSE_ECUDA;
+    if (!maps(box, &mK, &mV) || !make_map(&mQ, a.q, static_cast<int64_t>(a.batch) * a.hq, D, 64, a.rows, bf)) return FUSE_ECUDA;
+    mK16 = pK = mK;
+    mV16 = pV = mV;
+    if (box != 16 && !maps(16, &mK16, &mV16)) return FUSE_ECUDA;
+    if (a.plen > 0 && page > 64 && !maps(128, &pK, &pV)) return FUSE_ECUDA;
     uint32_t smem = 0;
     int ctas = 0;
     int rc = own_smem<D>(&a, &smem, &ctas);
     if (rc != FUSE_OK) return rc;
     rc = opt_in_smem((const void*)paged_own_kernel<T, D>, kOwnSmem, true);
     if (rc != FUSE_OK) return rc;
+    if (a.plen > 0) {
+        rc = prefix_opt_in<T, D>(a);
+        if (rc != FUSE_OK) return rc;
+    }
     // every CTA is resident at once; more than there can be units would have nothing to do
     int64_t grid = static_cast<int64_t>(sm_count()) * ctas;
     const int64_t units = static_cast<int64_t>(a.batch) * a.hk * a.rt * (ceil_div(a.table_ld << a.page_shift, kUnit) + 2);
     if (grid > units) grid = units;
     if (grid > kOwnGrid) grid = kOwnGrid;
-    if (units / grid >= 0x7fffffffLL) return FUSE_EUNSUPPORTED;
+    if (units / grid >= 0x7fffffffLL) return FUSE_EUNSUPPORTED;   // a CTA counts its places in 32 bits
+
+    if (a.plen > 0) {
+        rc = launch_prefix<T, D>(pK, pV, a, st);
+        if (rc != FUSE_OK) return rc;
+    }
     rc = launch_pdl(paged_own_kernel<T, D>, dim3(static_cast<unsigned>(grid)), dim3(kOwnThreads), smem, st, 1, mQ, mK, mV, mK16, mV16, a);
     if (rc != FUSE_OK || a.plen == 0) return rc;
     const int64_t warps = static_cast<int64_t>(a.batch) * a.hq;
@@ -1646,7 +1654,7 @@ extern "C" int fuse_paged_attention(const void* q, const void* k_cache, const vo
     if (batch > kMaxBatch || q_heads > 65536 || batch * q_heads >= top || num_pages >= top / (kv_heads * page_size) ||
         table_ld >= (top - 4096) / page_size || prefix_len >= top - 4096)
         return FUSE_EUNSUPPORTED;
-    // places of the whole batch, and tiles of the prefix, stay below 2^31
+    // places of the whole batch, and tiles of the prefix, stay below 2^31 (and a CTA's places: see run_paged())
     if ((table_ld * page_size / kUnit + 2) * batch >= top) return FUSE_EUNSUPPORTED;
     const int64_t group = q_heads / kv_heads;
     if (prefix_len > 0 && (ceil_div(prefix_len, 128) + kEntry) * kv_heads * ceil_div(batch * group, 128) >= top) return FUSE_EUNSUPPORTED;

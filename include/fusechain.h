@@ -383,7 +383,9 @@ int fuse_rope_append(const void* qkv, int64_t ld, const float* cos_sin, int64_t 
  *   Rules: dtype FUSE_F16 or FUSE_BF16; D in {64, 128, 256}; q_heads a multiple of kv_heads; page_size
  *          a power of two, 16..256; batch <= 4096; num_pages kv_heads page_size, table_ld page_size
  *          and prefix_len below 2^31 - 4096, batch table_ld page_size / 64 and (prefix_len / 128)
- *          kv_heads (rows per key/value head / 128) below 2^31 (else FUSE_EUNSUPPORTED); scale > 0;
+ *          kv_heads (rows per key/value head / 128) below 2^31, batch kv_heads ceil(q_heads / kv_heads /
+ *          16) (table_ld page_size / 64 + 2) below 2^31 for each CTA of the own-key kernel, as whatever is
+ *          below 2^38 in all is (else FUSE_EUNSUPPORTED, and nothing is enqueued); scale > 0;
  *          tensors 16-byte aligned, tables and lengths 4-byte.
  *   Out of range in device memory (fuse_check() then returns FUSE_EINDEX): a page index outside
  *   [0, num_pages) counts as a page of zeros; a length is taken into 0 .. table_ld page_size.

@@ -329,3 +329,21 @@ def test_a_timeout_leaves_nothing_in_the_modules_workspace(cuda_device):
     assert fc.fuse_check() == fc.FUSE_ETIMEOUT
     for _ in range(3):
         assert torch.equal(run(p), want)
+
+
+def test_a_refused_call_enqueues_nothing(cuda_device):
+    """65536 heads with room for 2^31 - 4112 keys each are more places than a CTA counts: refused, with the shared
+    prefix, which could be read, left alone."""
+    import torch
+    heads, page = 65536, 16
+    ld = ((1 << 31) - 4096) // page - 1
+    q = torch.zeros(1, heads, 64, dtype=torch.bfloat16, device="cuda")
+    o = torch.full_like(q, 7.0)
+    k, v = (torch.zeros(1, heads, page, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    table = torch.zeros(1, ld, dtype=torch.int32, device="cuda")
+    lens, ptable = torch.ones(1, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(fc.fuse_paged_attention_workspace_bytes(1, heads, heads, 64, page), dtype=torch.uint8, device="cuda")
+    with pytest.raises(fc.FuseError) as e:
+        fc.fuse_paged_attention(q, k, v, table, lens, o, 0.125, prefix_table=ptable, prefix_len=page, workspace=ws)
+    assert e.value.status == fc.FUSE_EUNSUPPORTED
+    assert fc.fuse_check() == fc.FUSE_OK and not ws.any() and bool((o == 7).all())
