@@ -125,7 +125,8 @@ __device__ __forceinline__ void join_parts(int c0, int c1, float& m, float& l, f
 #pragma unroll
         for (int i = 0; i < 8; ++i) po[i] = __ldcg(part(min(c + i, c1), pm[i], pl[i]));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) join(m, l, acc, c + i <= c1 ? pm[i] : -INFINITY, pl[i], po[i]);
+        for (int i = 0; i < 8; ++i)     // (past the last part nothing: an infinite sum once more, times zero, would be NaN)
+            if (c + i <= c1) join(m, l, acc, pm[i], pl[i], po[i]);
     }
 }
 

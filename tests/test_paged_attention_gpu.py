@@ -347,3 +347,27 @@ def test_a_refused_call_enqueues_nothing(cuda_device):
         fc.fuse_paged_attention(q, k, v, table, lens, o, 0.125, prefix_table=ptable, prefix_len=page, workspace=ws)
     assert e.value.status == fc.FUSE_EUNSUPPORTED
     assert fc.fuse_check() == fc.FUSE_OK and not ws.any() and bool((o == 7).all())
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("prefix", [0, 1000])
+def test_infinite_values(cuda_device, D, prefix):
+    """A component whose only infinite value has a weight is infinite, however many CTAs share the keys; the
+    others are as they would be without it."""
+    import torch
+    p = make([9000, 200, 40], 8, 2, D, 64, "bf16", prefix=prefix, seed=22, std=0.25)
+    clean = run(p).clone()
+    v = p["v"] = p["v"].clone()
+    at = []
+    for b, keys in enumerate(([70, 4000, 8999], [0, 199], [39])):
+        for n, key in enumerate(keys):
+            v[int(p["table"][b, key // 64]), :, key % 64, n] = -math.inf if n else math.inf
+            at.append((b, n, -math.inf if n else math.inf))
+    if prefix:
+        v[int(p["ptable"][500 // 64]), :, 500 % 64, 9] = math.inf
+        at += [(b, 9, math.inf) for b in range(3)]
+    o = run(p)
+    for b, c, x in at:
+        assert bool((o[b, :, c] == x).all()), (b, c, o[b, :, c])
+        o[b, :, c] = clean[b, :, c]
+    assert torch.equal(o, clean)
