@@ -1533,6 +1533,17 @@ int own_smem(PagedArgs* a, uint32_t* bytes, int* ctas) {
 template <int D> constexpr int prefix_smem() { return PrefixLayout<D>::SMEM > 120u * 1024u ? PrefixLayout<D>::SMEM : 120u * 1024u; }
 template <int D> constexpr int prefix2_smem() { return Prefix2Layout<D>::SMEM > 120u * 1024u ? Prefix2Layout<D>::SMEM : 120u * 1024u; }
 
+// What the report gives as shared memory of paged_own_kernel: a launch's for one sequence and groups of four heads.
+template <int D>
+int own_report_smem() {
+    PagedArgs a{};
+    a.batch = 1;
+    a.rows = 4;
+    uint32_t bytes = 0;
+    int ctas = 0;
+    return own_smem<D>(&a, &bytes, &ctas) == FUSE_OK ? static_cast<int>(bytes) : 0;
+}
+
 template <typename T, int D>
 int prefix_opt_in(const PagedArgs& a) {
     if constexpr (D <= 128)
@@ -1594,9 +1605,8 @@ int run_paged(PagedArgs a, const void* k, const void* v, cudaStream_t st) {
 
 int paged_report_count() { return 22; }
 int paged_report(int i, fuse_kernel_record* out) {
-    const int smem_own = 111 * 1024;
     switch (i) {
-#define FC_OWN(N, T, TN, D) case N: return describe_kernel((const void*)paged_own_kernel<T, D>, "paged_own_kernel<" TN ", D=" #D "> (own keys)", kOwnThreads, smem_own, out)
+#define FC_OWN(N, T, TN, D) case N: return describe_kernel((const void*)paged_own_kernel<T, D>, "paged_own_kernel<" TN ", D=" #D "> (own keys)", kOwnThreads, own_report_smem<D>(), out)
 #define FC_PRE(N, T, TN, D) case N: return describe_kernel((const void*)paged_prefix_kernel<T, D>, "paged_prefix_kernel<" TN ", D=" #D "> (shared prefix, tcgen05)", kPreThreads, PrefixLayout<D>::SMEM, out, PrefixLayout<D>::TMEM_COLS)
         FC_OWN(0, __nv_bfloat16, "bf16", 64);
         FC_OWN(1, __nv_bfloat16, "bf16", 128);

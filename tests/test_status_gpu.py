@@ -104,3 +104,15 @@ def test_a_check_takes_only_what_it_has_seen(cuda_device):
         then = fc.fuse_check(stream=there)
         assert fc.FUSE_ETIMEOUT in (first, then), (us, first, then)
         assert first != fc.FUSE_OK and fc.fuse_check() == fc.FUSE_OK
+
+
+def test_kernel_report_gives_the_own_key_kernels_launch(cuda_device):
+    """D = 256 runs one CTA per SM with most of its shared memory, the others two."""
+    own = {r["name"]: r for r in (fc.fuse_kernel_report(i) for i in range(fc.fuse_kernel_count()))
+           if r["name"].startswith("paged_own_kernel")}
+    assert len(own) == 6
+    for name, r in own.items():
+        one = "D=256" in name
+        assert r["blocks_per_sm"] == (1 if one else 2), r
+        # query rows and parts, and a ring of at least 64 KB
+        assert (120 if one else 64) * 1024 < r["dynamic_smem_bytes"] <= (226 if one else 112) * 1024, r
