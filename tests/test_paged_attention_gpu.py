@@ -371,3 +371,17 @@ def test_infinite_values(cuda_device, D, prefix):
         assert bool((o[b, :, c] == x).all()), (b, c, o[b, :, c])
         o[b, :, c] = clean[b, :, c]
     assert torch.equal(o, clean)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_growing_scores(cuda_device, dtype, D):
+    """Own keys six times as long at the end of every 1024 as at their start: the reference follows, run after run."""
+    import torch
+    p = make([30000, 2000, 130], 16, 2, D, 64, dtype, seed=23)
+    for b in range(3):
+        n = int(p["lens"][b])
+        ids = p["table"][b, :-(-n // 64)].long()
+        long = 1 + 5 * (torch.arange(len(ids), device="cuda") % 16) / 15
+        p["k"][ids] = (p["k"][ids].float() * long[:, None, None, None]).to(p["k"].dtype)
+    check(p)
