@@ -168,6 +168,22 @@ def summarize_clocks(rows, t0, t1):
             "samples": len(inside)}
 
 
+# ------------------------------------------------------------------------ kernel report
+# families of kernels that the rows launch
+ROW_KERNELS = ("chain_", "rmsnorm_", "rms_", "softmax_", "sm_", "gemm_", "epi_", "silu_", "attn_")
+REPORT_FIELDS = ("name", "regs_per_thread", "local_bytes_per_thread", "dynamic_smem_bytes", "block_threads",
+                 "blocks_per_sm", "cluster_size", "max_active_clusters", "blocks_per_sm_api", "tmem_cols",
+                 "ptxas_registers", "stack_bytes", "spill_store_bytes", "spill_load_bytes")
+
+
+def kernel_report(fc):
+    """Register / occupancy report of the kernels of this benchmark's rows ([K4] §③, [C05] §6.2).  The
+    library's other kernels, some fifty variants, are left to fuse_kernel_report(): with them the one
+    line of output was 38 KB long, with these it is 18."""
+    recs = (fc.fuse_kernel_report(i) for i in range(fc.fuse_kernel_count()))
+    return [{k: r[k] for k in REPORT_FIELDS} for r in recs if r["name"].startswith(ROW_KERNELS)]
+
+
 # ------------------------------------------------------------------------------ traffic
 def committed_traffic(group: str, src_name: str):
     """DRAM bytes per launch of a kernel from its committed ncu summary (profiles/<group>.txt),
@@ -652,16 +668,7 @@ def run_ours(args, rank, world, local):
             r4["frac_of_fp16_in_run"] = round(r4["achieved"] / tp["fp16_tflops"], 4)
             r4["fp16_peak_in_run"] = tp["fp16_tflops"]
 
-    # register / occupancy report of every kernel variant ([K4] §③, [C05] §6.2)
-    report_rows = []
-    for i in range(fc.fuse_kernel_count()):
-        r_ = fc.fuse_kernel_report(i)
-        report_rows.append({k: r_[k] for k in ("name", "regs_per_thread", "local_bytes_per_thread",
-                                               "dynamic_smem_bytes", "block_threads", "blocks_per_sm",
-                                               "cluster_size", "max_active_clusters", "blocks_per_sm_api",
-                                               "tmem_cols", "ptxas_registers",
-                                               "stack_bytes", "spill_store_bytes", "spill_load_bytes")})
-    rows["kernel_report"] = report_rows
+    rows["kernel_report"] = kernel_report(fc)
 
     # ---------------------------------------------------------------- e2e through host buffers
     e2e = run_e2e(args, fc, lib, wl, stage_sets, N, KS, chain_bytes, dev, stream, world)
