@@ -801,6 +801,7 @@ struct PrefixLayout {
     static constexpr uint32_t SMEM = OFF_HOLD + 16 + 1024;
     static constexpr uint32_t TMEM_COLS = 512, O_COL = 256;    // two 128-column score buffers, then O
     static_assert(SMEM <= 232448, "shared-memory budget");
+    static_assert(SMEM > 116 * 1024, "one CTA per SM: each takes all of TMEM");
 };
 
 // A whole 32-byte sector per thread.
@@ -1187,6 +1188,7 @@ struct Prefix2Layout {
     static constexpr uint32_t SMEM = OFF_HOLD + 16 + 1024;
     static constexpr uint32_t TMEM_COLS = 512, O_COL = 256;    // scores of tile t at 128 t, output at 256 + D t
     static_assert(SMEM <= 232448, "shared-memory budget");
+    static_assert(SMEM > 116 * 1024, "one CTA per SM: each takes all of TMEM");
 };
 
 template <typename T, int D>
@@ -1529,10 +1531,6 @@ int own_smem(PagedArgs* a, uint32_t* bytes, int* ctas) {
     return FUSE_OK;
 }
 
-// at least 120 KB, so that one CTA runs per SM (each takes all of TMEM)
-template <int D> constexpr int prefix_smem() { return PrefixLayout<D>::SMEM > 120u * 1024u ? PrefixLayout<D>::SMEM : 120u * 1024u; }
-template <int D> constexpr int prefix2_smem() { return Prefix2Layout<D>::SMEM > 120u * 1024u ? Prefix2Layout<D>::SMEM : 120u * 1024u; }
-
 // What the report gives as shared memory of paged_own_kernel: a launch's for one sequence and groups of four heads.
 template <int D>
 int own_report_smem() {
@@ -1547,16 +1545,16 @@ int own_report_smem() {
 template <typename T, int D>
 int prefix_opt_in(const PagedArgs& a) {
     if constexpr (D <= 128)
-        if (a.prow == 256) return opt_in_smem((const void*)paged_prefix2_kernel<T, D>, prefix2_smem<D>());
-    return opt_in_smem((const void*)paged_prefix_kernel<T, D>, prefix_smem<D>());
+        if (a.prow == 256) return opt_in_smem((const void*)paged_prefix2_kernel<T, D>, Prefix2Layout<D>::SMEM);
+    return opt_in_smem((const void*)paged_prefix_kernel<T, D>, PrefixLayout<D>::SMEM);
 }
 
 template <typename T, int D>
 int launch_prefix(const CUtensorMap& mK, const CUtensorMap& mV, const PagedArgs& a, cudaStream_t st) {
     const dim3 grid(static_cast<unsigned>(a.pgrid));
     if constexpr (D <= 128)
-        if (a.prow == 256) return launch_pdl(paged_prefix2_kernel<T, D>, grid, dim3(kPreThreads), prefix2_smem<D>(), st, 1, mK, mV, a);
-    return launch_pdl(paged_prefix_kernel<T, D>, grid, dim3(kPreThreads), prefix_smem<D>(), st, 1, mK, mV, a);
+        if (a.prow == 256) return launch_pdl(paged_prefix2_kernel<T, D>, grid, dim3(kPreThreads), Prefix2Layout<D>::SMEM, st, 1, mK, mV, a);
+    return launch_pdl(paged_prefix_kernel<T, D>, grid, dim3(kPreThreads), PrefixLayout<D>::SMEM, st, 1, mK, mV, a);
 }
 
 // Everything that can refuse a call comes before the first launch.

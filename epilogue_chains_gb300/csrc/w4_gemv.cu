@@ -535,8 +535,8 @@ struct TileLayout {
 };
 
 struct TileArgs {
-    int M, N, KG;
-    int nchunk;        // 128-k chunks, the last one possibly partial
+    int M, N;
+    int nchunk;        // 128-k chunks (whole ones: scales that the copy engine can load make K a multiple of 256)
     int per;           // chunks of a CTA
     int split, gelu, zeros;
     int y_vec;         // y is 8-byte aligned
@@ -897,8 +897,7 @@ int launch_tile(const W4Args& w, cudaStream_t st) {
     TileArgs a{};
     a.M = w.M;
     a.N = w.N;
-    a.KG = w.K / G;
-    a.nchunk = static_cast<int>(ceil_div(w.K, 128));
+    a.nchunk = w.K / 128;
     a.gelu = w.gelu;
     a.zeros = w.z ? 1 : 0;
     a.y_vec = is_aligned(w.y, 8) ? 1 : 0;
@@ -929,11 +928,12 @@ int launch_tile(const W4Args& w, cudaStream_t st) {
         }
     }
     CUtensorMap mW{}, mX{}, mS{}, mZ{};
+    const int64_t KG = w.K / G;
     const int64_t wd[3] = {w.K / 2, w.N, 1}, ws[2] = {w.K / 2, static_cast<int64_t>(w.K / 2) * w.N};
     const int wb[3] = {64, 128, 1};
-    const int64_t sd[3] = {a.KG, w.N, 1}, ss[2] = {static_cast<int64_t>(a.KG) * 2, static_cast<int64_t>(a.KG) * 2 * w.N};
+    const int64_t sd[3] = {KG, w.N, 1}, ss[2] = {KG * 2, KG * 2 * w.N};
     const int sbx[3] = {8, 128, 1};
-    const int64_t zd[3] = {a.KG, w.N, 1}, zs[2] = {a.KG, static_cast<int64_t>(a.KG) * w.N};
+    const int64_t zd[3] = {KG, w.N, 1}, zs[2] = {KG, KG * w.N};
     const int zbx[3] = {16, 128, 1};
     if (!make_map_3d(&mW, w.wq, kMapU8, wd, ws, wb, 64) || !make_map(&mX, w.x, w.M, w.K, 64, w.M, std::is_same<T, __nv_bfloat16>::value) ||
         !make_map_3d(&mS, w.s, kMap16, sd, ss, sbx, 0) || (w.z && !make_map_3d(&mZ, w.z, kMapU8, zd, zs, zbx, 0)))
