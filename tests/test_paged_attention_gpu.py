@@ -385,3 +385,9 @@ def test_growing_scores(cuda_device, dtype, D):
         long = 1 + 5 * (torch.arange(len(ids), device="cuda") % 16) / 15
         p["k"][ids] = (p["k"][ids].float() * long[:, None, None, None]).to(p["k"].dtype)
     check(p)
+
+
+@pytest.mark.parametrize("prefix", [0, 40])
+def test_the_largest_tables_in_shared_memory(cuda_device, prefix):
+    """4096 sequences at 16 rows of D = 256: what is left of an SM's shared memory holds a ring of one slot."""
+    check(make([(7 * i) % 90 if i % 64 == 0 else i % 2 for i in range(4096)], 16, 1, 256, 16, "bf16", prefix=prefix, seed=24))
