@@ -13,12 +13,12 @@
 //    warp loads units by TMA into a ring, four compute: each multiplies its 16 keys of a unit with the
 //    query rows by mma.sync (16 rows, mostly one group), and the warps' parts meet in shared memory when
 //    a run ends.  Parts of a sequence that several CTAs share go through the workspace: the CTA that
-//    arrives last joins them, in the order of the keys (with a prefix, paged_join_kernel does).  3 x 65536 keys (D = 128) take 108 us, 0.97 of
-//    the copy rate; 32 sequences of up to 4096 keys 49.4 us, 0.84.
+//    arrives last joins them, in the order of the keys (with a prefix, paged_join_kernel does).  3 x 65536 keys (D = 128) take 109 us, 0.97 of
+//    the copy rate; 32 sequences of up to 4096 keys 50 us, 0.83.
 //  * paged_prefix_kernel, paged_prefix2_kernel: the shared prefix.  Here all batch * group query rows of a
 //    key/value head meet the same keys: tcgen05 tiles of 128 or 256 rows by 128 keys, scores and output
 //    in TMEM, the key axis split over the SMs.  1024 rows per head over 16384 keys (8 heads, D = 128) take
-//    49 us of the call's 90, 1.4 PFLOP/s.
+//    49 us of the call's 91, 1.4 PFLOP/s.
 //  * paged_join_kernel, with a prefix: a row's own parts and the prefix's.
 //
 // The lengths are in device memory, so one launch configuration (and a captured graph) serves every
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnLayout<D>::CTAS) paged_own_ker
             return a.cache_rows;         // past the cache: zeros
         };
         const uint32_t one = elect_one();
-        const uint64_t once = policy_evict_first();      // ragged batch 51.8 -> 49.4 us: what else lies in L2 stays there
+        const uint64_t once = policy_evict_first();      // ragged batch 51.8 -> 49.4 us then: what else lies in L2 stays there
         int slot = 0, loads = 0, qs = 0, qloads = 0;
         uint32_t phase = 0, qphase = 0;          // completions of the current slot's barriers so far, mod 2
         bool ok = true;
@@ -600,7 +600,9 @@ __global__ void __launch_bounds__(kOwnThreads, OwnLayout<D>::CTAS) paged_own_ker
                 }
                 l0 += (s[0][0] + s[0][1]) + (s[1][0] + s[1][1]);
                 l1 += (s[0][2] + s[0][3]) + (s[1][2] + s[1][3]);
-                // the weights rounded to T for the product with V; the sums above are of the unrounded ones
+                // The weights rounded to T for the product with V, whose other operand has that type; the sums above are
+                // of the unrounded ones.  It moves the output by as much as rounding it to T does (1.4 times the error
+                // of the rounding alone, in all); carrying what is rounded off would take every product with V twice.
                 p[0] = pack2<T>(s[0][0], s[0][1]);
                 p[1] = pack2<T>(s[0][2], s[0][3]);
                 p[2] = pack2<T>(s[1][0], s[1][1]);
@@ -1078,7 +1080,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix_kernel(const __gr
                     m = x - SH;
                 }
                 const float ref = m == -INFINITY ? 0.0f : m;
-                uint32_t pk[HK / 2];
+                uint32_t pk[HK / 2];     // the weights rounded to T, as in paged_own_kernel
                 const float2 c2 = make_float2(a.c, a.c), nm2 = make_float2(-ref, -ref);
                 float2 sum2 = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -1405,7 +1407,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefix2_kernel(const __g
                 uint8_t* prow = gbase + L::OFF_P + t * L::P_BYTES + r * 128;
 #pragma unroll
                 for (int q = 0; q < 16; ++q) {
-                    uint32_t w[4];
+                    uint32_t w[4];       // the weights rounded to T, as in paged_own_kernel
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const float2 e = __ffma2_rn(make_float2(x[8 * q + 2 * k], x[8 * q + 2 * k + 1]), c2, nm2);

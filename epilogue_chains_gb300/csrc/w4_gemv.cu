@@ -502,9 +502,10 @@ int launch_w4(W4Args a, cudaStream_t st) {
 // TMEM column), X is the B operand from shared memory, and every group of k has its own fp32 accumulator
 // in TMEM, which is read out, multiplied by the group's scale and added up in registers.
 //
-// Measured: 64 x 28672 x 4096 in groups of 64 35.5 us, 64 x 4096 x 4096 in groups of 128 11.5 us, 32 x 8192 x 8192 18.1 us.  Not the loads but
-// the chain of a unit (unpack, MMAs, read-out) and its instructions bound it: the SMs issue half of the time, and
-// separate warps for unpacking and reading out were no faster (38.5 us).
+// Measured: 64 x 28672 x 4096 in groups of 64 36.9 us, 64 x 4096 x 4096 in groups of 128 11.5 us, 32 x 8192 x 8192 18.0 us.
+// Not the loads (36.7 us with X loaded for the first stages only, 36.9 with the weights so) but the chain of a unit
+// (unpack, MMAs, read-out) and its instructions bound it: the SMs issue half of the time.  Separate warps for unpacking
+// and for reading out took 38.5 us when this form took 35.4.
 //
 // 320 threads: warps 0-7 work (TMEM lane quadrant warp % 4, i.e. 32 weight rows, one per lane; half
 // warp / 4 of a unit's k when unpacking and of the tokens when reading out), warp 8 issues the MMAs, warp 9
@@ -948,6 +949,8 @@ int run_w4_g(const W4Args& a, cudaStream_t st) {
     const bool fits = scales_fit(a, G);
     // More than 8 tokens take another pass of w4_gemv_kernel over the weights.  At 9 tokens it takes 8.5 us for 4096 x
     // 4096 (tiles 8.2), 22.2 for 8192 x 8192 (17.2), 41 for 28672 x 4096 (29); at 8 7.8, 13.4 and 19.8.
+    // Without scales that the copy engine can load it is those passes all the same: 64 x 4096 x 11008 in groups of 128
+    // (86 scales a row) takes 51 us where 64 x 4096 x 11264 takes 17.8, 16 tokens 16.8 and 14.6, up to 8 are as fast.
     if (fits && a.M > 8) {
         if (a.M <= 16) return launch_tile<T, G, 16>(a, st);
         if (a.M <= 32) return launch_tile<T, G, 32>(a, st);
