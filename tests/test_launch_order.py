@@ -91,3 +91,42 @@ def test_small_tensor_memory_kernels_in_a_row(cuda_device):
     assert fc.fuse_check() == fc.FUSE_OK
     assert all(torch.equal(a, b) for a, b in zip((y, z, o), first))
     assert all(bool(t.isfinite().all()) for t in first)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("prefix,D,batch", [(40, 64, 3), (900, 128, 48), (300, 256, 8), (0, 128, 5)])
+def test_attention_sees_the_append_before_it(cuda_device, prefix, D, batch):
+    """Two tokens in turn overwrite the last place of every sequence, queries, keys and values, each followed at
+    once by attention over it, without a wait in between: every output is of its own token."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(6)
+    hq, hk, page, per = 8, 2, 16, 5
+    shared = -(-prefix // page)
+    pages = batch * per + shared
+    k, v = (torch.randn(pages, hk, page, D, generator=g, device="cuda").bfloat16() for _ in range(2))
+    table = torch.arange(batch * per, dtype=torch.int32, device="cuda").view(batch, per)
+    ptable = torch.arange(batch * per, pages, dtype=torch.int32, device="cuda") if prefix else None
+    lens = 1 + torch.arange(batch, dtype=torch.int32, device="cuda") * 7 % (page * per)
+    last = lens - 1
+    slots = table[torch.arange(batch, device="cuda"), last.long() // page] * page + last % page
+    cs = torch.cat([torch.ones(100, D // 2), torch.zeros(100, D // 2)], 1).cuda()
+    pos = torch.zeros(batch, dtype=torch.int32, device="cuda")
+    qkv = [torch.randn(batch, (hq + 2 * hk) * D, generator=g, device="cuda").bfloat16() for _ in range(2)]
+    q = torch.empty(batch, hq, D, device="cuda").bfloat16()
+    ws = torch.zeros(fc.fuse_paged_attention_workspace_bytes(batch, hq, hk, D, prefix), dtype=torch.uint8, device="cuda")
+
+    def step(i, o):
+        fc.fuse_rope_append(qkv[i], cs, pos, slots, q, k, v)
+        fc.fuse_paged_attention(q, k, v, table, lens, o, 0.1, prefix_table=ptable, prefix_len=prefix, workspace=ws)
+
+    want = [torch.empty_like(q) for _ in range(2)]
+    for i in range(2):
+        step(i, want[i])
+        torch.cuda.synchronize()
+    assert not torch.equal(want[0], want[1])
+    outs = [torch.empty_like(q) for _ in range(400)]
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        step(i % 2, o)
+    assert fc.fuse_check() == fc.FUSE_OK and not ws[:8192].any()
+    assert all(torch.equal(o, want[i % 2]) for i, o in enumerate(outs))
