@@ -113,6 +113,18 @@ SIGNATURES = {
     "fuse_paged_attention_flops": ([_I64, _I64, _I64, _I64, _I64], _I64),
     "fuse_w4_gemv": ([_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I32, _I32, _P], _I32),
     "fuse_w4_gemv_bytes": ([_I64, _I64, _I64, _I64, _I32, _I32, _I32], _I64),
+    "fuse_prompt_attention": ([_P, _I64, _P, _P, _P, _I64, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64, _I64,
+                               _F32, _I32, _P, _SZ, _P], _I32),
+    "fuse_prompt_attention_workspace_bytes": ([_I64, _I64, _I64, _I64], _SZ),
+    "fuse_prompt_attention_bytes": ([_I64, _I64, _I64, _I64, _I64], _I64),
+    "fuse_prompt_attention_flops": ([_I64, _I64, _I64], _I64),
+    "fuse_mxfp4_quantize": ([_P, _I64, _P, _P, _I64, _I64, _I32, _P], _I32),
+    "fuse_mxfp4_dequantize": ([_P, _P, _P, _I64, _I64, _I32, _P], _I32),
+    "fuse_mxfp4_scale_bytes": ([_I64, _I64], _I64),
+    "fuse_mxfp4_gemm": ([_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _I32, _P], _I32),
+    "fuse_mxfp4_gemm_bytes": ([_I64, _I64, _I64, _I32, _I32], _I64),
+    "fuse_token_logprobs": ([_P, _I64, _P, _P, _P, _P, _P, _I64, _I64, _I64, _F32, _I32, _P], _I32),
+    "fuse_token_logprobs_bytes": ([_I64, _I64, _I64, _I32], _I64),
     "fuse_kernel_count": ([], _I32),
     "fuse_kernel_report": ([_I32, ctypes.POINTER(fuse_kernel_record)], _I32),
     "fuse_ptxas_count": ([], _I32),
@@ -545,6 +557,182 @@ def fuse_paged_attention_flops(batch: int, q_heads: int, D: int, prefix_len: int
 def fuse_w4_gemv_bytes(M: int, N: int, K: int, group: int, zeros: bool = False, bias: bool = False,
                        residual: bool = False) -> int:
     return _load().fuse_w4_gemv_bytes(M, N, K, group, int(zeros), int(bias), int(residual))
+
+
+# ------------------------------------------------------------------------------- whole prompts
+# workspaces of fuse_prompt_attention(workspace=None): one buffer per (device, stream), of any content, grown as needed
+_PROMPT_WS = {}
+_PROMPT_LOCK = threading.Lock()
+
+
+def _prompt_workspace(need: int, dev: int, stream_handle):
+    torch = _torch
+    if stream_handle != _current_handle(dev) or torch.cuda.is_current_stream_capturing():
+        raise ValueError("pass a workspace of fuse_prompt_attention_workspace_bytes() bytes: this module's own ones serve "
+                         "calls on torch's current stream outside a graph capture only (a captured graph may be replayed "
+                         "next to other calls)")
+    ws = _PROMPT_WS.get((dev, stream_handle))
+    if ws is None or ws.numel() < need:
+        ws = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", dev))   # on the current stream
+        _PROMPT_WS[dev, stream_handle] = ws
+    return ws
+
+
+def fuse_prompt_attention(q, k_cache, v_cache, block_table, cu_queries, seq_lens, o, scale: float, workspace=None,
+                          stream=None) -> None:
+    """Causal attention of packed prompts: rows cu_queries[b] .. cu_queries[b + 1] - 1 of q (its rows may be strided) and
+    o, [tokens, q_heads, D], are sequence b's new tokens, and the last of its seq_lens[b] keys in the pages of
+    block_table[b] are theirs; k_cache, v_cache [num_pages, kv_heads, page_size, D].  Rows behind the last sequence are
+    left as they are.  workspace: a device tensor of fuse_prompt_attention_workspace_bytes() bytes; None: a buffer kept by
+    this module for the current stream."""
+    torch = _torch or _bind_torch()
+    dt, i32 = q.dtype, torch.int32
+    dev = _decode_operands(dt, (k_cache, v_cache, o), ((block_table, i32), (cu_queries, i32), (seq_lens, i32)))
+    tokens, q_heads, D = q.shape
+    pages, kv_heads, page_size, D2 = k_cache.shape
+    if (q.get_device() != dev or q.stride(2) != 1 or (q_heads > 1 and q.stride(1) != D)):
+        raise ValueError("q must be on the device of the others, each row of it contiguous")
+    if (D2 != D or o.shape != q.shape or v_cache.shape != k_cache.shape or block_table.dim() != 2
+            or seq_lens.shape != (block_table.shape[0],) or cu_queries.shape != (block_table.shape[0] + 1,)):
+        raise ValueError("shape mismatch")
+    ld = q.stride(0) if tokens > 1 else q_heads * D
+    lib, sh = _load(), _stream(stream)
+    own = workspace is None
+    if not own and (workspace.get_device() != dev or not workspace.is_contiguous()):
+        raise ValueError("the workspace must be a contiguous tensor on the device of the others")
+    if own:      # a call is two launches: those of two threads on one stream must not mix over one workspace
+        _PROMPT_LOCK.acquire()
+    try:
+        if own:
+            workspace = _prompt_workspace(fuse_prompt_attention_workspace_bytes(tokens, q_heads, kv_heads, D), dev, sh)
+        status = lib.fuse_prompt_attention(q.data_ptr(), ld, k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                                           block_table.shape[1], cu_queries.data_ptr(), seq_lens.data_ptr(), o.data_ptr(),
+                                           tokens, block_table.shape[0], q_heads, kv_heads, D, pages, page_size, scale,
+                                           FUSE_F16 if dt is torch.float16 else FUSE_BF16, workspace.data_ptr(),
+                                           workspace.nbytes, sh)
+    finally:
+        if own:
+            _PROMPT_LOCK.release()
+    _check(status, "fuse_prompt_attention")
+
+
+@functools.lru_cache(maxsize=256)
+def fuse_prompt_attention_workspace_bytes(tokens: int, q_heads: int, kv_heads: int, D: int) -> int:
+    return _load().fuse_prompt_attention_workspace_bytes(tokens, q_heads, kv_heads, D)
+
+
+def _float_code(dt) -> int:
+    torch = _torch
+    if dt is torch.bfloat16:
+        return FUSE_BF16
+    if dt is torch.float16:
+        return FUSE_F16
+    if dt is torch.float32:
+        return FUSE_F32
+    raise ValueError(f"fp16, bf16 or fp32 tensors expected, not {dt}")
+
+
+def _on_device(dev: int, *ts) -> None:
+    """Contiguous tensors on device `dev`, which must be torch's current one; pairs of a tensor or None and its dtype."""
+    if dev != _current_device():
+        raise ValueError("the tensors must be on the current CUDA device")
+    for t, want in ts:
+        if t is not None and (t.dtype is not want or t.get_device() != dev or not t.is_contiguous()):
+            raise ValueError(f"{tuple(t.shape)} {t.dtype} on {t.device}: contiguous {want} on one device expected")
+
+
+def fuse_mxfp4_quantize(x, q, scales, stream=None) -> None:
+    """x [rows, cols] (rows may be strided) in 4-bit floating point with a power-of-two scale per 32 values: codes
+    q uint8 [rows, cols / 2] and scales uint8 [fuse_mxfp4_scale_bytes(rows, cols)], in tiles (see the header)."""
+    torch = _torch or _bind_torch()
+    code = _float_code(x.dtype)
+    _on_device(x.get_device(), (q, torch.uint8), (scales, torch.uint8))
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError("x must be a 2-D tensor with unit column stride")
+    rows, cols = x.shape
+    if q.shape != (rows, cols // 2) or scales.numel() < fuse_mxfp4_scale_bytes(rows, cols):
+        raise ValueError("shape mismatch")
+    _check(_load().fuse_mxfp4_quantize(x.data_ptr(), x.stride(0) if rows > 1 else cols, q.data_ptr(), scales.data_ptr(),
+                                       rows, cols, code, _stream(stream)), "fuse_mxfp4_quantize")
+
+
+def fuse_mxfp4_dequantize(q, scales, y, stream=None) -> None:
+    """y [rows, cols] = the values that q and scales (see fuse_mxfp4_quantize()) stand for."""
+    torch = _torch or _bind_torch()
+    code = _float_code(y.dtype)
+    _on_device(y.get_device(), (y, y.dtype), (q, torch.uint8), (scales, torch.uint8))
+    rows, cols = y.shape
+    if q.shape != (rows, cols // 2) or scales.numel() < fuse_mxfp4_scale_bytes(rows, cols):
+        raise ValueError("shape mismatch")
+    _check(_load().fuse_mxfp4_dequantize(q.data_ptr(), scales.data_ptr(), y.data_ptr(), rows, cols, code, _stream(stream)),
+           "fuse_mxfp4_dequantize")
+
+
+@functools.lru_cache(maxsize=256)
+def fuse_mxfp4_scale_bytes(rows: int, cols: int) -> int:
+    n = _load().fuse_mxfp4_scale_bytes(rows, cols)
+    _check(min(n, 0), "fuse_mxfp4_scale_bytes")
+    return n
+
+
+def fuse_mxfp4_gemm(xq, xs, wq, ws, y, bias=None, residual=None, gelu: bool = False, stream=None) -> None:
+    """y = GELU(X W^T + bias) + residual for X [M, K] and W [N, K] in 4-bit floating point: xq uint8 [M, K / 2] with scales
+    xs, wq uint8 [N, K / 2] with scales ws, as fuse_mxfp4_quantize() writes them.  bias [N], residual [M, N] and the GELU
+    are optional; they and y are fp16 or bf16."""
+    torch = _torch or _bind_torch()
+    dt, u8 = y.dtype, torch.uint8
+    _decode_operands(dt, (y, bias, residual), ((xq, u8), (xs, u8), (wq, u8), (ws, u8)))
+    M, half = xq.shape
+    N, half_w = wq.shape
+    if (half != half_w or y.shape != (M, N) or xs.numel() < fuse_mxfp4_scale_bytes(M, 2 * half)
+            or ws.numel() < fuse_mxfp4_scale_bytes(N, 2 * half) or (bias is not None and bias.shape != (N,))
+            or (residual is not None and residual.shape != y.shape)):
+        raise ValueError("shape mismatch")
+    _check(_load().fuse_mxfp4_gemm(xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(), _ptr(bias), _ptr(residual),
+                                   y.data_ptr(), M, N, 2 * half, 1 if gelu else 0,
+                                   FUSE_F16 if dt is torch.float16 else FUSE_BF16, _stream(stream)), "fuse_mxfp4_gemm")
+
+
+def fuse_token_logprobs(logits, tokens, logprob, entropy=None, top_logprob=None, top_index=None, scale: float = 1.0,
+                        stream=None) -> None:
+    """Of logits [rows, vocab] (rows may be strided), times scale: the log probability of each row's token (int32; negative:
+    none, 0), the entropy of its distribution, and the best alternatives top_logprob, top_index [rows, top] (top <= 32; of
+    equal logits the lower index first).  Outputs are fp32 and int32; any of them may be None, not all."""
+    torch = _torch or _bind_torch()
+    code = _float_code(logits.dtype)
+    f32, i32 = torch.float32, torch.int32
+    _on_device(logits.get_device(), (tokens, i32), (logprob, f32), (entropy, f32), (top_logprob, f32), (top_index, i32))
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be a 2-D tensor with unit column stride")
+    rows, vocab = logits.shape
+    top = 0
+    for t in (top_logprob, top_index):
+        if t is not None:
+            if t.dim() != 2 or t.shape[0] != rows or (top and t.shape[1] != top):
+                raise ValueError("shape mismatch")
+            top = t.shape[1]
+    for t in (tokens, logprob, entropy):
+        if t is not None and t.shape != (rows,):
+            raise ValueError("shape mismatch")
+    _check(_load().fuse_token_logprobs(logits.data_ptr(), logits.stride(0) if rows > 1 else vocab, _ptr(tokens), _ptr(logprob),
+                                       _ptr(entropy), _ptr(top_logprob), _ptr(top_index), rows, vocab, top, scale, code,
+                                       _stream(stream)), "fuse_token_logprobs")
+
+
+def fuse_prompt_attention_bytes(tokens: int, keys: int, q_heads: int, kv_heads: int, D: int) -> int:
+    return _load().fuse_prompt_attention_bytes(tokens, keys, q_heads, kv_heads, D)
+
+
+def fuse_prompt_attention_flops(pairs: int, q_heads: int, D: int) -> int:
+    return _load().fuse_prompt_attention_flops(pairs, q_heads, D)
+
+
+def fuse_mxfp4_gemm_bytes(M: int, N: int, K: int, bias: bool = False, residual: bool = False) -> int:
+    return _load().fuse_mxfp4_gemm_bytes(M, N, K, int(bias), int(residual))
+
+
+def fuse_token_logprobs_bytes(rows: int, vocab: int, top: int, dtype: int) -> int:
+    return _load().fuse_token_logprobs_bytes(rows, vocab, top, dtype)
 
 
 # ------------------------------------------------------------------------------- ledgers

@@ -29,6 +29,12 @@ int paged_report_count();
 int paged_report(int i, fuse_kernel_record* out);
 int w4_report_count();
 int w4_report(int i, fuse_kernel_record* out);
+int prompt_report_count();
+int prompt_report(int i, fuse_kernel_record* out);
+int mxfp4_report_count();
+int mxfp4_report(int i, fuse_kernel_record* out);
+int logprob_report_count();
+int logprob_report(int i, fuse_kernel_record* out);
 // FUSE_ETIMEOUT if a bounded device wait expired, FUSE_EINDEX if a kernel met an index out of range,
 // since the last call, else FUSE_OK; clears what it has read.  `stream` has been synchronized.
 int status_take(cudaStream_t stream);
@@ -225,6 +231,9 @@ const ReportTable kTables[] = {
     {fc::rope_report_count, fc::rope_report},
     {fc::paged_report_count, fc::paged_report},
     {fc::w4_report_count, fc::w4_report},
+    {fc::prompt_report_count, fc::prompt_report},
+    {fc::mxfp4_report_count, fc::mxfp4_report},
+    {fc::logprob_report_count, fc::logprob_report},
 };
 }  // namespace
 

@@ -107,6 +107,11 @@ int blocks_per_sm(K kernel, int block, size_t dyn_smem = 0) {
 int describe_kernel(const void* kernel, const char* name, int block, int dyn_smem,
                     fuse_kernel_record* out, int tmem_cols = 0);
 
+// A case of a unit's report: entry N is the kernel (named as it is written), with its launch's threads, dynamic shared
+// memory and tensor-memory columns.
+#define FC_REPORT(N, BLOCK, SMEM, COLS, ...) \
+    case N: return describe_kernel((const void*)__VA_ARGS__, #__VA_ARGS__, BLOCK, SMEM, out, COLS)
+
 inline bool is_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // True if [a, a + a_bytes) and [b, b + b_bytes) share a byte.

@@ -5,6 +5,7 @@
 #include <cudaTypedefs.h>
 #include <stdint.h>
 
+#include "fc_internal.cuh"
 #include "fc_ptx.cuh"
 
 namespace fc {
@@ -66,6 +67,16 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// Tensor memory for the CTA (one warp, `warp` == 1, allocates), its barriers' initialisation made known, and only then the
+// next kernel let start.  `held` is `holder`'s generic address; all threads call it, and get the TMEM address.
+__device__ __forceinline__ uint32_t tmem_begin(uint32_t holder, const void* held, uint32_t ncols, int warp) {
+    if (warp == 1) tmem_alloc(holder, ncols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_trigger();
+    return __shfl_sync(0xffffffffu, *static_cast<const volatile uint32_t*>(held), 0);
+}
 
 __device__ __forceinline__ void tc_mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                        uint32_t accumulate) {
@@ -114,6 +125,14 @@ __device__ __forceinline__ void tma_load_2d_if(uint32_t one, uint32_t dst, const
         "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
         "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "r"(one)
+        : "memory");
+}
+// (the tensor map's rank is the load's: a 2-D load of a 3-D map faults)
+__device__ __forceinline__ void tma_load_3d_if(uint32_t one, uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+        "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "r"(one)
         : "memory");
 }
 // the same for data that is read once: first to leave L2 (`policy` from policy_evict_first())

@@ -1,0 +1,486 @@
+// mxfp4.cu -- microscaled 4-bit floating point: quantisation, and the product of two quantised operands.
+//
+// 32 consecutive values of a row share a scale 2^e, 2^(e + 2) <= max |v| < 2^(e + 3) (so the largest lies between 4
+// and 8, and what exceeds 6 becomes 6); each value is v / 2^e rounded to 0, 1/2, 1, 3/2, 2, 3, 4 or 6, ties to the even
+// code.  Dividing by a power of two is exact, so the codes are what the definition says, bit for bit.  Scales are
+// held as bytes e + 127 (255: not a number) in tiles of 128 rows by 4 scales, 512 bytes each, in the order in which
+// the tensor core takes them: byte (r % 32) 16 + (r / 32) 4 + s of a tile is row r's scale s.
+//
+//  * mxfp4_quantize_kernel, mxfp4_dequantize_kernel: bound by HBM.  A CTA takes a tile's 128 rows by 128 values.
+//  * mxfp4_gemm_kernel: Y = GELU(X W^T + bias) + R with X [M, K] and W [N, K] both quantised.  The weights are the
+//    tensor core's 128 rows and the tokens its columns, so a warp's stores of a token are consecutive outputs and
+//    few tokens cost few columns.  kind::mxf4 multiplies 64 values of a row at once, at four times the rate of 16-bit
+//    operands; the scales go from shared memory to TMEM next to the accumulators.  K may be split over a
+//    cluster of CTAs, whose sums meet in shared memory.
+#include <cudaTypedefs.h>
+#include <math.h>
+
+#include <type_traits>
+
+#include "fc_internal.cuh"
+#include "fc_mma.cuh"
+#include "fc_ptx.cuh"
+#include "fc_tc.cuh"
+#include "gemm_epi.cuh"
+
+namespace fc {
+namespace {
+
+constexpr int kQThreads = 256;
+
+// ================================================================== quantisation
+// Eight values to codes, the first in the lowest four bits.
+__device__ __forceinline__ uint32_t to_e2m1(const float* v) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return r;
+}
+// The value of the code in the lowest four bits.
+__device__ __forceinline__ float from_e2m1(uint32_t c) {
+    // exponent field x, mantissa bit m: (2 + m) 2^(x - 2), for x = 0: m / 2
+    const uint32_t x = (c >> 1) & 3u, m = c & 1u;
+    const float v = x == 0u ? 0.5f * static_cast<float>(m) : __uint_as_float(((126u + x) << 23) | (m << 22));
+    return (c & 8u) ? -v : v;
+}
+
+struct QuantArgs {
+    const void* x;
+    int64_t ld;
+    uint8_t *q, *s;
+    int64_t rows, cols;
+};
+
+// Eight threads of 16 values (16-bit x) or sixteen of 8 (fp32) take a row's 128 values.
+template <typename T>
+__global__ void __launch_bounds__(kQThreads) mxfp4_quantize_kernel(const __grid_constant__ QuantArgs a) {
+    constexpr int N = Vec32<T>::N, PER_ROW = 128 / N, ROWS = kQThreads / PER_ROW, GROUP = 32 / N, ITER = 128 / ROWS;
+    __shared__ uint8_t tile[512];
+    pdl_begin();
+    const int tid = threadIdx.x, ch = tid % PER_ROW;
+    const int64_t row0 = static_cast<int64_t>(blockIdx.y) * 128, col = static_cast<int64_t>(blockIdx.x) * 128 + ch * N;
+#pragma unroll
+    for (int i = 0; i < ITER; ++i) {
+        const int r = tid / PER_ROW + i * ROWS;
+        const bool in = row0 + r < a.rows && col < a.cols;
+        float v[N] = {};
+        if (in) Vec32<T>::load(static_cast<const T*>(a.x) + (row0 + r) * a.ld + col, v);
+        uint32_t top = 0;                    // the largest magnitude's bits (infinity and NaN above all)
+#pragma unroll
+        for (int e = 0; e < N; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
+#pragma unroll
+        for (int o = 1; o < GROUP; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const uint32_t field = top >> 23;    // max |v| >= 2^(field - 127)
+        const uint32_t scale = field == 255u ? 255u : field > 2u ? field - 2u : 0u;
+        const float inv = __uint_as_float((254u - min(scale, 253u)) << 23);
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] *= inv;
+        if (in) {
+            uint8_t* q = a.q + (row0 + r) * (a.cols / 2) + col / 2;
+            if constexpr (N == 16) *reinterpret_cast<uint2*>(q) = make_uint2(to_e2m1(v), to_e2m1(v + 8));
+            else *reinterpret_cast<uint32_t*>(q) = to_e2m1(v);
+        }
+        // (scales of rows and values past the matrix are 0: with codes of 0 they add nothing to a product)
+        if (ch % GROUP == 0) tile[(r % 32) * 16 + (r / 32) * 4 + ch / GROUP] = static_cast<uint8_t>(in ? scale : 0u);
+    }
+    __syncthreads();
+    if (tid < 32)
+        reinterpret_cast<uint4*>(a.s + (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * 512)[tid] = reinterpret_cast<uint4*>(tile)[tid];
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kQThreads) mxfp4_dequantize_kernel(const __grid_constant__ QuantArgs a, T* y) {
+    constexpr int N = Vec32<T>::N, PER_ROW = 128 / N, ROWS = kQThreads / PER_ROW, GROUP = 32 / N, ITER = 128 / ROWS;
+    __shared__ uint8_t tile[512];
+    pdl_begin();
+    const int tid = threadIdx.x, ch = tid % PER_ROW;
+    if (tid < 32)
+        reinterpret_cast<uint4*>(tile)[tid] = __ldcg(reinterpret_cast<const uint4*>(a.s + (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * 512) + tid);
+    const int64_t row0 = static_cast<int64_t>(blockIdx.y) * 128, col = static_cast<int64_t>(blockIdx.x) * 128 + ch * N;
+    uint2 w[ITER];
+#pragma unroll
+    for (int i = 0; i < ITER; ++i) {
+        const int64_t row = row0 + tid / PER_ROW + i * ROWS;
+        w[i] = make_uint2(0u, 0u);
+        if (row < a.rows && col < a.cols) {
+            const uint8_t* q = a.q + row * (a.cols / 2) + col / 2;
+            if constexpr (N == 16) w[i] = __ldcg(reinterpret_cast<const uint2*>(q));
+            else w[i].x = __ldcg(reinterpret_cast<const uint32_t*>(q));
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < ITER; ++i) {
+        const int r = tid / PER_ROW + i * ROWS;
+        if (row0 + r >= a.rows || col >= a.cols) continue;
+        const uint32_t s = tile[(r % 32) * 16 + (r / 32) * 4 + ch / GROUP];
+        const float scale = __uint_as_float(s == 255u ? 0x7fc00000u : s == 0u ? 0x00400000u : s << 23);
+        float v[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] = from_e2m1(((e < 8 ? w[i].x : w[i].y) >> (4 * (e % 8))) & 15u) * scale;
+        Vec32<T>::store(y + (row0 + r) * a.cols + col, v);
+    }
+}
+
+// ================================================================== product
+// The accumulator's rows are weights (N), its columns tokens (M).
+constexpr int kStageK = 256;                        // values of a row per stage: 128 bytes
+constexpr uint32_t kTileBytes = 128 * 128;          // 128 rows of a stage
+constexpr int kGemmThreads = 32 * 6;                // warp 0: loads, 1: MMA issue, 2-5: epilogue
+
+template <int NT>
+struct GemmLayout {
+    static constexpr uint32_t B_BYTES = NT * 128;
+    static constexpr uint32_t STAGE = kTileBytes + B_BYTES + 2048;      // weights, tokens, the two operands' scales
+    static constexpr int STAGES = NT <= 32 ? 5 : NT == 64 ? 4 : 6;      // up to 64 tokens two CTAs per SM
+    static constexpr uint32_t OFF_BAR = STAGES * STAGE;
+    static constexpr uint32_t OFF_HOLD = OFF_BAR + (2 * STAGES + 2) * 8;
+    static constexpr uint32_t SMEM = OFF_HOLD + 16 + 1024;
+    static constexpr uint32_t OFF_B = kTileBytes, OFF_SA = OFF_B + B_BYTES, OFF_SB = OFF_SA + 1024;
+    static constexpr uint32_t TMEM_COLS = NT <= 32 ? 64 : NT == 64 ? 128 : 256;
+    static constexpr uint32_t SFA_COL = NT, SFB_COL = NT + 8;           // two tiles of scales each
+    static_assert(B_BYTES % 1024 == 0, "swizzle atoms");
+    static_assert(SMEM <= 232448, "shared-memory budget");
+    static_assert(SFB_COL + 8 <= TMEM_COLS, "TMEM");
+    static_assert(128 * NT * 4 <= OFF_BAR, "partial sums fit over the stages");
+};
+
+struct GemmArgs {
+    const uint8_t *xs, *ws;       // scale tiles
+    const void *bias, *R;
+    void* y;
+    int M, N, K;
+    int xtk;                      // scale tiles along K
+    int stages;                   // of the whole K
+    int split;                    // CTAs that share a tile
+    int gelu;
+    int* flag;
+};
+
+// D += (A sa) (B sb) with 4-bit operands of 64 values, scales per 32; `id` names the scale bytes in use.
+__device__ __forceinline__ void tc_mma_mxf4_if(uint32_t one, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                               uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate), "r"(one)
+        : "memory");
+}
+// A tile of scales (512 bytes) from shared memory to four TMEM columns of every lane quadrant.
+__device__ __forceinline__ void tc_cp_scales_if(uint32_t one, uint32_t tmem, uint64_t desc) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+        "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(tmem), "l"(desc), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {   // no swizzle, 8 rows of 16 bytes after one another
+    return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
+}
+// Instruction descriptor, kind::mxf4: e2m1 operands, scales 2^e, fp32 sums; scale bytes `sf` and sf + 1.
+__host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N, int sf) {
+    return (static_cast<uint32_t>(sf) << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | (1u << 23) |
+           (static_cast<uint32_t>(M >> 4) << 24) | (static_cast<uint32_t>(sf) << 29);
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ void finish_store(const GemmArgs& a, int token, int n, float v, float bias) {
+    v += bias;
+    if (a.gelu) v = gelu_erf(v);
+    const int64_t at = static_cast<int64_t>(token) * a.N + n;
+    if (a.R) v += to_f32(static_cast<const T*>(a.R)[at]);
+    static_cast<T*>(a.y)[at] = from_f32<T>(v);
+}
+
+template <typename T, int NT>
+__global__ void __launch_bounds__(kGemmThreads, NT <= 64 ? 2 : 1) mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap mW,
+                                                                                   const __grid_constant__ CUtensorMap mX,
+                                                                                   const __grid_constant__ GemmArgs a) {
+    using L = GemmLayout<NT>;
+    constexpr int ST = L::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    uint8_t* gbase = smem_raw + (base - smem_addr(smem_raw));
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
+    auto full = [&](int i) { return base + L::OFF_BAR + 8u * i; };
+    auto empty = [&](int i) { return base + L::OFF_BAR + 8u * (ST + i); };
+    const uint32_t done = base + L::OFF_BAR + 8u * (2 * ST), drain = done + 8;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(full(i), 1);
+            mbar_init(empty(i), 1);
+        }
+        mbar_init(done, 1);
+        mbar_init(drain, 1);
+        fence_mbar_init();
+    }
+    const uint32_t tmem = tmem_begin(base + L::OFF_HOLD, gbase + L::OFF_HOLD, L::TMEM_COLS, warp);
+    pdl_wait();
+
+    const int split = a.split, part = static_cast<int>(blockIdx.x) % split, n_tile = static_cast<int>(blockIdx.x) / split;
+    const int n0 = n_tile * 128, m0 = static_cast<int>(blockIdx.y) * NT;
+    const int s0 = static_cast<int>(static_cast<int64_t>(a.stages) * part / split), s1 = static_cast<int>(static_cast<int64_t>(a.stages) * (part + 1) / split);
+    bool ok = true;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity & 1u, a.flag));
+        return ok;
+    };
+    if (warp == 0) {
+        if (lane == 0) {
+            prefetch_map(&mW);
+            prefetch_map(&mX);
+        }
+        const uint32_t one = elect_one();
+        const uint8_t* sw = a.ws + static_cast<int64_t>(n_tile) * a.xtk * 512;
+        const uint8_t* sx = a.xs + static_cast<int64_t>(m0 / 128) * a.xtk * 512;
+        int i = 0;
+        for (int s = s0; s < s1; ++s, ++i) {
+            const int slot = i % ST;
+            if (i >= ST && !wait(empty(slot), i / ST - 1)) break;
+            const uint32_t at = base + slot * L::STAGE, bytes = 512u * static_cast<uint32_t>(min(2, a.xtk - 2 * s));
+            if (lane == 0) mbar_arrive_expect_tx(full(slot), kTileBytes + L::B_BYTES + 2 * bytes);
+            __syncwarp();
+            tma_load_3d_if(one, at, &mW, s * 128, n0, 0, full(slot));
+            tma_load_3d_if(one, at + L::OFF_B, &mX, s * 128, m0, 0, full(slot));
+            if (one) {
+                bulk_load(at + L::OFF_SA, sw + s * 1024, bytes, full(slot));
+                bulk_load(at + L::OFF_SB, sx + s * 1024, bytes, full(slot));
+            }
+            __syncwarp();
+        }
+        if (!ok)   // copies in flight land before the shared memory goes away
+            for (int j = max(0, i - ST); j < i; ++j) (void)mbar_wait_drain(full(j % ST), (j / ST) & 1);
+    } else if (warp == 1) {
+        const uint32_t one = elect_one();
+        bool issued = false;
+        int i = 0;
+        for (int s = s0; s < s1; ++s, ++i) {
+            const int slot = i % ST;
+            if (!wait(full(slot), i / ST)) break;
+            tc_fence_after();
+            const uint32_t at = base + slot * L::STAGE;
+            const int left = a.K - s * kStageK, steps = min(4, (left + 63) / 64);
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                if (2 * t < steps) {
+                    tc_cp_scales_if(one, tmem + L::SFA_COL + 4 * t, scale_desc(at + L::OFF_SA + 512 * t));
+                    tc_cp_scales_if(one, tmem + L::SFB_COL + 4 * t, scale_desc(at + L::OFF_SB + 512 * t));
+                }
+            const uint64_t da = smem_desc_sw128(at, 16, 1024), db = smem_desc_sw128(at + L::OFF_B, 16, 1024);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (k < steps)
+                    tc_mma_mxf4_if(one, tmem, da + 2 * k, db + 2 * k, k % 2 ? idesc_mxf4(128, NT, 2) : idesc_mxf4(128, NT, 0),
+                                   tmem + L::SFA_COL + 4 * (k / 2), tmem + L::SFB_COL + 4 * (k / 2), i > 0 || k > 0 ? 1u : 0u);
+            tc_commit_if(one, empty(slot));
+            issued = true;
+        }
+        if (ok && issued) tc_commit_if(one, done);
+        if (!ok && issued) {
+            tc_commit_if(one, drain);
+            (void)mbar_wait_drain(drain, 0);
+        }
+        __syncwarp();
+    } else {
+        const int quad = warp % 4, row = 32 * quad + lane, n = n0 + row;
+        const bool in = n < a.N;
+        const float bias = in && a.bias ? to_f32(static_cast<const T*>(a.bias)[n]) : 0.0f;
+        const int tokens = min(NT, a.M - m0);
+        float* part_sums = reinterpret_cast<float*>(gbase);          // [token][128], over the stages
+        if (s1 == s0 || wait(done, 0)) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < tokens; c += 16) {
+                float v[16] = {};
+                if (s1 > s0) {
+                    tmem_ld16(tmem + (static_cast<uint32_t>(32 * quad) << 16) + c, v);
+                    tmem_ld_wait();
+                }
+                if (split > 1) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) part_sums[(c + e) * 128 + row] = v[e];
+                } else if (in) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (c + e < tokens) finish_store<T>(a, m0 + c + e, n, v[e], bias);
+                }
+            }
+            tc_fence_before();
+        }
+    }
+    if (split > 1) {
+        // each CTA finishes its share of the tile's tokens, summing the parts in order
+        cluster_sync();
+        if (warp >= 2 && ok) {
+            const int row = 32 * (warp % 4) + lane, n = n0 + row;
+            const bool in = n < a.N;
+            const float bias = in && a.bias ? to_f32(static_cast<const T*>(a.bias)[n]) : 0.0f;
+            const int tokens = min(NT, a.M - m0);
+            for (int c = part; c < tokens; c += split) {
+                float v = 0.0f;
+                for (int p = 0; p < split; ++p) {
+                    float x;
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(mapa_shared(base + (c * 128 + row) * 4, p)) : "memory");
+                    v += x;
+                }
+                if (in) finish_store<T>(a, m0 + c, n, v, bias);
+            }
+        }
+        cluster_sync();
+    } else {
+        __syncthreads();
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, L::TMEM_COLS);
+    }
+}
+
+bool map_u8(CUtensorMap* map, const void* q, int64_t rows, int64_t K, int box_rows) {
+    const int64_t dims[3] = {K / 2, rows, 1}, strides[2] = {K / 2, rows * (K / 2)};
+    const int box[3] = {128, box_rows, 1};
+    return make_map_3d(map, q, kMapU8, dims, strides, box, 128);
+}
+
+template <typename T, int NT>
+int launch_gemm(GemmArgs a, const void* xq, const void* wq, cudaStream_t st) {
+    CUtensorMap mW, mX;
+    if (!map_u8(&mW, wq, a.N, a.K, 128) || !map_u8(&mX, xq, a.M, a.K, NT)) return FUSE_ECUDA;
+    const int rc = opt_in_smem((const void*)mxfp4_gemm_kernel<T, NT>, GemmLayout<NT>::SMEM);
+    if (rc != FUSE_OK) return rc;
+    const int64_t tn = ceil_div(a.N, 128), tm = ceil_div(a.M, NT);
+    a.split = 1;
+    while (a.split < 8 && tn * tm * a.split * 2 <= sm_count() && a.stages >= 2 * a.split * 2) a.split *= 2;
+    return launch_pdl(mxfp4_gemm_kernel<T, NT>, dim3(static_cast<unsigned>(tn * a.split), static_cast<unsigned>(tm)), dim3(kGemmThreads),
+                      GemmLayout<NT>::SMEM, st, a.split, mW, mX, a);
+}
+
+template <typename T>
+int run_gemm(const GemmArgs& a, const void* xq, const void* wq, cudaStream_t st) {
+    if (a.M <= 32) return launch_gemm<T, 32>(a, xq, wq, st);
+    if (a.M <= 64) return launch_gemm<T, 64>(a, xq, wq, st);
+    return launch_gemm<T, 128>(a, xq, wq, st);
+}
+
+int64_t scale_bytes(int64_t rows, int64_t cols) { return ceil_div(rows, 128) * ceil_div(cols, 128) * 512; }
+
+// The rules on a quantised matrix that both directions share.
+int check_matrix(int64_t rows, int64_t cols) {
+    if (rows < 0 || cols < 1) return FUSE_EINVAL;
+    if (cols % 32 != 0 || cols >= int64_t(1) << 31 || rows >= int64_t(1) << 22) return FUSE_EUNSUPPORTED;
+    return FUSE_OK;
+}
+
+}  // namespace
+
+int mxfp4_report_count() { return 12; }
+int mxfp4_report(int i, fuse_kernel_record* out) {
+    switch (i) {
+        FC_REPORT(0, kQThreads, 0, 0, mxfp4_quantize_kernel<float>);
+        FC_REPORT(1, kQThreads, 0, 0, mxfp4_quantize_kernel<__half>);
+        FC_REPORT(2, kQThreads, 0, 0, mxfp4_quantize_kernel<__nv_bfloat16>);
+        FC_REPORT(3, kQThreads, 0, 0, mxfp4_dequantize_kernel<float>);
+        FC_REPORT(4, kQThreads, 0, 0, mxfp4_dequantize_kernel<__half>);
+        FC_REPORT(5, kQThreads, 0, 0, mxfp4_dequantize_kernel<__nv_bfloat16>);
+        FC_REPORT(6, kGemmThreads, GemmLayout<32>::SMEM, GemmLayout<32>::TMEM_COLS, mxfp4_gemm_kernel<__half, 32>);
+        FC_REPORT(7, kGemmThreads, GemmLayout<64>::SMEM, GemmLayout<64>::TMEM_COLS, mxfp4_gemm_kernel<__half, 64>);
+        FC_REPORT(8, kGemmThreads, GemmLayout<128>::SMEM, GemmLayout<128>::TMEM_COLS, mxfp4_gemm_kernel<__half, 128>);
+        FC_REPORT(9, kGemmThreads, GemmLayout<32>::SMEM, GemmLayout<32>::TMEM_COLS, mxfp4_gemm_kernel<__nv_bfloat16, 32>);
+        FC_REPORT(10, kGemmThreads, GemmLayout<64>::SMEM, GemmLayout<64>::TMEM_COLS, mxfp4_gemm_kernel<__nv_bfloat16, 64>);
+        FC_REPORT(11, kGemmThreads, GemmLayout<128>::SMEM, GemmLayout<128>::TMEM_COLS, mxfp4_gemm_kernel<__nv_bfloat16, 128>);
+        default: return FUSE_EINVAL;
+    }
+}
+
+}  // namespace fc
+
+extern "C" int64_t fuse_mxfp4_scale_bytes(int64_t rows, int64_t cols) {
+    const int rc = fc::check_matrix(rows, cols);
+    return rc != FUSE_OK ? rc : fc::scale_bytes(rows, cols);
+}
+
+extern "C" int fuse_mxfp4_quantize(const void* x, int64_t ld, void* q, void* scales, int64_t rows, int64_t cols, int dtype, fuse_stream_t stream) {
+    using namespace fc;
+    int rc = check_matrix(rows, cols);
+    if (rc != FUSE_OK) return rc;
+    if (ld < cols || (dtype != FUSE_F32 && dtype != FUSE_F16 && dtype != FUSE_BF16)) return FUSE_EINVAL;
+    if (ld >= int64_t(1) << 40) return FUSE_EUNSUPPORTED;
+    if (rows == 0) return FUSE_OK;
+    if (!x || !q || !scales) return FUSE_EINVAL;
+    const int64_t size = dtype == FUSE_F32 ? 4 : 2;
+    if (!is_aligned(x, 32) || ld * size % 32 != 0 || !is_aligned(q, 16) || !is_aligned(scales, 16)) return FUSE_EALIGN;
+    const int64_t xb = ((rows - 1) * ld + cols) * size, qb = rows * cols / 2, sb = scale_bytes(rows, cols);
+    if (ranges_overlap(x, xb, q, qb) || ranges_overlap(x, xb, scales, sb) || ranges_overlap(q, qb, scales, sb)) return FUSE_EINVAL;
+    const QuantArgs a{x, ld, static_cast<uint8_t*>(q), static_cast<uint8_t*>(scales), rows, cols};
+    const dim3 grid(static_cast<unsigned>(ceil_div(cols, 128)), static_cast<unsigned>(ceil_div(rows, 128)));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (dtype == FUSE_F32) return launch_pdl(mxfp4_quantize_kernel<float>, grid, dim3(kQThreads), 0, st, 1, a);
+    if (dtype == FUSE_F16) return launch_pdl(mxfp4_quantize_kernel<__half>, grid, dim3(kQThreads), 0, st, 1, a);
+    return launch_pdl(mxfp4_quantize_kernel<__nv_bfloat16>, grid, dim3(kQThreads), 0, st, 1, a);
+}
+
+extern "C" int fuse_mxfp4_dequantize(const void* q, const void* scales, void* y, int64_t rows, int64_t cols, int dtype, fuse_stream_t stream) {
+    using namespace fc;
+    int rc = check_matrix(rows, cols);
+    if (rc != FUSE_OK) return rc;
+    if (dtype != FUSE_F32 && dtype != FUSE_F16 && dtype != FUSE_BF16) return FUSE_EINVAL;
+    if (rows == 0) return FUSE_OK;
+    if (!y || !q || !scales) return FUSE_EINVAL;
+    if (!is_aligned(y, 32) || !is_aligned(q, 16) || !is_aligned(scales, 16)) return FUSE_EALIGN;
+    const int64_t yb = rows * cols * (dtype == FUSE_F32 ? 4 : 2), qb = rows * cols / 2, sb = scale_bytes(rows, cols);
+    if (ranges_overlap(y, yb, q, qb) || ranges_overlap(y, yb, scales, sb)) return FUSE_EINVAL;
+    const QuantArgs a{nullptr, 0, const_cast<uint8_t*>(static_cast<const uint8_t*>(q)), const_cast<uint8_t*>(static_cast<const uint8_t*>(scales)), rows, cols};
+    const dim3 grid(static_cast<unsigned>(ceil_div(cols, 128)), static_cast<unsigned>(ceil_div(rows, 128)));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (dtype == FUSE_F32) return launch_pdl(mxfp4_dequantize_kernel<float>, grid, dim3(kQThreads), 0, st, 1, a, static_cast<float*>(y));
+    if (dtype == FUSE_F16) return launch_pdl(mxfp4_dequantize_kernel<__half>, grid, dim3(kQThreads), 0, st, 1, a, static_cast<__half*>(y));
+    return launch_pdl(mxfp4_dequantize_kernel<__nv_bfloat16>, grid, dim3(kQThreads), 0, st, 1, a, static_cast<__nv_bfloat16*>(y));
+}
+
+extern "C" int fuse_mxfp4_gemm(const void* xq, const void* xs, const void* wq, const void* ws, const void* bias, const void* R, void* y, int64_t M,
+                               int64_t N, int64_t K, int gelu, int dtype, fuse_stream_t stream) {
+    using namespace fc;
+    int rc = check_matrix(M, K);
+    if (rc == FUSE_OK) rc = check_matrix(N, K);
+    if (rc != FUSE_OK) return rc;
+    if (N < 1 || (gelu != 0 && gelu != 1) || (dtype != FUSE_F16 && dtype != FUSE_BF16)) return FUSE_EINVAL;
+    if (M == 0) return FUSE_OK;
+    if (!xq || !xs || !wq || !ws || !y) return FUSE_EINVAL;
+    if (!is_aligned(xq, 16) || !is_aligned(xs, 16) || !is_aligned(wq, 16) || !is_aligned(ws, 16) || !is_aligned(y, 2) || !is_aligned(bias, 2) ||
+        !is_aligned(R, 2))
+        return FUSE_EALIGN;
+    const int64_t yb = M * N * 2;
+    struct { const void* p; int64_t n; } in[6] = {{xq, M * K / 2}, {xs, scale_bytes(M, K)}, {wq, N * K / 2}, {ws, scale_bytes(N, K)}, {bias, N * 2}, {R, yb}};
+    for (const auto& x : in)
+        if (x.p && ranges_overlap(y, yb, x.p, x.n)) return FUSE_EINVAL;
+    GemmArgs a{};
+    a.xs = static_cast<const uint8_t*>(xs);
+    a.ws = static_cast<const uint8_t*>(ws);
+    a.bias = bias;
+    a.R = R;
+    a.y = y;
+    a.M = static_cast<int>(M);
+    a.N = static_cast<int>(N);
+    a.K = static_cast<int>(K);
+    a.xtk = static_cast<int>(ceil_div(K, 128));
+    a.stages = static_cast<int>(ceil_div(K, kStageK));
+    a.gelu = gelu;
+    a.flag = watchdog_flag();
+    if (!a.flag) return FUSE_ECUDA;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return dtype == FUSE_F16 ? run_gemm<__half>(a, xq, wq, st) : run_gemm<__nv_bfloat16>(a, xq, wq, st);
+}
+
+extern "C" int64_t fuse_mxfp4_gemm_bytes(int64_t M, int64_t N, int64_t K, int bias, int residual) {
+    if (M < 0 || N < 1 || K < 32 || K % 32 != 0) return FUSE_EINVAL;
+    return (M + N) * (K / 2 + K / 32) + 2 * M * N * (residual ? 2 : 1) + (bias ? 2 * N : 0);
+}

@@ -427,6 +427,110 @@ int fuse_w4_gemv(const void* x, const void* wq, const void* scales, const void* 
                  const void* R, void* y, int64_t M, int64_t N, int64_t K, int64_t group, int gelu,
                  int dtype, fuse_stream_t stream);
 
+/* ===================================================================== attention of prompts over a paged cache
+ * The form of fuse_paged_attention() for whole prompts: causal attention of the new tokens of a packed
+ * batch, whose keys and values are in the cache (fuse_rope_append() has put them there) behind those of
+ * earlier turns.  Sequence b's new tokens are rows cu_queries[b] .. cu_queries[b + 1] - 1 of q and o, n of
+ * them, and the last n of its seq_lens[b] keys are theirs:
+ *     o_ih = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m),   s_j = scale q_ih . k_j,   m = max_j s_j,
+ *     over the keys j <= seq_lens[b] - n + i,
+ * with query head h reading key/value head h / (q_heads / kv_heads).  A row that sees no key (its sequence
+ * has fewer keys than new tokens) gets zeros.  A sequence may have no new tokens.  Rows behind the last
+ * sequence are left as they are.
+ *
+ *   q        device, rows of q_heads D elements of `dtype`, q_ld elements apart (q_ld = q_heads D: dense)
+ *   o        device [tokens, q_heads, D] of `dtype`; o must not overlap an input
+ *   tokens   rows of q and o
+ *   k_cache, v_cache  device [num_pages, kv_heads, page_size, D] of `dtype`; what lies in a page past the
+ *            keys in use is not used, whatever its bits.  A value that is not finite, at a key that is in
+ *            use, may make rows NaN that do not see it yet (those whose last key is less than 128 before it).
+ *   block_table  device int32 [batch, table_ld]: entry i is the page of keys i page_size .. ; only the
+ *            entries that seq_lens covers are read.  May be NULL when table_ld == 0.
+ *   cu_queries  device int32 [batch + 1], ascending, within 0 .. tokens
+ *   seq_lens device int32 [batch]: the keys of each sequence, 0 .. table_ld page_size
+ *   Rules: dtype FUSE_F16 or FUSE_BF16; D in {64, 128, 256}; q_heads a multiple of kv_heads, at most 128 of
+ *          them for each; page_size a power of two, 16..256; batch <= 4096; tokens < 2^24; num_pages kv_heads
+ *          page_size and table_ld page_size below 2^31 - 4096, (tokens + batch) kv_heads (table_ld page_size +
+ *          192) below 2^52 (else FUSE_EUNSUPPORTED, and nothing is enqueued); scale > 0; tensors 16-byte
+ *          aligned and q_ld a multiple of 8, tables and lengths 4-byte (else FUSE_EALIGN).
+ *   Out of range in device memory (fuse_check() then returns FUSE_EINDEX): a page index outside
+ *   [0, num_pages) counts as a page of zeros; a length is taken into 0 .. table_ld page_size, a row number
+ *   into 0 .. tokens, and a sequence whose rows end before they begin has none.  Sequences whose rows overlap
+ *   leave either one's output there.
+ *   workspace  device memory of at least fuse_prompt_attention_workspace_bytes() bytes, 256-byte aligned, of
+ *          any content, not shared with a call that may run at the same time, in a replayed graph or otherwise; it
+ *          must overlap no operand.
+ * Scores, maxima, sums and the accumulated output are fp32; the weights e^(s - m) are rounded to `dtype` for
+ * the product with V and the output once at the end.  The work is split over the SMs and the parts joined in a
+ * fixed order: equal calls give equal bits.
+ */
+int fuse_prompt_attention(const void* q, int64_t q_ld, const void* k_cache, const void* v_cache,
+                          const int32_t* block_table, int64_t table_ld, const int32_t* cu_queries,
+                          const int32_t* seq_lens, void* o, int64_t tokens, int64_t batch, int64_t q_heads,
+                          int64_t kv_heads, int64_t D, int64_t num_pages, int64_t page_size, float scale,
+                          int dtype, void* workspace, size_t ws_bytes, fuse_stream_t stream);
+size_t fuse_prompt_attention_workspace_bytes(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t D);
+
+/* ===================================================================== microscaled 4-bit floating point
+ * Values in 4 bits (sign, two exponent bits, one mantissa bit: 0, 1/2, 1, 3/2, 2, 3, 4, 6) with a scale 2^e
+ * for every 32 consecutive values of a row, the "MXFP4" of the OCP microscaling formats.
+ *
+ * fuse_mxfp4_quantize(): for every 32 values e is the whole number with 2^(e + 2) <= max |x| < 2^(e + 3), at
+ * least -127, and each value is x / 2^e rounded to the nearest of those above, ties to the one whose mantissa
+ * bit is 0, beyond 6 to 6.  32 zeros have e = -127.  Where one of the 32 is infinite or NaN the scale is NaN,
+ * and so are all of them when read.
+ *   x        device, `rows` rows of `cols` elements of `dtype` (FUSE_F32, FUSE_F16, FUSE_BF16), ld apart
+ *   q        device uint8 [rows, cols / 2]: byte j of a row has value 2j in its low and 2j + 1 in its high bits
+ *   scales   device uint8 [fuse_mxfp4_scale_bytes(rows, cols)]: bytes e + 127 (255: NaN) in tiles of 128 rows by
+ *            4 scales.  Row r's scale s (of values 32 s ..) is byte
+ *                ((r / 128) ceil(cols / 128) + s / 4) 512 + (r % 32) 16 + (r % 128 / 32) 4 + s % 4;
+ *            bytes that no row or value of the matrix has are written as 0.
+ *   Rules: cols a multiple of 32, below 2^31; rows < 2^22 (else FUSE_EUNSUPPORTED); ld >= cols; x and its rows
+ *          32-byte aligned, q and scales 16-byte (else FUSE_EALIGN); no two may overlap.
+ * fuse_mxfp4_dequantize(): y [rows, cols] of `dtype` = the values, rounded to `dtype` where it does not hold
+ * them (y 32-byte aligned).
+ */
+int fuse_mxfp4_quantize(const void* x, int64_t ld, void* q, void* scales, int64_t rows, int64_t cols,
+                        int dtype, fuse_stream_t stream);
+int fuse_mxfp4_dequantize(const void* q, const void* scales, void* y, int64_t rows, int64_t cols, int dtype,
+                          fuse_stream_t stream);
+int64_t fuse_mxfp4_scale_bytes(int64_t rows, int64_t cols);
+
+/* The projection with both operands in that form, from one token to whole prompts, and the epilogue of
+ * fuse_gemm_epilogue() (each stage optional):
+ *     Y = GELU(X W^T + bias) + R.
+ *   xq, xs   X [M, K] as fuse_mxfp4_quantize() writes it (M == 0 enqueues nothing);  wq, ws  W [N, K] likewise (of the
+ *            scales' bytes that no row or value has, those of existing rows must not be 255)
+ *   bias [N], R [M, N] of `dtype`, or NULL;  gelu 0 or 1;  y device [M, N] of `dtype`
+ *   Rules: dtype FUSE_F16 or FUSE_BF16; K a multiple of 32, below 2^31; M, N < 2^22 (else FUSE_EUNSUPPORTED);
+ *          xq, xs, wq and ws 16-byte aligned, the others to their element (else FUSE_EALIGN); y overlaps no input.
+ * The products are exact, their sums fp32, and Y is rounded once.  The order of the sums is fixed.
+ */
+int fuse_mxfp4_gemm(const void* xq, const void* xs, const void* wq, const void* ws, const void* bias,
+                    const void* R, void* y, int64_t M, int64_t N, int64_t K, int gelu, int dtype,
+                    fuse_stream_t stream);
+
+/* ===================================================================== log probabilities of tokens
+ * What a model's logits say of a given token, from one read of them.  Per row, with z_j = scale x_j,
+ *     lse = log sum_j e^(z_j),   logprob = z_token - lse,   entropy = lse - sum_j p_j z_j,  p_j = e^(z_j - lse),
+ * and the `top` tokens with the largest logits (of equal logits the one with the lower index first) with their
+ * log probabilities.
+ *   logits   device, `rows` rows of `vocab` elements of `dtype` (FUSE_F32, FUSE_F16, FUSE_BF16), ld elements apart,
+ *            aligned to their element
+ *   tokens   device int32 [rows]; a negative one: no token given (logprob 0; a padded row)
+ *   logprob, entropy  device fp32 [rows], top_logprob  device fp32 [rows, top], top_index  device int32
+ *            [rows, top]; each may be NULL, not all of them.  tokens may be NULL when logprob is.
+ *   Rules: 0 <= top <= vocab, top <= 32, vocab < 2^31 - 64, rows < 2^28 (else FUSE_EUNSUPPORTED); scale > 0, and
+ *          scale log2(e) finite; no output overlaps an input or another output.
+ * A logit of -inf has probability 0 (log probability -inf).  A row of nothing else has log probability -inf for
+ * every token and entropy 0.  A logit of +inf or NaN makes the row's log probabilities and entropy NaN; among the
+ * alternatives a NaN counts as -inf.  A token >= vocab gives NaN (fuse_check() then returns FUSE_EINDEX).
+ * Sums are fp32, and their order is fixed.
+ */
+int fuse_token_logprobs(const void* logits, int64_t ld, const int32_t* tokens, float* logprob,
+                        float* entropy, float* top_logprob, int32_t* top_index, int64_t rows, int64_t vocab,
+                        int64_t top, float scale, int dtype, fuse_stream_t stream);
+
 /* ===================================================================== ledgers
  * [K4] §① traffic(): a cut plan splits the K stages into consecutive kernels (cut_mask bit i =
  * a kernel boundary after stage i).  Each kernel reads the previous kernel's output (the
@@ -489,6 +593,11 @@ int64_t fuse_paged_attention_flops(int64_t batch, int64_t q_heads, int64_t D, in
                                    int64_t keys);
 int64_t fuse_w4_gemv_bytes(int64_t M, int64_t N, int64_t K, int64_t group, int zeros, int bias,
                            int residual);
+/* keys = the sum of seq_lens over sequences with new tokens; pairs = the query-key pairs that the mask leaves. */
+int64_t fuse_prompt_attention_bytes(int64_t tokens, int64_t keys, int64_t q_heads, int64_t kv_heads, int64_t D);
+int64_t fuse_prompt_attention_flops(int64_t pairs, int64_t q_heads, int64_t D);
+int64_t fuse_mxfp4_gemm_bytes(int64_t M, int64_t N, int64_t K, int bias, int residual);
+int64_t fuse_token_logprobs_bytes(int64_t rows, int64_t vocab, int64_t top, int dtype);
 
 /* ===================================================================== reports and status
  * [K4] §③ and [C05] §6.2: registers per thread, spills and blocks per SM decide when fusion
