@@ -207,7 +207,7 @@ bool make_map_3d(CUtensorMap* map, const void* ptr, MapType type, const int64_t 
         bx[i] = static_cast<cuuint32_t>(box[i]);
     }
     for (int i = 0; i < 2; ++i) st[i] = static_cast<cuuint64_t>(strides[i]);
-    CUresult r = enc(map, type == kMapU8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3,
+    CUresult r = enc(map, type == kMapU8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : type == kMap16 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT32, 3,
                      const_cast<void*>(ptr), d, st, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                      swizzle == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : swizzle == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);

@@ -15,9 +15,9 @@ namespace fc {
 // missing or the encoder rejects the arguments (base alignment, strides, box size).
 bool make_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols, int box_cols,
               int box_rows, bool bf16 = false);
-// Host: a TMA descriptor of a 3-D tensor of bytes or of 16-bit elements: extents dims[0..2] (innermost
+// Host: a TMA descriptor of a 3-D tensor of bytes, 16-bit or 32-bit elements: extents dims[0..2] (innermost
 // first), byte strides of dims[1] and dims[2], box extents, swizzle width in bytes (0, 64 or 128).
-enum MapType { kMapU8, kMap16 };
+enum MapType { kMapU8, kMap16, kMap32 };
 bool make_map_3d(CUtensorMap* map, const void* ptr, MapType type, const int64_t (&dims)[3],
                  const int64_t (&strides)[2], const int (&box)[3], int swizzle);
 
@@ -268,6 +268,21 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
+// The same by a whole converged warp, of which the elected lane's instruction counts.
+__device__ __forceinline__ void tma_load_2d_pair_if(uint32_t one, uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair_if(uint32_t one, uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+        "@q cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "r"(one)
+        : "memory");
+}
 // Collective over the pair: one warp of each CTA executes these together.
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t holder, uint32_t ncols) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(holder), "r"(ncols)
@@ -276,6 +291,15 @@ __device__ __forceinline__ void tmem_alloc_pair(uint32_t holder, uint32_t ncols)
 }
 __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// tmem_begin() for a pair.
+__device__ __forceinline__ uint32_t tmem_begin_pair(uint32_t holder, const void* held, uint32_t ncols, int warp) {
+    if (warp == 1) tmem_alloc_pair(holder, ncols);
+    tc_fence_before();
+    cluster_sync();      // both CTAs' barriers exist before either signals the other
+    tc_fence_after();
+    pdl_trigger();
+    return __shfl_sync(0xffffffffu, *static_cast<const volatile uint32_t*>(held), 0);
 }
 __device__ __forceinline__ void tc_mma_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                             uint32_t accumulate) {
@@ -301,6 +325,12 @@ __device__ __forceinline__ void tc_commit_pair_mc(uint32_t bar, uint16_t mask) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
         " [%0], %1;" ::"r"(bar), "h"(mask)
+        : "memory");
+}
+__device__ __forceinline__ void tc_commit_pair_mc_if(uint32_t one, uint32_t bar, uint16_t mask) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar), "h"(mask), "r"(one)
         : "memory");
 }
 __device__ __forceinline__ void tc_commit_pair(uint32_t bar) {

@@ -15,6 +15,7 @@
 #include <cudaTypedefs.h>
 #include <math.h>
 
+#include <mutex>
 #include <type_traits>
 
 #include "fc_internal.cuh"
@@ -201,6 +202,31 @@ __device__ __forceinline__ void finish_store(const GemmArgs& a, int token, int n
     static_cast<T*>(a.y)[at] = from_f32<T>(v);
 }
 
+// 32 tokens from `token` on of weight n, whose sums are v.
+template <typename T>
+__device__ __forceinline__ void finish_32(const GemmArgs& a, int token, int n, bool in, const float (&v)[32], float bias) {
+    const int64_t at = static_cast<int64_t>(token) * a.N + n;
+    const T* R = static_cast<const T*>(a.R) + at;
+    T* y = static_cast<T*>(a.y) + at;
+    const int left = in ? a.M - token : 0;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        float r[8] = {};
+        if (a.R)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (8 * g + e < left) r[e] = to_f32(R[static_cast<int64_t>(8 * g + e) * a.N]);
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+            float2 x = __fadd2_rn(make_float2(v[8 * g + e], v[8 * g + e + 1]), f2(bias));
+            if (a.gelu) x = gelu_erf2(x);
+            x = __fadd2_rn(x, make_float2(r[e], r[e + 1]));
+            if (8 * g + e < left) y[static_cast<int64_t>(8 * g + e) * a.N] = from_f32<T>(x.x);
+            if (8 * g + e + 1 < left) y[static_cast<int64_t>(8 * g + e + 1) * a.N] = from_f32<T>(x.y);
+        }
+    }
+}
+
 template <typename T, int NT>
 __global__ void __launch_bounds__(kGemmThreads, NT <= 64 ? 2 : 1) mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap mW,
                                                                                    const __grid_constant__ CUtensorMap mX,
@@ -249,8 +275,8 @@ __global__ void __launch_bounds__(kGemmThreads, NT <= 64 ? 2 : 1) mxfp4_gemm_ker
             const uint32_t at = base + slot * L::STAGE, bytes = 512u * static_cast<uint32_t>(min(2, a.xtk - 2 * s));
             if (lane == 0) mbar_arrive_expect_tx(full(slot), kTileBytes + L::B_BYTES + 2 * bytes);
             __syncwarp();
-            tma_load_3d_if(one, at, &mW, s * 128, n0, 0, full(slot));
-            tma_load_3d_if(one, at + L::OFF_B, &mX, s * 128, m0, 0, full(slot));
+            tma_load_2d_if(one, at, &mW, s * 64, n0, full(slot));
+            tma_load_2d_if(one, at + L::OFF_B, &mX, s * 64, m0, full(slot));
             if (one) {
                 bulk_load(at + L::OFF_SA, sw + s * 1024, bytes, full(slot));
                 bulk_load(at + L::OFF_SB, sx + s * 1024, bytes, full(slot));
@@ -345,16 +371,252 @@ __global__ void __launch_bounds__(kGemmThreads, NT <= 64 ? 2 : 1) mxfp4_gemm_ker
     }
 }
 
-bool map_u8(CUtensorMap* map, const void* q, int64_t rows, int64_t K, int box_rows) {
-    const int64_t dims[3] = {K / 2, rows, 1}, strides[2] = {K / 2, rows * (K / 2)};
-    const int box[3] = {128, box_rows, 1};
-    return make_map_3d(map, q, kMapU8, dims, strides, box, 128);
+// ------------------------------------------------------------------ many tokens: CTA pairs
+// Persistent clusters of two CTAs: M = 256 weights by N = 256 tokens (cta_group::2), each CTA holding its 128 weights, half of
+// the tokens and, of the scales, its weights' and all tokens'.  Two accumulators of 256 columns and 24 columns of scales do
+// not fit TMEM's 512, so the accumulators share 24 columns, which the epilogue reads first: the next tile's products
+// start as soon as those are read, and run while the rest is finished and stored.
+struct PairLayout {
+    static constexpr int STAGES = 6;
+    static constexpr uint32_t OFF_B = kTileBytes, OFF_SA = OFF_B + kTileBytes, OFF_SB = OFF_SA + 1024;
+    static constexpr uint32_t STAGE = OFF_SB + 2048;
+    static constexpr uint32_t OFF_BAR = STAGES * STAGE;
+    static constexpr uint32_t OFF_HOLD = OFF_BAR + (2 * STAGES + 4) * 8;
+    static constexpr uint32_t SMEM = OFF_HOLD + 16 + 1024;
+    static constexpr uint32_t ACC1 = 232, SFA_COL = 488, SFB_COL = 496;    // accumulators at 0 and 232
+    static_assert(STAGE % 1024 == 0, "swizzle atoms");
+    static_assert(SMEM <= 232448, "shared-memory budget");
+};
+constexpr int kPairEpiWarps = 8;                       // two per TMEM lane quadrant
+constexpr int kPairThreads = 32 * (2 + kPairEpiWarps);
+constexpr int kBand = 32;                              // token tiles of a band: 8192 tokens' values stay in L2
+
+__device__ __forceinline__ void tc_mma_mxf4_pair_if(uint32_t one, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sa,
+                                                    uint32_t sb, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate), "r"(one)
+        : "memory");
+}
+// (in each CTA of the pair from its own shared memory to its own TMEM)
+__device__ __forceinline__ void tc_cp_scales_pair_if(uint32_t one, uint32_t tmem, uint64_t desc) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+        "@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(tmem), "l"(desc), "r"(one)
+        : "memory");
+}
+
+struct PairArgs {
+    GemmArgs g;
+    int tiles_m, tiles_n;         // of 256 tokens, of 256 weights
+};
+// Tile t: bands of token tiles, weight by weight within a band.
+__device__ __forceinline__ void tile_of(const PairArgs& a, int t, int& m0, int& n0) {
+    const int per = kBand * a.tiles_n, band = t / per, first = band * kBand, wide = min(kBand, a.tiles_m - first), i = t - band * per;
+    m0 = (first + i % wide) * 256;
+    n0 = (i / wide) * 256;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kPairThreads, 1) mxfp4_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX,
+                                                                     const __grid_constant__ CUtensorMap mSW, const __grid_constant__ CUtensorMap mSX,
+                                                                     const __grid_constant__ PairArgs a) {
+    using L = PairLayout;
+    constexpr int ST = L::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    uint8_t* gbase = smem_raw + (base - smem_addr(smem_raw));
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
+    auto full = [&](int i) { return base + L::OFF_BAR + 8u * i; };
+    auto empty = [&](int i) { return base + L::OFF_BAR + 8u * (ST + i); };
+    auto acc_full = [&](int i) { return base + L::OFF_BAR + 8u * (2 * ST + i); };
+    const uint32_t acc_read = base + L::OFF_BAR + 8u * (2 * ST + 2), drain = acc_read + 8;
+    const uint32_t rank = cluster_rank();
+    const int cid = static_cast<int>(blockIdx.x) / 2, clusters = static_cast<int>(gridDim.x) / 2;
+    const int tiles = a.tiles_m * a.tiles_n, nk = a.g.stages;
+    int* flag = a.g.flag;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(full(i), 1);
+            mbar_init(empty(i), 1);
+        }
+        for (int i = 0; i < 2; ++i) mbar_init(acc_full(i), 1);
+        mbar_init(acc_read, 2 * kPairEpiWarps);
+        mbar_init(drain, 1);
+        fence_mbar_init();
+    }
+    const uint32_t tmem = tmem_begin_pair(base + L::OFF_HOLD, gbase + L::OFF_HOLD, 512, warp);
+    pdl_wait();
+
+    bool ok = true;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity & 1u, flag));
+        return ok;
+    };
+    if (warp == 0) {
+        // ---------------------------------------------------------------- loads; both CTAs' bytes count on the even one's barrier
+        if (lane == 0) {
+            prefetch_map(&mW);
+            prefetch_map(&mX);
+            prefetch_map(&mSW);
+            prefetch_map(&mSX);
+        }
+        const uint32_t one = elect_one();
+        int c = 0;
+        for (int t = cid; ok && t < tiles; t += clusters) {
+            int m0, n0;
+            tile_of(a, t, m0, n0);
+            for (int s = 0; s < nk; ++s, ++c) {
+                const int slot = c % ST;
+                if (c >= ST && !wait(empty(slot), c / ST - 1)) break;
+                if (rank == 0 && lane == 0) mbar_arrive_expect_tx(full(slot), 2 * L::STAGE);
+                __syncwarp();
+                const uint32_t at = base + slot * L::STAGE, bar = mapa_shared(full(slot), 0);
+                tma_load_2d_pair_if(one, at, &mW, s * 64, n0 + static_cast<int>(rank) * 128, bar);
+                tma_load_2d_pair_if(one, at + L::OFF_B, &mX, s * 64, m0 + static_cast<int>(rank) * 128, bar);
+                tma_load_3d_pair_if(one, at + L::OFF_SA, &mSW, s * 256, n0 / 128 + static_cast<int>(rank), 0, bar);
+                tma_load_3d_pair_if(one, at + L::OFF_SB, &mSX, s * 256, m0 / 128, 0, bar);
+            }
+        }
+        if (!ok && rank == 0)   // both CTAs' copies in flight land before either's shared memory goes away
+            for (int j = max(0, c - ST); j < c; ++j) (void)mbar_wait_drain(full(j % ST), (j / ST) & 1);
+    } else if (warp == 1 && rank == 0) {
+        // ---------------------------------------------------------------- MMA issue, for both CTAs
+        const uint32_t one = elect_one();
+        const int mine = tiles > cid ? (tiles - 1 - cid) / clusters + 1 : 0, total = mine * nk;
+        int c = 0;
+        for (int i = 0; ok && i < mine; ++i) {
+            // the accumulator has been read (two tiles ago), and the columns it shares with the other one
+            if (i > 0 && !wait(acc_read, i - 1)) break;
+            tc_fence_after();
+            const uint32_t d = tmem + (i % 2 ? L::ACC1 : 0);
+            for (int s = 0; s < nk; ++s, ++c) {
+                const int slot = c % ST;
+                if (!wait(full(slot), c / ST)) break;
+                tc_fence_after();
+                const uint32_t at = base + slot * L::STAGE;
+                const int steps = min(4, (a.g.K - s * kStageK + 63) / 64);
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+                    if (2 * t < steps) {
+                        tc_cp_scales_pair_if(one, tmem + L::SFA_COL + 4 * t, scale_desc(at + L::OFF_SA + 512 * t));
+                        tc_cp_scales_pair_if(one, tmem + L::SFB_COL + 8 * t, scale_desc(at + L::OFF_SB + 512 * t));
+                        tc_cp_scales_pair_if(one, tmem + L::SFB_COL + 8 * t + 4, scale_desc(at + L::OFF_SB + 1024 + 512 * t));
+                    }
+                const uint64_t da = smem_desc_sw128(at, 16, 1024), db = smem_desc_sw128(at + L::OFF_B, 16, 1024);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (k < steps)
+                        tc_mma_mxf4_pair_if(one, d, da + 2 * k, db + 2 * k, k % 2 ? idesc_mxf4(256, 256, 2) : idesc_mxf4(256, 256, 0),
+                                            tmem + L::SFA_COL + 4 * (k / 2), tmem + L::SFB_COL + 8 * (k / 2), s > 0 || k > 0 ? 1u : 0u);
+                // frees the stage in both CTAs, unless no later load uses it
+                if (c + ST < total) tc_commit_pair_mc_if(one, empty(slot), 0x3);
+            }
+            if (ok) tc_commit_pair_mc_if(one, acc_full(i % 2), 0x3);
+        }
+        if (!ok && c > 0) {     // MMAs in flight finish before TMEM is freed
+            if (one) tc_commit_pair(drain);
+            __syncwarp();
+            (void)mbar_wait_drain(drain, 0);
+        }
+    } else if (warp >= 2) {
+        // ---------------------------------------------------------------- epilogue: 32 weights by 128 tokens of a tile
+        const int q = warp % 4, h = (warp - 2) / 4;
+        const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
+        for (int t = cid, i = 0; t < tiles; t += clusters, ++i) {
+            int m0, n0;
+            tile_of(a, t, m0, n0);
+            const int b = i % 2, n = n0 + static_cast<int>(rank) * 128 + 32 * q + lane;
+            const bool in = n < a.g.N, shared = h == (b ? 0 : 1);      // (the shared columns are tokens 232..255 of accumulator 0, 0..23 of 1)
+            const float bias = in && a.g.bias ? to_f32(static_cast<const T*>(a.g.bias)[n]) : 0.0f;
+            if (!shared && lane == 0) mbar_arrive_cluster(mapa_shared(acc_read, 0));
+            if (!wait(acc_full(b), i / 2)) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int x = 0; x < 4; ++x) {
+                const int col = 128 * h + 32 * (b == 0 && h == 1 ? (x + 3) % 4 : x);
+                float v[32];
+                tmem_ld32(tmem + lanes + (b ? L::ACC1 : 0) + col, v);
+                tmem_ld_wait();
+                if (x == 0 && shared) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(mapa_shared(acc_read, 0));
+                }
+                finish_32<T>(a.g, m0 + col, n, in, v, bias);
+            }
+            tc_fence_before();
+            __syncwarp();
+        }
+    }
+    tc_fence_before();
+    cluster_sync();  // neither CTA leaves while its peer may still signal it
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
+// A quantised matrix as rows of 16-bit elements (four values each), boxes of 128 bytes.
+bool map_codes(CUtensorMap* map, const void* q, int64_t rows, int64_t K, int box_rows) { return make_map(map, q, rows, K / 4, 64, box_rows); }
+// Its scale tiles: a row of tiles as 32-bit elements, boxes of two tiles' 1024 bytes.
+bool map_scales(CUtensorMap* map, const void* s, int64_t rows, int64_t K, int box_rows) {
+    const int64_t row = ceil_div(K, 128) * 512, n = ceil_div(rows, 128);
+    const int64_t dims[3] = {row / 4, n, 1}, strides[2] = {row, row * n};
+    const int box[3] = {256, box_rows, 1};
+    return make_map_3d(map, s, kMap32, dims, strides, box, 0);
+}
+
+// Pairs that can be resident at once (both CTAs of one in one cluster of SMs).
+int pairs() {
+    static std::mutex mu;
+    static int cached[64] = {0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+        (void)cudaGetLastError();
+        return 1;
+    }
+    std::lock_guard<std::mutex> lock(mu);
+    if (cached[dev] == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2 * static_cast<unsigned>(sm_count()));
+        cfg.blockDim = dim3(kPairThreads);
+        cfg.dynamicSmemBytes = PairLayout::SMEM;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = 2;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (opt_in_smem((const void*)mxfp4_pair_kernel<__half>, PairLayout::SMEM) != FUSE_OK ||
+            cudaOccupancyMaxActiveClusters(&n, mxfp4_pair_kernel<__half>, &cfg) != cudaSuccess || n < 1) {
+            (void)cudaGetLastError();
+            n = sm_count() / 2;
+        }
+        cached[dev] = n > 0 ? n : 1;
+    }
+    return cached[dev];
+}
+
+template <typename T>
+int launch_pair(const GemmArgs& g, const void* xq, const void* wq, cudaStream_t st) {
+    CUtensorMap mW, mX, mSW, mSX;
+    if (!map_codes(&mW, wq, g.N, g.K, 128) || !map_codes(&mX, xq, g.M, g.K, 128) || !map_scales(&mSW, g.ws, g.N, g.K, 1) ||
+        !map_scales(&mSX, g.xs, g.M, g.K, 2))
+        return FUSE_ECUDA;
+    const int rc = opt_in_smem((const void*)mxfp4_pair_kernel<T>, PairLayout::SMEM);
+    if (rc != FUSE_OK) return rc;
+    const PairArgs a{g, static_cast<int>(ceil_div(g.M, 256)), static_cast<int>(ceil_div(g.N, 256))};
+    const int64_t tiles = static_cast<int64_t>(a.tiles_m) * a.tiles_n;
+    const int n = pairs();
+    return launch_pdl(mxfp4_pair_kernel<T>, dim3(2 * static_cast<unsigned>(tiles < n ? tiles : n)), dim3(kPairThreads), PairLayout::SMEM, st, 2, mW, mX,
+                      mSW, mSX, a);
 }
 
 template <typename T, int NT>
 int launch_gemm(GemmArgs a, const void* xq, const void* wq, cudaStream_t st) {
     CUtensorMap mW, mX;
-    if (!map_u8(&mW, wq, a.N, a.K, 128) || !map_u8(&mX, xq, a.M, a.K, NT)) return FUSE_ECUDA;
+    if (!map_codes(&mW, wq, a.N, a.K, 128) || !map_codes(&mX, xq, a.M, a.K, NT)) return FUSE_ECUDA;
     const int rc = opt_in_smem((const void*)mxfp4_gemm_kernel<T, NT>, GemmLayout<NT>::SMEM);
     if (rc != FUSE_OK) return rc;
     const int64_t tn = ceil_div(a.N, 128), tm = ceil_div(a.M, NT);
@@ -368,6 +630,7 @@ template <typename T>
 int run_gemm(const GemmArgs& a, const void* xq, const void* wq, cudaStream_t st) {
     if (a.M <= 32) return launch_gemm<T, 32>(a, xq, wq, st);
     if (a.M <= 64) return launch_gemm<T, 64>(a, xq, wq, st);
+    if (ceil_div(a.M, 256) * ceil_div(a.N, 256) >= pairs() / 2) return launch_pair<T>(a, xq, wq, st);
     return launch_gemm<T, 128>(a, xq, wq, st);
 }
 
@@ -382,7 +645,7 @@ int check_matrix(int64_t rows, int64_t cols) {
 
 }  // namespace
 
-int mxfp4_report_count() { return 12; }
+int mxfp4_report_count() { return 14; }
 int mxfp4_report(int i, fuse_kernel_record* out) {
     switch (i) {
         FC_REPORT(0, kQThreads, 0, 0, mxfp4_quantize_kernel<float>);
@@ -397,6 +660,8 @@ int mxfp4_report(int i, fuse_kernel_record* out) {
         FC_REPORT(9, kGemmThreads, GemmLayout<32>::SMEM, GemmLayout<32>::TMEM_COLS, mxfp4_gemm_kernel<__nv_bfloat16, 32>);
         FC_REPORT(10, kGemmThreads, GemmLayout<64>::SMEM, GemmLayout<64>::TMEM_COLS, mxfp4_gemm_kernel<__nv_bfloat16, 64>);
         FC_REPORT(11, kGemmThreads, GemmLayout<128>::SMEM, GemmLayout<128>::TMEM_COLS, mxfp4_gemm_kernel<__nv_bfloat16, 128>);
+        FC_REPORT(12, kPairThreads, PairLayout::SMEM, 512, mxfp4_pair_kernel<__half>);
+        FC_REPORT(13, kPairThreads, PairLayout::SMEM, 512, mxfp4_pair_kernel<__nv_bfloat16>);
         default: return FUSE_EINVAL;
     }
 }

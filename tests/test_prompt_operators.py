@@ -225,13 +225,16 @@ def test_dependents_start_with_the_tensor_memory_in_hand():
         with open(os.path.join(csrc, name), encoding="utf-8") as f:
             return re.sub(r"//[^\n]*", "", f.read())
 
-    body = re.search(r"uint32_t tmem_begin\([^{]*\{(.*?)\n\}", source("fc_tc.cuh"), re.S).group(1)
-    at = [body.index(x) for x in ("tmem_alloc(", "__syncthreads();", "pdl_trigger();", "return")]
-    assert at == sorted(at)
+    tc = source("fc_tc.cuh")
+    for name, alloc, barrier in (("tmem_begin", "tmem_alloc(", "__syncthreads();"), ("tmem_begin_pair", "tmem_alloc_pair(", "cluster_sync();")):
+        body = re.search(r"uint32_t %s\([^{]*\{(.*?)\n\}" % name, tc, re.S).group(1)
+        at = [body.index(x) for x in (alloc, barrier, "pdl_trigger();", "return")]
+        assert at == sorted(at)
     for name in ("prompt_attention.cu", "mxfp4.cu"):
         for kernel in re.findall(r"__global__.*?\n\}", source(name), re.S):
-            if "tmem_begin(" in kernel:
+            begin = re.search(r"tmem_begin(_pair)?\(", kernel)
+            if begin:
                 assert "pdl_trigger" not in kernel and "pdl_begin" not in kernel and "tmem_alloc" not in kernel
-                assert kernel.index("tmem_begin(") < kernel.index("pdl_wait();")
+                assert begin.start() < kernel.index("pdl_wait();")
             else:
                 assert kernel.index("pdl_begin();") > 0 and "tmem_dealloc" not in kernel
