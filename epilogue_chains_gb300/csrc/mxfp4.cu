@@ -202,28 +202,33 @@ __device__ __forceinline__ void finish_store(const GemmArgs& a, int token, int n
     static_cast<T*>(a.y)[at] = from_f32<T>(v);
 }
 
-// 32 tokens from `token` on of weight n, whose sums are v.
+// 32 tokens of one weight, N elements apart, `left` of them in the matrix: the residual, and the sums v finished and stored.
+// (Whether there are GELU and residual is decided once for all 32: a branch for each keeps their chains of instructions
+// from running next to one another, and took 8192 x 28672 x 4096 with GELU from 323 to 352 us.)
 template <typename T>
-__device__ __forceinline__ void finish_32(const GemmArgs& a, int token, int n, bool in, const float (&v)[32], float bias) {
-    const int64_t at = static_cast<int64_t>(token) * a.N + n;
-    const T* R = static_cast<const T*>(a.R) + at;
-    T* y = static_cast<T*>(a.y) + at;
-    const int left = in ? a.M - token : 0;
+__device__ __forceinline__ void load_32(const T* R, int64_t N, int left, T (&r)[32]) {
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        float r[8] = {};
-        if (a.R)
+    for (int e = 0; e < 32; ++e) r[e] = e < left ? __ldcs(R + e * N) : from_f32<T>(0.0f);
+}
+template <typename T, bool GELU, bool ADD>
+__device__ __forceinline__ void finish_pairs(T* y, int64_t N, int left, const float (&v)[32], float bias, const T (&r)[32]) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (8 * g + e < left) r[e] = to_f32(R[static_cast<int64_t>(8 * g + e) * a.N]);
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-            float2 x = __fadd2_rn(make_float2(v[8 * g + e], v[8 * g + e + 1]), f2(bias));
-            if (a.gelu) x = gelu_erf2(x);
-            x = __fadd2_rn(x, make_float2(r[e], r[e + 1]));
-            if (8 * g + e < left) y[static_cast<int64_t>(8 * g + e) * a.N] = from_f32<T>(x.x);
-            if (8 * g + e + 1 < left) y[static_cast<int64_t>(8 * g + e + 1) * a.N] = from_f32<T>(x.y);
-        }
+    for (int e = 0; e < 32; e += 2) {
+        float2 x = __fadd2_rn(make_float2(v[e], v[e + 1]), f2(bias));
+        if constexpr (GELU) x = gelu_erf2(x);
+        if constexpr (ADD) x = __fadd2_rn(x, make_float2(to_f32(r[e]), to_f32(r[e + 1])));
+        if (e < left) y[e * N] = from_f32<T>(x.x);
+        if (e + 1 < left) y[(e + 1) * N] = from_f32<T>(x.y);
+    }
+}
+template <typename T>
+__device__ __forceinline__ void finish_32(T* y, int64_t N, int left, bool gelu, const float (&v)[32], float bias, const T (&r)[32], bool add) {
+    if (gelu) {
+        if (add) finish_pairs<T, true, true>(y, N, left, v, bias, r);
+        else finish_pairs<T, true, false>(y, N, left, v, bias, r);
+    } else {
+        if (add) finish_pairs<T, false, true>(y, N, left, v, bias, r);
+        else finish_pairs<T, false, false>(y, N, left, v, bias, r);
     }
 }
 
@@ -325,19 +330,21 @@ __global__ void __launch_bounds__(kGemmThreads, NT <= 64 ? 2 : 1) mxfp4_gemm_ker
         if (s1 == s0 || wait(done, 0)) {
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < tokens; c += 16) {
-                float v[16] = {};
+            for (int c = 0; c < tokens; c += 32) {
+                float v[32] = {};
+                T r[32];
+                const int64_t at = static_cast<int64_t>(m0 + c) * a.N + n;
+                const int left = in ? tokens - c : 0;
+                if (a.R && split == 1) load_32<T>(static_cast<const T*>(a.R) + at, a.N, left, r);
                 if (s1 > s0) {
-                    tmem_ld16(tmem + (static_cast<uint32_t>(32 * quad) << 16) + c, v);
+                    tmem_ld32(tmem + (static_cast<uint32_t>(32 * quad) << 16) + c, v);
                     tmem_ld_wait();
                 }
                 if (split > 1) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) part_sums[(c + e) * 128 + row] = v[e];
-                } else if (in) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        if (c + e < tokens) finish_store<T>(a, m0 + c + e, n, v[e], bias);
+                    for (int e = 0; e < 32; ++e) part_sums[(c + e) * 128 + row] = v[e];
+                } else {
+                    finish_32<T>(static_cast<T*>(a.y) + at, a.N, left, a.gelu != 0, v, bias, r, a.R != nullptr);
                 }
             }
             tc_fence_before();
@@ -377,18 +384,19 @@ __global__ void __launch_bounds__(kGemmThreads, NT <= 64 ? 2 : 1) mxfp4_gemm_ker
 // not fit TMEM's 512, so the accumulators share 24 columns, which the epilogue reads first: the next tile's products
 // start as soon as those are read, and run while the rest is finished and stored.
 struct PairLayout {
-    static constexpr int STAGES = 6;
+    static constexpr int STAGES = 5;
     static constexpr uint32_t OFF_B = kTileBytes, OFF_SA = OFF_B + kTileBytes, OFF_SB = OFF_SA + 1024;
     static constexpr uint32_t STAGE = OFF_SB + 2048;
     static constexpr uint32_t OFF_BAR = STAGES * STAGE;
-    static constexpr uint32_t OFF_HOLD = OFF_BAR + (2 * STAGES + 4) * 8;
+    static constexpr uint32_t OFF_HOLD = OFF_BAR + (2 * STAGES + 6) * 8;
     static constexpr uint32_t SMEM = OFF_HOLD + 16 + 1024;
     static constexpr uint32_t ACC1 = 232, SFA_COL = 488, SFB_COL = 496;    // accumulators at 0 and 232
     static_assert(STAGE % 1024 == 0, "swizzle atoms");
     static_assert(SMEM <= 232448, "shared-memory budget");
 };
-constexpr int kPairEpiWarps = 8;                       // two per TMEM lane quadrant
-constexpr int kPairThreads = 32 * (2 + kPairEpiWarps);
+constexpr int kPairEpiWarps = 16;                      // four per TMEM lane quadrant
+constexpr int kPairThreads = 32 * (4 + kPairEpiWarps); // warp 0: loads, 1: MMA issue, 4-19: epilogue
+// Registers of a thread: 96 at the launch, then 40 and 104 (128 (40 + 4 x 104) = 58368 of the launch's 640 x 96 = 61440).
 constexpr int kBand = 32;                              // token tiles of a band: 8192 tokens' values stay in L2
 
 __device__ __forceinline__ void tc_mma_mxf4_pair_if(uint32_t one, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sa,
@@ -431,7 +439,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) mxfp4_pair_kernel(const __gri
     auto full = [&](int i) { return base + L::OFF_BAR + 8u * i; };
     auto empty = [&](int i) { return base + L::OFF_BAR + 8u * (ST + i); };
     auto acc_full = [&](int i) { return base + L::OFF_BAR + 8u * (2 * ST + i); };
-    const uint32_t acc_read = base + L::OFF_BAR + 8u * (2 * ST + 2), drain = acc_read + 8;
+    auto acc_done = [&](int i) { return base + L::OFF_BAR + 8u * (2 * ST + 2 + i); };
+    const uint32_t acc_read = base + L::OFF_BAR + 8u * (2 * ST + 4), drain = acc_read + 8;
     const uint32_t rank = cluster_rank();
     const int cid = static_cast<int>(blockIdx.x) / 2, clusters = static_cast<int>(gridDim.x) / 2;
     const int tiles = a.tiles_m * a.tiles_n, nk = a.g.stages;
@@ -442,7 +451,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) mxfp4_pair_kernel(const __gri
             mbar_init(empty(i), 1);
         }
         for (int i = 0; i < 2; ++i) mbar_init(acc_full(i), 1);
-        mbar_init(acc_read, 2 * kPairEpiWarps);
+        for (int i = 0; i < 2; ++i) mbar_init(acc_done(i), 2 * kPairEpiWarps);
+        mbar_init(acc_read, 2 * 4);
         mbar_init(drain, 1);
         fence_mbar_init();
     }
@@ -454,6 +464,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) mxfp4_pair_kernel(const __gri
         ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity & 1u, flag));
         return ok;
     };
+    if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == 0) {
         // ---------------------------------------------------------------- loads; both CTAs' bytes count on the even one's barrier
         if (lane == 0) {
@@ -487,7 +499,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) mxfp4_pair_kernel(const __gri
         const int mine = tiles > cid ? (tiles - 1 - cid) / clusters + 1 : 0, total = mine * nk;
         int c = 0;
         for (int i = 0; ok && i < mine; ++i) {
-            // the accumulator has been read (two tiles ago), and the columns it shares with the other one
+            // this accumulator has been read (two tiles ago), and the columns that it shares with the other one
+            if (i > 1 && !wait(acc_done(i % 2), i / 2 - 1)) break;
             if (i > 0 && !wait(acc_read, i - 1)) break;
             tc_fence_after();
             const uint32_t d = tmem + (i % 2 ? L::ACC1 : 0);
@@ -520,34 +533,42 @@ __global__ void __launch_bounds__(kPairThreads, 1) mxfp4_pair_kernel(const __gri
             __syncwarp();
             (void)mbar_wait_drain(drain, 0);
         }
-    } else if (warp >= 2) {
-        // ---------------------------------------------------------------- epilogue: 32 weights by 128 tokens of a tile
-        const int q = warp % 4, h = (warp - 2) / 4;
+    }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        // ---------------------------------------------------------------- epilogue: 32 weights by 64 tokens of a tile
+        // in two chunks, the one with the shared columns (tokens 232..255 of accumulator 0, 0..23 of 1) first.  The first
+        // chunk's residual is on its way while the tile's products run.
+        const int q = warp % 4, h = (warp - 4) / 4;
         const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
+        const bool add = a.g.R != nullptr;
         for (int t = cid, i = 0; t < tiles; t += clusters, ++i) {
             int m0, n0;
             tile_of(a, t, m0, n0);
             const int b = i % 2, n = n0 + static_cast<int>(rank) * 128 + 32 * q + lane;
-            const bool in = n < a.g.N, shared = h == (b ? 0 : 1);      // (the shared columns are tokens 232..255 of accumulator 0, 0..23 of 1)
+            const bool in = n < a.g.N;
             const float bias = in && a.g.bias ? to_f32(static_cast<const T*>(a.g.bias)[n]) : 0.0f;
-            if (!shared && lane == 0) mbar_arrive_cluster(mapa_shared(acc_read, 0));
+            auto token = [&](int x) { return 64 * h + 32 * (b ? x : 1 - x); };
+            auto at = [&](int x) { return static_cast<int64_t>(m0 + token(x)) * a.g.N + n; };
+            auto left = [&](int x) { return in ? a.g.M - m0 - token(x) : 0; };
+            T r[32];
+            if (add) load_32<T>(static_cast<const T*>(a.g.R) + at(0), a.g.N, left(0), r);
             if (!wait(acc_full(b), i / 2)) break;
             tc_fence_after();
 #pragma unroll 1
-            for (int x = 0; x < 4; ++x) {
-                const int col = 128 * h + 32 * (b == 0 && h == 1 ? (x + 3) % 4 : x);
+            for (int x = 0; x < 2; ++x) {
                 float v[32];
-                tmem_ld32(tmem + lanes + (b ? L::ACC1 : 0) + col, v);
+                tmem_ld32(tmem + lanes + (b ? L::ACC1 : 0) + token(x), v);
                 tmem_ld_wait();
-                if (x == 0 && shared) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(mapa_shared(acc_read, 0));
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (x == 0 && h == (b ? 0 : 3)) mbar_arrive_cluster(mapa_shared(acc_read, 0));
+                    if (x == 1) mbar_arrive_cluster(mapa_shared(acc_done(b), 0));
                 }
-                finish_32<T>(a.g, m0 + col, n, in, v, bias);
+                if (x == 1 && add) load_32<T>(static_cast<const T*>(a.g.R) + at(1), a.g.N, left(1), r);
+                finish_32<T>(static_cast<T*>(a.g.y) + at(x), a.g.N, left(x), a.g.gelu != 0, v, bias, r, add);
             }
-            tc_fence_before();
-            __syncwarp();
         }
     }
     tc_fence_before();
