@@ -60,11 +60,16 @@ __device__ __forceinline__ void st_v8(float* p, const float* v) {
                  : "memory");
 }
 
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint32_t (&v)[4]) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
+
 struct PromptArgs {
     const int32_t *table, *cu, *lens;
     int64_t table_ld;
     void* o;
     int batch, tokens, hq, hk, group;
+    int recip;                         // row / group = row recip >> 16 for rows below 128
     int tpt, tiles;                    // tokens of a tile of 128 rows; tiles of an item (1 or 2)
     int page_shift, num_pages, cache_rows;
     float c;                           // scale * log2(e)
@@ -210,12 +215,6 @@ struct Walk {
         return false;
     }
 };
-// A softmax warp's walk and segment are in shared memory: kept in registers, next to a row's 128 scores, they spill.
-struct WarpWalk {
-    Walk walk;
-    Seg seg;
-};
-
 // Where run `which` (0: this CTA's, 1: the next's) begins, for all threads; `scratch` is 64 * 8 bytes of shared memory.
 template <int THREADS>
 __device__ __forceinline__ void find_runs(const PromptArgs& a, int64_t* scratch, Pos (&run)[2]) {
@@ -272,16 +271,20 @@ __device__ __forceinline__ void find_runs(const PromptArgs& a, int64_t* scratch,
 }
 
 // ================================================================== the kernel
-constexpr int kSoftWarps = 8;                       // four per tile (one tile: the first four)
-constexpr int kThreads = 32 * (4 + kSoftWarps);     // warp 0: Q, K, V loads, 1: S, 2: PV, 4-11: softmax
-// Registers of a thread: 168 at the launch, then 96 for the first four warps and 200 for the softmax's, whose rows'
-// 128 scores are in registers (128 (96 + 2 x 200) = 63488 of the launch's 384 x 168 = 64512).
-constexpr int kFewRegs = 96, kManyRegs = 200;
+// Warp 0: Q, K, V loads, 1: S, 2: PV, 3: the walk, from 4 on the softmax: eight warps for each tile, two threads to a row.
+// (With a thread to a row, one warp per tile in each quarter of the SM, a step of 256 rows by 128 keys took 2600 cycles, where its
+// products take 2048: a softmax warp's own instructions, one after the other.)
+constexpr int kTileWarps = 8;
 constexpr int kFull = 4;                            // barriers of K tiles in turn, and of V tiles
+constexpr int kSegs = 4;                            // segments that the walk is ahead
 
 template <int D>
 struct Layout {
     static constexpr int TILES = D <= 128 ? 2 : 1;
+    static constexpr int THREADS = 32 * (4 + kTileWarps * TILES);
+    // Registers of a thread at the launch, and then of the first four warps and of the softmax's: within what the launch has.
+    static constexpr int REGS = TILES == 2 ? 96 : 168, FEW = TILES == 2 ? 64 : 96, MANY = TILES == 2 ? 104 : 200;
+    static_assert(128 * (FEW + kTileWarps / 4 * TILES * MANY) <= THREADS * REGS, "registers");
     static constexpr int RING = D == 64 ? 6 : D == 128 ? 3 : 2;    // K and V tiles
     static constexpr uint32_t REGION = 128 * 128;              // one 64-column atom of 128 rows
     static constexpr uint32_t TILE = REGION * (D / 64);
@@ -290,20 +293,21 @@ struct Layout {
     static constexpr uint32_t OFF_KV = TILES * TILE;
     static constexpr uint32_t OFF_P = OFF_KV + RING * TILE;
     static constexpr uint32_t OFF_BAR = OFF_P + TILES * P_BYTES;
-    static constexpr int N_BARS = 2 + 2 * kFull + RING + 8 + 2;
+    static constexpr int N_BARS = 2 + 2 * kFull + RING + 12 + 2 + 2 * kSegs + 4;
     static constexpr uint32_t OFF_HOLD = OFF_BAR + N_BARS * 8;
     static constexpr uint32_t OFF_SCRATCH = (OFF_HOLD + 16 + 7) / 8 * 8;
-    static constexpr uint32_t OFF_WALK = OFF_SCRATCH + 64 * 8;
-    static constexpr uint32_t SMEM = OFF_WALK + 4 * TILES * sizeof(WarpWalk) + 1024;
+    static constexpr uint32_t OFF_SEG = OFF_SCRATCH + 64 * 8;
+    static constexpr uint32_t SMEM = OFF_SEG + kSegs * sizeof(Seg) + 1024;
     static constexpr uint32_t TMEM_COLS = 512, O_COL = 256;    // scores of tile t at 128 t, output at 256 + D t
     static_assert(SMEM <= 232448, "shared-memory budget");
     static_assert(SMEM > 116 * 1024, "one CTA per SM: each takes all of TMEM");
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __grid_constant__ CUtensorMap mQ,
+__global__ void __launch_bounds__(Layout<D>::THREADS, 1) prompt_attention_kernel(const __grid_constant__ CUtensorMap mQ,
                                                                        const __grid_constant__ CUtensorMap mK,
                                                                        const __grid_constant__ CUtensorMap mV,
+                                                                       const __grid_constant__ CUtensorMap mO,
                                                                        const __grid_constant__ PromptArgs a) {
     using L = Layout<D>;
     constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
@@ -320,9 +324,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
     constexpr int X = 2 + 2 * kFull + RING;
     auto s_full = [&](int t) { return bar0 + 8u * (X + t); };
     auto s_free = [&](int t) { return bar0 + 8u * (X + 2 + t); };
-    auto p_full = [&](int t) { return bar0 + 8u * (X + 4 + t); };
-    auto o_done = [&](int t) { return bar0 + 8u * (X + 6 + t); };
-    auto drain = [&](int w) { return bar0 + 8u * (X + 8 + w); };       // of warps 1 and 2
+    auto p_full = [&](int t, int h) { return bar0 + 8u * (X + 4 + 2 * t + h); };      // 64 keys' weights
+    auto o_done = [&](int t, int h) { return bar0 + 8u * (X + 8 + 2 * t + h); };      // and their product with V
+    auto drain = [&](int w) { return bar0 + 8u * (X + 12 + w); };       // of warps 1 and 2
+    auto seg_full = [&](int i) { return bar0 + 8u * (X + 14 + i % kSegs); };
+    auto seg_free = [&](int i) { return bar0 + 8u * (X + 14 + kSegs + i % kSegs); };
+    auto out_full = [&](int t) { return bar0 + 8u * (X + 14 + 2 * kSegs + t); };      // a tile's output is in place of its P
+    auto out_free = [&](int t) { return bar0 + 8u * (X + 16 + 2 * kSegs + t); };      // and has been taken
     int* flag = a.flag;
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
@@ -332,11 +340,19 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
             mbar_init(v_full(i), 1);
         }
         for (int i = 0; i < RING; ++i) mbar_init(empty(i), 1);
+        for (int i = 0; i < kSegs; ++i) {
+            mbar_init(seg_full(i), 1);
+            mbar_init(seg_free(i), 3 + kTileWarps * TILES);
+        }
         for (int t = 0; t < 2; ++t) {
             mbar_init(s_full(t), 1);
-            mbar_init(s_free(t), 4);
-            mbar_init(p_full(t), 4);
-            mbar_init(o_done(t), 1);
+            mbar_init(s_free(t), kTileWarps);
+            mbar_init(out_full(t), kTileWarps);
+            mbar_init(out_free(t), 1);
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(p_full(t, h), kTileWarps);
+                mbar_init(o_done(t, h), 1);
+            }
             mbar_init(drain(t), 1);
         }
         fence_mbar_init();
@@ -345,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
     pdl_wait();
 
     Pos run[2];
-    find_runs<kThreads>(a, reinterpret_cast<int64_t*>(gbase + L::OFF_SCRATCH), run);
+    find_runs<L::THREADS>(a, reinterpret_cast<int64_t*>(gbase + L::OFF_SCRATCH), run);
     if (threadIdx.x == 0) {
         a.start[blockIdx.x] = make_int4(run[0].b, run[0].h, run[0].i, run[0].t);
         if (blockIdx.x + 1 == gridDim.x) a.start[gridDim.x] = make_int4(run[1].b, run[1].h, run[1].i, run[1].t);
@@ -353,11 +369,24 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
     // Steps of an item: K(0), then K(j + 1) before V(j), through one ring.
     auto k_at = [](int j) { return j == 0 ? 0 : 2 * j - 1; };
     auto v_at = [](int j, int n) { return j + 1 < n ? 2 * j + 2 : 2 * j + 1; };
-    Walk walk;
-    walk.begin(a, run[0], run[1]);
+    Seg* segs_at = reinterpret_cast<Seg*>(gbase + L::OFF_SEG);
+    bool ok = true;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity & 1u, flag));
+        return ok;
+    };
+    // Segment k of this CTA, for a warp that goes through them in order; it gives each back when it is done with it.
+    auto segment = [&](int k) {
+        if (!wait(seg_full(k), k / kSegs)) return false;
+        return segs_at[k % kSegs].b >= 0;
+    };
+    auto leave = [&](int k) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(seg_free(k));
+    };
 
     if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::FEW));
     if (warp == 0) {
         // ---------------------------------------------------------------- Q, K and V loads
         if (lane == 0) {
@@ -370,13 +399,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
         const uint32_t q_box = static_cast<uint32_t>(a.group * a.tpt) * 128u;
         int c = 0, slot = 0, kc = 0, vc = 0, segs = 0;    // loads, the next one's slot, K and V tiles, items
         uint32_t phase = 1;
-        bool ok = true;
-        auto wait = [&](uint32_t bar, uint32_t parity) {
-            ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity & 1u, flag));
-            return ok;
-        };
-        Seg g;
-        while (ok && walk.next(a, g)) {
+        for (int k = 0; ok && segment(k); ++k) {
+            const Seg g = segs_at[k % kSegs];
+            leave(k);
             const int n = g.steps();
             if (n == 0) continue;
             if (segs > 0 && !wait(q_free, segs - 1)) break;
@@ -429,18 +454,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
     } else if (warp == 1 || warp == 2) {
         // ---------------------------------------------------------------- MMA issue: S by warp 1, PV by warp 2
         const uint32_t one = elect_one();
-        bool issued = false, ok = true;
-        auto wait = [&](uint32_t bar, uint32_t parity) {
-            ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity & 1u, flag));
-            return ok;
-        };
+        bool issued = false;
         int c = 0, kv = 0, segs = 0;      // loads and K (or V) tiles of the items before this one; items
         int i[2] = {0, 0};                // products of each tile so far
-        Seg g;
         if (warp == 1) {
             constexpr uint32_t idS = idesc_f16(128, 128, false, false, BF);
             const uint64_t dq = smem_desc_sw128(base + L::OFF_Q, 16, 1024), dk = smem_desc_sw128(base + L::OFF_KV, 16, 1024);
-            while (ok && walk.next(a, g)) {
+            for (int k = 0; ok && segment(k); ++k) {
+                const Seg g = segs_at[k % kSegs];
+                leave(k);
                 const int n = g.steps();
                 if (n == 0) continue;
                 if (!wait(q_full, segs)) break;
@@ -472,7 +494,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
         } else {
             constexpr uint32_t idO = idesc_f16(128, D, false, true, BF);
             const uint64_t dp = smem_desc_sw128(base + L::OFF_P, 16, 1024), dv = smem_desc_sw128(base + L::OFF_KV, L::REGION, 1024);
-            while (ok && walk.next(a, g)) {
+            for (int k = 0; ok && segment(k); ++k) {
+                const Seg g = segs_at[k % kSegs];
+                leave(k);
                 const int n = g.steps();
                 for (int j = 0; ok && j < n; ++j) {
                     const int slot = (c + v_at(j, n)) % RING;
@@ -481,16 +505,19 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
 #pragma unroll
                     for (int t = 0; t < TILES; ++t) {
                         if (j >= (t == 0 ? g.n0 : g.n1)) continue;
-                        if (!wait(p_full(t), i[t])) break;
-                        ++i[t];
-                        tc_fence_after();
                         const uint64_t pd = dp + static_cast<uint64_t>(t * (L::P_BYTES >> 4));
 #pragma unroll
-                        for (int s = 0; s < 8; ++s)   // 16 keys each
-                            tc_mma_if(one, tmem + L::O_COL + t * D, pd + ((s / 4) * (L::REGION >> 4) + (s % 4) * 2), vd + s * (2048 >> 4), idO,
-                                      j > 0 || s > 0 ? 1u : 0u);
-                        tc_commit_if(one, o_done(t));
-                        issued = true;
+                        for (int h = 0; h < 2; ++h) {
+                            if (!wait(p_full(t, h), i[t])) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int s = 4 * h; s < 4 * h + 4; ++s)   // 16 keys each
+                                tc_mma_if(one, tmem + L::O_COL + t * D, pd + ((s / 4) * (L::REGION >> 4) + (s % 4) * 2), vd + s * (2048 >> 4), idO,
+                                          j > 0 || s > 0 ? 1u : 0u);
+                            tc_commit_if(one, o_done(t, h));
+                            issued = true;
+                        }
+                        ++i[t];
                     }
                     if (ok) tc_commit_if(one, empty(slot));
                 }
@@ -503,166 +530,219 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
             (void)mbar_wait_drain(drain(warp - 1), 0);
         }
         __syncwarp();
+    } else {
+        // ---------------------------------------------------------------- the walk along the run, ahead of the others
+        Walk walk;
+        walk.begin(a, run[0], run[1]);
+        Seg g;
+        for (int k = 0;; ++k) {
+            const bool more = walk.next(a, g);
+            if (!more) g.b = -1;
+            if (k >= kSegs && !wait(seg_free(k), k / kSegs - 1)) break;
+            if (lane == 0) {
+                segs_at[k % kSegs] = g;
+                mbar_arrive(seg_full(k));
+            }
+            __syncwarp();
+            if (!more) break;
+        }
     }
     } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
-    if (warp < 4 + 4 * TILES) {
-        // ---------------------------------------------------------------- softmax: thread r of tile t, one row
-        const int t = (warp - 4) / 4, r = 32 * (warp % 4) + lane;
-        const uint32_t lanes = static_cast<uint32_t>(32 * (warp % 4)) << 16;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::MANY));
+        // ---------------------------------------------------------------- softmax: threads l and l + 16 of a warp, one row
+        const int t = (warp - 4) / kTileWarps, u = (warp - 4) % kTileWarps, r0 = 32 * (warp % 4) + 16 * (u / 4), r = r0 + lane % 16, hf = lane / 16;
+        const uint32_t lanes = static_cast<uint32_t>(r0) << 16;
         const uint32_t st = tmem + lanes + t * 128, ot = tmem + lanes + L::O_COL + t * D;
+        const bool stores = u == 0 && lane == 0;      // the thread that stores the tile's output
+        // where the thread's weights go: chunk q of 16 bytes at this address with q 16 exchanged (128B swizzle)
+        const uint32_t p_at = base + L::OFF_P + t * L::P_BYTES + r * 128 + (((4 * hf) ^ (r & 7)) << 4);
         constexpr float SH = Shift<T>::V;
-        bool ok = true;
-        auto wait = [&](uint32_t bar, uint32_t parity) {
-            ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity & 1u, flag));
-            return ok;
-        };
-        int i = 0, c = 0, kv = 0;
-        WarpWalk& w = *reinterpret_cast<WarpWalk*>(gbase + L::OFF_WALK + (warp - 4) * sizeof(WarpWalk));
-        const Seg& g = w.seg;
-        if (lane == 0) w.walk = walk;
-        auto next = [&]() {
-            bool more = false;
-            if (lane == 0) {
-                Walk mine = w.walk;
-                Seg s;
-                more = mine.next(a, s);
-                w.walk = mine;
-                w.seg = s;
+        int i = 0, kv = 0, outs = 0;                  // steps of this tile; K (or V) tiles; outputs that P has held
+        bool held = false;                            // P holds an output that is being stored
+        // P may be written: what it held has been taken.
+        auto p_ready = [&]() {
+            if (!held) return true;
+            held = false;
+            if (stores) {
+                bulk_wait_read0();
+                mbar_arrive(out_free(t));
             }
-            return __shfl_sync(0xffffffffu, more, 0) != 0;
+            return wait(out_free(t), outs - 1);
         };
-        while (ok && next()) {
-            __syncwarp();
+        for (int k = 0; ok && segment(k); ++k) {
+            const Seg& g = segs_at[k % kSegs];       // (stays in shared memory: in registers, next to a row's scores, it spills)
             const int n = t == 0 ? g.n0 : g.n1;
-            int left, kleft;         // keys from the block on: those that this row sees, those of the sequence
-            {
-                const int rt = r / a.group;
-                kleft = g.L - g.t0 * 128;
-                left = kleft - g.n + g.tok0 + t * a.tpt + rt + 1;
-            }
+            // keys that this row sees, from its thread's first of the block on
+            int left = g.L - g.t0 * 128 - g.n + g.tok0 + t * a.tpt + (r * a.recip >> 16) + 1 - 32 * hf;
             float m = -INFINITY, l = 0.0f;
-            for (int j = 0; j < n; ++j, ++i, left -= 128, kleft -= 128) {
+            for (int j = 0; j < n; ++j, ++i, left -= 128) {
                 if (!wait(s_full(t), i)) break;
                 tc_fence_after();
-                float x[128];
+                // 64 keys at a time, so that the weights of the first half are multiplied with V while those of the second are
+                // computed, and half of P is free as soon as the last block's half has been multiplied.
 #pragma unroll
-                for (int k = 0; k < 4; ++k) tmem_ld32(st + 32 * k, x + 32 * k);
-                tmem_ld_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(s_free(t));
-                if (__any_sync(0xffffffffu, left < 128)) {
-#pragma unroll
-                    for (int k = 0; k < 128; ++k) x[k] = k >= left ? -INFINITY : x[k];
-                }
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int k = 0; k < 128; k += 2) mx[(k >> 1) & 3] = max3f(mx[(k >> 1) & 3], x[k], x[k + 1]);
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.c;
-                float alpha = 1.0f;
-                bool rescale = false;
-                if (top > m + (SH + kLag)) {
-                    if (j > 0) {
-                        alpha = ex2f(m - (top - SH));
-                        rescale = true;
+                for (int h = 0; h < 2; ++h) {
+                    float x[32];         // keys 64 h + 32 hf .. of the block
+                    tmem_ld_rows16(st + 64 * h, x);
+                    tmem_ld_wait();
+                    if (h == 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(s_free(t));
                     }
-                    m = top - SH;
-                }
-                // P and O are free once the previous PV has completed
-                if (i > 0 && !wait(o_done(t), i - 1)) break;
-                const float ref = m == -INFINITY ? 0.0f : m;
-                const float2 c2 = make_float2(a.c, a.c), nm2 = make_float2(-ref, -ref);
-                float2 sum2 = make_float2(0.0f, 0.0f);
-                uint8_t* prow = gbase + L::OFF_P + t * L::P_BYTES + r * 128;
+                    if (__any_sync(0xffffffffu, left - 64 * h < 32)) {
 #pragma unroll
-                for (int q = 0; q < 16; ++q) {
-                    // The weights rounded to T, as the tensor core takes both operands of a product in one type.  Each is
-                    // off by at most half a step of T, as the output's own rounding is.
-                    uint32_t w[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float2 e = __ffma2_rn(make_float2(x[8 * q + 2 * k], x[8 * q + 2 * k + 1]), c2, nm2);
-                        const float2 p = make_float2(ex2f(e.x), ex2f(e.y));
-                        sum2 = __fadd2_rn(sum2, p);
-                        w[k] = pack2<T>(p.x, p.y);
+                        for (int y = 0; y < 32; ++y) x[y] = y >= left - 64 * h ? -INFINITY : x[y];
                     }
-                    *reinterpret_cast<uint4*>(prow + (q / 8) * L::REGION + (((q % 8) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-                l = l * alpha + (sum2.x + sum2.y);
-                if (__any_sync(0xffffffffu, rescale)) {
-                    tc_fence_after();
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int y = 0; y < 32; y += 2) mx[(y >> 1) & 3] = max3f(mx[(y >> 1) & 3], x[y], x[y + 1]);
+                    float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.c;
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                    float alpha = 1.0f;
+                    if (top > m + (SH + kLag)) {
+                        if (j > 0 || h > 0) alpha = ex2f(m - (top - SH));     // (0 from -inf)
+                        m = top - SH;
+                    }
+                    if (h == 0 && j == 0 && !p_ready()) break;
+                    if (i > 0 && !wait(o_done(t, h), i - 1)) break;
+                    const float ref = m == -INFINITY ? 0.0f : m;
+                    const float2 c2 = make_float2(a.c, a.c), nm2 = make_float2(-ref, -ref);
+                    float2 sum2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        // Rounded to T, as the tensor core takes both operands of a product in one type.  Each is off by at most
+                        // half a step of T, as the output's own rounding is.
+                        uint32_t w[4];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const float2 e = __ffma2_rn(make_float2(x[8 * q + 2 * y], x[8 * q + 2 * y + 1]), c2, nm2);
+                            const float2 p = make_float2(ex2f(e.x), ex2f(e.y));
+                            sum2 = __fadd2_rn(sum2, p);
+                            w[y] = pack2<T>(p.x, p.y);
+                        }
+                        st_shared_v4((p_at ^ (q << 4)) + h * L::REGION, w);
+                    }
+                    if (__any_sync(0xffffffffu, alpha != 1.0f)) {      // rare: what has been issued of this tile's PV is waited for
+                        if (!(h == 0 ? wait(o_done(t, 1), i - 1) : wait(o_done(t, 0), i))) break;
+                        tc_fence_after();
 #pragma unroll 1
-                    for (int k = 0; k < D / 32; ++k) {
-                        float o[32];
-                        tmem_ld32(ot + 32 * k, o);
-                        tmem_ld_wait();
+                        for (int y = 0; y < D / 64; ++y) {
+                            float o[32];
+                            tmem_ld_rows16(ot + 64 * y, o);
+                            tmem_ld_wait();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] *= alpha;
-                        tmem_st32(ot + 32 * k, o);
+                            for (int e = 0; e < 32; ++e) o[e] *= alpha;
+                            tmem_st_rows16(ot + 64 * y, o);
+                        }
+                        tmem_st_wait();
                     }
-                    tmem_st_wait();
-                }
-                // V rows past the sequence's end: 0 x whatever lies there must be 0.  By the tile whose product with this
-                // block is issued first.
-                if (kleft < 128 && (t == 0 || j >= g.n0)) {
-                    const int vi = kv + j;
-                    if (!wait(v_full(vi % kFull), vi / kFull)) break;
-                    uint8_t* vb = gbase + L::OFF_KV + ((c + v_at(j, g.steps())) % RING) * L::TILE;
-                    for (int v = r; v < (128 - kleft) * (D / 8); v += 128) {
-                        const int row = kleft + v / (D / 8), ch = v % (D / 8);
-                        *reinterpret_cast<uint4*>(vb + (ch / 8) * L::REGION + row * 128 + (ch % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    l = l * alpha + (sum2.x + sum2.y);
+                    if (h == 0) {
+                        // V rows past the sequence's end: 0 x whatever lies there must be 0.  By the tile whose product with
+                        // this block is issued first.
+                        const int kleft = g.L - (g.t0 + j) * 128;
+                        if (kleft < 128 && (t == 0 || j >= g.n0)) {
+                            const int vi = kv + j;
+                            if (!wait(v_full(vi % kFull), vi / kFull)) break;
+                            uint8_t* vb = gbase + L::OFF_KV + ((2 * kv + v_at(j, g.steps())) % RING) * L::TILE;
+                            for (int v = 32 * u + lane; v < (128 - kleft) * (D / 8); v += 32 * kTileWarps) {
+                                const int row = kleft + v / (D / 8), ch = v % (D / 8);
+                                *reinterpret_cast<uint4*>(vb + (ch / 8) * L::REGION + row * 128 + (ch % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                            }
+                        }
                     }
+                    fence_async_smem();      // the generic-proxy writes become visible to the tensor core
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(p_full(t, h));
                 }
-                fence_async_smem();      // the generic-proxy writes become visible to the tensor core
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(p_full(t));
+                if (!ok) break;
             }
-            c += 2 * g.steps();
             kv += g.steps();
-            if (!ok || (n > 0 && !wait(o_done(t), i - 1))) break;
+            if (!ok || (n > 0 && !wait(o_done(t, 1), i - 1))) break;
             tc_fence_after();
-            const int rt = r / a.group, head = r - rt * a.group, tok = g.tok0 + t * a.tpt + rt;
-            const bool in = rt < a.tpt && tok < g.n;
+            l += __shfl_xor_sync(0xffffffffu, l, 16);
+            // Opaque copies: what depends on them is computed here, not kept in registers next to the scores (which spills).
+            int er = r, eh = hf, el = lane, et = t;
+            asm volatile("" : "+r"(er), "+r"(eh), "+r"(el), "+r"(et));
+            const int tok0 = g.tok0 + et * a.tpt;
             if (g.whole) {
+                // Through P, which is free: a whole tile is stored from there by one copy while the warps go on; of one that ends
+                // within the sequence each warp stores its rows, LANES lanes to a row.
                 const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
-                T* dst = static_cast<T*>(a.o) + (static_cast<int64_t>(g.q0 + tok) * a.hq + g.h * a.group + head) * D;
+                uint8_t* mine = gbase + L::OFF_P + et * L::P_BYTES;
+                constexpr int W = D < 128 ? D : 128, LANES = W / 8;      // columns at a time, lanes of a row
+                const bool full = tok0 + a.tpt <= g.n;
 #pragma unroll 1
-                for (int k = 0; k < D / 32; ++k) {
-                    float o[32];
-                    uint32_t w[16];
-                    if (n > 0) {
-                        tmem_ld32(ot + 32 * k, o);
-                        tmem_ld_wait();
+                for (int w0 = 0; w0 < D && tok0 < g.n; w0 += W) {
+                    if (!p_ready()) break;
+#pragma unroll
+                    for (int x = 0; x < W / 64; ++x) {
+                        float o[32];
+                        if (n > 0) {
+                            tmem_ld_rows16(ot + w0 + 64 * x, o);
+                            tmem_ld_wait();
+                        }
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t v[4];
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) v[y] = n == 0 || l == 0.0f ? 0u : pack2<T>(o[8 * q + 2 * y] * inv, o[8 * q + 2 * y + 1] * inv);
+                            *reinterpret_cast<uint4*>(mine + x * L::REGION + er * 128 + (((4 * eh + q) ^ (er & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+                        }
                     }
+                    if (full) {
+                        fence_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(out_full(t));
+                        if (u == 0) {
+                            if (!wait(out_full(t), outs)) break;
+                            if (lane == 0) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) w[e] = n == 0 || l == 0.0f ? 0u : pack2<T>(o[2 * e] * inv, o[2 * e + 1] * inv);
-                    if (in) {
+                                for (int x = 0; x < W / 64; ++x)
+                                    tma_store_3d(&mO, w0 + 64 * x, g.h * a.group, g.q0 + tok0, base + L::OFF_P + et * L::P_BYTES + x * L::REGION);
+                                bulk_commit();
+                            }
+                            __syncwarp();
+                        }
+                        held = true;
+                        ++outs;
+                    } else {
+                        __syncwarp();
+                        const int ch = el % LANES;
+                        T* out = static_cast<T*>(a.o) + (static_cast<int64_t>(g.q0 + tok0) * a.hq + g.h * a.group) * D + w0 + 8 * ch;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            *reinterpret_cast<uint4*>(dst + 32 * k + 8 * e) = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+                        for (int x = 0; x < LANES / 2; ++x) {
+                            const int row = er / 16 * 16 + x * (32 / LANES) + el / LANES, rt = row * a.recip >> 16;
+                            if (rt < a.tpt && tok0 + rt < g.n)
+                                *reinterpret_cast<uint4*>(out + (static_cast<int64_t>(rt) * a.hq + row - rt * a.group) * D) =
+                                    *reinterpret_cast<const uint4*>(mine + (ch / 8) * L::REGION + row * 128 + (((ch % 8) ^ (row & 7)) << 4));
+                        }
+                        __syncwarp();
                     }
                 }
             } else {
-                const int64_t at = static_cast<int64_t>(2 * blockIdx.x + (g.t0 == 0 ? 1 : 0)) * a.rows + t * 128 + r;
-                if (in) a.ml[at] = make_float2(m, l);
-                float* dst = a.po + at * D;
+                const int rt = er * a.recip >> 16, tok = tok0 + rt;
+                const bool in = rt < a.tpt && tok < g.n;
+                const int64_t at = static_cast<int64_t>(2 * blockIdx.x + (g.t0 == 0 ? 1 : 0)) * a.rows + et * 128 + er;
+                if (in && eh == 0) a.ml[at] = make_float2(m, l);
+                float* dst = a.po + at * D + 32 * eh;
                 if (n > 0)
 #pragma unroll 1
-                    for (int k = 0; k < D / 32; ++k) {
+                    for (int y = 0; y < D / 64; ++y) {
                         float o[32];
-                        tmem_ld32(ot + 32 * k, o);
+                        tmem_ld_rows16(ot + 64 * y, o);
                         tmem_ld_wait();
                         if (in)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) st_v8(dst + 32 * k + 8 * e, o + 8 * e);
+                            for (int e = 0; e < 4; ++e) st_v8(dst + 64 * y + 8 * e, o + 8 * e);
                     }
             }
             tc_fence_before();
-            __syncwarp();
+            leave(k);
         }
-    }
+        if (stores) bulk_wait0();      // shared memory goes away
     }
     tc_fence_before();
     __syncthreads();
@@ -673,12 +753,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
 }
 
 // ================================================================== join
-// The parts of an item that several CTAs share, one warp per row; blockIdx.y names the CTA whose run begins first within
-// the item.  Lane c takes D / 32 columns.
-constexpr int kJoinThreads = 128;
+// The parts of an item that several CTAs share; blockIdx.y names the CTA whose run begins first within the item.  A warp
+// takes a row at a time, lane c D / 32 columns of it.  It is bound by latency: the parts' outputs are loaded next to their
+// maxima and sums, several at a time.
+constexpr int kJoinThreads = 256, kJoinRows = 32;      // rows of a block
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const __grid_constant__ PromptArgs a, int grid) {
-    constexpr int W = D / 32;
+    constexpr int W = D / 32, AHEAD = D == 256 ? 4 : 8;
+    __shared__ int slots[kGrid + 1];
+    __shared__ int count;
     pdl_begin();
     const int c0 = blockIdx.y + 1;                 // run c0 begins within an item
     auto start = [&](int c) {
@@ -686,48 +769,80 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const __grid_
         return Pos{v.x, v.y, v.z, v.w};
     };
     auto same = [](const Pos& x, const Pos& y) { return x.b == y.b && x.h == y.h && x.i == y.i; };
-    const Pos p = start(c0);
-    if (p.t == 0 || p.b >= a.batch) return;
-    const Pos q = start(c0 - 1);
-    if (same(p, q) && q.t > 0) return;             // not the first
-    const int row = blockIdx.x * (kJoinThreads / 32) + threadIdx.x / 32, lane = threadIdx.x % 32;
+    const Pos p = start(c0), q = start(c0 - 1);
+    if (p.t == 0 || p.b >= a.batch || (same(p, q) && q.t > 0)) return;      // (or not the first)
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const Seq s = seq_of(a, p.b);
-    const int r = row % 128, rt = r / a.group, tok = (p.i * a.tiles + row / 128) * a.tpt + rt;
-    if (row >= a.rows || rt >= a.tpt || tok >= s.n) return;
-    float m = -INFINITY, l = 0.0f, acc[W] = {};
-    // part 0 is CTA c0 - 1's; then that of each run that begins within the item and has something of it
-    Pos at = p;
-    for (int c = c0 - 1;; ++c) {
-        bool has = true;
-        if (c >= c0) {
-            const Pos next = start(c + 1);
-            has = at.before(next);
-            at = next;
+    if (warp == 0) {
+        // part 0 is CTA c0 - 1's; then that of each run that begins within the item and has something of it
+        if (lane == 0) slots[0] = 2 * (c0 - 1) + 1;
+        int n = 1;
+        for (int c = c0;; c += 32) {
+            const Pos x = start(min(c + lane, grid)), y = start(min(c + lane + 1, grid));
+            const bool in = c + lane < grid && same(x, p) && x.t > 0, has = in && x.before(y);
+            const uint32_t mask = __ballot_sync(0xffffffffu, has);
+            if (has) slots[n + __popc(mask & ((1u << lane) - 1u))] = 2 * (c + lane);
+            n += __popc(mask);
+            if (!__all_sync(0xffffffffu, in)) break;
         }
-        if (has) {
-            const int64_t slot = static_cast<int64_t>(2 * c + (c < c0 ? 1 : 0)) * a.rows + row;
-            const float2 x = __ldcg(a.ml + slot);
-            if (x.x > -INFINITY || x.y != 0.0f) {        // (a part that this row sees nothing of has no output)
-                const float nm = fmaxf(m, x.x), e0 = m == -INFINITY ? 0.0f : ex2f(m - nm), e1 = ex2f(x.x - nm);
-                const float* src = a.po + slot * D + W * lane;
-                l = l * e0 + x.y * e1;
+        if (lane == 0) count = n;
+    }
+    __syncthreads();
+    const int parts = count;
+    for (int row = blockIdx.x * kJoinRows + warp; row < min(a.rows, static_cast<int>(blockIdx.x + 1) * kJoinRows); row += kJoinThreads / 32) {
+        const int r = row % 128, rt = r * a.recip >> 16, tok = (p.i * a.tiles + row / 128) * a.tpt + rt;
+        if (rt >= a.tpt || tok >= s.n) continue;
+        auto load = [&](float (&v)[W], int part) {
+            const float* src = a.po + (static_cast<int64_t>(slots[part]) * a.rows + row) * D + W * lane;
 #pragma unroll
-                for (int e = 0; e < W; e += 2) {
-                    const float2 v = __ldcg(reinterpret_cast<const float2*>(src + e));
-                    acc[e] = acc[e] * e0 + v.x * e1;
-                    acc[e + 1] = acc[e + 1] * e0 + v.y * e1;
+            for (int e = 0; e < W; e += 2) {
+                const float2 x = __ldcg(reinterpret_cast<const float2*>(src + e));
+                v[e] = x.x;
+                v[e + 1] = x.y;
+            }
+        };
+        float m = -INFINITY, l = 0.0f, acc[W] = {};
+        for (int p0 = 0; p0 < parts; p0 += 32) {
+            float v[AHEAD][W];
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i)
+                if (p0 + i < parts) load(v[i], p0 + i);
+            // lane i has part p0 + i's reference and sum
+            float2 x = make_float2(-INFINITY, 0.0f);
+            if (p0 + lane < parts) x = __ldcg(a.ml + static_cast<int64_t>(slots[p0 + lane]) * a.rows + row);
+            float top = fmaxf(m, x.x);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            // (a part that this row sees nothing of has no output; its weight is 0)
+            const bool none = x.x == -INFINITY && x.y == 0.0f;
+            const float e = none ? 0.0f : ex2f(x.x - top), e0 = m == -INFINITY ? 0.0f : ex2f(m - top);
+            float sum = none ? 0.0f : x.y * e;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            l = l * e0 + sum;
+            m = top;
+            const uint32_t with = __ballot_sync(0xffffffffu, !none);
+#pragma unroll
+            for (int y = 0; y < W; ++y) acc[y] *= e0;
+            for (int b = 0; b < 32 && p0 + b < parts; b += AHEAD) {
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) {
+                    const float w = __shfl_sync(0xffffffffu, e, b + i);
+                    if (with >> (b + i) & 1u)
+#pragma unroll
+                        for (int y = 0; y < W; ++y) acc[y] += w * v[i][y];
                 }
-                m = nm;
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i)
+                    if (b + AHEAD + i < 32 && p0 + b + AHEAD + i < parts) load(v[i], p0 + b + AHEAD + i);
             }
         }
-        if (c >= c0 && !(same(at, p) && at.t > 0)) break;
-        if (c + 1 >= grid) break;
-    }
-    const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
-    T* dst = static_cast<T*>(a.o) + (static_cast<int64_t>(s.q0 + tok) * a.hq + p.h * a.group + r % a.group) * D + W * lane;
+        const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
+        T* dst = static_cast<T*>(a.o) + (static_cast<int64_t>(s.q0 + tok) * a.hq + p.h * a.group + r - rt * a.group) * D + W * lane;
 #pragma unroll
-    for (int e = 0; e < W; e += 2)
-        *reinterpret_cast<uint32_t*>(dst + e) = l == 0.0f ? 0u : pack2<T>(acc[e] * inv, acc[e + 1] * inv);
+        for (int e = 0; e < W; e += 2)
+            *reinterpret_cast<uint32_t*>(dst + e) = l == 0.0f ? 0u : pack2<T>(acc[e] * inv, acc[e + 1] * inv);
+    }
 }
 
 // ================================================================== host side
@@ -757,11 +872,11 @@ int run_prompt(PromptArgs a, const void* q, int64_t q_ld, const void* k, const v
     using L = Layout<D>;
     const bool bf = std::is_same<T, __nv_bfloat16>::value;
     const int box = 1 << (a.page_shift < 7 ? a.page_shift : 7);
-    CUtensorMap mQ, mK, mV;
-    const int64_t dims[3] = {D, a.hq, a.tokens}, strides[2] = {D * 2, q_ld * 2};
+    CUtensorMap mQ, mK, mV, mO;
+    const int64_t dims[3] = {D, a.hq, a.tokens}, strides[2] = {D * 2, q_ld * 2}, o_strides[2] = {D * 2, static_cast<int64_t>(a.hq) * D * 2};
     const int qbox[3] = {64, a.group, a.tpt};
     if (!make_map(&mK, k, a.cache_rows, D, 64, box, bf) || !make_map(&mV, v, a.cache_rows, D, 64, box, bf) ||
-        !make_map_3d(&mQ, q, kMap16, dims, strides, qbox, 128))
+        !make_map_3d(&mQ, q, kMap16, dims, strides, qbox, 128) || !make_map_3d(&mO, a.o, kMap16, dims, o_strides, qbox, 128))
         return FUSE_ECUDA;
     int rc = opt_in_smem((const void*)prompt_attention_kernel<T, D>, L::SMEM);
     if (rc != FUSE_OK) return rc;
@@ -771,10 +886,10 @@ int run_prompt(PromptArgs a, const void* q, int64_t q_ld, const void* k, const v
     int64_t grid = sm_count() < kGrid ? sm_count() : kGrid;
     const int64_t runs = items * ceil_div(room + kEntry, kLeastRun);
     if (grid > runs) grid = runs;
-    rc = launch_pdl(prompt_attention_kernel<T, D>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), L::SMEM, st, 1, mQ, mK, mV, a);
+    rc = launch_pdl(prompt_attention_kernel<T, D>, dim3(static_cast<unsigned>(grid)), dim3(L::THREADS), L::SMEM, st, 1, mQ, mK, mV, mO, a);
     // an item of at most one block of keys is nobody's to share
     if (rc != FUSE_OK || grid == 1 || room <= 128) return rc;
-    return launch_pdl(prompt_join_kernel<T, D>, dim3(static_cast<unsigned>(ceil_div(a.rows, kJoinThreads / 32)), static_cast<unsigned>(grid - 1)),
+    return launch_pdl(prompt_join_kernel<T, D>, dim3(static_cast<unsigned>(ceil_div(a.rows, kJoinRows)), static_cast<unsigned>(grid - 1)),
                       dim3(kJoinThreads), 0, st, 1, a, static_cast<int>(grid));
 }
 
@@ -783,12 +898,12 @@ int run_prompt(PromptArgs a, const void* q, int64_t q_ld, const void* k, const v
 int prompt_report_count() { return 12; }
 int prompt_report(int i, fuse_kernel_record* out) {
     switch (i) {
-        FC_REPORT(0, kThreads, Layout<64>::SMEM, 512, prompt_attention_kernel<__nv_bfloat16, 64>);
-        FC_REPORT(1, kThreads, Layout<128>::SMEM, 512, prompt_attention_kernel<__nv_bfloat16, 128>);
-        FC_REPORT(2, kThreads, Layout<256>::SMEM, 512, prompt_attention_kernel<__nv_bfloat16, 256>);
-        FC_REPORT(3, kThreads, Layout<64>::SMEM, 512, prompt_attention_kernel<__half, 64>);
-        FC_REPORT(4, kThreads, Layout<128>::SMEM, 512, prompt_attention_kernel<__half, 128>);
-        FC_REPORT(5, kThreads, Layout<256>::SMEM, 512, prompt_attention_kernel<__half, 256>);
+        FC_REPORT(0, Layout<64>::THREADS, Layout<64>::SMEM, 512, prompt_attention_kernel<__nv_bfloat16, 64>);
+        FC_REPORT(1, Layout<128>::THREADS, Layout<128>::SMEM, 512, prompt_attention_kernel<__nv_bfloat16, 128>);
+        FC_REPORT(2, Layout<256>::THREADS, Layout<256>::SMEM, 512, prompt_attention_kernel<__nv_bfloat16, 256>);
+        FC_REPORT(3, Layout<64>::THREADS, Layout<64>::SMEM, 512, prompt_attention_kernel<__half, 64>);
+        FC_REPORT(4, Layout<128>::THREADS, Layout<128>::SMEM, 512, prompt_attention_kernel<__half, 128>);
+        FC_REPORT(5, Layout<256>::THREADS, Layout<256>::SMEM, 512, prompt_attention_kernel<__half, 256>);
         FC_REPORT(6, kJoinThreads, 0, 0, prompt_join_kernel<__nv_bfloat16, 64>);
         FC_REPORT(7, kJoinThreads, 0, 0, prompt_join_kernel<__nv_bfloat16, 128>);
         FC_REPORT(8, kJoinThreads, 0, 0, prompt_join_kernel<__nv_bfloat16, 256>);
@@ -849,6 +964,7 @@ extern "C" int fuse_prompt_attention(const void* q, int64_t q_ld, const void* k_
     a.hq = static_cast<int>(q_heads);
     a.hk = static_cast<int>(kv_heads);
     a.group = static_cast<int>(group);
+    a.recip = static_cast<int>((65536 + group - 1) / group);
     a.tpt = static_cast<int>(128 / group);
     a.tiles = D <= 128 ? 2 : 1;
     while ((1 << a.page_shift) < page_size) ++a.page_shift;
