@@ -54,8 +54,45 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
     return y;
 }
-// Is (a, ia) a better alternative than (b, ib)?
-__device__ __forceinline__ bool better(float a, int ia, float b, int ib) { return a > b || (a == b && ia < ib); }
+// An alternative as one number: the larger logit, of equal ones the lower index, has the larger.  0 is none (a logit above
+// -inf has a larger one).
+__device__ __forceinline__ uint64_t key_of(float x, int i) {
+    const uint32_t b = __float_as_uint(x + 0.0f);        // (zeros of both signs are equal)
+    return static_cast<uint64_t>(b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u)) << 32 | (0xffffffffu - static_cast<uint32_t>(i));
+}
+__device__ __forceinline__ float logit_of(uint64_t k) {
+    const uint32_t b = static_cast<uint32_t>(k >> 32);
+    return __uint_as_float(b ^ ((b >> 31) ? 0x80000000u : 0xffffffffu));
+}
+__device__ __forceinline__ int index_of(uint64_t k) { return static_cast<int>(0xffffffffu - static_cast<uint32_t>(k)); }
+__device__ __forceinline__ uint64_t shfl_xor_u64(uint64_t v, int o) { return __shfl_xor_sync(0xffffffffu, v, o); }
+// One comparison step of a bitonic network over the warp: the larger value goes to the lane with (lane & o) == 0 where `down`,
+// else to the other.
+__device__ __forceinline__ float exchange(float v, int o, bool down) {
+    const float u = __shfl_xor_sync(0xffffffffu, v, o);
+    return (((threadIdx.x & o) == 0) == down) ? fmaxf(v, u) : fminf(v, u);
+}
+__device__ __forceinline__ uint64_t exchange(uint64_t v, int o, bool down) {
+    const uint64_t u = shfl_xor_u64(v, o);
+    return ((((threadIdx.x & o) == 0) == down) == (v > u)) ? v : u;
+}
+// Sorted over the warp, largest first.
+template <typename V>
+__device__ __forceinline__ V sort_down(V v) {
+#pragma unroll
+    for (int k = 2; k <= 32; k <<= 1)
+#pragma unroll
+        for (int j = k >> 1; j > 0; j >>= 1) v = exchange(v, j, (threadIdx.x & 31 & k) == 0);
+    return v;
+}
+// The 32 largest of two sorted lists, `other` given back to front.
+template <typename V>
+__device__ __forceinline__ V merge_down(V v, V other) {
+    v = v > other ? v : other;
+#pragma unroll
+    for (int j = 16; j > 0; j >>= 1) v = exchange(v, j, true);
+    return v;
+}
 
 // Largest of a 16-byte vector's values (NaN left out).
 template <typename T> __device__ __forceinline__ float vec_max(const uint4& r);
@@ -79,12 +116,9 @@ struct Shared {
     float part[3];                          // this CTA's (m, S, T)
     int flagged, cands;
     int list[kThreads];
-    float cv[kCand];
-    int ci[kCand];
-    float tv[kMaxTop];                      // this CTA's alternatives, best first
-    int ti[kMaxTop];
-    float rv[kWarps];                       // one scan's best, by warp
-    int ri[kWarps];
+    uint64_t cand[kCand];
+    uint64_t best[kMaxTop];                 // this CTA's alternatives, best first, then 0
+    uint64_t scan[kWarps];                  // one scan's best, by warp
 };
 
 // The part of a row that one CTA reads: vectors v0 .. v0 + nv - 1 of the aligned middle, and, in the cluster's
@@ -116,57 +150,29 @@ __device__ __forceinline__ void for_each(const Slice<T>& s, F&& f) {
     }
 }
 
-// The slice's alternatives in sh.tv, sh.ti by one scan for each: the best that comes after the one before.
-// Logits of -inf (and NaN, which counts as -inf) are left out.  Returns how many there are.
+// The slice's alternatives in sh.best by one scan for each: the best that comes after the one before.  Logits of -inf (and
+// NaN, which counts as -inf) are left out.
 template <typename T>
-__device__ __noinline__ int scan_top(Shared& sh, const Slice<T>& s, int top) {
-    float lv = INFINITY;
-    int li = -1, n = 0;
-    for (; n < top; ++n) {
-        float bv = -INFINITY;
-        int bi = 0x7fffffff;
+__device__ __noinline__ void scan_top(Shared& sh, const Slice<T>& s, int top) {
+    uint64_t last = ~uint64_t(0);
+    for (int n = 0; n < top; ++n) {
+        uint64_t best = 0;
         for_each<T>(s, [&](float x, int i) {
-            if (x > -INFINITY && better(lv, li, x, i) && better(x, i, bv, bi)) {
-                bv = x;
-                bi = i;
-            }
+            const uint64_t k = key_of(x, i);
+            if (x > -INFINITY && k < last && k > best) best = k;
         });
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
-            const float v = __shfl_xor_sync(0xffffffffu, bv, o);
-            const int i = __shfl_xor_sync(0xffffffffu, bi, o);
-            if (better(v, i, bv, bi)) {
-                bv = v;
-                bi = i;
-            }
+            const uint64_t k = shfl_xor_u64(best, o);
+            best = k > best ? k : best;
         }
         __syncthreads();
-        if (threadIdx.x % 32 == 0) {
-            sh.rv[threadIdx.x / 32] = bv;
-            sh.ri[threadIdx.x / 32] = bi;
-        }
+        if (threadIdx.x % 32 == 0) sh.scan[threadIdx.x / 32] = best;
         __syncthreads();
-        for (int w = 0; w < kWarps; ++w)
-            if (better(sh.rv[w], sh.ri[w], bv, bi)) {
-                bv = sh.rv[w];
-                bi = sh.ri[w];
-            }
-        if (bi == 0x7fffffff) break;
-        if (threadIdx.x == 0) {
-            sh.tv[n] = bv;
-            sh.ti[n] = bi;
-        }
-        lv = bv;
-        li = bi;
+        for (int w = 0; w < kWarps; ++w) best = sh.scan[w] > best ? sh.scan[w] : best;
+        if (threadIdx.x == 0) sh.best[n] = best;
+        last = best;              // (0: none is left, and none will be found)
     }
-    return n;
-}
-
-// One comparison step of a bitonic network over the warp: the larger value goes to the lane with (lane & o) == 0 where
-// `down`, else to the other.
-__device__ __forceinline__ float exchange(float v, int o, bool down) {
-    const float u = __shfl_xor_sync(0xffffffffu, v, o);
-    return (((threadIdx.x & o) == 0) == down) ? fmaxf(v, u) : fminf(v, u);
 }
 
 template <typename T>
@@ -245,23 +251,22 @@ __global__ void __launch_bounds__(kThreads, 6) token_logprobs_kernel(const __gri
     }
 
     // ---------------------------------------------------------------- the CTA's sums, and the bound
-    float o = m;
+    if (a.top > 0) {
+        sh.sorted[warp][lane] = sort_down(m);
+    } else {
+        float o = m;
 #pragma unroll
-    for (int k = 2; k <= 32; k <<= 1)
-#pragma unroll
-        for (int j = k >> 1; j > 0; j >>= 1) o = exchange(o, j, (lane & k) == 0);
-    sh.sorted[warp][lane] = o;
+        for (int k = 16; k > 0; k >>= 1) o = fmaxf(o, __shfl_xor_sync(0xffffffffu, o, k));
+        if (lane == 0) sh.sorted[warp][0] = o;
+    }
     __syncthreads();
     float M = sh.sorted[0][0];
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) M = fmaxf(M, sh.sorted[w][0]);
     if (warp == 0 && a.top > 0) {
         float best = sh.sorted[0][lane];
-        for (int w = 1; w < kWarps; ++w) {
-            best = fmaxf(best, sh.sorted[w][31 - lane]);
 #pragma unroll
-            for (int j = 16; j > 0; j >>= 1) best = exchange(best, j, true);
-        }
+        for (int w = 1; w < kWarps; ++w) best = merge_down(best, sh.sorted[w][31 - lane]);
         if (lane == a.top - 1) sh.bound = best;
     }
     const bool some = m > -INFINITY;
@@ -297,10 +302,7 @@ __global__ void __launch_bounds__(kThreads, 6) token_logprobs_kernel(const __gri
         auto take = [&](float x, int i) {
             if (x >= bound && x > -INFINITY) {
                 const int at = atomicAdd(&sh.cands, 1);
-                if (at < kCand) {
-                    sh.cv[at] = x;
-                    sh.ci[at] = i;
-                }
+                if (at < kCand) sh.cand[at] = key_of(x, i);
             }
         };
         for (int f = warp; f < flagged; f += kWarps)
@@ -312,22 +314,17 @@ __global__ void __launch_bounds__(kThreads, 6) token_logprobs_kernel(const __gri
             }
         if (tid < s.peeled()) take(to_f32(s.row[s.peel_at(tid)]), s.peel_at(tid));
         __syncthreads();
-        int n = sh.cands;
+        const int n = sh.cands;
         if (n > kCand) {
-            n = scan_top<T>(sh, s, a.top);
-        } else {
-            for (int i = tid; i < n; i += kThreads) {
-                const float x = sh.cv[i];
-                const int xi = sh.ci[i];
-                int before = 0;
-                for (int j = 0; j < n; ++j) before += better(sh.cv[j], sh.ci[j], x, xi) ? 1 : 0;
-                if (before < a.top) {
-                    sh.tv[before] = x;
-                    sh.ti[before] = xi;
-                }
+            scan_top<T>(sh, s, a.top);
+        } else if (warp == 0) {
+            uint64_t best = sort_down(lane < n ? sh.cand[lane] : uint64_t(0));
+            for (int i = 32; i < n; i += 32) {
+                const uint64_t more = sort_down(i + lane < n ? sh.cand[i + lane] : uint64_t(0));
+                best = merge_down(best, static_cast<uint64_t>(__shfl_sync(0xffffffffu, more, 31 - lane)));
             }
+            if (lane < a.top) sh.best[lane] = best;
         }
-        if (tid < a.top && tid >= n) sh.ti[tid] = -1;
     }
 
     // ---------------------------------------------------------------- the row
@@ -376,38 +373,23 @@ __global__ void __launch_bounds__(kThreads, 6) token_logprobs_kernel(const __gri
         }
         if (a.top > 0) {
             // the CTAs' lists, each of them sorted, into one
-            int n = 0;                               // alternatives that some CTA has
             float* ov = a.top_logprob ? a.top_logprob + row * a.top : nullptr;
             int32_t* oi = a.top_index ? a.top_index + row * a.top : nullptr;
-            for (int q = 0; q < cluster; ++q) {
-                float x = -INFINITY;
-                int xi = -1;
-                if (lane < a.top) {
-                    if (cluster == 1) {
-                        x = sh.tv[lane];
-                        xi = sh.ti[lane];
-                    } else {
-                        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(mapa_shared(smem_addr(sh.tv + lane), q)) : "memory");
-                        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(xi) : "r"(mapa_shared(smem_addr(sh.ti + lane), q)) : "memory");
-                    }
-                }
-                const bool has = xi >= 0;
-                if (has) {
-                    sh.cv[n + lane] = x;             // (has is true for the first lanes only)
-                    sh.ci[n + lane] = xi;
-                }
-                n += __popc(__ballot_sync(0xffffffffu, has));
+            uint64_t best = lane < a.top ? sh.best[lane] : uint64_t(0);
+            uint64_t more[kMaxCluster];
+#pragma unroll
+            for (int q = 1; q < kMaxCluster; ++q) {
+                more[q] = 0;
+                if (q < cluster && 31 - lane < a.top)
+                    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(*reinterpret_cast<unsigned long long*>(&more[q])) : "r"(mapa_shared(smem_addr(sh.best + 31 - lane), q)) : "memory");
             }
-            __syncwarp();
-            for (int i = lane; i < n; i += 32) {
-                const float x = sh.cv[i];
-                const int xi = sh.ci[i];
-                int before = 0;
-                for (int j = 0; j < n; ++j) before += better(sh.cv[j], sh.ci[j], x, xi) ? 1 : 0;
-                if (before < a.top) {
-                    if (ov) ov[before] = log_p(x);
-                    if (oi) oi[before] = xi;
-                }
+#pragma unroll
+            for (int q = 1; q < kMaxCluster; ++q)
+                if (q < cluster) best = merge_down(best, more[q]);
+            const int n = __popc(__ballot_sync(0xffffffffu, lane < a.top && best != 0));
+            if (lane < n) {
+                if (ov) ov[lane] = log_p(logit_of(best));
+                if (oi) oi[lane] = index_of(best);
             }
             // Fewer than `top` logits above -inf: then the first tokens of the others, which are among the first `top`.
             if (n < a.top) {
