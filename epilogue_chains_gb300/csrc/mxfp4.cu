@@ -193,14 +193,7 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  : "memory");
 }
 
-template <typename T>
-__device__ __forceinline__ void finish_store(const GemmArgs& a, int token, int n, float v, float bias) {
-    v += bias;
-    if (a.gelu) v = gelu_erf(v);
-    const int64_t at = static_cast<int64_t>(token) * a.N + n;
-    if (a.R) v += to_f32(static_cast<const T*>(a.R)[at]);
-    static_cast<T*>(a.y)[at] = from_f32<T>(v);
-}
+__device__ __forceinline__ bool is_aligned_dev(const void* p, uint32_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 // 32 tokens of one weight, N elements apart, `left` of them in the matrix: the residual, and the sums v finished and stored.
 // (Whether there are GELU and residual is decided once for all 32: a branch for each keeps their chains of instructions
@@ -354,18 +347,48 @@ __global__ void __launch_bounds__(kGemmThreads, NT <= 64 ? 2 : 1) mxfp4_gemm_ker
         // each CTA finishes its share of the tile's tokens, summing the parts in order
         cluster_sync();
         if (warp >= 2 && ok) {
-            const int row = 32 * (warp % 4) + lane, n = n0 + row;
-            const bool in = n < a.N;
-            const float bias = in && a.bias ? to_f32(static_cast<const T*>(a.bias)[n]) : 0.0f;
+            // a warp takes a token at a time, a lane four weights; the parts of a token are on their way together
+            const int n = n0 + 4 * lane, wide = a.N - n;      // weights of this lane within the matrix, if below 4
+            float bias[4] = {};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (a.bias && e < wide) bias[e] = to_f32(static_cast<const T*>(a.bias)[n + e]);
             const int tokens = min(NT, a.M - m0);
-            for (int c = part; c < tokens; c += split) {
-                float v = 0.0f;
-                for (int p = 0; p < split; ++p) {
-                    float x;
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(mapa_shared(base + (c * 128 + row) * 4, p)) : "memory");
-                    v += x;
+#pragma unroll 2
+            for (int c = part + split * (warp - 2); c < tokens; c += 4 * split) {
+                float x[8][4], v[4] = {}, r[4] = {};
+                const int64_t at = static_cast<int64_t>(m0 + c) * a.N + n;
+#pragma unroll
+                for (int p = 0; p < 8; ++p)
+                    if (p < split)
+                        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                     : "=f"(x[p][0]), "=f"(x[p][1]), "=f"(x[p][2]), "=f"(x[p][3])
+                                     : "r"(mapa_shared(base + (c * 128 + 4 * lane) * 4, p))
+                                     : "memory");
+                if (a.R)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (e < wide) r[e] = to_f32(static_cast<const T*>(a.R)[at + e]);
+#pragma unroll
+                for (int p = 0; p < 8; ++p)
+                    if (p < split)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[e] += x[p][e];
+                T* y = static_cast<T*>(a.y) + at;
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                    float2 z = make_float2(v[e] + bias[e], v[e + 1] + bias[e + 1]);
+                    if (a.gelu) z = gelu_erf2(z);
+                    v[e] = z.x + r[e];
+                    v[e + 1] = z.y + r[e + 1];
                 }
-                if (in) finish_store<T>(a, m0 + c, n, v, bias);
+                if (a.N % 4 == 0 && is_aligned_dev(a.y, 8)) {
+                    if (wide > 0) *reinterpret_cast<uint2*>(y) = make_uint2(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (e < wide) y[e] = from_f32<T>(v[e]);
+                }
             }
         }
         cluster_sync();

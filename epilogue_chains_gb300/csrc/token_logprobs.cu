@@ -94,24 +94,38 @@ __device__ __forceinline__ V merge_down(V v, V other) {
     return v;
 }
 
-// Largest of a 16-byte vector's values (NaN left out).
-template <typename T> __device__ __forceinline__ float vec_max(const uint4& r);
-template <> __device__ __forceinline__ float vec_max<float>(const uint4& r) {
-    return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)), fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
+// A 32-byte vector of logits: whole sectors, also of the few that are read again.
+struct Vec {
+    uint4 lo, hi;
+};
+__device__ __forceinline__ Vec load(const Vec* p) {
+    Vec v;
+    asm volatile("ld.global.cg.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v.lo.x), "=r"(v.lo.y), "=r"(v.lo.z), "=r"(v.lo.w), "=r"(v.hi.x), "=r"(v.hi.y), "=r"(v.hi.z), "=r"(v.hi.w)
+                 : "l"(p));
+    return v;
 }
-template <> __device__ __forceinline__ float vec_max<__half>(const uint4& r) {
-    const __half2* h = reinterpret_cast<const __half2*>(&r);
-    const float2 f = __half22float2(__hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])));
-    return fmaxf(f.x, f.y);
+template <typename T> __device__ __forceinline__ void unpack(const Vec& v, float* f) {
+    Vec16<T>::unpack(v.lo, f);
+    Vec16<T>::unpack(v.hi, f + Vec16<T>::N);
 }
-template <> __device__ __forceinline__ float vec_max<__nv_bfloat16>(const uint4& r) {
-    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&r);
-    const float2 f = __bfloat1622float2(__hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])));
-    return fmaxf(f.x, f.y);
+// Largest of its values (NaN left out).
+template <typename T> __device__ __forceinline__ float vec_max(const Vec& v) {
+    if constexpr (std::is_same<T, float>::value) {
+        float f[8];
+        unpack<T>(v, f);
+        return fmaxf(fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])), fmaxf(fmaxf(f[4], f[5]), fmaxf(f[6], f[7])));
+    } else {
+        using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+        const T2 *a = reinterpret_cast<const T2*>(&v.lo), *b = reinterpret_cast<const T2*>(&v.hi);
+        const T2 m = __hmax2(__hmax2(__hmax2(a[0], a[1]), __hmax2(a[2], a[3])), __hmax2(__hmax2(b[0], b[1]), __hmax2(b[2], b[3])));
+        return fmaxf(to_f32(m.x), to_f32(m.y));
+    }
 }
 
 struct Shared {
     float sorted[kWarps][32];               // each warp's thread maxima, descending
+    float merged[kWarps / 4][32];           // the largest of four warps'
     float s[kWarps], t[kWarps], bound;
     float part[3];                          // this CTA's (m, S, T)
     int flagged, cands;
@@ -125,9 +139,9 @@ struct Shared {
 // first CTA, the `head` elements before the middle and those from `tail` on.
 template <typename T>
 struct Slice {
-    static constexpr int N = 16 / sizeof(T);
+    static constexpr int N = 32 / sizeof(T);
     const T* row;
-    const uint4* mid;
+    const Vec* mid;
     int head, tail, vocab, v0, nv;
     bool first;
     __device__ __forceinline__ int peeled() const { return first ? head + (vocab - tail) : 0; }
@@ -140,7 +154,7 @@ template <typename T, typename F>
 __device__ __forceinline__ void for_each(const Slice<T>& s, F&& f) {
     for (int v = threadIdx.x; v < s.nv; v += kThreads) {
         float x[Slice<T>::N];
-        Vec16<T>::unpack(__ldcg(s.mid + v), x);
+        unpack<T>(load(s.mid + v), x);
 #pragma unroll
         for (int e = 0; e < Slice<T>::N; ++e) f(x[e], s.index(v, e));
     }
@@ -177,7 +191,7 @@ __device__ __noinline__ void scan_top(Shared& sh, const Slice<T>& s, int top) {
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 6) token_logprobs_kernel(const __grid_constant__ LogprobArgs a, int cluster) {
-    constexpr int N = Slice<T>::N, U = 4;
+    constexpr int N = Slice<T>::N, U = 2;
     __shared__ Shared sh;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const uint32_t rank = cluster > 1 ? cluster_rank() : 0u;
@@ -189,13 +203,13 @@ __global__ void __launch_bounds__(kThreads, 6) token_logprobs_kernel(const __gri
     s.vocab = a.vocab;
     s.first = rank == 0;
     {
-        const int lead = static_cast<int>((16u - (reinterpret_cast<uintptr_t>(s.row) & 15u)) & 15u) / static_cast<int>(sizeof(T));
+        const int lead = static_cast<int>((32u - (reinterpret_cast<uintptr_t>(s.row) & 31u)) & 31u) / static_cast<int>(sizeof(T));
         s.head = min(lead, a.vocab);
         const int vecs = (a.vocab - s.head) / N, per = (vecs + cluster - 1) / cluster;
         s.tail = s.head + vecs * N;
         s.v0 = min(static_cast<int>(rank) * per, vecs);
         s.nv = min(per, vecs - s.v0);
-        s.mid = reinterpret_cast<const uint4*>(s.row + s.head) + s.v0;
+        s.mid = reinterpret_cast<const Vec*>(s.row + s.head) + s.v0;
     }
     if (tid == 0) sh.flagged = sh.cands = 0;
 
@@ -220,9 +234,9 @@ __global__ void __launch_bounds__(kThreads, 6) token_logprobs_kernel(const __gri
     };
     int v = tid;
     for (; v + (U - 1) * kThreads < s.nv; v += U * kThreads) {
-        uint4 r[U];
+        Vec r[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) r[u] = __ldcg(s.mid + v + u * kThreads);
+        for (int u = 0; u < U; ++u) r[u] = load(s.mid + v + u * kThreads);
         float mx = vec_max<T>(r[0]);
 #pragma unroll
         for (int u = 1; u < U; ++u) mx = fmaxf(mx, vec_max<T>(r[u]));
@@ -230,17 +244,17 @@ __global__ void __launch_bounds__(kThreads, 6) token_logprobs_kernel(const __gri
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 float x[N];
-                Vec16<T>::unpack(r[u], x);
+                unpack<T>(r[u], x);
 #pragma unroll
                 for (int e = 0; e < N; ++e) f(x[e]);
             }
         });
     }
     for (; v < s.nv; v += kThreads) {
-        const uint4 r = __ldcg(s.mid + v);
+        const Vec r = load(s.mid + v);
         add(vec_max<T>(r), [&](auto&& f) {
             float x[N];
-            Vec16<T>::unpack(r, x);
+            unpack<T>(r, x);
 #pragma unroll
             for (int e = 0; e < N; ++e) f(x[e]);
         });
@@ -263,10 +277,19 @@ __global__ void __launch_bounds__(kThreads, 6) token_logprobs_kernel(const __gri
     float M = sh.sorted[0][0];
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) M = fmaxf(M, sh.sorted[w][0]);
-    if (warp == 0 && a.top > 0) {
-        float best = sh.sorted[0][lane];
+    if (a.top > 0) {         // the warps' lists into one, four at a time
+        if (warp < kWarps / 4) {
+            float best = sh.sorted[4 * warp][lane];
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) best = merge_down(best, sh.sorted[w][31 - lane]);
+            for (int w = 1; w < 4; ++w) best = merge_down(best, sh.sorted[4 * warp + w][31 - lane]);
+            sh.merged[warp][lane] = best;
+        }
+        __syncthreads();
+    }
+    if (warp == 0 && a.top > 0) {
+        float best = sh.merged[0][lane];
+#pragma unroll
+        for (int w = 1; w < kWarps / 4; ++w) best = merge_down(best, sh.merged[w][31 - lane]);
         if (lane == a.top - 1) sh.bound = best;
     }
     const bool some = m > -INFINITY;
@@ -308,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 6) token_logprobs_kernel(const __gri
         for (int f = warp; f < flagged; f += kWarps)
             for (int w = sh.list[f] + lane * kThreads; w < s.nv; w += 32 * kThreads) {
                 float x[N];
-                Vec16<T>::unpack(__ldcg(s.mid + w), x);
+                unpack<T>(load(s.mid + w), x);
 #pragma unroll
                 for (int e = 0; e < N; ++e) take(x[e], s.index(w, e));
             }
