@@ -43,12 +43,23 @@ __device__ __forceinline__ uint32_t to_e2m1(const float* v) {
         : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
     return r;
 }
-// The value of the code in the lowest four bits.
-__device__ __forceinline__ float from_e2m1(uint32_t c) {
-    // exponent field x, mantissa bit m: (2 + m) 2^(x - 2), for x = 0: m / 2
-    const uint32_t x = (c >> 1) & 3u, m = c & 1u;
-    const float v = x == 0u ? 0.5f * static_cast<float>(m) : __uint_as_float(((126u + x) << 23) | (m << 22));
-    return (c & 8u) ? -v : v;
+// The values of eight codes (exact in fp16).
+__device__ __forceinline__ void from_e2m1(uint32_t c, float* v) {
+    uint32_t h[4];
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "mov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(c));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack2<__half>(h[i]);
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+    }
 }
 
 struct QuantArgs {
@@ -66,29 +77,41 @@ __global__ void __launch_bounds__(kQThreads) mxfp4_quantize_kernel(const __grid_
     pdl_begin();
     const int tid = threadIdx.x, ch = tid % PER_ROW;
     const int64_t row0 = static_cast<int64_t>(blockIdx.y) * 128, col = static_cast<int64_t>(blockIdx.x) * 128 + ch * N;
+    // (fp32: four vectors on their way at a time, 8192 x 4096 28.1 -> 23.8 us; the shorter 16-bit vectors gain nothing by it)
+    constexpr int AHEAD = sizeof(T) == 4 ? 4 : 1;
 #pragma unroll
-    for (int i = 0; i < ITER; ++i) {
-        const int r = tid / PER_ROW + i * ROWS;
-        const bool in = row0 + r < a.rows && col < a.cols;
-        float v[N] = {};
-        if (in) Vec32<T>::load(static_cast<const T*>(a.x) + (row0 + r) * a.ld + col, v);
-        uint32_t top = 0;                    // the largest magnitude's bits (infinity and NaN above all)
+    for (int i0 = 0; i0 < ITER; i0 += AHEAD) {
+        float vs[AHEAD][N];
 #pragma unroll
-        for (int e = 0; e < N; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
+        for (int i = 0; i < AHEAD; ++i) {
+            const int r = tid / PER_ROW + (i0 + i) * ROWS;
 #pragma unroll
-        for (int o = 1; o < GROUP; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const uint32_t field = top >> 23;    // max |v| >= 2^(field - 127)
-        const uint32_t scale = field == 255u ? 255u : field > 2u ? field - 2u : 0u;
-        const float inv = __uint_as_float((254u - min(scale, 253u)) << 23);
-#pragma unroll
-        for (int e = 0; e < N; ++e) v[e] *= inv;
-        if (in) {
-            uint8_t* q = a.q + (row0 + r) * (a.cols / 2) + col / 2;
-            if constexpr (N == 16) *reinterpret_cast<uint2*>(q) = make_uint2(to_e2m1(v), to_e2m1(v + 8));
-            else *reinterpret_cast<uint32_t*>(q) = to_e2m1(v);
+            for (int e = 0; e < N; ++e) vs[i][e] = 0.0f;
+            if (row0 + r < a.rows && col < a.cols) Vec32<T>::load(static_cast<const T*>(a.x) + (row0 + r) * a.ld + col, vs[i]);
         }
-        // (scales of rows and values past the matrix are 0: with codes of 0 they add nothing to a product)
-        if (ch % GROUP == 0) tile[(r % 32) * 16 + (r / 32) * 4 + ch / GROUP] = static_cast<uint8_t>(in ? scale : 0u);
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int r = tid / PER_ROW + (i0 + i) * ROWS;
+            const bool in = row0 + r < a.rows && col < a.cols;
+            float (&v)[N] = vs[i];
+            uint32_t top = 0;                    // the largest magnitude's bits (infinity and NaN above all)
+#pragma unroll
+            for (int e = 0; e < N; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
+#pragma unroll
+            for (int o = 1; o < GROUP; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const uint32_t field = top >> 23;    // max |v| >= 2^(field - 127)
+            const uint32_t scale = field == 255u ? 255u : field > 2u ? field - 2u : 0u;
+            const float inv = __uint_as_float((254u - min(scale, 253u)) << 23);
+#pragma unroll
+            for (int e = 0; e < N; ++e) v[e] *= inv;
+            if (in) {
+                uint8_t* q = a.q + (row0 + r) * (a.cols / 2) + col / 2;
+                if constexpr (N == 16) *reinterpret_cast<uint2*>(q) = make_uint2(to_e2m1(v), to_e2m1(v + 8));
+                else *reinterpret_cast<uint32_t*>(q) = to_e2m1(v);
+            }
+            // (scales of rows and values past the matrix are 0: with codes of 0 they add nothing to a product)
+            if (ch % GROUP == 0) tile[(r % 32) * 16 + (r / 32) * 4 + ch / GROUP] = static_cast<uint8_t>(in ? scale : 0u);
+        }
     }
     __syncthreads();
     if (tid < 32)
@@ -123,8 +146,10 @@ __global__ void __launch_bounds__(kQThreads) mxfp4_dequantize_kernel(const __gri
         const uint32_t s = tile[(r % 32) * 16 + (r / 32) * 4 + ch / GROUP];
         const float scale = __uint_as_float(s == 255u ? 0x7fc00000u : s == 0u ? 0x00400000u : s << 23);
         float v[N];
+        from_e2m1(w[i].x, v);
+        if constexpr (N == 16) from_e2m1(w[i].y, v + 8);
 #pragma unroll
-        for (int e = 0; e < N; ++e) v[e] = from_e2m1(((e < 8 ? w[i].x : w[i].y) >> (4 * (e % 8))) & 15u) * scale;
+        for (int e = 0; e < N; ++e) v[e] *= scale;
         Vec32<T>::store(y + (row0 + r) * a.cols + col, v);
     }
 }
@@ -193,8 +218,6 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  : "memory");
 }
 
-__device__ __forceinline__ bool is_aligned_dev(const void* p, uint32_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
 // 32 tokens of one weight, N elements apart, `left` of them in the matrix: the residual, and the sums v finished and stored.
 // (Whether there are GELU and residual is decided once for all 32: a branch for each keeps their chains of instructions
 // from running next to one another, and took 8192 x 28672 x 4096 with GELU from 323 to 352 us.)
@@ -222,6 +245,68 @@ __device__ __forceinline__ void finish_32(T* y, int64_t N, int left, bool gelu, 
     } else {
         if (add) finish_pairs<T, false, true>(y, N, left, v, bias, r);
         else finish_pairs<T, false, false>(y, N, left, v, bias, r);
+    }
+}
+
+// CTA `part` of the SPLIT that share a tile finishes every SPLIT-th of its tokens: a warp takes a token at a time, a lane four
+// weights.  The parts are summed in order; sixteen reads of other CTAs' shared memory are on their way together (one token
+// at a time, 200 tokens of 4096 x 4096 over two CTAs took 9.0 us, 2.2 more than unsplit).
+template <typename T, int SPLIT>
+__device__ __forceinline__ void join_tokens(const GemmArgs& a, uint32_t base, int m0, int n0, int part, int tokens, int warp, int lane) {
+    constexpr int AHEAD = 16 / SPLIT;
+    const int n = n0 + 4 * lane, wide = a.N - n;      // weights of this lane within the matrix, if below 4
+    float bias[4] = {};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (a.bias && e < wide) bias[e] = to_f32(static_cast<const T*>(a.bias)[n + e]);
+    uint32_t at[SPLIT];
+#pragma unroll
+    for (int p = 0; p < SPLIT; ++p) at[p] = mapa_shared(base + 16 * lane, p);
+    const bool whole = a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 7) == 0;
+    for (int c0 = part + SPLIT * warp; c0 < tokens; c0 += 4 * SPLIT * AHEAD) {
+        float x[AHEAD][SPLIT][4];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int c = min(c0 + 4 * SPLIT * i, tokens - 1);
+#pragma unroll
+            for (int p = 0; p < SPLIT; ++p)
+                asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                             : "=f"(x[i][p][0]), "=f"(x[i][p][1]), "=f"(x[i][p][2]), "=f"(x[i][p][3])
+                             : "r"(at[p] + c * 512)
+                             : "memory");
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int c = c0 + 4 * SPLIT * i;
+            if (c >= tokens) break;
+            const int64_t to = static_cast<int64_t>(m0 + c) * a.N + n;
+            T* y = static_cast<T*>(a.y) + to;
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[e] = x[i][0][e];
+#pragma unroll
+                for (int p = 1; p < SPLIT; ++p) v[e] += x[i][p][e];
+            }
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+                float2 z = make_float2(v[e] + bias[e], v[e + 1] + bias[e + 1]);
+                if (a.gelu) z = gelu_erf2(z);
+                v[e] = z.x;
+                v[e + 1] = z.y;
+            }
+            if (a.R)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (e < wide) v[e] += to_f32(static_cast<const T*>(a.R)[to + e]);
+            if (whole) {
+                if (wide > 0) *reinterpret_cast<uint2*>(y) = make_uint2(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (e < wide) y[e] = from_f32<T>(v[e]);
+            }
+        }
     }
 }
 
@@ -347,49 +432,9 @@ __global__ void __launch_bounds__(kGemmThreads, NT <= 64 ? 2 : 1) mxfp4_gemm_ker
         // each CTA finishes its share of the tile's tokens, summing the parts in order
         cluster_sync();
         if (warp >= 2 && ok) {
-            // a warp takes a token at a time, a lane four weights; the parts of a token are on their way together
-            const int n = n0 + 4 * lane, wide = a.N - n;      // weights of this lane within the matrix, if below 4
-            float bias[4] = {};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (a.bias && e < wide) bias[e] = to_f32(static_cast<const T*>(a.bias)[n + e]);
-            const int tokens = min(NT, a.M - m0);
-#pragma unroll 2
-            for (int c = part + split * (warp - 2); c < tokens; c += 4 * split) {
-                float x[8][4], v[4] = {}, r[4] = {};
-                const int64_t at = static_cast<int64_t>(m0 + c) * a.N + n;
-#pragma unroll
-                for (int p = 0; p < 8; ++p)
-                    if (p < split)
-                        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                                     : "=f"(x[p][0]), "=f"(x[p][1]), "=f"(x[p][2]), "=f"(x[p][3])
-                                     : "r"(mapa_shared(base + (c * 128 + 4 * lane) * 4, p))
-                                     : "memory");
-                if (a.R)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (e < wide) r[e] = to_f32(static_cast<const T*>(a.R)[at + e]);
-#pragma unroll
-                for (int p = 0; p < 8; ++p)
-                    if (p < split)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) v[e] += x[p][e];
-                T* y = static_cast<T*>(a.y) + at;
-#pragma unroll
-                for (int e = 0; e < 4; e += 2) {
-                    float2 z = make_float2(v[e] + bias[e], v[e + 1] + bias[e + 1]);
-                    if (a.gelu) z = gelu_erf2(z);
-                    v[e] = z.x + r[e];
-                    v[e + 1] = z.y + r[e + 1];
-                }
-                if (a.N % 4 == 0 && is_aligned_dev(a.y, 8)) {
-                    if (wide > 0) *reinterpret_cast<uint2*>(y) = make_uint2(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]));
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (e < wide) y[e] = from_f32<T>(v[e]);
-                }
-            }
+            if (split == 2) join_tokens<T, 2>(a, base, m0, n0, part, min(NT, a.M - m0), warp - 2, lane);
+            else if (split == 4) join_tokens<T, 4>(a, base, m0, n0, part, min(NT, a.M - m0), warp - 2, lane);
+            else join_tokens<T, 8>(a, base, m0, n0, part, min(NT, a.M - m0), warp - 2, lane);
         }
         cluster_sync();
     } else {
@@ -664,8 +709,13 @@ int launch_gemm(GemmArgs a, const void* xq, const void* wq, cudaStream_t st) {
     const int rc = opt_in_smem((const void*)mxfp4_gemm_kernel<T, NT>, GemmLayout<NT>::SMEM);
     if (rc != FUSE_OK) return rc;
     const int64_t tn = ceil_div(a.N, 128), tm = ceil_div(a.M, NT);
+    // K over up to eight CTAs while all of them are resident at once (two per SM up to 64 tokens) and each has two stages.  Over
+    // two only from 24 stages on: joining them takes what 12 stages do (4096 weights, K = 4096, 16 stages: one token 4.2 us over
+    // eight, 4.6 over four, 5.7 unsplit, but 200 tokens 7.7 over two and 6.8 unsplit; K = 14336: 256 tokens 12.7 over two, 15.1 unsplit).
+    const int64_t room = sm_count() * (NT <= 64 ? 2 : 1);
     a.split = 1;
-    while (a.split < 8 && tn * tm * a.split * 2 <= sm_count() && a.stages >= 2 * a.split * 2) a.split *= 2;
+    while (a.split < 8 && tn * tm * a.split * 2 <= room && a.stages >= 2 * a.split * 2) a.split *= 2;
+    if (a.split == 2 && a.stages < 24) a.split = 1;
     return launch_pdl(mxfp4_gemm_kernel<T, NT>, dim3(static_cast<unsigned>(tn * a.split), static_cast<unsigned>(tm)), dim3(kGemmThreads),
                       GemmLayout<NT>::SMEM, st, a.split, mW, mX, a);
 }
