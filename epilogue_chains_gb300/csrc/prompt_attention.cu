@@ -70,6 +70,7 @@ struct PromptArgs {
     void* o;
     int batch, tokens, hq, hk, group;
     int recip;                         // row / group = row recip >> 16 for rows below 128
+    uint64_t item_recip;               // ceil(2^32 / (tpt tiles))
     int tpt, tiles;                    // tokens of a tile of 128 rows; tiles of an item (1 or 2)
     int page_shift, num_pages, cache_rows;
     float c;                           // scale * log2(e)
@@ -97,10 +98,9 @@ __device__ __forceinline__ Seq seq_of(const PromptArgs& a, int b, int* bad = nul
     if (bad && (c0 < 0 || c1 > a.tokens || c1 < c0 || len < 0 || len > room)) atomicExch(bad, 1);
     return s;
 }
-__device__ __forceinline__ int items_of(const PromptArgs& a, const Seq& s) {
-    const int ti = a.tpt * a.tiles;
-    return (s.n + ti - 1) / ti;
-}
+// n / (tokens of an item), for n below 2^24 (a division takes several times as long).
+__device__ __forceinline__ int over_item(const PromptArgs& a, int n) { return static_cast<int>(static_cast<uint64_t>(n) * a.item_recip >> 32); }
+__device__ __forceinline__ int items_of(const PromptArgs& a, const Seq& s) { return over_item(a, s.n + a.tpt * a.tiles - 1); }
 // Keys that the first `tokens` new tokens of a sequence see between them.
 __device__ __forceinline__ int extent(const Seq& s, int tokens) { return max(s.L - s.n + min(tokens, s.n), 0); }
 // Places of a head's first k items: sum over i < k of kEntry + extent((i + 1) ti).
@@ -111,7 +111,7 @@ __device__ __forceinline__ int64_t places(const PromptArgs& a, const Seq& s, int
         sum += extent(s, s.n);
         --k;
     }
-    const int64_t i0 = d >= 0 ? 0 : -d / ti;          // the first item with d + (i + 1) ti > 0
+    const int64_t i0 = d >= 0 ? 0 : over_item(a, static_cast<int>(-d));     // the first item with d + (i + 1) ti > 0
     if (k > i0) sum += (k - i0) * d + ti * ((static_cast<int64_t>(k) * (k + 1) - i0 * (i0 + 1)) / 2);
     return sum;
 }
@@ -127,14 +127,22 @@ struct Pos {
     }
 };
 
+// x / y, both positive (64-bit divisions take several times as long as 32-bit ones).
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
+    if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+    return x / y;
+}
 // Place r of sequence b; within `snap` blocks of an item's end, that end.
 __device__ __forceinline__ Pos pos_in(const PromptArgs& a, const Seq& s, int b, int64_t r, int snap) {
     const int items = items_of(a, s);
     const int64_t per = places(a, s, items, items);
     Pos p;
     p.b = b;
-    p.h = static_cast<int>(r / per);
-    r -= p.h * per;
+    p.h = 0;
+    if (r >= per) {
+        p.h = static_cast<int>(quotient(r, per));
+        r -= p.h * per;
+    }
     int lo = 0, hi = items - 1;                        // the last item that begins at or before r
     while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
@@ -144,7 +152,7 @@ __device__ __forceinline__ Pos pos_in(const PromptArgs& a, const Seq& s, int b, 
     const int64_t in = r - places(a, s, items, lo);
     const int blocks = (extent(s, (lo + 1) * a.tpt * a.tiles) + 127) / 128;
     p.i = lo;
-    p.t = in <= kEntry ? 0 : static_cast<int>((in - kEntry) / 128);
+    p.t = in <= kEntry ? 0 : static_cast<int>((in - kEntry) >> 7);
     if (p.t <= snap) {
         p.t = 0;
     } else if (blocks - p.t <= snap) {
@@ -215,20 +223,22 @@ struct Walk {
         return false;
     }
 };
-// Where run `which` (0: this CTA's, 1: the next's) begins, for all threads; `scratch` is 64 * 8 bytes of shared memory.
+// Where this CTA's run begins and where the next's does, for all threads; `scratch` is 80 * 8 bytes of shared memory.
 template <int THREADS>
 __device__ __forceinline__ void find_runs(const PromptArgs& a, int64_t* scratch, Pos (&run)[2]) {
     constexpr int WARPS = THREADS / 32;
-    static_assert(WARPS <= 32, "scratch");
+    static_assert(WARPS <= 24, "scratch");
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int per = (a.batch + THREADS - 1) / THREADS;
     int64_t mine = 0;
+    int count = 0;                                     // items
     for (int i = 0; i < per; ++i) {
         const int b = tid * per + i;
         if (b >= a.batch) break;
         const Seq s = seq_of(a, b, blockIdx.x == 0 ? a.bad : nullptr);
         const int items = items_of(a, s);
         mine += a.hk * places(a, s, items, items);
+        count += a.hk * items;
     }
     int64_t upto = mine;
 #pragma unroll
@@ -236,34 +246,52 @@ __device__ __forceinline__ void find_runs(const PromptArgs& a, int64_t* scratch,
         const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
         if (lane >= o) upto += v;
     }
-    Pos* found = reinterpret_cast<Pos*>(scratch + 32);
-    if (lane == 31) scratch[warp] = upto;
-    if (tid < 2) found[tid] = Pos{a.batch, 0, 0, 0};
-    __syncthreads();
-    int64_t total = 0;
-    for (int w = 0; w < WARPS; ++w) {
-        if (w < warp) upto += scratch[w];
-        total += scratch[w];
+    count = __reduce_add_sync(0xffffffffu, count);
+    // per warp its places and items; then for each target its thread and place there, and where it is found
+    int64_t *sums = scratch, *counts = scratch + 24, *target = scratch + 48;
+    Pos* found = reinterpret_cast<Pos*>(scratch + 52);
+    if (lane == 31) {
+        sums[warp] = upto;
+        counts[warp] = count;
     }
-    int64_t len = (total + gridDim.x - 1) / gridDim.x;
-    if (len < kLeastRun) len = kLeastRun;
-    const int snap = static_cast<int>(min(len / (128 * 32), static_cast<int64_t>(64)));
+    if (tid < 2) target[2 * tid] = -1;
+    __syncthreads();
+    int64_t total = 0, items = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+        if (w < warp) upto += sums[w];
+        total += sums[w];
+        items += counts[w];
+    }
+    // Equal runs, but none shorter than an item of kLeastRun or the average one: with few short items a CTA for each.
+    int64_t len = quotient(total + gridDim.x - 1, gridDim.x), least = items > 0 ? quotient(total + items - 1, items) : 1;
+    if (least > kLeastRun) least = kLeastRun;
+    if (len < least) len = least;
+    const int snap = len < kLeastRun ? 4 : static_cast<int>(min(len >> 12, static_cast<int64_t>(64)));
     for (int w = 0; w < 2; ++w) {
         const int64_t x = static_cast<int64_t>(blockIdx.x + w) * len;
-        if (x >= upto || x < upto - mine) continue;
-        int64_t at = upto - mine;                      // this thread's sequences have it
-        for (int i = 0; i < per; ++i) {
-            const int b = tid * per + i;
-            if (b >= a.batch) break;
-            const Seq s = seq_of(a, b);
-            const int items = items_of(a, s);
-            const int64_t here = a.hk * places(a, s, items, items);
-            if (x < at + here) {
-                found[w] = pos_in(a, s, b, x - at, snap);
-                break;
-            }
-            at += here;
+        if (x < upto && x >= upto - mine) {            // this thread's sequences have it
+            target[2 * w] = tid;
+            target[2 * w + 1] = x - (upto - mine);
         }
+    }
+    __syncthreads();
+    if (warp < 2 && lane == 0) {
+        Pos p{a.batch, 0, 0, 0};
+        if (target[2 * warp] >= 0) {
+            int64_t x = target[2 * warp + 1];
+            for (int b = static_cast<int>(target[2 * warp]) * per;; ++b) {
+                const Seq s = seq_of(a, b);
+                const int n = items_of(a, s);
+                const int64_t here = a.hk * places(a, s, n, n);
+                if (x < here) {
+                    p = pos_in(a, s, b, x, snap);
+                    break;
+                }
+                x -= here;
+            }
+        }
+        found[warp] = p;
     }
     __syncthreads();
     run[0] = found[0];
@@ -296,7 +324,7 @@ struct Layout {
     static constexpr int N_BARS = 2 + 2 * kFull + RING + 12 + 2 + 2 * kSegs + 4;
     static constexpr uint32_t OFF_HOLD = OFF_BAR + N_BARS * 8;
     static constexpr uint32_t OFF_SCRATCH = (OFF_HOLD + 16 + 7) / 8 * 8;
-    static constexpr uint32_t OFF_SEG = OFF_SCRATCH + 64 * 8;
+    static constexpr uint32_t OFF_SEG = OFF_SCRATCH + 80 * 8;
     static constexpr uint32_t SMEM = OFF_SEG + kSegs * sizeof(Seg) + 1024;
     static constexpr uint32_t TMEM_COLS = 512, O_COL = 256;    // scores of tile t at 128 t, output at 256 + D t
     static_assert(SMEM <= 232448, "shared-memory budget");
@@ -357,6 +385,12 @@ __global__ void __launch_bounds__(Layout<D>::THREADS, 1) prompt_attention_kernel
         }
         fence_mbar_init();
     }
+    if (threadIdx.x == 32 * 4) {
+        prefetch_map(&mQ);
+        prefetch_map(&mK);
+        prefetch_map(&mV);
+        prefetch_map(&mO);
+    }
     const uint32_t tmem = tmem_begin(base + L::OFF_HOLD, gbase + L::OFF_HOLD, L::TMEM_COLS, warp);
     pdl_wait();
 
@@ -389,11 +423,6 @@ __global__ void __launch_bounds__(Layout<D>::THREADS, 1) prompt_attention_kernel
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::FEW));
     if (warp == 0) {
         // ---------------------------------------------------------------- Q, K and V loads
-        if (lane == 0) {
-            prefetch_map(&mQ);
-            prefetch_map(&mK);
-            prefetch_map(&mV);
-        }
         const uint32_t one = elect_one();
         const int box_shift = min(a.page_shift, 7);
         const uint32_t q_box = static_cast<uint32_t>(a.group * a.tpt) * 128u;
@@ -967,6 +996,7 @@ extern "C" int fuse_prompt_attention(const void* q, int64_t q_ld, const void* k_
     a.recip = static_cast<int>((65536 + group - 1) / group);
     a.tpt = static_cast<int>(128 / group);
     a.tiles = D <= 128 ? 2 : 1;
+    a.item_recip = ((uint64_t(1) << 32) + a.tpt * a.tiles - 1) / (a.tpt * a.tiles);
     while ((1 << a.page_shift) < page_size) ++a.page_shift;
     a.num_pages = static_cast<int>(num_pages);
     a.cache_rows = static_cast<int>(num_pages * kv_heads * page_size);
