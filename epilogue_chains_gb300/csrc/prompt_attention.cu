@@ -782,96 +782,137 @@ __global__ void __launch_bounds__(Layout<D>::THREADS, 1) prompt_attention_kernel
 }
 
 // ================================================================== join
-// The parts of an item that several CTAs share; blockIdx.y names the CTA whose run begins first within the item.  A warp
-// takes a row at a time, lane c D / 32 columns of it.  It is bound by latency: the parts' outputs are loaded next to their
-// maxima and sums, several at a time.
-constexpr int kJoinThreads = 256, kJoinRows = 32;      // rows of a block
-template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const __grid_constant__ PromptArgs a, int grid) {
-    constexpr int W = D / 32, AHEAD = D == 256 ? 4 : 8;
-    __shared__ int slots[kGrid + 1];
-    __shared__ int count;
-    pdl_begin();
-    const int c0 = blockIdx.y + 1;                 // run c0 begins within an item
-    auto start = [&](int c) {
-        const int4 v = __ldcg(a.start + c);
-        return Pos{v.x, v.y, v.z, v.w};
-    };
-    auto same = [](const Pos& x, const Pos& y) { return x.b == y.b && x.h == y.h && x.i == y.i; };
-    const Pos p = start(c0), q = start(c0 - 1);
-    if (p.t == 0 || p.b >= a.batch || (same(p, q) && q.t > 0)) return;      // (or not the first)
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const Seq s = seq_of(a, p.b);
-    if (warp == 0) {
-        // part 0 is CTA c0 - 1's; then that of each run that begins within the item and has something of it
-        if (lane == 0) slots[0] = 2 * (c0 - 1) + 1;
-        int n = 1;
-        for (int c = c0;; c += 32) {
-            const Pos x = start(min(c + lane, grid)), y = start(min(c + lane + 1, grid));
-            const bool in = c + lane < grid && same(x, p) && x.t > 0, has = in && x.before(y);
-            const uint32_t mask = __ballot_sync(0xffffffffu, has);
-            if (has) slots[n + __popc(mask & ((1u << lane) - 1u))] = 2 * (c + lane);
-            n += __popc(mask);
-            if (!__all_sync(0xffffffffu, in)) break;
-        }
-        if (lane == 0) count = n;
+// The parts of an item that several CTAs share.  Every run that begins within an item brings kJoinWarps warps, among which the
+// item's rows are shared out: four rows to a warp where two CTAs share the item, one where many do.  It is bound by latency: of
+// where the runs begin, then of the parts, so a warp reads all it can at once.
+constexpr int kJoinThreads = 128, kJoinWarps = 64, kJoinWords = (kGrid + 1 + 31) / 32;
+template <typename T, int D, int ROWS, int AHEAD>
+__device__ __forceinline__ void join_rows(const PromptArgs& a, const Pos& p, const Seq& s, int row0, int rows, int c0, const uint32_t (&has)[kJoinWords], int lane) {
+    constexpr int W = D / 32;
+    float m[ROWS], l[ROWS], acc[ROWS][W];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.0f;
+#pragma unroll
+        for (int y = 0; y < W; ++y) acc[i][y] = 0.0f;
     }
-    __syncthreads();
-    const int parts = count;
-    for (int row = blockIdx.x * kJoinRows + warp; row < min(a.rows, static_cast<int>(blockIdx.x + 1) * kJoinRows); row += kJoinThreads / 32) {
-        const int r = row % 128, rt = r * a.recip >> 16, tok = (p.i * a.tiles + row / 128) * a.tpt + rt;
-        if (rt >= a.tpt || tok >= s.n) continue;
-        auto load = [&](float (&v)[W], int part) {
-            const float* src = a.po + (static_cast<int64_t>(slots[part]) * a.rows + row) * D + W * lane;
+    // parts in the order of the keys: CTA c0 - 1's, then those of the runs in `has`
+    int word = 0;
+    uint32_t left = has[0];
+    bool first = true;
+    for (;;) {
+        int slot[AHEAD];
 #pragma unroll
-            for (int e = 0; e < W; e += 2) {
-                const float2 x = __ldcg(reinterpret_cast<const float2*>(src + e));
-                v[e] = x.x;
-                v[e + 1] = x.y;
+        for (int j = 0; j < AHEAD; ++j) {
+            slot[j] = -1;
+            if (first) {
+                first = false;
+                slot[j] = 2 * (c0 - 1) + 1;
+                continue;
             }
-        };
-        float m = -INFINITY, l = 0.0f, acc[W] = {};
-        for (int p0 = 0; p0 < parts; p0 += 32) {
-            float v[AHEAD][W];
+            while (left == 0 && word + 1 < kJoinWords) {
+                ++word;
 #pragma unroll
-            for (int i = 0; i < AHEAD; ++i)
-                if (p0 + i < parts) load(v[i], p0 + i);
-            // lane i has part p0 + i's reference and sum
-            float2 x = make_float2(-INFINITY, 0.0f);
-            if (p0 + lane < parts) x = __ldcg(a.ml + static_cast<int64_t>(slots[p0 + lane]) * a.rows + row);
-            float top = fmaxf(m, x.x);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            // (a part that this row sees nothing of has no output; its weight is 0)
-            const bool none = x.x == -INFINITY && x.y == 0.0f;
-            const float e = none ? 0.0f : ex2f(x.x - top), e0 = m == -INFINITY ? 0.0f : ex2f(m - top);
-            float sum = none ? 0.0f : x.y * e;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            l = l * e0 + sum;
-            m = top;
-            const uint32_t with = __ballot_sync(0xffffffffu, !none);
-#pragma unroll
-            for (int y = 0; y < W; ++y) acc[y] *= e0;
-            for (int b = 0; b < 32 && p0 + b < parts; b += AHEAD) {
-#pragma unroll
-                for (int i = 0; i < AHEAD; ++i) {
-                    const float w = __shfl_sync(0xffffffffu, e, b + i);
-                    if (with >> (b + i) & 1u)
-#pragma unroll
-                        for (int y = 0; y < W; ++y) acc[y] += w * v[i][y];
-                }
-#pragma unroll
-                for (int i = 0; i < AHEAD; ++i)
-                    if (b + AHEAD + i < 32 && p0 + b + AHEAD + i < parts) load(v[i], p0 + b + AHEAD + i);
+                for (int k = 1; k < kJoinWords; ++k)
+                    if (word == k) left = has[k];
+            }
+            if (left != 0) {
+                slot[j] = 2 * (32 * word + __ffs(left) - 1);
+                left &= left - 1;
             }
         }
-        const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
+        if (slot[0] < 0) break;
+        float2 ml[ROWS][AHEAD];
+        float v[ROWS][AHEAD][W];
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j)
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) {
+                ml[i][j] = make_float2(-INFINITY, 0.0f);
+                if (slot[j] < 0 || i >= rows) continue;
+                const int64_t at = static_cast<int64_t>(slot[j]) * a.rows + row0 + i;
+                ml[i][j] = __ldcg(a.ml + at);
+#pragma unroll
+                for (int y = 0; y < W; y += 2) {
+                    const float2 x = __ldcg(reinterpret_cast<const float2*>(a.po + at * D + W * lane + y));
+                    v[i][j][y] = x.x;
+                    v[i][j][y + 1] = x.y;
+                }
+            }
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) {
+                if (ml[i][j].x == -INFINITY && ml[i][j].y == 0.0f) continue;      // (a part that the row sees nothing of has no output)
+                const float top = fmaxf(m[i], ml[i][j].x), e0 = m[i] == -INFINITY ? 0.0f : ex2f(m[i] - top), e1 = ex2f(ml[i][j].x - top);
+                l[i] = l[i] * e0 + ml[i][j].y * e1;
+                m[i] = top;
+#pragma unroll
+                for (int y = 0; y < W; ++y) acc[i][y] = acc[i][y] * e0 + v[i][j][y] * e1;
+            }
+    }
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int row = row0 + i, r = row % 128, rt = r * a.recip >> 16, tok = (p.i * a.tiles + row / 128) * a.tpt + rt;
+        if (i >= rows || rt >= a.tpt || tok >= s.n) continue;
+        const float inv = l[i] > 0.0f ? 1.0f / l[i] : l[i] == 0.0f ? 0.0f : l[i];
         T* dst = static_cast<T*>(a.o) + (static_cast<int64_t>(s.q0 + tok) * a.hq + p.h * a.group + r - rt * a.group) * D + W * lane;
 #pragma unroll
-        for (int e = 0; e < W; e += 2)
-            *reinterpret_cast<uint32_t*>(dst + e) = l == 0.0f ? 0u : pack2<T>(acc[e] * inv, acc[e + 1] * inv);
+        for (int y = 0; y < W; y += 2)
+            *reinterpret_cast<uint32_t*>(dst + y) = l[i] == 0.0f ? 0u : pack2<T>(acc[i][y] * inv, acc[i][y + 1] * inv);
     }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const __grid_constant__ PromptArgs a, int grid) {
+    pdl_begin();
+    const int lane = threadIdx.x % 32, run = blockIdx.y + 1, unit = blockIdx.x * (kJoinThreads / 32) + threadIdx.x / 32;
+    auto start = [&](int c) {
+        const int4 v = __ldcg(a.start + min(c, grid));
+        return Pos{v.x, v.y, v.z, v.w};
+    };
+    const Pos p = start(run);
+    if (p.t == 0 || p.b >= a.batch) return;            // this run begins with an item
+    // The runs that begin within the same item, and of them those that have something of it (runs may be empty), as bits; the
+    // first warp looks from this run on both ways.
+    __shared__ uint32_t bits[2][kJoinWords];
+    if (threadIdx.x < 2 * kJoinWords) bits[threadIdx.x / kJoinWords][threadIdx.x % kJoinWords] = 0;
+    if (threadIdx.x < 32) {
+        __syncwarp();
+        auto look = [&](int k) {
+            const Pos x = start(32 * k + lane), next = start(32 * k + lane + 1);
+            const bool in = 32 * k + lane < grid && x.b == p.b && x.h == p.h && x.i == p.i && x.t > 0;
+            const uint32_t w = __ballot_sync(0xffffffffu, in), h = __ballot_sync(0xffffffffu, in && x.before(next));
+            if (lane == 0) {
+                bits[0][k] = w;
+                bits[1][k] = h;
+            }
+            return w;
+        };
+        const uint32_t w = look(run / 32);
+        if (w & 1u)
+            for (int k = run / 32 - 1; k >= 0 && (look(k) & 1u); --k) {}
+        if (w >> 31)
+            for (int k = run / 32 + 1; k < kJoinWords && (look(k) >> 31); ++k) {}
+    }
+    const Seq s = seq_of(a, p.b);
+    __syncthreads();
+    uint32_t has[kJoinWords];
+    int runs = 0, rank = 0, c0 = 0;
+#pragma unroll
+    for (int k = 0; k < kJoinWords; ++k) {
+        const uint32_t within = bits[0][k];
+        has[k] = bits[1][k];
+        if (runs == 0 && within != 0) c0 = 32 * k + __ffs(within) - 1;
+        runs += __popc(within);
+        rank += __popc(run >= 32 * k + 32 ? within : run > 32 * k ? within & ((1u << (run - 32 * k)) - 1u) : 0u);
+    }
+    const int rows = runs == 1 ? 4 : runs < 4 ? 2 : 1, row0 = (rank * kJoinWarps + unit) * rows;
+    if (row0 >= a.rows) return;
+    if (rows == 4) join_rows<T, D, 4, 2>(a, p, s, row0, min(4, a.rows - row0), c0, has, lane);
+    else if (rows == 2) join_rows<T, D, 2, 4>(a, p, s, row0, min(2, a.rows - row0), c0, has, lane);
+    else join_rows<T, D, 1, 8>(a, p, s, row0, 1, c0, has, lane);
 }
 
 // ================================================================== host side
@@ -918,7 +959,7 @@ int run_prompt(PromptArgs a, const void* q, int64_t q_ld, const void* k, const v
     rc = launch_pdl(prompt_attention_kernel<T, D>, dim3(static_cast<unsigned>(grid)), dim3(L::THREADS), L::SMEM, st, 1, mQ, mK, mV, mO, a);
     // an item of at most one block of keys is nobody's to share
     if (rc != FUSE_OK || grid == 1 || room <= 128) return rc;
-    return launch_pdl(prompt_join_kernel<T, D>, dim3(static_cast<unsigned>(ceil_div(a.rows, kJoinRows)), static_cast<unsigned>(grid - 1)),
+    return launch_pdl(prompt_join_kernel<T, D>, dim3(kJoinWarps / (kJoinThreads / 32), static_cast<unsigned>(grid - 1)),
                       dim3(kJoinThreads), 0, st, 1, a, static_cast<int>(grid));
 }
 
