@@ -304,6 +304,7 @@ __device__ __forceinline__ void find_runs(const PromptArgs& a, int64_t* scratch,
 // products take 2048: a softmax warp's own instructions, one after the other.)
 constexpr int kTileWarps = 8;
 constexpr int kFull = 4;                            // barriers of K tiles in turn, and of V tiles
+constexpr uint32_t kMostTries = 1u << 18;
 constexpr int kSegs = 4;                            // segments that the walk is ahead
 
 template <int D>
@@ -405,8 +406,15 @@ __global__ void __launch_bounds__(Layout<D>::THREADS, 1) prompt_attention_kernel
     auto v_at = [](int j, int n) { return j + 1 < n ? 2 * j + 2 : 2 * j + 1; };
     Seg* segs_at = reinterpret_cast<Seg*>(gbase + L::OFF_SEG);
     bool ok = true;
+    // (A bound by tries, each of which ends by itself after kTryWaitHintNs: mbar_wait_bounded()'s clock makes more code at each of
+    // the many waits, which the warps fetch over and over: 32 prompts to 1024 142 -> 139 us.)
     auto wait = [&](uint32_t bar, uint32_t parity) {
-        ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity & 1u, flag));
+        for (uint32_t n = 0; !__all_sync(0xffffffffu, mbar_try_wait(bar, parity & 1u)); ++n)
+            if (n >= kMostTries || (n % 64 == 63 && *reinterpret_cast<volatile int*>(flag) != 0)) {
+                atomicExch(flag, 1);
+                ok = false;
+                break;
+            }
         return ok;
     };
     // Segment k of this CTA, for a warp that goes through them in order; it gives each back when it is done with it.
@@ -601,15 +609,16 @@ __global__ void __launch_bounds__(Layout<D>::THREADS, 1) prompt_attention_kernel
         for (int k = 0; ok && segment(k); ++k) {
             const Seg& g = segs_at[k % kSegs];       // (stays in shared memory: in registers, next to a row's scores, it spills)
             const int n = t == 0 ? g.n0 : g.n1;
-            // keys that this row sees, from its thread's first of the block on
-            int left = g.L - g.t0 * 128 - g.n + g.tok0 + t * a.tpt + (r * a.recip >> 16) + 1 - 32 * hf;
+            // the first block that some row of the tile does not see all of, and the one that the sequence's last key is in
+            const int partial = ((g.L - g.n + g.tok0 + t * a.tpt + 1) >> 7) - g.t0, last = ((g.L - 1) >> 7) - g.t0;
             float m = -INFINITY, l = 0.0f;
-            for (int j = 0; j < n; ++j, ++i, left -= 128) {
+            for (int j = 0; j < n; ++j, ++i) {
                 if (!wait(s_full(t), i)) break;
                 tc_fence_after();
                 // 64 keys at a time, so that the weights of the first half are multiplied with V while those of the second are
-                // computed, and half of P is free as soon as the last block's half has been multiplied.
-#pragma unroll
+                // computed, and half of P is free as soon as the last block's half has been multiplied.  (Not unrolled: the warps
+                // fetch half the instructions.  32 prompts to 1024 133 us, unrolled 144 to 153; one of 4096 126, unrolled 120.)
+#pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
                     float x[32];         // keys 64 h + 32 hf .. of the block
                     tmem_ld_rows16(st + 64 * h, x);
@@ -619,9 +628,13 @@ __global__ void __launch_bounds__(Layout<D>::THREADS, 1) prompt_attention_kernel
                         __syncwarp();
                         if (lane == 0) mbar_arrive(s_free(t));
                     }
-                    if (__any_sync(0xffffffffu, left - 64 * h < 32)) {
+                    if (j >= partial) {
+                        // keys that this row sees, from the thread's first on
+                        const int left = g.L - g.n + g.tok0 + t * a.tpt + (r * a.recip >> 16) + 1 - (g.t0 + j) * 128 - 64 * h - 32 * hf;
+                        if (__any_sync(0xffffffffu, left < 32)) {
 #pragma unroll
-                        for (int y = 0; y < 32; ++y) x[y] = y >= left - 64 * h ? -INFINITY : x[y];
+                            for (int y = 0; y < 32; ++y) x[y] = y >= left ? -INFINITY : x[y];
+                        }
                     }
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -670,9 +683,8 @@ __global__ void __launch_bounds__(Layout<D>::THREADS, 1) prompt_attention_kernel
                     if (h == 0) {
                         // V rows past the sequence's end: 0 x whatever lies there must be 0.  By the tile whose product with
                         // this block is issued first.
-                        const int kleft = g.L - (g.t0 + j) * 128;
-                        if (kleft < 128 && (t == 0 || j >= g.n0)) {
-                            const int vi = kv + j;
+                        if (j == last && (t == 0 || j >= g.n0)) {
+                            const int vi = kv + j, kleft = g.L - (g.t0 + j) * 128;
                             if (!wait(v_full(vi % kFull), vi / kFull)) break;
                             uint8_t* vb = gbase + L::OFF_KV + ((2 * kv + v_at(j, g.steps())) % RING) * L::TILE;
                             for (int v = 32 * u + lane; v < (128 - kleft) * (D / 8); v += 32 * kTileWarps) {
@@ -910,9 +922,11 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const __grid_
     }
     const int rows = runs == 1 ? 4 : runs < 4 ? 2 : 1, row0 = (rank * kJoinWarps + unit) * rows;
     if (row0 >= a.rows) return;
-    if (rows == 4) join_rows<T, D, 4, 2>(a, p, s, row0, min(4, a.rows - row0), c0, has, lane);
-    else if (rows == 2) join_rows<T, D, 2, 4>(a, p, s, row0, min(2, a.rows - row0), c0, has, lane);
-    else join_rows<T, D, 1, 8>(a, p, s, row0, 1, c0, has, lane);
+    if (rows == 1) {
+        join_rows<T, D, 1, 4>(a, p, s, row0, 1, c0, has, lane);
+    } else {
+        for (int i = 0; i < rows && row0 + i < a.rows; i += 2) join_rows<T, D, 2, 2>(a, p, s, row0 + i, min(2, a.rows - row0 - i), c0, has, lane);
+    }
 }
 
 // ================================================================== host side
