@@ -650,7 +650,7 @@ bool map_codes(CUtensorMap* map, const void* q, int64_t rows, int64_t K, int box
 // Its scale tiles: a row of tiles as 32-bit elements, boxes of two tiles' 1024 bytes.
 bool map_scales(CUtensorMap* map, const void* s, int64_t rows, int64_t K, int box_rows) {
     const int64_t row = ceil_div(K, 128) * 512, n = ceil_div(rows, 128);
-    const int64_t dims[3] = {row / 4, n, 1}, strides[2] = {row, row * n};
+    const int64_t dims[3] = {row / 4, n, 1}, strides[2] = {row, row};
     const int box[3] = {256, box_rows, 1};
     return make_map_3d(map, s, kMap32, dims, strides, box, 0);
 }
@@ -812,6 +812,7 @@ extern "C" int fuse_mxfp4_gemm(const void* xq, const void* xs, const void* wq, c
     if (rc == FUSE_OK) rc = check_matrix(N, K);
     if (rc != FUSE_OK) return rc;
     if (N < 1 || (gelu != 0 && gelu != 1) || (dtype != FUSE_F16 && dtype != FUSE_BF16)) return FUSE_EINVAL;
+    if (ceil_div(M, 256) * ceil_div(N, 256) >= (int64_t(1) << 30) / ceil_div(K, kStageK)) return FUSE_EUNSUPPORTED;   // stages are counted in 32 bits
     if (M == 0) return FUSE_OK;
     if (!xq || !xs || !wq || !ws || !y) return FUSE_EINVAL;
     if (!is_aligned(xq, 16) || !is_aligned(xs, 16) || !is_aligned(wq, 16) || !is_aligned(ws, 16) || !is_aligned(y, 2) || !is_aligned(bias, 2) ||

@@ -1020,8 +1020,8 @@ extern "C" int fuse_prompt_attention(const void* q, int64_t q_ld, const void* k_
     if (group > 128 || batch > kMaxBatch || q_heads > 65536 || tokens >= int64_t(1) << 24 || num_pages >= top / (kv_heads * page_size) ||
         table_ld >= (top - 4096) / page_size || q_ld >= int64_t(1) << 32)
         return FUSE_EUNSUPPORTED;
-    // the line's places, times the CTAs, stay within 64 bits
-    if ((tokens + batch) * kv_heads >= (int64_t(1) << 52) / (table_ld * page_size + kEntry)) return FUSE_EUNSUPPORTED;
+    // items are counted in 32 bits, the line's places, times the CTAs, in 64
+    if ((tokens + batch) * kv_heads >= top || (tokens + batch) * kv_heads >= (int64_t(1) << 52) / (table_ld * page_size + kEntry)) return FUSE_EUNSUPPORTED;
     if (q_ld < q_heads * D) return FUSE_EINVAL;
     if (tokens == 0 || batch == 0) return FUSE_OK;
     if (!q || !k_cache || !v_cache || !o || !cu_queries || !seq_lens || (table_ld > 0 && !block_table)) return FUSE_EINVAL;

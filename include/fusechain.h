@@ -450,8 +450,8 @@ int fuse_w4_gemv(const void* x, const void* wq, const void* scales, const void* 
  *   seq_lens device int32 [batch]: the keys of each sequence, 0 .. table_ld page_size
  *   Rules: dtype FUSE_F16 or FUSE_BF16; D in {64, 128, 256}; q_heads a multiple of kv_heads, at most 128 of
  *          them for each; page_size a power of two, 16..256; batch <= 4096; tokens < 2^24; num_pages kv_heads
- *          page_size and table_ld page_size below 2^31 - 4096, (tokens + batch) kv_heads (table_ld page_size +
- *          192) below 2^52 (else FUSE_EUNSUPPORTED, and nothing is enqueued); scale > 0; tensors 16-byte
+ *          page_size and table_ld page_size below 2^31 - 4096, (tokens + batch) kv_heads below 2^31 and, times
+ *          (table_ld page_size + 192), below 2^52 (else FUSE_EUNSUPPORTED, and nothing is enqueued); scale > 0; tensors 16-byte
  *          aligned and q_ld a multiple of 8, tables and lengths 4-byte (else FUSE_EALIGN).
  *   Out of range in device memory (fuse_check() then returns FUSE_EINDEX): a page index outside
  *   [0, num_pages) counts as a page of zeros; a length is taken into 0 .. table_ld page_size, a row number
@@ -502,7 +502,8 @@ int64_t fuse_mxfp4_scale_bytes(int64_t rows, int64_t cols);
  *   xq, xs   X [M, K] as fuse_mxfp4_quantize() writes it (M == 0 enqueues nothing);  wq, ws  W [N, K] likewise (of the
  *            scales' bytes that no row or value has, those of existing rows must not be 255)
  *   bias [N], R [M, N] of `dtype`, or NULL;  gelu 0 or 1;  y device [M, N] of `dtype`
- *   Rules: dtype FUSE_F16 or FUSE_BF16; K a multiple of 32, below 2^31; M, N < 2^22 (else FUSE_EUNSUPPORTED);
+ *   Rules: dtype FUSE_F16 or FUSE_BF16; K a multiple of 32, below 2^31; M, N < 2^22, ceil(M / 256) ceil(N / 256)
+ *          ceil(K / 256) below 2^30 (else FUSE_EUNSUPPORTED);
  *          xq, xs, wq and ws 16-byte aligned, the others to their element (else FUSE_EALIGN); y overlaps no input.
  * The products are exact, their sums fp32, and Y is rounded once.  The order of the sums is fixed.
  */

@@ -69,6 +69,7 @@ def score(**kw):
     (dict(pages=1 << 28), fc.FUSE_EUNSUPPORTED),
     (dict(ld=1 << 28), fc.FUSE_EUNSUPPORTED),
     (dict(tokens=(1 << 24) - 1, ld=(1 << 27) - 1024, hk=64, hq=64, q_ld=64 * 128, pages=1), fc.FUSE_EUNSUPPORTED),
+    (dict(tokens=(1 << 24) - 1, hk=128, hq=128, q_ld=128 * 128, pages=1), fc.FUSE_EUNSUPPORTED),
     (dict(q=None), fc.FUSE_EINVAL),
     (dict(table=None), fc.FUSE_EINVAL),
     (dict(cu=None), fc.FUSE_EINVAL),
@@ -128,6 +129,7 @@ def test_dequantize_refusals(kw, want):
     (dict(K=48), fc.FUSE_EUNSUPPORTED),
     (dict(M=1 << 22), fc.FUSE_EUNSUPPORTED),
     (dict(N=1 << 22), fc.FUSE_EUNSUPPORTED),
+    (dict(M=(1 << 22) - 1, N=(1 << 22) - 1, K=2048), fc.FUSE_EUNSUPPORTED),
     (dict(gelu=2), fc.FUSE_EINVAL),
     (dict(dtype=fc.FUSE_F32), fc.FUSE_EINVAL),
     (dict(xs=None), fc.FUSE_EINVAL),
