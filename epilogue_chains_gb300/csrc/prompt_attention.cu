@@ -332,7 +332,8 @@ struct Layout {
     static_assert(SMEM > 116 * 1024, "one CTA per SM: each takes all of TMEM");
 };
 
-template <typename T, int D>
+// HALVES: the two halves of a block's weights as one piece of code (2), or as a loop (1).
+template <typename T, int D, int HALVES>
 __global__ void __launch_bounds__(Layout<D>::THREADS, 1) prompt_attention_kernel(const __grid_constant__ CUtensorMap mQ,
                                                                        const __grid_constant__ CUtensorMap mK,
                                                                        const __grid_constant__ CUtensorMap mV,
@@ -616,9 +617,8 @@ __global__ void __launch_bounds__(Layout<D>::THREADS, 1) prompt_attention_kernel
                 if (!wait(s_full(t), i)) break;
                 tc_fence_after();
                 // 64 keys at a time, so that the weights of the first half are multiplied with V while those of the second are
-                // computed, and half of P is free as soon as the last block's half has been multiplied.  (Not unrolled: the warps
-                // fetch half the instructions.  32 prompts to 1024 133 us, unrolled 144 to 153; one of 4096 126, unrolled 120.)
-#pragma unroll 1
+                // computed, and half of P is free as soon as the last block's half has been multiplied.
+#pragma unroll HALVES
                 for (int h = 0; h < 2; ++h) {
                     float x[32];         // keys 64 h + 32 hf .. of the block
                     tmem_ld_rows16(st + 64 * h, x);
@@ -954,7 +954,7 @@ Sizes sizes(int64_t tokens, int64_t hq, int64_t hk, int64_t D) {
 template <typename T, int D>
 int run_prompt(PromptArgs a, const void* q, int64_t q_ld, const void* k, const void* v, cudaStream_t st) {
     using L = Layout<D>;
-    const bool bf = std::is_same<T, __nv_bfloat16>::value;
+    constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
     const int box = 1 << (a.page_shift < 7 ? a.page_shift : 7);
     CUtensorMap mQ, mK, mV, mO;
     const int64_t dims[3] = {D, a.hq, a.tokens}, strides[2] = {D * 2, q_ld * 2}, o_strides[2] = {D * 2, static_cast<int64_t>(a.hq) * D * 2};
@@ -962,7 +962,14 @@ int run_prompt(PromptArgs a, const void* q, int64_t q_ld, const void* k, const v
     if (!make_map(&mK, k, a.cache_rows, D, 64, box, bf) || !make_map(&mV, v, a.cache_rows, D, 64, box, bf) ||
         !make_map_3d(&mQ, q, kMap16, dims, strides, qbox, 128) || !make_map_3d(&mO, a.o, kMap16, dims, o_strides, qbox, 128))
         return FUSE_ECUDA;
-    int rc = opt_in_smem((const void*)prompt_attention_kernel<T, D>, L::SMEM);
+    // D = 128 and short prompts: the loop, whose instructions the warps fetch half of.  In us, loop and one piece: 32 prompts to
+    // 1024 133 and 144 to 153, 8 of 2000 (28 heads, 4 for keys and values) 106 and 108 to 113; one of 4096 126 and 120.  With D = 64
+    // one piece is faster throughout (16 to 4096, 32 heads: 639 and 585; in fp16 it spills), with D = 256 they take the same.
+    constexpr int USUAL = D == 64 && bf ? 2 : 1;
+    auto* kernel = prompt_attention_kernel<T, D, USUAL>;
+    if constexpr (D == 128)
+        if (a.tokens >= 3000 * static_cast<int64_t>(a.batch)) kernel = prompt_attention_kernel<T, D, 2>;
+    int rc = opt_in_smem((const void*)kernel, L::SMEM);
     if (rc != FUSE_OK) return rc;
     // no more CTAs than there can be runs
     const int64_t ti = static_cast<int64_t>(a.tpt) * a.tiles, room = a.table_ld << a.page_shift;
@@ -970,7 +977,7 @@ int run_prompt(PromptArgs a, const void* q, int64_t q_ld, const void* k, const v
     int64_t grid = sm_count() < kGrid ? sm_count() : kGrid;
     const int64_t runs = items * ceil_div(room + kEntry, kLeastRun);
     if (grid > runs) grid = runs;
-    rc = launch_pdl(prompt_attention_kernel<T, D>, dim3(static_cast<unsigned>(grid)), dim3(L::THREADS), L::SMEM, st, 1, mQ, mK, mV, mO, a);
+    rc = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(L::THREADS), L::SMEM, st, 1, mQ, mK, mV, mO, a);
     // an item of at most one block of keys is nobody's to share
     if (rc != FUSE_OK || grid == 1 || room <= 128) return rc;
     return launch_pdl(prompt_join_kernel<T, D>, dim3(kJoinWarps / (kJoinThreads / 32), static_cast<unsigned>(grid - 1)),
@@ -979,21 +986,23 @@ int run_prompt(PromptArgs a, const void* q, int64_t q_ld, const void* k, const v
 
 }  // namespace
 
-int prompt_report_count() { return 12; }
+int prompt_report_count() { return 14; }
 int prompt_report(int i, fuse_kernel_record* out) {
     switch (i) {
-        FC_REPORT(0, Layout<64>::THREADS, Layout<64>::SMEM, 512, prompt_attention_kernel<__nv_bfloat16, 64>);
-        FC_REPORT(1, Layout<128>::THREADS, Layout<128>::SMEM, 512, prompt_attention_kernel<__nv_bfloat16, 128>);
-        FC_REPORT(2, Layout<256>::THREADS, Layout<256>::SMEM, 512, prompt_attention_kernel<__nv_bfloat16, 256>);
-        FC_REPORT(3, Layout<64>::THREADS, Layout<64>::SMEM, 512, prompt_attention_kernel<__half, 64>);
-        FC_REPORT(4, Layout<128>::THREADS, Layout<128>::SMEM, 512, prompt_attention_kernel<__half, 128>);
-        FC_REPORT(5, Layout<256>::THREADS, Layout<256>::SMEM, 512, prompt_attention_kernel<__half, 256>);
-        FC_REPORT(6, kJoinThreads, 0, 0, prompt_join_kernel<__nv_bfloat16, 64>);
-        FC_REPORT(7, kJoinThreads, 0, 0, prompt_join_kernel<__nv_bfloat16, 128>);
-        FC_REPORT(8, kJoinThreads, 0, 0, prompt_join_kernel<__nv_bfloat16, 256>);
-        FC_REPORT(9, kJoinThreads, 0, 0, prompt_join_kernel<__half, 64>);
-        FC_REPORT(10, kJoinThreads, 0, 0, prompt_join_kernel<__half, 128>);
-        FC_REPORT(11, kJoinThreads, 0, 0, prompt_join_kernel<__half, 256>);
+        FC_REPORT(0, Layout<64>::THREADS, Layout<64>::SMEM, 512, prompt_attention_kernel<__nv_bfloat16, 64, 2>);
+        FC_REPORT(1, Layout<128>::THREADS, Layout<128>::SMEM, 512, prompt_attention_kernel<__nv_bfloat16, 128, 1>);
+        FC_REPORT(2, Layout<128>::THREADS, Layout<128>::SMEM, 512, prompt_attention_kernel<__nv_bfloat16, 128, 2>);
+        FC_REPORT(3, Layout<256>::THREADS, Layout<256>::SMEM, 512, prompt_attention_kernel<__nv_bfloat16, 256, 1>);
+        FC_REPORT(4, Layout<64>::THREADS, Layout<64>::SMEM, 512, prompt_attention_kernel<__half, 64, 1>);
+        FC_REPORT(5, Layout<128>::THREADS, Layout<128>::SMEM, 512, prompt_attention_kernel<__half, 128, 1>);
+        FC_REPORT(6, Layout<128>::THREADS, Layout<128>::SMEM, 512, prompt_attention_kernel<__half, 128, 2>);
+        FC_REPORT(7, Layout<256>::THREADS, Layout<256>::SMEM, 512, prompt_attention_kernel<__half, 256, 1>);
+        FC_REPORT(8, kJoinThreads, 0, 0, prompt_join_kernel<__nv_bfloat16, 64>);
+        FC_REPORT(9, kJoinThreads, 0, 0, prompt_join_kernel<__nv_bfloat16, 128>);
+        FC_REPORT(10, kJoinThreads, 0, 0, prompt_join_kernel<__nv_bfloat16, 256>);
+        FC_REPORT(11, kJoinThreads, 0, 0, prompt_join_kernel<__half, 64>);
+        FC_REPORT(12, kJoinThreads, 0, 0, prompt_join_kernel<__half, 128>);
+        FC_REPORT(13, kJoinThreads, 0, 0, prompt_join_kernel<__half, 256>);
         default: return FUSE_EINVAL;
     }
 }
