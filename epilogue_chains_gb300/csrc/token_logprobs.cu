@@ -167,7 +167,7 @@ __device__ __forceinline__ void for_each(const Slice<T>& s, F&& f) {
 // The slice's alternatives in sh.best by one scan for each: the best that comes after the one before.  Logits of -inf (and
 // NaN, which counts as -inf) are left out.
 template <typename T>
-__device__ __noinline__ void scan_top(Shared& sh, const Slice<T>& s, int top) {
+__device__ __noinline__ void scan_top(Shared& sh, Slice<T> s, int top) {
     uint64_t last = ~uint64_t(0);
     for (int n = 0; n < top; ++n) {
         uint64_t best = 0;
