@@ -533,75 +533,75 @@ __global__ void __launch_bounds__(kPairThreads, 1) mxfp4_pair_kernel(const __gri
         return ok;
     };
     if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    if (warp == 0) {
-        // ---------------------------------------------------------------- loads; both CTAs' bytes count on the even one's barrier
-        if (lane == 0) {
-            prefetch_map(&mW);
-            prefetch_map(&mX);
-            prefetch_map(&mSW);
-            prefetch_map(&mSX);
-        }
-        const uint32_t one = elect_one();
-        int c = 0;
-        for (int t = cid; ok && t < tiles; t += clusters) {
-            int m0, n0;
-            tile_of(a, t, m0, n0);
-            for (int s = 0; s < nk; ++s, ++c) {
-                const int slot = c % ST;
-                if (c >= ST && !wait(empty(slot), c / ST - 1)) break;
-                if (rank == 0 && lane == 0) mbar_arrive_expect_tx(full(slot), 2 * L::STAGE);
-                __syncwarp();
-                const uint32_t at = base + slot * L::STAGE, bar = mapa_shared(full(slot), 0);
-                tma_load_2d_pair_if(one, at, &mW, s * 64, n0 + static_cast<int>(rank) * 128, bar);
-                tma_load_2d_pair_if(one, at + L::OFF_B, &mX, s * 64, m0 + static_cast<int>(rank) * 128, bar);
-                tma_load_3d_pair_if(one, at + L::OFF_SA, &mSW, s * 256, n0 / 128 + static_cast<int>(rank), 0, bar);
-                tma_load_3d_pair_if(one, at + L::OFF_SB, &mSX, s * 256, m0 / 128, 0, bar);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if (warp == 0) {
+            // ---------------------------------------------------------------- loads; both CTAs' bytes count on the even one's barrier
+            if (lane == 0) {
+                prefetch_map(&mW);
+                prefetch_map(&mX);
+                prefetch_map(&mSW);
+                prefetch_map(&mSX);
             }
-        }
-        if (!ok && rank == 0)   // both CTAs' copies in flight land before either's shared memory goes away
-            for (int j = max(0, c - ST); j < c; ++j) (void)mbar_wait_drain(full(j % ST), (j / ST) & 1);
-    } else if (warp == 1 && rank == 0) {
-        // ---------------------------------------------------------------- MMA issue, for both CTAs
-        const uint32_t one = elect_one();
-        const int mine = tiles > cid ? (tiles - 1 - cid) / clusters + 1 : 0, total = mine * nk;
-        int c = 0;
-        for (int i = 0; ok && i < mine; ++i) {
-            // this accumulator has been read (two tiles ago), and the columns that it shares with the other one
-            if (i > 1 && !wait(acc_done(i % 2), i / 2 - 1)) break;
-            if (i > 0 && !wait(acc_read, i - 1)) break;
-            tc_fence_after();
-            const uint32_t d = tmem + (i % 2 ? L::ACC1 : 0);
-            for (int s = 0; s < nk; ++s, ++c) {
-                const int slot = c % ST;
-                if (!wait(full(slot), c / ST)) break;
+            const uint32_t one = elect_one();
+            int c = 0;
+            for (int t = cid; ok && t < tiles; t += clusters) {
+                int m0, n0;
+                tile_of(a, t, m0, n0);
+                for (int s = 0; s < nk; ++s, ++c) {
+                    const int slot = c % ST;
+                    if (c >= ST && !wait(empty(slot), c / ST - 1)) break;
+                    if (rank == 0 && lane == 0) mbar_arrive_expect_tx(full(slot), 2 * L::STAGE);
+                    __syncwarp();
+                    const uint32_t at = base + slot * L::STAGE, bar = mapa_shared(full(slot), 0);
+                    tma_load_2d_pair_if(one, at, &mW, s * 64, n0 + static_cast<int>(rank) * 128, bar);
+                    tma_load_2d_pair_if(one, at + L::OFF_B, &mX, s * 64, m0 + static_cast<int>(rank) * 128, bar);
+                    tma_load_3d_pair_if(one, at + L::OFF_SA, &mSW, s * 256, n0 / 128 + static_cast<int>(rank), 0, bar);
+                    tma_load_3d_pair_if(one, at + L::OFF_SB, &mSX, s * 256, m0 / 128, 0, bar);
+                }
+            }
+            if (!ok && rank == 0)   // both CTAs' copies in flight land before either's shared memory goes away
+                for (int j = max(0, c - ST); j < c; ++j) (void)mbar_wait_drain(full(j % ST), (j / ST) & 1);
+        } else if (warp == 1 && rank == 0) {
+            // ---------------------------------------------------------------- MMA issue, for both CTAs
+            const uint32_t one = elect_one();
+            const int mine = tiles > cid ? (tiles - 1 - cid) / clusters + 1 : 0, total = mine * nk;
+            int c = 0;
+            for (int i = 0; ok && i < mine; ++i) {
+                // this accumulator has been read (two tiles ago), and the columns that it shares with the other one
+                if (i > 1 && !wait(acc_done(i % 2), i / 2 - 1)) break;
+                if (i > 0 && !wait(acc_read, i - 1)) break;
                 tc_fence_after();
-                const uint32_t at = base + slot * L::STAGE;
-                const int steps = min(4, (a.g.K - s * kStageK + 63) / 64);
+                const uint32_t d = tmem + (i % 2 ? L::ACC1 : 0);
+                for (int s = 0; s < nk; ++s, ++c) {
+                    const int slot = c % ST;
+                    if (!wait(full(slot), c / ST)) break;
+                    tc_fence_after();
+                    const uint32_t at = base + slot * L::STAGE;
+                    const int steps = min(4, (a.g.K - s * kStageK + 63) / 64);
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    if (2 * t < steps) {
-                        tc_cp_scales_pair_if(one, tmem + L::SFA_COL + 4 * t, scale_desc(at + L::OFF_SA + 512 * t));
-                        tc_cp_scales_pair_if(one, tmem + L::SFB_COL + 8 * t, scale_desc(at + L::OFF_SB + 512 * t));
-                        tc_cp_scales_pair_if(one, tmem + L::SFB_COL + 8 * t + 4, scale_desc(at + L::OFF_SB + 1024 + 512 * t));
-                    }
-                const uint64_t da = smem_desc_sw128(at, 16, 1024), db = smem_desc_sw128(at + L::OFF_B, 16, 1024);
+                    for (int t = 0; t < 2; ++t)
+                        if (2 * t < steps) {
+                            tc_cp_scales_pair_if(one, tmem + L::SFA_COL + 4 * t, scale_desc(at + L::OFF_SA + 512 * t));
+                            tc_cp_scales_pair_if(one, tmem + L::SFB_COL + 8 * t, scale_desc(at + L::OFF_SB + 512 * t));
+                            tc_cp_scales_pair_if(one, tmem + L::SFB_COL + 8 * t + 4, scale_desc(at + L::OFF_SB + 1024 + 512 * t));
+                        }
+                    const uint64_t da = smem_desc_sw128(at, 16, 1024), db = smem_desc_sw128(at + L::OFF_B, 16, 1024);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (k < steps)
-                        tc_mma_mxf4_pair_if(one, d, da + 2 * k, db + 2 * k, k % 2 ? idesc_mxf4(256, 256, 2) : idesc_mxf4(256, 256, 0),
-                                            tmem + L::SFA_COL + 4 * (k / 2), tmem + L::SFB_COL + 8 * (k / 2), s > 0 || k > 0 ? 1u : 0u);
-                // frees the stage in both CTAs, unless no later load uses it
-                if (c + ST < total) tc_commit_pair_mc_if(one, empty(slot), 0x3);
+                    for (int k = 0; k < 4; ++k)
+                        if (k < steps)
+                            tc_mma_mxf4_pair_if(one, d, da + 2 * k, db + 2 * k, k % 2 ? idesc_mxf4(256, 256, 2) : idesc_mxf4(256, 256, 0),
+                                                tmem + L::SFA_COL + 4 * (k / 2), tmem + L::SFB_COL + 8 * (k / 2), s > 0 || k > 0 ? 1u : 0u);
+                    // frees the stage in both CTAs, unless no later load uses it
+                    if (c + ST < total) tc_commit_pair_mc_if(one, empty(slot), 0x3);
+                }
+                if (ok) tc_commit_pair_mc_if(one, acc_full(i % 2), 0x3);
             }
-            if (ok) tc_commit_pair_mc_if(one, acc_full(i % 2), 0x3);
+            if (!ok && c > 0) {     // MMAs in flight finish before TMEM is freed
+                if (one) tc_commit_pair(drain);
+                __syncwarp();
+                (void)mbar_wait_drain(drain, 0);
+            }
         }
-        if (!ok && c > 0) {     // MMAs in flight finish before TMEM is freed
-            if (one) tc_commit_pair(drain);
-            __syncwarp();
-            (void)mbar_wait_drain(drain, 0);
-        }
-    }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
         // ---------------------------------------------------------------- epilogue: 32 weights by 64 tokens of a tile
