@@ -8,8 +8,8 @@
 // It is bound by the tensor cores: 4 D operations per query head and visible key.  An item is one key/value
 // head and the query rows of its group of heads for some consecutive tokens, token by token, so a tile of 128
 // rows spans few tokens where heads are grouped (less of the diagonal is computed in vain) and single tokens
-// still fill rows with their group.  With D <= 128 an item has two tiles of 128 rows against the same K and V
-// tiles, so that one tile's softmax runs while the tensor core works for the other.
+// still fill rows with their group.  An item has two tiles of 128 rows against the same K and V tiles: in one CTA,
+// where one tile's softmax runs while the tensor core works for the other, or with D = 256 in a pair of CTAs.
 //
 // Work is dealt out in equal runs: all items of the batch lie in one line, each counting for its visible keys
 // and an entry, and every CTA takes an equal run of it, whatever the lengths are.  What one CTA has of an item
@@ -19,6 +19,7 @@
 #include <cudaTypedefs.h>
 #include <math.h>
 
+#include <mutex>
 #include <type_traits>
 
 #include "fc_internal.cuh"
@@ -30,7 +31,7 @@ namespace fc {
 namespace {
 
 constexpr int kMaxBatch = 4096;
-constexpr int kGrid = 160;                 // most CTAs (workspace bound)
+constexpr int kGrid = 160;                 // most CTAs (workspace bound); half as many pairs of them
 // A running reference is replaced when a row's maximum exceeds it by more than 2^8, so weights stay
 // within [0, 2^8]; for fp16 weights it is also set 2^7 below the maximum, which uses fp16's range
 // upwards (2^15 at most) and keeps weights down to 2^-21 of the maximum at full precision.
@@ -71,14 +72,14 @@ struct PromptArgs {
     int batch, tokens, hq, hk, group;
     int recip;                         // row / group = row recip >> 16 for rows below 128
     uint64_t item_recip;               // ceil(2^32 / (tpt tiles))
-    int tpt, tiles;                    // tokens of a tile of 128 rows; tiles of an item (1 or 2)
+    int tpt, tiles;                    // tokens of a tile of 128 rows; tiles of an item (2)
     int page_shift, num_pages, cache_rows;
     float c;                           // scale * log2(e)
     // workspace: where each CTA's run begins, and the parts of items that CTAs share: of CTA c slot 2 c has the part of
     // an item that began in an earlier CTA, slot 2 c + 1 that of one which begins here and goes on in a later one
     int4* start;                       // [kGrid + 1]
-    float2* ml;                        // [2 kGrid][rows]
-    float* po;                         // [2 kGrid][rows][D]
+    float2* ml;                        // [2 for each run][rows]
+    float* po;                         // [2 for each run][rows][D]
     int rows;
     int *flag, *bad;
 };
@@ -223,9 +224,9 @@ struct Walk {
         return false;
     }
 };
-// Where this CTA's run begins and where the next's does, for all threads; `scratch` is 80 * 8 bytes of shared memory.
+// Where run `me` of `runs` begins and where the next does, for all threads; `scratch` is 80 * 8 bytes of shared memory.
 template <int THREADS>
-__device__ __forceinline__ void find_runs(const PromptArgs& a, int64_t* scratch, Pos (&run)[2]) {
+__device__ __forceinline__ void find_runs(const PromptArgs& a, int me, int runs, int64_t* scratch, Pos (&run)[2]) {
     constexpr int WARPS = THREADS / 32;
     static_assert(WARPS <= 24, "scratch");
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -235,7 +236,7 @@ __device__ __forceinline__ void find_runs(const PromptArgs& a, int64_t* scratch,
     for (int i = 0; i < per; ++i) {
         const int b = tid * per + i;
         if (b >= a.batch) break;
-        const Seq s = seq_of(a, b, blockIdx.x == 0 ? a.bad : nullptr);
+        const Seq s = seq_of(a, b, me == 0 ? a.bad : nullptr);
         const int items = items_of(a, s);
         mine += a.hk * places(a, s, items, items);
         count += a.hk * items;
@@ -264,12 +265,12 @@ __device__ __forceinline__ void find_runs(const PromptArgs& a, int64_t* scratch,
         items += counts[w];
     }
     // Equal runs, but none shorter than an item of kLeastRun or the average one: with few short items a CTA for each.
-    int64_t len = quotient(total + gridDim.x - 1, gridDim.x), least = items > 0 ? quotient(total + items - 1, items) : 1;
+    int64_t len = quotient(total + runs - 1, runs), least = items > 0 ? quotient(total + items - 1, items) : 1;
     if (least > kLeastRun) least = kLeastRun;
     if (len < least) len = least;
     const int snap = len < kLeastRun ? 4 : static_cast<int>(min(len >> 12, static_cast<int64_t>(64)));
     for (int w = 0; w < 2; ++w) {
-        const int64_t x = static_cast<int64_t>(blockIdx.x + w) * len;
+        const int64_t x = static_cast<int64_t>(me + w) * len;
         if (x < upto && x >= upto - mine) {            // this thread's sequences have it
             target[2 * w] = tid;
             target[2 * w + 1] = x - (upto - mine);
@@ -309,12 +310,12 @@ constexpr int kSegs = 4;                            // segments that the walk is
 
 template <int D>
 struct Layout {
-    static constexpr int TILES = D <= 128 ? 2 : 1;
+    static constexpr int TILES = 2;
     static constexpr int THREADS = 32 * (4 + kTileWarps * TILES);
     // Registers of a thread at the launch, and then of the first four warps and of the softmax's: within what the launch has.
-    static constexpr int REGS = TILES == 2 ? 96 : 168, FEW = TILES == 2 ? 64 : 96, MANY = TILES == 2 ? 104 : 200;
+    static constexpr int REGS = 96, FEW = 64, MANY = 104;
     static_assert(128 * (FEW + kTileWarps / 4 * TILES * MANY) <= THREADS * REGS, "registers");
-    static constexpr int RING = D == 64 ? 6 : D == 128 ? 3 : 2;    // K and V tiles
+    static constexpr int RING = D == 64 ? 6 : 3;                    // K and V tiles
     static constexpr uint32_t REGION = 128 * 128;              // one 64-column atom of 128 rows
     static constexpr uint32_t TILE = REGION * (D / 64);
     static constexpr uint32_t P_BYTES = 128 * 128 * 2;
@@ -397,7 +398,7 @@ __global__ void __launch_bounds__(Layout<D>::THREADS, 1) prompt_attention_kernel
     pdl_wait();
 
     Pos run[2];
-    find_runs<L::THREADS>(a, reinterpret_cast<int64_t*>(gbase + L::OFF_SCRATCH), run);
+    find_runs<L::THREADS>(a, blockIdx.x, gridDim.x, reinterpret_cast<int64_t*>(gbase + L::OFF_SCRATCH), run);
     if (threadIdx.x == 0) {
         a.start[blockIdx.x] = make_int4(run[0].b, run[0].h, run[0].i, run[0].t);
         if (blockIdx.x + 1 == gridDim.x) a.start[gridDim.x] = make_int4(run[1].b, run[1].h, run[1].i, run[1].t);
@@ -429,164 +430,164 @@ __global__ void __launch_bounds__(Layout<D>::THREADS, 1) prompt_attention_kernel
     };
 
     if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::FEW));
-    if (warp == 0) {
-        // ---------------------------------------------------------------- Q, K and V loads
-        const uint32_t one = elect_one();
-        const int box_shift = min(a.page_shift, 7);
-        const uint32_t q_box = static_cast<uint32_t>(a.group * a.tpt) * 128u;
-        int c = 0, slot = 0, kc = 0, vc = 0, segs = 0;    // loads, the next one's slot, K and V tiles, items
-        uint32_t phase = 1;
-        for (int k = 0; ok && segment(k); ++k) {
-            const Seg g = segs_at[k % kSegs];
-            leave(k);
-            const int n = g.steps();
-            if (n == 0) continue;
-            if (segs > 0 && !wait(q_free, segs - 1)) break;
-            const int tiles = g.n1 > 0 ? TILES : 1;
-            if (lane == 0) mbar_arrive_expect_tx(q_full, tiles * (D / 64) * q_box);
-            __syncwarp();
-            for (int t = 0; t < tiles; ++t)
-#pragma unroll
-                for (int x = 0; x < D / 64; ++x)
-                    tma_load_3d_if(one, base + L::OFF_Q + t * L::TILE + x * L::REGION, &mQ, 64 * x, g.h * a.group, g.q0 + g.tok0 + t * a.tpt, q_full);
-            ++segs;
-            const int32_t* table = a.table + static_cast<int64_t>(g.b) * a.table_ld;
-            for (int x = 0; x < 2 * n; ++x, ++c) {
-                // x-th load of the item: K for 0 and odd x below 2 n - 1, V for the others
-                const bool is_k = x == 0 || (x % 2 == 1 && x < 2 * n - 1);
-                const int j = is_k ? (x + 1) / 2 : (x == 2 * n - 1 ? n - 1 : x / 2 - 1);
-                const int key0 = (g.t0 + j) * 128, nk = min(128, g.L - key0), nbox = (nk + (1 << box_shift) - 1) >> box_shift;
-                const int key = key0 + (lane << box_shift);
-                int row = a.cache_rows;         // past the cache: zeros
-                if (lane < nbox) {
-                    const int page = table[key >> a.page_shift];
-                    if (page >= 0 && page < a.num_pages)
-                        row = ((page * a.hk + g.h) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
-                    else
-                        atomicExch(a.bad, 1);
-                }
-                if (c >= RING && !wait(empty(slot), phase)) break;
-                const uint32_t full = is_k ? k_full(kc++ % kFull) : v_full(vc++ % kFull);
-                const uint32_t dst = base + L::OFF_KV + slot * L::TILE;
-                if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(nbox << box_shift) * (D * 2));
-                __syncwarp();
-                for (int y = 0; y < nbox; ++y) {
-                    const int r = __shfl_sync(0xffffffffu, row, y);
-#pragma unroll
-                    for (int e = 0; e < D / 64; ++e)
-                        tma_load_2d_if(one, dst + e * L::REGION + ((static_cast<uint32_t>(y) << box_shift) * 128), is_k ? &mK : &mV, 64 * e, r, full);
-                }
-                if (++slot == RING) {
-                    slot = 0;
-                    phase ^= 1u;
-                }
-            }
-        }
-        if (!ok) {   // copies in flight land before the shared memory goes away
-            if (segs > 0) (void)mbar_wait_drain(q_full, (segs - 1) & 1);
-            for (int i = max(0, kc - kFull); i < kc; ++i) (void)mbar_wait_drain(k_full(i % kFull), (i / kFull) & 1);
-            for (int i = max(0, vc - kFull); i < vc; ++i) (void)mbar_wait_drain(v_full(i % kFull), (i / kFull) & 1);
-        }
-        __syncwarp();
-    } else if (warp == 1 || warp == 2) {
-        // ---------------------------------------------------------------- MMA issue: S by warp 1, PV by warp 2
-        const uint32_t one = elect_one();
-        bool issued = false;
-        int c = 0, kv = 0, segs = 0;      // loads and K (or V) tiles of the items before this one; items
-        int i[2] = {0, 0};                // products of each tile so far
-        if (warp == 1) {
-            constexpr uint32_t idS = idesc_f16(128, 128, false, false, BF);
-            const uint64_t dq = smem_desc_sw128(base + L::OFF_Q, 16, 1024), dk = smem_desc_sw128(base + L::OFF_KV, 16, 1024);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::FEW));
+        if (warp == 0) {
+            // ---------------------------------------------------------------- Q, K and V loads
+            const uint32_t one = elect_one();
+            const int box_shift = min(a.page_shift, 7);
+            const uint32_t q_box = static_cast<uint32_t>(a.group * a.tpt) * 128u;
+            int c = 0, slot = 0, kc = 0, vc = 0, segs = 0;    // loads, the next one's slot, K and V tiles, items
+            uint32_t phase = 1;
             for (int k = 0; ok && segment(k); ++k) {
                 const Seg g = segs_at[k % kSegs];
                 leave(k);
                 const int n = g.steps();
                 if (n == 0) continue;
-                if (!wait(q_full, segs)) break;
-                for (int j = 0; ok && j < n; ++j) {
-                    const int slot = (c + k_at(j)) % RING;
-                    const uint64_t kd = dk + static_cast<uint64_t>(slot * (L::TILE >> 4));
-                    if (!wait(k_full((kv + j) % kFull), (kv + j) / kFull)) break;
+                if (segs > 0 && !wait(q_free, segs - 1)) break;
+                const int tiles = g.n1 > 0 ? TILES : 1;
+                if (lane == 0) mbar_arrive_expect_tx(q_full, tiles * (D / 64) * q_box);
+                __syncwarp();
+                for (int t = 0; t < tiles; ++t)
 #pragma unroll
-                    for (int t = 0; t < TILES; ++t) {
-                        if (j >= (t == 0 ? g.n0 : g.n1)) continue;
-                        if (i[t] > 0 && !wait(s_free(t), i[t] - 1)) break;
-                        ++i[t];
-                        tc_fence_after();
-                        const uint64_t qd = dq + static_cast<uint64_t>(t * (L::TILE >> 4));
-#pragma unroll
-                        for (int s = 0; s < D / 16; ++s)
-                            tc_mma_if(one, tmem + t * 128, qd + ((s / 4) * (L::REGION >> 4) + (s % 4) * 2),
-                                      kd + ((s / 4) * (L::REGION >> 4) + (s % 4) * 2), idS, s > 0 ? 1u : 0u);
-                        tc_commit_if(one, s_full(t));
-                        issued = true;
-                    }
-                    if (ok) tc_commit_if(one, empty(slot));
-                }
-                if (ok) tc_commit_if(one, q_free);
+                    for (int x = 0; x < D / 64; ++x)
+                        tma_load_3d_if(one, base + L::OFF_Q + t * L::TILE + x * L::REGION, &mQ, 64 * x, g.h * a.group, g.q0 + g.tok0 + t * a.tpt, q_full);
                 ++segs;
-                kv += n;
-                c += 2 * n;
-            }
-        } else {
-            constexpr uint32_t idO = idesc_f16(128, D, false, true, BF);
-            const uint64_t dp = smem_desc_sw128(base + L::OFF_P, 16, 1024), dv = smem_desc_sw128(base + L::OFF_KV, L::REGION, 1024);
-            for (int k = 0; ok && segment(k); ++k) {
-                const Seg g = segs_at[k % kSegs];
-                leave(k);
-                const int n = g.steps();
-                for (int j = 0; ok && j < n; ++j) {
-                    const int slot = (c + v_at(j, n)) % RING;
-                    const uint64_t vd = dv + static_cast<uint64_t>(slot * (L::TILE >> 4));
-                    if (!wait(v_full((kv + j) % kFull), (kv + j) / kFull)) break;
-#pragma unroll
-                    for (int t = 0; t < TILES; ++t) {
-                        if (j >= (t == 0 ? g.n0 : g.n1)) continue;
-                        const uint64_t pd = dp + static_cast<uint64_t>(t * (L::P_BYTES >> 4));
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (!wait(p_full(t, h), i[t])) break;
-                            tc_fence_after();
-#pragma unroll
-                            for (int s = 4 * h; s < 4 * h + 4; ++s)   // 16 keys each
-                                tc_mma_if(one, tmem + L::O_COL + t * D, pd + ((s / 4) * (L::REGION >> 4) + (s % 4) * 2), vd + s * (2048 >> 4), idO,
-                                          j > 0 || s > 0 ? 1u : 0u);
-                            tc_commit_if(one, o_done(t, h));
-                            issued = true;
-                        }
-                        ++i[t];
+                const int32_t* table = a.table + static_cast<int64_t>(g.b) * a.table_ld;
+                for (int x = 0; x < 2 * n; ++x, ++c) {
+                    // x-th load of the item: K for 0 and odd x below 2 n - 1, V for the others
+                    const bool is_k = x == 0 || (x % 2 == 1 && x < 2 * n - 1);
+                    const int j = is_k ? (x + 1) / 2 : (x == 2 * n - 1 ? n - 1 : x / 2 - 1);
+                    const int key0 = (g.t0 + j) * 128, nk = min(128, g.L - key0), nbox = (nk + (1 << box_shift) - 1) >> box_shift;
+                    const int key = key0 + (lane << box_shift);
+                    int row = a.cache_rows;         // past the cache: zeros
+                    if (lane < nbox) {
+                        const int page = table[key >> a.page_shift];
+                        if (page >= 0 && page < a.num_pages)
+                            row = ((page * a.hk + g.h) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+                        else
+                            atomicExch(a.bad, 1);
                     }
-                    if (ok) tc_commit_if(one, empty(slot));
+                    if (c >= RING && !wait(empty(slot), phase)) break;
+                    const uint32_t full = is_k ? k_full(kc++ % kFull) : v_full(vc++ % kFull);
+                    const uint32_t dst = base + L::OFF_KV + slot * L::TILE;
+                    if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(nbox << box_shift) * (D * 2));
+                    __syncwarp();
+                    for (int y = 0; y < nbox; ++y) {
+                        const int r = __shfl_sync(0xffffffffu, row, y);
+#pragma unroll
+                        for (int e = 0; e < D / 64; ++e)
+                            tma_load_2d_if(one, dst + e * L::REGION + ((static_cast<uint32_t>(y) << box_shift) * 128), is_k ? &mK : &mV, 64 * e, r, full);
+                    }
+                    if (++slot == RING) {
+                        slot = 0;
+                        phase ^= 1u;
+                    }
                 }
-                kv += n;
-                c += 2 * n;
             }
-        }
-        if (!ok && issued) {   // MMAs in flight finish before TMEM is freed
-            tc_commit_if(one, drain(warp - 1));
-            (void)mbar_wait_drain(drain(warp - 1), 0);
-        }
-        __syncwarp();
-    } else {
-        // ---------------------------------------------------------------- the walk along the run, ahead of the others
-        Walk walk;
-        walk.begin(a, run[0], run[1]);
-        Seg g;
-        for (int k = 0;; ++k) {
-            const bool more = walk.next(a, g);
-            if (!more) g.b = -1;
-            if (k >= kSegs && !wait(seg_free(k), k / kSegs - 1)) break;
-            if (lane == 0) {
-                segs_at[k % kSegs] = g;
-                mbar_arrive(seg_full(k));
+            if (!ok) {   // copies in flight land before the shared memory goes away
+                if (segs > 0) (void)mbar_wait_drain(q_full, (segs - 1) & 1);
+                for (int i = max(0, kc - kFull); i < kc; ++i) (void)mbar_wait_drain(k_full(i % kFull), (i / kFull) & 1);
+                for (int i = max(0, vc - kFull); i < vc; ++i) (void)mbar_wait_drain(v_full(i % kFull), (i / kFull) & 1);
             }
             __syncwarp();
-            if (!more) break;
+        } else if (warp == 1 || warp == 2) {
+            // ---------------------------------------------------------------- MMA issue: S by warp 1, PV by warp 2
+            const uint32_t one = elect_one();
+            bool issued = false;
+            int c = 0, kv = 0, segs = 0;      // loads and K (or V) tiles of the items before this one; items
+            int i[2] = {0, 0};                // products of each tile so far
+            if (warp == 1) {
+                constexpr uint32_t idS = idesc_f16(128, 128, false, false, BF);
+                const uint64_t dq = smem_desc_sw128(base + L::OFF_Q, 16, 1024), dk = smem_desc_sw128(base + L::OFF_KV, 16, 1024);
+                for (int k = 0; ok && segment(k); ++k) {
+                    const Seg g = segs_at[k % kSegs];
+                    leave(k);
+                    const int n = g.steps();
+                    if (n == 0) continue;
+                    if (!wait(q_full, segs)) break;
+                    for (int j = 0; ok && j < n; ++j) {
+                        const int slot = (c + k_at(j)) % RING;
+                        const uint64_t kd = dk + static_cast<uint64_t>(slot * (L::TILE >> 4));
+                        if (!wait(k_full((kv + j) % kFull), (kv + j) / kFull)) break;
+#pragma unroll
+                        for (int t = 0; t < TILES; ++t) {
+                            if (j >= (t == 0 ? g.n0 : g.n1)) continue;
+                            if (i[t] > 0 && !wait(s_free(t), i[t] - 1)) break;
+                            ++i[t];
+                            tc_fence_after();
+                            const uint64_t qd = dq + static_cast<uint64_t>(t * (L::TILE >> 4));
+#pragma unroll
+                            for (int s = 0; s < D / 16; ++s)
+                                tc_mma_if(one, tmem + t * 128, qd + ((s / 4) * (L::REGION >> 4) + (s % 4) * 2),
+                                          kd + ((s / 4) * (L::REGION >> 4) + (s % 4) * 2), idS, s > 0 ? 1u : 0u);
+                            tc_commit_if(one, s_full(t));
+                            issued = true;
+                        }
+                        if (ok) tc_commit_if(one, empty(slot));
+                    }
+                    if (ok) tc_commit_if(one, q_free);
+                    ++segs;
+                    kv += n;
+                    c += 2 * n;
+                }
+            } else {
+                constexpr uint32_t idO = idesc_f16(128, D, false, true, BF);
+                const uint64_t dp = smem_desc_sw128(base + L::OFF_P, 16, 1024), dv = smem_desc_sw128(base + L::OFF_KV, L::REGION, 1024);
+                for (int k = 0; ok && segment(k); ++k) {
+                    const Seg g = segs_at[k % kSegs];
+                    leave(k);
+                    const int n = g.steps();
+                    for (int j = 0; ok && j < n; ++j) {
+                        const int slot = (c + v_at(j, n)) % RING;
+                        const uint64_t vd = dv + static_cast<uint64_t>(slot * (L::TILE >> 4));
+                        if (!wait(v_full((kv + j) % kFull), (kv + j) / kFull)) break;
+#pragma unroll
+                        for (int t = 0; t < TILES; ++t) {
+                            if (j >= (t == 0 ? g.n0 : g.n1)) continue;
+                            const uint64_t pd = dp + static_cast<uint64_t>(t * (L::P_BYTES >> 4));
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                if (!wait(p_full(t, h), i[t])) break;
+                                tc_fence_after();
+#pragma unroll
+                                for (int s = 4 * h; s < 4 * h + 4; ++s)   // 16 keys each
+                                    tc_mma_if(one, tmem + L::O_COL + t * D, pd + ((s / 4) * (L::REGION >> 4) + (s % 4) * 2), vd + s * (2048 >> 4), idO,
+                                              j > 0 || s > 0 ? 1u : 0u);
+                                tc_commit_if(one, o_done(t, h));
+                                issued = true;
+                            }
+                            ++i[t];
+                        }
+                        if (ok) tc_commit_if(one, empty(slot));
+                    }
+                    kv += n;
+                    c += 2 * n;
+                }
+            }
+            if (!ok && issued) {   // MMAs in flight finish before TMEM is freed
+                tc_commit_if(one, drain(warp - 1));
+                (void)mbar_wait_drain(drain(warp - 1), 0);
+            }
+            __syncwarp();
+        } else {
+            // ---------------------------------------------------------------- the walk along the run, ahead of the others
+            Walk walk;
+            walk.begin(a, run[0], run[1]);
+            Seg g;
+            for (int k = 0;; ++k) {
+                const bool more = walk.next(a, g);
+                if (!more) g.b = -1;
+                if (k >= kSegs && !wait(seg_free(k), k / kSegs - 1)) break;
+                if (lane == 0) {
+                    segs_at[k % kSegs] = g;
+                    mbar_arrive(seg_full(k));
+                }
+                __syncwarp();
+                if (!more) break;
+            }
         }
-    }
     } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::MANY));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::MANY));
         // ---------------------------------------------------------------- softmax: threads l and l + 16 of a warp, one row
         const int t = (warp - 4) / kTileWarps, u = (warp - 4) % kTileWarps, r0 = 32 * (warp % 4) + 16 * (u / 4), r = r0 + lane % 16, hf = lane / 16;
         const uint32_t lanes = static_cast<uint32_t>(r0) << 16;
@@ -793,6 +794,467 @@ __global__ void __launch_bounds__(Layout<D>::THREADS, 1) prompt_attention_kernel
     }
 }
 
+// ================================================================== D = 256: a pair of CTAs
+// TMEM holds one output of 256 columns next to a tile of scores, so the two tiles of an item lie in two CTAs, which act as one
+// M = 256 unit (cta_group::2): CTA t of the pair has tile t's queries, weights and output, and of every block of K and V one half
+// (64 keys; 128 columns), which leaves room for two blocks of each and takes half the bytes to every SM.  P is in TMEM, two
+// blocks in turn.  CTA 0 issues all products; the bytes of both CTAs count on its barriers, its commits signal both.  The rest is
+// as above.  (8 prompts to 2048 with 16 heads: 123.7 us.  One CTA by itself, a K or V tile of 64 KB at a time, took 151 us.)
+struct PairLayout {
+    static constexpr int THREADS = 32 * (4 + kTileWarps);
+    static constexpr uint32_t Q_REGION = 128 * 128, K_REGION = 64 * 128, V_REGION = 128 * 128;   // 64-column atoms
+    static constexpr uint32_t K_BYTES = 4 * K_REGION, V_BYTES = 2 * V_REGION;
+    static constexpr uint32_t OFF_Q = 0, OFF_K = 4 * Q_REGION, OFF_V = OFF_K + 2 * K_BYTES, OFF_OUT = OFF_V + 2 * V_BYTES;
+    static constexpr uint32_t OFF_BAR = OFF_OUT + 2 * Q_REGION;
+    static constexpr int N_BARS = 2 + 8 + 2 + 4 + 2 + 1 + 2 + 2 * kSegs + 2;
+    static constexpr uint32_t OFF_HOLD = OFF_BAR + N_BARS * 8;
+    static constexpr uint32_t OFF_SCRATCH = (OFF_HOLD + 16 + 7) / 8 * 8;
+    static constexpr uint32_t OFF_SEG = OFF_SCRATCH + 80 * 8;
+    static constexpr uint32_t SMEM = OFF_SEG + kSegs * sizeof(Seg) + 1024;
+    static constexpr uint32_t P_COL = 128, O_COL = 256;        // scores at 0
+    static_assert(SMEM <= 232448, "shared-memory budget");
+    static_assert(SMEM > 116 * 1024, "one CTA per SM: each takes all of TMEM");
+};
+
+template <typename T>
+__global__ void __launch_bounds__(PairLayout::THREADS, 1) prompt_pair_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
+                                                                             const __grid_constant__ CUtensorMap mV, const __grid_constant__ CUtensorMap mO,
+                                                                             const __grid_constant__ PromptArgs a) {
+    using L = PairLayout;
+    constexpr int D = 256;
+    constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    uint8_t* gbase = smem_raw + (base - smem_addr(smem_raw));
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
+    const int rank = static_cast<int>(cluster_rank()), pair = static_cast<int>(blockIdx.x) / 2, pairs = static_cast<int>(gridDim.x) / 2;
+    const uint32_t bar0 = base + L::OFF_BAR;
+    // of CTA 0: what is loaded, what both CTAs' softmax warps hand over
+    const uint32_t q_full = bar0;
+    auto k_full = [&](int i) { return bar0 + 8u * (1 + i % 2); };
+    auto v_full = [&](int i) { return bar0 + 8u * (3 + i % 2); };
+    const uint32_t s_free = bar0 + 8u * 5;
+    auto p_full = [&](int i, int h) { return bar0 + 8u * (6 + 2 * (i % 2) + h); };      // block i's weights, 64 keys
+    // of each CTA
+    const uint32_t q_free = bar0 + 8u * 10, s_full = bar0 + 8u * 11;
+    auto k_free = [&](int i) { return bar0 + 8u * (12 + i % 2); };
+    auto v_free = [&](int i) { return bar0 + 8u * (14 + i % 2); };
+    auto o_done = [&](int i) { return bar0 + 8u * (16 + i % 2); };                      // block i's product with V
+    const uint32_t v_here = bar0 + 8u * 18;                                             // a V block that has to be patched has landed
+    const uint32_t out_full = bar0 + 8u * 19, out_free = bar0 + 8u * 20;
+    auto seg_full = [&](int i) { return bar0 + 8u * (21 + i % kSegs); };
+    auto seg_free = [&](int i) { return bar0 + 8u * (21 + kSegs + i % kSegs); };
+    auto drain = [&](int w) { return bar0 + 8u * (21 + 2 * kSegs + w); };
+    static_assert(23 + 2 * kSegs <= L::N_BARS, "barriers");
+    int* flag = a.flag;
+    if (threadIdx.x == 0) {
+        mbar_init(q_full, 1);
+        mbar_init(q_free, 1);
+        mbar_init(s_full, 1);
+        mbar_init(s_free, 2 * kTileWarps);
+        mbar_init(v_here, 1);
+        mbar_init(out_full, kTileWarps);
+        mbar_init(out_free, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(k_full(i), 1);
+            mbar_init(v_full(i), 1);
+            mbar_init(k_free(i), 1);
+            mbar_init(v_free(i), 1);
+            mbar_init(o_done(i), 1);
+            mbar_init(p_full(i, 0), 2 * kTileWarps);
+            mbar_init(p_full(i, 1), 2 * kTileWarps);
+            mbar_init(drain(i), 1);
+        }
+        for (int i = 0; i < kSegs; ++i) {
+            mbar_init(seg_full(i), 1);
+            mbar_init(seg_free(i), (rank == 0 ? 3 : 1) + kTileWarps);
+        }
+        fence_mbar_init();
+    }
+    if (threadIdx.x == 32 * 4) {
+        prefetch_map(&mQ);
+        prefetch_map(&mK);
+        prefetch_map(&mV);
+        prefetch_map(&mO);
+    }
+    const uint32_t tmem = tmem_begin_pair(base + L::OFF_HOLD, gbase + L::OFF_HOLD, 512, warp);
+    pdl_wait();
+
+    Pos run[2];
+    find_runs<L::THREADS>(a, pair, pairs, reinterpret_cast<int64_t*>(gbase + L::OFF_SCRATCH), run);
+    if (threadIdx.x == 0 && rank == 0) {
+        a.start[pair] = make_int4(run[0].b, run[0].h, run[0].i, run[0].t);
+        if (pair + 1 == pairs) a.start[pairs] = make_int4(run[1].b, run[1].h, run[1].i, run[1].t);
+    }
+    Seg* segs_at = reinterpret_cast<Seg*>(gbase + L::OFF_SEG);
+    bool ok = true;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        for (uint32_t n = 0; !__all_sync(0xffffffffu, mbar_try_wait(bar, parity & 1u)); ++n)
+            if (n >= kMostTries || (n % 64 == 63 && *reinterpret_cast<volatile int*>(flag) != 0)) {
+                atomicExch(flag, 1);
+                ok = false;
+                break;
+            }
+        return ok;
+    };
+    auto segment = [&](int k) {
+        if (!wait(seg_full(k), k / kSegs)) return false;
+        return segs_at[k % kSegs].b >= 0;
+    };
+    auto leave = [&](int k) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(seg_free(k));
+    };
+
+    if (warp < 4) {
+        if (warp == 0) {
+            // ---------------------------------------------------------------- loads: this CTA's queries, keys and columns of V
+            const uint32_t one = elect_one();
+            const int k_shift = min(a.page_shift, 6), v_shift = min(a.page_shift, 7);
+            const uint32_t q_box = static_cast<uint32_t>(a.group * a.tpt) * 128u;
+            int kc = 0, vc = 0, segs = 0;
+            const uint32_t q_bar = mapa_shared(q_full, 0);
+            for (int k = 0; ok && segment(k); ++k) {
+                const Seg g = segs_at[k % kSegs];
+                leave(k);
+                const int n = g.steps();
+                if (n == 0) continue;
+                if (segs > 0 && !wait(q_free, segs - 1)) break;
+                if (rank == 0 && lane == 0) mbar_arrive_expect_tx(q_full, (g.n1 > 0 ? 2 : 1) * 4 * q_box);
+                __syncwarp();
+                if (rank == 0 || g.n1 > 0)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        tma_load_3d_pair_if(one, base + L::OFF_Q + x * L::Q_REGION, &mQ, 64 * x, g.h * a.group, g.q0 + g.tok0 + rank * a.tpt, q_bar);
+                ++segs;
+                const int32_t* table = a.table + static_cast<int64_t>(g.b) * a.table_ld;
+                // the cache row of a key, or one past the cache: zeros
+                auto row_of = [&](int key) {
+                    const int page = table[key >> a.page_shift];
+                    if (page >= 0 && page < a.num_pages) return ((page * a.hk + g.h) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+                    atomicExch(a.bad, 1);
+                    return a.cache_rows;
+                };
+                for (int x = 0; x < 2 * n; ++x) {
+                    // K(0), then K(j + 1) before V(j)
+                    const bool is_k = x == 0 || (x % 2 == 1 && x < 2 * n - 1);
+                    const int j = is_k ? (x + 1) / 2 : (x == 2 * n - 1 ? n - 1 : x / 2 - 1);
+                    const int key0 = (g.t0 + j) * 128, nk = min(128, g.L - key0);
+                    if (is_k) {
+                        const int mine = min(max(nk - 64 * rank, 0), 64), box = 1 << k_shift, boxes = (mine + box - 1) >> k_shift;
+                        const int all = ((min(nk, 64) + box - 1) >> k_shift) + ((max(nk - 64, 0) + box - 1) >> k_shift);
+                        const int row = lane < boxes ? row_of(key0 + 64 * rank + (lane << k_shift)) : 0;
+                        if (kc >= 2 && !wait(k_free(kc), kc / 2 - 1)) break;
+                        if (rank == 0 && lane == 0) mbar_arrive_expect_tx(k_full(kc), static_cast<uint32_t>(all << k_shift) * (D * 2));
+                        __syncwarp();
+                        const uint32_t dst = base + L::OFF_K + kc % 2 * L::K_BYTES, bar = mapa_shared(k_full(kc), 0);
+                        for (int y = 0; y < boxes; ++y) {
+                            const int r = __shfl_sync(0xffffffffu, row, y);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                tma_load_2d_pair_if(one, dst + e * L::K_REGION + ((static_cast<uint32_t>(y) << k_shift) * 128), &mK, 64 * e, r, bar);
+                        }
+                        ++kc;
+                    } else {
+                        const int box = 1 << v_shift, boxes = (nk + box - 1) >> v_shift;
+                        const int row = lane < boxes ? row_of(key0 + (lane << v_shift)) : 0;
+                        if (vc >= 2 && !wait(v_free(vc), vc / 2 - 1)) break;
+                        if (rank == 0 && lane == 0) mbar_arrive_expect_tx(v_full(vc), static_cast<uint32_t>(boxes << v_shift) * (D * 2));
+                        __syncwarp();
+                        const uint32_t dst = base + L::OFF_V + vc % 2 * L::V_BYTES, bar = mapa_shared(v_full(vc), 0);
+                        for (int y = 0; y < boxes; ++y) {
+                            const int r = __shfl_sync(0xffffffffu, row, y);
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                tma_load_2d_pair_if(one, dst + e * L::V_REGION + ((static_cast<uint32_t>(y) << v_shift) * 128), &mV, 128 * rank + 64 * e, r, bar);
+                        }
+                        ++vc;
+                    }
+                }
+            }
+            if (!ok && rank == 0) {   // both CTAs' copies in flight land before either's shared memory goes away
+                if (segs > 0) (void)mbar_wait_drain(q_full, (segs - 1) & 1);
+                for (int i = max(0, kc - 2); i < kc; ++i) (void)mbar_wait_drain(k_full(i), (i / 2) & 1);
+                for (int i = max(0, vc - 2); i < vc; ++i) (void)mbar_wait_drain(v_full(i), (i / 2) & 1);
+            }
+            __syncwarp();
+        } else if (rank == 0 && warp < 3) {
+            // ---------------------------------------------------------------- MMA issue for both CTAs: S by warp 1, PV by warp 2
+            const uint32_t one = elect_one();
+            bool issued = false;
+            int i = 0, segs = 0;         // blocks and items so far
+            if (warp == 1) {
+                constexpr uint32_t idS = idesc_f16(256, 128, false, false, BF);
+                const uint64_t dq = smem_desc_sw128(base + L::OFF_Q, 16, 1024);
+                for (int k = 0; ok && segment(k); ++k) {
+                    const Seg g = segs_at[k % kSegs];
+                    leave(k);
+                    const int n = g.steps();
+                    if (n == 0) continue;
+                    if (!wait(q_full, segs)) break;
+                    for (int j = 0; j < n; ++j, ++i) {
+                        if (!wait(k_full(i), i / 2) || (i > 0 && !wait(s_free, i - 1))) break;
+                        tc_fence_after();
+                        const uint64_t dk = smem_desc_sw128(base + L::OFF_K + i % 2 * L::K_BYTES, 16, 1024);
+#pragma unroll
+                        for (int s = 0; s < D / 16; ++s)
+                            tc_mma_pair_if(one, tmem, dq + ((s / 4) * (L::Q_REGION >> 4) + (s % 4) * 2), dk + ((s / 4) * (L::K_REGION >> 4) + (s % 4) * 2), idS,
+                                           s > 0 ? 1u : 0u);
+                        tc_commit_pair_mc_if(one, s_full, 0x3);
+                        tc_commit_pair_mc_if(one, k_free(i), 0x3);
+                        issued = true;
+                    }
+                    if (ok) tc_commit_pair_mc_if(one, q_free, 0x3);
+                    ++segs;
+                }
+            } else {
+                constexpr uint32_t idO = idesc_f16(256, D, false, true, BF);
+                for (int k = 0; ok && segment(k); ++k) {
+                    const Seg g = segs_at[k % kSegs];
+                    leave(k);
+                    const int n = g.steps();
+                    for (int j = 0; ok && j < n; ++j, ++i) {
+                        if (!wait(v_full(i), i / 2)) break;
+                        if (g.L - (g.t0 + j) * 128 < 128 && lane < 2) mbar_arrive_cluster_release(mapa_shared(v_here, lane));
+                        __syncwarp();
+                        const uint64_t dv = smem_desc_sw128(base + L::OFF_V + i % 2 * L::V_BYTES, L::V_REGION, 1024);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (!wait(p_full(i, h), i / 2)) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int s = 4 * h; s < 4 * h + 4; ++s)   // 16 keys each
+                                tc_mma_pair_ts_if(one, tmem + L::O_COL, tmem + L::P_COL + 64 * (i % 2) + 8 * s, dv + s * (2048 >> 4), idO, j > 0 || s > 0 ? 1u : 0u);
+                            issued = true;
+                        }
+                        if (!ok) break;
+                        tc_commit_pair_mc_if(one, v_free(i), 0x3);
+                        tc_commit_pair_mc_if(one, o_done(i), 0x3);
+                    }
+                }
+            }
+            if (!ok && issued) {   // MMAs in flight finish before TMEM is freed
+                if (one) tc_commit_pair(drain(warp - 1));
+                __syncwarp();
+                (void)mbar_wait_drain(drain(warp - 1), 0);
+            }
+            __syncwarp();
+        } else if (warp == 3) {
+            // ---------------------------------------------------------------- the walk along the run, ahead of the others
+            Walk walk;
+            walk.begin(a, run[0], run[1]);
+            Seg g;
+            for (int k = 0;; ++k) {
+                const bool more = walk.next(a, g);
+                if (!more) g.b = -1;
+                if (k >= kSegs && !wait(seg_free(k), k / kSegs - 1)) break;
+                if (lane == 0) {
+                    segs_at[k % kSegs] = g;
+                    mbar_arrive(seg_full(k));
+                }
+                __syncwarp();
+                if (!more) break;
+            }
+        }
+    } else {
+        // ---------------------------------------------------------------- softmax: threads l and l + 16 of a warp, one row
+        const int u = warp - 4, r0 = 32 * (warp % 4) + 16 * (u / 4), r = r0 + lane % 16, hf = lane / 16;
+        const uint32_t st = tmem + (static_cast<uint32_t>(r0) << 16), ot = st + L::O_COL;
+        const uint32_t s_free0 = mapa_shared(s_free, 0);
+        const bool stores = u == 0 && lane == 0;
+        constexpr float SH = Shift<T>::V;
+        int i = 0, patched = 0, outs = 0;             // blocks, blocks with a patched V, outputs so far
+        bool held = false;
+        auto out_ready = [&]() {
+            if (!held) return true;
+            held = false;
+            if (stores) {
+                bulk_wait_read0();
+                mbar_arrive(out_free);
+            }
+            return wait(out_free, outs - 1);
+        };
+        for (int k = 0; ok && segment(k); ++k) {
+            const Seg& g = segs_at[k % kSegs];
+            const int n = rank == 0 ? g.n0 : g.n1, steps = g.steps();
+            const int partial = ((g.L - g.n + g.tok0 + rank * a.tpt + 1) >> 7) - g.t0;
+            float m = -INFINITY, l = 0.0f;
+            for (int j = 0; j < steps; ++j, ++i) {
+                if (!wait(s_full, i)) break;
+                tc_fence_after();
+                float x[64];         // keys 32 hf .. and 64 + 32 hf .. of the block
+                tmem_ld_rows16(st, x);
+                tmem_ld_rows16(st + 64, x + 32);
+                tmem_ld_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(s_free0);
+                float alpha = 1.0f;
+                if (j < n) {
+                    if (j >= partial) {
+                        const int left = g.L - g.n + g.tok0 + rank * a.tpt + (r * a.recip >> 16) + 1 - (g.t0 + j) * 128 - 32 * hf;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            if (__any_sync(0xffffffffu, left - 64 * h < 32)) {
+#pragma unroll
+                                for (int y = 0; y < 32; ++y) x[32 * h + y] = y >= left - 64 * h ? -INFINITY : x[32 * h + y];
+                            }
+                    }
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int y = 0; y < 64; y += 2) mx[(y >> 1) & 3] = max3f(mx[(y >> 1) & 3], x[y], x[y + 1]);
+                    float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.c;
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                    if (top > m + (SH + kLag)) {
+                        if (j > 0) alpha = ex2f(m - (top - SH));
+                        m = top - SH;
+                    }
+                }
+                if (i >= 2 && !wait(o_done(i), i / 2 - 1)) break;          // this block's place in P is free
+                if (__any_sync(0xffffffffu, alpha != 1.0f)) {              // rare: the last block's product is waited for
+                    if (!wait(o_done(i - 1), (i - 1) / 2)) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int y = 0; y < D / 64; ++y) {
+                        float o[32];
+                        tmem_ld_rows16(ot + 64 * y, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] *= alpha;
+                        tmem_st_rows16(ot + 64 * y, o);
+                    }
+                    tmem_st_wait();
+                }
+                tc_fence_after();
+                const float ref = m == -INFINITY ? 0.0f : m;
+                const float2 c2 = make_float2(a.c, a.c), nm2 = make_float2(-ref, -ref);
+                float2 sum2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t w[16];      // rounded to T, as in the kernel above; a tile that sees nothing of the block: 0
+#pragma unroll
+                    for (int y = 0; y < 16; ++y) w[y] = 0u;
+                    if (j < n)
+#pragma unroll
+                        for (int y = 0; y < 16; ++y) {
+                            const float2 e = __ffma2_rn(make_float2(x[32 * h + 2 * y], x[32 * h + 2 * y + 1]), c2, nm2);
+                            const float2 p = make_float2(ex2f(e.x), ex2f(e.y));
+                            sum2 = __fadd2_rn(sum2, p);
+                            w[y] = pack2<T>(p.x, p.y);
+                        }
+                    tmem_st_pairs16(st + L::P_COL + 64 * (i % 2) + 32 * h, w);
+                    tmem_st_wait();
+                    bool far = false;    // what is handed over is in shared memory as well
+                    if (h == 0) {
+                        const int kleft = g.L - (g.t0 + j) * 128;
+                        if (kleft < 128) {       // V rows past the sequence's end: 0 x whatever lies there must be 0
+                            if (!wait(v_here, patched)) break;
+                            ++patched;
+                            uint8_t* vb = gbase + L::OFF_V + i % 2 * L::V_BYTES;
+                            for (int v = 32 * u + lane; v < (128 - kleft) * 16; v += 32 * kTileWarps) {
+                                const int row = kleft + v / 16, ch = v % 16;
+                                *reinterpret_cast<uint4*>(vb + (ch / 8) * L::V_REGION + row * 128 + (ch % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                            }
+                            fence_async_smem();
+                            far = true;
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (far) mbar_arrive_cluster_release(mapa_shared(p_full(i, h), 0));
+                        else mbar_arrive_cluster(mapa_shared(p_full(i, h), 0));
+                    }
+                }
+                if (!ok) break;
+                l = l * alpha + (sum2.x + sum2.y);
+            }
+            if (!ok || (steps > 0 && !wait(o_done(i - 1), (i - 1) / 2))) break;
+            tc_fence_after();
+            l += __shfl_xor_sync(0xffffffffu, l, 16);
+            const int tok0 = g.tok0 + rank * a.tpt;
+            if (g.whole) {
+                // 128 columns at a time through shared memory: a whole tile is stored from there by a copy, of one that ends within
+                // the sequence each warp stores its rows, 16 lanes to a row
+                const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
+                const bool full = tok0 + a.tpt <= g.n;
+#pragma unroll 1
+                for (int w0 = 0; w0 < D && tok0 < g.n; w0 += 128) {
+                    if (!out_ready()) break;
+                    uint8_t* mine = gbase + L::OFF_OUT;
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        float o[32];
+                        if (n > 0) {
+                            tmem_ld_rows16(ot + w0 + 64 * y, o);
+                            tmem_ld_wait();
+                        }
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t v[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) v[e] = n == 0 || l == 0.0f ? 0u : pack2<T>(o[8 * q + 2 * e] * inv, o[8 * q + 2 * e + 1] * inv);
+                            *reinterpret_cast<uint4*>(mine + y * L::Q_REGION + r * 128 + (((4 * hf + q) ^ (r & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+                        }
+                    }
+                    if (full) {
+                        fence_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(out_full);
+                        if (u == 0) {
+                            if (!wait(out_full, outs)) break;
+                            if (lane == 0) {
+#pragma unroll
+                                for (int y = 0; y < 2; ++y)
+                                    tma_store_3d(&mO, w0 + 64 * y, g.h * a.group, g.q0 + tok0, base + L::OFF_OUT + y * L::Q_REGION);
+                                bulk_commit();
+                            }
+                            __syncwarp();
+                        }
+                        held = true;
+                        ++outs;
+                    } else {
+                        __syncwarp();
+                        const int ch = lane % 16;
+                        T* out = static_cast<T*>(a.o) + (static_cast<int64_t>(g.q0 + tok0) * a.hq + g.h * a.group) * D + w0 + 8 * ch;
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) {
+                            const int row = r0 + 2 * y + lane / 16, rt = row * a.recip >> 16;
+                            if (rt < a.tpt && tok0 + rt < g.n)
+                                *reinterpret_cast<uint4*>(out + (static_cast<int64_t>(rt) * a.hq + row - rt * a.group) * D) =
+                                    *reinterpret_cast<const uint4*>(mine + (ch / 8) * L::Q_REGION + row * 128 + (((ch % 8) ^ (row & 7)) << 4));
+                        }
+                        __syncwarp();
+                    }
+                }
+            } else {
+                const int rt = r * a.recip >> 16, tok = tok0 + rt;
+                const bool in = rt < a.tpt && tok < g.n;
+                const int64_t at = static_cast<int64_t>(2 * pair + (g.t0 == 0 ? 1 : 0)) * a.rows + rank * 128 + r;
+                if (in && hf == 0) a.ml[at] = make_float2(m, l);
+                float* dst = a.po + at * D + 32 * hf;
+                if (n > 0)
+#pragma unroll 1
+                    for (int y = 0; y < D / 64; ++y) {
+                        float o[32];
+                        tmem_ld_rows16(ot + 64 * y, o);
+                        tmem_ld_wait();
+                        if (in)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) st_v8(dst + 64 * y + 8 * e, o + 8 * e);
+                    }
+            }
+            tc_fence_before();
+            leave(k);
+        }
+        if (stores) bulk_wait0();      // shared memory goes away
+    }
+    tc_fence_before();
+    cluster_sync();  // neither CTA leaves while its peer may still signal it
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
 // ================================================================== join
 // The parts of an item that several CTAs share.  Every run that begins within an item brings kJoinWarps warps, among which the
 // item's rows are shared out: four rows to a warp where two CTAs share the item, one where many do.  It is bound by latency: of
@@ -936,8 +1398,8 @@ struct Sizes {
 };
 Sizes sizes(int64_t tokens, int64_t hq, int64_t hk, int64_t D) {
     Sizes s{};
-    const int64_t group = hq / hk, tpt = 128 / group, tiles = D <= 128 ? 2 : 1;
-    s.rows = tokens <= tpt ? tokens * group : tiles * 128;
+    const int64_t group = hq / hk, tpt = 128 / group;
+    s.rows = tokens <= tpt ? tokens * group : 256;
     size_t at = (kGrid + 1) * sizeof(int4);
     auto part = [&](int64_t n) {
         at = (at + 255) / 256 * 256;
@@ -945,43 +1407,86 @@ Sizes sizes(int64_t tokens, int64_t hq, int64_t hk, int64_t D) {
         at += static_cast<size_t>(n);
         return was;
     };
-    s.ml = part(2 * kGrid * s.rows * 8);
-    s.po = part(2 * kGrid * s.rows * D * 4);
+    const int64_t runs = D == 256 ? kGrid / 2 : kGrid;
+    s.ml = part(2 * runs * s.rows * 8);
+    s.po = part(2 * runs * s.rows * D * 4);
     s.bytes = (at + 255) / 256 * 256;
     return s;
 }
 
+// Pairs of CTAs that can be resident at once.
+int pairs_resident() {
+    static std::mutex mu;
+    static int cached[64] = {0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+        (void)cudaGetLastError();
+        return 1;
+    }
+    std::lock_guard<std::mutex> lock(mu);
+    if (cached[dev] == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2 * static_cast<unsigned>(sm_count()));
+        cfg.blockDim = dim3(PairLayout::THREADS);
+        cfg.dynamicSmemBytes = PairLayout::SMEM;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = 2;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (opt_in_smem((const void*)prompt_pair_kernel<__half>, PairLayout::SMEM) != FUSE_OK ||
+            cudaOccupancyMaxActiveClusters(&n, prompt_pair_kernel<__half>, &cfg) != cudaSuccess || n < 1) {
+            (void)cudaGetLastError();
+            n = sm_count() / 2;
+        }
+        cached[dev] = n > 0 ? n : 1;
+    }
+    return cached[dev];
+}
+
 template <typename T, int D>
 int run_prompt(PromptArgs a, const void* q, int64_t q_ld, const void* k, const void* v, cudaStream_t st) {
-    using L = Layout<D>;
     constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
-    const int box = 1 << (a.page_shift < 7 ? a.page_shift : 7);
+    const int box = 1 << (a.page_shift < 7 ? a.page_shift : 7), k_box = D == 256 && box > 64 ? 64 : box;
     CUtensorMap mQ, mK, mV, mO;
     const int64_t dims[3] = {D, a.hq, a.tokens}, strides[2] = {D * 2, q_ld * 2}, o_strides[2] = {D * 2, static_cast<int64_t>(a.hq) * D * 2};
     const int qbox[3] = {64, a.group, a.tpt};
-    if (!make_map(&mK, k, a.cache_rows, D, 64, box, bf) || !make_map(&mV, v, a.cache_rows, D, 64, box, bf) ||
+    if (!make_map(&mK, k, a.cache_rows, D, 64, k_box, bf) || !make_map(&mV, v, a.cache_rows, D, 64, box, bf) ||
         !make_map_3d(&mQ, q, kMap16, dims, strides, qbox, 128) || !make_map_3d(&mO, a.o, kMap16, dims, o_strides, qbox, 128))
         return FUSE_ECUDA;
-    // D = 128 and short prompts: the loop, whose instructions the warps fetch half of.  In us, loop and one piece: 32 prompts to
-    // 1024 133 and 144 to 153, 8 of 2000 (28 heads, 4 for keys and values) 106 and 108 to 113; one of 4096 126 and 120.  With D = 64
-    // one piece is faster throughout (16 to 4096, 32 heads: 639 and 585; in fp16 it spills), with D = 256 they take the same.
-    constexpr int USUAL = D == 64 && bf ? 2 : 1;
-    auto* kernel = prompt_attention_kernel<T, D, USUAL>;
-    if constexpr (D == 128)
-        if (a.tokens >= 3000 * static_cast<int64_t>(a.batch)) kernel = prompt_attention_kernel<T, D, 2>;
-    int rc = opt_in_smem((const void*)kernel, L::SMEM);
-    if (rc != FUSE_OK) return rc;
-    // no more CTAs than there can be runs
+    // no more runs than there can be
     const int64_t ti = static_cast<int64_t>(a.tpt) * a.tiles, room = a.table_ld << a.page_shift;
     const int64_t items = (ceil_div(a.tokens, ti) + (a.batch < a.tokens ? a.batch : a.tokens)) * a.hk;
-    int64_t grid = sm_count() < kGrid ? sm_count() : kGrid;
-    const int64_t runs = items * ceil_div(room + kEntry, kLeastRun);
-    if (grid > runs) grid = runs;
-    rc = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(L::THREADS), L::SMEM, st, 1, mQ, mK, mV, mO, a);
+    const int64_t most = items * ceil_div(room + kEntry, kLeastRun);
+    int64_t runs;
+    int rc;
+    if constexpr (D == 256) {
+        runs = pairs_resident() < kGrid / 2 ? pairs_resident() : kGrid / 2;
+        if (runs > most) runs = most;
+        rc = opt_in_smem((const void*)prompt_pair_kernel<T>, PairLayout::SMEM);
+        if (rc != FUSE_OK) return rc;
+        rc = launch_pdl(prompt_pair_kernel<T>, dim3(static_cast<unsigned>(2 * runs)), dim3(PairLayout::THREADS), PairLayout::SMEM, st, 2, mQ, mK, mV, mO, a);
+    } else {
+        using L = Layout<D>;
+        // D = 128 and short prompts: the loop, whose instructions the warps fetch half of.  In us, loop and one piece: 32 prompts to
+        // 1024 133 and 144 to 153, 8 of 2000 (28 heads, 4 for keys and values) 106 and 108 to 113; one of 4096 126 and 120.  With D = 64
+        // one piece is faster throughout (16 to 4096, 32 heads: 639 and 585; in fp16 it spills).
+        constexpr int USUAL = D == 64 && bf ? 2 : 1;
+        auto* kernel = prompt_attention_kernel<T, D, USUAL>;
+        if constexpr (D == 128)
+            if (a.tokens >= 3000 * static_cast<int64_t>(a.batch)) kernel = prompt_attention_kernel<T, D, 2>;
+        rc = opt_in_smem((const void*)kernel, L::SMEM);
+        if (rc != FUSE_OK) return rc;
+        runs = sm_count() < kGrid ? sm_count() : kGrid;
+        if (runs > most) runs = most;
+        rc = launch_pdl(kernel, dim3(static_cast<unsigned>(runs)), dim3(L::THREADS), L::SMEM, st, 1, mQ, mK, mV, mO, a);
+    }
     // an item of at most one block of keys is nobody's to share
-    if (rc != FUSE_OK || grid == 1 || room <= 128) return rc;
-    return launch_pdl(prompt_join_kernel<T, D>, dim3(kJoinWarps / (kJoinThreads / 32), static_cast<unsigned>(grid - 1)),
-                      dim3(kJoinThreads), 0, st, 1, a, static_cast<int>(grid));
+    if (rc != FUSE_OK || runs == 1 || room <= 128) return rc;
+    return launch_pdl(prompt_join_kernel<T, D>, dim3(kJoinWarps / (kJoinThreads / 32), static_cast<unsigned>(runs - 1)), dim3(kJoinThreads), 0, st, 1, a,
+                      static_cast<int>(runs));
 }
 
 }  // namespace
@@ -992,11 +1497,11 @@ int prompt_report(int i, fuse_kernel_record* out) {
         FC_REPORT(0, Layout<64>::THREADS, Layout<64>::SMEM, 512, prompt_attention_kernel<__nv_bfloat16, 64, 2>);
         FC_REPORT(1, Layout<128>::THREADS, Layout<128>::SMEM, 512, prompt_attention_kernel<__nv_bfloat16, 128, 1>);
         FC_REPORT(2, Layout<128>::THREADS, Layout<128>::SMEM, 512, prompt_attention_kernel<__nv_bfloat16, 128, 2>);
-        FC_REPORT(3, Layout<256>::THREADS, Layout<256>::SMEM, 512, prompt_attention_kernel<__nv_bfloat16, 256, 1>);
+        FC_REPORT(3, PairLayout::THREADS, PairLayout::SMEM, 512, prompt_pair_kernel<__nv_bfloat16>);
         FC_REPORT(4, Layout<64>::THREADS, Layout<64>::SMEM, 512, prompt_attention_kernel<__half, 64, 1>);
         FC_REPORT(5, Layout<128>::THREADS, Layout<128>::SMEM, 512, prompt_attention_kernel<__half, 128, 1>);
         FC_REPORT(6, Layout<128>::THREADS, Layout<128>::SMEM, 512, prompt_attention_kernel<__half, 128, 2>);
-        FC_REPORT(7, Layout<256>::THREADS, Layout<256>::SMEM, 512, prompt_attention_kernel<__half, 256, 1>);
+        FC_REPORT(7, PairLayout::THREADS, PairLayout::SMEM, 512, prompt_pair_kernel<__half>);
         FC_REPORT(8, kJoinThreads, 0, 0, prompt_join_kernel<__nv_bfloat16, 64>);
         FC_REPORT(9, kJoinThreads, 0, 0, prompt_join_kernel<__nv_bfloat16, 128>);
         FC_REPORT(10, kJoinThreads, 0, 0, prompt_join_kernel<__nv_bfloat16, 256>);
@@ -1059,7 +1564,7 @@ extern "C" int fuse_prompt_attention(const void* q, int64_t q_ld, const void* k_
     a.group = static_cast<int>(group);
     a.recip = static_cast<int>((65536 + group - 1) / group);
     a.tpt = static_cast<int>(128 / group);
-    a.tiles = D <= 128 ? 2 : 1;
+    a.tiles = 2;
     a.item_recip = ((uint64_t(1) << 32) + a.tpt * a.tiles - 1) / (a.tpt * a.tiles);
     while ((1 << a.page_shift) < page_size) ++a.page_shift;
     a.num_pages = static_cast<int>(num_pages);

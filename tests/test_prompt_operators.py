@@ -182,7 +182,7 @@ def test_sizes_are_host_arithmetic():
     # where 160 runs begin, then (m, l) and fp32 rows of two parts for each of at most 160 CTAs
     assert ws(1000, 32, 8, 128) == 2816 + 320 * 256 * 8 + 320 * 256 * 128 * 4
     assert ws(100000, 32, 8, 128) == ws(1000, 32, 8, 128)
-    assert ws(1000, 32, 8, 256) == 2816 + 320 * 128 * 8 + 320 * 128 * 256 * 4       # one tile of rows
+    assert ws(1000, 32, 8, 256) == 2816 + 320 * 128 * 8 + 320 * 128 * 256 * 4       # of 80 pairs of CTAs
     assert ws(17, 32, 8, 128) == 2816 + 320 * 68 * 8 + 320 * 68 * 128 * 4           # 17 tokens of four heads in one tile
     assert ws(1, 30, 8, 128) == 0 and ws(0, 32, 8, 128) == 0 and ws(1, 129, 1, 128) == 0
     assert fc.fuse_mxfp4_scale_bytes(1, 32) == 512
