@@ -588,14 +588,19 @@ def fuse_prompt_attention(q, k_cache, v_cache, block_table, cu_queries, seq_lens
     torch = _torch or _bind_torch()
     dt, i32 = q.dtype, torch.int32
     dev = _decode_operands(dt, (k_cache, v_cache, o), ((block_table, i32), (cu_queries, i32), (seq_lens, i32)))
-    tokens, q_heads, D = q.shape
-    pages, kv_heads, page_size, D2 = k_cache.shape
-    if (q.get_device() != dev or q.stride(2) != 1 or (q_heads > 1 and q.stride(1) != D)):
+    shape, cache = q.shape, k_cache.shape        # (each such call to torch costs the host 0.2 us or more)
+    tokens, q_heads, D = shape
+    pages, kv_heads, page_size, D2 = cache
+    ld, head, one = q.stride()
+    if q.get_device() != dev or one != 1 or (q_heads > 1 and head != D):
         raise ValueError("q must be on the device of the others, each row of it contiguous")
-    if (D2 != D or o.shape != q.shape or v_cache.shape != k_cache.shape or block_table.dim() != 2
-            or seq_lens.shape != (block_table.shape[0],) or cu_queries.shape != (block_table.shape[0] + 1,)):
+    if D2 != D or o.shape != shape or v_cache.shape != cache or block_table.dim() != 2:
         raise ValueError("shape mismatch")
-    ld = q.stride(0) if tokens > 1 else q_heads * D
+    batch, table_ld = block_table.shape
+    if seq_lens.shape != (batch,) or cu_queries.shape != (batch + 1,):
+        raise ValueError("shape mismatch")
+    if tokens <= 1:
+        ld = q_heads * D
     lib, sh = _load(), _stream(stream)
     own = workspace is None
     if not own and (workspace.get_device() != dev or not workspace.is_contiguous()):
@@ -606,8 +611,8 @@ def fuse_prompt_attention(q, k_cache, v_cache, block_table, cu_queries, seq_lens
         if own:
             workspace = _prompt_workspace(fuse_prompt_attention_workspace_bytes(tokens, q_heads, kv_heads, D), dev, sh)
         status = lib.fuse_prompt_attention(q.data_ptr(), ld, k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-                                           block_table.shape[1], cu_queries.data_ptr(), seq_lens.data_ptr(), o.data_ptr(),
-                                           tokens, block_table.shape[0], q_heads, kv_heads, D, pages, page_size, scale,
+                                           table_ld, cu_queries.data_ptr(), seq_lens.data_ptr(), o.data_ptr(),
+                                           tokens, batch, q_heads, kv_heads, D, pages, page_size, scale,
                                            FUSE_F16 if dt is torch.float16 else FUSE_BF16, workspace.data_ptr(),
                                            workspace.nbytes, sh)
     finally:
@@ -647,12 +652,13 @@ def fuse_mxfp4_quantize(x, q, scales, stream=None) -> None:
     torch = _torch or _bind_torch()
     code = _float_code(x.dtype)
     _on_device(x.get_device(), (q, torch.uint8), (scales, torch.uint8))
-    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+    shape, strides = x.shape, x.stride()
+    if len(shape) != 2 or (shape[1] > 1 and strides[1] != 1):
         raise ValueError("x must be a 2-D tensor with unit column stride")
-    rows, cols = x.shape
+    rows, cols = shape
     if q.shape != (rows, cols // 2) or scales.numel() < fuse_mxfp4_scale_bytes(rows, cols):
         raise ValueError("shape mismatch")
-    _check(_load().fuse_mxfp4_quantize(x.data_ptr(), x.stride(0) if rows > 1 else cols, q.data_ptr(), scales.data_ptr(),
+    _check(_load().fuse_mxfp4_quantize(x.data_ptr(), strides[0] if rows > 1 else cols, q.data_ptr(), scales.data_ptr(),
                                        rows, cols, code, _stream(stream)), "fuse_mxfp4_quantize")
 
 
@@ -702,19 +708,21 @@ def fuse_token_logprobs(logits, tokens, logprob, entropy=None, top_logprob=None,
     code = _float_code(logits.dtype)
     f32, i32 = torch.float32, torch.int32
     _on_device(logits.get_device(), (tokens, i32), (logprob, f32), (entropy, f32), (top_logprob, f32), (top_index, i32))
-    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+    shape, strides = logits.shape, logits.stride()
+    if len(shape) != 2 or (shape[1] > 1 and strides[1] != 1):
         raise ValueError("logits must be a 2-D tensor with unit column stride")
-    rows, vocab = logits.shape
+    rows, vocab = shape
     top = 0
     for t in (top_logprob, top_index):
         if t is not None:
-            if t.dim() != 2 or t.shape[0] != rows or (top and t.shape[1] != top):
+            shape = t.shape
+            if len(shape) != 2 or shape[0] != rows or (top and shape[1] != top):
                 raise ValueError("shape mismatch")
-            top = t.shape[1]
+            top = shape[1]
     for t in (tokens, logprob, entropy):
         if t is not None and t.shape != (rows,):
             raise ValueError("shape mismatch")
-    _check(_load().fuse_token_logprobs(logits.data_ptr(), logits.stride(0) if rows > 1 else vocab, _ptr(tokens), _ptr(logprob),
+    _check(_load().fuse_token_logprobs(logits.data_ptr(), strides[0] if rows > 1 else vocab, _ptr(tokens), _ptr(logprob),
                                        _ptr(entropy), _ptr(top_logprob), _ptr(top_index), rows, vocab, top, scale, code,
                                        _stream(stream)), "fuse_token_logprobs")
 
