@@ -621,6 +621,9 @@ __global__ void __launch_bounds__(Layout<D>::THREADS, 1) prompt_attention_kernel
                 // computed, and half of P is free as soon as the last block's half has been multiplied.
 #pragma unroll HALVES
                 for (int h = 0; h < 2; ++h) {
+                    // Asked here, needed below: a wait takes 200 cycles also where nothing is left to wait for, of 2800 that a step
+                    // takes (32 prompts to 1024 134 -> 128.5 us; one vote for both rare cases below: 127).
+                    const bool taken = mbar_test(o_done(t, h), (i - 1) & 1);
                     float x[32];         // keys 64 h + 32 hf .. of the block
                     tmem_ld_rows16(st + 64 * h, x);
                     tmem_ld_wait();
@@ -648,7 +651,9 @@ __global__ void __launch_bounds__(Layout<D>::THREADS, 1) prompt_attention_kernel
                         m = top - SH;
                     }
                     if (h == 0 && j == 0 && !p_ready()) break;
-                    if (i > 0 && !wait(o_done(t, h), i - 1)) break;
+                    // (D = 64 in one piece: the second vote's alpha, kept for longer, spills)
+                    const bool plain = __all_sync(0xffffffffu, taken && (HALVES == 2 || alpha == 1.0f));
+                    if (!plain && !wait(o_done(t, h), i - 1)) break;
                     const float ref = m == -INFINITY ? 0.0f : m;
                     const float2 c2 = make_float2(a.c, a.c), nm2 = make_float2(-ref, -ref);
                     float2 sum2 = make_float2(0.0f, 0.0f);
@@ -666,7 +671,7 @@ __global__ void __launch_bounds__(Layout<D>::THREADS, 1) prompt_attention_kernel
                         }
                         st_shared_v4((p_at ^ (q << 4)) + h * L::REGION, w);
                     }
-                    if (__any_sync(0xffffffffu, alpha != 1.0f)) {      // rare: what has been issued of this tile's PV is waited for
+                    if ((HALVES == 2 || !plain) && __any_sync(0xffffffffu, alpha != 1.0f)) {      // rare: what has been issued of this tile's PV is waited for
                         if (!(h == 0 ? wait(o_done(t, 1), i - 1) : wait(o_done(t, 0), i))) break;
                         tc_fence_after();
 #pragma unroll 1
@@ -1082,6 +1087,7 @@ __global__ void __launch_bounds__(PairLayout::THREADS, 1) prompt_pair_kernel(con
             for (int j = 0; j < steps; ++j, ++i) {
                 if (!wait(s_full, i)) break;
                 tc_fence_after();
+                const bool taken = mbar_test(o_done(i), (i / 2 - 1) & 1);      // this block's place in P is free
                 float x[64];         // keys 32 hf .. and 64 + 32 hf .. of the block
                 tmem_ld_rows16(st, x);
                 tmem_ld_rows16(st + 64, x + 32);
@@ -1110,8 +1116,9 @@ __global__ void __launch_bounds__(PairLayout::THREADS, 1) prompt_pair_kernel(con
                         m = top - SH;
                     }
                 }
-                if (i >= 2 && !wait(o_done(i), i / 2 - 1)) break;          // this block's place in P is free
-                if (__any_sync(0xffffffffu, alpha != 1.0f)) {              // rare: the last block's product is waited for
+                const bool plain = __all_sync(0xffffffffu, taken && alpha == 1.0f);
+                if (!plain && !wait(o_done(i), i / 2 - 1)) break;
+                if (!plain && __any_sync(0xffffffffu, alpha != 1.0f)) {    // rare: the last block's product is waited for
                     if (!wait(o_done(i - 1), (i - 1) / 2)) break;
                     tc_fence_after();
 #pragma unroll 1
