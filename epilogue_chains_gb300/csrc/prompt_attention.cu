@@ -72,6 +72,7 @@ struct PromptArgs {
     int batch, tokens, hq, hk, group;
     int recip;                         // row / group = row recip >> 16 for rows below 128
     uint64_t item_recip;               // ceil(2^32 / (tpt tiles))
+    bool o_sectors;                    // o lies on a 32-byte boundary
     int tpt, tiles;                    // tokens of a tile of 128 rows; tiles of an item (2)
     int page_shift, num_pages, cache_rows;
     float c;                           // scale * log2(e)
@@ -804,14 +805,14 @@ __global__ void __launch_bounds__(Layout<D>::THREADS, 1) prompt_attention_kernel
 // M = 256 unit (cta_group::2): CTA t of the pair has tile t's queries, weights and output, and of every block of K and V one half
 // (64 keys; 128 columns), which leaves room for two blocks of each and takes half the bytes to every SM.  P is in TMEM, two
 // blocks in turn.  CTA 0 issues all products; the bytes of both CTAs count on its barriers, its commits signal both.  The rest is
-// as above.  (8 prompts to 2048 with 16 heads: 123.7 us.  One CTA by itself, a K or V tile of 64 KB at a time, took 151 us.)
+// as above.  (8 prompts to 2048 with 16 heads: 109 us.  One CTA by itself, a K or V tile of 64 KB at a time, took 151 us.)
 struct PairLayout {
     static constexpr int THREADS = 32 * (4 + kTileWarps);
     static constexpr uint32_t Q_REGION = 128 * 128, K_REGION = 64 * 128, V_REGION = 128 * 128;   // 64-column atoms
     static constexpr uint32_t K_BYTES = 4 * K_REGION, V_BYTES = 2 * V_REGION;
-    static constexpr uint32_t OFF_Q = 0, OFF_K = 4 * Q_REGION, OFF_V = OFF_K + 2 * K_BYTES, OFF_OUT = OFF_V + 2 * V_BYTES;
-    static constexpr uint32_t OFF_BAR = OFF_OUT + 2 * Q_REGION;
-    static constexpr int N_BARS = 2 + 8 + 2 + 4 + 2 + 1 + 2 + 2 * kSegs + 2;
+    static constexpr uint32_t OFF_Q = 0, OFF_K = 4 * Q_REGION, OFF_V = OFF_K + 2 * K_BYTES;
+    static constexpr uint32_t OFF_BAR = OFF_V + 2 * V_BYTES;
+    static constexpr int N_BARS = 2 + 8 + 2 + 4 + 2 + 1 + 2 * kSegs + 2;
     static constexpr uint32_t OFF_HOLD = OFF_BAR + N_BARS * 8;
     static constexpr uint32_t OFF_SCRATCH = (OFF_HOLD + 16 + 7) / 8 * 8;
     static constexpr uint32_t OFF_SEG = OFF_SCRATCH + 80 * 8;
@@ -823,7 +824,7 @@ struct PairLayout {
 
 template <typename T>
 __global__ void __launch_bounds__(PairLayout::THREADS, 1) prompt_pair_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
-                                                                             const __grid_constant__ CUtensorMap mV, const __grid_constant__ CUtensorMap mO,
+                                                                             const __grid_constant__ CUtensorMap mV,
                                                                              const __grid_constant__ PromptArgs a) {
     using L = PairLayout;
     constexpr int D = 256;
@@ -846,11 +847,10 @@ __global__ void __launch_bounds__(PairLayout::THREADS, 1) prompt_pair_kernel(con
     auto v_free = [&](int i) { return bar0 + 8u * (14 + i % 2); };
     auto o_done = [&](int i) { return bar0 + 8u * (16 + i % 2); };                      // block i's product with V
     const uint32_t v_here = bar0 + 8u * 18;                                             // a V block that has to be patched has landed
-    const uint32_t out_full = bar0 + 8u * 19, out_free = bar0 + 8u * 20;
-    auto seg_full = [&](int i) { return bar0 + 8u * (21 + i % kSegs); };
-    auto seg_free = [&](int i) { return bar0 + 8u * (21 + kSegs + i % kSegs); };
-    auto drain = [&](int w) { return bar0 + 8u * (21 + 2 * kSegs + w); };
-    static_assert(23 + 2 * kSegs <= L::N_BARS, "barriers");
+    auto seg_full = [&](int i) { return bar0 + 8u * (19 + i % kSegs); };
+    auto seg_free = [&](int i) { return bar0 + 8u * (19 + kSegs + i % kSegs); };
+    auto drain = [&](int w) { return bar0 + 8u * (19 + 2 * kSegs + w); };
+    static_assert(21 + 2 * kSegs <= L::N_BARS, "barriers");
     int* flag = a.flag;
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
@@ -858,8 +858,6 @@ __global__ void __launch_bounds__(PairLayout::THREADS, 1) prompt_pair_kernel(con
         mbar_init(s_full, 1);
         mbar_init(s_free, 2 * kTileWarps);
         mbar_init(v_here, 1);
-        mbar_init(out_full, kTileWarps);
-        mbar_init(out_free, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(k_full(i), 1);
             mbar_init(v_full(i), 1);
@@ -880,7 +878,6 @@ __global__ void __launch_bounds__(PairLayout::THREADS, 1) prompt_pair_kernel(con
         prefetch_map(&mQ);
         prefetch_map(&mK);
         prefetch_map(&mV);
-        prefetch_map(&mO);
     }
     const uint32_t tmem = tmem_begin_pair(base + L::OFF_HOLD, gbase + L::OFF_HOLD, 512, warp);
     pdl_wait();
@@ -1066,19 +1063,8 @@ __global__ void __launch_bounds__(PairLayout::THREADS, 1) prompt_pair_kernel(con
         const int u = warp - 4, r0 = 32 * (warp % 4) + 16 * (u / 4), r = r0 + lane % 16, hf = lane / 16;
         const uint32_t st = tmem + (static_cast<uint32_t>(r0) << 16), ot = st + L::O_COL;
         const uint32_t s_free0 = mapa_shared(s_free, 0);
-        const bool stores = u == 0 && lane == 0;
         constexpr float SH = Shift<T>::V;
-        int i = 0, patched = 0, outs = 0;             // blocks, blocks with a patched V, outputs so far
-        bool held = false;
-        auto out_ready = [&]() {
-            if (!held) return true;
-            held = false;
-            if (stores) {
-                bulk_wait_read0();
-                mbar_arrive(out_free);
-            }
-            return wait(out_free, outs - 1);
-        };
+        int i = 0, patched = 0;                       // blocks, and blocks with a patched V, so far
         for (int k = 0; ok && segment(k); ++k) {
             const Seg& g = segs_at[k % kSegs];
             const int n = rank == 0 ? g.n0 : g.n1, steps = g.steps();
@@ -1181,57 +1167,30 @@ __global__ void __launch_bounds__(PairLayout::THREADS, 1) prompt_pair_kernel(con
             l += __shfl_xor_sync(0xffffffffu, l, 16);
             const int tok0 = g.tok0 + rank * a.tpt;
             if (g.whole) {
-                // 128 columns at a time through shared memory: a whole tile is stored from there by a copy, of one that ends within
-                // the sequence each warp stores its rows, 16 lanes to a row
+                // A row's two threads store whole 32-byte sectors, if o lies on one.  (Through shared memory and a copy, 128 columns or twice 64 at a
+                // time, it takes 4000 cycles too: 64 KB from each CTA of the pair at once.)
                 const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
-                const bool full = tok0 + a.tpt <= g.n;
+                const int rt = r * a.recip >> 16;
+                const bool in = rt < a.tpt && tok0 + rt < g.n;
+                T* out = static_cast<T*>(a.o) + (static_cast<int64_t>(g.q0 + tok0 + rt) * a.hq + g.h * a.group + r - rt * a.group) * D + 32 * hf;
 #pragma unroll 1
-                for (int w0 = 0; w0 < D && tok0 < g.n; w0 += 128) {
-                    if (!out_ready()) break;
-                    uint8_t* mine = gbase + L::OFF_OUT;
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        float o[32];
-                        if (n > 0) {
-                            tmem_ld_rows16(ot + w0 + 64 * y, o);
-                            tmem_ld_wait();
-                        }
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            uint32_t v[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) v[e] = n == 0 || l == 0.0f ? 0u : pack2<T>(o[8 * q + 2 * e] * inv, o[8 * q + 2 * e + 1] * inv);
-                            *reinterpret_cast<uint4*>(mine + y * L::Q_REGION + r * 128 + (((4 * hf + q) ^ (r & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
-                        }
+                for (int y = 0; y < D / 64 && tok0 < g.n; ++y) {
+                    float o[32];
+                    if (n > 0) {
+                        tmem_ld_rows16(ot + 64 * y, o);
+                        tmem_ld_wait();
                     }
-                    if (full) {
-                        fence_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(out_full);
-                        if (u == 0) {
-                            if (!wait(out_full, outs)) break;
-                            if (lane == 0) {
 #pragma unroll
-                                for (int y = 0; y < 2; ++y)
-                                    tma_store_3d(&mO, w0 + 64 * y, g.h * a.group, g.q0 + tok0, base + L::OFF_OUT + y * L::Q_REGION);
-                                bulk_commit();
-                            }
-                            __syncwarp();
-                        }
-                        held = true;
-                        ++outs;
-                    } else {
-                        __syncwarp();
-                        const int ch = lane % 16;
-                        T* out = static_cast<T*>(a.o) + (static_cast<int64_t>(g.q0 + tok0) * a.hq + g.h * a.group) * D + w0 + 8 * ch;
+                    for (int q = 0; q < 2; ++q) {
+                        float v[8];
 #pragma unroll
-                        for (int y = 0; y < 8; ++y) {
-                            const int row = r0 + 2 * y + lane / 16, rt = row * a.recip >> 16;
-                            if (rt < a.tpt && tok0 + rt < g.n)
-                                *reinterpret_cast<uint4*>(out + (static_cast<int64_t>(rt) * a.hq + row - rt * a.group) * D) =
-                                    *reinterpret_cast<const uint4*>(mine + (ch / 8) * L::Q_REGION + row * 128 + (((ch % 8) ^ (row & 7)) << 4));
+                        for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(n == 0 || l == 0.0f ? 0u : pack2<T>(o[16 * q + 2 * e] * inv, o[16 * q + 2 * e + 1] * inv));
+                        float* dst = reinterpret_cast<float*>(out + 64 * y + 16 * q);
+                        if (in && a.o_sectors) st_v8(dst, v);
+                        if (in && !a.o_sectors) {
+                            *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
+                            *reinterpret_cast<float4*>(dst + 4) = make_float4(v[4], v[5], v[6], v[7]);
                         }
-                        __syncwarp();
                     }
                 }
             } else {
@@ -1254,7 +1213,6 @@ __global__ void __launch_bounds__(PairLayout::THREADS, 1) prompt_pair_kernel(con
             tc_fence_before();
             leave(k);
         }
-        if (stores) bulk_wait0();      // shared memory goes away
     }
     tc_fence_before();
     cluster_sync();  // neither CTA leaves while its peer may still signal it
@@ -1457,11 +1415,11 @@ template <typename T, int D>
 int run_prompt(PromptArgs a, const void* q, int64_t q_ld, const void* k, const void* v, cudaStream_t st) {
     constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
     const int box = 1 << (a.page_shift < 7 ? a.page_shift : 7), k_box = D == 256 && box > 64 ? 64 : box;
-    CUtensorMap mQ, mK, mV, mO;
-    const int64_t dims[3] = {D, a.hq, a.tokens}, strides[2] = {D * 2, q_ld * 2}, o_strides[2] = {D * 2, static_cast<int64_t>(a.hq) * D * 2};
+    CUtensorMap mQ, mK, mV;
+    const int64_t dims[3] = {D, a.hq, a.tokens}, strides[2] = {D * 2, q_ld * 2};
     const int qbox[3] = {64, a.group, a.tpt};
     if (!make_map(&mK, k, a.cache_rows, D, 64, k_box, bf) || !make_map(&mV, v, a.cache_rows, D, 64, box, bf) ||
-        !make_map_3d(&mQ, q, kMap16, dims, strides, qbox, 128) || !make_map_3d(&mO, a.o, kMap16, dims, o_strides, qbox, 128))
+        !make_map_3d(&mQ, q, kMap16, dims, strides, qbox, 128))
         return FUSE_ECUDA;
     // no more runs than there can be
     const int64_t ti = static_cast<int64_t>(a.tpt) * a.tiles, room = a.table_ld << a.page_shift;
@@ -1474,9 +1432,12 @@ int run_prompt(PromptArgs a, const void* q, int64_t q_ld, const void* k, const v
         if (runs > most) runs = most;
         rc = opt_in_smem((const void*)prompt_pair_kernel<T>, PairLayout::SMEM);
         if (rc != FUSE_OK) return rc;
-        rc = launch_pdl(prompt_pair_kernel<T>, dim3(static_cast<unsigned>(2 * runs)), dim3(PairLayout::THREADS), PairLayout::SMEM, st, 2, mQ, mK, mV, mO, a);
+        rc = launch_pdl(prompt_pair_kernel<T>, dim3(static_cast<unsigned>(2 * runs)), dim3(PairLayout::THREADS), PairLayout::SMEM, st, 2, mQ, mK, mV, a);
     } else {
         using L = Layout<D>;
+        CUtensorMap mO;
+        const int64_t o_strides[2] = {D * 2, static_cast<int64_t>(a.hq) * D * 2};
+        if (!make_map_3d(&mO, a.o, kMap16, dims, o_strides, qbox, 128)) return FUSE_ECUDA;
         // D = 128 and short prompts: the loop, whose instructions the warps fetch half of.  In us, loop and one piece: 32 prompts to
         // 1024 133 and 144 to 153, 8 of 2000 (28 heads, 4 for keys and values) 106 and 108 to 113; one of 4096 126 and 120.  With D = 64
         // one piece is faster throughout (16 to 4096, 32 heads: 639 and 585; in fp16 it spills).
@@ -1572,6 +1533,7 @@ extern "C" int fuse_prompt_attention(const void* q, int64_t q_ld, const void* k_
     a.recip = static_cast<int>((65536 + group - 1) / group);
     a.tpt = static_cast<int>(128 / group);
     a.tiles = 2;
+    a.o_sectors = is_aligned(o, 32);
     a.item_recip = ((uint64_t(1) << 32) + a.tpt * a.tiles - 1) / (a.tpt * a.tiles);
     while ((1 << a.page_shift) < page_size) ++a.page_shift;
     a.num_pages = static_cast<int>(num_pages);

@@ -443,7 +443,7 @@ int fuse_w4_gemv(const void* x, const void* wq, const void* scales, const void* 
  *   tokens   rows of q and o
  *   k_cache, v_cache  device [num_pages, kv_heads, page_size, D] of `dtype`; what lies in a page past the
  *            keys in use is not used, whatever its bits.  A value that is not finite, at a key that is in
- *            use, may make rows NaN that do not see it yet (those whose last key is less than 128 before it).
+ *            use, may make rows NaN that do not see it yet (those whose last key is less than 384 before it).
  *   block_table  device int32 [batch, table_ld]: entry i is the page of keys i page_size .. ; only the
  *            entries that seq_lens covers are read.  May be NULL when table_ld == 0.
  *   cu_queries  device int32 [batch + 1], ascending, within 0 .. tokens

@@ -173,6 +173,43 @@ def test_what_is_past_the_keys_is_not_used(cuda_device):
     assert torch.equal(run(p), a)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_tensors_on_16_byte_boundaries(cuda_device, D):
+    import torch
+    p = make([(300, 280), (40, 40), (129, 2)], 4, 2, D, 16, "bf16", seed=21)
+    want = check(p)
+
+    def moved(t):
+        buf = torch.zeros(t.numel() + 8, dtype=t.dtype, device="cuda")
+        out = buf[8:].view(t.shape)
+        out.copy_(t)
+        assert out.data_ptr() % 32 == 16
+        return out
+
+    for c in "qkv":
+        p[c] = moved(p[c])
+    o = moved(torch.full_like(want, 7.0))
+    fc.fuse_prompt_attention(p["q"], p["k"], p["v"], p["table"], p["cu"], p["lens"], o, p["scale"])
+    assert fc.fuse_check() == fc.FUSE_OK
+    assert torch.equal(o, want)
+
+
+def test_wide_heads(cuda_device):
+    """D = 256: strided queries, infinities past the keys, workspaces of any content, parts joined over many runs."""
+    import torch
+    p = make([(3000, 40), (700, 700), (1, 1), (0, 3), (260, 3)], 8, 2, 256, 32, "f16", seed=22, pad=2)
+    want = check(p)
+    rows = int(p["cu"][-1])
+    for c in "kv":
+        p[c] = torch.where(p[c].isnan(), torch.full_like(p[c], -math.inf), p[c])
+    wide = torch.full((p["q"].shape[0], 9 * 256), float("nan"), dtype=p["q"].dtype, device="cuda")
+    wide[:, :8 * 256] = p["q"].view(-1, 8 * 256)
+    p["q"] = wide[:, :8 * 256].unflatten(1, (8, 256))
+    ws = torch.full((fc.fuse_prompt_attention_workspace_bytes(rows + 2, 8, 2, 256),), 0xff, dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        assert torch.equal(run(p, workspace=ws), want)
+
+
 def test_equal_calls_and_any_workspace(cuda_device):
     import torch
     p = make([(3000, 40), (700, 700)], 8, 2, 128, 32, "f16", seed=9)
