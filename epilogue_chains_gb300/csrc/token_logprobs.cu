@@ -14,7 +14,8 @@
 // of candidates; then k scans of the row find them one by one.
 //
 // A row is read by a cluster of 1, 2, 4 or 8 CTAs (few rows: more CTAs for each), whose parts and alternatives
-// meet in the first CTA's shared memory.  It is bound by HBM.
+// meet in the first CTA's shared memory.  It is bound by HBM: 4096 x 131072 in bf16, the best five of each, 167 us (6.4 TB/s);
+// one row or a few by latency: 128000 fp32 logits of one row 4.3 us, with the best twenty 7.5 us.
 #include <math.h>
 
 #include <type_traits>
