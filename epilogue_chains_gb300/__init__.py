@@ -185,12 +185,13 @@ def _ptr(t) -> int | None:
 _torch = None         # the torch module, and its calls for the current device's index and stream handle
 _current_device = None
 _current_handle = None
+_capturing = None     # whether the current stream is being captured
 
 
 def _bind_torch():
     """torch, imported at the first call that needs it (an import statement or a Stream object at every
     call costs the host more than the launch of a small kernel)."""
-    global _torch, _current_device, _current_handle
+    global _torch, _current_device, _current_handle, _capturing
     import torch
     if not torch.cuda.is_available():
         raise ValueError("no CUDA device")
@@ -198,6 +199,7 @@ def _bind_torch():
     _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
     _current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    _capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
     _torch = torch
     return torch
 
@@ -567,7 +569,7 @@ _PROMPT_LOCK = threading.Lock()
 
 def _prompt_workspace(need: int, dev: int, stream_handle):
     torch = _torch
-    if stream_handle != _current_handle(dev) or torch.cuda.is_current_stream_capturing():
+    if stream_handle != _current_handle(dev) or _capturing():
         raise ValueError("pass a workspace of fuse_prompt_attention_workspace_bytes() bytes: this module's own ones serve "
                          "calls on torch's current stream outside a graph capture only (a captured graph may be replayed "
                          "next to other calls)")
@@ -586,9 +588,17 @@ def fuse_prompt_attention(q, k_cache, v_cache, block_table, cu_queries, seq_lens
     left as they are.  workspace: a device tensor of fuse_prompt_attention_workspace_bytes() bytes; None: a buffer kept by
     this module for the current stream."""
     torch = _torch or _bind_torch()
-    dt, i32 = q.dtype, torch.int32
-    dev = _decode_operands(dt, (k_cache, v_cache, o), ((block_table, i32), (cu_queries, i32), (seq_lens, i32)))
-    shape, cache = q.shape, k_cache.shape        # (each such call to torch costs the host 0.2 us or more)
+    dt, i32, dev = q.dtype, torch.int32, o.get_device()
+    # (here and below in one expression: the loops and tuples of the call that names what is wrong cost the host 1 us)
+    if ((dt is not torch.bfloat16 and dt is not torch.float16) or dev != _current_device()
+            or o.dtype is not dt or not o.is_contiguous()
+            or k_cache.dtype is not dt or k_cache.get_device() != dev or not k_cache.is_contiguous()
+            or v_cache.dtype is not dt or v_cache.get_device() != dev or not v_cache.is_contiguous()
+            or block_table.dtype is not i32 or block_table.get_device() != dev or not block_table.is_contiguous()
+            or cu_queries.dtype is not i32 or cu_queries.get_device() != dev or not cu_queries.is_contiguous()
+            or seq_lens.dtype is not i32 or seq_lens.get_device() != dev or not seq_lens.is_contiguous()):
+        _decode_operands(dt, (o, k_cache, v_cache), ((block_table, i32), (cu_queries, i32), (seq_lens, i32)))
+    shape, cache = q.shape, k_cache.shape
     tokens, q_heads, D = shape
     pages, kv_heads, page_size, D2 = cache
     ld, head, one = q.stride()
@@ -601,7 +611,7 @@ def fuse_prompt_attention(q, k_cache, v_cache, block_table, cu_queries, seq_lens
         raise ValueError("shape mismatch")
     if tokens <= 1:
         ld = q_heads * D
-    lib, sh = _load(), _stream(stream)
+    lib, sh = _lib or _load(), _current_handle(dev) if stream is None else _stream(stream)
     own = workspace is None
     if not own and (workspace.get_device() != dev or not workspace.is_contiguous()):
         raise ValueError("the workspace must be a contiguous tensor on the device of the others")
@@ -618,7 +628,8 @@ def fuse_prompt_attention(q, k_cache, v_cache, block_table, cu_queries, seq_lens
     finally:
         if own:
             _PROMPT_LOCK.release()
-    _check(status, "fuse_prompt_attention")
+    if status:
+        _check(status, "fuse_prompt_attention")
 
 
 @functools.lru_cache(maxsize=256)
@@ -650,16 +661,21 @@ def fuse_mxfp4_quantize(x, q, scales, stream=None) -> None:
     """x [rows, cols] (rows may be strided) in 4-bit floating point with a power-of-two scale per 32 values: codes
     q uint8 [rows, cols / 2] and scales uint8 [fuse_mxfp4_scale_bytes(rows, cols)], in tiles (see the header)."""
     torch = _torch or _bind_torch()
-    code = _float_code(x.dtype)
-    _on_device(x.get_device(), (q, torch.uint8), (scales, torch.uint8))
+    code, u8, dev = _float_code(x.dtype), torch.uint8, x.get_device()
+    if (dev != _current_device() or q.dtype is not u8 or q.get_device() != dev or not q.is_contiguous()
+            or scales.dtype is not u8 or scales.get_device() != dev or not scales.is_contiguous()):
+        _on_device(dev, (q, u8), (scales, u8))
     shape, strides = x.shape, x.stride()
     if len(shape) != 2 or (shape[1] > 1 and strides[1] != 1):
         raise ValueError("x must be a 2-D tensor with unit column stride")
     rows, cols = shape
     if q.shape != (rows, cols // 2) or scales.numel() < fuse_mxfp4_scale_bytes(rows, cols):
         raise ValueError("shape mismatch")
-    _check(_load().fuse_mxfp4_quantize(x.data_ptr(), strides[0] if rows > 1 else cols, q.data_ptr(), scales.data_ptr(),
-                                       rows, cols, code, _stream(stream)), "fuse_mxfp4_quantize")
+    status = (_lib or _load()).fuse_mxfp4_quantize(x.data_ptr(), strides[0] if rows > 1 else cols, q.data_ptr(),
+                                                   scales.data_ptr(), rows, cols, code,
+                                                   _current_handle(dev) if stream is None else _stream(stream))
+    if status:
+        _check(status, "fuse_mxfp4_quantize")
 
 
 def fuse_mxfp4_dequantize(q, scales, y, stream=None) -> None:
@@ -686,17 +702,28 @@ def fuse_mxfp4_gemm(xq, xs, wq, ws, y, bias=None, residual=None, gelu: bool = Fa
     xs, wq uint8 [N, K / 2] with scales ws, as fuse_mxfp4_quantize() writes them.  bias [N], residual [M, N] and the GELU
     are optional; they and y are fp16 or bf16."""
     torch = _torch or _bind_torch()
-    dt, u8 = y.dtype, torch.uint8
-    _decode_operands(dt, (y, bias, residual), ((xq, u8), (xs, u8), (wq, u8), (ws, u8)))
+    dt, u8, dev = y.dtype, torch.uint8, y.get_device()
+    if ((dt is not torch.bfloat16 and dt is not torch.float16) or dev != _current_device() or not y.is_contiguous()
+            or (bias is not None and (bias.dtype is not dt or bias.get_device() != dev or not bias.is_contiguous()))
+            or (residual is not None
+                and (residual.dtype is not dt or residual.get_device() != dev or not residual.is_contiguous()))
+            or xq.dtype is not u8 or xq.get_device() != dev or not xq.is_contiguous()
+            or xs.dtype is not u8 or xs.get_device() != dev or not xs.is_contiguous()
+            or wq.dtype is not u8 or wq.get_device() != dev or not wq.is_contiguous()
+            or ws.dtype is not u8 or ws.get_device() != dev or not ws.is_contiguous()):
+        _decode_operands(dt, (y, bias, residual), ((xq, u8), (xs, u8), (wq, u8), (ws, u8)))
     M, half = xq.shape
     N, half_w = wq.shape
     if (half != half_w or y.shape != (M, N) or xs.numel() < fuse_mxfp4_scale_bytes(M, 2 * half)
             or ws.numel() < fuse_mxfp4_scale_bytes(N, 2 * half) or (bias is not None and bias.shape != (N,))
             or (residual is not None and residual.shape != y.shape)):
         raise ValueError("shape mismatch")
-    _check(_load().fuse_mxfp4_gemm(xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(), _ptr(bias), _ptr(residual),
-                                   y.data_ptr(), M, N, 2 * half, 1 if gelu else 0,
-                                   FUSE_F16 if dt is torch.float16 else FUSE_BF16, _stream(stream)), "fuse_mxfp4_gemm")
+    status = (_lib or _load()).fuse_mxfp4_gemm(
+        xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(), None if bias is None else bias.data_ptr(),
+        None if residual is None else residual.data_ptr(), y.data_ptr(), M, N, 2 * half, 1 if gelu else 0,
+        FUSE_F16 if dt is torch.float16 else FUSE_BF16, _current_handle(dev) if stream is None else _stream(stream))
+    if status:
+        _check(status, "fuse_mxfp4_gemm")
 
 
 def fuse_token_logprobs(logits, tokens, logprob, entropy=None, top_logprob=None, top_index=None, scale: float = 1.0,
@@ -706,8 +733,8 @@ def fuse_token_logprobs(logits, tokens, logprob, entropy=None, top_logprob=None,
     equal logits the lower index first).  Outputs are fp32 and int32; any of them may be None, not all."""
     torch = _torch or _bind_torch()
     code = _float_code(logits.dtype)
-    f32, i32 = torch.float32, torch.int32
-    _on_device(logits.get_device(), (tokens, i32), (logprob, f32), (entropy, f32), (top_logprob, f32), (top_index, i32))
+    f32, i32, dev = torch.float32, torch.int32, logits.get_device()
+    _on_device(dev, (tokens, i32), (logprob, f32), (entropy, f32), (top_logprob, f32), (top_index, i32))
     shape, strides = logits.shape, logits.stride()
     if len(shape) != 2 or (shape[1] > 1 and strides[1] != 1):
         raise ValueError("logits must be a 2-D tensor with unit column stride")
@@ -722,9 +749,13 @@ def fuse_token_logprobs(logits, tokens, logprob, entropy=None, top_logprob=None,
     for t in (tokens, logprob, entropy):
         if t is not None and t.shape != (rows,):
             raise ValueError("shape mismatch")
-    _check(_load().fuse_token_logprobs(logits.data_ptr(), strides[0] if rows > 1 else vocab, _ptr(tokens), _ptr(logprob),
-                                       _ptr(entropy), _ptr(top_logprob), _ptr(top_index), rows, vocab, top, scale, code,
-                                       _stream(stream)), "fuse_token_logprobs")
+    status = (_lib or _load()).fuse_token_logprobs(
+        logits.data_ptr(), strides[0] if rows > 1 else vocab, None if tokens is None else tokens.data_ptr(),
+        None if logprob is None else logprob.data_ptr(), None if entropy is None else entropy.data_ptr(),
+        None if top_logprob is None else top_logprob.data_ptr(), None if top_index is None else top_index.data_ptr(), rows,
+        vocab, top, scale, code, _current_handle(dev) if stream is None else _stream(stream))
+    if status:
+        _check(status, "fuse_token_logprobs")
 
 
 def fuse_prompt_attention_bytes(tokens: int, keys: int, q_heads: int, kv_heads: int, D: int) -> int:
