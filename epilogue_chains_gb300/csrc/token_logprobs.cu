@@ -341,13 +341,15 @@ __global__ void __launch_bounds__(kThreads, 6) token_logprobs_kernel(const __gri
         const int n = sh.cands;
         if (n > kCand) {
             scan_top<T>(sh, s, a.top);
-        } else if (warp == 0) {
-            uint64_t best = sort_down(lane < n ? sh.cand[lane] : uint64_t(0));
-            for (int i = 32; i < n; i += 32) {
-                const uint64_t more = sort_down(i + lane < n ? sh.cand[i + lane] : uint64_t(0));
-                best = merge_down(best, static_cast<uint64_t>(__shfl_sync(0xffffffffu, more, 31 - lane)));
+        } else {
+            // each candidate's place is the number of larger ones (no two are equal)
+            for (int i = tid; i < n; i += kThreads) {
+                const uint64_t k = sh.cand[i];
+                int place = 0;
+                for (int j = 0; j < n; ++j) place += sh.cand[j] > k;
+                if (place < a.top) sh.best[place] = k;
             }
-            if (lane < a.top) sh.best[lane] = best;
+            if (tid >= n && tid < a.top) sh.best[tid] = 0;
         }
     }
 
@@ -399,17 +401,22 @@ __global__ void __launch_bounds__(kThreads, 6) token_logprobs_kernel(const __gri
             // the CTAs' lists, each of them sorted, into one
             float* ov = a.top_logprob ? a.top_logprob + row * a.top : nullptr;
             int32_t* oi = a.top_index ? a.top_index + row * a.top : nullptr;
-            uint64_t best = lane < a.top ? sh.best[lane] : uint64_t(0);
-            uint64_t more[kMaxCluster];
+            uint64_t part[kMaxCluster];      // odd ones back to front
+            part[0] = lane < a.top ? sh.best[lane] : uint64_t(0);
 #pragma unroll
             for (int q = 1; q < kMaxCluster; ++q) {
-                more[q] = 0;
-                if (q < cluster && 31 - lane < a.top)
-                    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(*reinterpret_cast<unsigned long long*>(&more[q])) : "r"(mapa_shared(smem_addr(sh.best + 31 - lane), q)) : "memory");
+                const int i = q % 2 ? 31 - lane : lane;
+                part[q] = 0;
+                if (q < cluster && i < a.top)
+                    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(*reinterpret_cast<unsigned long long*>(&part[q])) : "r"(mapa_shared(smem_addr(sh.best + i), q)) : "memory");
             }
 #pragma unroll
-            for (int q = 1; q < kMaxCluster; ++q)
-                if (q < cluster) best = merge_down(best, more[q]);
+            for (int step = 1; step < kMaxCluster; step *= 2)
+                if (step < cluster)
+#pragma unroll
+                    for (int q = 0; q < kMaxCluster; q += 2 * step)
+                        part[q] = merge_down(part[q], step == 1 ? part[q + step] : static_cast<uint64_t>(__shfl_sync(0xffffffffu, part[q + step], 31 - lane)));
+            const uint64_t best = part[0];
             const int n = __popc(__ballot_sync(0xffffffffu, lane < a.top && best != 0));
             if (lane < n) {
                 if (ov) ov[lane] = log_p(logit_of(best));
