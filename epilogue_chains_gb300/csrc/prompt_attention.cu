@@ -42,10 +42,16 @@ constexpr int kGrid = 160;                 // most CTAs (workspace bound); half 
 constexpr float kLag = 8.0f;
 template <typename T> struct Shift { static constexpr float V = 0.0f; };
 template <> struct Shift<__half> { static constexpr float V = 7.0f; };
-// What an item counts for apart from its keys, in keys: its entry and its output.
-constexpr int kEntry = 192;
-// A CTA's run is at least this many keys: shorter runs cost more to join than they save.
-constexpr int kLeastRun = 512 + kEntry;
+// What an item counts for apart from its keys, in keys: its entry and its output, of which D = 256 has the longer.  (8 prompts to
+// 2048 109 -> 106 us, 100 to 300 with 16 heads on 4 110 -> 102.)
+constexpr int kMostEntry = 352;
+constexpr int entry_of(int D) { return D == 256 ? kMostEntry : 192; }
+// A CTA's run is at least this many keys and an entry: shorter runs cost more to join than they save.
+constexpr int kLeastRun = 512;
+// Within this many blocks of an item's end a run ends there: so short a part costs more than it evens out.  (In us, from 0 to 2, 3
+// and 4: D = 128, 32 prompts to 1024 126, 127, 121, 122, 64 to 200 52, 48, 48, 49, 16 to 500 44, 38, 37, 38, 8 to 2000 102, 98, 99,
+// 101; D = 64, 20 to 600 53, 47, 51, 52; D = 256, 8 to 2048 109, 106, 107, 109.)
+constexpr int snap_of(int D) { return D == 128 ? 3 : 2; }
 
 __device__ __forceinline__ float ex2f(float x) {
     float y;
@@ -75,6 +81,7 @@ struct PromptArgs {
     void* o;
     int batch, tokens, hq, hk, group;
     int recip;                         // row / group = row recip >> 16 for rows below 128
+    int entry, snap;                   // entry_of(D), snap_of(D)
     uint64_t item_recip;               // ceil(2^32 / (tpt tiles))
     bool o_sectors;                    // o lies on a 32-byte boundary
     int tpt, tiles;                    // tokens of a tile of 128 rows; tiles of an item (2)
@@ -109,10 +116,10 @@ __device__ __forceinline__ int over_item(const PromptArgs& a, int n) { return st
 __device__ __forceinline__ int items_of(const PromptArgs& a, const Seq& s) { return over_item(a, s.n + a.tpt * a.tiles - 1); }
 // Keys that the first `tokens` new tokens of a sequence see between them.
 __device__ __forceinline__ int extent(const Seq& s, int tokens) { return max(s.L - s.n + min(tokens, s.n), 0); }
-// Places of a head's first k items: sum over i < k of kEntry + extent((i + 1) ti).
+// Places of a head's first k items: sum over i < k of entry + extent((i + 1) ti).
 __device__ __forceinline__ int64_t places(const PromptArgs& a, const Seq& s, int items, int k) {
     const int64_t ti = a.tpt * a.tiles, d = s.L - s.n;
-    int64_t sum = static_cast<int64_t>(k) * kEntry;
+    int64_t sum = static_cast<int64_t>(k) * a.entry;
     if (k == items && k > 0) {
         sum += extent(s, s.n);
         --k;
@@ -158,7 +165,7 @@ __device__ __forceinline__ Pos pos_in(const PromptArgs& a, const Seq& s, int b, 
     const int64_t in = r - places(a, s, items, lo);
     const int blocks = (extent(s, (lo + 1) * a.tpt * a.tiles) + 127) / 128;
     p.i = lo;
-    p.t = in <= kEntry ? 0 : static_cast<int>((in - kEntry) >> 7);
+    p.t = in <= a.entry ? 0 : static_cast<int>((in - a.entry) >> 7);
     if (p.t <= snap) {
         p.t = 0;
     } else if (blocks - p.t <= snap) {
@@ -269,11 +276,11 @@ __device__ __forceinline__ void find_runs(const PromptArgs& a, int me, int runs,
         total += sums[w];
         items += counts[w];
     }
-    // Equal runs, but none shorter than an item of kLeastRun or the average one: with few short items a CTA for each.
+    // Equal runs, but none shorter than an item of kLeastRun keys or the average one: with few short items a CTA for each.
     int64_t len = quotient(total + runs - 1, runs), least = items > 0 ? quotient(total + items - 1, items) : 1;
-    if (least > kLeastRun) least = kLeastRun;
+    if (least > kLeastRun + a.entry) least = kLeastRun + a.entry;
     if (len < least) len = least;
-    const int snap = len < kLeastRun ? 4 : static_cast<int>(min(len >> 12, static_cast<int64_t>(64)));
+    const int snap = len < kLeastRun + a.entry ? 4 : max(a.snap, static_cast<int>(min(len >> 12, static_cast<int64_t>(64))));
     for (int w = 0; w < 2; ++w) {
         const int64_t x = static_cast<int64_t>(me + w) * len;
         if (x < upto && x >= upto - mine) {            // this thread's sequences have it
@@ -1431,7 +1438,7 @@ int run_prompt(PromptArgs a, const void* q, int64_t q_ld, const void* k, const v
     // no more runs than there can be
     const int64_t ti = static_cast<int64_t>(a.tpt) * a.tiles, room = a.table_ld << a.page_shift;
     const int64_t items = (ceil_div(a.tokens, ti) + (a.batch < a.tokens ? a.batch : a.tokens)) * a.hk;
-    const int64_t most = items * ceil_div(room + kEntry, kLeastRun);
+    const int64_t most = items * ceil_div(room + a.entry, kLeastRun + a.entry);
     int64_t runs;
     int rc;
     if constexpr (D == 256) {
@@ -1510,7 +1517,7 @@ extern "C" int fuse_prompt_attention(const void* q, int64_t q_ld, const void* k_
         table_ld >= (top - 4096) / page_size || q_ld >= int64_t(1) << 32)
         return FUSE_EUNSUPPORTED;
     // items are counted in 32 bits, the line's places, times the CTAs, in 64
-    if ((tokens + batch) * kv_heads >= top || (tokens + batch) * kv_heads >= (int64_t(1) << 52) / (table_ld * page_size + kEntry)) return FUSE_EUNSUPPORTED;
+    if ((tokens + batch) * kv_heads >= top || (tokens + batch) * kv_heads >= (int64_t(1) << 52) / (table_ld * page_size + kMostEntry)) return FUSE_EUNSUPPORTED;
     if (q_ld < q_heads * D) return FUSE_EINVAL;
     if (tokens == 0 || batch == 0) return FUSE_OK;
     if (!q || !k_cache || !v_cache || !o || !cu_queries || !seq_lens || (table_ld > 0 && !block_table)) return FUSE_EINVAL;
@@ -1540,6 +1547,8 @@ extern "C" int fuse_prompt_attention(const void* q, int64_t q_ld, const void* k_
     a.recip = static_cast<int>((65536 + group - 1) / group);
     a.tpt = static_cast<int>(128 / group);
     a.tiles = 2;
+    a.entry = entry_of(static_cast<int>(D));
+    a.snap = snap_of(static_cast<int>(D));
     a.o_sectors = is_aligned(o, 32);
     a.item_recip = ((uint64_t(1) << 32) + a.tpt * a.tiles - 1) / (a.tpt * a.tiles);
     while ((1 << a.page_shift) < page_size) ++a.page_shift;

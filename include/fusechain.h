@@ -451,7 +451,7 @@ int fuse_w4_gemv(const void* x, const void* wq, const void* scales, const void* 
  *   Rules: dtype FUSE_F16 or FUSE_BF16; D in {64, 128, 256}; q_heads a multiple of kv_heads, at most 128 of
  *          them for each; page_size a power of two, 16..256; batch <= 4096; tokens < 2^24; num_pages kv_heads
  *          page_size and table_ld page_size below 2^31 - 4096, (tokens + batch) kv_heads below 2^31 and, times
- *          (table_ld page_size + 192), below 2^52 (else FUSE_EUNSUPPORTED, and nothing is enqueued); scale > 0; tensors 16-byte
+ *          (table_ld page_size + 352), below 2^52 (else FUSE_EUNSUPPORTED, and nothing is enqueued); scale > 0; tensors 16-byte
  *          aligned and q_ld a multiple of 8, tables and lengths 4-byte (else FUSE_EALIGN).
  *   Out of range in device memory (fuse_check() then returns FUSE_EINDEX): a page index outside
  *   [0, num_pages) counts as a page of zeros; a length is taken into 0 .. table_ld page_size, a row number
