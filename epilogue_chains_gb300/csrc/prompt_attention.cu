@@ -1235,10 +1235,13 @@ __global__ void __launch_bounds__(PairLayout::THREADS, 1) prompt_pair_kernel(con
 }
 
 // ================================================================== join
-// The parts of an item that several CTAs share.  Every run that begins within an item brings kJoinWarps warps, among which the
+// The parts of an item that several CTAs share.  Every run that begins within an item brings join_warps() warps, among which the
 // item's rows are shared out: four rows to a warp where two CTAs share the item, one where many do.  It is bound by latency: of
 // where the runs begin, then of the parts, so a warp reads all it can at once.
-constexpr int kJoinThreads = 128, kJoinWarps = 64, kJoinWords = (kGrid + 1 + 31) / 32;
+constexpr int kJoinThreads = 128, kJoinWords = (kGrid + 1 + 31) / 32;
+// Warps for each run that begins within an item.  (32 and 64, in us: D = 128, 32 prompts to 1024 119.4 and 120.7, 2 to 700 24.2 and
+// 25.5; D = 256, 8 to 2048 111.6 and 105.9; 16 for D = 128, one of 4096 131 where 32 take 122.)
+constexpr int join_warps(int D) { return D == 256 ? 64 : 32; }
 template <typename T, int D, int ROWS, int AHEAD>
 __device__ __forceinline__ void join_rows(const PromptArgs& a, const Pos& p, const Seq& s, int row0, int rows, int c0, const uint32_t (&has)[kJoinWords], int lane) {
     constexpr int W = D / 32;
@@ -1361,7 +1364,9 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const __grid_
         runs += __popc(within);
         rank += __popc(run >= 32 * k + 32 ? within : run > 32 * k ? within & ((1u << (run - 32 * k)) - 1u) : 0u);
     }
-    const int rows = runs == 1 ? 4 : runs < 4 ? 2 : 1, row0 = (rank * kJoinWarps + unit) * rows;
+    int rows = 1;                                      // of a warp, so that all of an item's are someone's
+    while (rows * runs * join_warps(D) < 256) rows *= 2;
+    const int row0 = (rank * join_warps(D) + unit) * rows;
     if (row0 >= a.rows) return;
     if (rows == 1) {
         join_rows<T, D, 1, 4>(a, p, s, row0, 1, c0, has, lane);
@@ -1467,7 +1472,7 @@ int run_prompt(PromptArgs a, const void* q, int64_t q_ld, const void* k, const v
     }
     // an item of at most one block of keys is nobody's to share
     if (rc != FUSE_OK || runs == 1 || room <= 128) return rc;
-    return launch_pdl(prompt_join_kernel<T, D>, dim3(kJoinWarps / (kJoinThreads / 32), static_cast<unsigned>(runs - 1)), dim3(kJoinThreads), 0, st, 1, a,
+    return launch_pdl(prompt_join_kernel<T, D>, dim3(join_warps(D) / (kJoinThreads / 32), static_cast<unsigned>(runs - 1)), dim3(kJoinThreads), 0, st, 1, a,
                       static_cast<int>(runs));
 }
 
