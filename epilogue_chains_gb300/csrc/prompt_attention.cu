@@ -18,8 +18,8 @@
 // waits are bounded (watchdog).
 //
 // Measured (32 query heads on 8 for keys and values, D = 128, bf16): one prompt of 16384 1.44 ms, 1.53 PFLOP/s of the visible
-// pairs, where the chip's power is the limit; 32 of up to 1024 (fp16) 127 to 129 us, 0.80; 64 new tokens after 65536 71 us, 0.97, of
-// which the join is a fifth.  16 ungrouped heads of 256: 16384 1.40 ms, 1.57; 8 of up to 2048 109 to 113 us, 1.0.
+// pairs, where the chip's power is the limit; 32 of up to 1024 (fp16) 120 us, 0.85; 64 new tokens after 65536 71 us, 0.97, of
+// which the join is a fifth.  16 ungrouped heads of 256: 16384 1.40 ms, 1.57; 8 of up to 2048 106 to 110 us, 1.0.
 #include <cudaTypedefs.h>
 #include <math.h>
 
@@ -819,7 +819,7 @@ __global__ void __launch_bounds__(Layout<D>::THREADS, 1) prompt_attention_kernel
 // M = 256 unit (cta_group::2): CTA t of the pair has tile t's queries, weights and output, and of every block of K and V one half
 // (64 keys; 128 columns), which leaves room for two blocks of each and takes half the bytes to every SM.  P is in TMEM, two
 // blocks in turn.  CTA 0 issues all products; the bytes of both CTAs count on its barriers, its commits signal both.  The rest is
-// as above.  (8 prompts to 2048 with 16 heads: 109 to 113 us.  One CTA by itself, a K or V tile of 64 KB at a time, took 151 us.)
+// as above.  (8 prompts to 2048 with 16 heads: 106 to 110 us.  One CTA by itself, a K or V tile of 64 KB at a time, took 151 us.)
 struct PairLayout {
     static constexpr int THREADS = 32 * (4 + kTileWarps);
     static constexpr uint32_t Q_REGION = 128 * 128, K_REGION = 64 * 128, V_REGION = 128 * 128;   // 64-column atoms
@@ -1236,8 +1236,9 @@ __global__ void __launch_bounds__(PairLayout::THREADS, 1) prompt_pair_kernel(con
 
 // ================================================================== join
 // The parts of an item that several CTAs share.  Every run that begins within an item brings join_warps() warps, among which the
-// item's rows are shared out: four rows to a warp where two CTAs share the item, one where many do.  It is bound by latency: of
-// where the runs begin, then of the parts, so a warp reads all it can at once.
+// item's rows are shared out: four or eight rows to a warp where two CTAs share the item, one where many do.  It is bound by
+// latency: of its launch (about 3 us: the kernel before leaves no room for it), of where the runs begin, then of the parts, so a
+// warp reads all it can at once.
 constexpr int kJoinThreads = 128, kJoinWords = (kGrid + 1 + 31) / 32;
 // Warps for each run that begins within an item.  (32 and 64, in us: D = 128, 32 prompts to 1024 119.4 and 120.7, 2 to 700 24.2 and
 // 25.5; D = 256, 8 to 2048 111.6 and 105.9; 16 for D = 128, one of 4096 131 where 32 take 122.)
