@@ -1458,13 +1458,11 @@ int run_prompt(PromptArgs a, const void* q, int64_t q_ld, const void* k, const v
         CUtensorMap mO;
         const int64_t o_strides[2] = {D * 2, static_cast<int64_t>(a.hq) * D * 2};
         if (!make_map_3d(&mO, a.o, kMap16, dims, o_strides, qbox, 128)) return FUSE_ECUDA;
-        // D = 128 and short prompts: the loop, whose instructions the warps fetch half of.  In us, loop and one piece: 32 prompts to
-        // 1024 133 and 144 to 153, 8 of 2000 (28 heads, 4 for keys and values) 106 and 108 to 113; one of 4096 126 and 120.  With D = 64
-        // one piece is faster throughout (16 to 4096, 32 heads: 639 and 585; in fp16 it spills).
-        constexpr int USUAL = D == 64 && bf ? 2 : 1;
-        auto* kernel = prompt_attention_kernel<T, D, USUAL>;
-        if constexpr (D == 128)
-            if (a.tokens >= 3000 * static_cast<int64_t>(a.batch)) kernel = prompt_attention_kernel<T, D, 2>;
+        // Short prompts: the loop, whose instructions the warps fetch half of.  In us, loop and one piece: D = 128, 32 prompts to 1024
+        // 120 and 143, 8 to 2000 (28 heads on 4) 107 and 122, one of 4096 120 and 120, of 8192 400 and 366, of 16384 1450 and 1415;
+        // D = 64 (32 heads on 4), 20 to 600 45 and 47, 8 to 2000 100 and 102, 8 to 3000 180 and 178, 16 to 4096 580 and 538.
+        constexpr int64_t LONG = D == 64 ? 1200 : 3000;    // tokens of a sequence
+        const auto kernel = a.tokens >= LONG * a.batch ? prompt_attention_kernel<T, D, 2> : prompt_attention_kernel<T, D, 1>;
         rc = opt_in_smem((const void*)kernel, L::SMEM);
         if (rc != FUSE_OK) return rc;
         runs = sm_count() < kGrid ? sm_count() : kGrid;
@@ -1479,23 +1477,25 @@ int run_prompt(PromptArgs a, const void* q, int64_t q_ld, const void* k, const v
 
 }  // namespace
 
-int prompt_report_count() { return 14; }
+int prompt_report_count() { return 16; }
 int prompt_report(int i, fuse_kernel_record* out) {
     switch (i) {
-        FC_REPORT(0, Layout<64>::THREADS, Layout<64>::SMEM, 512, prompt_attention_kernel<__nv_bfloat16, 64, 2>);
-        FC_REPORT(1, Layout<128>::THREADS, Layout<128>::SMEM, 512, prompt_attention_kernel<__nv_bfloat16, 128, 1>);
-        FC_REPORT(2, Layout<128>::THREADS, Layout<128>::SMEM, 512, prompt_attention_kernel<__nv_bfloat16, 128, 2>);
-        FC_REPORT(3, PairLayout::THREADS, PairLayout::SMEM, 512, prompt_pair_kernel<__nv_bfloat16>);
-        FC_REPORT(4, Layout<64>::THREADS, Layout<64>::SMEM, 512, prompt_attention_kernel<__half, 64, 1>);
-        FC_REPORT(5, Layout<128>::THREADS, Layout<128>::SMEM, 512, prompt_attention_kernel<__half, 128, 1>);
-        FC_REPORT(6, Layout<128>::THREADS, Layout<128>::SMEM, 512, prompt_attention_kernel<__half, 128, 2>);
-        FC_REPORT(7, PairLayout::THREADS, PairLayout::SMEM, 512, prompt_pair_kernel<__half>);
-        FC_REPORT(8, kJoinThreads, 0, 0, prompt_join_kernel<__nv_bfloat16, 64>);
-        FC_REPORT(9, kJoinThreads, 0, 0, prompt_join_kernel<__nv_bfloat16, 128>);
-        FC_REPORT(10, kJoinThreads, 0, 0, prompt_join_kernel<__nv_bfloat16, 256>);
-        FC_REPORT(11, kJoinThreads, 0, 0, prompt_join_kernel<__half, 64>);
-        FC_REPORT(12, kJoinThreads, 0, 0, prompt_join_kernel<__half, 128>);
-        FC_REPORT(13, kJoinThreads, 0, 0, prompt_join_kernel<__half, 256>);
+        FC_REPORT(0, Layout<64>::THREADS, Layout<64>::SMEM, 512, prompt_attention_kernel<__nv_bfloat16, 64, 1>);
+        FC_REPORT(1, Layout<64>::THREADS, Layout<64>::SMEM, 512, prompt_attention_kernel<__nv_bfloat16, 64, 2>);
+        FC_REPORT(2, Layout<128>::THREADS, Layout<128>::SMEM, 512, prompt_attention_kernel<__nv_bfloat16, 128, 1>);
+        FC_REPORT(3, Layout<128>::THREADS, Layout<128>::SMEM, 512, prompt_attention_kernel<__nv_bfloat16, 128, 2>);
+        FC_REPORT(4, PairLayout::THREADS, PairLayout::SMEM, 512, prompt_pair_kernel<__nv_bfloat16>);
+        FC_REPORT(5, Layout<64>::THREADS, Layout<64>::SMEM, 512, prompt_attention_kernel<__half, 64, 1>);
+        FC_REPORT(6, Layout<64>::THREADS, Layout<64>::SMEM, 512, prompt_attention_kernel<__half, 64, 2>);
+        FC_REPORT(7, Layout<128>::THREADS, Layout<128>::SMEM, 512, prompt_attention_kernel<__half, 128, 1>);
+        FC_REPORT(8, Layout<128>::THREADS, Layout<128>::SMEM, 512, prompt_attention_kernel<__half, 128, 2>);
+        FC_REPORT(9, PairLayout::THREADS, PairLayout::SMEM, 512, prompt_pair_kernel<__half>);
+        FC_REPORT(10, kJoinThreads, 0, 0, prompt_join_kernel<__nv_bfloat16, 64>);
+        FC_REPORT(11, kJoinThreads, 0, 0, prompt_join_kernel<__nv_bfloat16, 128>);
+        FC_REPORT(12, kJoinThreads, 0, 0, prompt_join_kernel<__nv_bfloat16, 256>);
+        FC_REPORT(13, kJoinThreads, 0, 0, prompt_join_kernel<__half, 64>);
+        FC_REPORT(14, kJoinThreads, 0, 0, prompt_join_kernel<__half, 128>);
+        FC_REPORT(15, kJoinThreads, 0, 0, prompt_join_kernel<__half, 256>);
         default: return FUSE_EINVAL;
     }
 }
