@@ -131,6 +131,14 @@ def test_long_and_ragged(cuda_device, dtype, D):
     check(make([((37 * i) % 611, min((37 * i) % 611, (11 * i) % 97)) for i in range(70)], 8, 2, D, 16, dtype, seed=4, pad=7))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_long_prompts(cuda_device, dtype, D):
+    """The form of a step's code for long prompts, also with a cached part, an odd group and a second sequence."""
+    check(make([(4100, 4000)], 4, 1, D, 64, dtype, seed=23))
+    check(make([(3333, 3333), (3001, 2999)], 6, 2, D, 16, dtype, seed=24, std=3.0, pad=1))
+
+
 def test_many_sequences(cuda_device):
     check(make([(1 + i % 70, 1 + i % 3 if i % 70 > 2 else 1) for i in range(1500)], 4, 1, 64, 16, "bf16", seed=5))
 
