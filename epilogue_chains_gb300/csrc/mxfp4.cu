@@ -160,6 +160,9 @@ __global__ void __launch_bounds__(kQThreads) mxfp4_dequantize_kernel(const __gri
 // ================================================================== product
 // The accumulator's rows are weights (N), its columns tokens (M).
 constexpr int kStageK = 256;                        // values of a row per stage: 128 bytes
+// The product's K: a row's scales (8 bytes a stage, 1024 for its tile) are counted in 32 bits, and the 2^21 stages of a longest K
+// take some 0.4 s, within what the epilogue's bounded wait allows.
+constexpr int64_t kMostK = int64_t(1) << 29;
 constexpr uint32_t kTileBytes = 128 * 128;          // 128 rows of a stage
 constexpr int kGemmThreads = 32 * 6;                // warp 0: loads, 1: MMA issue, 2-5: epilogue
 
@@ -825,7 +828,7 @@ extern "C" int fuse_mxfp4_gemm(const void* xq, const void* xs, const void* wq, c
     if (rc == FUSE_OK) rc = check_matrix(N, K);
     if (rc != FUSE_OK) return rc;
     if (N < 1 || (gelu != 0 && gelu != 1) || (dtype != FUSE_F16 && dtype != FUSE_BF16)) return FUSE_EINVAL;
-    if (ceil_div(M, 256) * ceil_div(N, 256) >= (int64_t(1) << 30) / ceil_div(K, kStageK)) return FUSE_EUNSUPPORTED;   // stages are counted in 32 bits
+    if (K >= kMostK || ceil_div(M, 256) * ceil_div(N, 256) >= (int64_t(1) << 30) / ceil_div(K, kStageK)) return FUSE_EUNSUPPORTED;   // stages are counted in 32 bits
     if (M == 0) return FUSE_OK;
     if (!xq || !xs || !wq || !ws || !y) return FUSE_EINVAL;
     if (!is_aligned(xq, 16) || !is_aligned(xs, 16) || !is_aligned(wq, 16) || !is_aligned(ws, 16) || !is_aligned(y, 2) || !is_aligned(bias, 2) ||

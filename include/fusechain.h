@@ -502,7 +502,7 @@ int64_t fuse_mxfp4_scale_bytes(int64_t rows, int64_t cols);
  *   xq, xs   X [M, K] as fuse_mxfp4_quantize() writes it (M == 0 enqueues nothing);  wq, ws  W [N, K] likewise (of the
  *            scales' bytes that no row or value has, those of existing rows must not be 255)
  *   bias [N], R [M, N] of `dtype`, or NULL;  gelu 0 or 1;  y device [M, N] of `dtype`
- *   Rules: dtype FUSE_F16 or FUSE_BF16; K a multiple of 32, below 2^31; M, N < 2^22, ceil(M / 256) ceil(N / 256)
+ *   Rules: dtype FUSE_F16 or FUSE_BF16; K a multiple of 32, below 2^29; M, N < 2^22, ceil(M / 256) ceil(N / 256)
  *          ceil(K / 256) below 2^30 (else FUSE_EUNSUPPORTED);
  *          xq, xs, wq and ws 16-byte aligned, the others to their element (else FUSE_EALIGN); y overlaps no input.
  * The products are exact, their sums fp32, and Y is rounded once.  The order of the sums is fixed.
