@@ -739,11 +739,11 @@ def fuse_token_logprobs(logits, tokens, logprob, entropy=None, top_logprob=None,
     if len(shape) != 2 or (shape[1] > 1 and strides[1] != 1):
         raise ValueError("logits must be a 2-D tensor with unit column stride")
     rows, vocab = shape
-    top = 0
+    top = None
     for t in (top_logprob, top_index):
         if t is not None:
             shape = t.shape
-            if len(shape) != 2 or shape[0] != rows or (top and shape[1] != top):
+            if len(shape) != 2 or shape[0] != rows or (top is not None and shape[1] != top):
                 raise ValueError("shape mismatch")
             top = shape[1]
     for t in (tokens, logprob, entropy):
@@ -753,7 +753,7 @@ def fuse_token_logprobs(logits, tokens, logprob, entropy=None, top_logprob=None,
         logits.data_ptr(), strides[0] if rows > 1 else vocab, None if tokens is None else tokens.data_ptr(),
         None if logprob is None else logprob.data_ptr(), None if entropy is None else entropy.data_ptr(),
         None if top_logprob is None else top_logprob.data_ptr(), None if top_index is None else top_index.data_ptr(), rows,
-        vocab, top, scale, code, _current_handle(dev) if stream is None else _stream(stream))
+        vocab, top or 0, scale, code, _current_handle(dev) if stream is None else _stream(stream))
     if status:
         _check(status, "fuse_token_logprobs")
 
