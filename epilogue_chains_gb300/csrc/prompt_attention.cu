@@ -94,6 +94,8 @@ struct PromptArgs {
     float* po;                         // [2 for each run][rows][D]
     int rows;
     int *flag, *bad;
+    const void *q, *k, *v;             // for mend_row()
+    int64_t q_ld;
 };
 
 // ================================================================== the line of items
@@ -236,7 +238,9 @@ struct Walk {
         return false;
     }
 };
-// Where run `me` of `runs` begins and where the next does, for all threads; `scratch` is 80 * 8 bytes of shared memory.
+__device__ __forceinline__ Pos* found_at(int64_t* scratch) { return reinterpret_cast<Pos*>(scratch + 52); }
+// Where run `me` of `runs` begins and where the next does, for all threads; `scratch` is 80 * 8 bytes of shared memory, in which both
+// stay, at found_at().
 template <int THREADS>
 __device__ __forceinline__ void find_runs(const PromptArgs& a, int me, int runs, int64_t* scratch, Pos (&run)[2]) {
     constexpr int WARPS = THREADS / 32;
@@ -262,7 +266,7 @@ __device__ __forceinline__ void find_runs(const PromptArgs& a, int me, int runs,
     count = __reduce_add_sync(0xffffffffu, count);
     // per warp its places and items; then for each target its thread and place there, and where it is found
     int64_t *sums = scratch, *counts = scratch + 24, *target = scratch + 48;
-    Pos* found = reinterpret_cast<Pos*>(scratch + 52);
+    Pos* found = found_at(scratch);
     if (lane == 31) {
         sums[warp] = upto;
         counts[warp] = count;
@@ -311,6 +315,197 @@ __device__ __forceinline__ void find_runs(const PromptArgs& a, int me, int runs,
     run[1] = found[1];
 }
 
+// ================================================================== values that are not finite
+// A weight of 0 is no mask in a product: 0 x infinity is NaN, in every row of a tile that does not see the key.  Of a tile's rows the
+// first that sees a key sees the fewest, so its output tells whether that has happened.  Where it is not finite, the tile's rows for which
+// one of the values that were multiplied with a weight of 0 is not finite are computed again, from the keys that they see alone:
+// rare, and slow.  CTAs of the join's launch look at the outputs of all whole items, which takes 2 to 3 us where the join is short
+// (32 prompts to 1024 123.5 -> 126.5 us).  Code for it in prompt_attention_kernel costs more, there: looking the values over ahead of
+// the products, by the softmax warps, 14 us, a look at the first row's sums by its softmax warp, before, with or after the output,
+// or by the warp that issues PV, 7 to 13.  Where nothing is joined the kernel does it, in a form of its own (MEND).
+
+// Whether one of eight values of type T is not finite: its exponent's bits are all ones.
+template <typename T>
+__device__ __forceinline__ bool not_finite(const uint4& v) {
+    constexpr uint32_t MAG = 0x7fff7fffu, STEP = std::is_same<T, __half>::value ? 0x04000400u : 0x00800080u;
+    return ((((v.x & MAG) + STEP) | ((v.y & MAG) + STEP) | ((v.z & MAG) + STEP) | ((v.w & MAG) + STEP)) & 0x80008000u) != 0;
+}
+
+// A key/value head of a sequence in the cache.
+struct Keys {
+    const int32_t* table;
+    int h;
+    __device__ __forceinline__ Keys(const PromptArgs& a, int b, int h) : table(a.table + static_cast<int64_t>(b) * a.table_ld), h(h) {}
+    __device__ __forceinline__ int row(const PromptArgs& a, int key) const {        // -1: a page of zeros
+        const int page = table[key >> a.page_shift];
+        return page >= 0 && page < a.num_pages ? ((page * a.hk + h) << a.page_shift) + (key & ((1 << a.page_shift) - 1)) : -1;
+    }
+};
+
+// By a warp: one row of the output again (sequence b's token tok, query head `head`), if of the keys that it does not see one before
+// `end` has a value that is not finite.
+template <typename T, int D>
+__device__ __forceinline__ void mend_row(const PromptArgs& a, int b, int tok, int head, int end) {
+    const Seq s = seq_of(a, b);
+    const Keys keys(a, b, head / a.group);
+    constexpr int W = D / 32, LANES = D / 8;        // columns of a thread; threads that read a row in 16-byte vectors
+    const int lane = threadIdx.x % 32, seen = s.L - s.n + tok + 1;
+    bool bad = false;
+#pragma unroll 1
+    for (int key = seen + lane / LANES; key < min(end, s.L); key += 32 / LANES) {        // (past the sequence's end there were zeros)
+        const int row = keys.row(a, key);
+        if (row >= 0) bad = bad || not_finite<T>(__ldcg(static_cast<const uint4*>(a.v) + static_cast<int64_t>(row) * LANES + lane % LANES));
+    }
+    if (!__any_sync(0xffffffffu, bad) || seen <= 0) return;
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (s.q0 + tok) * a.q_ld + head * D);
+    float m = -INFINITY, l = 0.0f, acc[W];
+#pragma unroll
+    for (int e = 0; e < W; ++e) acc[e] = 0.0f;
+#pragma unroll 1
+    for (int key0 = 0; key0 < seen; key0 += 32) {
+        // 32 scores, one to a thread; then the keys' values, of each W columns to a thread
+        const int row = key0 + lane < seen ? keys.row(a, key0 + lane) : -1;
+        float x = 0.0f;
+        if (row >= 0) {
+            const uint4* k = static_cast<const uint4*>(a.k) + static_cast<int64_t>(row) * LANES;
+#pragma unroll 2
+            for (int c = 0; c < LANES; ++c) {
+                const uint4 kv = __ldcg(k + c), qv = __ldcg(q + c);
+                const uint32_t kw[4] = {kv.x, kv.y, kv.z, kv.w}, qw[4] = {qv.x, qv.y, qv.z, qv.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 fk = unpack2<T>(kw[e]), fq = unpack2<T>(qw[e]);
+                    x = fmaf(fk.x, fq.x, x);
+                    x = fmaf(fk.y, fq.y, x);
+                }
+            }
+        }
+        x = key0 + lane < seen ? x * a.c : -INFINITY;
+        float top = x;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (top > m) {
+            const float alpha = ex2f(m - top);      // (0 from -inf, with sums of 0)
+            m = top;
+            l *= alpha;
+#pragma unroll
+            for (int e = 0; e < W; ++e) acc[e] *= alpha;
+        }
+        const float p = ex2f(x - (m == -INFINITY ? 0.0f : m));
+        l += p;
+#pragma unroll 4
+        for (int j = 0; j < 32; ++j) {
+            const float pj = __shfl_sync(0xffffffffu, p, j);
+            const int rj = __shfl_sync(0xffffffffu, row, j);
+            if (rj < 0) continue;
+            const uint32_t* v = reinterpret_cast<const uint32_t*>(static_cast<const T*>(a.v) + static_cast<int64_t>(rj) * D + W * lane);
+#pragma unroll
+            for (int e = 0; e < W; e += 2) {
+                const float2 f = unpack2<T>(__ldcg(v + e / 2));
+                acc[e] = fmaf(pj, f.x, acc[e]);
+                acc[e + 1] = fmaf(pj, f.y, acc[e + 1]);
+            }
+        }
+        bool nan = true;                            // nothing left that more keys could change
+#pragma unroll
+        for (int e = 0; e < W; ++e) nan = nan && acc[e] != acc[e];
+        if (__all_sync(0xffffffffu, nan) && __any_sync(0xffffffffu, l > 0.0f)) break;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
+    T* out = static_cast<T*>(a.o) + (static_cast<int64_t>(s.q0 + tok) * a.hq + head) * D + W * lane;
+#pragma unroll
+    for (int e = 0; e < W; e += 2) *reinterpret_cast<uint32_t*>(out + e) = l == 0.0f ? 0u : pack2<T>(acc[e] * inv, acc[e + 1] * inv);
+}
+
+// By a warp: rows row0 to row0 + rows - 1 of sequence b's item `at` (of all heads' in line).
+template <typename T, int D>
+__device__ __forceinline__ void mend_rows(const PromptArgs& a, int b, int at, int row0, int rows) {
+    const Seq s = seq_of(a, b);
+    const int items = items_of(a, s), h = at / items, tok0 = (at - h * items) * a.tpt * a.tiles;
+#pragma unroll 1
+    for (int row = row0; row < row0 + rows; ++row) {
+        const int t = row / 128, r = row % 128, rt = r * a.recip >> 16, tok = tok0 + t * a.tpt + rt;
+        if (rt >= a.tpt || tok >= s.n) continue;
+        // (a pair's tiles are multiplied with all of the item's blocks)
+        const int end = (extent(s, tok0 + (D == 256 ? a.tiles : t + 1) * a.tpt) + 127) / 128 * 128;
+        mend_row<T, D>(a, b, tok, h * a.group + r - rt * a.group, end);
+    }
+}
+
+// The same out of the way of the join's code.
+template <typename T, int D>
+__device__ __noinline__ void mend_apart(const PromptArgs& a, int b, int at, int row0, int rows) {
+    mend_rows<T, D>(a, b, at, row0, rows);
+}
+
+// The items that a run (from..to) has whole, an item to each of `warps` warps, of which this is number `me`: mend(b, at) for
+// each that has to be mended.
+template <typename T, int D, typename Mend>
+__device__ __forceinline__ void look_over(const PromptArgs& a, const Pos& from, const Pos& to, int me, int warps, Mend&& mend) {
+    const int lane = threadIdx.x % 32;
+    int before = 0;                                 // items of the run in the sequences before b0
+    // (up to 32 sequences are read without waiting for where the run begins)
+    for (int b0 = a.batch <= 32 ? 0 : from.b; b0 < a.batch && b0 <= to.b; b0 += 32) {
+        // a sequence to each lane: its items in the run, all heads in line, from the lo-th on
+        const int b = b0 + lane;
+        Seq s{0, 0, 0};
+        int items = 0, lo = 0, count = 0;
+        if (b < a.batch) s = seq_of(a, b);
+        if (b >= from.b && b <= to.b) {
+            items = items_of(a, s);
+            lo = b == from.b ? from.h * items + from.i + (from.t > 0 ? 1 : 0) : 0;
+            count = max((b == to.b ? to.h * items + to.i : a.hk * items) - lo, 0);
+        }
+        int upto = count;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        const int all = __shfl_sync(0xffffffffu, upto, 31);
+        for (int x = me >= before ? me - before : (warps - (before - me) % warps) % warps; x < all; x += warps) {
+            const int from_lane = __popc(__ballot_sync(0xffffffffu, upto <= x));
+            const int at = x - __shfl_sync(0xffffffffu, upto - count - lo, from_lane), per = __shfl_sync(0xffffffffu, items, from_lane);
+            const int q0 = __shfl_sync(0xffffffffu, s.q0, from_lane), n = __shfl_sync(0xffffffffu, s.n, from_lane), unseen = n - __shfl_sync(0xffffffffu, s.L, from_lane);
+            const int h = at / per, i = at - h * per;
+            // of each tile the first token that sees a key: 16 bytes of its row by each of D / 8 lanes
+            constexpr int LANES = D / 8, TILES = D == 256 ? 1 : 2;
+            uint32_t bad = 0;
+#pragma unroll
+            for (int t0 = 0; t0 < 2; t0 += TILES) {
+                const int t = t0 + lane / LANES, begin = (2 * i + t) * a.tpt, tok = max(begin, unseen);
+                bool mine = false;
+                if (t < t0 + TILES && tok < min(begin + a.tpt, n))
+                    mine = not_finite<T>(__ldcg(static_cast<const uint4*>(a.o) + (static_cast<int64_t>(q0 + tok) * a.hq + h * a.group) * LANES + lane % LANES));
+                bad |= __ballot_sync(0xffffffffu, mine);
+            }
+            if (bad != 0) mend(b0 + from_lane, at);
+        }
+        before += all;
+    }
+}
+template <typename T, int D>
+__device__ __noinline__ void mend_run(const PromptArgs& a, const Pos* run, int me, int warps) {
+    look_over<T, D>(a, run[0], run[1], me, warps, [&](int b, int at) { mend_rows<T, D>(a, b, at, 0, 256); });
+}
+
+// Whether the thread's row of a tile's sums in tensor memory has one that is not finite: 0 times it is NaN.
+template <int D>
+__device__ __forceinline__ bool row_bad(uint32_t out) {
+    float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll 1
+    for (int y = 0; y < D; y += 64) {
+        float o[32];
+        tmem_ld_rows16(out + y, o);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sum[e % 2] = __ffma2_rn(make_float2(o[2 * e], o[2 * e + 1]), make_float2(0.0f, 0.0f), sum[e % 2]);
+    }
+    return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y) != 0.0f;
+}
+
 // ================================================================== the kernel
 // Warp 0: Q, K, V loads, 1: S, 2: PV, 3: the walk, from 4 on the softmax: eight warps for each tile, two threads to a row.
 // A step of 256 rows by 128 keys takes about 2400 cycles, of which its products would take 2048: it is bound by the softmax
@@ -342,14 +537,15 @@ struct Layout {
     static constexpr uint32_t OFF_HOLD = OFF_BAR + N_BARS * 8;
     static constexpr uint32_t OFF_SCRATCH = (OFF_HOLD + 16 + 7) / 8 * 8;
     static constexpr uint32_t OFF_SEG = OFF_SCRATCH + 80 * 8;
-    static constexpr uint32_t SMEM = OFF_SEG + kSegs * sizeof(Seg) + 1024;
+    static constexpr uint32_t OFF_NOTED = OFF_SEG + kSegs * sizeof(Seg);      // whether there may be something to mend
+    static constexpr uint32_t SMEM = OFF_NOTED + 4 + 1024;
     static constexpr uint32_t TMEM_COLS = 512, O_COL = 256;    // scores of tile t at 128 t, output at 256 + D t
     static_assert(SMEM <= 232448, "shared-memory budget");
     static_assert(SMEM > 116 * 1024, "one CTA per SM: each takes all of TMEM");
 };
 
-// HALVES: the two halves of a block's weights as one piece of code (2), or as a loop (1).
-template <typename T, int D, int HALVES>
+// HALVES: the two halves of a block's weights as one piece of code (2), or as a loop (1).  MEND: no join comes after it.
+template <typename T, int D, int HALVES, bool MEND>
 __global__ void __launch_bounds__(Layout<D>::THREADS, 1) prompt_attention_kernel(const __grid_constant__ CUtensorMap mQ,
                                                                        const __grid_constant__ CUtensorMap mK,
                                                                        const __grid_constant__ CUtensorMap mV,
@@ -379,6 +575,7 @@ __global__ void __launch_bounds__(Layout<D>::THREADS, 1) prompt_attention_kernel
     auto out_free = [&](int t) { return bar0 + 8u * (X + 16 + 2 * kSegs + t); };      // and has been taken
     int* flag = a.flag;
     if (threadIdx.x == 0) {
+        if (MEND) *reinterpret_cast<int*>(gbase + L::OFF_NOTED) = 0;
         mbar_init(q_full, 1);
         mbar_init(q_free, 1);
         for (int i = 0; i < kFull; ++i) {
@@ -729,6 +926,7 @@ __global__ void __launch_bounds__(Layout<D>::THREADS, 1) prompt_attention_kernel
             int er = r, eh = hf, el = lane, et = t;
             asm volatile("" : "+r"(er), "+r"(eh), "+r"(el), "+r"(et));
             const int tok0 = g.tok0 + et * a.tpt;
+            if (MEND && u == 0 && n > 0 && row_bad<D>(ot) && el % 16 == 0) *reinterpret_cast<volatile int*>(gbase + L::OFF_NOTED) = 1;
             if (g.whole) {
                 // Through P, which is free: a whole tile is stored from there by one copy while the warps go on; of one that ends
                 // within the sequence each warp stores its rows, LANES lanes to a row.
@@ -812,6 +1010,13 @@ __global__ void __launch_bounds__(Layout<D>::THREADS, 1) prompt_attention_kernel
         tc_fence_after();
         tmem_dealloc(tmem, L::TMEM_COLS);
     }
+    if constexpr (MEND) {      // (addresses anew: kept, they would take registers of the loops above)
+        uint32_t raw = smem_addr(smem_raw), thread;
+        asm volatile("mov.u32 %0, %%tid.x;" : "=r"(thread), "+r"(raw));
+        uint8_t* at = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+        if (*reinterpret_cast<volatile int*>(at + L::OFF_NOTED) != 0 && thread >= 32 * 4)
+            mend_run<T, D>(a, found_at(reinterpret_cast<int64_t*>(at + L::OFF_SCRATCH)), static_cast<int>(thread / 32) - 4, kTileWarps * TILES);
+    }
 }
 
 // ================================================================== D = 256: a pair of CTAs
@@ -830,13 +1035,14 @@ struct PairLayout {
     static constexpr uint32_t OFF_HOLD = OFF_BAR + N_BARS * 8;
     static constexpr uint32_t OFF_SCRATCH = (OFF_HOLD + 16 + 7) / 8 * 8;
     static constexpr uint32_t OFF_SEG = OFF_SCRATCH + 80 * 8;
-    static constexpr uint32_t SMEM = OFF_SEG + kSegs * sizeof(Seg) + 1024;
+    static constexpr uint32_t OFF_NOTED = OFF_SEG + kSegs * sizeof(Seg);      // whether there may be something to mend
+    static constexpr uint32_t SMEM = OFF_NOTED + 4 + 1024;
     static constexpr uint32_t P_COL = 128, O_COL = 256;        // scores at 0
     static_assert(SMEM <= 232448, "shared-memory budget");
     static_assert(SMEM > 116 * 1024, "one CTA per SM: each takes all of TMEM");
 };
 
-template <typename T>
+template <typename T, bool MEND>
 __global__ void __launch_bounds__(PairLayout::THREADS, 1) prompt_pair_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
                                                                              const __grid_constant__ CUtensorMap mV,
                                                                              const __grid_constant__ PromptArgs a) {
@@ -867,6 +1073,7 @@ __global__ void __launch_bounds__(PairLayout::THREADS, 1) prompt_pair_kernel(con
     static_assert(21 + 2 * kSegs <= L::N_BARS, "barriers");
     int* flag = a.flag;
     if (threadIdx.x == 0) {
+        if (MEND) *reinterpret_cast<int*>(gbase + L::OFF_NOTED) = 0;
         mbar_init(q_full, 1);
         mbar_init(q_free, 1);
         mbar_init(s_full, 1);
@@ -1224,6 +1431,7 @@ __global__ void __launch_bounds__(PairLayout::THREADS, 1) prompt_pair_kernel(con
                             for (int e = 0; e < 4; ++e) st_v8(dst + 64 * y + 8 * e, o + 8 * e);
                     }
             }
+            if (MEND && u == 0 && n > 0 && row_bad<D>(ot) && lane % 16 == 0) *reinterpret_cast<volatile int*>(gbase + L::OFF_NOTED) = 1;
             tc_fence_before();
             leave(k);
         }
@@ -1232,6 +1440,9 @@ __global__ void __launch_bounds__(PairLayout::THREADS, 1) prompt_pair_kernel(con
     cluster_sync();  // neither CTA leaves while its peer may still signal it
     tc_fence_after();
     if (warp == 1) tmem_dealloc_pair(tmem, 512);
+    // (each CTA has its own tile's word; what one mends again the other has mended alike)
+    if (MEND && warp >= 4 && *reinterpret_cast<volatile int*>(gbase + L::OFF_NOTED) != 0)
+        mend_run<T, D>(a, found_at(reinterpret_cast<int64_t*>(gbase + L::OFF_SCRATCH)), warp - 4, kTileWarps);
 }
 
 // ================================================================== join
@@ -1243,9 +1454,13 @@ constexpr int kJoinThreads = 128, kJoinWords = (kGrid + 1 + 31) / 32;
 // Warps for each run that begins within an item.  (32 and 64, in us: D = 128, 32 prompts to 1024 119.4 and 120.7, 2 to 700 24.2 and
 // 25.5; D = 256, 8 to 2048 111.6 and 105.9; 16 for D = 128, one of 4096 131 where 32 take 122.)
 constexpr int join_warps(int D) { return D == 256 ? 64 : 32; }
+// CTAs of each run that look at its whole items' outputs (look_over()), behind those that join.
+constexpr int kMendCtas = 2;
+// Returns whether some of the rows' sums are not finite.
 template <typename T, int D, int ROWS, int AHEAD>
-__device__ __forceinline__ void join_rows(const PromptArgs& a, const Pos& p, const Seq& s, int row0, int rows, int c0, const uint32_t (&has)[kJoinWords], int lane) {
+__device__ __forceinline__ bool join_rows(const PromptArgs& a, const Pos& p, const Seq& s, int row0, int rows, int c0, const uint32_t (&has)[kJoinWords], int lane) {
     constexpr int W = D / 32;
+    bool bad = false;
     float m[ROWS], l[ROWS], acc[ROWS][W];
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
@@ -1314,22 +1529,32 @@ __device__ __forceinline__ void join_rows(const PromptArgs& a, const Pos& p, con
         const int row = row0 + i, r = row % 128, rt = r * a.recip >> 16, tok = (p.i * a.tiles + row / 128) * a.tpt + rt;
         if (i >= rows || rt >= a.tpt || tok >= s.n) continue;
         const float inv = l[i] > 0.0f ? 1.0f / l[i] : l[i] == 0.0f ? 0.0f : l[i];
+        float look = 0.0f;                                 // 0 times what is not finite is NaN
+#pragma unroll
+        for (int y = 0; y < W; ++y) look = fmaf(acc[i][y], 0.0f, look);
+        bad = bad || __any_sync(0xffffffffu, look != 0.0f);
         T* dst = static_cast<T*>(a.o) + (static_cast<int64_t>(s.q0 + tok) * a.hq + p.h * a.group + r - rt * a.group) * D + W * lane;
 #pragma unroll
         for (int y = 0; y < W; y += 2)
             *reinterpret_cast<uint32_t*>(dst + y) = l[i] == 0.0f ? 0u : pack2<T>(acc[i][y] * inv, acc[i][y + 1] * inv);
     }
+    return bad;
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const __grid_constant__ PromptArgs a, int grid) {
+__global__ void __launch_bounds__(kJoinThreads, 5) prompt_join_kernel(const __grid_constant__ PromptArgs a, int grid) {
     pdl_begin();
-    const int lane = threadIdx.x % 32, run = blockIdx.y + 1, unit = blockIdx.x * (kJoinThreads / 32) + threadIdx.x / 32;
+    const int lane = threadIdx.x % 32, run = blockIdx.y, unit = blockIdx.x * (kJoinThreads / 32) + threadIdx.x / 32;
     auto start = [&](int c) {
         const int4 v = __ldcg(a.start + min(c, grid));
         return Pos{v.x, v.y, v.z, v.w};
     };
     const Pos p = start(run);
+    if (unit >= join_warps(D)) {
+        look_over<T, D>(a, p, start(run + 1), unit - join_warps(D), kMendCtas * (kJoinThreads / 32),
+                        [&](int b, int at) { mend_apart<T, D>(a, b, at, 0, 256); });
+        return;
+    }
     if (p.t == 0 || p.b >= a.batch) return;            // this run begins with an item
     // The runs that begin within the same item, and of them those that have something of it (runs may be empty), as bits; the
     // first warp looks from this run on both ways.
@@ -1369,11 +1594,13 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const __grid_
     while (rows * runs * join_warps(D) < 256) rows *= 2;
     const int row0 = (rank * join_warps(D) + unit) * rows;
     if (row0 >= a.rows) return;
+    bool bad = false;
     if (rows == 1) {
-        join_rows<T, D, 1, 4>(a, p, s, row0, 1, c0, has, lane);
+        bad = join_rows<T, D, 1, 4>(a, p, s, row0, 1, c0, has, lane);
     } else {
-        for (int i = 0; i < rows && row0 + i < a.rows; i += 2) join_rows<T, D, 2, 2>(a, p, s, row0 + i, min(2, a.rows - row0 - i), c0, has, lane);
+        for (int i = 0; i < rows && row0 + i < a.rows; i += 2) bad |= join_rows<T, D, 2, 2>(a, p, s, row0 + i, min(2, a.rows - row0 - i), c0, has, lane);
     }
+    if (bad) mend_apart<T, D>(a, p.b, p.h * items_of(a, s) + p.i, row0, min(rows, a.rows - row0));
 }
 
 // ================================================================== host side
@@ -1421,8 +1648,8 @@ int pairs_resident() {
         cfg.attrs = at;
         cfg.numAttrs = 1;
         int n = 0;
-        if (opt_in_smem((const void*)prompt_pair_kernel<__half>, PairLayout::SMEM) != FUSE_OK ||
-            cudaOccupancyMaxActiveClusters(&n, prompt_pair_kernel<__half>, &cfg) != cudaSuccess || n < 1) {
+        if (opt_in_smem((const void*)prompt_pair_kernel<__half, false>, PairLayout::SMEM) != FUSE_OK ||
+            cudaOccupancyMaxActiveClusters(&n, prompt_pair_kernel<__half, false>, &cfg) != cudaSuccess || n < 1) {
             (void)cudaGetLastError();
             n = sm_count() / 2;
         }
@@ -1445,14 +1672,16 @@ int run_prompt(PromptArgs a, const void* q, int64_t q_ld, const void* k, const v
     const int64_t ti = static_cast<int64_t>(a.tpt) * a.tiles, room = a.table_ld << a.page_shift;
     const int64_t items = (ceil_div(a.tokens, ti) + (a.batch < a.tokens ? a.batch : a.tokens)) * a.hk;
     const int64_t most = items * ceil_div(room + a.entry, kLeastRun + a.entry);
-    int64_t runs;
+    const int64_t resident = D == 256 ? pairs_resident() : sm_count(), limit = D == 256 ? kGrid / 2 : kGrid;
+    int64_t runs = resident < limit ? resident : limit;
+    if (runs > most) runs = most;
+    const bool join = runs > 1 && room > 128;      // an item of at most one block of keys is nobody's to share
     int rc;
     if constexpr (D == 256) {
-        runs = pairs_resident() < kGrid / 2 ? pairs_resident() : kGrid / 2;
-        if (runs > most) runs = most;
-        rc = opt_in_smem((const void*)prompt_pair_kernel<T>, PairLayout::SMEM);
+        const auto kernel = join ? prompt_pair_kernel<T, false> : prompt_pair_kernel<T, true>;
+        rc = opt_in_smem((const void*)kernel, PairLayout::SMEM);
         if (rc != FUSE_OK) return rc;
-        rc = launch_pdl(prompt_pair_kernel<T>, dim3(static_cast<unsigned>(2 * runs)), dim3(PairLayout::THREADS), PairLayout::SMEM, st, 2, mQ, mK, mV, a);
+        rc = launch_pdl(kernel, dim3(static_cast<unsigned>(2 * runs)), dim3(PairLayout::THREADS), PairLayout::SMEM, st, 2, mQ, mK, mV, a);
     } else {
         using L = Layout<D>;
         CUtensorMap mO;
@@ -1462,40 +1691,45 @@ int run_prompt(PromptArgs a, const void* q, int64_t q_ld, const void* k, const v
         // 120 and 143, 8 to 2000 (28 heads on 4) 107 and 122, one of 4096 120 and 120, of 8192 400 and 366, of 16384 1450 and 1415;
         // D = 64 (32 heads on 4), 20 to 600 45 and 47, 8 to 2000 100 and 102, 8 to 3000 180 and 178, 16 to 4096 580 and 538.
         constexpr int64_t LONG = D == 64 ? 1200 : 3000;    // tokens of a sequence
-        const auto kernel = a.tokens >= LONG * a.batch ? prompt_attention_kernel<T, D, 2> : prompt_attention_kernel<T, D, 1>;
+        const auto kernel = !join                        ? prompt_attention_kernel<T, D, 1, true>
+                            : a.tokens >= LONG * a.batch ? prompt_attention_kernel<T, D, 2, false>
+                                                         : prompt_attention_kernel<T, D, 1, false>;
         rc = opt_in_smem((const void*)kernel, L::SMEM);
         if (rc != FUSE_OK) return rc;
-        runs = sm_count() < kGrid ? sm_count() : kGrid;
-        if (runs > most) runs = most;
         rc = launch_pdl(kernel, dim3(static_cast<unsigned>(runs)), dim3(L::THREADS), L::SMEM, st, 1, mQ, mK, mV, mO, a);
     }
-    // an item of at most one block of keys is nobody's to share
-    if (rc != FUSE_OK || runs == 1 || room <= 128) return rc;
-    return launch_pdl(prompt_join_kernel<T, D>, dim3(join_warps(D) / (kJoinThreads / 32), static_cast<unsigned>(runs - 1)), dim3(kJoinThreads), 0, st, 1, a,
+    if (rc != FUSE_OK || !join) return rc;
+    return launch_pdl(prompt_join_kernel<T, D>, dim3(join_warps(D) / (kJoinThreads / 32) + kMendCtas, static_cast<unsigned>(runs)), dim3(kJoinThreads), 0, st, 1, a,
                       static_cast<int>(runs));
 }
 
 }  // namespace
 
-int prompt_report_count() { return 16; }
+int prompt_report_count() { return 22; }
 int prompt_report(int i, fuse_kernel_record* out) {
     switch (i) {
-        FC_REPORT(0, Layout<64>::THREADS, Layout<64>::SMEM, 512, prompt_attention_kernel<__nv_bfloat16, 64, 1>);
-        FC_REPORT(1, Layout<64>::THREADS, Layout<64>::SMEM, 512, prompt_attention_kernel<__nv_bfloat16, 64, 2>);
-        FC_REPORT(2, Layout<128>::THREADS, Layout<128>::SMEM, 512, prompt_attention_kernel<__nv_bfloat16, 128, 1>);
-        FC_REPORT(3, Layout<128>::THREADS, Layout<128>::SMEM, 512, prompt_attention_kernel<__nv_bfloat16, 128, 2>);
-        FC_REPORT(4, PairLayout::THREADS, PairLayout::SMEM, 512, prompt_pair_kernel<__nv_bfloat16>);
-        FC_REPORT(5, Layout<64>::THREADS, Layout<64>::SMEM, 512, prompt_attention_kernel<__half, 64, 1>);
-        FC_REPORT(6, Layout<64>::THREADS, Layout<64>::SMEM, 512, prompt_attention_kernel<__half, 64, 2>);
-        FC_REPORT(7, Layout<128>::THREADS, Layout<128>::SMEM, 512, prompt_attention_kernel<__half, 128, 1>);
-        FC_REPORT(8, Layout<128>::THREADS, Layout<128>::SMEM, 512, prompt_attention_kernel<__half, 128, 2>);
-        FC_REPORT(9, PairLayout::THREADS, PairLayout::SMEM, 512, prompt_pair_kernel<__half>);
-        FC_REPORT(10, kJoinThreads, 0, 0, prompt_join_kernel<__nv_bfloat16, 64>);
-        FC_REPORT(11, kJoinThreads, 0, 0, prompt_join_kernel<__nv_bfloat16, 128>);
-        FC_REPORT(12, kJoinThreads, 0, 0, prompt_join_kernel<__nv_bfloat16, 256>);
-        FC_REPORT(13, kJoinThreads, 0, 0, prompt_join_kernel<__half, 64>);
-        FC_REPORT(14, kJoinThreads, 0, 0, prompt_join_kernel<__half, 128>);
-        FC_REPORT(15, kJoinThreads, 0, 0, prompt_join_kernel<__half, 256>);
+        FC_REPORT(0, Layout<64>::THREADS, Layout<64>::SMEM, 512, prompt_attention_kernel<__nv_bfloat16, 64, 1, true>);
+        FC_REPORT(1, Layout<64>::THREADS, Layout<64>::SMEM, 512, prompt_attention_kernel<__nv_bfloat16, 64, 1, false>);
+        FC_REPORT(2, Layout<64>::THREADS, Layout<64>::SMEM, 512, prompt_attention_kernel<__nv_bfloat16, 64, 2, false>);
+        FC_REPORT(3, Layout<128>::THREADS, Layout<128>::SMEM, 512, prompt_attention_kernel<__nv_bfloat16, 128, 1, true>);
+        FC_REPORT(4, Layout<128>::THREADS, Layout<128>::SMEM, 512, prompt_attention_kernel<__nv_bfloat16, 128, 1, false>);
+        FC_REPORT(5, Layout<128>::THREADS, Layout<128>::SMEM, 512, prompt_attention_kernel<__nv_bfloat16, 128, 2, false>);
+        FC_REPORT(6, PairLayout::THREADS, PairLayout::SMEM, 512, prompt_pair_kernel<__nv_bfloat16, true>);
+        FC_REPORT(7, PairLayout::THREADS, PairLayout::SMEM, 512, prompt_pair_kernel<__nv_bfloat16, false>);
+        FC_REPORT(8, Layout<64>::THREADS, Layout<64>::SMEM, 512, prompt_attention_kernel<__half, 64, 1, true>);
+        FC_REPORT(9, Layout<64>::THREADS, Layout<64>::SMEM, 512, prompt_attention_kernel<__half, 64, 1, false>);
+        FC_REPORT(10, Layout<64>::THREADS, Layout<64>::SMEM, 512, prompt_attention_kernel<__half, 64, 2, false>);
+        FC_REPORT(11, Layout<128>::THREADS, Layout<128>::SMEM, 512, prompt_attention_kernel<__half, 128, 1, true>);
+        FC_REPORT(12, Layout<128>::THREADS, Layout<128>::SMEM, 512, prompt_attention_kernel<__half, 128, 1, false>);
+        FC_REPORT(13, Layout<128>::THREADS, Layout<128>::SMEM, 512, prompt_attention_kernel<__half, 128, 2, false>);
+        FC_REPORT(14, PairLayout::THREADS, PairLayout::SMEM, 512, prompt_pair_kernel<__half, true>);
+        FC_REPORT(15, PairLayout::THREADS, PairLayout::SMEM, 512, prompt_pair_kernel<__half, false>);
+        FC_REPORT(16, kJoinThreads, 0, 0, prompt_join_kernel<__nv_bfloat16, 64>);
+        FC_REPORT(17, kJoinThreads, 0, 0, prompt_join_kernel<__nv_bfloat16, 128>);
+        FC_REPORT(18, kJoinThreads, 0, 0, prompt_join_kernel<__nv_bfloat16, 256>);
+        FC_REPORT(19, kJoinThreads, 0, 0, prompt_join_kernel<__half, 64>);
+        FC_REPORT(20, kJoinThreads, 0, 0, prompt_join_kernel<__half, 128>);
+        FC_REPORT(21, kJoinThreads, 0, 0, prompt_join_kernel<__half, 256>);
         default: return FUSE_EINVAL;
     }
 }
@@ -1566,6 +1800,10 @@ extern "C" int fuse_prompt_attention(const void* q, int64_t q_ld, const void* k_
     a.ml = reinterpret_cast<float2*>(ws + s.ml);
     a.po = reinterpret_cast<float*>(ws + s.po);
     a.rows = static_cast<int>(s.rows);
+    a.q = q;
+    a.k = k_cache;
+    a.v = v_cache;
+    a.q_ld = q_ld;
     a.flag = watchdog_flag();
     a.bad = index_flag();
     if (!a.flag || !a.bad) return FUSE_ECUDA;

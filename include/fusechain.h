@@ -442,8 +442,8 @@ int fuse_w4_gemv(const void* x, const void* wq, const void* scales, const void* 
  *   o        device [tokens, q_heads, D] of `dtype`; o must not overlap an input
  *   tokens   rows of q and o
  *   k_cache, v_cache  device [num_pages, kv_heads, page_size, D] of `dtype`; what lies in a page past the
- *            keys in use is not used, whatever its bits.  A value that is not finite, at a key that is in
- *            use, may make rows NaN that do not see it yet (those whose last key is less than 384 before it).
+ *            keys in use is not used, whatever its bits, and what lies at keys in use reaches only the rows
+ *            that see them: an infinity or NaN there changes no bit of the others (but costs time).
  *   block_table  device int32 [batch, table_ld]: entry i is the page of keys i page_size .. ; only the
  *            entries that seq_lens covers are read.  May be NULL when table_ld == 0.
  *   cu_queries  device int32 [batch + 1], ascending, within 0 .. tokens

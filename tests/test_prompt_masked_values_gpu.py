@@ -1,0 +1,105 @@
+"""Values that are not finite, at keys in use: the mask keeps them from the rows that do not see them.  Each column of V has one
+such value, at a key of its own.  A row that sees it has it in that column: an infinity or NaN times a positive weight.  Every
+other output is what the formula gives with a zero in its place, within the tolerance of reference(), or, where a sequence has
+no such value, the same bits as without them in the batch."""
+import math
+
+import pytest
+
+import epilogue_chains_gb300 as fc
+from test_prompt_attention_gpu import make, reference, run
+
+pytestmark = pytest.mark.gpu
+
+
+def check(seqs, hq, hk, D, page, dtype, seed=0, std=1.0):
+    """Of every sequence and head each column gets a value that is not finite, at keys that are spread over the sequence, near
+    the ends of blocks and of tiles and over all of its new tokens."""
+    import torch
+    p = make(seqs, hq, hk, D, page, dtype, seed=seed, std=std)
+    poison = [math.inf, -math.inf, math.nan]
+    dirty, expect = p["v"].clone(), []
+    for b, (L, n) in enumerate(seqs):
+        if not L:
+            continue
+        keys = [L - 1, max(L - n, 0), max(L - n + 1, 0), L // 2, 0]
+        keys += [k for k in range(max(L - n, 0), L) if k % 128 in (0, 1, 63, 64, 127)][:D // 2]
+        keys += [max(L - 1 - (7 * i) % max(n, 1), 0) for i in range(D)]
+        pages = p["table"][b].tolist()
+        for h in range(hk):
+            for c in range(D):
+                j, x = min(keys[(c + 11 * h) % len(keys)], L - 1), poison[(c + h) % 3]
+                dirty[pages[j // page], h, j % page, c] = x
+                p["v"][pages[j // page], h, j % page, c] = 0.0
+                expect.append((b, h, c, j, x))
+    want, tol = reference(p)
+    first = [int(x) for x in p["cu"]]
+    for b, h, c, j, x in expect:
+        L, n = seqs[b]
+        i = max(j - (L - n), 0)                        # the first row that sees key j
+        if i < n:
+            g = hq // hk
+            want[first[b] + i:first[b] + n, h * g:(h + 1) * g, c] = x
+    got = run({**p, "v": dirty}).double()
+    near = torch.where(want.isfinite(), (got - want).abs() <= tol, (got == want) | (got.isnan() & want.isnan()))
+    assert bool(near.all()), [(r, float(got[tuple(r)]), float(want[tuple(r)])) for r in (~near).nonzero()[:6].tolist()]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("hq,hk", [(2, 2), (8, 2), (7, 1)])
+@pytest.mark.parametrize("seqs", [[(300, 300)], [(1, 1), (0, 3), (700, 200), (5, 9), (129, 129)], [(2000, 150), (17, 17), (640, 1)]])
+def test_values_that_a_row_does_not_see(cuda_device, dtype, D, hq, hk, seqs):
+    check(seqs, hq, hk, D, 16 if D == 128 else 64, dtype, seed=D + hq)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D,page", [(64, 32), (128, 256), (256, 128)])
+def test_parts_that_several_ctas_share(cuda_device, dtype, D, page):
+    check([(20000, 130)], 4, 1, D, page, dtype, seed=3)
+    check([(9000, 300), (600, 600)], 3, 3, D, page, dtype, seed=4, std=2.0)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_long_prompts(cuda_device, D):
+    check([(3500, 3500)], 2, 1, D, 64, "bf16", seed=5)
+
+
+@pytest.mark.parametrize("hq,hk,D", [(32, 8, 128), (8, 8, 256), (8, 1, 64)])
+def test_every_value_from_a_key_on(cuda_device, hq, hk, D):
+    """A long prompt whose every value from some key on is not a number, next to one without: rows before that key are what they
+    are with zeros there, and the other prompt's have the same bits."""
+    import torch
+    p = make([(8000, 8000), (500, 400)], hq, hk, D, 64, "bf16", seed=6)
+    at = 333
+    pages = p["table"][0, :125].long()
+    rows = torch.arange(8000, device="cuda").view(125, 1, 64, 1) >= at
+    dirty = p["v"].clone()
+    dirty[pages] = torch.where(rows, torch.full_like(dirty[pages], math.nan), dirty[pages])
+    p["v"][pages] = torch.where(rows, torch.zeros_like(p["v"][pages]), p["v"][pages])
+    clean = run(p)
+    want, tol = reference(p)
+    got = run({**p, "v": dirty})
+    assert bool(((got.double() - want).abs() <= tol)[:at].all()) and torch.equal(got[8000:], clean[8000:])
+    assert bool(got[at:8000].isnan().all())
+
+
+def test_pages_out_of_range_next_to_them(cuda_device):
+    """A page index out of range counts as a page of zeros here too."""
+    import torch
+    p = make([(200, 200)], 4, 2, 128, 16, "bf16", seed=7)
+    p["table"][0, 11] = -3
+    zero = {**p, "v": p["v"].clone()}
+    last = int(p["table"][0, 12])
+    zero["v"][last, :, 7, 5] = 0.0
+    p["v"][last, :, 7, 5] = math.inf
+    out = []
+    for x in (zero, p):
+        o = torch.full_like(x["q"], 7.0)
+        fc.fuse_prompt_attention(x["q"], x["k"], x["v"], x["table"], x["cu"], x["lens"], o, x["scale"])
+        assert fc.fuse_check() == fc.FUSE_EINDEX
+        out.append(o)
+    assert bool((out[1][199, :, 5] == math.inf).all())
+    out[1][199, :, 5] = out[0][199, :, 5]
+    u = 2.0 ** -8                   # each is off by less than 2 u (|o| + E) and the scores' part, for weights that sum to 1 and |v| < 6
+    assert bool(((out[0].double() - out[1].double()).abs() <= 4 * u * (out[0].double().abs() + 1.0)).all())
