@@ -418,19 +418,17 @@ __global__ void __launch_bounds__(kGemmThreads, NT <= 64 ? 2 : 1) mxfp4_gemm_ker
         const float bias = in && a.bias ? to_f32(static_cast<const T*>(a.bias)[n]) : 0.0f;
         const int tokens = min(NT, a.M - m0);
         float* part_sums = reinterpret_cast<float*>(gbase);          // [token][128], over the stages
-        if (s1 == s0 || wait(done, 0)) {
+        if (wait(done, 0)) {
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < tokens; c += 32) {
-                float v[32] = {};
+                float v[32] = {};      // (not read: without the zeros the compiler's order takes 100 tokens of 4096 x 14336 from 18.6 to 20.7 us)
                 T r[32];
                 const int64_t at = static_cast<int64_t>(m0 + c) * a.N + n;
                 const int left = in ? tokens - c : 0;
                 if (a.R && split == 1) load_32<T>(static_cast<const T*>(a.R) + at, a.N, left, r);
-                if (s1 > s0) {
-                    tmem_ld32(tmem + (static_cast<uint32_t>(32 * quad) << 16) + c, v);
-                    tmem_ld_wait();
-                }
+                tmem_ld32(tmem + (static_cast<uint32_t>(32 * quad) << 16) + c, v);
+                tmem_ld_wait();
                 if (split > 1) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) part_sums[(c + e) * 128 + row] = v[e];
@@ -725,9 +723,10 @@ int launch_gemm(GemmArgs a, const void* xq, const void* wq, cudaStream_t st) {
     const int rc = opt_in_smem((const void*)mxfp4_gemm_kernel<T, NT>, GemmLayout<NT>::SMEM);
     if (rc != FUSE_OK) return rc;
     const int64_t tn = ceil_div(a.N, 128), tm = ceil_div(a.M, NT);
-    // K over up to eight CTAs while all of them are resident at once (two per SM up to 64 tokens) and each has two stages.  Over
-    // two only from 24 stages on: joining them takes what 12 stages do (4096 weights, K = 4096, 16 stages: one token 4.2 us over
-    // eight, 4.6 over four, 5.7 unsplit, but 200 tokens 7.7 over two and 6.8 unsplit; K = 14336: 256 tokens 12.7 over two, 15.1 unsplit).
+    // K over up to eight CTAs while all of them are resident at once (two per SM up to 64 tokens) and each has two stages, so that none
+    // is without.  Over two only from 24 stages on: joining them takes what 12 stages do (4096 weights, K = 4096, 16 stages, which lie
+    // in L2: one token 4.2 us over eight, 4.6 over four, 5.7 unsplit, but 200 tokens 7.7 over two and 6.8 unsplit; K = 14336: 256 tokens
+    // 12.7 over two, 15.1 unsplit).
     const int64_t room = sm_count() * (NT <= 64 ? 2 : 1);
     a.split = 1;
     while (a.split < 8 && tn * tm * a.split * 2 <= room && a.stages >= 2 * a.split * 2) a.split *= 2;
