@@ -35,6 +35,7 @@ namespace fc {
 namespace {
 
 constexpr int kMaxBatch = 4096;
+constexpr int kTiles = 2;                  // of 128 rows, of an item
 constexpr int kGrid = 160;                 // most CTAs (workspace bound); half as many pairs of them
 // A running reference is replaced when a row's maximum exceeds it by more than 2^8, so weights stay
 // within [0, 2^8]; for fp16 weights it is also set 2^7 below the maximum, which uses fp16's range
@@ -84,7 +85,7 @@ struct PromptArgs {
     int entry, snap;                   // entry_of(D), snap_of(D)
     uint64_t item_recip;               // ceil(2^32 / (tpt tiles))
     bool o_sectors;                    // o lies on a 32-byte boundary
-    int tpt, tiles;                    // tokens of a tile of 128 rows; tiles of an item (2)
+    int tpt;                           // tokens of a tile of 128 rows
     int page_shift, num_pages, cache_rows;
     float c;                           // scale * log2(e)
     // workspace: where each CTA's run begins, and the parts of items that CTAs share: of CTA c slot 2 c has the part of
@@ -115,12 +116,12 @@ __device__ __forceinline__ Seq seq_of(const PromptArgs& a, int b, int* bad = nul
 }
 // n / (tokens of an item), for n below 2^24 (a division takes several times as long).
 __device__ __forceinline__ int over_item(const PromptArgs& a, int n) { return static_cast<int>(static_cast<uint64_t>(n) * a.item_recip >> 32); }
-__device__ __forceinline__ int items_of(const PromptArgs& a, const Seq& s) { return over_item(a, s.n + a.tpt * a.tiles - 1); }
+__device__ __forceinline__ int items_of(const PromptArgs& a, const Seq& s) { return over_item(a, s.n + a.tpt * kTiles - 1); }
 // Keys that the first `tokens` new tokens of a sequence see between them.
 __device__ __forceinline__ int extent(const Seq& s, int tokens) { return max(s.L - s.n + min(tokens, s.n), 0); }
 // Places of a head's first k items: sum over i < k of entry + extent((i + 1) ti).
 __device__ __forceinline__ int64_t places(const PromptArgs& a, const Seq& s, int items, int k) {
-    const int64_t ti = a.tpt * a.tiles, d = s.L - s.n;
+    const int64_t ti = a.tpt * kTiles, d = s.L - s.n;
     int64_t sum = static_cast<int64_t>(k) * a.entry;
     if (k == items && k > 0) {
         sum += extent(s, s.n);
@@ -165,7 +166,7 @@ __device__ __forceinline__ Pos pos_in(const PromptArgs& a, const Seq& s, int b, 
         else hi = mid - 1;
     }
     const int64_t in = r - places(a, s, items, lo);
-    const int blocks = (extent(s, (lo + 1) * a.tpt * a.tiles) + 127) / 128;
+    const int blocks = (extent(s, (lo + 1) * a.tpt * kTiles) + 127) / 128;
     p.i = lo;
     p.t = in <= a.entry ? 0 : static_cast<int>((in - a.entry) >> 7);
     if (p.t <= snap) {
@@ -214,9 +215,9 @@ struct Walk {
     }
     __device__ __forceinline__ bool next(const PromptArgs& a, Seg& g) {
         while (p.before(end)) {
-            const int tok0 = p.i * a.tpt * a.tiles;
+            const int tok0 = p.i * a.tpt * kTiles;
             const int b0 = (extent(s, tok0 + a.tpt) + 127) / 128;
-            const int b1 = a.tiles == 2 && tok0 + a.tpt < s.n ? (extent(s, tok0 + 2 * a.tpt) + 127) / 128 : 0;
+            const int b1 = tok0 + a.tpt < s.n ? (extent(s, tok0 + 2 * a.tpt) + 127) / 128 : 0;
             g.blocks = max(b0, b1);
             const bool cut = p.b == end.b && p.h == end.h && p.i == end.i;
             const int t1 = cut ? min(end.t, g.blocks) : g.blocks;
@@ -423,13 +424,13 @@ __device__ __forceinline__ void mend_row(const PromptArgs& a, int b, int tok, in
 template <typename T, int D>
 __device__ __forceinline__ void mend_rows(const PromptArgs& a, int b, int at, int row0, int rows) {
     const Seq s = seq_of(a, b);
-    const int items = items_of(a, s), h = at / items, tok0 = (at - h * items) * a.tpt * a.tiles;
+    const int items = items_of(a, s), h = at / items, tok0 = (at - h * items) * a.tpt * kTiles;
 #pragma unroll 1
     for (int row = row0; row < row0 + rows; ++row) {
         const int t = row / 128, r = row % 128, rt = r * a.recip >> 16, tok = tok0 + t * a.tpt + rt;
         if (rt >= a.tpt || tok >= s.n) continue;
         // (a pair's tiles are multiplied with all of the item's blocks)
-        const int end = (extent(s, tok0 + (D == 256 ? a.tiles : t + 1) * a.tpt) + 127) / 128 * 128;
+        const int end = (extent(s, tok0 + (D == 256 ? kTiles : t + 1) * a.tpt) + 127) / 128 * 128;
         mend_row<T, D>(a, b, tok, h * a.group + r - rt * a.group, end);
     }
 }
@@ -471,11 +472,11 @@ __device__ __forceinline__ void look_over(const PromptArgs& a, const Pos& from, 
             const int q0 = __shfl_sync(0xffffffffu, s.q0, from_lane), n = __shfl_sync(0xffffffffu, s.n, from_lane), unseen = n - __shfl_sync(0xffffffffu, s.L, from_lane);
             const int h = at / per, i = at - h * per;
             // of each tile the first token that sees a key: 16 bytes of its row by each of D / 8 lanes
-            constexpr int LANES = D / 8, TILES = D == 256 ? 1 : 2;
+            constexpr int LANES = D / 8, TILES = D == 256 ? 1 : kTiles;
             uint32_t bad = 0;
 #pragma unroll
-            for (int t0 = 0; t0 < 2; t0 += TILES) {
-                const int t = t0 + lane / LANES, begin = (2 * i + t) * a.tpt, tok = max(begin, unseen);
+            for (int t0 = 0; t0 < kTiles; t0 += TILES) {
+                const int t = t0 + lane / LANES, begin = (kTiles * i + t) * a.tpt, tok = max(begin, unseen);
                 bool mine = false;
                 if (t < t0 + TILES && tok < min(begin + a.tpt, n))
                     mine = not_finite<T>(__ldcg(static_cast<const uint4*>(a.o) + (static_cast<int64_t>(q0 + tok) * a.hq + h * a.group) * LANES + lane % LANES));
@@ -520,7 +521,7 @@ constexpr int kSegs = 4;                            // segments that the walk is
 
 template <int D>
 struct Layout {
-    static constexpr int TILES = 2;
+    static constexpr int TILES = kTiles;
     static constexpr int THREADS = 32 * (4 + kTileWarps * TILES);
     // Registers of a thread at the launch, and then of the first four warps and of the softmax's: within what the launch has.
     static constexpr int REGS = 96, FEW = 64, MANY = 104;
@@ -1526,7 +1527,7 @@ __device__ __forceinline__ bool join_rows(const PromptArgs& a, const Pos& p, con
     }
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
-        const int row = row0 + i, r = row % 128, rt = r * a.recip >> 16, tok = (p.i * a.tiles + row / 128) * a.tpt + rt;
+        const int row = row0 + i, r = row % 128, rt = r * a.recip >> 16, tok = (p.i * kTiles + row / 128) * a.tpt + rt;
         if (i >= rows || rt >= a.tpt || tok >= s.n) continue;
         const float inv = l[i] > 0.0f ? 1.0f / l[i] : l[i] == 0.0f ? 0.0f : l[i];
         float look = 0.0f;                                 // 0 times what is not finite is NaN
@@ -1669,7 +1670,7 @@ int run_prompt(PromptArgs a, const void* q, int64_t q_ld, const void* k, const v
         !make_map_3d(&mQ, q, kMap16, dims, strides, qbox, 128))
         return FUSE_ECUDA;
     // no more runs than there can be
-    const int64_t ti = static_cast<int64_t>(a.tpt) * a.tiles, room = a.table_ld << a.page_shift;
+    const int64_t ti = static_cast<int64_t>(a.tpt) * kTiles, room = a.table_ld << a.page_shift;
     const int64_t items = (ceil_div(a.tokens, ti) + (a.batch < a.tokens ? a.batch : a.tokens)) * a.hk;
     const int64_t most = items * ceil_div(room + a.entry, kLeastRun + a.entry);
     const int64_t resident = D == 256 ? pairs_resident() : sm_count(), limit = D == 256 ? kGrid / 2 : kGrid;
@@ -1786,11 +1787,10 @@ extern "C" int fuse_prompt_attention(const void* q, int64_t q_ld, const void* k_
     a.group = static_cast<int>(group);
     a.recip = static_cast<int>((65536 + group - 1) / group);
     a.tpt = static_cast<int>(128 / group);
-    a.tiles = 2;
     a.entry = entry_of(static_cast<int>(D));
     a.snap = snap_of(static_cast<int>(D));
     a.o_sectors = is_aligned(o, 32);
-    a.item_recip = ((uint64_t(1) << 32) + a.tpt * a.tiles - 1) / (a.tpt * a.tiles);
+    a.item_recip = ((uint64_t(1) << 32) + a.tpt * kTiles - 1) / (a.tpt * kTiles);
     while ((1 << a.page_shift) < page_size) ++a.page_shift;
     a.num_pages = static_cast<int>(num_pages);
     a.cache_rows = static_cast<int>(num_pages * kv_heads * page_size);
