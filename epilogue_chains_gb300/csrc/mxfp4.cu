@@ -12,8 +12,9 @@
 //    tensor core's 128 rows and the tokens its columns, so a warp's stores of a token are consecutive outputs and
 //    few tokens cost few columns.  kind::mxf4 multiplies 64 values of a row at once, at four times the rate of 16-bit
 //    operands; the scales go from shared memory to TMEM next to the accumulators.  K may be split over a
-//    cluster of CTAs, whose sums meet in shared memory.  One token of 4096 x 4096 4.3 us, 100 of 4096 x 14336 10.2 us, 13.3
-//    with their quantisation: bound by latency, the weights' way through a ring of stages and the join.
+//    cluster of CTAs, whose sums meet in shared memory.  In a stream of equal calls, their weights in L2, one token of 4096 x 4096 4.2
+//    us, 100 of 4096 x 14336 10.2 and 13.3 with their quantisation; with weights from HBM 4.4, and 18.6 with the quantisation: bound
+//    by latency, the weights' way through a ring of stages and the join.
 //  * mxfp4_pair_kernel: the same for many tokens, bound by the tensor cores and at short K by the change of accumulators.
 #include <cudaTypedefs.h>
 #include <math.h>
@@ -160,8 +161,8 @@ __global__ void __launch_bounds__(kQThreads) mxfp4_dequantize_kernel(const __gri
 // ================================================================== product
 // The accumulator's rows are weights (N), its columns tokens (M).
 constexpr int kStageK = 256;                        // values of a row per stage: 128 bytes
-// The product's K: a row's scales (8 bytes a stage, 1024 for its tile) are counted in 32 bits, and the 2^21 stages of a longest K
-// take some 0.4 s, within what the epilogue's bounded wait allows.
+// The product's K: a tile's scales (1024 bytes a stage) are counted in 32 bits, and the epilogue waits for all stages of an output in
+// one bounded wait of a second.
 constexpr int64_t kMostK = int64_t(1) << 29;
 constexpr uint32_t kTileBytes = 128 * 128;          // 128 rows of a stage
 constexpr int kGemmThreads = 32 * 6;                // warp 0: loads, 1: MMA issue, 2-5: epilogue
@@ -343,7 +344,8 @@ __global__ void __launch_bounds__(kGemmThreads, NT <= 64 ? 2 : 1) mxfp4_gemm_ker
     const int n0 = n_tile * 128, m0 = static_cast<int>(blockIdx.y) * NT;
     const int s0 = static_cast<int>(static_cast<int64_t>(a.stages) * part / split), s1 = static_cast<int>(static_cast<int64_t>(a.stages) * (part + 1) / split);
     // The first weights on their way into L2 while the kernel before (mostly the quantisation of X) runs out: 100 tokens of
-    // 4096 x 14336 10.65 -> 10.25 us, 14.15 -> 13.4 with that kernel; more than the first six stages gain less.
+    // 4096 x 14336 10.65 -> 10.25 us, 14.15 -> 13.4 with that kernel (in a stream of equal calls); more than the first six stages
+    // gain less.
     if (warp == 0 && blockIdx.y == 0 && lane < 6 && s0 + lane < s1) {
         const int s = s0 + lane;
         tma_prefetch_2d(&mW, s * 64, n0);
@@ -735,6 +737,11 @@ int launch_gemm(GemmArgs a, const void* xq, const void* wq, cudaStream_t st) {
                       GemmLayout<NT>::SMEM, st, a.split, mW, mX, a);
 }
 
+// Tiles by the number of tokens, pairs of CTAs where their tiles are as many as half of those that can be resident.  In us, weights
+// from HBM, K = 4096; tiles of 32, 64 and 128 tokens: one token of 4096 weights 4.4, 4.9 and 4.3, 32 of 14336 7.5, 8.0 and 7.5, 64 of
+// 4096 -, 6.7 and 5.7, of 14336 -, 8.4 and 7.7, of 28672 -, 11.9 and 15.5.  128 tokens and pairs: 512 of 4096 6.6 and 9.4, 1024 of 4096
+// 12.8 and 9.9, 256 of 14336 13.8 and 10.7, 128 of 28672 16.4 and 16.5; where pairs' tiles are half empty or few the rule takes the
+// slower side, 128 of 14336 8.0 and 10.2, 256 of 9728 7.3 and 9.9.
 template <typename T>
 int run_gemm(const GemmArgs& a, const void* xq, const void* wq, cudaStream_t st) {
     if (a.M <= 32) return launch_gemm<T, 32>(a, xq, wq, st);

@@ -17,9 +17,10 @@
 // lengths are in device memory, so one launch configuration (and a captured graph) serves every batch.  All
 // waits are bounded (watchdog).
 //
-// Measured (32 query heads on 8 for keys and values, D = 128, bf16): one prompt of 16384 1.44 ms, 1.53 PFLOP/s of the visible
-// pairs, where the chip's power is the limit; 32 of up to 1024 (fp16) 120 us, 0.85; 64 new tokens after 65536 71 us, 0.97, of
-// which the join is a fifth.  16 ungrouped heads of 256: 16384 1.40 ms, 1.57; 8 of up to 2048 106 to 110 us, 1.0.
+// Measured (32 query heads on 8 for keys and values, D = 128, bf16): one prompt of 16384 1.43 ms, 1.54 PFLOP/s of the visible
+// pairs, where the chip's power is the limit; 32 of up to 1024 (fp16) 126 us, 0.81; 64 new tokens after 65536 69 us, 1.0, of
+// which the join is a fifth.  16 ungrouped heads of 256: 16384 1.40 ms, 1.57; 8 of up to 2048 108 to 111 us, 1.0.  D = 64 (32 heads
+// on 8, bf16): 16384 1.10 ms, 1.0.
 #include <cudaTypedefs.h>
 #include <math.h>
 
@@ -285,6 +286,8 @@ __device__ __forceinline__ void find_runs(const PromptArgs& a, int me, int runs,
     int64_t len = quotient(total + runs - 1, runs), least = items > 0 ? quotient(total + items - 1, items) : 1;
     if (least > kLeastRun + a.entry) least = kLeastRun + a.entry;
     if (len < least) len = least;
+    // Long runs snap further, as their parts are the longer for it: 1 / 4096 of a run (64 after 65536 70.1 us, without 71.8, 4 times
+    // that 160 and 165; with 1 / 1024 8 of 512 after 16384 341 instead of 315).  Short ones as one likes: 2, 4 or 8 blocks take the same.
     const int snap = len < kLeastRun + a.entry ? 4 : max(a.snap, static_cast<int>(min(len >> 12, static_cast<int64_t>(64))));
     for (int w = 0; w < 2; ++w) {
         const int64_t x = static_cast<int64_t>(me + w) * len;
@@ -509,11 +512,12 @@ __device__ __forceinline__ bool row_bad(uint32_t out) {
 
 // ================================================================== the kernel
 // Warp 0: Q, K, V loads, 1: S, 2: PV, 3: the walk, from 4 on the softmax: eight warps for each tile, two threads to a row.
-// A step of 256 rows by 128 keys takes about 2400 cycles, of which its products would take 2048: it is bound by the softmax
-// warps' instructions (600 a warp, four to a scheduler), of which 160 are the exponentials and their sums; without exponentials,
-// or without loads, it takes as long.  An item's first step, output and diagonal cost 4000 cycles more, so short prompts are slower.
-// (With a thread to a row, one warp per tile in each quarter of the SM, a step of 256 rows by 128 keys took 2600 cycles, where its
-// products take 2048: a softmax warp's own instructions, one after the other.)
+// A step of 256 rows by 128 keys takes, between one prompt of 8192 and one of 16384 (32 heads on 8): D = 128 1.66 us in either form, some
+// 3000 cycles of the 1.75 to 1.9 GHz that the power limit leaves, of which the products would take 2048; D = 64 1.23 us in one
+// piece (2550 cycles, products 1024), 1.42 as a loop.  It is bound by the softmax warps' instructions (600 a warp, four to a scheduler), of
+// which 160 are the exponentials and their sums; without exponentials, or without loads, it takes as long.  An item's first step,
+// output and diagonal cost 4000 cycles more, so short prompts are slower.  (A thread to a row, one warp per tile in each quarter of
+// the SM, was slower: a softmax warp's own instructions, one after the other.)
 constexpr int kTileWarps = 8;
 constexpr int kFull = 4;                            // barriers of K tiles in turn, and of V tiles
 constexpr uint32_t kMostTries = 1u << 18;
@@ -621,7 +625,7 @@ __global__ void __launch_bounds__(Layout<D>::THREADS, 1) prompt_attention_kernel
     auto v_at = [](int j, int n) { return j + 1 < n ? 2 * j + 2 : 2 * j + 1; };
     Seg* segs_at = reinterpret_cast<Seg*>(gbase + L::OFF_SEG);
     bool ok = true;
-    // (A bound by tries, each of which ends by itself after kTryWaitHintNs: mbar_wait_bounded()'s clock makes more code at each of
+    // (A bound by tries, each of which ends by itself after kTryWaitHintNs, together 5 s at most: mbar_wait_bounded()'s clock makes more code at each of
     // the many waits, which the warps fetch over and over: 32 prompts to 1024 142 -> 139 us.)
     auto wait = [&](uint32_t bar, uint32_t parity) {
         for (uint32_t n = 0; !__all_sync(0xffffffffu, mbar_try_wait(bar, parity & 1u)); ++n)
@@ -834,8 +838,8 @@ __global__ void __launch_bounds__(Layout<D>::THREADS, 1) prompt_attention_kernel
                 // computed, and half of P is free as soon as the last block's half has been multiplied.
 #pragma unroll HALVES
                 for (int h = 0; h < 2; ++h) {
-                    // Asked here, needed below: a wait takes 200 cycles also where nothing is left to wait for, of 2800 that a step
-                    // takes (32 prompts to 1024 134 -> 128.5 us; one vote for both rare cases below: 127).
+                    // Asked here, needed below: a wait takes 200 cycles also where nothing is left to wait for (32 prompts to 1024
+                    // 134 -> 128.5 us; one vote for both rare cases below: 127).
                     const bool taken = mbar_test(o_done(t, h), (i - 1) & 1);
                     float x[32];         // keys 64 h + 32 hf .. of the block
                     tmem_ld_rows16(st + 64 * h, x);
@@ -1690,7 +1694,9 @@ int run_prompt(PromptArgs a, const void* q, int64_t q_ld, const void* k, const v
         if (!make_map_3d(&mO, a.o, kMap16, dims, o_strides, qbox, 128)) return FUSE_ECUDA;
         // Short prompts: the loop, whose instructions the warps fetch half of.  In us, loop and one piece: D = 128, 32 prompts to 1024
         // 120 and 143, 8 to 2000 (28 heads on 4) 107 and 122, one of 4096 120 and 120, of 8192 400 and 366, of 16384 1450 and 1415;
-        // D = 64 (32 heads on 4), 20 to 600 45 and 47, 8 to 2000 100 and 102, 8 to 3000 180 and 178, 16 to 4096 580 and 538.
+        // D = 64 (32 heads on 4), 20 to 600 45 and 47, 8 to 2000 100 and 102, 8 to 3000 180 and 178, 16 to 4096 580 and 538.  Tokens with
+        // those behind the last sequence, as the lengths are in device memory; keys of earlier turns are not counted, where the forms
+        // differ less: 64 after 65536 70.5 and 70.1, 8 of 512 after 16384 322 and 318 (D = 128), 64 after 65536 57 and 53 (D = 64).
         constexpr int64_t LONG = D == 64 ? 1200 : 3000;    // tokens of a sequence
         const auto kernel = !join                        ? prompt_attention_kernel<T, D, 1, true>
                             : a.tokens >= LONG * a.batch ? prompt_attention_kernel<T, D, 2, false>

@@ -15,7 +15,8 @@
 //
 // A row is read by a cluster of 1, 2, 4 or 8 CTAs (few rows: more CTAs for each), whose parts and alternatives
 // meet in the first CTA's shared memory.  It is bound by HBM: 4096 x 131072 in bf16, the best five of each, 167 us (6.4 TB/s);
-// one row or a few by latency: 128000 fp32 logits of one row 4.2 us, with the best twenty 6.5 us.
+// one row or a few by latency: 128000 fp32 logits of one row 4.2 us, with the best twenty 6.5 us (in a captured graph; a call
+// takes 7.1).
 #include <math.h>
 
 #include <type_traits>
@@ -439,7 +440,10 @@ __global__ void __launch_bounds__(kThreads, 6) token_logprobs_kernel(const __gri
     if (cluster > 1) cluster_sync();      // the first CTA has read the others' shared memory
 }
 
-// CTAs of a row.
+// CTAs of a row: twice as many while there are fewer than two for each SM and 2048 logits are left to each.  In us, over 1, 2, 4 and 8
+// (bf16, the best five): 128000 logits of one row 10.6, 8.3, 7.2, 6.5, of 38 17.2, 11.9, 10.1, 10.9, of 152 17.9, 13.8, 16.2, 20.5, of
+// 303 22.7, 23.7, 26.2, 32.9; 32000 of one row 6.2, 6.2, 5.9, 5.5, 8000 5.1, 5.2, 5.3, 5.5, 4000 4.6, 5.2, 5.3, 5.4.  Between such numbers
+// of rows the last CTAs run alone, and the rule is off by up to a third: 200 rows 26.5, 22.1 (its choice), 16.4, 23.1.
 int cluster_of(int64_t rows, int64_t vocab) {
     int c = 1;
     while (c < kMaxCluster && rows * c < 2 * static_cast<int64_t>(sm_count()) && vocab >= 4096 * c) c *= 2;
