@@ -323,7 +323,7 @@ __device__ __forceinline__ void find_runs(const PromptArgs& a, int me, int runs,
 // A weight of 0 is no mask in a product: 0 x infinity is NaN, in every row of a tile that does not see the key.  Of a tile's rows the
 // first that sees a key sees the fewest, so its output tells whether that has happened.  Where it is not finite, the tile's rows for which
 // one of the values that were multiplied with a weight of 0 is not finite are computed again, from the keys that they see alone:
-// rare, and slow.  CTAs of the join's launch look at the outputs of all whole items, which takes 2 to 3 us where the join is short
+// rare, and slow (a warp takes 8 ms to a row of 16384 keys).  CTAs of the join's launch look at the outputs of all whole items, which takes 2 to 3 us where the join is short
 // (32 prompts to 1024 123.5 -> 126.5 us).  Code for it in prompt_attention_kernel costs more, there: looking the values over ahead of
 // the products, by the softmax warps, 14 us, a look at the first row's sums by its softmax warp, before, with or after the output,
 // or by the warp that issues PV, 7 to 13.  Where nothing is joined the kernel does it, in a form of its own (MEND).
@@ -346,21 +346,48 @@ struct Keys {
     }
 };
 
-// By a warp: one row of the output again (sequence b's token tok, query head `head`), if of the keys that it does not see one before
-// `end` has a value that is not finite.
+// By a warp: the last of the keys first .. end - 1 with a value that is not finite, or -1.
 template <typename T, int D>
-__device__ __forceinline__ void mend_row(const PromptArgs& a, int b, int tok, int head, int end) {
-    const Seq s = seq_of(a, b);
-    const Keys keys(a, b, head / a.group);
-    constexpr int W = D / 32, LANES = D / 8;        // columns of a thread; threads that read a row in 16-byte vectors
-    const int lane = threadIdx.x % 32, seen = s.L - s.n + tok + 1;
-    bool bad = false;
-#pragma unroll 1
-    for (int key = seen + lane / LANES; key < min(end, s.L); key += 32 / LANES) {        // (past the sequence's end there were zeros)
+__device__ __forceinline__ int last_bad(const PromptArgs& a, const Keys& keys, int first, int end) {
+    constexpr int LANES = D / 8;                    // threads that read a row in 16-byte vectors
+    const int lane = threadIdx.x % 32;
+    int last = -1;
+#pragma unroll 2
+    for (int key = first + lane / LANES; key < end; key += 32 / LANES) {
         const int row = keys.row(a, key);
-        if (row >= 0) bad = bad || not_finite<T>(__ldcg(static_cast<const uint4*>(a.v) + static_cast<int64_t>(row) * LANES + lane % LANES));
+        if (row >= 0 && not_finite<T>(__ldcg(static_cast<const uint4*>(a.v) + static_cast<int64_t>(row) * LANES + lane % LANES))) last = key;
     }
-    if (!__any_sync(0xffffffffu, bad) || seen <= 0) return;
+    return __reduce_max_sync(0xffffffffu, last);
+}
+
+// By a warp: f(j, x) for key key0 + j and the thread's columns x of its values, of 32 keys whose rows in the cache the threads have (-1: zeros).
+// (No branch, so that the loads of AHEAD keys are on their way together.)
+template <typename T, int D, int AHEAD, typename F>
+__device__ __forceinline__ void for_values(const PromptArgs& a, int row, F&& f) {
+    constexpr int W = D / 32;
+    const int lane = threadIdx.x % 32;
+#pragma unroll AHEAD
+    for (int j = 0; j < 32; ++j) {
+        const int rj = __shfl_sync(0xffffffffu, row, j);
+        const uint32_t* v = reinterpret_cast<const uint32_t*>(static_cast<const T*>(a.v) + static_cast<int64_t>(max(rj, 0)) * D + W * lane);
+        float x[W];
+#pragma unroll
+        for (int e = 0; e < W; e += 2) {
+            const uint32_t w = __ldcg(v + e / 2);
+            const float2 g = unpack2<T>(rj < 0 ? 0u : w);
+            x[e] = g.x;
+            x[e + 1] = g.y;
+        }
+        f(j, x);
+    }
+}
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
+
+// By a warp: one row of the output again (sequence s's token tok, query head `head`).
+template <typename T, int D, int AHEAD>
+__device__ __forceinline__ void mend_row(const PromptArgs& a, const Keys& keys, const Seq& s, int tok, int head) {
+    constexpr int W = D / 32, LANES = D / 8;        // columns of a thread; 16-byte vectors of a row
+    const int lane = threadIdx.x % 32, seen = s.L - s.n + tok + 1;
     const uint4* q = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (s.q0 + tok) * a.q_ld + head * D);
     float m = -INFINITY, l = 0.0f, acc[W];
 #pragma unroll
@@ -369,22 +396,20 @@ __device__ __forceinline__ void mend_row(const PromptArgs& a, int b, int tok, in
     for (int key0 = 0; key0 < seen; key0 += 32) {
         // 32 scores, one to a thread; then the keys' values, of each W columns to a thread
         const int row = key0 + lane < seen ? keys.row(a, key0 + lane) : -1;
+        const uint4* k = static_cast<const uint4*>(a.k) + static_cast<int64_t>(max(row, 0)) * LANES;
         float x = 0.0f;
-        if (row >= 0) {
-            const uint4* k = static_cast<const uint4*>(a.k) + static_cast<int64_t>(row) * LANES;
-#pragma unroll 2
-            for (int c = 0; c < LANES; ++c) {
-                const uint4 kv = __ldcg(k + c), qv = __ldcg(q + c);
-                const uint32_t kw[4] = {kv.x, kv.y, kv.z, kv.w}, qw[4] = {qv.x, qv.y, qv.z, qv.w};
+#pragma unroll AHEAD
+        for (int c = 0; c < LANES; ++c) {
+            const uint4 kv = __ldcg(k + c), qv = __ldcg(q + c);
+            const uint32_t kw[4] = {kv.x, kv.y, kv.z, kv.w}, qw[4] = {qv.x, qv.y, qv.z, qv.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 fk = unpack2<T>(kw[e]), fq = unpack2<T>(qw[e]);
-                    x = fmaf(fk.x, fq.x, x);
-                    x = fmaf(fk.y, fq.y, x);
-                }
+            for (int e = 0; e < 4; ++e) {
+                const float2 fk = unpack2<T>(kw[e]), fq = unpack2<T>(qw[e]);
+                x = fmaf(fk.x, fq.x, x);
+                x = fmaf(fk.y, fq.y, x);
             }
         }
-        x = key0 + lane < seen ? x * a.c : -INFINITY;
+        x = key0 + lane < seen ? (row >= 0 ? x * a.c : 0.0f) : -INFINITY;
         float top = x;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -397,23 +422,11 @@ __device__ __forceinline__ void mend_row(const PromptArgs& a, int b, int tok, in
         }
         const float p = ex2f(x - (m == -INFINITY ? 0.0f : m));
         l += p;
-#pragma unroll 4
-        for (int j = 0; j < 32; ++j) {
+        for_values<T, D, 2 * AHEAD>(a, row, [&](int j, const float (&v)[W]) {
             const float pj = __shfl_sync(0xffffffffu, p, j);
-            const int rj = __shfl_sync(0xffffffffu, row, j);
-            if (rj < 0) continue;
-            const uint32_t* v = reinterpret_cast<const uint32_t*>(static_cast<const T*>(a.v) + static_cast<int64_t>(rj) * D + W * lane);
 #pragma unroll
-            for (int e = 0; e < W; e += 2) {
-                const float2 f = unpack2<T>(__ldcg(v + e / 2));
-                acc[e] = fmaf(pj, f.x, acc[e]);
-                acc[e + 1] = fmaf(pj, f.y, acc[e + 1]);
-            }
-        }
-        bool nan = true;                            // nothing left that more keys could change
-#pragma unroll
-        for (int e = 0; e < W; ++e) nan = nan && acc[e] != acc[e];
-        if (__all_sync(0xffffffffu, nan) && __any_sync(0xffffffffu, l > 0.0f)) break;
+            for (int e = 0; e < W; ++e) acc[e] = fmaf(pj, v[e], acc[e]);
+        });
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
@@ -423,25 +436,70 @@ __device__ __forceinline__ void mend_row(const PromptArgs& a, int b, int tok, in
     for (int e = 0; e < W; e += 2) *reinterpret_cast<uint32_t*>(out + e) = l == 0.0f ? 0u : pack2<T>(acc[e] * inv, acc[e + 1] * inv);
 }
 
-// By a warp: rows row0 to row0 + rows - 1 of sequence b's item `at` (of all heads' in line).
-template <typename T, int D>
-__device__ __forceinline__ void mend_rows(const PromptArgs& a, int b, int at, int row0, int rows) {
+// By a warp: of sequence b's item `at` (of all heads' in line) rows row, row + step .. below `end`, those that do not see a key by whose
+// value, which is not finite, they have been multiplied.  A column in which a row sees such a value as well is the sum of those, whatever
+// the weights are (so that a cache full of them, or a column of it, does not take long); only rows with another column to mend
+// are computed again.  LONG false: all of them, as there are few keys.
+template <typename T, int D, int AHEAD, bool LONG>
+__device__ __forceinline__ void mend_rows(const PromptArgs& a, int b, int at, int row, int end, int step) {
+    constexpr int W = D / 32;
+    const int lane = threadIdx.x % 32;
     const Seq s = seq_of(a, b);
     const int items = items_of(a, s), h = at / items, tok0 = (at - h * items) * a.tpt * kTiles;
+    const Keys keys(a, b, h);
+    int tile = -1, first = 0, last = -1;            // keys that all rows of the tile see; the last one to mend
+    float before[W];                                // the sum of what is not finite of those
+    // adds what is not finite of keys from .. to - 1 to `sum`, or notes it from key `seen` on
+    auto collect = [&](int from, int to, int seen, float (&sum)[W], uint32_t& unseen) {
 #pragma unroll 1
-    for (int row = row0; row < row0 + rows; ++row) {
-        const int t = row / 128, r = row % 128, rt = r * a.recip >> 16, tok = tok0 + t * a.tpt + rt;
-        if (rt >= a.tpt || tok >= s.n) continue;
-        // (a pair's tiles are multiplied with all of the item's blocks)
-        const int end = (extent(s, tok0 + (D == 256 ? kTiles : t + 1) * a.tpt) + 127) / 128 * 128;
-        mend_row<T, D>(a, b, tok, h * a.group + r - rt * a.group, end);
+        for (int key0 = from; key0 < to; key0 += 32)
+            for_values<T, D, 2 * AHEAD>(a, key0 + lane < to ? keys.row(a, key0 + lane) : -1, [&](int j, const float (&v)[W]) {
+#pragma unroll
+                for (int e = 0; e < W; ++e)
+                    if (!finite(v[e])) {
+                        if (key0 + j < seen) sum[e] += v[e];
+                        else unseen |= 1u << e;
+                    }
+            });
+    };
+#pragma unroll 1
+    for (; row < end; row += step) {
+        const int t = row / 128, r = row % 128, rt = r * a.recip >> 16, tok = tok0 + t * a.tpt + rt, seen = s.L - s.n + tok + 1;
+        if (rt >= a.tpt || tok >= s.n || seen <= 0) continue;
+        uint32_t unseen = 0;
+        if (t != tile) {
+            // the tile's blocks (a pair's tiles are multiplied with all of the item's; past the sequence's end there were zeros)
+            tile = t;
+            first = max(s.L - s.n + tok0 + t * a.tpt + 1, 0);
+            last = last_bad<T, D>(a, keys, first, min(s.L, (extent(s, tok0 + (D == 256 ? kTiles : t + 1) * a.tpt) + 127) / 128 * 128));
+#pragma unroll
+            for (int e = 0; e < W; ++e) before[e] = 0.0f;
+            if (LONG && last >= 0) collect(0, first, first, before, unseen);
+        }
+        if (seen > last) continue;
+        const int head = h * a.group + r - rt * a.group;
+        float sum[W];
+        bool again = !LONG;
+#pragma unroll
+        for (int e = 0; e < W; ++e) sum[e] = before[e];
+        if (LONG) collect(first, last + 1, seen, sum, unseen);
+#pragma unroll
+        for (int e = 0; e < W; ++e) again = again || ((unseen >> e & 1u) && finite(sum[e]));
+        if (__any_sync(0xffffffffu, again)) {
+            mend_row<T, D, AHEAD>(a, keys, s, tok, head);
+        } else {
+            T* out = static_cast<T*>(a.o) + (static_cast<int64_t>(s.q0 + tok) * a.hq + head) * D + W * lane;
+#pragma unroll
+            for (int e = 0; e < W; ++e)
+                if (unseen >> e & 1u) out[e] = from_f32<T>(sum[e]);
+        }
     }
 }
 
 // The same out of the way of the join's code.
 template <typename T, int D>
-__device__ __noinline__ void mend_apart(const PromptArgs& a, int b, int at, int row0, int rows) {
-    mend_rows<T, D>(a, b, at, row0, rows);
+__device__ __noinline__ void mend_apart(const PromptArgs& a, int b, int at, int row, int end, int step) {
+    mend_rows<T, D, 2, true>(a, b, at, row, end, step);
 }
 
 // The items that a run (from..to) has whole, an item to each of `warps` warps, of which this is number `me`: mend(b, at) for
@@ -492,7 +550,7 @@ __device__ __forceinline__ void look_over(const PromptArgs& a, const Pos& from, 
 }
 template <typename T, int D>
 __device__ __noinline__ void mend_run(const PromptArgs& a, const Pos* run, int me, int warps) {
-    look_over<T, D>(a, run[0], run[1], me, warps, [&](int b, int at) { mend_rows<T, D>(a, b, at, 0, 256); });
+    look_over<T, D>(a, run[0], run[1], me, warps, [&](int b, int at) { mend_rows<T, D, 1, false>(a, b, at, 0, 128 * kTiles, 1); });
 }
 
 // Whether the thread's row of a tile's sums in tensor memory has one that is not finite: 0 times it is NaN.
@@ -1556,8 +1614,24 @@ __global__ void __launch_bounds__(kJoinThreads, 5) prompt_join_kernel(const __gr
     };
     const Pos p = start(run);
     if (unit >= join_warps(D)) {
-        look_over<T, D>(a, p, start(run + 1), unit - join_warps(D), kMendCtas * (kJoinThreads / 32),
-                        [&](int b, int at) { mend_apart<T, D>(a, b, at, 0, 256); });
+        // what has to be mended is listed, so that all of the CTA's warps share its rows
+        constexpr int WARPS = kJoinThreads / 32, MOST = 64;
+        __shared__ int count, list[MOST][2];
+        if (threadIdx.x == 0) count = 0;
+        __syncthreads();
+        look_over<T, D>(a, p, start(run + 1), unit - join_warps(D), kMendCtas * WARPS, [&](int b, int at) {
+            int n = 0;
+            if (lane == 0) {
+                n = atomicAdd(&count, 1);
+                if (n < MOST) {
+                    list[n][0] = b;
+                    list[n][1] = at;
+                }
+            }
+            if (__shfl_sync(0xffffffffu, n, 0) >= MOST) mend_apart<T, D>(a, b, at, 0, 128 * kTiles, 1);
+        });
+        __syncthreads();
+        for (int n = 0; n < min(count, MOST); ++n) mend_apart<T, D>(a, list[n][0], list[n][1], unit % WARPS, 128 * kTiles, WARPS);
         return;
     }
     if (p.t == 0 || p.b >= a.batch) return;            // this run begins with an item
@@ -1605,7 +1679,7 @@ __global__ void __launch_bounds__(kJoinThreads, 5) prompt_join_kernel(const __gr
     } else {
         for (int i = 0; i < rows && row0 + i < a.rows; i += 2) bad |= join_rows<T, D, 2, 2>(a, p, s, row0 + i, min(2, a.rows - row0 - i), c0, has, lane);
     }
-    if (bad) mend_apart<T, D>(a, p.b, p.h * items_of(a, s) + p.i, row0, min(rows, a.rows - row0));
+    if (bad) mend_apart<T, D>(a, p.b, p.h * items_of(a, s) + p.i, row0, min(row0 + rows, a.rows), 1);
 }
 
 // ================================================================== host side

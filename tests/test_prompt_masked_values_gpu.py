@@ -103,3 +103,41 @@ def test_pages_out_of_range_next_to_them(cuda_device):
     out[1][199, :, 5] = out[0][199, :, 5]
     u = 2.0 ** -8                   # each is off by less than 2 u (|o| + E) and the scores' part, for weights that sum to 1 and |v| < 6
     assert bool(((out[0].double() - out[1].double()).abs() <= 4 * u * (out[0].double().abs() + 1.0)).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("hq,hk,D", [(8, 2, 128), (4, 4, 256), (8, 1, 64)])
+@pytest.mark.parametrize("seqs", [[(3000, 3000), (700, 700)], [(2600, 500), (9, 9)], [(100, 100), (33, 20)]])
+def test_columns_of_infinities(cuda_device, dtype, hq, hk, D, seqs):
+    """One column infinite from a key on, one of minus infinities from another on, one of both signs (NaN where a row sees both) and
+    one that has a single infinity far back: the first sequence's, the others stay as they are."""
+    import torch
+    p = make(seqs, hq, hk, D, 16, dtype, seed=11)
+    (L, n), inf = seqs[0], math.inf
+    a, b, c, e = L - n + 7, L - 1 - n // 3, L - n // 2, (L - n) // 2
+    pages = p["table"][0, :-(-L // 16)].long()
+    pos = torch.arange(len(pages) * 16, device="cuda").view(-1, 1, 16)
+    dirty = p["v"].clone()
+    part, zero = dirty[pages], p["v"][pages]
+    live = pos < L
+    for x, where, value in ((3, pos >= a, inf), (7, pos >= b, -inf), (D - 1, pos >= c, inf), (D - 1, (pos >= c) & (pos % 5 == 2), -inf), (20, pos == e, inf)):
+        hit = (where & live).expand(-1, hk, -1)
+        part[..., x] = torch.where(hit, torch.full_like(part[..., x], value), part[..., x])
+        zero[..., x] = torch.where(hit, torch.zeros_like(zero[..., x]), zero[..., x])
+    dirty[pages], p["v"][pages] = part, zero
+    clean = run(p)
+    want, tol = reference(p)
+    seen = L - n + 1 + torch.arange(n, device="cuda")                      # keys that a row of the first sequence sees
+    two = next(k for k in range(c, L + 5) if k % 5 == 2)                   # the last column's first -inf, and its first inf
+    one = next(k for k in range(c, L + 5) if k % 5 != 2)
+    w = want[:n].clone()
+    w[seen > a, :, 3] = inf
+    w[seen > b, :, 7] = -inf
+    w[(seen > one) & (seen <= two), :, D - 1] = inf
+    w[(seen > two) & (seen <= one), :, D - 1] = -inf
+    w[(seen > one) & (seen > two), :, D - 1] = math.nan
+    w[seen > e, :, 20] = inf
+    got = run({**p, "v": dirty})
+    near = torch.where(w.isfinite(), (got[:n].double() - w).abs() <= tol[:n], (got[:n].double() == w) | (got[:n].isnan() & w.isnan()))
+    assert bool(near.all()), [(r, float(got[tuple(r)]), float(w[tuple(r)])) for r in (~near).nonzero()[:6].tolist()]
+    assert torch.equal(got[n:], clean[n:])
