@@ -15,8 +15,8 @@ pytestmark = pytest.mark.gpu
 DT = {"bf16": "bfloat16", "f16": "float16"}
 
 
-def check(seqs, hq, hk, D, page, dtype, seed=0):
-    """seqs: (keys, new tokens) of each sequence."""
+def check(seqs, hq, hk, D, page, dtype, seed=0, room=0):
+    """seqs: (keys, new tokens) of each sequence; room: keys that the table has entries for, if more."""
     import torch
     g = torch.Generator(device="cuda").manual_seed(seed)
     dt = getattr(torch, DT[dtype])
@@ -26,7 +26,7 @@ def check(seqs, hq, hk, D, page, dtype, seed=0):
     kc = torch.full((pages, hk, page, D), math.nan, dtype=dt, device="cuda")
     vc = kc.clone()
     order = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)
-    table = torch.full((len(seqs), max(counts)), 1 << 30, dtype=torch.int32, device="cuda")
+    table = torch.full((len(seqs), max(*counts, -(-room // page))), 1 << 30, dtype=torch.int32, device="cuda")
     at = 0
     for b, (n, _) in enumerate(seqs):
         ids = order[at:at + counts[b]]
@@ -77,3 +77,12 @@ def test_every_key_counts_once(cuda_device, dtype, D):
 @pytest.mark.parametrize("hq,hk", [(3, 3), (7, 1), (24, 3), (100, 1)])
 def test_every_key_counts_once_in_every_head_layout(cuda_device, hq, hk, D):
     check([(300, 300), (1500, 77), (4000, 3), (2, 2)], hq, hk, D, 256, "f16", hq)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_tables_wider_than_the_sequences(cuda_device, dtype, D):
+    """As a server's are: a table as wide as its longest context, sequences of one block of keys and less among those of several."""
+    check([(17, 17)], 8, 2, D, 16, dtype, 6, room=8192)
+    check([(128, 100), (1, 1), (60, 3), (128, 128)], 8, 8, D, 64, dtype, 7, room=20000)
+    check([(300, 300), (2, 5), (129, 1)], 6, 2, D, 32, dtype, 8, room=100000)

@@ -12,11 +12,13 @@ from test_prompt_attention_gpu import make, reference, run
 pytestmark = pytest.mark.gpu
 
 
-def check(seqs, hq, hk, D, page, dtype, seed=0, std=1.0):
+def check(seqs, hq, hk, D, page, dtype, seed=0, std=1.0, room=0):
     """Of every sequence and head each column gets a value that is not finite, at keys that are spread over the sequence, near
     the ends of blocks and of tiles and over all of its new tokens."""
     import torch
     p = make(seqs, hq, hk, D, page, dtype, seed=seed, std=std)
+    if room > p["table"].shape[1] * page:        # a wider table
+        p["table"] = torch.nn.functional.pad(p["table"], (0, room // page - p["table"].shape[1]), value=1 << 30)
     poison = [math.inf, -math.inf, math.nan]
     dirty, expect = p["v"].clone(), []
     for b, (L, n) in enumerate(seqs):
@@ -58,6 +60,16 @@ def test_values_that_a_row_does_not_see(cuda_device, dtype, D, hq, hk, seqs):
 def test_parts_that_several_ctas_share(cuda_device, dtype, D, page):
     check([(20000, 130)], 4, 1, D, page, dtype, seed=3)
     check([(9000, 300), (600, 600)], 3, 3, D, page, dtype, seed=4, std=2.0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("room", [0, 8192])
+def test_one_block_of_keys(cuda_device, dtype, D, room):
+    """Nothing to join, by the table's width or by the sequences' alone."""
+    check([(17, 17), (128, 128), (1, 1), (100, 3), (3, 6)], 8, 2, D, 16, dtype, seed=8, room=room)
+    check([(33, 33)], 5, 1, D, 16, dtype, seed=9, room=room)
+    check([(64, 64)] * 40, 2, 1, D, 64, dtype, seed=10, room=room)
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
